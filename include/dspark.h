@@ -374,6 +374,63 @@ dspark_status dspark_pctree_verify(dspark_ws* ws, const float* P, const int32_t*
                                    uint64_t seed, uint64_t round, int32_t* path, int32_t* n_accepted,
                                    int32_t* next_anchor, dspark_stream_t stream);
 
+/*
+ * Training the head: the cross entropy of eq. (9) for any linear layer over
+ * the vocabulary, with its gradients ("DeepSeek-V4.1 模型结构（6）：解码，
+ * DSpark", section on training; deepseek.csdn.net §6). For N rows of K
+ * features,
+ *   z[n][v] = sum_k X[n][k] W[v][k] (+ U[n][v]),  lse[n] = log sum_v e^z[n][v],
+ *   loss[n] = lse[n] - z[n][target[n]],
+ * and, for row weights wt (NULL: 1) and a factor scale, the gradients of
+ * scale * sum_n wt[n] loss[n]:
+ *   G[n][v] = wt[n] (e^(z[n][v] - lse[n]) - [v == target[n]]),
+ *   dX = scale G W,   dW = scale G^T X.
+ * The Markov head on fixed parallel logits is X = W1[x_prev], W = W2 (layout
+ * DSPARK_W_KV), U = U_k; a head that trains with its hidden state has
+ * X = [h, W1[x_prev]] and W the output matrix beside W2's transpose. The
+ * logits are not kept: the gradient call makes them again from lse, a piece
+ * of the vocabulary at a time (scratch: at most 256 MiB of G, or 2048 columns
+ * of it).
+ *
+ * X [N][ldx], W [V][ldw] (DSPARK_W_VK) or [K][ldw] (DSPARK_W_KV), dX [N][lddx]
+ * and dW (W's layout, lddw) are bf16; U [N][ldu] (or NULL), loss, lse and wt
+ * [N] fp32; target [N] int32. Leading dimensions are multiples of 8 (ldu: 4),
+ * values past a row's last are neither read nor written, and every base
+ * pointer is 16-byte aligned (scratch: 256). Sums, statistics and the products'
+ * accumulators are fp32; G enters the gradients' products as bf16. dX or dW
+ * may be NULL (not both): a frozen X or W.
+ *
+ * target[n] = -1 leaves row n out: loss 0 and no part in either gradient; any
+ * other value outside [0, V) does the same and sets DSPARK_ERANGE in
+ * *device_status, the caller's int32, which keeps its first error until the
+ * caller clears it. U may hold -inf, or
+ * the type's lowest value, where a token is masked (with U, z <= -1e30 counts
+ * as -inf): its probability is 0, and a row whose target is masked has loss
+ * +inf. A row with every token masked has lse -inf, loss +inf (0 if
+ * left out) and no part in the gradients. +inf and NaN make their row's
+ * results NaN. N = 0 is allowed (dW is then 0). 0 <= N <= 2^20, K <= 65536,
+ * V <= 2^24, else DSPARK_EINVAL. Asynchronous on `stream`; each result is the same
+ * from call to call.
+ */
+typedef enum { DSPARK_W_VK = 0, DSPARK_W_KV = 1 } dspark_w_layout;
+
+typedef struct {
+    int N;                   /* rows (training positions) */
+    int K;                   /* features */
+    int V;                   /* vocabulary size */
+    int layout;              /* dspark_w_layout of W and dW */
+    int64_t ldx, ldw, ldu;   /* leading dimensions, in elements (ldu unused without U) */
+    int64_t lddx, lddw;      /* of the gradients (unused by dspark_linear_ce) */
+} dspark_lce_dims;
+
+dspark_status dspark_linear_ce(const dspark_lce_dims* dims, const void* X, const void* W, const float* U,
+                               const int32_t* target, float* loss, float* lse, void* scratch,
+                               int32_t* device_status, dspark_stream_t stream);
+dspark_status dspark_linear_ce_grad(const dspark_lce_dims* dims, const void* X, const void* W, const float* U,
+                                    const int32_t* target, const float* lse, const float* wt, float scale, void* dX,
+                                    void* dW, void* scratch, int32_t* device_status, dspark_stream_t stream);
+size_t dspark_linear_ce_scratch_bytes(const dspark_lce_dims* dims);
+
 #ifdef __cplusplus
 }
 #endif

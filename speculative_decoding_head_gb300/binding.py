@@ -18,6 +18,7 @@ from .build import LIB_PATH
 
 MODES = {"static": 0, "compact": 1, "lagged": 2}
 WDTYPES = {"f32": 0, "bf16": 1}
+LAYOUTS = {"vk": 0, "kv": 1}
 
 SYMBOLS = [
     "dspark_ws_create", "dspark_ws_destroy", "dspark_ws_reset", "dspark_last_error",
@@ -27,6 +28,7 @@ SYMBOLS = [
     "dspark_rnn_draft", "dspark_rnn_draft_scratch_bytes", "dspark_verify_rnn",
     "dspark_pctree_scratch_bytes", "dspark_pctree_build", "dspark_pctree_verify",
     "dspark_ws_set_shard", "dspark_plan_shard",
+    "dspark_linear_ce", "dspark_linear_ce_grad", "dspark_linear_ce_scratch_bytes",
 ]
 
 
@@ -37,6 +39,11 @@ class DsparkError(RuntimeError):
 class Dims(C.Structure):
     _fields_ = [("B", C.c_int), ("gamma", C.c_int), ("V", C.c_int), ("r", C.c_int), ("H", C.c_int),
                 ("wdtype", C.c_int), ("mode", C.c_int), ("lag", C.c_int)]
+
+
+class LceDims(C.Structure):
+    _fields_ = [("N", C.c_int), ("K", C.c_int), ("V", C.c_int), ("layout", C.c_int), ("ldx", C.c_int64),
+                ("ldw", C.c_int64), ("ldu", C.c_int64), ("lddx", C.c_int64), ("lddw", C.c_int64)]
 
 
 _lock = threading.Lock()
@@ -105,6 +112,12 @@ def load() -> C.CDLL:
         lib.dspark_ws_set_shard.restype = i32
         lib.dspark_plan_shard.argtypes = [P, P, P, i32, i32, P, P, P, P, P]
         lib.dspark_plan_shard.restype = i32
+        lib.dspark_linear_ce.argtypes = [C.POINTER(LceDims)] + [P] * 9
+        lib.dspark_linear_ce.restype = i32
+        lib.dspark_linear_ce_grad.argtypes = [C.POINTER(LceDims)] + [P] * 6 + [C.c_float] + [P] * 5
+        lib.dspark_linear_ce_grad.restype = i32
+        lib.dspark_linear_ce_scratch_bytes.argtypes = [C.POINTER(LceDims)]
+        lib.dspark_linear_ce_scratch_bytes.restype = C.c_size_t
         _lib = lib
         return lib
 
@@ -128,6 +141,26 @@ def _ptr(t: Optional[torch.Tensor], dtype=None, name="") -> C.c_void_p:
     if dtype is not None and t.dtype != dtype:
         raise DsparkError(f"{name} must be {dtype}, got {t.dtype}")
     return C.c_void_p(t.data_ptr())
+
+
+def _rows(t: torch.Tensor, shape, dtype, name: str):
+    """Pointer and leading dimension of a matrix whose rows are contiguous."""
+    if not t.is_cuda:
+        raise DsparkError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise DsparkError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise DsparkError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    rows, cols = t.shape
+    if cols > 1 and rows > 0 and t.stride(1) != 1:
+        raise DsparkError(f"{name} must have contiguous rows")
+    return C.c_void_p(t.data_ptr()), (t.stride(0) if rows > 1 else -(-max(cols, 1) // 8) * 8)
+
+
+def _vec(t: Optional[torch.Tensor], n: int, dtype, name: str) -> C.c_void_p:
+    if t is not None and tuple(t.shape) != (n,):
+        raise DsparkError(f"{name} must be [{n}], got {list(t.shape)}")
+    return _ptr(t, dtype, name)
 
 
 def _stream(stream) -> C.c_void_p:
@@ -400,4 +433,93 @@ class Workspace:
             _ptr(out["n_acc"], i32, "n_acc"), _ptr(out["next_anchor"], i32, "next_anchor"),
             _stream(stream))
         _check(code, "dspark_round")
+        return out
+
+
+class LinearCE:
+    """Softmax cross entropy of z = X W (+ U) over the vocabulary, with its
+    gradients and without keeping z (``dspark_linear_ce``,
+    ``dspark_linear_ce_grad``), for N rows of K features and V tokens. Holds
+    the calls' scratch and status word; calls that share one object must be
+    ordered on one stream.
+
+    X [N, K] and W ([V, K] for layout "vk", [K, V] for "kv") are bf16 with
+    contiguous rows whose stride is a multiple of 8; U [N, V] fp32 (row stride
+    a multiple of 4) or None; target [N] int32, -1 for a row left out."""
+
+    def __init__(self, N: int, K: int, V: int, layout: str = "vk", device="cuda"):
+        self.lib = load()
+        if layout not in LAYOUTS:
+            raise DsparkError(f"layout must be one of {sorted(LAYOUTS)}, got {layout!r}")
+        self.N, self.K, self.V, self.layout = int(N), int(K), int(V), layout
+        d = LceDims(self.N, self.K, self.V, LAYOUTS[layout], 0, 0, 0, 0, 0)
+        nbytes = int(self.lib.dspark_linear_ce_scratch_bytes(C.byref(d)))
+        if nbytes == 0:
+            raise DsparkError(f"dspark_linear_ce: unsupported N={N}, K={K}, V={V}")
+        self.scratch = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        self.status = torch.zeros(1, dtype=torch.int32, device=device)
+
+    @property
+    def w_shape(self):
+        return (self.V, self.K) if self.layout == "vk" else (self.K, self.V)
+
+    def device_status(self) -> int:
+        """The first device error since the last reset (synchronises)."""
+        return int(self.status.item())
+
+    def reset(self) -> None:
+        self.status.zero_()
+
+    def new_outputs(self, dx: bool = True, dw: bool = True) -> Dict[str, torch.Tensor]:
+        """loss and lse [N] fp32; dX [N, K] and dW (W's shape) bf16 where wanted,
+        their rows padded to a multiple of 8 in memory."""
+        dev = self.scratch.device
+
+        def mat(rows, cols):
+            return torch.empty(rows, -(-cols // 8) * 8, dtype=torch.bfloat16, device=dev)[:, :cols]
+
+        out = {k: torch.empty(self.N, dtype=torch.float32, device=dev) for k in ("loss", "lse")}
+        if dx:
+            out["dX"] = mat(self.N, self.K)
+        if dw:
+            out["dW"] = mat(*self.w_shape)
+        return out
+
+    def _inputs(self, X, W, target, U):
+        bf16 = torch.bfloat16
+        d = LceDims(self.N, self.K, self.V, LAYOUTS[self.layout], 0, 0, 0, 0, 0)
+        px, d.ldx = _rows(X, (self.N, self.K), bf16, "X")
+        pw, d.ldw = _rows(W, self.w_shape, bf16, "W")
+        pu = C.c_void_p(0)
+        if U is not None:
+            pu, d.ldu = _rows(U, (self.N, self.V), torch.float32, "U")
+        return d, (px, pw, pu, _vec(target, self.N, torch.int32, "target"))
+
+    def forward(self, X, W, target, U=None, out=None, stream=None):
+        """loss and lse of every row."""
+        out = self.new_outputs(False, False) if out is None else out
+        d, ins = self._inputs(X, W, target, U)
+        f32 = torch.float32
+        code = self.lib.dspark_linear_ce(C.byref(d), *ins, _vec(out["loss"], self.N, f32, "loss"),
+                                         _vec(out["lse"], self.N, f32, "lse"), C.c_void_p(self.scratch.data_ptr()),
+                                         C.c_void_p(self.status.data_ptr()), _stream(stream))
+        _check(code, "dspark_linear_ce")
+        return out
+
+    def grad(self, X, W, target, lse, wt=None, scale: float = 1.0, U=None, out=None, stream=None):
+        """Gradients of scale * sum_n wt[n] loss[n] with lse from ``forward``,
+        into out["dX"] and out["dW"] (the ones that ``out`` has)."""
+        out = self.new_outputs() if out is None else out
+        d, ins = self._inputs(X, W, target, U)
+        f32, bf16 = torch.float32, torch.bfloat16
+        px = pw = C.c_void_p(0)
+        if out.get("dX") is not None:
+            px, d.lddx = _rows(out["dX"], (self.N, self.K), bf16, "dX")
+        if out.get("dW") is not None:
+            pw, d.lddw = _rows(out["dW"], self.w_shape, bf16, "dW")
+        code = self.lib.dspark_linear_ce_grad(C.byref(d), *ins, _vec(lse, self.N, f32, "lse"),
+                                              _vec(wt, self.N, f32, "wt"), float(scale), px, pw,
+                                              C.c_void_p(self.scratch.data_ptr()),
+                                              C.c_void_p(self.status.data_ptr()), _stream(stream))
+        _check(code, "dspark_linear_ce_grad")
         return out
