@@ -431,6 +431,53 @@ dspark_status dspark_linear_ce_grad(const dspark_lce_dims* dims, const void* X, 
                                     void* dW, void* scratch, int32_t* device_status, dspark_stream_t stream);
 size_t dspark_linear_ce_scratch_bytes(const dspark_lce_dims* dims);
 
+/*
+ * Rows of a table looked up by token, and the table's gradient (eq. (4)'s
+ * W1[x_{k-1}], or any embedding):
+ *   dspark_embed        out[n] = scale * E[idx[n]],  n < N
+ *   dspark_embed_grad   dE[v] = base[v] + scale * sum over n with idx[n] = v of dout[n],  v < V
+ * E [V][lde] and out [N][ldo] share a type, dout [N][ldd] has `type`, dE
+ * [V][lde] and base [V][ldb] have `grad_type`. base may be NULL (0), another
+ * matrix, or dE itself: then only the rows of tokens that occur are touched.
+ * Products and sums are fp32, rounded once. Each sum runs over its rows in
+ * increasing n in a fixed grouping (rows are sorted by token), so results are the same from call to
+ * call. idx[n] = -1 looks up a row of zeros and has no part in the gradient;
+ * any other value outside [0, V) does the same and sets DSPARK_ERANGE in
+ * *device_status (the caller's int32; the first error is kept until the
+ * caller clears it). Any leading dimension of at least D and any base address
+ * on the type's own size will do; rows on 16 bytes run faster. Outputs must
+ * not overlap inputs (but for base == dE with ldb == lde). 0 <= N <= 2^24,
+ * V <= 2^24, D <= 2^20, else DSPARK_EINVAL. scratch: dspark_embed_grad_scratch_bytes(N,
+ * V, D) bytes, 256-byte aligned. Asynchronous on `stream`.
+ */
+dspark_status dspark_embed(const void* E, dspark_wdtype type, int64_t lde, int V, int D, const int32_t* idx, int N,
+                           float scale, void* out, int64_t ldo, int32_t* device_status, dspark_stream_t stream);
+dspark_status dspark_embed_grad(const void* dout, dspark_wdtype type, int64_t ldd, const int32_t* idx, int N, int V,
+                                int D, float scale, const void* base, int64_t ldb, void* dE, dspark_wdtype grad_type,
+                                int64_t lde, void* scratch, int32_t* device_status, dspark_stream_t stream);
+size_t dspark_embed_grad_scratch_bytes(int N, int V, int D);
+
+/*
+ * The 2-norm over `count` gradient tensors together, and the tensors scaled
+ * to a largest norm:
+ *   *norm = sqrt(sum over tensors and values of x^2),
+ *   out_i = in_i * min(1, max_norm / (norm + 1e-6)).
+ * in, out, numel and types are HOST arrays of `count` entries (device
+ * pointers, values, dspark_wdtype), read before the call returns; out[i] may be
+ * in[i], and is left alone then if the norm is within max_norm. A tensor may be empty (its
+ * pointers are then not looked at). Squares are summed so that neither their
+ * overflow nor their underflow changes the norm. *norm is a device fp32. If it
+ * is not finite, the outputs are the inputs unscaled and *device_status (the caller's
+ * int32, first error kept) becomes DSPARK_ENUMERIC. max_norm >= 0 (infinity
+ * measures alone), else DSPARK_EINVAL. scratch:
+ * dspark_clip_grads_scratch_bytes(count) bytes, 8-byte aligned. Two launches for every 512
+ * tensors, asynchronous on `stream`; the result is the same from call to call.
+ */
+dspark_status dspark_clip_grads(int count, const void* const* in, void* const* out, const int64_t* numel,
+                                const int32_t* types, float max_norm, float* norm, void* scratch,
+                                int32_t* device_status, dspark_stream_t stream);
+size_t dspark_clip_grads_scratch_bytes(int count);
+
 #ifdef __cplusplus
 }
 #endif

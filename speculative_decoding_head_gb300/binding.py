@@ -10,7 +10,7 @@ from __future__ import annotations
 import ctypes as C
 import os
 import threading
-from typing import Dict, Optional
+from typing import Dict, Optional, Sequence
 
 import torch
 
@@ -29,6 +29,8 @@ SYMBOLS = [
     "dspark_pctree_scratch_bytes", "dspark_pctree_build", "dspark_pctree_verify",
     "dspark_ws_set_shard", "dspark_plan_shard",
     "dspark_linear_ce", "dspark_linear_ce_grad", "dspark_linear_ce_scratch_bytes",
+    "dspark_embed", "dspark_embed_grad", "dspark_embed_grad_scratch_bytes",
+    "dspark_clip_grads", "dspark_clip_grads_scratch_bytes",
 ]
 
 
@@ -118,6 +120,17 @@ def load() -> C.CDLL:
         lib.dspark_linear_ce_grad.restype = i32
         lib.dspark_linear_ce_scratch_bytes.argtypes = [C.POINTER(LceDims)]
         lib.dspark_linear_ce_scratch_bytes.restype = C.c_size_t
+        i64, f = C.c_int64, C.c_float
+        lib.dspark_embed.argtypes = [P, i32, i64, i32, i32, P, i32, f, P, i64, P, P]
+        lib.dspark_embed.restype = i32
+        lib.dspark_embed_grad.argtypes = [P, i32, i64, P, i32, i32, i32, f, P, i64, P, i32, i64, P, P, P]
+        lib.dspark_embed_grad.restype = i32
+        lib.dspark_embed_grad_scratch_bytes.argtypes = [i32, i32, i32]
+        lib.dspark_embed_grad_scratch_bytes.restype = C.c_size_t
+        lib.dspark_clip_grads.argtypes = [i32, P, P, P, P, f, P, P, P, P]
+        lib.dspark_clip_grads.restype = i32
+        lib.dspark_clip_grads_scratch_bytes.argtypes = [i32]
+        lib.dspark_clip_grads_scratch_bytes.restype = C.c_size_t
         _lib = lib
         return lib
 
@@ -141,6 +154,14 @@ def _ptr(t: Optional[torch.Tensor], dtype=None, name="") -> C.c_void_p:
     if dtype is not None and t.dtype != dtype:
         raise DsparkError(f"{name} must be {dtype}, got {t.dtype}")
     return C.c_void_p(t.data_ptr())
+
+
+def _dtype_code(t: torch.Tensor, name: str) -> int:
+    if t.dtype == torch.bfloat16:
+        return 1
+    if t.dtype == torch.float32:
+        return 0
+    raise DsparkError(f"{name} must be bf16 or fp32, got {t.dtype}")
 
 
 def _rows(t: torch.Tensor, shape, dtype, name: str):
@@ -523,3 +544,105 @@ class LinearCE:
                                               C.c_void_p(self.status.data_ptr()), _stream(stream))
         _check(code, "dspark_linear_ce_grad")
         return out
+
+
+class Embedding:
+    """Rows of a table [V, D] looked up for N tokens and scaled
+    (``dspark_embed``), and the table's gradient (``dspark_embed_grad``).
+    Holds the gradient's scratch (made at its first call) and a status word; calls that share one
+    object must be ordered on one stream. Matrices are bf16 or fp32 with contiguous
+    rows; idx [N] int32, -1 for a row without a token."""
+
+    def __init__(self, N: int, V: int, D: int, device="cuda"):
+        self.lib = load()
+        self.N, self.V, self.D = int(N), int(V), int(D)
+        self._bytes = int(self.lib.dspark_embed_grad_scratch_bytes(self.N, self.V, self.D))
+        if self._bytes == 0:
+            raise DsparkError(f"dspark_embed: unsupported N={N}, V={V}, D={D}")
+        self.scratch: Optional[torch.Tensor] = None
+        self.status = torch.zeros(1, dtype=torch.int32, device=device)
+
+    def device_status(self) -> int:
+        """The first device error since the last reset (synchronises)."""
+        return int(self.status.item())
+
+    def reset(self) -> None:
+        self.status.zero_()
+
+    def _mat(self, t, rows, dtype, name):
+        ptr, ld = _rows(t, (rows, self.D), dtype, name)
+        return ptr, max(ld, self.D)
+
+    def lookup(self, E, idx, scale: float = 1.0, out=None, stream=None):
+        """scale * E[idx] as [N, D] in E's type (into ``out`` if given)."""
+        code = _dtype_code(E, "E")
+        if out is None:
+            out = torch.empty(self.N, self.D, dtype=E.dtype, device=E.device)
+        pe, lde = self._mat(E, self.V, E.dtype, "E")
+        po, ldo = self._mat(out, self.N, E.dtype, "out")
+        r = self.lib.dspark_embed(pe, code, lde, self.V, self.D, _vec(idx, self.N, torch.int32, "idx"), self.N,
+                                  float(scale), po, ldo, C.c_void_p(self.status.data_ptr()), _stream(stream))
+        _check(r, "dspark_embed")
+        return out
+
+    def grad(self, dout, idx, scale: float = 1.0, base=None, out=None, stream=None):
+        """base + scale * the rows of ``dout`` [N, D] summed per token, as
+        [V, D] into ``out`` (dout's type if not given). ``base`` has out's type;
+        it may be ``out`` itself."""
+        code = _dtype_code(dout, "dout")
+        if out is None:
+            out = torch.empty(self.V, self.D, dtype=dout.dtype if base is None else base.dtype, device=dout.device)
+        if self.scratch is None:
+            self.scratch = torch.empty(self._bytes, dtype=torch.uint8, device=self.status.device)
+        pd, ldd = self._mat(dout, self.N, dout.dtype, "dout")
+        po, ldo = self._mat(out, self.V, out.dtype, "out")
+        pb, ldb = (C.c_void_p(0), self.D) if base is None else self._mat(base, self.V, out.dtype, "base")
+        r = self.lib.dspark_embed_grad(pd, code, ldd, _vec(idx, self.N, torch.int32, "idx"), self.N, self.V, self.D,
+                                       float(scale), pb, ldb, po, _dtype_code(out, "out"), ldo,
+                                       C.c_void_p(self.scratch.data_ptr()), C.c_void_p(self.status.data_ptr()),
+                                       _stream(stream))
+        _check(r, "dspark_embed_grad")
+        return out
+
+
+class GradClip:
+    """The 2-norm over a list of gradient tensors and their scaling to a largest
+    norm (``dspark_clip_grads``), in place or into ``outs``. The object keeps
+    the list (and the scratch and status word): make it for the gradient buffers
+    that a training loop reuses. Tensors are contiguous, bf16 or fp32."""
+
+    def __init__(self, grads: Sequence[torch.Tensor], outs: Optional[Sequence[torch.Tensor]] = None):
+        self.lib = load()
+        self.grads = list(grads)
+        self.outs = self.grads if outs is None else list(outs)
+        if len(self.outs) != len(self.grads):
+            raise DsparkError(f"{len(self.grads)} gradients, {len(self.outs)} outputs")
+        for i, (g, o) in enumerate(zip(self.grads, self.outs)):
+            _ptr(g, None, f"grads[{i}]")
+            _ptr(o, g.dtype, f"outs[{i}]")
+            if o.shape != g.shape:
+                raise DsparkError(f"outs[{i}] must be {list(g.shape)}, got {list(o.shape)}")
+        n = self.count = len(self.grads)
+        self._in = (C.c_void_p * max(n, 1))(*[g.data_ptr() for g in self.grads])
+        self._out = (C.c_void_p * max(n, 1))(*[o.data_ptr() for o in self.outs])
+        self._numel = (C.c_int64 * max(n, 1))(*[g.numel() for g in self.grads])
+        self._types = (C.c_int32 * max(n, 1))(*[_dtype_code(g, f"grads[{i}]") for i, g in enumerate(self.grads)])
+        device = self.grads[0].device if n else "cuda"
+        self.scratch = torch.empty(int(self.lib.dspark_clip_grads_scratch_bytes(n)), dtype=torch.uint8, device=device)
+        self.norm = torch.zeros((), dtype=torch.float32, device=device)
+        self.status = torch.zeros(1, dtype=torch.int32, device=device)
+
+    def device_status(self) -> int:
+        """The first device error since the last reset (synchronises)."""
+        return int(self.status.item())
+
+    def reset(self) -> None:
+        self.status.zero_()
+
+    def clip(self, max_norm: float, stream=None) -> torch.Tensor:
+        """Scale the gradients; returns their norm before that (a device fp32 scalar)."""
+        code = self.lib.dspark_clip_grads(self.count, self._in, self._out, self._numel, self._types, float(max_norm),
+                                          C.c_void_p(self.norm.data_ptr()), C.c_void_p(self.scratch.data_ptr()),
+                                          C.c_void_p(self.status.data_ptr()), _stream(stream))
+        _check(code, "dspark_clip_grads")
+        return self.norm

@@ -1,0 +1,316 @@
+// k_clip.cu -- the 2-norm over many gradient tensors, and their scaling to a
+// largest norm:
+//   norm = sqrt(sum over tensors and values of x^2),
+//   out  = x * min(1, max_norm / (norm + 1e-6)).
+//
+// Two launches over the same list of pieces (32768 values of one tensor each):
+// the first leaves a partial sum of squares per CTA, the second adds those in
+// order (every CTA the same way) and scales, going through the pieces in
+// reverse so that what the first read last is still in L2. The list of tensors
+// travels in the kernel's parameters, so a call keeps nothing on the device.
+//
+// Squares are summed in fp32 over 16 or 32 values whose largest magnitude lies in
+// [2^-50, 2^60], where no square that counts is lost or overflows, and those
+// sums in fp64; other groups (and groups with an infinity) are squared in fp64.
+#include <math.h>
+#include <stdio.h>
+#include <string.h>
+
+#include "dspark_common.cuh"
+#include "dspark_internal.h"
+
+namespace dspark {
+
+namespace {
+
+constexpr int kClThreads = 256;
+constexpr int kClPiece = 32768;    // values of a piece
+constexpr int kClCtas = 152 * 4;   // CTAs of a full grid; partial sums of a launch
+constexpr int kClLaunch = 512;     // tensors of one launch
+
+struct ClTensor {
+  const void* in;
+  void* out;
+  long long n;
+  int first;   // index of its first piece
+  int bf16;
+};
+template <int MAXT>
+struct ClList {
+  ClTensor t[MAXT];
+  int count, pieces;
+};
+
+__device__ __forceinline__ float bf_lo(uint32_t x) { return __uint_as_float(x << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t x) { return __uint_as_float(x & 0xFFFF0000u); }
+
+// the tensor that piece i belongs to (tensors without values have no piece)
+template <int MAXT>
+__device__ __forceinline__ int cl_find(const ClList<MAXT>& l, int i) {
+  int lo = 0, hi = l.count - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (l.t[mid].first <= i)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  return lo;
+}
+
+// sum of squares of K values: fp32 where their range allows, else fp64
+template <int K>
+__device__ __forceinline__ double cl_squares(const float* x) {
+  float s[4] = {0.f, 0.f, 0.f, 0.f}, m = 0.f;
+#pragma unroll
+  for (int i = 0; i < K; ++i) {
+    s[i & 3] = fmaf(x[i], x[i], s[i & 3]);
+    m = fmaxf(m, fabsf(x[i]));
+  }
+  if (m == 0.f || (m >= 0x1p-50f && m <= 0x1p60f)) return (double)((s[0] + s[1]) + (s[2] + s[3]));
+  double d = 0.0;
+  for (int i = 0; i < K; ++i) d += (double)x[i] * (double)x[i];
+  return d;
+}
+
+template <int MAXT>
+__global__ void __launch_bounds__(kClThreads)
+    k_clip_norm(const __grid_constant__ ClList<MAXT> l, double* __restrict__ part) {
+  double acc = 0.0;
+  for (int i = blockIdx.x; i < l.pieces; i += gridDim.x) {
+    const ClTensor& t = l.t[cl_find(l, i)];
+    const long long off = (long long)(i - t.first) * kClPiece;
+    const int n = (int)min((long long)kClPiece, t.n - off);
+    int done = 0;
+    if (t.bf16) {
+      const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(t.in) + off;
+      if ((reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
+        const uint4* q = reinterpret_cast<const uint4*>(p);
+        const int m = n / 8;
+        for (int u = threadIdx.x; u < m; u += 4 * kClThreads) {
+          uint4 v[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            v[k] = u + k * kClThreads < m ? __ldg(q + u + k * kClThreads) : make_uint4(0, 0, 0, 0);
+          float x[32];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              x[k * 8 + 2 * e] = bf_lo(w[e]);
+              x[k * 8 + 2 * e + 1] = bf_hi(w[e]);
+            }
+          }
+          acc += cl_squares<32>(x);
+        }
+        done = m * 8;
+      }
+      for (int e = done + threadIdx.x; e < n; e += kClThreads) {
+        const float x[1] = {__bfloat162float(p[e])};
+        acc += cl_squares<1>(x);
+      }
+    } else {
+      const float* p = static_cast<const float*>(t.in) + off;
+      if ((reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
+        const float4* q = reinterpret_cast<const float4*>(p);
+        const int m = n / 4;
+        for (int u = threadIdx.x; u < m; u += 4 * kClThreads) {
+          float x[16];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float4 v = u + k * kClThreads < m ? __ldg(q + u + k * kClThreads) : make_float4(0.f, 0.f, 0.f, 0.f);
+            x[4 * k] = v.x;
+            x[4 * k + 1] = v.y;
+            x[4 * k + 2] = v.z;
+            x[4 * k + 3] = v.w;
+          }
+          acc += cl_squares<16>(x);
+        }
+        done = m * 4;
+      }
+      for (int e = done + threadIdx.x; e < n; e += kClThreads) {
+        const float x[1] = {p[e]};
+        acc += cl_squares<1>(x);
+      }
+    }
+  }
+  __shared__ double red[kClThreads];
+  red[threadIdx.x] = acc;
+  __syncthreads();
+  for (int o = kClThreads / 2; o > 0; o >>= 1) {
+    if ((int)threadIdx.x < o) red[threadIdx.x] += red[threadIdx.x + o];
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) part[blockIdx.x] = red[0];
+}
+
+template <int MAXT>
+__global__ void __launch_bounds__(kClThreads)
+    k_clip_scale(const __grid_constant__ ClList<MAXT> l, const double* __restrict__ part, int parts, float max_norm,
+                 int write_norm, float* __restrict__ norm_out, int* status) {
+  __shared__ double red[kClThreads];
+  double s = 0.0;
+  for (int i = threadIdx.x; i < parts; i += kClThreads) s += part[i];
+  red[threadIdx.x] = s;
+  __syncthreads();
+  for (int o = kClThreads / 2; o > 0; o >>= 1) {
+    if ((int)threadIdx.x < o) red[threadIdx.x] += red[threadIdx.x + o];
+    __syncthreads();
+  }
+  const double norm = sqrt(red[0]);
+  const float nf = (float)norm;
+  // a norm that is not finite scales nothing: the caller sees it and skips the step
+  const bool finite = isfinite(nf);
+  const float coef = finite ? (float)fmin(1.0, (double)max_norm / (norm + 1e-6)) : 1.f;
+  if (write_norm && blockIdx.x == 0 && threadIdx.x == 0) {
+    *norm_out = nf;
+    if (!finite) raise_status(status, DSPARK_ENUMERIC);
+  }
+  for (int i = l.pieces - 1 - (int)blockIdx.x; i >= 0; i -= gridDim.x) {
+    const ClTensor& t = l.t[cl_find(l, i)];
+    if (coef == 1.f && t.in == t.out) continue;  // in place and within the norm: nothing to do
+    const long long off = (long long)(i - t.first) * kClPiece;
+    const int n = (int)min((long long)kClPiece, t.n - off);
+    int done = 0;
+    if (t.bf16) {
+      const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(t.in) + off;
+      __nv_bfloat16* o = static_cast<__nv_bfloat16*>(t.out) + off;
+      if (((reinterpret_cast<uintptr_t>(p) | reinterpret_cast<uintptr_t>(o)) & 15u) == 0) {
+        const uint4* q = reinterpret_cast<const uint4*>(p);
+        uint4* r = reinterpret_cast<uint4*>(o);
+        const int m = n / 8;
+        for (int u = threadIdx.x; u < m; u += 4 * kClThreads) {
+          uint4 v[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (u + k * kClThreads < m) v[k] = q[u + k * kClThreads];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if (u + k * kClThreads >= m) break;
+            uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const __nv_bfloat162 b = __floats2bfloat162_rn(coef * bf_lo(w[e]), coef * bf_hi(w[e]));
+              w[e] = *reinterpret_cast<const uint32_t*>(&b);
+            }
+            r[u + k * kClThreads] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+        done = m * 8;
+      }
+      for (int e = done + threadIdx.x; e < n; e += kClThreads) o[e] = __float2bfloat16_rn(coef * __bfloat162float(p[e]));
+    } else {
+      const float* p = static_cast<const float*>(t.in) + off;
+      float* o = static_cast<float*>(t.out) + off;
+      if (((reinterpret_cast<uintptr_t>(p) | reinterpret_cast<uintptr_t>(o)) & 15u) == 0) {
+        const float4* q = reinterpret_cast<const float4*>(p);
+        float4* r = reinterpret_cast<float4*>(o);
+        const int m = n / 4;
+        for (int u = threadIdx.x; u < m; u += 4 * kClThreads) {
+          float4 v[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (u + k * kClThreads < m) v[k] = q[u + k * kClThreads];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if (u + k * kClThreads >= m) break;
+            r[u + k * kClThreads] = make_float4(coef * v[k].x, coef * v[k].y, coef * v[k].z, coef * v[k].w);
+          }
+        }
+        done = m * 4;
+      }
+      for (int e = done + threadIdx.x; e < n; e += kClThreads) o[e] = coef * p[e];
+    }
+  }
+}
+
+int cl_launches(int count) { return count > 0 ? (count + kClLaunch - 1) / kClLaunch : 1; }
+
+// the tensors [a, b) of the call as a launch's list
+template <int MAXT>
+bool cl_list(ClList<MAXT>& l, const void* const* in, void* const* out, const int64_t* numel, const int32_t* types,
+             int a, int b) {
+  memset(&l, 0, sizeof(l));
+  long long at = 0;
+  for (int i = a; i < b; ++i) {
+    if (numel[i] == 0) continue;
+    ClTensor& t = l.t[l.count++];
+    t.in = in[i];
+    t.out = out[i];
+    t.n = numel[i];
+    t.first = (int)at;
+    t.bf16 = types[i] == DSPARK_BF16;
+    at += (numel[i] + kClPiece - 1) / kClPiece;
+    if (at > 0x7FFF0000ll) return false;
+  }
+  l.pieces = (int)at;
+  return true;
+}
+
+template <int MAXT>
+cudaError_t cl_run(bool scale, const ClList<MAXT>& l, double* part, int parts, float max_norm, bool last, float* norm,
+                   int* status, cudaStream_t st) {
+  const int grid = l.pieces < 1 ? 1 : l.pieces < kClCtas ? l.pieces : kClCtas;
+  if (scale)
+    k_clip_scale<MAXT><<<grid, kClThreads, 0, st>>>(l, part, parts, max_norm, last ? 1 : 0, norm, status);
+  else
+    k_clip_norm<MAXT><<<grid, kClThreads, 0, st>>>(l, part);
+  return cudaGetLastError();
+}
+
+int cl_grid(int64_t pieces) { return pieces < 1 ? 1 : pieces < kClCtas ? (int)pieces : kClCtas; }
+
+}  // namespace
+
+}  // namespace dspark
+
+using namespace dspark;
+
+extern "C" size_t dspark_clip_grads_scratch_bytes(int count) {
+  if (count < 0) return 0;
+  return sizeof(double) * (size_t)kClCtas * cl_launches(count);
+}
+
+extern "C" dspark_status dspark_clip_grads(int count, const void* const* in, void* const* out, const int64_t* numel,
+                                           const int32_t* types, float max_norm, float* norm, void* scratch,
+                                           int32_t* device_status, dspark_stream_t stream) {
+  if (count < 0 || (count > 0 && (!in || !out || !numel || !types))) return DSPARK_EINVAL;
+  if (!norm || !scratch || !device_status || (reinterpret_cast<uintptr_t>(scratch) & 7u) != 0) return DSPARK_EINVAL;
+  if (!(max_norm >= 0.f)) return DSPARK_EINVAL;
+  for (int i = 0; i < count; ++i) {
+    if (types[i] != DSPARK_F32 && types[i] != DSPARK_BF16) return DSPARK_EINVAL;
+    if (numel[i] < 0 || (numel[i] > 0 && (!in[i] || !out[i]))) return DSPARK_EINVAL;
+    const uintptr_t mask = types[i] == DSPARK_BF16 ? 1u : 3u;
+    if (((reinterpret_cast<uintptr_t>(in[i]) | reinterpret_cast<uintptr_t>(out[i])) & mask) != 0) return DSPARK_EINVAL;
+    if (numel[i] > ((int64_t)1 << 44)) return DSPARK_EINVAL;
+  }
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  double* part = static_cast<double*>(scratch);
+  const int launches = cl_launches(count);
+  cudaError_t e = cudaSuccess;
+  if (count <= 32) {
+    ClList<32> l;
+    if (!cl_list(l, in, out, numel, types, 0, count)) return DSPARK_EUNSUPPORTED;
+    e = cl_run(false, l, part, 0, max_norm, false, norm, device_status, st);
+    if (e == cudaSuccess) e = cl_run(true, l, part, cl_grid(l.pieces), max_norm, true, norm, device_status, st);
+  } else {
+    // every launch's partial sums in one run, then the scaling launches on all of them
+    ClList<kClLaunch> l;
+    int parts = 0;
+    for (int k = 0; k < launches && e == cudaSuccess; ++k) {
+      const int a = k * kClLaunch, b = a + kClLaunch < count ? a + kClLaunch : count;
+      if (!cl_list(l, in, out, numel, types, a, b)) return DSPARK_EUNSUPPORTED;
+      e = cl_run(false, l, part + parts, 0, max_norm, false, norm, device_status, st);
+      parts += cl_grid(l.pieces);
+    }
+    for (int k = launches - 1; k >= 0 && e == cudaSuccess; --k) {
+      const int a = k * kClLaunch, b = a + kClLaunch < count ? a + kClLaunch : count;
+      if (!cl_list(l, in, out, numel, types, a, b)) return DSPARK_EUNSUPPORTED;
+      e = cl_run(true, l, part, parts, max_norm, k == launches - 1, norm, device_status, st);
+    }
+  }
+  if (e == cudaSuccess) return DSPARK_OK;
+  fprintf(stderr, "dspark: CUDA error %s\n", cudaGetErrorString(e));
+  return DSPARK_ECUDA;
+}

@@ -633,7 +633,6 @@ dspark_status check_inputs(const dspark_lce_dims* d, const void* X, const void* 
   if (!scratch || (reinterpret_cast<uintptr_t>(scratch) & 255u) != 0) return DSPARK_EINVAL;
   if (!ld_ok(d->ldx, d->K, 8) || !ld_ok(d->ldw, d->layout == DSPARK_W_VK ? d->K : d->V, 8)) return DSPARK_EINVAL;
   if (U && (!aligned16(U) || !ld_ok(d->ldu, d->V, 4))) return DSPARK_EINVAL;
-  if (!encode_fn()) return DSPARK_ECUDA;
   return DSPARK_OK;
 }
 
@@ -655,6 +654,7 @@ extern "C" dspark_status dspark_linear_ce(const dspark_lce_dims* d, const void* 
   const dspark_status bad = check_inputs(d, X, W, U, target, scratch, device_status);
   if (bad != DSPARK_OK) return bad;
   if (d->N > 0 && (!aligned16(loss) || !aligned16(lse))) return DSPARK_EINVAL;
+  if (!encode_fn()) return DSPARK_ECUDA;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (d->N == 0) return DSPARK_OK;
   const LcPlan p = make_plan(*d);
@@ -685,6 +685,7 @@ extern "C" dspark_status dspark_linear_ce_grad(const dspark_lce_dims* d, const v
   if (!dX && !dW) return DSPARK_EINVAL;
   if (dX && (!aligned16(dX) || !ld_ok(d->lddx, d->K, 8))) return DSPARK_EINVAL;
   if (dW && (!aligned16(dW) || !ld_ok(d->lddw, vk ? d->K : d->V, 8))) return DSPARK_EINVAL;
+  if (!encode_fn()) return DSPARK_ECUDA;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
   if (d->N == 0) {  // no rows: dW is zero
