@@ -404,11 +404,11 @@ dspark_status dspark_pctree_verify(dspark_ws* ws, const float* P, const int32_t*
  * other value outside [0, V) does the same and sets DSPARK_ERANGE in
  * *device_status, the caller's int32, which keeps its first error until the
  * caller clears it. U may hold -inf, or
- * the type's lowest value, where a token is masked (with U, z <= -1e30 counts
- * as -inf): its probability is 0, and a row whose target is masked has loss
+ * the type's lowest value, where a token is masked (z <= -1e29 counts as
+ * -inf): its probability is 0, and a row whose target is masked has loss
  * +inf. A row with every token masked has lse -inf, loss +inf (0 if
- * left out) and no part in the gradients. +inf and NaN make their row's
- * results NaN. N = 0 is allowed (dW is then 0). 0 <= N <= 2^20, K <= 65536,
+ * left out) and no part in the gradients. NaN and z above 1e38 make their
+ * row's results NaN. N = 0 is allowed (dW is then 0). 0 <= N <= 2^20, K <= 65536,
  * V <= 2^24, else DSPARK_EINVAL. Asynchronous on `stream`; each result is the same
  * from call to call.
  */

@@ -164,24 +164,32 @@ def _dtype_code(t: torch.Tensor, name: str) -> int:
     raise DsparkError(f"{name} must be bf16 or fp32, got {t.dtype}")
 
 
-def _rows(t: torch.Tensor, shape, dtype, name: str):
-    """Pointer and leading dimension of a matrix whose rows are contiguous."""
-    if not t.is_cuda:
-        raise DsparkError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
-        raise DsparkError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise DsparkError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    rows, cols = t.shape
-    if cols > 1 and rows > 0 and t.stride(1) != 1:
+def _rows(t: torch.Tensor, rows: int, cols: int, dtype, name: str):
+    """Address and leading dimension of a matrix whose rows are contiguous."""
+    if t.dtype != dtype or not t.is_cuda or t.dim() != 2:
+        raise DsparkError(f"{name} must be a CUDA matrix of {dtype}, got {list(t.shape)} {t.dtype} on {t.device}")
+    r, c = t.shape
+    if r != rows or c != cols:
+        raise DsparkError(f"{name} must be [{rows}, {cols}], got {list(t.shape)}")
+    ld, step = t.stride()
+    if step != 1 and c > 1:
         raise DsparkError(f"{name} must have contiguous rows")
-    return C.c_void_p(t.data_ptr()), (t.stride(0) if rows > 1 else -(-max(cols, 1) // 8) * 8)
+    return t.data_ptr(), (ld if r > 1 else -(-c // 8) * 8)
 
 
-def _vec(t: Optional[torch.Tensor], n: int, dtype, name: str) -> C.c_void_p:
-    if t is not None and tuple(t.shape) != (n,):
-        raise DsparkError(f"{name} must be [{n}], got {list(t.shape)}")
-    return _ptr(t, dtype, name)
+def _vec(t: Optional[torch.Tensor], n: int, dtype, name: str):
+    """Address of a contiguous vector of n values (None: no vector)."""
+    if t is None:
+        return None
+    if t.dtype != dtype or not t.is_cuda or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        raise DsparkError(f"{name} must be a contiguous CUDA vector [{n}] of {dtype}, got {list(t.shape)} {t.dtype} "
+                          f"on {t.device}")
+    return t.data_ptr()
+
+
+def _raw_stream(stream, device: int) -> int:
+    """Address of the stream (the current one of the device if None)."""
+    return torch.cuda.current_stream(device).cuda_stream if stream is None else stream.cuda_stream
 
 
 def _stream(stream) -> C.c_void_p:
@@ -506,24 +514,26 @@ class LinearCE:
             out["dW"] = mat(*self.w_shape)
         return out
 
-    def _inputs(self, X, W, target, U):
-        bf16 = torch.bfloat16
-        d = LceDims(self.N, self.K, self.V, LAYOUTS[self.layout], 0, 0, 0, 0, 0)
-        px, d.ldx = _rows(X, (self.N, self.K), bf16, "X")
-        pw, d.ldw = _rows(W, self.w_shape, bf16, "W")
-        pu = C.c_void_p(0)
+    def _inputs(self, d, X, W, target, U):
+        px, d.ldx = _rows(X, self.N, self.K, torch.bfloat16, "X")
+        pw, d.ldw = _rows(W, *self.w_shape, torch.bfloat16, "W")
+        pu = None
         if U is not None:
-            pu, d.ldu = _rows(U, (self.N, self.V), torch.float32, "U")
-        return d, (px, pw, pu, _vec(target, self.N, torch.int32, "target"))
+            pu, d.ldu = _rows(U, self.N, self.V, torch.float32, "U")
+        return px, pw, pu, _vec(target, self.N, torch.int32, "target")
+
+    def _dims(self):
+        return LceDims(self.N, self.K, self.V, LAYOUTS[self.layout], 0, 0, 0, 0, 0)
 
     def forward(self, X, W, target, U=None, out=None, stream=None):
         """loss and lse of every row."""
         out = self.new_outputs(False, False) if out is None else out
-        d, ins = self._inputs(X, W, target, U)
+        d = self._dims()
+        ins = self._inputs(d, X, W, target, U)
         f32 = torch.float32
         code = self.lib.dspark_linear_ce(C.byref(d), *ins, _vec(out["loss"], self.N, f32, "loss"),
-                                         _vec(out["lse"], self.N, f32, "lse"), C.c_void_p(self.scratch.data_ptr()),
-                                         C.c_void_p(self.status.data_ptr()), _stream(stream))
+                                         _vec(out["lse"], self.N, f32, "lse"), self.scratch.data_ptr(),
+                                         self.status.data_ptr(), _raw_stream(stream, X.device.index))
         _check(code, "dspark_linear_ce")
         return out
 
@@ -531,17 +541,17 @@ class LinearCE:
         """Gradients of scale * sum_n wt[n] loss[n] with lse from ``forward``,
         into out["dX"] and out["dW"] (the ones that ``out`` has)."""
         out = self.new_outputs() if out is None else out
-        d, ins = self._inputs(X, W, target, U)
+        d = self._dims()
+        ins = self._inputs(d, X, W, target, U)
         f32, bf16 = torch.float32, torch.bfloat16
-        px = pw = C.c_void_p(0)
+        px = pw = None
         if out.get("dX") is not None:
-            px, d.lddx = _rows(out["dX"], (self.N, self.K), bf16, "dX")
+            px, d.lddx = _rows(out["dX"], self.N, self.K, bf16, "dX")
         if out.get("dW") is not None:
-            pw, d.lddw = _rows(out["dW"], self.w_shape, bf16, "dW")
+            pw, d.lddw = _rows(out["dW"], *self.w_shape, bf16, "dW")
         code = self.lib.dspark_linear_ce_grad(C.byref(d), *ins, _vec(lse, self.N, f32, "lse"),
-                                              _vec(wt, self.N, f32, "wt"), float(scale), px, pw,
-                                              C.c_void_p(self.scratch.data_ptr()),
-                                              C.c_void_p(self.status.data_ptr()), _stream(stream))
+                                              _vec(wt, self.N, f32, "wt"), scale, px, pw, self.scratch.data_ptr(),
+                                              self.status.data_ptr(), _raw_stream(stream, X.device.index))
         _check(code, "dspark_linear_ce_grad")
         return out
 
@@ -570,8 +580,7 @@ class Embedding:
         self.status.zero_()
 
     def _mat(self, t, rows, dtype, name):
-        ptr, ld = _rows(t, (rows, self.D), dtype, name)
-        return ptr, max(ld, self.D)
+        return _rows(t, rows, self.D, dtype, name)
 
     def lookup(self, E, idx, scale: float = 1.0, out=None, stream=None):
         """scale * E[idx] as [N, D] in E's type (into ``out`` if given)."""
@@ -581,7 +590,7 @@ class Embedding:
         pe, lde = self._mat(E, self.V, E.dtype, "E")
         po, ldo = self._mat(out, self.N, E.dtype, "out")
         r = self.lib.dspark_embed(pe, code, lde, self.V, self.D, _vec(idx, self.N, torch.int32, "idx"), self.N,
-                                  float(scale), po, ldo, C.c_void_p(self.status.data_ptr()), _stream(stream))
+                                  scale, po, ldo, self.status.data_ptr(), _raw_stream(stream, E.device.index))
         _check(r, "dspark_embed")
         return out
 
@@ -596,11 +605,10 @@ class Embedding:
             self.scratch = torch.empty(self._bytes, dtype=torch.uint8, device=self.status.device)
         pd, ldd = self._mat(dout, self.N, dout.dtype, "dout")
         po, ldo = self._mat(out, self.V, out.dtype, "out")
-        pb, ldb = (C.c_void_p(0), self.D) if base is None else self._mat(base, self.V, out.dtype, "base")
+        pb, ldb = (None, self.D) if base is None else self._mat(base, self.V, out.dtype, "base")
         r = self.lib.dspark_embed_grad(pd, code, ldd, _vec(idx, self.N, torch.int32, "idx"), self.N, self.V, self.D,
-                                       float(scale), pb, ldb, po, _dtype_code(out, "out"), ldo,
-                                       C.c_void_p(self.scratch.data_ptr()), C.c_void_p(self.status.data_ptr()),
-                                       _stream(stream))
+                                       scale, pb, ldb, po, _dtype_code(out, "out"), ldo, self.scratch.data_ptr(),
+                                       self.status.data_ptr(), _raw_stream(stream, dout.device.index))
         _check(r, "dspark_embed_grad")
         return out
 
@@ -641,8 +649,8 @@ class GradClip:
 
     def clip(self, max_norm: float, stream=None) -> torch.Tensor:
         """Scale the gradients; returns their norm before that (a device fp32 scalar)."""
-        code = self.lib.dspark_clip_grads(self.count, self._in, self._out, self._numel, self._types, float(max_norm),
-                                          C.c_void_p(self.norm.data_ptr()), C.c_void_p(self.scratch.data_ptr()),
-                                          C.c_void_p(self.status.data_ptr()), _stream(stream))
+        code = self.lib.dspark_clip_grads(self.count, self._in, self._out, self._numel, self._types, max_norm,
+                                          self.norm.data_ptr(), self.scratch.data_ptr(), self.status.data_ptr(),
+                                          _raw_stream(stream, self.norm.device.index))
         _check(code, "dspark_clip_grads")
         return self.norm

@@ -41,44 +41,58 @@ namespace {
 constexpr int kLcTile = 256;     // rows and columns of a pair's tile
 constexpr int kLcHalf = 128;     // rows (A) and columns (B) one CTA loads
 constexpr int kLcKb = 64;        // contraction depth of a stage (one 128-byte swizzled row)
-constexpr int kLcStages = 6;
 constexpr int kLcOpBytes = kLcHalf * kLcKb * 2;   // 16 KB: one operand's half of a stage
 constexpr int kLcStageBytes = 2 * kLcOpBytes;
 constexpr int kLcBox = 64 * kLcKb * 2;            // 8 KB: a 64 x 64 box of an MN-major operand
-constexpr int kLcEpiWarps = 8;
+// Epilogue warps: two groups that take tiles in turn (one accumulator each), so
+// that one's latencies lie under the other's arithmetic; in a group two warps
+// per TMEM lane quarter, 128 columns each in parts of 32.
+constexpr int kLcEpiWarps = 16;
+constexpr int kLcGroupWarps = 8;
+constexpr int kLcWarpCols = 128;
+constexpr int kLcPart = 32;
 constexpr int kLcThreads = 32 * (2 + kLcEpiWarps);
 constexpr int kLcTmemCols = 512;                  // two accumulators of 256 columns
-constexpr size_t kLcSmem = (size_t)kLcStages * kLcStageBytes + 1024 + 256;
+// Operand ring: six stages, or three and two 32 x 32 fp32 boxes of U per epilogue warp.
+constexpr int kLcMaxStages = 6, kLcStagesU = 3;
+constexpr int kLcUBox = 32 * kLcPart * 4;         // 4 KB
+constexpr int kLcUWarp = 2 * kLcUBox;
+constexpr int kLcUBytes = kLcUWarp * kLcEpiWarps;
+constexpr int kLcRing = kLcMaxStages * kLcStageBytes > kLcStagesU * kLcStageBytes + kLcUBytes
+                            ? kLcMaxStages * kLcStageBytes
+                            : kLcStagesU * kLcStageBytes + kLcUBytes;
+constexpr int kLcAhead = 16;                      // tiles announced: the producer is at most 6 + 2 + 2 ahead
+constexpr int kLcBars = 2 * kLcMaxStages + 5 + 2 * kLcEpiWarps + kLcAhead + 1;
+constexpr int kLcBarBytes = 16 * kLcAhead + 8 * kLcBars + 16;
+static_assert(kLcBars % 2 == 0, "16-byte ring entries");
+constexpr size_t kLcSmem = (size_t)kLcRing + 1024 + kLcBarBytes;
+static_assert(kLcSmem <= 232448, "one CTA's shared memory");
 constexpr int kLcPairs = 76;                      // CTA pairs of a full grid (152 SMs)
-
-constexpr float kLcMasked = -1e30f;
-
-enum : int { kLcStats = 0, kLcG = 1, kLcOut = 2 };
+constexpr float kLcRefMin = -1e29f;               // least log2 reference: what lies below it counts as masked
 
 // One product C[M][Nn] = A B^T over a contraction of nkb blocks of 64.
 struct LcJob {
-  CUtensorMap ta, tb;
-  int mode;
+  CUtensorMap ta, tb, tu;
   int M, Nn;            // rows and columns of the result
-  int nkb;              // contraction blocks in all
-  int slices, per;      // contraction slices and the blocks of each
+  int nkb;              // contraction blocks
   int mt, nt;           // tiles of 256 rows, of 256 columns
+  int split;            // pairs that share the tiles' blocks evenly (0: whole tiles)
   int a_mn, b_mn;       // operand's contraction index is its row (MN-major)
-  int a_k0, b_k0;       // contraction offset in the operand's map
-  int b_n0;             // column offset in B's map (and of U)
-  // kLcStats, kLcG
-  const float* U;
-  int64_t ldu;
+  int b_k0;             // contraction offset in B's map
+  int b_n0;             // column offset in B's map (and in U's)
+  // logits (statistics, G)
+  int has_u;
+  int V;                // vocabulary
   const int32_t* target;
   const float* lse;
   const float* wt;
-  float2* part;         // [2 nt][M] (max, sum exp) per half tile
+  float2* part;         // [M][2 nt] (log2 reference, sum of 2^(z log2 e - reference)) per half tile
   float* zt;            // [M] z at the target
   __nv_bfloat16* G;     // [M][ldg] the piece's G
   int64_t ldg;
-  int V;                // vocabulary
-  // kLcOut
-  float* acc;           // [slices][M][lda] fp32 partial results, or null
+  // gradients
+  float* slots;         // [2 split][256][256] parts of tiles that several pairs share
+  float* acc;           // [M][lda] sums so far, or null
   int64_t lda;
   int acc_in;           // add what acc holds
   __nv_bfloat16* out;   // [M][ldo] the result, or null: acc is written
@@ -86,9 +100,14 @@ struct LcJob {
   float scale;
 };
 
+// The jobs of a launch: the statistics alone (in place 0), or the gradient's,
+// each in a place of its own (a launch may lack some: no tiles, no split), so
+// that the epilogue finds its job's values at fixed parameter addresses.
+enum : int { kLcDx = 0, kLcDw = 1, kLcMakeG = 2, kLcJobs = 3 };
 struct LcParams {
-  LcJob job;
-  int tiles;
+  LcJob job[kLcJobs];
+  int tiles[kLcJobs];   // whole tiles of jobs 0 .. i (running totals; split jobs add none)
+  int stages;
   int* status;
 };
 
@@ -102,59 +121,134 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&b);
 }
 
-// Tile index -> (row tile, column tile, slice): slices outermost, then column
-// tiles, with up to 16 row tiles innermost, so that the tiles in flight share
-// their columns' operand in L2.
-__device__ __forceinline__ void lc_tile(const LcJob& j, int t, int& m, int& n, int& s) {
-  const int per = j.mt * j.nt;
-  s = t / per;
-  t -= s * per;
-  const int g = t / (16 * j.nt), gm = min(16, j.mt - g * 16);
-  t -= g * 16 * j.nt;
-  n = t / gm;
-  m = g * 16 + t - n * gm;
+// first block of pair p's share of `units` blocks split over `split` pairs
+__host__ __device__ __forceinline__ int lc_share(int units, int split, int p) {
+  return (int)((long long)units * p / split);
 }
 
-// columns of B the MMA takes for a tile: a multiple of 32
-__device__ __forceinline__ int lc_cols(const LcJob& j, int n) {
-  return min(kLcTile, (j.Nn - n * kLcTile + 31) & ~31);
-}
+// What a pair works on next: its share of the split jobs, then whole tiles of
+// the others, one in npairs. The producer goes through it and announces each
+// tile to its CTA's other warps.
+struct LcWork {
+  int job, m, n, kb0, kb1;
+  int slot;  // part of a shared tile: its slot; -1: a whole tile
+};
+struct LcIter {
+  int j, u, uend, t;
+  __device__ __forceinline__ LcIter(int pair) : j(-1), u(0), uend(0), t(pair) {}
+  __device__ __forceinline__ bool next(const LcParams& p, int pair, int npairs, LcWork& w) {
+    while (u >= uend && j + 1 < kLcJobs) {
+      ++j;
+      const LcJob& q = p.job[j];
+      if (q.split > pair) {
+        const int units = q.mt * q.nt * q.nkb;
+        u = lc_share(units, q.split, pair);
+        uend = lc_share(units, q.split, pair + 1);
+      }
+    }
+    int tile;
+    if (u < uend) {
+      const LcJob& q = p.job[j];
+      w.job = j;
+      tile = u / q.nkb;
+      w.kb0 = u - tile * q.nkb;
+      w.kb1 = min(q.nkb, w.kb0 + uend - u);
+      u += w.kb1 - w.kb0;
+      w.slot = w.kb0 == 0 && w.kb1 == q.nkb ? -1 : 2 * pair + (w.kb0 == 0 ? 1 : 0);
+    } else {
+      if (t >= p.tiles[kLcJobs - 1]) return false;
+      int k = 0, before = 0;
+      while (t >= p.tiles[k]) before = p.tiles[k++];
+      w.job = k;
+      w.kb0 = 0;
+      w.kb1 = p.job[k].nkb;
+      w.slot = -1;
+      tile = t - before;
+      t += npairs;
+    }
+    // column tiles outermost, up to 16 row tiles innermost, so that the tiles
+    // in flight share their columns' operand in L2
+    const LcJob& q = p.job[w.job];
+    int g = 0, gm = q.mt;
+    if (gm > 16) {
+      g = tile / (16 * q.nt);
+      gm = min(16, gm - g * 16);
+      tile -= g * 16 * q.nt;
+    }
+    w.n = tile / gm;
+    w.m = g * 16 + tile - w.n * gm;
+    return true;
+  }
+};
 
+// An announced tile: job and slot + 1 (x; -1: no more), row tile, column tile,
+// blocks of the contraction.
+struct LcTile {
+  int job, slot, m, n, nkb;
+  __device__ __forceinline__ LcTile() {}
+  __device__ __forceinline__ explicit LcTile(int4 a) : job(a.x & 3), slot((a.x >> 2) - 1), m(a.y), n(a.z), nkb(a.w) {}
+  static __device__ __forceinline__ int4 pack(const LcWork& w) {
+    return make_int4(w.job | (w.slot + 1) << 2, w.m, w.n, w.kb1 - w.kb0);
+  }
+};
+
+// columns of B the MMA takes for a tile of a result of Nn columns: a multiple of 32
+__device__ __forceinline__ int lc_cols(int Nn, int n) { return min(kLcTile, (Nn - n * kLcTile + 31) & ~31); }
+
+// ring position and the parity of its pass
+struct LcRing {
+  int s, ph;
+  __device__ __forceinline__ void step(int stages) {
+    if (++s == stages) {
+      s = 0;
+      ph ^= 1;
+    }
+  }
+};
+
+template <bool GRAD>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
     k_lce(const __grid_constant__ LcParams p) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t sbase = tc::smem_u32(smem);
-  const uint32_t bars = sbase + kLcStages * kLcStageBytes;
+  const uint32_t bars = sbase + kLcRing;
   auto full = [&](int s) { return bars + 8u * s; };
-  auto empty = [&](int s) { return bars + 8u * (kLcStages + s); };
-  auto tfull = [&](int b) { return bars + 8u * (2 * kLcStages + b); };
-  auto tempty = [&](int b) { return bars + 8u * (2 * kLcStages + 2 + b); };
-  const uint32_t drain = bars + 8u * (2 * kLcStages + 4);
-  unsigned char* tail = smem + kLcStages * kLcStageBytes + 8 * (2 * kLcStages + 5);
+  auto empty = [&](int s) { return bars + 8u * (kLcMaxStages + s); };
+  auto tfull = [&](int b) { return bars + 8u * (2 * kLcMaxStages + b); };
+  auto tempty = [&](int b) { return bars + 8u * (2 * kLcMaxStages + 2 + b); };
+  const uint32_t drain = bars + 8u * (2 * kLcMaxStages + 4);
+  auto ufull = [&](int w, int b) { return bars + 8u * (2 * kLcMaxStages + 5 + 2 * w + b); };
+  auto told = [&](int i) { return bars + 8u * (2 * kLcMaxStages + 5 + 2 * kLcEpiWarps + (i & (kLcAhead - 1))); };
+  int4* tile_ring = reinterpret_cast<int4*>(smem + kLcRing + 8 * kLcBars);
+  unsigned char* tail = reinterpret_cast<unsigned char*>(tile_ring + kLcAhead);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(tail);
   volatile int* abort = reinterpret_cast<volatile int*>(tail + 8);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = tc::cluster_ctarank();
   const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
-  const LcJob& j = p.job;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kLcStages; ++s) {
+    for (int s = 0; s < kLcMaxStages; ++s) {
       tc::mbar_init(full(s), 1);
       tc::mbar_init(empty(s), 1);
     }
     for (int b = 0; b < 2; ++b) {
       tc::mbar_init(tfull(b), 1);
-      tc::mbar_init(tempty(b), 2 * kLcEpiWarps);  // both CTAs' epilogue warps, on the even CTA
+      tc::mbar_init(tempty(b), 2 * kLcGroupWarps);  // both CTAs' warps of a group, on the even CTA
     }
     tc::mbar_init(drain, 1);
+    for (int w = 0; w < 2 * kLcEpiWarps; ++w) tc::mbar_init(ufull(w >> 1, w & 1), 1);
+    for (int i = 0; i < kLcAhead; ++i) tc::mbar_init(told(i), 1);
     *abort = 0;
     tc::fence_barrier_init();
-    tc::prefetch_tmap(&j.ta);
-    tc::prefetch_tmap(&j.tb);
+    for (int k = 0; k < kLcJobs; ++k) {
+      if (p.job[k].mt == 0) continue;
+      tc::prefetch_tmap(&p.job[k].ta);
+      tc::prefetch_tmap(&p.job[k].tb);
+    }
   }
   if (warp == 1) {
     tc::tmem_alloc_pair(tc::smem_u32(tmem_holder), kLcTmemCols);
@@ -165,63 +259,81 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
   tc::cluster_sync();
   tc::tc_fence_after();
   const uint32_t tmem = *tmem_holder;
+  pdl_wait();  // everything below reads or writes what earlier kernels of the stream write or read
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
+      LcRing r{0, 0};
       int iss = 0;
       bool ok = true;
-      for (int t = pair; t < p.tiles && ok; t += npairs) {
-        int m, n, sl;
-        lc_tile(j, t, m, n, sl);
-        const int half = lc_cols(j, n) >> 1;  // columns of B in each CTA
-        const int am = m * kLcTile + (int)rank * kLcHalf, bn = j.b_n0 + n * kLcTile + (int)rank * half;
-        const int kb0 = sl * j.per, kb1 = min(j.nkb, kb0 + j.per);
+      LcWork w;
+      int tj = 0;
+      auto tell = [&](int4 x) {
+        tile_ring[tj & (kLcAhead - 1)] = x;
+        tc::mbar_arrive(told(tj));
+        ++tj;
+      };
+      for (LcIter it(pair); ok && it.next(p, pair, npairs, w);) {
+        tell(LcTile::pack(w));
+        const LcJob& j = p.job[w.job];
+        const int half = lc_cols(j.Nn, w.n) >> 1;  // columns of B in each CTA
+        const int am = w.m * kLcTile + (int)rank * kLcHalf, bn = j.b_n0 + w.n * kLcTile + (int)rank * half;
         const int bboxes = (half + 63) >> 6;  // boxes of an MN-major B
         const uint32_t bytes = (uint32_t)(kLcOpBytes + (j.b_mn ? bboxes * kLcBox : kLcOpBytes));
-        for (int kb = kb0; kb < kb1; ++kb, ++iss) {
-          const int s = iss % kLcStages;
-          ok = tc::mbar_wait(empty(s), ((iss / kLcStages) & 1) ^ 1, abort);
+        const bool a_mn = j.a_mn, b_mn = j.b_mn;
+        const int b_k0 = j.b_k0;
+        for (int kb = w.kb0; kb < w.kb1; ++kb) {
+          ok = tc::mbar_wait(empty(r.s), r.ph ^ 1, abort);
           if (!ok) break;
-          const uint32_t bar = tc::map_rank(full(s), 0);
-          if (rank == 0) tc::mbar_arrive_expect_tx(full(s), 2 * bytes);  // both CTAs' copies
-          const uint32_t da = sbase + s * kLcStageBytes, db = da + kLcOpBytes;
-          const int ka = j.a_k0 + kb * kLcKb, kbn = j.b_k0 + kb * kLcKb;
-          if (j.a_mn) {
+          const uint32_t bar = tc::map_rank(full(r.s), 0);
+          if (rank == 0) tc::mbar_arrive_expect_tx(full(r.s), 2 * bytes);  // both CTAs' copies
+          const uint32_t da = sbase + r.s * kLcStageBytes, db = da + kLcOpBytes;
+          const int ka = kb * kLcKb, kbn = b_k0 + kb * kLcKb;
+          if (a_mn) {
             tc::tma_load_2d_pair(da, &j.ta, am, ka, bar);
             tc::tma_load_2d_pair(da + kLcBox, &j.ta, am + 64, ka, bar);
           } else {
             tc::tma_load_2d_pair(da, &j.ta, ka, am, bar);
           }
-          if (j.b_mn) {
+          if (b_mn) {
             for (int b = 0; b < bboxes; ++b) tc::tma_load_2d_pair(db + b * kLcBox, &j.tb, bn + b * 64, kbn, bar);
           } else {
             tc::tma_load_2d_pair(db, &j.tb, kbn, bn, bar);
           }
+          r.step(p.stages);
+          ++iss;
         }
       }
+      // the end, for either group of epilogue warps
+      for (int k = 0; k < 2 && ok; ++k) tell(make_int4(-1, 0, 0, 0));
       // the last stages' releases, which the even CTA's MMAs send to both CTAs, have arrived before either exits
-      for (int i = max(0, iss - kLcStages); i < iss && ok; ++i)
-        ok = tc::mbar_wait(empty(i % kLcStages), (i / kLcStages) & 1, abort);
+      for (int i = min(iss, p.stages); i > 0 && ok; --i) {
+        const int k = iss - i;
+        ok = tc::mbar_wait(empty(k % p.stages), (k / p.stages) & 1, abort);
+      }
       if (!ok) {
         if (!*abort) raise_status(p.status, DSPARK_ETIMEOUT);
         *abort = 1;
         // copies already issued land (they complete on the even CTA's barriers) before the pair can exit
         volatile int never = 0;
-        for (int i = max(0, iss - kLcStages); i < iss; ++i)
-          tc::mbar_wait(full(i % kLcStages), (i / kLcStages) & 1, &never);
+        for (int k = max(0, iss - p.stages); k < iss; ++k)
+          tc::mbar_wait(full(k % p.stages), (k / p.stages) & 1, &never);
       }
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0 && rank == 0) {
       bool ok = true;
-      int it = 0, tj = 0;
-      for (int t = pair; t < p.tiles && ok; t += npairs, ++tj) {
-        int m, n, sl;
-        lc_tile(j, t, m, n, sl);
-        const int cols = lc_cols(j, n), kb0 = sl * j.per, kb1 = min(j.nkb, kb0 + j.per);
-        const uint32_t idesc = tc::idesc_bf16_f32(kLcTile, cols, j.b_mn) | (j.a_mn ? 1u << 15 : 0u);
+      LcRing r{0, 0};
+      for (int tj = 0;; ++tj) {
+        ok = tc::mbar_wait(told(tj), (tj / kLcAhead) & 1, abort);
+        if (!ok) break;
+        const int4 x = tile_ring[tj & (kLcAhead - 1)];
+        if (x.x < 0) break;
+        const LcTile w(x);
+        const LcJob& j = p.job[w.job];
+        const uint32_t idesc = tc::idesc_bf16_f32(kLcTile, lc_cols(j.Nn, w.n), j.b_mn) | (j.a_mn ? 1u << 15 : 0u);
         const int ab = tj & 1;
         ok = tc::mbar_wait(tempty(ab), ((tj >> 1) & 1) ^ 1, abort);
         if (!ok) break;
@@ -229,19 +341,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
         const uint32_t d = tmem + (uint32_t)(ab * kLcTile);
         const uint32_t a_step = j.a_mn ? 2048 : 32, b_step = j.b_mn ? 2048 : 32;
         const uint32_t a_lbo = j.a_mn ? kLcBox : 16, b_lbo = j.b_mn ? kLcBox : 16;
-        for (int kb = kb0; kb < kb1; ++kb, ++it) {
-          const int s = it % kLcStages;
-          ok = tc::mbar_wait(full(s), (it / kLcStages) & 1, abort);
+        for (int kb = 0; kb < w.nkb; ++kb) {
+          ok = tc::mbar_wait(full(r.s), r.ph, abort);
           if (!ok) break;
           tc::tc_fence_after();
-          const uint32_t da = sbase + s * kLcStageBytes, db = da + kLcOpBytes;
+          const uint32_t da = sbase + r.s * kLcStageBytes, db = da + kLcOpBytes;
 #pragma unroll
           for (int kk = 0; kk < kLcKb / 16; ++kk)
             tc::mma_bf16_pair(d, tc::smem_desc(da + kk * a_step, a_lbo, 1024),
-                              tc::smem_desc(db + kk * b_step, b_lbo, 1024), idesc, (kb > kb0 || kk > 0) ? 1u : 0u);
-          tc::mma_commit_pair(empty(s));
+                              tc::smem_desc(db + kk * b_step, b_lbo, 1024), idesc, (kb > 0 || kk > 0) ? 1u : 0u);
+          tc::mma_commit_pair(empty(r.s));
+          r.step(p.stages);
         }
-        if (ok) tc::mma_commit_pair(tfull(ab));
+        if (!ok) break;
+        tc::mma_commit_pair(tfull(ab));
       }
       if (!ok) {
         if (!*abort) raise_status(p.status, DSPARK_ETIMEOUT);
@@ -253,166 +366,243 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ epilogue
-    const int q = warp & 3, hf = (warp - 2) >> 2;
+    // group grp takes tiles grp, grp + 2, ..; its warp reads lane quarter q and
+    // 128 columns (half hf) of the accumulator in parts of 32, the next part on
+    // its way while one is worked on
+    const int e = warp - 2, grp = e >> 3, q = warp & 3, hf = (e >> 2) & 1, c0 = hf * kLcWarpCols;
+    const uint32_t ub = sbase + kLcStagesU * kLcStageBytes + (uint32_t)e * kLcUWarp;
+    const unsigned char* up = smem + kLcStagesU * kLcStageBytes + e * kLcUWarp;
+    const uint32_t ta = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(grp * kLcTile + c0);
+    const uint32_t released = tc::map_rank(tempty(grp), 0);
+    const LcJob& z = p.job[GRAD ? kLcMakeG : 0];  // the job that makes logits
+    const bool has_u = z.has_u != 0;
+    const int row0 = (int)rank * kLcHalf + q * 32;  // the warp's first row in a tile
     bool ok = true;
-    int tj = 0;
-    for (int t = pair; t < p.tiles; t += npairs, ++tj) {
-      int m, n, sl;
-      lc_tile(j, t, m, n, sl);
-      const int cols = lc_cols(j, n), ab = tj & 1;
-      const int row = m * kLcTile + (int)rank * kLcHalf + q * 32 + lane;
-      const bool has = row < j.M;
-      const uint32_t ta = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(ab * kLcTile);
-      // this warp's columns of the tile: [c0, c1), in steps of 32
-      const int c0 = hf * kLcHalf, c1 = min(cols, c0 + kLcHalf);
-      const int col0 = n * kLcTile;
-      int tgt = -1;
-      float lse = 0.f, w = 0.f;
-      if (j.mode != kLcOut && has) {
-        tgt = j.target[row];
-        if (tgt < -1 || tgt >= j.V) {
-          if (n == 0 && hf == 0) raise_status(p.status, DSPARK_ERANGE);
-          tgt = -1;
-        }
-        if (j.mode == kLcG) {
-          lse = j.lse[row];
-          w = j.wt ? j.wt[row] : 1.f;
+    int ubox = 0;  // boxes of U taken so far
+
+    // the tile announced as number i; a logit tile's target, lse and weight of this lane's row
+    LcTile w;
+    int tgt = -1;
+    float lse = 0.f, wt = 1.f;
+    bool is_z = false, has = false;
+    int row = 0, parts = 0;
+    auto announced = [&](int i) {
+      ok = tc::mbar_wait(told(i), (i / kLcAhead) & 1, abort);
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      if (!ok) return false;
+      const int4 x = tile_ring[i & (kLcAhead - 1)];
+      if (x.x < 0) return false;
+      w = LcTile(x);
+      is_z = !GRAD || w.job == kLcMakeG;
+      const int M = is_z ? z.M : w.job == kLcDx ? p.job[kLcDx].M : p.job[kLcDw].M;
+      const int Nn = is_z ? z.Nn : w.job == kLcDx ? p.job[kLcDx].Nn : p.job[kLcDw].Nn;
+      row = w.m * kLcTile + row0 + lane;
+      has = row < M;
+      // parts of 32 columns this warp has (0: none, or no rows; the same for its lanes)
+      parts = row - lane < M ? max(0, min(kLcWarpCols, lc_cols(Nn, w.n) - c0)) / kLcPart : 0;
+      if (is_z) {
+        tgt = -1;
+        if (has) {
+          tgt = z.target[row];
+          if (GRAD) {
+            lse = z.lse[row];
+            wt = z.wt ? z.wt[row] : 1.f;
+          }
         }
       }
-      ok = tc::mbar_wait(tfull(ab), (tj >> 1) & 1, abort);
+      return true;
+    };
+    // box number b of U of the tile's parts, into the warp's slot for it
+    auto load_u = [&](int b) {
+      if (has_u && is_z && b < parts && lane == 0) {
+        const int s = (ubox + b) & 1;
+        tc::mbar_arrive_expect_tx(ufull(e, s), kLcUBox);
+        tc::tma_load_2d(ub + s * kLcUBox, &z.tu, z.b_n0 + w.n * kLcTile + c0 + b * kLcPart, row - lane, ufull(e, s),
+                        tc::policy_evict_first());
+      }
+    };
+    for (int tj = grp; announced(tj); tj += 2) {
+      load_u(0);
+      load_u(1);
+      if (is_z && (tgt < -1 || tgt >= z.V)) {
+        if (w.n == 0 && hf == 0) raise_status(p.status, DSPARK_ERANGE);
+        tgt = -1;
+      }
+      ok = tc::mbar_wait(tfull(grp), (tj >> 1) & 1, abort);
       ok = __all_sync(0xFFFFFFFFu, ok);
       if (!ok) break;
       tc::tc_fence_after();
-      const bool any = __any_sync(0xFFFFFFFFu, has);
-      if (j.mode == kLcOut) {
-        const int64_t o_row = (int64_t)sl * j.M + row;
-        for (int c = c0; c < c1 && any; c += 32) {
-          float v[32];
-          tc::tmem_ld32(ta + (uint32_t)c, v);
-          tc::tmem_wait_ld();
-          if (!has) continue;
-          const int col = col0 + c;
-          float* ap = j.acc ? j.acc + o_row * j.lda + col : nullptr;
-          if (j.acc_in) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              const float4 x = *reinterpret_cast<const float4*>(ap + e);
-              v[e] += x.x;
-              v[e + 1] += x.y;
-              v[e + 2] += x.z;
-              v[e + 3] += x.w;
-            }
-          }
-          if (!j.out) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 8) st_v8(ap + e, reinterpret_cast<const uint32_t*>(v + e));
-          } else {
-            __nv_bfloat16* op = j.out + (int64_t)row * j.ldo + col;
-            const int left = j.Nn - col;
-            if (left >= 32) {
-#pragma unroll
-              for (int e = 0; e < 32; e += 8) {
-                uint4 x;
-                x.x = pack_bf16(v[e] * j.scale, v[e + 1] * j.scale);
-                x.y = pack_bf16(v[e + 2] * j.scale, v[e + 3] * j.scale);
-                x.z = pack_bf16(v[e + 4] * j.scale, v[e + 5] * j.scale);
-                x.w = pack_bf16(v[e + 6] * j.scale, v[e + 7] * j.scale);
-                *reinterpret_cast<uint4*>(op + e) = x;
-              }
-            } else {
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (e < left) op[e] = __float2bfloat16_rn(v[e] * j.scale);
-            }
-          }
-        }
-      } else {
-        // a row's logits, 32 at a time: U added, columns past the vocabulary out
-        float mx = -INFINITY, sum = 0.f;
-        for (int c = c0; c < c1 && any; c += 32) {
-          float v[32];
-          tc::tmem_ld32(ta + (uint32_t)c, v);
-          tc::tmem_wait_ld();
-          const int col = j.b_n0 + col0 + c;  // vocabulary index of v[0]
-          const int left = min(32, j.V - col);
-          if (j.U && has) {
-            const float* up = j.U + (int64_t)row * j.ldu + col;
-            if (left == 32) {
-#pragma unroll
-              for (int e = 0; e < 32; e += 4) {
-                const float4 x = __ldg(reinterpret_cast<const float4*>(up + e));
-                v[e] += x.x;
-                v[e + 1] += x.y;
-                v[e + 2] += x.z;
-                v[e + 3] += x.w;
-              }
-            } else {
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (e < left) v[e] += up[e];
-            }
-            // a mask's finite stand-in (the type's lowest value) masks as -inf does:
-            // a row that holds nothing else would lose its sum of exponentials to lse's rounding
-#pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = v[e] <= kLcMasked ? -INFINITY : v[e];
-          }
-          const int te = tgt - col;  // the target's place among these columns
-          if (j.mode == kLcStats) {
-            if (left < 32) {
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (e >= left) v[e] = -INFINITY;
-            }
-            if (te >= 0 && te < 32) {
-              float z = 0.f;
-#pragma unroll
-              for (int e = 0; e < 32; ++e) z = e == te ? v[e] : z;
-              j.zt[row] = z;
-            }
-            float cm = v[0];
-#pragma unroll
-            for (int e = 1; e < 31; e += 2) cm = tc::max3f(cm, v[e], v[e + 1]);
-            cm = tc::max3f(cm, v[31], mx);
-            // a row that is -inf so far keeps its sum at 0 (no -inf - -inf)
-            const float ref = cm == -INFINITY ? 0.f : cm;
-            sum *= tc::ex2_ftz((mx - ref) * tc::kLog2e);
-            mx = cm;
-            float s4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int e = 0; e < 32; ++e) s4[e & 3] += tc::ex2_ftz((v[e] - ref) * tc::kLog2e);
-            sum += (s4[0] + s4[1]) + (s4[2] + s4[3]);
-          } else {
-            // G: a row without a target, or with nothing left by its mask, has none
-            const bool live = tgt >= 0 && lse != -INFINITY;
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const float pv = tc::ex2_ftz((v[e] - lse) * tc::kLog2e);
-              v[e] = live ? w * (e == te ? pv - 1.f : pv) : 0.f;
-            }
-            if (has) {
-              // the piece's rows are padded to whole 32-column groups
-              __nv_bfloat16* gp = j.G + (int64_t)row * j.ldg + col0 + c;
-#pragma unroll
-              for (int e = 0; e < 32; e += 16) {
-                uint32_t r[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) r[i] = pack_bf16(v[e + 2 * i], v[e + 2 * i + 1]);
-                st_v8(gp + e, r);
-              }
-            }
-          }
-        }
-        if (j.mode == kLcStats && has) j.part[(int64_t)(2 * n + hf) * j.M + row] = make_float2(mx, sum);
+      auto release = [&]() {
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive_cluster_relaxed(released);
+      };
+      const int col = w.n * kLcTile + c0;  // the half's first column in the result
+      if (parts == 0) {
+        release();
+        if (!GRAD && has) z.part[(int64_t)row * (2 * z.nt) + 2 * w.n + hf] = make_float2(kLcRefMin, 0.f);
+        continue;
       }
-      tc::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive_cluster(tc::map_rank(tempty(ab), 0));
+      const unsigned long long l2e = tc::f2pack(tc::kLog2e, tc::kLog2e);
+      const int vcol = z.b_n0 + col;  // vocabulary index of the half's first column
+      float ref = kLcRefMin, sum = 0.f;
+
+      // one part of 32 columns, h = 0 .. 3
+      auto part = [&](float* v, int h) {
+        if (has_u && is_z) {
+          const int s = (ubox + h) & 1;
+          ok = ok && tc::mbar_wait(ufull(e, s), ((ubox + h) >> 1) & 1, abort);
+          const unsigned char* box = up + s * kLcUBox + lane * 128;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const float4 x = *reinterpret_cast<const float4*>(box + ((c ^ (lane & 7)) << 4));
+            v[4 * c] += x.x;
+            v[4 * c + 1] += x.y;
+            v[4 * c + 2] += x.z;
+            v[4 * c + 3] += x.w;
+          }
+          __syncwarp();  // every lane has read the box before the next one lands on it
+          load_u(h + 2);
+        }
+        const int t = tgt - vcol - kLcPart * h;  // the target's place in the part
+        if (!GRAD) {
+          const int left = z.V - vcol - kLcPart * h;  // columns past the vocabulary are out
+          if (left < kLcPart) {
+#pragma unroll
+            for (int i = 0; i < kLcPart; ++i)
+              if (i >= left) v[i] = -INFINITY;
+          }
+          if (t >= 0 && t < kLcPart) {
+            float x = 0.f;
+#pragma unroll
+            for (int i = 0; i < kLcPart; ++i) x = i == t ? v[i] : x;
+            if (has) z.zt[row] = x;
+          }
+          float mx[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+          for (int i = 4; i < 28; i += 8)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mx[k] = tc::max3f(mx[k], v[i + k], v[i + 4 + k]);
+          mx[0] = tc::max3f(mx[0], v[28], v[29]);
+          mx[1] = tc::max3f(mx[1], v[30], v[31]);
+          // reference: the maximum in log2 units, rounded up to a whole number,
+          // so that one fused step gives each exponent with one rounding; what
+          // lies below its least value (-inf, the type's lowest value as a
+          // mask) adds nothing to the sum
+          const float nr = fmaxf(ref, ceilf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * tc::kLog2e));
+          sum *= tc::ex2_ftz(ref - nr);
+          ref = nr;
+          const unsigned long long nref = tc::f2pack(-ref, -ref);
+          unsigned long long s2[4] = {0, 0, 0, 0};
+#pragma unroll
+          for (int i = 0; i < kLcPart; i += 2) {
+            float a, b;
+            tc::f2unpack(tc::fma2(tc::f2pack(v[i], v[i + 1]), l2e, nref), a, b);
+            s2[(i >> 1) & 3] = tc::add2(s2[(i >> 1) & 3], tc::f2pack(tc::ex2_ftz(a), tc::ex2_ftz(b)));
+          }
+          float a, b;
+          tc::f2unpack(tc::add2(tc::add2(s2[0], s2[1]), tc::add2(s2[2], s2[3])), a, b);
+          sum += a + b;
+        } else if (is_z) {
+          // a row without a target, or with nothing left by its mask, has no G
+          const bool live = tgt >= 0 && lse != -INFINITY;
+          const float nl = -lse * tc::kLog2e;
+          const unsigned long long nl2 = tc::f2pack(nl, nl), w2 = tc::f2pack(wt, wt);
+#pragma unroll
+          for (int i = 0; i < kLcPart; i += 2) {
+            float a, b;
+            tc::f2unpack(tc::fma2(tc::f2pack(v[i], v[i + 1]), l2e, nl2), a, b);
+            v[i] = tc::ex2_ftz(a);
+            v[i + 1] = tc::ex2_ftz(b);
+          }
+          if (t >= 0 && t < kLcPart) {
+#pragma unroll
+            for (int i = 0; i < kLcPart; ++i) v[i] = i == t ? v[i] - 1.f : v[i];
+          }
+          __nv_bfloat16* gp = z.G + (int64_t)row * z.ldg + col + kLcPart * h;  // rows padded to whole parts
+#pragma unroll
+          for (int i = 0; i < kLcPart; i += 16) {
+            uint32_t r[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              float a, b;
+              tc::f2unpack(tc::fma2(tc::f2pack(v[i + 2 * k], v[i + 2 * k + 1]), w2, 0ull), a, b);
+              r[k] = live ? pack_bf16(a, b) : 0u;
+            }
+            if (has) st_v8(gp + i, r);
+          }
+        } else if (has) {
+          const LcJob &jx = p.job[kLcDx], &jw = p.job[kLcDw];
+          const bool dx = w.job == kLcDx;
+          const int oc = col + kLcPart * h, lda = dx ? (int)jx.lda : (int)jw.lda;
+          __nv_bfloat16* out = dx ? jx.out : jw.out;
+          float* ap = w.slot >= 0 ? (dx ? jx.slots : jw.slots) +
+                                        ((int64_t)w.slot * kLcTile + (row - w.m * kLcTile)) * kLcTile + c0 + kLcPart * h
+                                  : (dx ? jx.acc : jw.acc) + (int64_t)row * lda + oc;
+          if (w.slot < 0 && (dx ? jx.acc_in : jw.acc_in)) {
+#pragma unroll
+            for (int i = 0; i < kLcPart; i += 4) {
+              const float4 x = *reinterpret_cast<const float4*>(ap + i);  // rows padded to whole parts
+              v[i] += x.x;
+              v[i + 1] += x.y;
+              v[i + 2] += x.z;
+              v[i + 3] += x.w;
+            }
+          }
+          if (w.slot >= 0 || !out) {
+#pragma unroll
+            for (int i = 0; i < kLcPart; i += 8) st_v8(ap + i, reinterpret_cast<const uint32_t*>(v + i));
+          } else {
+            __nv_bfloat16* op = out + (int64_t)row * (dx ? jx.ldo : jw.ldo) + oc;
+            const int left = (dx ? jx.Nn : jw.Nn) - oc;
+            const float sc = dx ? jx.scale : jw.scale;
+#pragma unroll
+            for (int i = 0; i < kLcPart; i += 8) {
+              if (i + 8 <= left) {
+                uint4 x;
+                x.x = pack_bf16(v[i] * sc, v[i + 1] * sc);
+                x.y = pack_bf16(v[i + 2] * sc, v[i + 3] * sc);
+                x.z = pack_bf16(v[i + 4] * sc, v[i + 5] * sc);
+                x.w = pack_bf16(v[i + 6] * sc, v[i + 7] * sc);
+                *reinterpret_cast<uint4*>(op + i) = x;
+              } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                  if (i + k < left) op[i + k] = __float2bfloat16_rn(v[i + k] * sc);
+              }
+            }
+          }
+        }
+      };
+
+      float v[2][kLcPart];
+      tc::tmem_ld32(ta, v[0]);
+#pragma unroll
+      for (int h = 0; h < kLcWarpCols / kLcPart; ++h) {
+        if (h < parts) {
+          tc::tmem_wait_ld();
+          tc::tmem_tie32(v[h & 1]);
+          if (h + 1 < parts)
+            tc::tmem_ld32(ta + (h + 1) * kLcPart, v[(h + 1) & 1]);
+          else
+            release();
+          part(v[h & 1], h);
+        }
+      }
+      if (has_u && is_z) ubox += parts;
+      if (!GRAD && has) z.part[(int64_t)row * (2 * z.nt) + 2 * w.n + hf] = make_float2(ref, sum);
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      if (!ok) break;
     }
     if (!ok && lane == 0) {
       if (!*abort) raise_status(p.status, DSPARK_ETIMEOUT);
       *abort = 1;
+      // boxes of U still in flight land before the CTA can exit
+      volatile int never = 0;
+      for (int b = ubox; b < ubox + kLcWarpCols / kLcPart; ++b) tc::mbar_wait(ufull(e, b & 1), (b >> 1) & 1, &never);
     }
   }
+  pdl_trigger();
   __syncwarp();
   tc::tc_fence_before();
   __syncthreads();
@@ -423,63 +613,126 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
   }
 }
 
-// lse and loss of 32 rows per CTA from the half tiles' (max, sum exp): a
-// warp-wide lane of partials per row, joined in a fixed order.
-__global__ void __launch_bounds__(1024)
+// lse and loss of a row per warp from the half tiles' (reference, sum), joined
+// in a fixed order.
+constexpr int kLcRowsCta = 4;
+
+// log 2 as a value of 11 significant bits (exact products with whole references below 2^13) and the rest
+constexpr float kLn2Hi = 0.693359375f, kLn2Lo = -2.12194440e-4f;
+
+__device__ __forceinline__ float2 lc_join(float2 a, float2 b) {
+  const float m = fmaxf(a.x, b.x);
+  return make_float2(m, a.y * tc::ex2_ftz(a.x - m) + b.y * tc::ex2_ftz(b.x - m));
+}
+
+__global__ void __launch_bounds__(32 * kLcRowsCta)
     k_lce_rows(const float2* __restrict__ part, const float* __restrict__ zt, const int32_t* __restrict__ target,
                int N, int parts, int V, float* __restrict__ loss, float* __restrict__ lse) {
-  __shared__ float2 sh[32][33];
-  const int r = threadIdx.x & 31, g = threadIdx.x >> 5, row = blockIdx.x * 32 + r;
-  float m = -INFINITY, s = 0.f;
-  if (row < N)
-    for (int i = g; i < parts; i += 32) {
-      const float2 x = part[(int64_t)i * N + row];
-      const float nm = fmaxf(m, x.x), ref = nm == -INFINITY ? 0.f : nm;
-      s = s * __expf(m - ref) + x.y * __expf(x.x - ref);
-      m = nm;
-    }
-  sh[g][r] = make_float2(m, s);
-  __syncthreads();
-  if (g == 0 && row < N) {
-    for (int i = 1; i < 32; ++i) {
-      const float2 x = sh[i][r];
-      const float nm = fmaxf(m, x.x), ref = nm == -INFINITY ? 0.f : nm;
-      s = s * __expf(m - ref) + x.y * __expf(x.x - ref);
-      m = nm;
-    }
-    // a row whose every logit is -inf has no distribution: lse -inf, loss +inf
-    const float l = (m == -INFINITY && s == 0.f) ? -INFINITY : m + logf(s);
+  const int lane = threadIdx.x & 31, row = blockIdx.x * kLcRowsCta + (threadIdx.x >> 5);
+  pdl_wait();
+  pdl_trigger();
+  if (row >= N) return;
+  // two partials per load (parts is even)
+  const float4* p = reinterpret_cast<const float4*>(part + (int64_t)row * parts);
+  const float2 none = make_float2(kLcRefMin, 0.f);
+  float2 a[4] = {none, none, none, none};
+  for (int i = lane; i < parts / 2; i += 128) {
+    float4 x[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      x[k] = i + 32 * k < parts / 2 ? p[i + 32 * k] : make_float4(kLcRefMin, 0.f, kLcRefMin, 0.f);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) a[k] = lc_join(a[k], lc_join(make_float2(x[k].x, x[k].y), make_float2(x[k].z, x[k].w)));
+  }
+  float2 x = lc_join(lc_join(a[0], a[1]), lc_join(a[2], a[3]));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    float2 y;
+    y.x = __shfl_xor_sync(0xFFFFFFFFu, x.x, o);
+    y.y = __shfl_xor_sync(0xFFFFFFFFu, x.y, o);
+    x = lc_join(x, y);
+  }
+  if (lane == 0) {
+    // a row whose every logit is masked has no distribution: lse -inf, loss +inf
+    const float v = x.y == 0.f ? -INFINITY : fmaf(x.x, kLn2Hi, fmaf(x.x, kLn2Lo, logf(x.y)));
     const int t = target[row];
-    lse[row] = l;
-    loss[row] = (t < 0 || t >= V) ? 0.f : (l == -INFINITY ? INFINITY : l - zt[row]);
+    lse[row] = v;
+    loss[row] = (t < 0 || t >= V) ? 0.f : (v == -INFINITY ? INFINITY : v - zt[row]);
   }
 }
 
-// out[m][c] = bf16(scale * sum over slices of acc[s][m][c]), slices in order.
-__global__ void __launch_bounds__(256)
-    k_lce_join(const float* __restrict__ acc, int slices, int M, int Nn, int64_t lda, float scale,
-               __nv_bfloat16* __restrict__ out, int64_t ldo) {
-  const int q = (Nn + 3) >> 2;
-  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (i >= (int64_t)M * q) return;
-  const int m = (int)(i / q), c = (int)(i - (int64_t)m * q) * 4;
-  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s = 0; s < slices; ++s) {
-    const float4 x = *reinterpret_cast<const float4*>(acc + ((int64_t)s * M + m) * lda + c);
-    a.x += x.x;
-    a.y += x.y;
-    a.z += x.z;
-    a.w += x.w;
-  }
-  __nv_bfloat16* o = out + (int64_t)m * ldo + c;
-  if (c + 4 <= Nn) {
-    uint2 x;
-    x.x = pack_bf16(a.x * scale, a.y * scale);
-    x.y = pack_bf16(a.z * scale, a.w * scale);
-    *reinterpret_cast<uint2*>(o) = x;
-  } else {
-    const float v[4] = {a.x, a.y, a.z, a.w};
-    for (int e = 0; c + e < Nn; ++e) o[e] = __float2bfloat16_rn(v[e] * scale);
+// Tiles that several pairs share: their parts added in the contraction's
+// order, then what the epilogue does with a whole tile.
+struct LcJoin {
+  const float* slots;
+  int M, Nn, nkb, mt, nt, split;
+  float* acc;
+  int64_t lda;
+  int acc_in;
+  __nv_bfloat16* out;
+  int64_t ldo;
+  float scale;
+};
+struct LcJoins {
+  LcJoin j[2];
+};
+
+constexpr int kLcJoinRows = 4;   // rows of a tile per CTA: a float4 per thread
+
+__global__ void __launch_bounds__(256) k_lce_join(const __grid_constant__ LcJoins p) {
+  pdl_wait();
+  pdl_trigger();
+  const LcJoin& j = p.j[blockIdx.z];
+  int tile = blockIdx.x;
+  if (tile >= j.mt * j.nt) return;
+  const int units = j.mt * j.nt * j.nkb, u0 = tile * j.nkb, u1 = u0 + j.nkb;
+  // the pairs that hold the tile's first and last block
+  int pf = (int)((long long)u0 * j.split / units), pl = (int)((long long)(u1 - 1) * j.split / units);
+  while (lc_share(units, j.split, pf + 1) <= u0) ++pf;
+  while (lc_share(units, j.split, pl + 1) <= u1 - 1) ++pl;
+  if (pf == pl) return;  // one pair held all of it and wrote it
+  const int g = tile / (16 * j.nt), gm = min(16, j.mt - g * 16);
+  tile -= g * 16 * j.nt;
+  const int n = tile / gm, m = g * 16 + tile - n * gm;
+  const int c = (threadIdx.x & 63) * 4, col = n * kLcTile + c;
+  if (col >= j.Nn) return;
+  {
+    const int lr = blockIdx.y * kLcJoinRows + (threadIdx.x >> 6), row = m * kLcTile + lr;
+    if (row >= j.M) return;
+    // the first pair's part began with the tile (an odd slot); the others' ranges begin inside it
+    const float* sl = j.slots + ((int64_t)(2 * pf + 1) * kLcTile + lr) * kLcTile + c;
+    float4 a = *reinterpret_cast<const float4*>(sl);
+    sl += kLcTile * kLcTile;
+#pragma unroll 8
+    for (int q = pf + 1; q <= pl; ++q, sl += 2 * kLcTile * kLcTile) {
+      const float4 x = *reinterpret_cast<const float4*>(sl);
+      a.x += x.x;
+      a.y += x.y;
+      a.z += x.z;
+      a.w += x.w;
+    }
+    float4* ap = reinterpret_cast<float4*>(j.acc + (int64_t)row * j.lda + col);
+    if (j.acc_in) {
+      const float4 x = *ap;
+      a.x += x.x;
+      a.y += x.y;
+      a.z += x.z;
+      a.w += x.w;
+    }
+    if (!j.out) {
+      *ap = a;
+      return;
+    }
+    __nv_bfloat16* o = j.out + (int64_t)row * j.ldo + col;
+    if (col + 4 <= j.Nn) {
+      uint2 x;
+      x.x = pack_bf16(a.x * j.scale, a.y * j.scale);
+      x.y = pack_bf16(a.z * j.scale, a.w * j.scale);
+      *reinterpret_cast<uint2*>(o) = x;
+    } else {
+      const float f[4] = {a.x, a.y, a.z, a.w};
+      for (int e = 0; col + e < j.Nn; ++e) o[e] = __float2bfloat16_rn(f[e] * j.scale);
+    }
   }
 }
 
@@ -506,33 +759,42 @@ bool encode(CUtensorMap* tm, const void* p, int64_t cols, int64_t rows, int64_t 
                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+// U: fp32, boxes of 32 x 32.
+bool encode_u(CUtensorMap* tm, const float* p, int64_t cols, int64_t rows, int64_t ld) {
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)ld * 4};
+  const cuuint32_t box[2] = {32, 32};
+  const cuuint32_t es[2] = {1, 1};
+  return encode_fn()(tm, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<float*>(p), dims, strides, box, es,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 int64_t up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 int tiles_of(int64_t x) { return (int)((x + kLcTile - 1) / kLcTile); }
 
-// Slices of a contraction of nkb blocks so that `tiles` tiles fill the grid;
-// a slice keeps at least eight blocks. A function of the sizes alone, so the
-// order of the sums does not depend on the device.
-void slice(int tiles, int nkb, int* slices, int* per) {
-  int s = 1;
-  if (tiles < kLcPairs) s = kLcPairs / tiles;
-  s = s < nkb / 8 ? s : nkb / 8;
-  s = s < 1 ? 1 : s;
-  *per = (nkb + s - 1) / s;
-  *slices = (nkb + *per - 1) / *per;
+// Pairs that share a product's tiles block by block: where whole tiles would
+// leave part of the grid idle (fewer than two per pair), as long as every pair
+// gets eight blocks. A function of the sizes alone, so the order of the sums
+// does not depend on the device.
+int split_of(int tiles, int nkb) {
+  if (tiles >= 2 * kLcPairs) return 0;
+  const int64_t most = (int64_t)tiles * nkb / 8;
+  const int s = (int)(most < kLcPairs ? most : kLcPairs);
+  return s > tiles ? s : 0;
 }
 
 // The gradient's pieces of the vocabulary and its scratch.
 struct LcPlan {
   int piece, pieces;
   int64_t ldg;
-  int dx_slices, dx_per, dw_slices, dw_per;
-  int64_t dx_lda, dw_lda;
-  size_t part, zt, fwd_total;            // forward
-  size_t G, dx_acc, dw_acc, bwd_total;   // gradient
+  int dx_split, dw_split;
+  int64_t dx_lda;
+  size_t part, zt, fwd_total;                          // forward
+  size_t G[2], dx_acc, dx_slots, dw_slots, bwd_total;  // gradient
 };
 
-constexpr int64_t kLcPieceBytes = 256ll << 20;
+constexpr int64_t kLcPieceBytes = 64ll << 20;
 
 LcPlan make_plan(const dspark_lce_dims& d) {
   LcPlan p;
@@ -555,14 +817,15 @@ LcPlan make_plan(const dspark_lce_dims& d) {
   const int64_t widest = p.piece < V ? p.piece : V;
   p.ldg = up(widest, 64);
   const int64_t nkb_v = (widest + kLcKb - 1) / kLcKb, nkb_n = (N + kLcKb - 1) / kLcKb;
-  slice(tiles_of(N) * tiles_of(K), (int)nkb_v, &p.dx_slices, &p.dx_per);
-  slice(tiles_of(widest) * tiles_of(K), (int)nkb_n, &p.dw_slices, &p.dw_per);
+  p.dx_split = split_of(tiles_of(N) * tiles_of(K), (int)nkb_v);
+  p.dw_split = split_of(tiles_of(widest) * tiles_of(K), (int)nkb_n);
   p.dx_lda = up(K, 32);
-  p.dw_lda = d.layout == DSPARK_W_VK ? up(K, 32) : up(widest, 32);
   off = 0;
-  p.G = carve(2 * N * p.ldg);
-  p.dx_acc = carve(p.dx_slices > 1 || p.pieces > 1 ? 4 * p.dx_slices * N * p.dx_lda : 0);
-  p.dw_acc = carve(p.dw_slices > 1 ? 4 * p.dw_slices * (d.layout == DSPARK_W_VK ? widest : K) * p.dw_lda : 0);
+  p.G[0] = carve(2 * N * p.ldg);
+  p.G[1] = p.pieces > 1 ? carve(2 * N * p.ldg) : p.G[0];
+  p.dx_acc = carve(p.pieces > 1 ? 4 * N * p.dx_lda : 0);
+  p.dx_slots = carve(4ll * 2 * p.dx_split * kLcTile * kLcTile);
+  p.dw_slots = carve(4ll * 2 * p.dw_split * kLcTile * kLcTile);
   p.bwd_total = off;
   return p;
 }
@@ -576,31 +839,50 @@ bool dims_ok(const dspark_lce_dims* d) {
 // leading dimension of a matrix of `cols` columns: long enough, rows 16-byte aligned
 bool ld_ok(int64_t ld, int64_t cols, int mult) { return ld >= cols && ld % mult == 0 && ld < ((int64_t)1 << 32); }
 
-cudaError_t run_job(LcJob& j, int* status, cudaStream_t st) {
+cudaError_t lce_configure() {
   static bool configured = false;
-  if (!configured) {
-    const cudaError_t e = cudaFuncSetAttribute(k_lce, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kLcSmem);
-    if (e != cudaSuccess) return e;
-    configured = true;
-  }
-  LcParams p;
-  memset(&p, 0, sizeof(p));
-  j.mt = tiles_of(j.M);
-  j.nt = tiles_of(j.Nn);
-  p.job = j;
-  p.tiles = j.mt * j.nt * j.slices;
-  p.status = status;
-  const int pairs = p.tiles < kLcPairs ? p.tiles : kLcPairs;
-  k_lce<<<2 * pairs, kLcThreads, kLcSmem, st>>>(p);
-  return cudaGetLastError();
+  if (configured) return cudaSuccess;
+  cudaError_t e = cudaFuncSetAttribute(k_lce<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kLcSmem);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(k_lce<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kLcSmem);
+  if (e == cudaSuccess) configured = true;
+  return e;
 }
 
-LcJob empty_job() {
-  LcJob j;
-  memset(&j, 0, sizeof(j));
-  j.slices = 1;
-  return j;
-}
+// One launch: the statistics, or up to three of the gradient's products (the
+// longest tiles first).
+struct LcLaunch {
+  LcParams p;
+  bool grad, any;
+  LcLaunch(bool grad, int* status) : grad(grad), any(false) {
+    memset(&p, 0, sizeof(p));
+    p.status = status;
+    p.stages = kLcMaxStages;
+  }
+  LcJob& add(int place) {
+    any = true;
+    return p.job[place];
+  }
+  cudaError_t run(cudaStream_t st) {
+    if (!any) return cudaSuccess;
+    cudaError_t e = lce_configure();
+    if (e != cudaSuccess) return e;
+    int pairs = 0, tiles = 0;
+    for (int k = 0; k < kLcJobs; ++k) {
+      LcJob& j = p.job[k];
+      j.mt = tiles_of(j.M);
+      j.nt = tiles_of(j.Nn);
+      if (j.split == 0) tiles += j.mt * j.nt;
+      p.tiles[k] = tiles;
+      pairs = pairs > j.split ? pairs : j.split;
+      if (j.has_u) p.stages = kLcStagesU;
+    }
+    pairs = pairs > tiles ? pairs : tiles;
+    pairs = pairs < kLcPairs ? pairs : kLcPairs;
+    e = launch_ex(grad ? k_lce<true> : k_lce<false>, dim3(2 * pairs), dim3(kLcThreads), kLcSmem, st, true, p);
+    return e != cudaSuccess ? e : cudaGetLastError();
+  }
+};
 
 // z of the columns [v0, v0 + cols) of the vocabulary (statistics or G)
 bool z_job(LcJob& j, const dspark_lce_dims* d, const void* X, const void* W, const float* U, const int32_t* target,
@@ -608,16 +890,33 @@ bool z_job(LcJob& j, const dspark_lce_dims* d, const void* X, const void* W, con
   j.M = d->N;
   j.Nn = cols;
   j.nkb = (d->K + kLcKb - 1) / kLcKb;
-  j.per = j.nkb;
   j.b_mn = d->layout == DSPARK_W_KV;
   j.b_n0 = v0;
-  j.U = U;
-  j.ldu = d->ldu;
+  j.has_u = U != nullptr;
   j.target = target;
   j.V = d->V;
+  if (U && !encode_u(&j.tu, U, d->V, d->N, d->ldu)) return false;
   if (!encode(&j.ta, X, d->K, d->N, d->ldx, kLcHalf)) return false;
   return d->layout == DSPARK_W_VK ? encode(&j.tb, W, d->K, d->V, d->ldw, kLcHalf)
                                   : encode(&j.tb, W, d->V, d->K, d->ldw, kLcKb);
+}
+
+LcJoin join_of(const LcJob& j) {
+  LcJoin q;
+  q.slots = j.slots;
+  q.M = j.M;
+  q.Nn = j.Nn;
+  q.nkb = j.nkb;
+  q.mt = tiles_of(j.M);
+  q.nt = tiles_of(j.Nn);
+  q.split = j.split;
+  q.acc = j.acc;
+  q.lda = j.lda;
+  q.acc_in = j.acc_in;
+  q.out = j.out;
+  q.ldo = j.ldo;
+  q.scale = j.scale;
+  return q;
 }
 
 dspark_status lce_fail(cudaError_t e) {
@@ -661,16 +960,16 @@ extern "C" dspark_status dspark_linear_ce(const dspark_lce_dims* d, const void* 
   char* base = static_cast<char*>(scratch);
   float2* part = reinterpret_cast<float2*>(base + p.part);
   float* zt = reinterpret_cast<float*>(base + p.zt);
-  LcJob j = empty_job();
-  j.mode = kLcStats;
+  LcLaunch l(false, device_status);
+  LcJob& j = l.add(0);
   if (!z_job(j, d, X, W, U, target, 0, d->V)) return DSPARK_EINVAL;
   j.part = part;
   j.zt = zt;
-  cudaError_t e = run_job(j, device_status, st);
-  if (e == cudaSuccess) {
-    k_lce_rows<<<(d->N + 31) / 32, 1024, 0, st>>>(part, zt, target, d->N, 2 * tiles_of(d->V), d->V, loss, lse);
-    e = cudaGetLastError();
-  }
+  cudaError_t e = l.run(st);
+  if (e == cudaSuccess)
+    e = launch_ex(k_lce_rows, dim3((d->N + kLcRowsCta - 1) / kLcRowsCta), dim3(32 * kLcRowsCta), 0, st,
+                  true, part, zt, target, d->N, 2 * tiles_of(d->V),
+                  d->V, loss, lse);
   return lce_fail(e);
 }
 
@@ -695,74 +994,71 @@ extern "C" dspark_status dspark_linear_ce_grad(const dspark_lce_dims* d, const v
   }
   const LcPlan p = make_plan(*d);
   char* base = static_cast<char*>(scratch);
-  __nv_bfloat16* G = reinterpret_cast<__nv_bfloat16*>(base + p.G);
-  float* dx_acc = reinterpret_cast<float*>(base + p.dx_acc);
-  float* dw_acc = reinterpret_cast<float*>(base + p.dw_acc);
-  for (int i = 0; i < p.pieces && e == cudaSuccess; ++i) {
-    const int v0 = i * p.piece, cols = d->V - v0 < p.piece ? d->V - v0 : p.piece;
-    LcJob g = empty_job();
-    g.mode = kLcG;
-    if (!z_job(g, d, X, W, U, target, v0, cols)) return DSPARK_EINVAL;
-    g.lse = lse;
-    g.wt = wt;
-    g.G = G;
-    g.ldg = p.ldg;
-    e = run_job(g, device_status, st);
-    if (dX && e == cudaSuccess) {
-      LcJob x = empty_job();
-      x.mode = kLcOut;
-      x.M = d->N;
-      x.Nn = d->K;
-      x.nkb = (cols + kLcKb - 1) / kLcKb;
-      x.slices = p.dx_slices;
-      x.per = (x.nkb + x.slices - 1) / x.slices;
-      x.slices = (x.nkb + x.per - 1) / x.per;  // a short last piece may fill fewer slices; the rest keep their sums
-      x.b_mn = vk;
-      x.b_k0 = v0;
-      x.acc = dx_acc;
-      x.lda = p.dx_lda;
-      x.acc_in = i > 0;
-      x.scale = scale;
-      x.ldo = d->lddx;
-      if (p.dx_slices == 1 && i == p.pieces - 1) x.out = static_cast<__nv_bfloat16*>(dX);
-      if (!encode(&x.ta, G, cols, d->N, p.ldg, kLcHalf)) return DSPARK_EINVAL;
-      if (!(vk ? encode(&x.tb, W, d->K, d->V, d->ldw, kLcKb) : encode(&x.tb, W, d->V, d->K, d->ldw, kLcHalf)))
-        return DSPARK_EINVAL;
-      e = run_job(x, device_status, st);
-    }
-    if (dW && e == cudaSuccess) {
-      LcJob w = empty_job();
-      w.mode = kLcOut;
-      w.M = vk ? cols : d->K;
-      w.Nn = vk ? d->K : cols;
-      w.nkb = (d->N + kLcKb - 1) / kLcKb;
-      w.slices = p.dw_slices;
-      w.per = p.dw_per;
-      w.a_mn = w.b_mn = 1;
-      w.scale = scale;
-      w.ldo = d->lddw;
-      w.lda = p.dw_lda;
-      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(dW) + (vk ? (int64_t)v0 * d->lddw : v0);
-      if (p.dw_slices == 1)
-        w.out = out;
-      else
-        w.acc = dw_acc;
-      CUtensorMap* tg = vk ? &w.ta : &w.tb;
-      CUtensorMap* tx = vk ? &w.tb : &w.ta;
-      if (!encode(tg, G, cols, d->N, p.ldg, kLcKb) || !encode(tx, X, d->K, d->N, d->ldx, kLcKb)) return DSPARK_EINVAL;
-      e = run_job(w, device_status, st);
-      if (p.dw_slices > 1 && e == cudaSuccess) {
-        const int64_t n = (int64_t)w.M * ((w.Nn + 3) / 4);
-        k_lce_join<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(dw_acc, w.slices, w.M, w.Nn, w.lda, scale, out, w.ldo);
-        e = cudaGetLastError();
+  // launch i makes G of piece i beside the gradients' products of piece i - 1
+  for (int i = 0; i <= p.pieces && e == cudaSuccess; ++i) {
+    LcLaunch l(true, device_status);
+    LcJoins joins;
+    int njoin = 0, join_tiles = 0;
+    if (i > 0) {
+      const int v0 = (i - 1) * p.piece, cols = d->V - v0 < p.piece ? d->V - v0 : p.piece;
+      const __nv_bfloat16* G = reinterpret_cast<const __nv_bfloat16*>(base + p.G[(i - 1) & 1]);
+      if (dX) {
+        LcJob& x = l.add(kLcDx);
+        x.M = d->N;
+        x.Nn = d->K;
+        x.nkb = (cols + kLcKb - 1) / kLcKb;
+        x.split = p.dx_split ? split_of(tiles_of(x.M) * tiles_of(x.Nn), x.nkb) : 0;
+        x.b_mn = vk;
+        x.b_k0 = v0;
+        x.slots = reinterpret_cast<float*>(base + p.dx_slots);
+        x.acc = reinterpret_cast<float*>(base + p.dx_acc);
+        x.lda = p.dx_lda;
+        x.acc_in = i > 1;
+        x.scale = scale;
+        x.ldo = d->lddx;
+        if (i == p.pieces) x.out = static_cast<__nv_bfloat16*>(dX);
+        if (!encode(&x.ta, G, cols, d->N, p.ldg, kLcHalf)) return DSPARK_EINVAL;
+        if (!(vk ? encode(&x.tb, W, d->K, d->V, d->ldw, kLcKb) : encode(&x.tb, W, d->V, d->K, d->ldw, kLcHalf)))
+          return DSPARK_EINVAL;
+        if (x.split) {
+          joins.j[njoin++] = join_of(x);
+          join_tiles = tiles_of(x.M) * tiles_of(x.Nn);
+        }
+      }
+      if (dW) {
+        LcJob& w = l.add(kLcDw);
+        w.M = vk ? cols : d->K;
+        w.Nn = vk ? d->K : cols;
+        w.nkb = (d->N + kLcKb - 1) / kLcKb;
+        // a last piece of fewer tiles than the others shares them only if the others do (its slots are theirs)
+        w.split = p.dw_split ? split_of(tiles_of(w.M) * tiles_of(w.Nn), w.nkb) : 0;
+        w.a_mn = w.b_mn = 1;
+        w.slots = reinterpret_cast<float*>(base + p.dw_slots);
+        w.scale = scale;
+        w.ldo = d->lddw;
+        w.out = static_cast<__nv_bfloat16*>(dW) + (vk ? (int64_t)v0 * d->lddw : v0);
+        CUtensorMap* tg = vk ? &w.ta : &w.tb;
+        CUtensorMap* tx = vk ? &w.tb : &w.ta;
+        if (!encode(tg, G, cols, d->N, p.ldg, kLcKb) || !encode(tx, X, d->K, d->N, d->ldx, kLcKb)) return DSPARK_EINVAL;
+        if (w.split) {
+          joins.j[njoin++] = join_of(w);
+          const int n = tiles_of(w.M) * tiles_of(w.Nn);
+          join_tiles = join_tiles > n ? join_tiles : n;
+        }
       }
     }
-  }
-  if (dX && p.dx_slices > 1 && e == cudaSuccess) {
-    const int64_t n = (int64_t)d->N * ((d->K + 3) / 4);
-    k_lce_join<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(dx_acc, p.dx_slices, d->N, d->K, p.dx_lda, scale,
-                                                            static_cast<__nv_bfloat16*>(dX), d->lddx);
-    e = cudaGetLastError();
+    if (i < p.pieces) {
+      const int v0 = i * p.piece, cols = d->V - v0 < p.piece ? d->V - v0 : p.piece;
+      LcJob& g = l.add(kLcMakeG);
+      if (!z_job(g, d, X, W, U, target, v0, cols)) return DSPARK_EINVAL;
+      g.lse = lse;
+      g.wt = wt;
+      g.G = reinterpret_cast<__nv_bfloat16*>(base + p.G[i & 1]);
+      g.ldg = p.ldg;
+    }
+    e = l.run(st);
+    if (njoin > 0 && e == cudaSuccess)
+      e = launch_ex(k_lce_join, dim3(join_tiles, kLcTile / kLcJoinRows, njoin), dim3(256), 0, st, true, joins);
   }
   return lce_fail(e);
 }
