@@ -38,6 +38,9 @@ namespace dspark {
 
 namespace {
 
+// a lambda whose arrays stay in registers
+#define LC_INLINE __attribute__((always_inline))
+
 constexpr int kLcTile = 256;     // rows and columns of a pair's tile
 constexpr int kLcHalf = 128;     // rows (A) and columns (B) one CTA loads
 constexpr int kLcKb = 64;        // contraction depth of a stage (one 128-byte swizzled row)
@@ -53,14 +56,18 @@ constexpr int kLcWarpCols = 128;
 constexpr int kLcPart = 32;
 constexpr int kLcThreads = 32 * (2 + kLcEpiWarps);
 constexpr int kLcTmemCols = 512;                  // two accumulators of 256 columns
-// Operand ring: six stages, or three and two 32 x 32 fp32 boxes of U per epilogue warp.
-constexpr int kLcMaxStages = 6, kLcStagesU = 3;
-constexpr int kLcUBox = 32 * kLcPart * 4;         // 4 KB
-constexpr int kLcUWarp = 2 * kLcUBox;
-constexpr int kLcUBytes = kLcUWarp * kLcEpiWarps;
-constexpr int kLcRing = kLcMaxStages * kLcStageBytes > kLcStagesU * kLcStageBytes + kLcUBytes
-                            ? kLcMaxStages * kLcStageBytes
-                            : kLcStagesU * kLcStageBytes + kLcUBytes;
+// Shared memory: the operand ring and, from its end, 32 x 32 boxes of the
+// epilogue warps. Statistics: six stages, or three and two boxes of U a warp.
+// Gradient: five stages and an output box a warp, or three, a box of U and an
+// output box a warp.
+constexpr int kLcMaxStages = 6;
+constexpr int kLcBoxBytes = 32 * kLcPart * 4;     // 4 KB (fp32)
+constexpr int kLcBoxesU = 2;                      // boxes of U a warp of the statistics has
+constexpr int kLcRing = 224 * 1024;
+__host__ __device__ constexpr int lc_stages(bool grad, bool u) { return u ? 3 : grad ? 5 : 6; }
+static_assert(lc_stages(true, false) * kLcStageBytes + kLcEpiWarps * kLcBoxBytes <= kLcRing, "gradient");
+static_assert(lc_stages(true, true) * kLcStageBytes + 2 * kLcEpiWarps * kLcBoxBytes <= kLcRing, "gradient with U");
+static_assert(lc_stages(false, true) * kLcStageBytes + kLcBoxesU * kLcEpiWarps * kLcBoxBytes <= kLcRing, "U");
 constexpr int kLcAhead = 16;                      // tiles announced: the producer is at most 6 + 2 + 2 ahead
 constexpr int kLcBars = 2 * kLcMaxStages + 5 + 2 * kLcEpiWarps + kLcAhead + 1;
 constexpr int kLcBarBytes = 16 * kLcAhead + 8 * kLcBars + 16;
@@ -73,6 +80,7 @@ constexpr float kLcRefMin = -1e29f;               // least log2 reference: what 
 // One product C[M][Nn] = A B^T over a contraction of nkb blocks of 64.
 struct LcJob {
   CUtensorMap ta, tb, tu;
+  CUtensorMap to, tacc, tslots;  // stores: result (bf16; G's piece), fp32 sums, parts
   int M, Nn;            // rows and columns of the result
   int nkb;              // contraction blocks
   int mt, nt;           // tiles of 256 rows, of 256 columns
@@ -88,14 +96,12 @@ struct LcJob {
   const float* wt;
   float2* part;         // [M][2 nt] (log2 reference, sum of 2^(z log2 e - reference)) per half tile
   float* zt;            // [M] z at the target
-  __nv_bfloat16* G;     // [M][ldg] the piece's G
-  int64_t ldg;
   // gradients
-  float* slots;         // [2 split][256][256] parts of tiles that several pairs share
-  float* acc;           // [M][lda] sums so far, or null
+  const float* acc;     // [M][lda] sums so far
   int64_t lda;
   int acc_in;           // add what acc holds
-  __nv_bfloat16* out;   // [M][ldo] the result, or null: acc is written
+  int to_out;           // the result is complete: to out (through `to`), scaled; else to acc
+  __nv_bfloat16* out;   // [M][ldo]
   int64_t ldo;
   float scale;
 };
@@ -111,11 +117,6 @@ struct LcParams {
   int* status;
 };
 
-__device__ __forceinline__ void st_v8(void* p, const uint32_t* r) {
-  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
-               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
-}
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&b);
@@ -370,8 +371,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
     // 128 columns (half hf) of the accumulator in parts of 32, the next part on
     // its way while one is worked on
     const int e = warp - 2, grp = e >> 3, q = warp & 3, hf = (e >> 2) & 1, c0 = hf * kLcWarpCols;
-    const uint32_t ub = sbase + kLcStagesU * kLcStageBytes + (uint32_t)e * kLcUWarp;
-    const unsigned char* up = smem + kLcStagesU * kLcStageBytes + e * kLcUWarp;
+    // this warp's boxes: GRAD one for stores (the last 64 KB) and one of U before
+    // it, else kLcBoxesU of U
+    constexpr int kUb = GRAD ? 1 : kLcBoxesU;
+    const uint32_t box0 = kLcRing - (GRAD ? 1 : kUb) * kLcEpiWarps * kLcBoxBytes;
+    const uint32_t ooff = kLcRing - (kLcEpiWarps - e) * kLcBoxBytes;
+    const uint32_t uoff = GRAD ? ooff - kLcEpiWarps * kLcBoxBytes : box0 + e * kUb * kLcBoxBytes;
     const uint32_t ta = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(grp * kLcTile + c0);
     const uint32_t released = tc::map_rank(tempty(grp), 0);
     const LcJob& z = p.job[GRAD ? kLcMakeG : 0];  // the job that makes logits
@@ -380,19 +385,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
     bool ok = true;
     int ubox = 0;  // boxes of U taken so far
 
-    // the tile announced as number i; a logit tile's target, lse and weight of this lane's row
+    // the tile announced as number i; a logit tile's target, lse and weight of this
+    // lane's row, asked for a tile early where the tile is announced by then
     LcTile w;
-    int tgt = -1;
+    int tgt = -1, row = 0, parts = 0;
     float lse = 0.f, wt = 1.f;
-    bool is_z = false, has = false;
-    int row = 0, parts = 0;
-    auto announced = [&](int i) {
-      ok = tc::mbar_wait(told(i), (i / kLcAhead) & 1, abort);
-      ok = __all_sync(0xFFFFFFFFu, ok);
-      if (!ok) return false;
+    bool is_z = false, has = false, asked = false;
+    auto ask = [&](const LcTile& x) LC_INLINE {
+      const int r = x.m * kLcTile + row0 + lane;
+      tgt = -1;
+      if ((!GRAD || x.job == kLcMakeG) && r < z.M) {
+        tgt = z.target[r];
+        if (GRAD) {
+          lse = z.lse[r];
+          wt = z.wt ? z.wt[r] : 1.f;
+        }
+      }
+    };
+    auto announced = [&](int i) LC_INLINE {
+      if (!asked) {
+        ok = tc::mbar_wait(told(i), (i / kLcAhead) & 1, abort);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) return false;
+      }
       const int4 x = tile_ring[i & (kLcAhead - 1)];
       if (x.x < 0) return false;
       w = LcTile(x);
+      if (!asked) ask(w);
       is_z = !GRAD || w.job == kLcMakeG;
       const int M = is_z ? z.M : w.job == kLcDx ? p.job[kLcDx].M : p.job[kLcDw].M;
       const int Nn = is_z ? z.Nn : w.job == kLcDx ? p.job[kLcDx].Nn : p.job[kLcDw].Nn;
@@ -400,39 +419,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
       has = row < M;
       // parts of 32 columns this warp has (0: none, or no rows; the same for its lanes)
       parts = row - lane < M ? max(0, min(kLcWarpCols, lc_cols(Nn, w.n) - c0)) / kLcPart : 0;
-      if (is_z) {
-        tgt = -1;
-        if (has) {
-          tgt = z.target[row];
-          if (GRAD) {
-            lse = z.lse[row];
-            wt = z.wt ? z.wt[row] : 1.f;
-          }
-        }
-      }
       return true;
     };
     // box number b of U of the tile's parts, into the warp's slot for it
-    auto load_u = [&](int b) {
+    auto load_u = [&](int b) LC_INLINE {
       if (has_u && is_z && b < parts && lane == 0) {
-        const int s = (ubox + b) & 1;
-        tc::mbar_arrive_expect_tx(ufull(e, s), kLcUBox);
-        tc::tma_load_2d(ub + s * kLcUBox, &z.tu, z.b_n0 + w.n * kLcTile + c0 + b * kLcPart, row - lane, ufull(e, s),
+        const int s = (ubox + b) % kUb;
+        tc::mbar_arrive_expect_tx(ufull(e, s), kLcBoxBytes);
+        tc::tma_load_2d(sbase + uoff + s * kLcBoxBytes, &z.tu, z.b_n0 + w.n * kLcTile + c0 + b * kLcPart, row - lane, ufull(e, s),
                         tc::policy_evict_first());
       }
     };
     for (int tj = grp; announced(tj); tj += 2) {
-      load_u(0);
-      load_u(1);
+      for (int b = 0; b < kUb; ++b) load_u(b);
       if (is_z && (tgt < -1 || tgt >= z.V)) {
         if (w.n == 0 && hf == 0) raise_status(p.status, DSPARK_ERANGE);
         tgt = -1;
       }
+      // the target's place in the half, the exponent's offset: with the weight in it for G
+      const int te = tgt - (z.b_n0 + w.n * kLcTile + c0);
+      const bool live = !is_z || (tgt >= 0 && lse != -INFINITY);  // else the row has no G
+      const float wr = is_z ? wt : 1.f;
+      const float off = GRAD ? fmaf(-lse, tc::kLog2e, log2f(fabsf(wr))) : 0.f;
+      const bool plain = __all_sync(0xFFFFFFFFu, live && wr >= 0.f);
       ok = tc::mbar_wait(tfull(grp), (tj >> 1) & 1, abort);
       ok = __all_sync(0xFFFFFFFFu, ok);
       if (!ok) break;
       tc::tc_fence_after();
-      auto release = [&]() {
+      asked = __all_sync(0xFFFFFFFFu, tc::mbar_test(told(tj + 2), ((tj + 2) / kLcAhead) & 1));
+      if (asked) {
+        const int4 x = tile_ring[(tj + 2) & (kLcAhead - 1)];
+        if (x.x >= 0) ask(LcTile(x));
+      }
+      auto release = [&]() LC_INLINE {
         tc::tc_fence_before();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive_cluster_relaxed(released);
@@ -444,29 +463,81 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
         continue;
       }
       const unsigned long long l2e = tc::f2pack(tc::kLog2e, tc::kLog2e);
-      const int vcol = z.b_n0 + col;  // vocabulary index of the half's first column
-      float ref = kLcRefMin, sum = 0.f;
 
-      // one part of 32 columns, h = 0 .. 3
-      auto part = [&](float* v, int h) {
-        if (has_u && is_z) {
-          const int s = (ubox + h) & 1;
-          ok = ok && tc::mbar_wait(ufull(e, s), ((ubox + h) >> 1) & 1, abort);
-          const unsigned char* box = up + s * kLcUBox + lane * 128;
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            const float4 x = *reinterpret_cast<const float4*>(box + ((c ^ (lane & 7)) << 4));
-            v[4 * c] += x.x;
-            v[4 * c + 1] += x.y;
-            v[4 * c + 2] += x.z;
-            v[4 * c + 3] += x.w;
-          }
-          __syncwarp();  // every lane has read the box before the next one lands on it
-          load_u(h + 2);
+      // the warp's parts in order: `use` takes a part's values from v, the next
+      // part is asked for and `send` does what is left of this one meanwhile;
+      // the accumulator is released with the last part's arrival
+      float v[kLcPart];
+      auto each_part = [&](auto&& use, auto&& send) LC_INLINE {
+        tc::tmem_ld32(ta, v);
+#pragma unroll 1
+        for (int h = 0; h < parts; ++h) {
+          tc::tmem_wait_ld();
+          tc::tmem_tie32(v);
+          if (h + 1 == parts) release();
+          use(h);
+          if (h + 1 < parts) tc::tmem_ld32(ta + (h + 1) * kLcPart, v);
+          send(h);
         }
-        const int t = tgt - vcol - kLcPart * h;  // the target's place in the part
-        if (!GRAD) {
-          const int left = z.V - vcol - kLcPart * h;  // columns past the vocabulary are out
+      };
+      // U's columns of part h onto its logits
+      auto add_u = [&](int h) LC_INLINE {
+        const int s = (ubox + h) % kUb;
+        ok = ok && tc::mbar_wait(ufull(e, s), ((ubox + h) / kUb) & 1, abort);
+        const unsigned char* box = smem + uoff + s * kLcBoxBytes + lane * 128;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const float4 x = *reinterpret_cast<const float4*>(box + ((c ^ (lane & 7)) << 4));
+          v[4 * c] += x.x;
+          v[4 * c + 1] += x.y;
+          v[4 * c + 2] += x.z;
+          v[4 * c + 3] += x.w;
+        }
+        __syncwarp();  // every lane has read the box before the next one lands on it
+        load_u(h + kUb);
+      };
+      // Stores (gradient): through the warp's box in the layout of the store's
+      // swizzle (conflict-free both ways) and on by the copy engine, which leaves
+      // out what lies past the result's extents. bf16 results go 64 columns (two
+      // parts) at a time, fp32 parts and sums 32.
+      unsigned char* const obox = smem + ooff + lane * 128;
+      auto box_free = [&]() LC_INLINE {  // the store before has read the box
+        if (lane == 0) tc::bulk_wait_read();
+        __syncwarp();
+      };
+      auto put = [&](const CUtensorMap* tm, int c, int r) LC_INLINE {
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tc::tma_store_2d(tm, c, r, sbase + ooff);
+          tc::bulk_commit();
+        }
+      };
+      auto put16 = [&](const uint32_t* r, int h, const CUtensorMap* tm, int Nn, __nv_bfloat16* out, int64_t ldo) LC_INLINE {
+        if ((h & 1) == 0) box_free();
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          *reinterpret_cast<uint4*>(obox + (((k + 4 * (h & 1)) ^ (lane & 7)) << 4)) =
+              make_uint4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
+        if ((h & 1) != 0 || h + 1 == parts) {
+          const int cc = col + kLcPart * (h & ~1);
+          if ((Nn & 7) != 0 && cc + 64 > Nn) {
+            // the copy engine writes whole 16-byte pieces: each lane takes a ragged row's end value by value
+            if (has)
+              for (int i = 0; i < Nn - cc; ++i)
+                out[row * ldo + cc + i] =
+                    *reinterpret_cast<const __nv_bfloat16*>(obox + (((i >> 3) ^ (lane & 7)) << 4) + 2 * (i & 7));
+          } else {
+            put(tm, cc, row - lane);
+          }
+        }
+      };
+
+      if constexpr (!GRAD) {
+        float ref = kLcRefMin, sum = 0.f;
+        each_part([&](int h) LC_INLINE {
+          if (has_u) add_u(h);
+          const int t = te - kLcPart * h, left = z.V - col - kLcPart * h;  // columns past the vocabulary are out
           if (left < kLcPart) {
 #pragma unroll
             for (int i = 0; i < kLcPart; ++i)
@@ -503,94 +574,73 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
           float a, b;
           tc::f2unpack(tc::add2(tc::add2(s2[0], s2[1]), tc::add2(s2[2], s2[3])), a, b);
           sum += a + b;
-        } else if (is_z) {
-          // a row without a target, or with nothing left by its mask, has no G
-          const bool live = tgt >= 0 && lse != -INFINITY;
-          const float nl = -lse * tc::kLog2e;
-          const unsigned long long nl2 = tc::f2pack(nl, nl), w2 = tc::f2pack(wt, wt);
+        }, [](int) {});
+        if (has) z.part[(int64_t)row * (2 * z.nt) + 2 * w.n + hf] = make_float2(ref, sum);
+      } else if (is_z) {
+        const unsigned long long off2 = tc::f2pack(off, off);
+        uint32_t r[kLcPart / 2];
+        each_part([&](int h) LC_INLINE {
+          if (has_u) add_u(h);
+          const int t = te - kLcPart * h;
 #pragma unroll
           for (int i = 0; i < kLcPart; i += 2) {
             float a, b;
-            tc::f2unpack(tc::fma2(tc::f2pack(v[i], v[i + 1]), l2e, nl2), a, b);
+            tc::f2unpack(tc::fma2(tc::f2pack(v[i], v[i + 1]), l2e, off2), a, b);
             v[i] = tc::ex2_ftz(a);
             v[i + 1] = tc::ex2_ftz(b);
           }
           if (t >= 0 && t < kLcPart) {
 #pragma unroll
-            for (int i = 0; i < kLcPart; ++i) v[i] = i == t ? v[i] - 1.f : v[i];
+            for (int i = 0; i < kLcPart; ++i) v[i] = i == t ? v[i] - fabsf(wr) : v[i];
           }
-          __nv_bfloat16* gp = z.G + (int64_t)row * z.ldg + col + kLcPart * h;  // rows padded to whole parts
 #pragma unroll
-          for (int i = 0; i < kLcPart; i += 16) {
-            uint32_t r[8];
+          for (int k = 0; k < kLcPart / 2; ++k) r[k] = pack_bf16(v[2 * k], v[2 * k + 1]);
+          if (!plain) {  // a row without G, or of negative weight
+            const uint32_t keep = live ? 0xFFFFFFFFu : 0u, flip = wr < 0.f ? 0x80008000u : 0u;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              float a, b;
-              tc::f2unpack(tc::fma2(tc::f2pack(v[i + 2 * k], v[i + 2 * k + 1]), w2, 0ull), a, b);
-              r[k] = live ? pack_bf16(a, b) : 0u;
-            }
-            if (has) st_v8(gp + i, r);
+            for (int k = 0; k < kLcPart / 2; ++k) r[k] = (r[k] ^ flip) & keep;
           }
-        } else if (has) {
-          const LcJob &jx = p.job[kLcDx], &jw = p.job[kLcDw];
-          const bool dx = w.job == kLcDx;
-          const int oc = col + kLcPart * h, lda = dx ? (int)jx.lda : (int)jw.lda;
-          __nv_bfloat16* out = dx ? jx.out : jw.out;
-          float* ap = w.slot >= 0 ? (dx ? jx.slots : jw.slots) +
-                                        ((int64_t)w.slot * kLcTile + (row - w.m * kLcTile)) * kLcTile + c0 + kLcPart * h
-                                  : (dx ? jx.acc : jw.acc) + (int64_t)row * lda + oc;
-          if (w.slot < 0 && (dx ? jx.acc_in : jw.acc_in)) {
+        }, [&](int h) LC_INLINE { put16(r, h, &z.to, 0, nullptr, 0); });
+      } else {
+        const LcJob &jx = p.job[kLcDx], &jw = p.job[kLcDw];
+        const bool dx = w.job == kLcDx, whole = w.slot < 0;
+        auto add_acc = [&](int h) LC_INLINE {  // the sums of the pieces before (rows padded to whole parts)
+          const float* ap = (dx ? jx.acc + row * jx.lda : jw.acc + row * jw.lda) + col + kLcPart * h;
 #pragma unroll
-            for (int i = 0; i < kLcPart; i += 4) {
-              const float4 x = *reinterpret_cast<const float4*>(ap + i);  // rows padded to whole parts
-              v[i] += x.x;
-              v[i + 1] += x.y;
-              v[i + 2] += x.z;
-              v[i + 3] += x.w;
-            }
+          for (int i = 0; i < kLcPart; i += 4) {
+            const float4 x = *reinterpret_cast<const float4*>(ap + i);
+            v[i] += x.x;
+            v[i + 1] += x.y;
+            v[i + 2] += x.z;
+            v[i + 3] += x.w;
           }
-          if (w.slot >= 0 || !out) {
+        };
+        const bool acc_in = whole && has && (dx ? jx.acc_in : jw.acc_in);
+        if (whole && (dx ? jx.to_out : jw.to_out)) {
+          const float f = dx ? jx.scale : jw.scale;
+          const int Nn = dx ? jx.Nn : jw.Nn;
+          uint32_t r[kLcPart / 2];
+          each_part([&](int h) LC_INLINE {
+            if (acc_in) add_acc(h);
 #pragma unroll
-            for (int i = 0; i < kLcPart; i += 8) st_v8(ap + i, reinterpret_cast<const uint32_t*>(v + i));
-          } else {
-            __nv_bfloat16* op = out + (int64_t)row * (dx ? jx.ldo : jw.ldo) + oc;
-            const int left = (dx ? jx.Nn : jw.Nn) - oc;
-            const float sc = dx ? jx.scale : jw.scale;
+            for (int k = 0; k < kLcPart / 2; ++k) r[k] = pack_bf16(v[2 * k] * f, v[2 * k + 1] * f);
+          }, [&](int h) LC_INLINE {
+            put16(r, h, dx ? &jx.to : &jw.to, Nn, dx ? jx.out : jw.out, dx ? jx.ldo : jw.ldo);
+          });
+        } else {
+          const CUtensorMap* tm = whole ? (dx ? &jx.tacc : &jw.tacc) : (dx ? &jx.tslots : &jw.tslots);
+          const int sc = whole ? col : c0, sr = whole ? row - lane : w.slot * kLcTile + row0;
+          each_part([&](int h) LC_INLINE {
+            if (acc_in) add_acc(h);
+            box_free();
 #pragma unroll
-            for (int i = 0; i < kLcPart; i += 8) {
-              if (i + 8 <= left) {
-                uint4 x;
-                x.x = pack_bf16(v[i] * sc, v[i + 1] * sc);
-                x.y = pack_bf16(v[i + 2] * sc, v[i + 3] * sc);
-                x.z = pack_bf16(v[i + 4] * sc, v[i + 5] * sc);
-                x.w = pack_bf16(v[i + 6] * sc, v[i + 7] * sc);
-                *reinterpret_cast<uint4*>(op + i) = x;
-              } else {
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                  if (i + k < left) op[i + k] = __float2bfloat16_rn(v[i + k] * sc);
-              }
-            }
-          }
-        }
-      };
-
-      float v[2][kLcPart];
-      tc::tmem_ld32(ta, v[0]);
-#pragma unroll
-      for (int h = 0; h < kLcWarpCols / kLcPart; ++h) {
-        if (h < parts) {
-          tc::tmem_wait_ld();
-          tc::tmem_tie32(v[h & 1]);
-          if (h + 1 < parts)
-            tc::tmem_ld32(ta + (h + 1) * kLcPart, v[(h + 1) & 1]);
-          else
-            release();
-          part(v[h & 1], h);
+            for (int k = 0; k < 8; ++k)
+              *reinterpret_cast<float4*>(obox + ((k ^ (lane & 7)) << 4)) =
+                  make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+          }, [&](int h) LC_INLINE { put(tm, sc + kLcPart * h, sr); });
         }
       }
       if (has_u && is_z) ubox += parts;
-      if (!GRAD && has) z.part[(int64_t)row * (2 * z.nt) + 2 * w.n + hf] = make_float2(ref, sum);
       ok = __all_sync(0xFFFFFFFFu, ok);
       if (!ok) break;
     }
@@ -599,8 +649,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
       *abort = 1;
       // boxes of U still in flight land before the CTA can exit
       volatile int never = 0;
-      for (int b = ubox; b < ubox + kLcWarpCols / kLcPart; ++b) tc::mbar_wait(ufull(e, b & 1), (b >> 1) & 1, &never);
+      for (int b = ubox; b < ubox + kLcWarpCols / kLcPart; ++b)
+        tc::mbar_wait(ufull(e, b % kUb), (b / kUb) & 1, &never);
     }
+    if (GRAD && lane == 0) tc::bulk_wait_all();
   }
   pdl_trigger();
   __syncwarp();
@@ -759,15 +811,15 @@ bool encode(CUtensorMap* tm, const void* p, int64_t cols, int64_t rows, int64_t 
                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-// U: fp32, boxes of 32 x 32.
-bool encode_u(CUtensorMap* tm, const float* p, int64_t cols, int64_t rows, int64_t ld) {
+// The epilogue's boxes of 32 rows of 128 bytes: fp32 (U, sums, parts) or bf16 (results).
+bool encode_box(CUtensorMap* tm, const void* p, bool bf16, int64_t cols, int64_t rows, int64_t ld) {
   const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)ld * 4};
-  const cuuint32_t box[2] = {32, 32};
+  const cuuint64_t strides[1] = {(cuuint64_t)ld * (bf16 ? 2 : 4)};
+  const cuuint32_t box[2] = {bf16 ? 64u : 32u, 32};
   const cuuint32_t es[2] = {1, 1};
-  return encode_fn()(tm, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<float*>(p), dims, strides, box, es,
-                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encode_fn()(tm, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2,
+                     const_cast<void*>(p), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 int64_t up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
@@ -794,7 +846,7 @@ struct LcPlan {
   size_t G[2], dx_acc, dx_slots, dw_slots, bwd_total;  // gradient
 };
 
-constexpr int64_t kLcPieceBytes = 64ll << 20;
+constexpr int64_t kLcPieceBytes = 256ll << 20;
 
 LcPlan make_plan(const dspark_lce_dims& d) {
   LcPlan p;
@@ -857,7 +909,7 @@ struct LcLaunch {
   LcLaunch(bool grad, int* status) : grad(grad), any(false) {
     memset(&p, 0, sizeof(p));
     p.status = status;
-    p.stages = kLcMaxStages;
+    p.stages = lc_stages(grad, false);
   }
   LcJob& add(int place) {
     any = true;
@@ -875,7 +927,7 @@ struct LcLaunch {
       if (j.split == 0) tiles += j.mt * j.nt;
       p.tiles[k] = tiles;
       pairs = pairs > j.split ? pairs : j.split;
-      if (j.has_u) p.stages = kLcStagesU;
+      if (j.has_u) p.stages = lc_stages(grad, true);
     }
     pairs = pairs > tiles ? pairs : tiles;
     pairs = pairs < kLcPairs ? pairs : kLcPairs;
@@ -895,28 +947,38 @@ bool z_job(LcJob& j, const dspark_lce_dims* d, const void* X, const void* W, con
   j.has_u = U != nullptr;
   j.target = target;
   j.V = d->V;
-  if (U && !encode_u(&j.tu, U, d->V, d->N, d->ldu)) return false;
+  if (U && !encode_box(&j.tu, U, false, d->V, d->N, d->ldu)) return false;
   if (!encode(&j.ta, X, d->K, d->N, d->ldx, kLcHalf)) return false;
   return d->layout == DSPARK_W_VK ? encode(&j.tb, W, d->K, d->V, d->ldw, kLcHalf)
                                   : encode(&j.tb, W, d->V, d->K, d->ldw, kLcKb);
 }
 
-LcJoin join_of(const LcJob& j) {
-  LcJoin q;
-  q.slots = j.slots;
+// Where a gradient's product goes: parts of shared tiles to slots, whole tiles
+// to acc (summed over the vocabulary's pieces) or, complete, to out.
+bool out_job(LcJob& j, LcJoin& q, float* slots, float* acc, int64_t lda, bool acc_in, bool to_out,
+             __nv_bfloat16* out, int64_t ldo, float scale) {
+  j.acc = acc;
+  j.lda = lda;
+  j.acc_in = acc_in;
+  j.to_out = to_out;
+  j.out = out;
+  j.ldo = ldo;
+  j.scale = scale;
+  q.slots = slots;
   q.M = j.M;
   q.Nn = j.Nn;
   q.nkb = j.nkb;
   q.mt = tiles_of(j.M);
   q.nt = tiles_of(j.Nn);
   q.split = j.split;
-  q.acc = j.acc;
-  q.lda = j.lda;
-  q.acc_in = j.acc_in;
-  q.out = j.out;
-  q.ldo = j.ldo;
-  q.scale = j.scale;
-  return q;
+  q.acc = acc;
+  q.lda = lda;
+  q.acc_in = acc_in;
+  q.out = to_out ? out : nullptr;
+  q.ldo = ldo;
+  q.scale = scale;
+  if (j.split && !encode_box(&j.tslots, slots, false, kLcTile, 2ll * j.split * kLcTile, kLcTile)) return false;
+  return to_out ? encode_box(&j.to, out, true, j.Nn, j.M, ldo) : encode_box(&j.tacc, acc, false, lda, j.M, lda);
 }
 
 dspark_status lce_fail(cudaError_t e) {
@@ -1010,18 +1072,15 @@ extern "C" dspark_status dspark_linear_ce_grad(const dspark_lce_dims* d, const v
         x.split = p.dx_split ? split_of(tiles_of(x.M) * tiles_of(x.Nn), x.nkb) : 0;
         x.b_mn = vk;
         x.b_k0 = v0;
-        x.slots = reinterpret_cast<float*>(base + p.dx_slots);
-        x.acc = reinterpret_cast<float*>(base + p.dx_acc);
-        x.lda = p.dx_lda;
-        x.acc_in = i > 1;
-        x.scale = scale;
-        x.ldo = d->lddx;
-        if (i == p.pieces) x.out = static_cast<__nv_bfloat16*>(dX);
+        if (!out_job(x, joins.j[njoin], reinterpret_cast<float*>(base + p.dx_slots),
+                     reinterpret_cast<float*>(base + p.dx_acc), p.dx_lda, i > 1, i == p.pieces,
+                     static_cast<__nv_bfloat16*>(dX), d->lddx, scale))
+          return DSPARK_EINVAL;
         if (!encode(&x.ta, G, cols, d->N, p.ldg, kLcHalf)) return DSPARK_EINVAL;
         if (!(vk ? encode(&x.tb, W, d->K, d->V, d->ldw, kLcKb) : encode(&x.tb, W, d->V, d->K, d->ldw, kLcHalf)))
           return DSPARK_EINVAL;
         if (x.split) {
-          joins.j[njoin++] = join_of(x);
+          ++njoin;
           join_tiles = tiles_of(x.M) * tiles_of(x.Nn);
         }
       }
@@ -1033,15 +1092,14 @@ extern "C" dspark_status dspark_linear_ce_grad(const dspark_lce_dims* d, const v
         // a last piece of fewer tiles than the others shares them only if the others do (its slots are theirs)
         w.split = p.dw_split ? split_of(tiles_of(w.M) * tiles_of(w.Nn), w.nkb) : 0;
         w.a_mn = w.b_mn = 1;
-        w.slots = reinterpret_cast<float*>(base + p.dw_slots);
-        w.scale = scale;
-        w.ldo = d->lddw;
-        w.out = static_cast<__nv_bfloat16*>(dW) + (vk ? (int64_t)v0 * d->lddw : v0);
+        if (!out_job(w, joins.j[njoin], reinterpret_cast<float*>(base + p.dw_slots), nullptr, 0, false, true,
+                     static_cast<__nv_bfloat16*>(dW) + (vk ? (int64_t)v0 * d->lddw : v0), d->lddw, scale))
+          return DSPARK_EINVAL;
         CUtensorMap* tg = vk ? &w.ta : &w.tb;
         CUtensorMap* tx = vk ? &w.tb : &w.ta;
         if (!encode(tg, G, cols, d->N, p.ldg, kLcKb) || !encode(tx, X, d->K, d->N, d->ldx, kLcKb)) return DSPARK_EINVAL;
         if (w.split) {
-          joins.j[njoin++] = join_of(w);
+          ++njoin;
           const int n = tiles_of(w.M) * tiles_of(w.Nn);
           join_tiles = join_tiles > n ? join_tiles : n;
         }
@@ -1053,8 +1111,7 @@ extern "C" dspark_status dspark_linear_ce_grad(const dspark_lce_dims* d, const v
       if (!z_job(g, d, X, W, U, target, v0, cols)) return DSPARK_EINVAL;
       g.lse = lse;
       g.wt = wt;
-      g.G = reinterpret_cast<__nv_bfloat16*>(base + p.G[i & 1]);
-      g.ldg = p.ldg;
+      if (!encode_box(&g.to, base + p.G[i & 1], true, cols, d->N, p.ldg)) return DSPARK_EINVAL;
     }
     e = l.run(st);
     if (njoin > 0 && e == cudaSuccess)
