@@ -18,8 +18,9 @@
 // columns, 32 KB per 64-deep stage instead of the 48 KB of a 128 x 256 tile
 // per CTA), TMA into a six-stage ring, two accumulators so that the epilogue
 // of a tile runs under the next tile's products. An operand whose contraction
-// index is its row (W in dX, G and X in dW) is read in place as an MN-major
-// operand; nothing is transposed in memory.
+// index is its row (W in dX, G in dW) is read in place as an MN-major operand;
+// only X is transposed in memory, once, for a long dW (the reason is at
+// make_plan).
 //
 //   warp 0      TMA producer (both CTAs; bytes counted on the even CTA)
 //   warp 1      allocates TMEM; in the even CTA issues the MMAs of the pair
@@ -101,6 +102,7 @@ struct LcJob {
   int64_t lda;
   int acc_in;           // add what acc holds
   int to_out;           // the result is complete: to out (through `to`), scaled; else to acc
+  int t_out;            // the result is written transposed: out is [Nn][ldo]
   __nv_bfloat16* out;   // [M][ldo]
   int64_t ldo;
   float scale;
@@ -619,14 +621,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
         if (whole && (dx ? jx.to_out : jw.to_out)) {
           const float f = dx ? jx.scale : jw.scale;
           const int Nn = dx ? jx.Nn : jw.Nn;
+          __nv_bfloat16* out = dx ? jx.out : jw.out;
+          const int64_t ldo = dx ? jx.ldo : jw.ldo;
+          const CUtensorMap* to = dx ? &jx.to : &jw.to;
           uint32_t r[kLcPart / 2];
-          each_part([&](int h) LC_INLINE {
+          auto pack = [&](int h) LC_INLINE {
             if (acc_in) add_acc(h);
 #pragma unroll
             for (int k = 0; k < kLcPart / 2; ++k) r[k] = pack_bf16(v[2 * k] * f, v[2 * k + 1] * f);
-          }, [&](int h) LC_INLINE {
-            put16(r, h, dx ? &jx.to : &jw.to, Nn, dx ? jx.out : jw.out, dx ? jx.ldo : jw.ldo);
-          });
+          };
+          if (dx ? jx.t_out : jw.t_out) {
+            // a 32 x 32 box with the result's columns as rows: lanes side by side
+            const int M = dx ? jx.M : jw.M, r0 = row - lane;
+            __nv_bfloat16* tb = reinterpret_cast<__nv_bfloat16*>(smem + ooff);
+            each_part(pack, [&](int h) LC_INLINE {
+              const int oc = col + kLcPart * h;
+              box_free();
+#pragma unroll
+              for (int k = 0; k < kLcPart; ++k)
+                tb[32 * k + lane] = __ushort_as_bfloat16((unsigned short)(r[k / 2] >> (16 * (k & 1))));
+              if ((M & 7) != 0 && r0 + 32 > M) {  // a ragged end of the rows written, value by value
+                if (has)
+                  for (int k = 0; k < min(kLcPart, Nn - oc); ++k) out[(oc + k) * ldo + row] = tb[32 * k + lane];
+              } else {
+                put(to, r0, oc);
+              }
+            });
+          } else {
+            each_part(pack, [&](int h) LC_INLINE { put16(r, h, to, Nn, out, ldo); });
+          }
         } else {
           const CUtensorMap* tm = whole ? (dx ? &jx.tacc : &jw.tacc) : (dx ? &jx.tslots : &jw.tslots);
           const int sc = whole ? col : c0, sr = whole ? row - lane : w.slot * kLcTile + row0;
@@ -721,17 +744,20 @@ struct LcJoin {
   float* acc;
   int64_t lda;
   int acc_in;
-  __nv_bfloat16* out;
+  __nv_bfloat16* out;   // null: acc
   int64_t ldo;
+  int t_out;
   float scale;
 };
 struct LcJoins {
   LcJoin j[2];
 };
 
-constexpr int kLcJoinRows = 4;   // rows of a tile per CTA: a float4 per thread
+// a CTA takes 32 rows x 32 columns of a tile: a float4 per thread
+constexpr int kLcJoinDim = 32;
 
 __global__ void __launch_bounds__(256) k_lce_join(const __grid_constant__ LcJoins p) {
+  __shared__ float sh[kLcJoinDim][kLcJoinDim + 1];
   pdl_wait();
   pdl_trigger();
   const LcJoin& j = p.j[blockIdx.z];
@@ -743,17 +769,24 @@ __global__ void __launch_bounds__(256) k_lce_join(const __grid_constant__ LcJoin
   while (lc_share(units, j.split, pf + 1) <= u0) ++pf;
   while (lc_share(units, j.split, pl + 1) <= u1 - 1) ++pl;
   if (pf == pl) return;  // one pair held all of it and wrote it
-  const int g = tile / (16 * j.nt), gm = min(16, j.mt - g * 16);
-  tile -= g * 16 * j.nt;
+  int g = 0, gm = j.mt;
+  if (gm > 16) {
+    g = tile / (16 * j.nt);
+    gm = min(16, gm - g * 16);
+    tile -= g * 16 * j.nt;
+  }
   const int n = tile / gm, m = g * 16 + tile - n * gm;
-  const int c = (threadIdx.x & 63) * 4, col = n * kLcTile + c;
-  if (col >= j.Nn) return;
-  {
-    const int lr = blockIdx.y * kLcJoinRows + (threadIdx.x >> 6), row = m * kLcTile + lr;
-    if (row >= j.M) return;
+  const int lr0 = (blockIdx.y >> 3) * kLcJoinDim, lc0 = (blockIdx.y & 7) * kLcJoinDim;
+  const int r = threadIdx.x >> 3, c = (threadIdx.x & 7) * 4;
+  const int row0 = m * kLcTile + lr0, col0 = n * kLcTile + lc0;
+  if (row0 >= j.M || col0 >= j.Nn) return;
+  const int row = row0 + r, col = col0 + c;
+  const bool has = row < j.M && col < j.Nn;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (has) {
     // the first pair's part began with the tile (an odd slot); the others' ranges begin inside it
-    const float* sl = j.slots + ((int64_t)(2 * pf + 1) * kLcTile + lr) * kLcTile + c;
-    float4 a = *reinterpret_cast<const float4*>(sl);
+    const float* sl = j.slots + ((int64_t)(2 * pf + 1) * kLcTile + lr0 + r) * kLcTile + lc0 + c;
+    a = *reinterpret_cast<const float4*>(sl);
     sl += kLcTile * kLcTile;
 #pragma unroll 8
     for (int q = pf + 1; q <= pl; ++q, sl += 2 * kLcTile * kLcTile) {
@@ -771,20 +804,64 @@ __global__ void __launch_bounds__(256) k_lce_join(const __grid_constant__ LcJoin
       a.z += x.z;
       a.w += x.w;
     }
-    if (!j.out) {
-      *ap = a;
-      return;
-    }
-    __nv_bfloat16* o = j.out + (int64_t)row * j.ldo + col;
-    if (col + 4 <= j.Nn) {
-      uint2 x;
-      x.x = pack_bf16(a.x * j.scale, a.y * j.scale);
-      x.y = pack_bf16(a.z * j.scale, a.w * j.scale);
-      *reinterpret_cast<uint2*>(o) = x;
+    if (!j.out) *ap = a;
+  }
+  if (!j.out) return;
+  float f[4] = {a.x * j.scale, a.y * j.scale, a.z * j.scale, a.w * j.scale};
+  int orow = row, ocol = col, oN = j.Nn;
+  if (j.t_out) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sh[r][c + i] = f[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = sh[c + i][r];
+    orow = col0 + r;
+    ocol = row0 + c;
+    oN = j.M;
+    if (orow >= j.Nn) return;
+  } else if (!has) {
+    return;
+  }
+  __nv_bfloat16* o = j.out + (int64_t)orow * j.ldo + ocol;
+  if (ocol + 4 <= oN) {
+    uint2 x;
+    x.x = pack_bf16(f[0], f[1]);
+    x.y = pack_bf16(f[2], f[3]);
+    *reinterpret_cast<uint2*>(o) = x;
+  } else {
+    for (int e = 0; ocol + e < oN; ++e) o[e] = __float2bfloat16_rn(f[e]);
+  }
+}
+
+// XT[k][n] = X[n][k], rows of XT padded to a multiple of 8 (with zeros): 64 x 64
+// through shared memory, 16-byte pieces on both sides.
+__global__ void __launch_bounds__(256)
+    k_lce_transpose(const __nv_bfloat16* __restrict__ X, int64_t ldx, int N, int K, __nv_bfloat16* __restrict__ XT,
+                    int64_t ldt) {
+  __shared__ __nv_bfloat16 sh[64][66];
+  pdl_wait();
+  pdl_trigger();
+  const int k0 = blockIdx.x * 64, n0 = blockIdx.y * 64;
+  for (int i = threadIdx.x; i < 512; i += 256) {
+    const int r = i >> 3, c = (i & 7) * 8, n = n0 + r, k = k0 + c;
+    __align__(16) __nv_bfloat16 x[8];
+    if (n < N && k + 8 <= K) {
+      *reinterpret_cast<uint4*>(x) = *reinterpret_cast<const uint4*>(X + n * ldx + k);
     } else {
-      const float f[4] = {a.x, a.y, a.z, a.w};
-      for (int e = 0; col + e < j.Nn; ++e) o[e] = __float2bfloat16_rn(f[e] * j.scale);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = n < N && k + e < K ? X[n * ldx + k + e] : __float2bfloat16_rn(0.f);
     }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sh[r][c + e] = x[e];
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 512; i += 256) {
+    const int r = i >> 3, c = (i & 7) * 8, k = k0 + r, n = n0 + c;
+    if (k >= K || n >= N) continue;
+    __align__(16) __nv_bfloat16 x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = sh[c + e][r];
+    *reinterpret_cast<uint4*>(XT + k * ldt + n) = *reinterpret_cast<const uint4*>(x);
   }
 }
 
@@ -812,14 +889,15 @@ bool encode(CUtensorMap* tm, const void* p, int64_t cols, int64_t rows, int64_t 
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 // The epilogue's boxes of 32 rows of 128 bytes: fp32 (U, sums, parts) or bf16 (results).
-bool encode_box(CUtensorMap* tm, const void* p, bool bf16, int64_t cols, int64_t rows, int64_t ld) {
+// Transposed results: bf16, 32 rows of 32 columns, as they lie.
+bool encode_box(CUtensorMap* tm, const void* p, bool bf16, int64_t cols, int64_t rows, int64_t ld, bool t = false) {
   const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
   const cuuint64_t strides[1] = {(cuuint64_t)ld * (bf16 ? 2 : 4)};
-  const cuuint32_t box[2] = {bf16 ? 64u : 32u, 32};
+  const cuuint32_t box[2] = {bf16 && !t ? 64u : 32u, 32};
   const cuuint32_t es[2] = {1, 1};
   return encode_fn()(tm, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2,
                      const_cast<void*>(p), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+                     t ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 int64_t up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
@@ -842,8 +920,10 @@ struct LcPlan {
   int64_t ldg;
   int dx_split, dw_split;
   int64_t dx_lda;
-  size_t part, zt, fwd_total;                          // forward
-  size_t G[2], dx_acc, dx_slots, dw_slots, bwd_total;  // gradient
+  bool swap;    // the operand whose contraction index is its row goes to A (see make_plan)
+  int64_t ldt;  // of X's transpose
+  size_t part, zt, fwd_total;                              // forward
+  size_t G[2], dx_acc, dx_slots, dw_slots, XT, bwd_total;  // gradient
 };
 
 constexpr int64_t kLcPieceBytes = 256ll << 20;
@@ -871,11 +951,20 @@ LcPlan make_plan(const dspark_lce_dims& d) {
   const int64_t nkb_v = (widest + kLcKb - 1) / kLcKb, nkb_n = (N + kLcKb - 1) / kLcKb;
   p.dx_split = split_of(tiles_of(N) * tiles_of(K), (int)nkb_v);
   p.dw_split = split_of(tiles_of(widest) * tiles_of(K), (int)nkb_n);
-  p.dx_lda = up(K, 32);
+  // An MN-major B (its contraction index is its row) costs the tensor cores
+  // 1.38x the time of a K-major one, an MN-major A nothing (256 x 256 tiles,
+  // contraction 5376: 885 against 640 cycles a block). So where the products are
+  // long, dX with W [V][K] is made transposed (A = W, B = G) and turned in its
+  // epilogue, and dW takes X's transpose, made once, as B. Where they are short
+  // the extra launch costs more than it saves (N K V = 2e10: 10 us saved, 3 spent).
+  p.swap = (double)N * K * V >= 1e10;
+  p.ldt = up(N, 8);
+  p.dx_lda = p.swap && d.layout == DSPARK_W_VK ? up(N, 32) : up(K, 32);
   off = 0;
   p.G[0] = carve(2 * N * p.ldg);
   p.G[1] = p.pieces > 1 ? carve(2 * N * p.ldg) : p.G[0];
-  p.dx_acc = carve(p.pieces > 1 ? 4 * N * p.dx_lda : 0);
+  p.dx_acc = carve(p.pieces > 1 ? 4 * p.dx_lda * (p.swap && d.layout == DSPARK_W_VK ? K : N) : 0);
+  p.XT = carve(p.swap ? 2 * K * p.ldt : 0);
   p.dx_slots = carve(4ll * 2 * p.dx_split * kLcTile * kLcTile);
   p.dw_slots = carve(4ll * 2 * p.dw_split * kLcTile * kLcTile);
   p.bwd_total = off;
@@ -956,11 +1045,12 @@ bool z_job(LcJob& j, const dspark_lce_dims* d, const void* X, const void* W, con
 // Where a gradient's product goes: parts of shared tiles to slots, whole tiles
 // to acc (summed over the vocabulary's pieces) or, complete, to out.
 bool out_job(LcJob& j, LcJoin& q, float* slots, float* acc, int64_t lda, bool acc_in, bool to_out,
-             __nv_bfloat16* out, int64_t ldo, float scale) {
+             __nv_bfloat16* out, int64_t ldo, bool t_out, float scale) {
   j.acc = acc;
   j.lda = lda;
   j.acc_in = acc_in;
   j.to_out = to_out;
+  j.t_out = t_out;
   j.out = out;
   j.ldo = ldo;
   j.scale = scale;
@@ -976,9 +1066,11 @@ bool out_job(LcJob& j, LcJoin& q, float* slots, float* acc, int64_t lda, bool ac
   q.acc_in = acc_in;
   q.out = to_out ? out : nullptr;
   q.ldo = ldo;
+  q.t_out = t_out;
   q.scale = scale;
   if (j.split && !encode_box(&j.tslots, slots, false, kLcTile, 2ll * j.split * kLcTile, kLcTile)) return false;
-  return to_out ? encode_box(&j.to, out, true, j.Nn, j.M, ldo) : encode_box(&j.tacc, acc, false, lda, j.M, lda);
+  if (!to_out) return encode_box(&j.tacc, acc, false, lda, j.M, lda);
+  return t_out ? encode_box(&j.to, out, true, j.M, j.Nn, ldo, true) : encode_box(&j.to, out, true, j.Nn, j.M, ldo);
 }
 
 dspark_status lce_fail(cudaError_t e) {
@@ -1056,6 +1148,10 @@ extern "C" dspark_status dspark_linear_ce_grad(const dspark_lce_dims* d, const v
   }
   const LcPlan p = make_plan(*d);
   char* base = static_cast<char*>(scratch);
+  if (dW && p.swap)
+    e = launch_ex(k_lce_transpose, dim3((d->K + 63) / 64, (d->N + 63) / 64), dim3(256), 0, st, true,
+                  static_cast<const __nv_bfloat16*>(X), d->ldx, d->N, d->K, reinterpret_cast<__nv_bfloat16*>(base + p.XT),
+                  p.ldt);
   // launch i makes G of piece i beside the gradients' products of piece i - 1
   for (int i = 0; i <= p.pieces && e == cudaSuccess; ++i) {
     LcLaunch l(true, device_status);
@@ -1066,19 +1162,27 @@ extern "C" dspark_status dspark_linear_ce_grad(const dspark_lce_dims* d, const v
       const __nv_bfloat16* G = reinterpret_cast<const __nv_bfloat16*>(base + p.G[(i - 1) & 1]);
       if (dX) {
         LcJob& x = l.add(kLcDx);
-        x.M = d->N;
-        x.Nn = d->K;
+        const bool t = p.swap && vk;  // dX^T = W^T G^T
+        x.M = t ? d->K : d->N;
+        x.Nn = t ? d->N : d->K;
         x.nkb = (cols + kLcKb - 1) / kLcKb;
         x.split = p.dx_split ? split_of(tiles_of(x.M) * tiles_of(x.Nn), x.nkb) : 0;
-        x.b_mn = vk;
-        x.b_k0 = v0;
         if (!out_job(x, joins.j[njoin], reinterpret_cast<float*>(base + p.dx_slots),
                      reinterpret_cast<float*>(base + p.dx_acc), p.dx_lda, i > 1, i == p.pieces,
-                     static_cast<__nv_bfloat16*>(dX), d->lddx, scale))
+                     static_cast<__nv_bfloat16*>(dX), d->lddx, t, scale))
           return DSPARK_EINVAL;
-        if (!encode(&x.ta, G, cols, d->N, p.ldg, kLcHalf)) return DSPARK_EINVAL;
-        if (!(vk ? encode(&x.tb, W, d->K, d->V, d->ldw, kLcKb) : encode(&x.tb, W, d->V, d->K, d->ldw, kLcHalf)))
-          return DSPARK_EINVAL;
+        bool ok;
+        if (t) {
+          x.a_mn = 1;
+          ok = encode(&x.ta, static_cast<const __nv_bfloat16*>(W) + (int64_t)v0 * d->ldw, d->K, cols, d->ldw, kLcKb) &&
+               encode(&x.tb, G, cols, d->N, p.ldg, kLcHalf);
+        } else {
+          x.b_mn = vk;
+          x.b_k0 = v0;
+          ok = encode(&x.ta, G, cols, d->N, p.ldg, kLcHalf) &&
+               (vk ? encode(&x.tb, W, d->K, d->V, d->ldw, kLcKb) : encode(&x.tb, W, d->V, d->K, d->ldw, kLcHalf));
+        }
+        if (!ok) return DSPARK_EINVAL;
         if (x.split) {
           ++njoin;
           join_tiles = tiles_of(x.M) * tiles_of(x.Nn);
@@ -1086,18 +1190,24 @@ extern "C" dspark_status dspark_linear_ce_grad(const dspark_lce_dims* d, const v
       }
       if (dW) {
         LcJob& w = l.add(kLcDw);
-        w.M = vk ? cols : d->K;
-        w.Nn = vk ? d->K : cols;
+        const bool rows_v = vk || p.swap;  // the product's rows are tokens (W [K][V]: written transposed)
+        w.M = rows_v ? cols : d->K;
+        w.Nn = rows_v ? d->K : cols;
         w.nkb = (d->N + kLcKb - 1) / kLcKb;
         // a last piece of fewer tiles than the others shares them only if the others do (its slots are theirs)
         w.split = p.dw_split ? split_of(tiles_of(w.M) * tiles_of(w.Nn), w.nkb) : 0;
-        w.a_mn = w.b_mn = 1;
         if (!out_job(w, joins.j[njoin], reinterpret_cast<float*>(base + p.dw_slots), nullptr, 0, false, true,
-                     static_cast<__nv_bfloat16*>(dW) + (vk ? (int64_t)v0 * d->lddw : v0), d->lddw, scale))
+                     static_cast<__nv_bfloat16*>(dW) + (vk ? (int64_t)v0 * d->lddw : v0), d->lddw, rows_v && !vk,
+                     scale))
           return DSPARK_EINVAL;
-        CUtensorMap* tg = vk ? &w.ta : &w.tb;
-        CUtensorMap* tx = vk ? &w.tb : &w.ta;
-        if (!encode(tg, G, cols, d->N, p.ldg, kLcKb) || !encode(tx, X, d->K, d->N, d->ldx, kLcKb)) return DSPARK_EINVAL;
+        w.a_mn = 1;
+        w.b_mn = !p.swap;
+        CUtensorMap* tg = rows_v ? &w.ta : &w.tb;
+        CUtensorMap* tx = rows_v ? &w.tb : &w.ta;
+        if (!encode(tg, G, cols, d->N, p.ldg, kLcKb) ||
+            !(p.swap ? encode(tx, base + p.XT, d->N, d->K, p.ldt, kLcHalf)
+                     : encode(tx, X, d->K, d->N, d->ldx, kLcKb)))
+          return DSPARK_EINVAL;
         if (w.split) {
           ++njoin;
           const int n = tiles_of(w.M) * tiles_of(w.Nn);
@@ -1115,7 +1225,8 @@ extern "C" dspark_status dspark_linear_ce_grad(const dspark_lce_dims* d, const v
     }
     e = l.run(st);
     if (njoin > 0 && e == cudaSuccess)
-      e = launch_ex(k_lce_join, dim3(join_tiles, kLcTile / kLcJoinRows, njoin), dim3(256), 0, st, true, joins);
+      e = launch_ex(k_lce_join, dim3(join_tiles, (kLcTile / kLcJoinDim) * (kLcTile / kLcJoinDim), njoin), dim3(256), 0,
+                    st, true, joins);
   }
   return lce_fail(e);
 }

@@ -144,6 +144,18 @@ def test_vocabulary_in_pieces():
         _check(X, W, U, t, wt, 0.5, layout)
 
 
+@pytest.mark.parametrize("layout", ["vk", "kv"])
+@pytest.mark.parametrize("N,K,V,U,pad,ignored", [
+    (1500, 1001, 7003, False, 0, 0.1),     # ragged in every size, parts of tiles shared by pairs of CTAs
+    (1030, 1300, 9000, True, 8, 0.0),
+    (3000, 2100, 40003, False, 0, 0.2),    # many tiles, the second piece narrower than the first
+])
+def test_long_products(N, K, V, U, pad, ignored, layout):
+    """N K V of 1e10 and more: dX or dW is made transposed, X's transpose is an operand."""
+    X, W, Um, t, wt = _inputs(N, K, V, layout, U, pad, ignored)
+    _check(X, W, Um, t, wt, 0.25, layout)
+
+
 @pytest.mark.parametrize("dx,dw", [(True, False), (False, True)])
 @pytest.mark.parametrize("layout", ["vk", "kv"])
 def test_one_gradient_alone(dx, dw, layout):
@@ -245,12 +257,13 @@ def test_no_rows_and_all_rows_left_out():
 
 
 def test_padding_of_the_outputs_is_left_alone():
-    for layout, N, K, V in (("vk", 70, 50, 300), ("kv", 70, 50, 301)):
+    for layout, N, K, V in (("vk", 70, 50, 300), ("kv", 70, 50, 301), ("vk", 2050, 1250, 5003), ("kv", 2050, 1250, 5003)):
         X, W, U, t, wt = _inputs(N, K, V, layout)
         op = LinearCE(N, K, V, layout)
         out = op.new_outputs(False, False)
-        full = {"dX": torch.full((N, 64), 9.0, dtype=BF16, device="cuda"),
-                "dW": torch.full((V, 64) if layout == "vk" else (K, 320), 9.0, dtype=BF16, device="cuda")}
+        k64, v64 = -(-K // 64) * 64, -(-V // 64) * 64
+        full = {"dX": torch.full((N, k64), 9.0, dtype=BF16, device="cuda"),
+                "dW": torch.full((V, k64) if layout == "vk" else (K, v64), 9.0, dtype=BF16, device="cuda")}
         cols = {"dX": K, "dW": K if layout == "vk" else V}
         for k in full:
             out[k] = full[k][:, :cols[k]]
