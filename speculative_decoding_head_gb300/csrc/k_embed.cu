@@ -12,7 +12,7 @@
 // takes 256 consecutive sorted rows whatever tokens they hold (frequent tokens
 // own long runs, rare ones short runs, most of a large vocabulary none), so the
 // work is even: runs inside the CTA are written at once, a run that crosses CTAs
-// leaves fp32 partial sums that the last kernel adds in order. The same launch
+// leaves fp32 partial sums that the last kernel adds in order. That kernel also
 // writes the rows of the tokens that do not occur.
 #include <math.h>
 #include <stdio.h>
@@ -124,73 +124,98 @@ constexpr int kSoThreads = 512;
 constexpr int kSoWarps = kSoThreads / 32;
 constexpr int kSoBits = 10;
 constexpr int kSoBins = 1 << kSoBits;
-constexpr int kSoTile = 4096;    // rows of a CTA, while that leaves at most kSoCtas CTAs
-constexpr int kSoCtas = 64;
+constexpr int kSoKeys = 8;                              // pairs a thread holds
+constexpr int kSoTile = kSoThreads * kSoKeys;           // 4096 pairs a CTA holds at a time
+constexpr int kSoCtas = 128;
 constexpr size_t kSoSmem = sizeof(int) * (size_t)kSoWarps * kSoBins;
 
 // One pass's input: the tokens themselves (rows without one are left out) or
 // the pairs of the pass before.
-struct SoIn {
-  const int32_t* idx;
-  const int2* pairs;   // (token, row)
-  const int* count;    // pairs in all
+struct SoPass {
+  const int32_t* idx;   // [N], or null:
+  const int2* pairs;    // (token, row)
   int N, V;
+  int shift, bins;
+  int per;              // pairs of a CTA (a multiple of kSoTile)
+  int* cta;             // [CTAs][bins] counts
+  int2* out;            // pairs, or null in the last pass:
+  int32_t* rows;        // [N] sorted rows
+  int32_t* toks;        // [N] their tokens
+  int* total;           // pairs in all (written by the first pass)
+  unsigned char* seen;  // [V] token occurs (cleared before the first placement, set by it)
+  int* status;
 };
-__device__ __forceinline__ int so_n(const SoIn& in) { return in.idx ? in.N : *in.count; }
-__device__ __forceinline__ bool so_load(const SoIn& in, int i, int n, int2& p) {
-  if (i >= n) return false;
-  if (!in.idx) {
-    p = in.pairs[i];
-    return true;
+
+// A warp's pairs of the tile that begins at a: kSoKeys runs of 32 in order. A
+// row without a token has digit -1.
+struct SoKeys {
+  int2 p[kSoKeys];
+  int d[kSoKeys];
+};
+__device__ __forceinline__ void so_load(const SoPass& q, int a, int n, SoKeys& k) {
+  const int w0 = a + (threadIdx.x >> 5) * (32 * kSoKeys) + (threadIdx.x & 31);
+#pragma unroll
+  for (int i = 0; i < kSoKeys; ++i) {
+    const int at = w0 + 32 * i;
+    k.p[i] = make_int2(-1, at);
+    if (at < n) {
+      if (q.idx)
+        k.p[i].x = q.idx[at];
+      else
+        k.p[i] = q.pairs[at];
+    }
   }
-  p = make_int2(in.idx[i], i);
-  return p.x >= 0 && p.x < in.V;
+#pragma unroll
+  for (int i = 0; i < kSoKeys; ++i)
+    k.d[i] = k.p[i].x >= 0 && k.p[i].x < q.V ? (k.p[i].x >> q.shift) & (q.bins - 1) : -1;
 }
 
-// Counts of each warp's rows by digit, in warp order: hist [warps][bins].
-__device__ __forceinline__ void so_count(const SoIn& in, int a, int b, int n, int shift, int mask, int* hist,
-                                         int bins) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+// Counts of each warp's pairs by digit into hist [warps][bins].
+__device__ __forceinline__ void so_count(const SoKeys& k, int* hist, int bins) {
   for (int i = threadIdx.x; i < kSoWarps * bins; i += kSoThreads) hist[i] = 0;
   __syncthreads();
-  const int per = (b - a + kSoWarps - 1) / kSoWarps, wa = min(b, a + warp * per), wb = min(b, wa + per);
-  for (int i = wa; i < wb; i += 32) {
-    int2 p;
-    const bool has = i + lane < wb && so_load(in, i + lane, n, p);
-    if (has) atomicAdd(&hist[warp * bins + ((p.x >> shift) & mask)], 1);
-  }
+  int* h = hist + (threadIdx.x >> 5) * bins;
+#pragma unroll
+  for (int i = 0; i < kSoKeys; ++i)
+    if (k.d[i] >= 0) atomicAdd(h + k.d[i], 1);
   __syncthreads();
 }
 
-// The rows of [a, b) to their places: hist holds each warp's first place per digit.
-__device__ __forceinline__ void so_place(const SoIn& in, int a, int b, int n, int shift, int mask, int* hist, int bins,
-                                         int2* out, int32_t* rows, int32_t* toks) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int per = (b - a + kSoWarps - 1) / kSoWarps, wa = min(b, a + warp * per), wb = min(b, wa + per);
-  for (int i = wa; i < wb; i += 32) {
-    int2 p;
-    const bool has = i + lane < wb && so_load(in, i + lane, n, p);
-    const int d = has ? (p.x >> shift) & mask : bins;  // lanes without a row match one another only
-    const unsigned same = __match_any_sync(0xFFFFFFFFu, d);
+// The pairs to their places: hist holds each warp's first place per digit.
+__device__ __forceinline__ void so_place(const SoPass& q, const SoKeys& k, int* hist) {
+  const int lane = threadIdx.x & 31;
+  int* h = hist + (threadIdx.x >> 5) * q.bins;
+#pragma unroll
+  for (int i = 0; i < kSoKeys; ++i) {
+    const unsigned same = __match_any_sync(0xFFFFFFFFu, k.d[i]);
     const int rank = __popc(same & ((1u << lane) - 1u));
     int at = 0;
-    if (has) at = hist[warp * bins + d] + rank;
+    if (k.d[i] >= 0) at = h[k.d[i]] + rank;
     __syncwarp();
-    if (has && rank == 0) hist[warp * bins + d] += __popc(same);
+    if (k.d[i] >= 0 && rank == 0) h[k.d[i]] += __popc(same);
     __syncwarp();
-    if (has) {
-      if (out)
-        out[at] = p;
-      else {
-        toks[at] = p.x;
-        rows[at] = p.y;
-      }
+    if (k.d[i] < 0) continue;
+    if (q.out) {
+      q.out[at] = k.p[i];
+    } else {
+      q.toks[at] = k.p[i].x;
+      q.rows[at] = k.p[i].y;
     }
   }
 }
 
-// Exclusive prefix of one value per thread over the first `bins` values of
-// bin totals held by threads two apart; tot[bins] in shared memory, returns the sum.
+// Marks of the tokens that occur, and tokens out of range reported (first pass).
+__device__ __forceinline__ void so_mark(const SoPass& q, const SoKeys& k) {
+#pragma unroll
+  for (int i = 0; i < kSoKeys; ++i) {
+    if (k.d[i] >= 0)
+      q.seen[k.p[i].x] = 1;
+    else if (k.p[i].x != -1)
+      raise_status(q.status, DSPARK_ERANGE);
+  }
+}
+
+// tot[bins] in shared memory to its exclusive prefix; returns the sum.
 __device__ __forceinline__ int so_scan(int* tot, int bins, int* wsum) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int i0 = 2 * tid, x0 = i0 < bins ? tot[i0] : 0, x1 = i0 + 1 < bins ? tot[i0 + 1] : 0;
@@ -220,79 +245,77 @@ __device__ __forceinline__ int so_scan(int* tot, int bins, int* wsum) {
   return all;
 }
 
-// Warp counts -> first places: base[d] (start of the CTA's rows of digit d) plus the earlier warps' counts.
-__device__ __forceinline__ void so_offsets(int* hist, int bins, const int* base) {
+// Warp counts -> first places from base[d] on; base[d] moves past the tile's pairs.
+__device__ __forceinline__ void so_offsets(int* hist, int bins, int* base) {
   for (int d = threadIdx.x; d < bins; d += kSoThreads) {
+    int c[kSoWarps];
+#pragma unroll
+    for (int w = 0; w < kSoWarps; ++w) c[w] = hist[w * bins + d];
     int at = base[d];
+#pragma unroll
     for (int w = 0; w < kSoWarps; ++w) {
-      const int c = hist[w * bins + d];
       hist[w * bins + d] = at;
-      at += c;
+      at += c[w];
     }
+    base[d] = at;
   }
   __syncthreads();
 }
 
-struct SoPass {
-  SoIn in;
-  int shift, mask, bins;
-  int per;              // rows of a CTA
-  int* cta;             // [CTAs][bins] counts
-  int2* out;            // pairs, or null in the last pass:
-  int32_t* rows;        // [N] sorted rows
-  int32_t* toks;        // [N] their tokens
-  int* total;           // pairs in all (written by the first pass)
-  unsigned char* seen;  // [V] token occurs (cleared by the first count, set by the first placement)
-  int V;
-  int* status;
-};
+__device__ __forceinline__ int so_n(const SoPass& q) { return q.idx ? q.N : *q.total; }
 
-// Bounds of a token and its mark: the first pass alone reads the tokens.
-__device__ __forceinline__ void so_mark(const SoPass& p, int a, int b) {
-  for (int i = a + (int)threadIdx.x; i < b; i += kSoThreads) {
-    const int t = p.in.idx[i];
-    if (t >= 0 && t < p.V) p.seen[t] = 1;
-    if (t < -1 || t >= p.V) raise_status(p.status, DSPARK_ERANGE);
-  }
-}
-
-__global__ void __launch_bounds__(kSoThreads) k_sort_count(SoPass p) {
+__global__ void __launch_bounds__(kSoThreads) k_sort_count(SoPass q) {
   extern __shared__ int so_hist[];
-  const int n = so_n(p.in), a = min(n, (int)blockIdx.x * p.per), b = min(n, a + p.per);
-  if (p.in.idx)
-    for (int i = blockIdx.x * kSoThreads + threadIdx.x; i < p.V; i += gridDim.x * kSoThreads) p.seen[i] = 0;
-  so_count(p.in, a, b, n, p.shift, p.mask, so_hist, p.bins);
-  for (int d = threadIdx.x; d < p.bins; d += kSoThreads) {
-    int s = 0;
-    for (int w = 0; w < kSoWarps; ++w) s += so_hist[w * p.bins + d];
-    p.cta[blockIdx.x * p.bins + d] = s;
+  pdl_wait();
+  if (q.idx)
+    for (int i = blockIdx.x * kSoThreads + threadIdx.x; i < q.V; i += gridDim.x * kSoThreads) q.seen[i] = 0;
+  const int n = so_n(q), a = min(n, (int)blockIdx.x * q.per), b = min(n, a + q.per);
+  for (int i = threadIdx.x; i < q.bins; i += kSoThreads) so_hist[i] = 0;
+  __syncthreads();
+  for (int t = a; t < b; t += kSoTile) {
+    SoKeys k;
+    so_load(q, t, b, k);
+#pragma unroll
+    for (int i = 0; i < kSoKeys; ++i)
+      if (k.d[i] >= 0) atomicAdd(so_hist + k.d[i], 1);
   }
+  __syncthreads();
+  pdl_trigger();
+  for (int d = threadIdx.x; d < q.bins; d += kSoThreads) q.cta[blockIdx.x * q.bins + d] = so_hist[d];
 }
 
-__global__ void __launch_bounds__(kSoThreads) k_sort_place(SoPass p) {
+__global__ void __launch_bounds__(kSoThreads) k_sort_place(SoPass q) {
   extern __shared__ int so_hist[];
   __shared__ int tot[kSoBins], mine[kSoBins], wsum[kSoWarps];
-  const int n = so_n(p.in), a = min(n, (int)blockIdx.x * p.per), b = min(n, a + p.per);
-  for (int d = threadIdx.x; d < p.bins; d += kSoThreads) {
+  pdl_wait();
+  const int n = so_n(q), a = min(n, (int)blockIdx.x * q.per), b = min(n, a + q.per);
+  SoKeys k;
+  so_load(q, a, b, k);  // on their way while the counts are added up
+  for (int d = threadIdx.x; d < q.bins; d += kSoThreads) {
     int s = 0, before = 0;
-#pragma unroll 8
-    for (int c = 0; c < (int)gridDim.x; ++c) {
-      if (c == (int)blockIdx.x) before = s;
-      s += p.cta[c * p.bins + d];
+    const int* c = q.cta + d;
+#pragma unroll 16
+    for (int i = 0; i < (int)gridDim.x; ++i) {
+      const int x = c[i * q.bins];
+      before += i < (int)blockIdx.x ? x : 0;
+      s += x;
     }
     tot[d] = s;
     mine[d] = before;
   }
-  so_count(p.in, a, b, n, p.shift, p.mask, so_hist, p.bins);
-  const int all = so_scan(tot, p.bins, wsum);
-  for (int d = threadIdx.x; d < p.bins; d += kSoThreads) mine[d] += tot[d];
   __syncthreads();
-  so_offsets(so_hist, p.bins, mine);
-  so_place(p.in, a, b, n, p.shift, p.mask, so_hist, p.bins, p.out, p.rows, p.toks);
-  if (p.in.idx) {
-    if (blockIdx.x == 0 && threadIdx.x == 0) *p.total = all;
-    so_mark(p, a, b);
+  const int all = so_scan(tot, q.bins, wsum);
+  for (int d = threadIdx.x; d < q.bins; d += kSoThreads) mine[d] += tot[d];
+  if (q.idx && blockIdx.x == 0 && threadIdx.x == 0) *q.total = all;
+  for (int t = a; t < b; t += kSoTile) {
+    if (t > a) so_load(q, t, b, k);
+    so_count(k, so_hist, q.bins);
+    so_offsets(so_hist, q.bins, mine);
+    so_place(q, k, so_hist);
+    if (q.idx) so_mark(q, k);
+    __syncthreads();
   }
+  pdl_trigger();
 }
 
 // All passes in one CTA, for few rows.
@@ -302,53 +325,60 @@ struct SoSmall {
   int2* buf[2];
 };
 
-__global__ void __launch_bounds__(kSoThreads) k_sort_small(SoSmall q) {
+__global__ void __launch_bounds__(kSoThreads) k_sort_small(SoSmall s) {
   extern __shared__ int so_hist[];
-  __shared__ int tot[kSoBins], wsum[kSoWarps];
-  SoPass p = q.first;
-  for (int i = threadIdx.x; i < p.V; i += kSoThreads) p.seen[i] = 0;
-  int n = p.in.N;
-  for (int k = 0; k < q.passes; ++k) {
-    p.shift = k * q.bits;
-    so_count(p.in, 0, n, n, p.shift, p.mask, so_hist, p.bins);  // its barriers order the clearing of `seen`
-    for (int d = threadIdx.x; d < p.bins; d += kSoThreads) {
-      int s = 0;
-      for (int w = 0; w < kSoWarps; ++w) s += so_hist[w * p.bins + d];
-      tot[d] = s;
+  __shared__ int base[kSoBins], wsum[kSoWarps];
+  pdl_wait();
+  SoPass q = s.first;
+  for (int i = threadIdx.x; i < q.V; i += kSoThreads) q.seen[i] = 0;
+  int n = q.N;
+  for (int pass = 0; pass < s.passes; ++pass) {
+    q.shift = pass * s.bits;
+    q.out = pass + 1 < s.passes ? s.buf[pass & 1] : nullptr;
+    SoKeys k;
+    so_load(q, 0, n, k);
+    so_count(k, so_hist, q.bins);  // its barriers order the clearing of `seen` before the marks
+    for (int d = threadIdx.x; d < q.bins; d += kSoThreads) {
+      int c = 0;
+#pragma unroll
+      for (int w = 0; w < kSoWarps; ++w) c += so_hist[w * q.bins + d];
+      base[d] = c;
     }
     __syncthreads();
-    const int all = so_scan(tot, p.bins, wsum);
-    so_offsets(so_hist, p.bins, tot);
-    int2* out = k + 1 < q.passes ? q.buf[k & 1] : nullptr;
-    so_place(p.in, 0, n, n, p.shift, p.mask, so_hist, p.bins, out, p.rows, p.toks);
-    if (k == 0) {
-      if (threadIdx.x == 0) *p.total = all;
-      so_mark(p, 0, n);
+    const int all = so_scan(base, q.bins, wsum);
+    so_offsets(so_hist, q.bins, base);
+    so_place(q, k, so_hist);
+    if (pass == 0) {
+      so_mark(q, k);
+      if (threadIdx.x == 0) *q.total = all;
       n = all;
     }
     __syncthreads();
-    p.in.idx = nullptr;
-    p.in.pairs = out;
-    p.in.count = p.total;
+    q.idx = nullptr;
+    q.pairs = q.out;
   }
+  pdl_trigger();
 }
 
 // ---------------------------------------------------------------- sums
 constexpr int kSuRows = 256;     // sorted rows of a CTA (32 per warp)
-constexpr int kSuFly = 8;        // rows a warp has in flight
-constexpr int kSuFill = 32;      // vocabulary rows a CTA fills where tokens do not occur
+constexpr int kSuGroup = 4;      // rows asked for together
+constexpr int kSuGroups = 4;     // groups a warp has on their way or at hand (fp32: half of them)
+constexpr int kSuFill = 32;      // vocabulary rows a CTA of the last launch fills where tokens do not occur
 
 struct SuArgs {
   const int32_t* rows;
   const int32_t* toks;
   const int* total;
   const unsigned char* seen;
-  int V, D, chunks;        // chunks: CTAs of sorted rows (the others fill)
+  int V, D, chunks;        // chunks: CTAs of sorted rows
+  int fills;               // CTAs that fill
+  int64_t ldp;             // of head and tail: D rounded up to 4
   int64_t ldd, ldb, lde;
   float scale;
-  float* head;             // [chunks][D] sums of a run that begins in an earlier CTA
-  float* tail;             // [chunks][D] sums of a run that goes on in the next CTA
-  int has_base, fill;
+  float* head;             // [chunks][ldp] sums of a run that begins in an earlier CTA
+  float* tail;             // [chunks][ldp] sums of a run that goes on in the next CTA
+  int has_base;
 };
 
 template <typename TO, bool VEC>
@@ -364,76 +394,98 @@ __device__ __forceinline__ void su_finish(const SuArgs& a, const TO* base, TO* d
   store8<TO, VEC>(dE + v * a.lde + c0, lane, left, o);
 }
 
+template <typename TI>
+__host__ __device__ constexpr int su_groups() {
+  return sizeof(TI) == 2 ? kSuGroups : kSuGroups / 2;
+}
+template <typename TI>
+__host__ __device__ constexpr size_t su_smem() {
+  return (size_t)8 * su_groups<TI>() * kSuGroup * kEmSpan * sizeof(TI);
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// Eight values of a row (a lane's) to shared memory, from where the same lane
+// takes them: asynchronously where the row's pieces lie on 16 bytes.
+template <typename TI, bool VEC>
+__device__ __forceinline__ void su_stage(const TI* row, int lane, int left, TI* to) {
+  if (VEC && lane * 8 + 8 <= left) {
+    const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(to));
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(TI) / 2; ++i) cp_async16(d + 16 * i, row + lane * 8 + 16 / sizeof(TI) * i);
+  } else {
+    __align__(16) TI x[8];
+    load8<TI, VEC>(row, lane, left, x);
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(TI) / 2; ++i)
+      reinterpret_cast<uint4*>(to)[i] = reinterpret_cast<const uint4*>(x)[i];
+  }
+}
+
 template <typename TI, typename TO, bool VEC>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 3)
     k_embed_sum(SuArgs a, const TI* __restrict__ dout, const TO* base, TO* dE) {
-  __shared__ float hd[8][kEmSpan], tl[8][kEmSpan];
+  extern __shared__ __align__(16) unsigned char su_ring[];
+  __shared__ __align__(16) float hd[8][kEmSpan], tl[8][kEmSpan];
   __shared__ int kfirst[8], klast[8], whole[8];
+  constexpr int G = su_groups<TI>();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c0 = blockIdx.y * kEmSpan, left = a.D - c0;
-  if ((int)blockIdx.x >= a.chunks) {
-    // tokens that do not occur: zero, or what is there already
-    const int v0 = ((int)blockIdx.x - a.chunks) * kSuFill;
-    __align__(16) TO o[4][8];
-    int v[4];
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      v[r] = v0 + warp * 4 + r;
-      if (v[r] >= a.V || a.seen[v[r]]) v[r] = -1;
-    }
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      if (a.has_base && v[r] >= 0) {
-        load8<TO, VEC>(base + v[r] * a.ldb + c0, lane, left, o[r]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[r][i] = Num<TO>::down(0.f);
-      }
-    }
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-      if (v[r] >= 0) store8<TO, VEC>(dE + v[r] * a.lde + c0, lane, left, o[r]);
-    return;
-  }
+  TI* ring = reinterpret_cast<TI*>(su_ring) + (size_t)warp * G * kSuGroup * kEmSpan + lane * 8;
+  pdl_wait();
   const int ns = *a.total, p0 = blockIdx.x * kSuRows;
   if (p0 >= ns) return;
   const int w0 = p0 + warp * 32, cnt = max(0, min(32, ns - w0));
   if (cnt > 0) {
     const int tok = lane < cnt ? a.toks[w0 + lane] : -1;
-    const int64_t row = lane < cnt ? a.rows[w0 + lane] : 0;
+    const int row = lane < cnt ? a.rows[w0 + lane] : 0;
     const int first = __shfl_sync(0xFFFFFFFFu, tok, 0), last = __shfl_sync(0xFFFFFFFFu, tok, cnt - 1);
+    // ask for the group that begins with row r0 (the last ones: empty groups keep the count)
+    auto ask = [&](int r0) {
+#pragma unroll
+      for (int f = 0; f < kSuGroup; ++f) {
+        const int r = r0 + f;
+        const int64_t n = __shfl_sync(0xFFFFFFFFu, row, r & 31);
+        if (r < cnt)
+          su_stage<TI, VEC>(dout + n * a.ldd + c0, lane, left, ring + (r % (G * kSuGroup)) * kEmSpan);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int g = 0; g < G - 1; ++g) ask(g * kSuGroup);
     float acc[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i] = 0.f;
     int cur = first;
     bool inner = false;  // the run began after this warp's first row
-    for (int r0 = 0; r0 < cnt; r0 += kSuFly) {
-      __align__(16) TI x[kSuFly][8];
-#pragma unroll
-      for (int f = 0; f < kSuFly; ++f) {
-        const int64_t n = __shfl_sync(0xFFFFFFFFu, row, r0 + f);
-        if (r0 + f < cnt) load8<TI, VEC>(dout + n * a.ldd + c0, lane, left, x[f]);
+#pragma unroll 1
+    for (int r = 0; r < cnt; ++r) {
+      if ((r & (kSuGroup - 1)) == 0) {
+        ask(r + (G - 1) * kSuGroup);
+        asm volatile("cp.async.wait_group %0;" ::"n"(G - 1) : "memory");
       }
+      const int t = __shfl_sync(0xFFFFFFFFu, tok, r);
+      if (t != cur) {
+        if (inner) {
+          su_finish<TO, VEC>(a, base, dE, cur, c0, lane, left, acc);
+        } else {
 #pragma unroll
-      for (int f = 0; f < kSuFly; ++f) {
-        const int t = __shfl_sync(0xFFFFFFFFu, tok, r0 + f);
-        if (r0 + f < cnt) {
-          if (t != cur) {
-            if (inner) {
-              su_finish<TO, VEC>(a, base, dE, cur, c0, lane, left, acc);
-            } else {
-#pragma unroll
-              for (int i = 0; i < 8; ++i) hd[warp][col_of<TI, VEC>(lane, i)] = acc[i];
-            }
-            inner = true;
-            cur = t;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) acc[i] = 0.f;
-          }
-#pragma unroll
-          for (int i = 0; i < 8; ++i) acc[i] += Num<TI>::up(x[f][i]);
+          for (int i = 0; i < 8; ++i) hd[warp][col_of<TI, VEC>(lane, i)] = acc[i];
         }
+        inner = true;
+        cur = t;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] = 0.f;
       }
+      __align__(16) TI x[8];
+#pragma unroll
+      for (int i = 0; i < (int)sizeof(TI) / 2; ++i)
+        reinterpret_cast<uint4*>(x)[i] =
+            reinterpret_cast<const uint4*>(ring + (r % (G * kSuGroup)) * kEmSpan)[i];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i] += Num<TI>::up(x[i]);
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) (inner ? tl : hd)[warp][col_of<TI, VEC>(lane, i)] = acc[i];
@@ -453,7 +505,7 @@ __global__ void __launch_bounds__(256)
   bool begun = p0 == 0 || a.toks[p0 - 1] != key;  // the run begins in this CTA
   auto flush = [&]() {
     if (!begun) {
-      a.head[(int64_t)blockIdx.x * a.D + c0 + c] = cur;
+      a.head[(int64_t)blockIdx.x * a.ldp + c0 + c] = cur;
       return;
     }
     TO* o = dE + key * a.lde + c0 + c;
@@ -477,27 +529,50 @@ __global__ void __launch_bounds__(256)
   }
   const bool on = p0 + kSuRows < ns && a.toks[p0 + kSuRows] == key;  // it goes on in the next CTA
   if (on && begun)
-    a.tail[(int64_t)blockIdx.x * a.D + c0 + c] = cur;
+    a.tail[(int64_t)blockIdx.x * a.ldp + c0 + c] = cur;
   else if (on)
-    a.head[(int64_t)blockIdx.x * a.D + c0 + c] = cur;
+    a.head[(int64_t)blockIdx.x * a.ldp + c0 + c] = cur;
   else
     flush();
 }
 
 // Runs that cross CTAs: the CTA of the chunk where one begins adds the tail
 // there and the heads of the chunks that follow, four quarters side by side,
-// each in order.
-template <typename TO>
-__global__ void __launch_bounds__(1024)
-    k_embed_join(SuArgs a, const TO* base, TO* dE) {
-  __shared__ float part[4][kEmSpan];
-  const int ns = *a.total, ch = blockIdx.x, p0 = ch * kSuRows, p1 = p0 + kSuRows;
+// each in order. The first CTAs write the rows of the tokens that do not occur:
+// zero, or what is there already.
+template <typename TO, bool VEC>
+__global__ void __launch_bounds__(256) k_embed_join(SuArgs a, const TO* base, TO* dE) {
+  __shared__ __align__(16) float part[4][kEmSpan];
+  pdl_wait();
+  if ((int)blockIdx.x < a.fills) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c0 = blockIdx.y * kEmSpan, left = a.D - c0;
+    const int v0 = (int)blockIdx.x * kSuFill + warp * 4;
+    __align__(16) TO o[4][8];
+    bool mine[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) mine[r] = v0 + r < a.V && !a.seen[v0 + r];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      if (a.has_base && mine[r]) {
+        load8<TO, VEC>(base + (v0 + r) * a.ldb + c0, lane, left, o[r]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[r][i] = Num<TO>::down(0.f);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (mine[r]) store8<TO, VEC>(dE + (v0 + r) * a.lde + c0, lane, left, o[r]);
+    return;
+  }
+  const int ns = *a.total, ch = (int)blockIdx.x - a.fills, p0 = ch * kSuRows, p1 = p0 + kSuRows;
   if (p1 >= ns) return;
-  const int key = a.toks[p1];
-  if (a.toks[p1 - 1] != key) return;                                             // no run crosses here
-  if (a.toks[p0] == key && p0 > 0 && a.toks[p0 - 1] == key) return;              // it began earlier
+  const int key = a.toks[p1], last = a.toks[p1 - 1], first = a.toks[p0], before = p0 > 0 ? a.toks[p0 - 1] : -1;
+  if (last != key) return;                    // no run crosses here
+  if (first == key && before == key) return;  // it began earlier
   // last chunk whose first row is still this token's
   int lo = ch + 1, hi = (ns - 1) / kSuRows;
+  if (lo < hi && a.toks[(lo + 1) * kSuRows] != key) hi = lo;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (a.toks[mid * kSuRows] == key)
@@ -505,21 +580,29 @@ __global__ void __launch_bounds__(1024)
     else
       hi = mid - 1;
   }
-  const int c = threadIdx.x & (kEmSpan - 1), g = threadIdx.x / kEmSpan, col = blockIdx.y * kEmSpan + c;
+  const int c = (threadIdx.x & 63) * 4, g = threadIdx.x >> 6, col = blockIdx.y * kEmSpan + c;
   const int m = lo - ch, per = (m + 3) / 4, i0 = ch + 1 + min(m, g * per), i1 = ch + 1 + min(m, (g + 1) * per);
-  float s = 0.f;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
   if (col < a.D) {
+    const float* p = a.head + (int64_t)i0 * a.ldp + col;
 #pragma unroll 8
-    for (int i = i0; i < i1; ++i) s += a.head[(int64_t)i * a.D + col];
+    for (int i = i0; i < i1; ++i, p += a.ldp) {
+      const float4 x = *reinterpret_cast<const float4*>(p);
+      s.x += x.x;
+      s.y += x.y;
+      s.z += x.z;
+      s.w += x.w;
+    }
   }
-  part[g][c] = s;
+  *reinterpret_cast<float4*>(&part[g][c]) = s;
   __syncthreads();
-  if (g != 0 || col >= a.D) return;
-  float t = a.tail[(int64_t)ch * a.D + col];
+  const int cc = threadIdx.x, cl = blockIdx.y * kEmSpan + cc;
+  if (cl >= a.D) return;
+  float t = a.tail[(int64_t)ch * a.ldp + cl];
 #pragma unroll
-  for (int q = 0; q < 4; ++q) t += part[q][c];
+  for (int q = 0; q < 4; ++q) t += part[q][cc];
   t *= a.scale;
-  dE[key * a.lde + col] = Num<TO>::down(a.has_base ? Num<TO>::up(base[key * a.ldb + col]) + t : t);
+  dE[key * a.lde + cl] = Num<TO>::down(a.has_base ? Num<TO>::up(base[key * a.ldb + cl]) + t : t);
 }
 
 // ---------------------------------------------------------------- host
@@ -545,8 +628,9 @@ EmScratch em_scratch(int N, int V, int D) {
   s.cta = carve(sizeof(int) * (size_t)kSoCtas * kSoBins);
   s.total = carve(4);
   s.seen = carve((size_t)V);
-  s.head = carve(4 * (size_t)s.chunks * D);
-  s.tail = carve(4 * (size_t)s.chunks * D);
+  const size_t ldp = ((size_t)D + 3) / 4 * 4;
+  s.head = carve(4 * (size_t)s.chunks * ldp);
+  s.tail = carve(4 * (size_t)s.chunks * ldp);
   s.all = off;
   return s;
 }
@@ -584,58 +668,63 @@ cudaError_t em_sort(const int32_t* idx, int N, int V, char* base, const EmScratc
   while (width < 24 && (1 << width) < V) ++width;
   const int passes = (width + kSoBits - 1) / kSoBits, bits = (width + passes - 1) / passes;
   int2* buf[2] = {reinterpret_cast<int2*>(base + s.bufa), reinterpret_cast<int2*>(base + s.bufb)};
-  SoPass p;
-  p.in.idx = idx;
-  p.in.pairs = nullptr;
-  p.in.count = nullptr;
-  p.in.N = N;
-  p.in.V = V;
-  p.bins = 1 << bits;
-  p.mask = p.bins - 1;
-  p.shift = 0;
-  p.cta = reinterpret_cast<int*>(base + s.cta);
-  p.rows = reinterpret_cast<int32_t*>(base + s.rows);
-  p.toks = reinterpret_cast<int32_t*>(base + s.toks);
-  p.total = reinterpret_cast<int*>(base + s.total);
-  p.seen = reinterpret_cast<unsigned char*>(base + s.seen);
-  p.V = V;
-  p.status = status;
-  p.out = nullptr;
-  p.per = N;
-  const size_t smem = sizeof(int) * (size_t)kSoWarps * p.bins;
-  if (N <= 2 * kSoTile) {
-    SoSmall q{p, passes, bits, {buf[0], buf[1]}};
-    k_sort_small<<<1, kSoThreads, smem, st>>>(q);
-    return cudaGetLastError();
+  SoPass q;
+  q.idx = idx;
+  q.pairs = nullptr;
+  q.N = N;
+  q.V = V;
+  q.bins = 1 << bits;
+  q.shift = 0;
+  q.cta = reinterpret_cast<int*>(base + s.cta);
+  q.rows = reinterpret_cast<int32_t*>(base + s.rows);
+  q.toks = reinterpret_cast<int32_t*>(base + s.toks);
+  q.total = reinterpret_cast<int*>(base + s.total);
+  q.seen = reinterpret_cast<unsigned char*>(base + s.seen);
+  q.status = status;
+  q.out = nullptr;
+  q.per = kSoTile;
+  const size_t smem = sizeof(int) * (size_t)kSoWarps * q.bins;
+  if (N <= kSoTile) {
+    const SoSmall small{q, passes, bits, {buf[0], buf[1]}};
+    return launch_ex(k_sort_small, dim3(1), dim3(kSoThreads), smem, st, true, small);
   }
   int ctas = (N + kSoTile - 1) / kSoTile;
-  if (ctas > kSoCtas) ctas = kSoCtas;
-  p.per = (N + ctas - 1) / ctas;
+  if (ctas > kSoCtas) {
+    q.per = (((N + kSoCtas - 1) / kSoCtas) + kSoTile - 1) / kSoTile * kSoTile;
+    ctas = (N + q.per - 1) / q.per;
+  }
   cudaError_t e = cudaSuccess;
   for (int k = 0; k < passes && e == cudaSuccess; ++k) {
-    p.shift = k * bits;
-    p.out = k + 1 < passes ? buf[k & 1] : nullptr;
-    k_sort_count<<<ctas, kSoThreads, smem, st>>>(p);
-    k_sort_place<<<ctas, kSoThreads, smem, st>>>(p);
-    e = cudaGetLastError();
-    p.in.idx = nullptr;
-    p.in.pairs = p.out;
-    p.in.count = p.total;
+    q.shift = k * bits;
+    q.out = k + 1 < passes ? buf[k & 1] : nullptr;
+    e = launch_ex(k_sort_count, dim3(ctas), dim3(kSoThreads), sizeof(int) * (size_t)q.bins, st, true, q);
+    if (e == cudaSuccess) e = launch_ex(k_sort_place, dim3(ctas), dim3(kSoThreads), smem, st, true, q);
+    q.idx = nullptr;
+    q.pairs = q.out;
   }
   return e;
 }
 
 template <typename TI, typename TO, bool VEC>
 cudaError_t em_sum(const SuArgs& a, const void* dout, const void* base, void* dE, cudaStream_t st) {
-  const int fills = a.fill ? (a.V + kSuFill - 1) / kSuFill : 0;
+  static bool configured = false;
+  if (!configured) {
+    const cudaError_t c = cudaFuncSetAttribute(k_embed_sum<TI, TO, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)su_smem<TI>());
+    if (c != cudaSuccess) return c;
+    configured = true;
+  }
   const int spans = (a.D + kEmSpan - 1) / kEmSpan;
-  if (a.chunks + fills > 0)
-    k_embed_sum<TI, TO, VEC><<<dim3(a.chunks + fills, spans), 256, 0, st>>>(
-        a, static_cast<const TI*>(dout), static_cast<const TO*>(base), static_cast<TO*>(dE));
-  if (a.chunks > 1)
-    k_embed_join<TO><<<dim3(a.chunks - 1, spans), 1024, 0, st>>>(a, static_cast<const TO*>(base),
-                                                                  static_cast<TO*>(dE));
-  return cudaGetLastError();
+  const TO* b = static_cast<const TO*>(base);
+  TO* o = static_cast<TO*>(dE);
+  cudaError_t e = cudaSuccess;
+  if (a.chunks > 0)
+    e = launch_ex(k_embed_sum<TI, TO, VEC>, dim3(a.chunks, spans), dim3(256), su_smem<TI>(), st, true, a,
+                  static_cast<const TI*>(dout), b, o);
+  const int last = a.fills + (a.chunks > 1 ? a.chunks - 1 : 0);
+  if (e == cudaSuccess && last > 0)
+    e = launch_ex(k_embed_join<TO, VEC>, dim3(last, spans), dim3(256), 0, st, true, a, b, o);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 template <typename TI, typename TO>
 cudaError_t em_sum_v(bool vec, const SuArgs& a, const void* dout, const void* base, void* dE, cudaStream_t st) {
@@ -711,7 +800,8 @@ extern "C" dspark_status dspark_embed_grad(const void* dout, dspark_wdtype type,
   a.head = reinterpret_cast<float*>(b + s.head);
   a.tail = reinterpret_cast<float*>(b + s.tail);
   a.has_base = base != nullptr;
-  a.fill = base != dE;  // added in place: the other rows stay as they are
+  a.fills = base != dE ? (V + kSuFill - 1) / kSuFill : 0;  // added in place: the other rows stay as they are
+  a.ldp = ((int64_t)D + 3) / 4 * 4;
   const bool vec = em_vec(dout, ldd, type) && em_vec(dE, lde, grad_type) && (!base || em_vec(base, ldb, grad_type));
   typedef __nv_bfloat16 bf;
   if (type == DSPARK_BF16)
