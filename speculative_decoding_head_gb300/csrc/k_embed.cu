@@ -78,16 +78,19 @@ constexpr int kEmSpan = 256;     // columns a warp covers at a time
 constexpr int kEmRows = 4;       // rows a warp of the lookup has in flight
 
 // ---------------------------------------------------------------- lookup
-template <typename T, bool VEC>
+// CH spans of 256 columns of four rows per warp, all loads in flight together.
+template <typename T, bool VEC, int CH>
 __global__ void __launch_bounds__(256)
     k_embed(const T* __restrict__ E, int64_t lde, int V, int D, const int32_t* __restrict__ idx, int N, float scale,
             T* __restrict__ out, int64_t ldo, int* status) {
+  constexpr int kCols = CH * kEmSpan;
   const int lane = threadIdx.x & 31;
-  const int64_t spans = (D + kEmSpan - 1) / kEmSpan, groups = (N + kEmRows - 1) / kEmRows;
+  const int spans = (D + kCols - 1) / kCols, groups = (N + kEmRows - 1) / kEmRows;
   const int64_t t = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (t >= spans * groups) return;
-  const int g = (int)(t / spans), c0 = (int)(t - (int64_t)g * spans) * kEmSpan, left = D - c0;
-  __align__(16) T v[kEmRows][8];
+  pdl_wait();
+  if (t >= (int64_t)spans * groups) return;
+  const int g = (int)(t / spans), c0 = (int)(t - (int64_t)g * spans) * kCols, left = D - c0;
+  __align__(16) T v[kEmRows][CH][8];
   int id[kEmRows];
 #pragma unroll
   for (int r = 0; r < kEmRows; ++r) {
@@ -99,32 +102,47 @@ __global__ void __launch_bounds__(256)
     }
   }
 #pragma unroll
-  for (int r = 0; r < kEmRows; ++r) {
-    if (id[r] >= 0) {
-      load8<T, VEC>(E + id[r] * lde + c0, lane, left, v[r]);
-    } else {
+  for (int r = 0; r < kEmRows; ++r)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[r][i] = Num<T>::down(0.f);
+    for (int h = 0; h < CH; ++h) {
+      if (id[r] >= 0) {
+        load8<T, VEC>(E + id[r] * lde + c0 + h * kEmSpan, lane, left - h * kEmSpan, v[r][h]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[r][h][i] = Num<T>::down(0.f);
+      }
     }
-  }
 #pragma unroll
   for (int r = 0; r < kEmRows; ++r) {
     const int n = g * kEmRows + r;
     if (n >= N) break;
-    if (id[r] >= 0) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[r][i] = Num<T>::down(scale * Num<T>::up(v[r][i]));
+    for (int h = 0; h < CH; ++h) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[r][h][i] = Num<T>::down(id[r] >= 0 ? scale * Num<T>::up(v[r][h][i]) : 0.f);
+      store8<T, VEC>(out + n * ldo + c0 + h * kEmSpan, lane, left - h * kEmSpan, v[r][h]);
     }
-    store8<T, VEC>(out + n * ldo + c0, lane, left, v[r]);
   }
 }
 
+template <typename T>
+cudaError_t em_lookup(bool vec, const void* E, int64_t lde, int V, int D, const int32_t* idx, int N, float scale,
+                      void* out, int64_t ldo, int* status, cudaStream_t st) {
+  const bool wide = D > kEmSpan && sizeof(T) == 2;
+  const int cols = wide ? 2 * kEmSpan : kEmSpan;
+  const int64_t warps = (int64_t)((N + kEmRows - 1) / kEmRows) * ((D + cols - 1) / cols);
+  void (*k)(const T*, int64_t, int, int, const int32_t*, int, float, T*, int64_t, int*) =
+      wide ? (vec ? k_embed<T, true, 2> : k_embed<T, false, 2>) : (vec ? k_embed<T, true, 1> : k_embed<T, false, 1>);
+  return launch_ex(k, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, st, true, static_cast<const T*>(E), lde, V, D,
+                   idx, N, scale, static_cast<T*>(out), ldo, status);
+}
+
 // ---------------------------------------------------------------- sort
-constexpr int kSoThreads = 512;
+constexpr int kSoThreads = 1024;
 constexpr int kSoWarps = kSoThreads / 32;
 constexpr int kSoBits = 10;
 constexpr int kSoBins = 1 << kSoBits;
-constexpr int kSoKeys = 8;                              // pairs a thread holds
+constexpr int kSoKeys = 4;                              // pairs a thread holds
 constexpr int kSoTile = kSoThreads * kSoKeys;           // 4096 pairs a CTA holds at a time
 constexpr int kSoCtas = 128;
 constexpr size_t kSoSmem = sizeof(int) * (size_t)kSoWarps * kSoBins;
@@ -142,7 +160,7 @@ struct SoPass {
   int32_t* rows;        // [N] sorted rows
   int32_t* toks;        // [N] their tokens
   int* total;           // pairs in all (written by the first pass)
-  unsigned char* seen;  // [V] token occurs (cleared before the first placement, set by it)
+  unsigned char* seen;  // [V] token occurs (cleared here, set where the rows are summed)
   int* status;
 };
 
@@ -204,22 +222,18 @@ __device__ __forceinline__ void so_place(const SoPass& q, const SoKeys& k, int* 
   }
 }
 
-// Marks of the tokens that occur, and tokens out of range reported (first pass).
-__device__ __forceinline__ void so_mark(const SoPass& q, const SoKeys& k) {
+// Tokens out of range reported (first pass).
+__device__ __forceinline__ void so_check(const SoPass& q, const SoKeys& k) {
 #pragma unroll
-  for (int i = 0; i < kSoKeys; ++i) {
-    if (k.d[i] >= 0)
-      q.seen[k.p[i].x] = 1;
-    else if (k.p[i].x != -1)
-      raise_status(q.status, DSPARK_ERANGE);
-  }
+  for (int i = 0; i < kSoKeys; ++i)
+    if (k.d[i] < 0 && k.p[i].x != -1) raise_status(q.status, DSPARK_ERANGE);
 }
 
 // tot[bins] in shared memory to its exclusive prefix; returns the sum.
 __device__ __forceinline__ int so_scan(int* tot, int bins, int* wsum) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int i0 = 2 * tid, x0 = i0 < bins ? tot[i0] : 0, x1 = i0 + 1 < bins ? tot[i0 + 1] : 0;
-  int s = x0 + x1;
+  const int x0 = tid < bins ? tot[tid] : 0;
+  int s = x0;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int y = __shfl_up_sync(0xFFFFFFFFu, s, o);
@@ -237,9 +251,7 @@ __device__ __forceinline__ int so_scan(int* tot, int bins, int* wsum) {
     if (lane < kSoWarps) wsum[lane] = w;
   }
   __syncthreads();
-  const int before = s - x0 - x1 + (warp > 0 ? wsum[warp - 1] : 0);
-  if (i0 < bins) tot[i0] = before;
-  if (i0 + 1 < bins) tot[i0 + 1] = before + x0;
+  if (tid < bins) tot[tid] = s - x0 + (warp > 0 ? wsum[warp - 1] : 0);
   const int all = wsum[kSoWarps - 1];
   __syncthreads();
   return all;
@@ -248,14 +260,12 @@ __device__ __forceinline__ int so_scan(int* tot, int bins, int* wsum) {
 // Warp counts -> first places from base[d] on; base[d] moves past the tile's pairs.
 __device__ __forceinline__ void so_offsets(int* hist, int bins, int* base) {
   for (int d = threadIdx.x; d < bins; d += kSoThreads) {
-    int c[kSoWarps];
-#pragma unroll
-    for (int w = 0; w < kSoWarps; ++w) c[w] = hist[w * bins + d];
     int at = base[d];
-#pragma unroll
+#pragma unroll 8
     for (int w = 0; w < kSoWarps; ++w) {
+      const int c = hist[w * bins + d];
       hist[w * bins + d] = at;
-      at += c[w];
+      at += c;
     }
     base[d] = at;
   }
@@ -278,6 +288,7 @@ __global__ void __launch_bounds__(kSoThreads) k_sort_count(SoPass q) {
 #pragma unroll
     for (int i = 0; i < kSoKeys; ++i)
       if (k.d[i] >= 0) atomicAdd(so_hist + k.d[i], 1);
+    if (q.idx) so_check(q, k);
   }
   __syncthreads();
   pdl_trigger();
@@ -291,17 +302,22 @@ __global__ void __launch_bounds__(kSoThreads) k_sort_place(SoPass q) {
   const int n = so_n(q), a = min(n, (int)blockIdx.x * q.per), b = min(n, a + q.per);
   SoKeys k;
   so_load(q, a, b, k);  // on their way while the counts are added up
-  for (int d = threadIdx.x; d < q.bins; d += kSoThreads) {
+  // a digit's counts of all CTAs: kSoThreads / bins threads share them
+  for (int d = threadIdx.x; d < q.bins; d += kSoThreads) tot[d] = mine[d] = 0;
+  __syncthreads();
+  {
+    const int d = threadIdx.x & (q.bins - 1), share = kSoThreads / q.bins, g = threadIdx.x / q.bins;
+    const int per = ((int)gridDim.x + share - 1) / share, i0 = g * per, i1 = min((int)gridDim.x, i0 + per);
     int s = 0, before = 0;
     const int* c = q.cta + d;
 #pragma unroll 16
-    for (int i = 0; i < (int)gridDim.x; ++i) {
+    for (int i = i0; i < i1; ++i) {
       const int x = c[i * q.bins];
       before += i < (int)blockIdx.x ? x : 0;
       s += x;
     }
-    tot[d] = s;
-    mine[d] = before;
+    atomicAdd(&tot[d], s);
+    atomicAdd(&mine[d], before);
   }
   __syncthreads();
   const int all = so_scan(tot, q.bins, wsum);
@@ -312,7 +328,6 @@ __global__ void __launch_bounds__(kSoThreads) k_sort_place(SoPass q) {
     so_count(k, so_hist, q.bins);
     so_offsets(so_hist, q.bins, mine);
     so_place(q, k, so_hist);
-    if (q.idx) so_mark(q, k);
     __syncthreads();
   }
   pdl_trigger();
@@ -337,7 +352,7 @@ __global__ void __launch_bounds__(kSoThreads) k_sort_small(SoSmall s) {
     q.out = pass + 1 < s.passes ? s.buf[pass & 1] : nullptr;
     SoKeys k;
     so_load(q, 0, n, k);
-    so_count(k, so_hist, q.bins);  // its barriers order the clearing of `seen` before the marks
+    so_count(k, so_hist, q.bins);
     for (int d = threadIdx.x; d < q.bins; d += kSoThreads) {
       int c = 0;
 #pragma unroll
@@ -349,7 +364,7 @@ __global__ void __launch_bounds__(kSoThreads) k_sort_small(SoSmall s) {
     so_offsets(so_hist, q.bins, base);
     so_place(q, k, so_hist);
     if (pass == 0) {
-      so_mark(q, k);
+      so_check(q, k);
       if (threadIdx.x == 0) *q.total = all;
       n = all;
     }
@@ -361,16 +376,16 @@ __global__ void __launch_bounds__(kSoThreads) k_sort_small(SoSmall s) {
 }
 
 // ---------------------------------------------------------------- sums
-constexpr int kSuRows = 256;     // sorted rows of a CTA (32 per warp)
+constexpr int kSuWarp = 32;      // sorted rows of a warp at most (8 warps a CTA)
 constexpr int kSuGroup = 4;      // rows asked for together
 constexpr int kSuGroups = 4;     // groups a warp has on their way or at hand (fp32: half of them)
-constexpr int kSuFill = 32;      // vocabulary rows a CTA of the last launch fills where tokens do not occur
+constexpr int kSuFill = 64;      // vocabulary rows a CTA of the last launch fills where tokens do not occur
 
 struct SuArgs {
   const int32_t* rows;
   const int32_t* toks;
   const int* total;
-  const unsigned char* seen;
+  unsigned char* seen;
   int V, D, chunks;        // chunks: CTAs of sorted rows
   int fills;               // CTAs that fill
   int64_t ldp;             // of head and tail: D rounded up to 4
@@ -378,6 +393,7 @@ struct SuArgs {
   float scale;
   float* head;             // [chunks][ldp] sums of a run that begins in an earlier CTA
   float* tail;             // [chunks][ldp] sums of a run that goes on in the next CTA
+  int rpw;                 // sorted rows of a warp
   int has_base;
 };
 
@@ -435,12 +451,14 @@ __global__ void __launch_bounds__(256, 3)
   const int c0 = blockIdx.y * kEmSpan, left = a.D - c0;
   TI* ring = reinterpret_cast<TI*>(su_ring) + (size_t)warp * G * kSuGroup * kEmSpan + lane * 8;
   pdl_wait();
-  const int ns = *a.total, p0 = blockIdx.x * kSuRows;
+  const int ns = *a.total, crows = 8 * a.rpw, p0 = blockIdx.x * crows;
   if (p0 >= ns) return;
-  const int w0 = p0 + warp * 32, cnt = max(0, min(32, ns - w0));
+  const int w0 = p0 + warp * a.rpw, cnt = max(0, min(a.rpw, ns - w0));
   if (cnt > 0) {
     const int tok = lane < cnt ? a.toks[w0 + lane] : -1;
     const int row = lane < cnt ? a.rows[w0 + lane] : 0;
+    const int left_tok = __shfl_up_sync(0xFFFFFFFFu, tok, 1);
+    if (blockIdx.y == 0 && lane < cnt && (lane == 0 || tok != left_tok)) a.seen[tok] = 1;
     const int first = __shfl_sync(0xFFFFFFFFu, tok, 0), last = __shfl_sync(0xFFFFFFFFu, tok, cnt - 1);
     // ask for the group that begins with row r0 (the last ones: empty groups keep the count)
     auto ask = [&](int r0) {
@@ -499,7 +517,7 @@ __global__ void __launch_bounds__(256, 3)
   // the warps' first and last runs, joined in order, one column per thread
   const int c = threadIdx.x;
   if (c >= left) return;
-  const int nw = min(8, (ns - p0 + 31) / 32);
+  const int nw = min(8, (ns - p0 + a.rpw - 1) / a.rpw);
   float cur = 0.f;
   int key = kfirst[0];
   bool begun = p0 == 0 || a.toks[p0 - 1] != key;  // the run begins in this CTA
@@ -527,7 +545,7 @@ __global__ void __launch_bounds__(256, 3)
       begun = true;
     }
   }
-  const bool on = p0 + kSuRows < ns && a.toks[p0 + kSuRows] == key;  // it goes on in the next CTA
+  const bool on = p0 + crows < ns && a.toks[p0 + crows] == key;  // it goes on in the next CTA
   if (on && begun)
     a.tail[(int64_t)blockIdx.x * a.ldp + c0 + c] = cur;
   else if (on)
@@ -538,44 +556,47 @@ __global__ void __launch_bounds__(256, 3)
 
 // Runs that cross CTAs: the CTA of the chunk where one begins adds the tail
 // there and the heads of the chunks that follow, four quarters side by side,
-// each in order. The first CTAs write the rows of the tokens that do not occur:
+// each in order. The other CTAs write the rows of the tokens that do not occur:
 // zero, or what is there already.
 template <typename TO, bool VEC>
 __global__ void __launch_bounds__(256) k_embed_join(SuArgs a, const TO* base, TO* dE) {
   __shared__ __align__(16) float part[4][kEmSpan];
   pdl_wait();
-  if ((int)blockIdx.x < a.fills) {
+  const int crows = 8 * a.rpw, joins = (int)gridDim.x - a.fills;
+  if ((int)blockIdx.x >= joins) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c0 = blockIdx.y * kEmSpan, left = a.D - c0;
-    const int v0 = (int)blockIdx.x * kSuFill + warp * 4;
-    __align__(16) TO o[4][8];
-    bool mine[4];
+    const int v0 = ((int)blockIdx.x - joins) * kSuFill + warp * (kSuFill / 8);
+    const unsigned absent =
+        __ballot_sync(0xFFFFFFFFu, lane < kSuFill / 8 && v0 + lane < a.V && !a.seen[min(v0 + lane, a.V - 1)]);
 #pragma unroll
-    for (int r = 0; r < 4; ++r) mine[r] = v0 + r < a.V && !a.seen[v0 + r];
+    for (int q = 0; q < kSuFill / 8; q += 4) {
+      __align__(16) TO o[4][8];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      if (a.has_base && mine[r]) {
-        load8<TO, VEC>(base + (v0 + r) * a.ldb + c0, lane, left, o[r]);
-      } else {
+      for (int r = 0; r < 4; ++r) {
+        if (a.has_base && (absent >> (q + r) & 1)) {
+          load8<TO, VEC>(base + (v0 + q + r) * a.ldb + c0, lane, left, o[r]);
+        } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[r][i] = Num<TO>::down(0.f);
+          for (int i = 0; i < 8; ++i) o[r][i] = Num<TO>::down(0.f);
+        }
       }
-    }
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
-      if (mine[r]) store8<TO, VEC>(dE + (v0 + r) * a.lde + c0, lane, left, o[r]);
+      for (int r = 0; r < 4; ++r)
+        if (absent >> (q + r) & 1) store8<TO, VEC>(dE + (v0 + q + r) * a.lde + c0, lane, left, o[r]);
+    }
     return;
   }
-  const int ns = *a.total, ch = (int)blockIdx.x - a.fills, p0 = ch * kSuRows, p1 = p0 + kSuRows;
+  const int ns = *a.total, ch = (int)blockIdx.x, p0 = ch * crows, p1 = p0 + crows;
   if (p1 >= ns) return;
   const int key = a.toks[p1], last = a.toks[p1 - 1], first = a.toks[p0], before = p0 > 0 ? a.toks[p0 - 1] : -1;
   if (last != key) return;                    // no run crosses here
   if (first == key && before == key) return;  // it began earlier
   // last chunk whose first row is still this token's
-  int lo = ch + 1, hi = (ns - 1) / kSuRows;
-  if (lo < hi && a.toks[(lo + 1) * kSuRows] != key) hi = lo;
+  int lo = ch + 1, hi = (ns - 1) / crows;
+  if (lo < hi && a.toks[(lo + 1) * crows] != key) hi = lo;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (a.toks[mid * kSuRows] == key)
+    if (a.toks[mid * crows] == key)
       lo = mid;
     else
       hi = mid - 1;
@@ -605,12 +626,89 @@ __global__ void __launch_bounds__(256) k_embed_join(SuArgs a, const TO* base, TO
   dE[key * a.lde + cl] = Num<TO>::down(a.has_base ? Num<TO>::up(base[key * a.ldb + cl]) + t : t);
 }
 
+// ---------------------------------------------------------------- few rows
+// At most 256 rows: one launch and no sort. A CTA lists the rows whose tokens
+// lie in its 32 vocabulary rows, in order; a warp has four of those, sums a
+// token's rows eight loads at a time in that order, and writes the others' zeros
+// or what is there already.
+constexpr int kDiRows = 256, kDiVocab = 32;
+
+template <typename TI, typename TO, bool VEC>
+__global__ void __launch_bounds__(256)
+    k_embed_few(SuArgs a, const TI* __restrict__ dout, const int32_t* __restrict__ idx, int N, const TO* base, TO* dE,
+                int in_place, int* status) {
+  __shared__ int ln[kDiRows], lt[kDiRows], wcount[8];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c0 = blockIdx.y * kEmSpan, left = a.D - c0;
+  const int v0 = blockIdx.x * kDiVocab;
+  pdl_wait();
+  const int t = (int)threadIdx.x < N ? idx[threadIdx.x] : -1;
+  if (blockIdx.x == 0 && blockIdx.y == 0 && (t < -1 || t >= a.V)) raise_status(status, DSPARK_ERANGE);
+  const bool in = t >= v0 && t < min(v0 + kDiVocab, a.V);
+  const unsigned has = __ballot_sync(0xFFFFFFFFu, in);
+  if (lane == 0) wcount[warp] = __popc(has);
+  __syncthreads();
+  int at = __popc(has & ((1u << lane) - 1u)), m = 0;
+  for (int w = 0; w < 8; ++w) {
+    if (w < warp) at += wcount[w];
+    m += wcount[w];
+  }
+  if (in) {
+    ln[at] = threadIdx.x;
+    lt[at] = t;
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int r = 0; r < kDiVocab / 8; ++r) {
+    const int v = v0 + warp * (kDiVocab / 8) + r;
+    if (v >= a.V) break;
+    float acc[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+    bool any = false;
+    for (int i0 = 0; i0 < m; i0 += 32) {
+      unsigned rows = __ballot_sync(0xFFFFFFFFu, i0 + lane < m && lt[min(i0 + lane, kDiRows - 1)] == v);
+      any |= rows != 0;
+      while (rows) {
+        __align__(16) TI x[8][8];
+        int k = 0;
+#pragma unroll
+        for (int f = 0; f < 8; ++f) {
+          if (rows) {
+            const int n = ln[i0 + __ffs(rows) - 1];
+            rows &= rows - 1;
+            load8<TI, VEC>(dout + n * a.ldd + c0, lane, left, x[f]);
+            k = f + 1;
+          }
+        }
+#pragma unroll
+        for (int f = 0; f < 8; ++f)
+          if (f < k) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[i] += Num<TI>::up(x[f][i]);
+          }
+      }
+    }
+    if (any) {
+      su_finish<TO, VEC>(a, base, dE, v, c0, lane, left, acc);
+    } else if (!in_place) {
+      __align__(16) TO o[8];
+      if (a.has_base) {
+        load8<TO, VEC>(base + v * a.ldb + c0, lane, left, o);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = Num<TO>::down(0.f);
+      }
+      store8<TO, VEC>(dE + v * a.lde + c0, lane, left, o);
+    }
+  }
+}
+
 // ---------------------------------------------------------------- host
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 struct EmScratch {
   size_t rows, toks, bufa, bufb, cta, total, seen, head, tail, all;
-  int chunks;
+  int chunks, rpw;
 };
 EmScratch em_scratch(int N, int V, int D) {
   EmScratch s;
@@ -620,7 +718,10 @@ EmScratch em_scratch(int N, int V, int D) {
     off += up256(bytes > 0 ? bytes : 1);
     return o;
   };
-  s.chunks = (N + kSuRows - 1) / kSuRows;
+  // short runs of sorted rows where few CTAs would have long ones (8 rows a
+  // warp: 8190 x 1001 took 45 us with 32)
+  s.rpw = (int64_t)N * ((D + kEmSpan - 1) / kEmSpan) >= 152 * 2 * 8 * kSuWarp ? kSuWarp : kSuWarp / 4;
+  s.chunks = (N + 8 * s.rpw - 1) / (8 * s.rpw);
   s.rows = carve(4 * (size_t)N);
   s.toks = carve(4 * (size_t)N);
   s.bufa = carve(8 * (size_t)N);
@@ -706,7 +807,12 @@ cudaError_t em_sort(const int32_t* idx, int N, int V, char* base, const EmScratc
 }
 
 template <typename TI, typename TO, bool VEC>
-cudaError_t em_sum(const SuArgs& a, const void* dout, const void* base, void* dE, cudaStream_t st) {
+cudaError_t em_sum(const SuArgs& a, const void* dout, const int32_t* idx, int N, const void* base, void* dE,
+                   int* status, cudaStream_t st) {
+  if (N <= kDiRows)
+    return launch_ex(k_embed_few<TI, TO, VEC>, dim3((a.V + kDiVocab - 1) / kDiVocab, (a.D + kEmSpan - 1) / kEmSpan),
+                     dim3(256), 0, st, true, a, static_cast<const TI*>(dout), idx, N, static_cast<const TO*>(base),
+                     static_cast<TO*>(dE), base == dE ? 1 : 0, status);
   static bool configured = false;
   if (!configured) {
     const cudaError_t c = cudaFuncSetAttribute(k_embed_sum<TI, TO, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -727,8 +833,10 @@ cudaError_t em_sum(const SuArgs& a, const void* dout, const void* base, void* dE
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 template <typename TI, typename TO>
-cudaError_t em_sum_v(bool vec, const SuArgs& a, const void* dout, const void* base, void* dE, cudaStream_t st) {
-  return vec ? em_sum<TI, TO, true>(a, dout, base, dE, st) : em_sum<TI, TO, false>(a, dout, base, dE, st);
+cudaError_t em_sum_v(bool vec, const SuArgs& a, const void* dout, const int32_t* idx, int N, const void* base,
+                     void* dE, int* status, cudaStream_t st) {
+  return vec ? em_sum<TI, TO, true>(a, dout, idx, N, base, dE, status, st)
+             : em_sum<TI, TO, false>(a, dout, idx, N, base, dE, status, st);
 }
 
 }  // namespace
@@ -745,24 +853,9 @@ extern "C" dspark_status dspark_embed(const void* E, dspark_wdtype type, int64_t
   if (!em_ptr_ok(E, type) || !em_ptr_ok(out, type) || !em_ptr_ok(idx, DSPARK_F32)) return DSPARK_EINVAL;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const bool vec = em_vec(E, lde, type) && em_vec(out, ldo, type);
-  const int64_t warps = (int64_t)((N + kEmRows - 1) / kEmRows) * ((D + kEmSpan - 1) / kEmSpan);
-  const unsigned grid = (unsigned)((warps + 7) / 8);
-  if (type == DSPARK_BF16) {
-    const auto* e = static_cast<const __nv_bfloat16*>(E);
-    auto* o = static_cast<__nv_bfloat16*>(out);
-    if (vec)
-      k_embed<__nv_bfloat16, true><<<grid, 256, 0, st>>>(e, lde, V, D, idx, N, scale, o, ldo, device_status);
-    else
-      k_embed<__nv_bfloat16, false><<<grid, 256, 0, st>>>(e, lde, V, D, idx, N, scale, o, ldo, device_status);
-  } else {
-    const auto* e = static_cast<const float*>(E);
-    auto* o = static_cast<float*>(out);
-    if (vec)
-      k_embed<float, true><<<grid, 256, 0, st>>>(e, lde, V, D, idx, N, scale, o, ldo, device_status);
-    else
-      k_embed<float, false><<<grid, 256, 0, st>>>(e, lde, V, D, idx, N, scale, o, ldo, device_status);
-  }
-  return em_fail(cudaGetLastError());
+  return em_fail(type == DSPARK_BF16
+                     ? em_lookup<__nv_bfloat16>(vec, E, lde, V, D, idx, N, scale, out, ldo, device_status, st)
+                     : em_lookup<float>(vec, E, lde, V, D, idx, N, scale, out, ldo, device_status, st));
 }
 
 extern "C" size_t dspark_embed_grad_scratch_bytes(int N, int V, int D) {
@@ -783,13 +876,16 @@ extern "C" dspark_status dspark_embed_grad(const void* dout, dspark_wdtype type,
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const EmScratch s = em_scratch(N, V, D);
   char* b = static_cast<char*>(scratch);
-  const cudaError_t e = em_sort(idx, N, V, b, s, device_status, st);
-  if (e != cudaSuccess) return em_fail(e);
+  if (N > kDiRows) {
+    const cudaError_t e = em_sort(idx, N, V, b, s, device_status, st);
+    if (e != cudaSuccess) return em_fail(e);
+  }
   SuArgs a;
   a.rows = reinterpret_cast<const int32_t*>(b + s.rows);
   a.toks = reinterpret_cast<const int32_t*>(b + s.toks);
   a.total = reinterpret_cast<const int*>(b + s.total);
-  a.seen = reinterpret_cast<const unsigned char*>(b + s.seen);
+  a.seen = reinterpret_cast<unsigned char*>(b + s.seen);
+  a.rpw = s.rpw;
   a.V = V;
   a.D = D;
   a.chunks = s.chunks;
@@ -805,8 +901,8 @@ extern "C" dspark_status dspark_embed_grad(const void* dout, dspark_wdtype type,
   const bool vec = em_vec(dout, ldd, type) && em_vec(dE, lde, grad_type) && (!base || em_vec(base, ldb, grad_type));
   typedef __nv_bfloat16 bf;
   if (type == DSPARK_BF16)
-    return em_fail(grad_type == DSPARK_BF16 ? em_sum_v<bf, bf>(vec, a, dout, base, dE, st)
-                                            : em_sum_v<bf, float>(vec, a, dout, base, dE, st));
-  return em_fail(grad_type == DSPARK_BF16 ? em_sum_v<float, bf>(vec, a, dout, base, dE, st)
-                                          : em_sum_v<float, float>(vec, a, dout, base, dE, st));
+    return em_fail(grad_type == DSPARK_BF16 ? em_sum_v<bf, bf>(vec, a, dout, idx, N, base, dE, device_status, st)
+                                            : em_sum_v<bf, float>(vec, a, dout, idx, N, base, dE, device_status, st));
+  return em_fail(grad_type == DSPARK_BF16 ? em_sum_v<float, bf>(vec, a, dout, idx, N, base, dE, device_status, st)
+                                          : em_sum_v<float, float>(vec, a, dout, idx, N, base, dE, device_status, st));
 }
