@@ -291,7 +291,6 @@ __global__ void __launch_bounds__(kSoThreads) k_sort_count(SoPass q) {
     if (q.idx) so_check(q, k);
   }
   __syncthreads();
-  pdl_trigger();
   for (int d = threadIdx.x; d < q.bins; d += kSoThreads) q.cta[blockIdx.x * q.bins + d] = so_hist[d];
 }
 
@@ -330,7 +329,6 @@ __global__ void __launch_bounds__(kSoThreads) k_sort_place(SoPass q) {
     so_place(q, k, so_hist);
     __syncthreads();
   }
-  pdl_trigger();
 }
 
 // All passes in one CTA, for few rows.
@@ -372,13 +370,12 @@ __global__ void __launch_bounds__(kSoThreads) k_sort_small(SoSmall s) {
     q.idx = nullptr;
     q.pairs = q.out;
   }
-  pdl_trigger();
 }
 
 // ---------------------------------------------------------------- sums
 constexpr int kSuWarp = 32;      // sorted rows of a warp at most (8 warps a CTA)
 constexpr int kSuGroup = 4;      // rows asked for together
-constexpr int kSuGroups = 4;     // groups a warp has on their way or at hand (fp32: half of them)
+constexpr int kSuGroups = 2;     // groups a warp has on their way or at hand
 constexpr int kSuFill = 64;      // vocabulary rows a CTA of the last launch fills where tokens do not occur
 
 struct SuArgs {
@@ -397,11 +394,10 @@ struct SuArgs {
   int has_base;
 };
 
+// o: the base's values of the row (with has_base), taken over by the result
 template <typename TO, bool VEC>
-__device__ __forceinline__ void su_finish(const SuArgs& a, const TO* base, TO* dE, int v, int c0, int lane, int left,
+__device__ __forceinline__ void su_finish(const SuArgs& a, TO* o, TO* dE, int v, int c0, int lane, int left,
                                           const float* acc) {
-  __align__(16) TO o[8];
-  if (a.has_base) load8<TO, VEC>(base + v * a.ldb + c0, lane, left, o);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const float s = a.scale * acc[i];
@@ -411,12 +407,8 @@ __device__ __forceinline__ void su_finish(const SuArgs& a, const TO* base, TO* d
 }
 
 template <typename TI>
-__host__ __device__ constexpr int su_groups() {
-  return sizeof(TI) == 2 ? kSuGroups : kSuGroups / 2;
-}
-template <typename TI>
-__host__ __device__ constexpr size_t su_smem() {
-  return (size_t)8 * su_groups<TI>() * kSuGroup * kEmSpan * sizeof(TI);
+constexpr size_t su_smem() {
+  return (size_t)8 * kSuGroups * kSuGroup * kEmSpan * sizeof(TI);
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
@@ -441,12 +433,12 @@ __device__ __forceinline__ void su_stage(const TI* row, int lane, int left, TI* 
 }
 
 template <typename TI, typename TO, bool VEC>
-__global__ void __launch_bounds__(256, 3)
+__global__ void __launch_bounds__(256, sizeof(TI) == 2 ? 4 : 2)
     k_embed_sum(SuArgs a, const TI* __restrict__ dout, const TO* base, TO* dE) {
   extern __shared__ __align__(16) unsigned char su_ring[];
   __shared__ __align__(16) float hd[8][kEmSpan], tl[8][kEmSpan];
   __shared__ int kfirst[8], klast[8], whole[8];
-  constexpr int G = su_groups<TI>();
+  constexpr int G = kSuGroups;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c0 = blockIdx.y * kEmSpan, left = a.D - c0;
   TI* ring = reinterpret_cast<TI*>(su_ring) + (size_t)warp * G * kSuGroup * kEmSpan + lane * 8;
@@ -478,6 +470,7 @@ __global__ void __launch_bounds__(256, 3)
     for (int i = 0; i < 8; ++i) acc[i] = 0.f;
     int cur = first;
     bool inner = false;  // the run began after this warp's first row
+    __align__(16) TO o[8];
 #pragma unroll 1
     for (int r = 0; r < cnt; ++r) {
       if ((r & (kSuGroup - 1)) == 0) {
@@ -487,13 +480,14 @@ __global__ void __launch_bounds__(256, 3)
       const int t = __shfl_sync(0xFFFFFFFFu, tok, r);
       if (t != cur) {
         if (inner) {
-          su_finish<TO, VEC>(a, base, dE, cur, c0, lane, left, acc);
+          su_finish<TO, VEC>(a, o, dE, cur, c0, lane, left, acc);
         } else {
 #pragma unroll
           for (int i = 0; i < 8; ++i) hd[warp][col_of<TI, VEC>(lane, i)] = acc[i];
         }
         inner = true;
         cur = t;
+        if (a.has_base) load8<TO, VEC>(base + cur * a.ldb + c0, lane, left, o);  // needed when the run ends
 #pragma unroll
         for (int i = 0; i < 8; ++i) acc[i] = 0.f;
       }
@@ -518,8 +512,19 @@ __global__ void __launch_bounds__(256, 3)
   const int c = threadIdx.x;
   if (c >= left) return;
   const int nw = min(8, (ns - p0 + a.rpw - 1) / a.rpw);
+  // what the rows of the warps' first and last tokens are added to, asked for at once
+  TO bfirst[8], blast[8];
+#pragma unroll
+  for (int w = 0; w < 8; ++w) {
+    bfirst[w] = blast[w] = Num<TO>::down(0.f);
+    if (a.has_base && w < nw) {
+      bfirst[w] = base[kfirst[w] * a.ldb + c0 + c];
+      blast[w] = base[klast[w] * a.ldb + c0 + c];
+    }
+  }
   float cur = 0.f;
   int key = kfirst[0];
+  TO kb = bfirst[0];
   bool begun = p0 == 0 || a.toks[p0 - 1] != key;  // the run begins in this CTA
   auto flush = [&]() {
     if (!begun) {
@@ -528,13 +533,16 @@ __global__ void __launch_bounds__(256, 3)
     }
     TO* o = dE + key * a.lde + c0 + c;
     const float s = a.scale * cur;
-    *o = Num<TO>::down(a.has_base ? Num<TO>::up(base[key * a.ldb + c0 + c]) + s : s);
+    *o = Num<TO>::down(a.has_base ? Num<TO>::up(kb) + s : s);
   };
-  for (int w = 0; w < nw; ++w) {
+#pragma unroll
+  for (int w = 0; w < 8; ++w) {
+    if (w >= nw) break;
     if (w > 0 && kfirst[w] != key) {
       flush();
       cur = 0.f;
       key = kfirst[w];
+      kb = bfirst[w];
       begun = true;
     }
     cur += hd[w][c];
@@ -542,6 +550,7 @@ __global__ void __launch_bounds__(256, 3)
       flush();
       cur = tl[w][c];
       key = klast[w];
+      kb = blast[w];
       begun = true;
     }
   }
@@ -559,7 +568,7 @@ __global__ void __launch_bounds__(256, 3)
 // each in order. The other CTAs write the rows of the tokens that do not occur:
 // zero, or what is there already.
 template <typename TO, bool VEC>
-__global__ void __launch_bounds__(256) k_embed_join(SuArgs a, const TO* base, TO* dE) {
+__global__ void __launch_bounds__(256, 8) k_embed_join(SuArgs a, const TO* base, TO* dE) {
   __shared__ __align__(16) float part[4][kEmSpan];
   pdl_wait();
   const int crows = 8 * a.rpw, joins = (int)gridDim.x - a.fills;
@@ -569,10 +578,10 @@ __global__ void __launch_bounds__(256) k_embed_join(SuArgs a, const TO* base, TO
     const unsigned absent =
         __ballot_sync(0xFFFFFFFFu, lane < kSuFill / 8 && v0 + lane < a.V && !a.seen[min(v0 + lane, a.V - 1)]);
 #pragma unroll
-    for (int q = 0; q < kSuFill / 8; q += 4) {
-      __align__(16) TO o[4][8];
+    for (int q = 0; q < kSuFill / 8; q += 2) {
+      __align__(16) TO o[2][8];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
+      for (int r = 0; r < 2; ++r) {
         if (a.has_base && (absent >> (q + r) & 1)) {
           load8<TO, VEC>(base + (v0 + q + r) * a.ldb + c0, lane, left, o[r]);
         } else {
@@ -581,7 +590,7 @@ __global__ void __launch_bounds__(256) k_embed_join(SuArgs a, const TO* base, TO
         }
       }
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
+      for (int r = 0; r < 2; ++r)
         if (absent >> (q + r) & 1) store8<TO, VEC>(dE + (v0 + q + r) * a.lde + c0, lane, left, o[r]);
     }
     return;
@@ -606,7 +615,7 @@ __global__ void __launch_bounds__(256) k_embed_join(SuArgs a, const TO* base, TO
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
   if (col < a.D) {
     const float* p = a.head + (int64_t)i0 * a.ldp + col;
-#pragma unroll 8
+#pragma unroll 4
     for (int i = i0; i < i1; ++i, p += a.ldp) {
       const float4 x = *reinterpret_cast<const float4*>(p);
       s.x += x.x;
@@ -688,18 +697,18 @@ __global__ void __launch_bounds__(256)
           }
       }
     }
-    if (any) {
-      su_finish<TO, VEC>(a, base, dE, v, c0, lane, left, acc);
-    } else if (!in_place) {
-      __align__(16) TO o[8];
-      if (a.has_base) {
-        load8<TO, VEC>(base + v * a.ldb + c0, lane, left, o);
-      } else {
+    if (!any && in_place) continue;
+    __align__(16) TO o[8];
+    if (a.has_base) {
+      load8<TO, VEC>(base + v * a.ldb + c0, lane, left, o);
+    } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = Num<TO>::down(0.f);
-      }
-      store8<TO, VEC>(dE + v * a.lde + c0, lane, left, o);
+      for (int i = 0; i < 8; ++i) o[i] = Num<TO>::down(0.f);
     }
+    if (any)
+      su_finish<TO, VEC>(a, o, dE, v, c0, lane, left, acc);
+    else
+      store8<TO, VEC>(dE + v * a.lde + c0, lane, left, o);
   }
 }
 
@@ -718,9 +727,13 @@ EmScratch em_scratch(int N, int V, int D) {
     off += up256(bytes > 0 ? bytes : 1);
     return o;
   };
-  // short runs of sorted rows where few CTAs would have long ones (8 rows a
-  // warp: 8190 x 1001 took 45 us with 32)
-  s.rpw = (int64_t)N * ((D + kEmSpan - 1) / kEmSpan) >= 152 * 2 * 8 * kSuWarp ? kSuWarp : kSuWarp / 4;
+  // Rows of a warp: whole waves of four CTAs per SM (152 SMs), each warp at most
+  // 32 rows; where there is less than a wave, at least 8 (8190 x 1001 took 45 us
+  // with 32, when one CTA's rows follow one another).
+  const int64_t spans = (D + kEmSpan - 1) / kEmSpan, slots = 152 * 4, work = (int64_t)N * spans;
+  const int64_t waves = (work + 8 * kSuWarp * slots - 1) / (8 * kSuWarp * slots);
+  const int64_t rpw = (work + 8 * slots * (waves > 0 ? waves : 1) - 1) / (8 * slots * (waves > 0 ? waves : 1));
+  s.rpw = (int)(rpw < 8 ? 8 : rpw > kSuWarp ? kSuWarp : rpw);
   s.chunks = (N + 8 * s.rpw - 1) / (8 * s.rpw);
   s.rows = carve(4 * (size_t)N);
   s.toks = carve(4 * (size_t)N);
