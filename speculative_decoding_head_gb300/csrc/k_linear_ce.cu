@@ -100,7 +100,7 @@ struct LcJob {
   // gradients
   const float* acc;     // [M][lda] sums so far
   int64_t lda;
-  int acc_in;           // add what acc holds
+  int acc_in;           // acc and slots hold the sums of the pieces before: added to
   int to_out;           // the result is complete: to out (through `to`), scaled; else to acc
   int t_out;            // the result is written transposed: out is [Nn][ldo]
   __nv_bfloat16* out;   // [M][ldo]
@@ -263,6 +263,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
   tc::tc_fence_after();
   const uint32_t tmem = *tmem_holder;
   pdl_wait();  // everything below reads or writes what earlier kernels of the stream write or read
+  // a small grid leaves SMs on which the next kernel can set up meanwhile
+  const bool early = gridDim.x <= kLcPairs;
+  if (early) pdl_trigger();
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -507,11 +510,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
         if (lane == 0) tc::bulk_wait_read();
         __syncwarp();
       };
-      auto put = [&](const CUtensorMap* tm, int c, int r) LC_INLINE {
+      auto put = [&](const CUtensorMap* tm, int c, int r, bool add = false) LC_INLINE {
         tc::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          tc::tma_store_2d(tm, c, r, sbase + ooff);
+          if (add)
+            tc::tma_add_2d(tm, c, r, sbase + ooff);
+          else
+            tc::tma_store_2d(tm, c, r, sbase + ooff);
           tc::bulk_commit();
         }
       };
@@ -653,14 +659,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
         } else {
           const CUtensorMap* tm = whole ? (dx ? &jx.tacc : &jw.tacc) : (dx ? &jx.tslots : &jw.tslots);
           const int sc = whole ? col : c0, sr = whole ? row - lane : w.slot * kLcTile + row0;
+          const bool add = dx ? jx.acc_in : jw.acc_in;  // onto the sums of the pieces before
           each_part([&](int h) LC_INLINE {
-            if (acc_in) add_acc(h);
             box_free();
 #pragma unroll
             for (int k = 0; k < 8; ++k)
               *reinterpret_cast<float4*>(obox + ((k ^ (lane & 7)) << 4)) =
                   make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-          }, [&](int h) LC_INLINE { put(tm, sc + kLcPart * h, sr); });
+          }, [&](int h) LC_INLINE { put(tm, sc + kLcPart * h, sr, add); });
         }
       }
       if (has_u && is_z) ubox += parts;
@@ -677,7 +683,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
     }
     if (GRAD && lane == 0) tc::bulk_wait_all();
   }
-  pdl_trigger();
+  if (!early) pdl_trigger();
   __syncwarp();
   tc::tc_fence_before();
   __syncthreads();
@@ -736,15 +742,12 @@ __global__ void __launch_bounds__(32 * kLcRowsCta)
   }
 }
 
-// Tiles that several pairs share: their parts added in the contraction's
-// order, then what the epilogue does with a whole tile.
+// Tiles that several pairs share: their parts (each already summed over the
+// pieces of the vocabulary) added in the contraction's order.
 struct LcJoin {
   const float* slots;
   int M, Nn, nkb, mt, nt, split;
-  float* acc;
-  int64_t lda;
-  int acc_in;
-  __nv_bfloat16* out;   // null: acc
+  __nv_bfloat16* out;
   int64_t ldo;
   int t_out;
   float scale;
@@ -796,17 +799,7 @@ __global__ void __launch_bounds__(256) k_lce_join(const __grid_constant__ LcJoin
       a.z += x.z;
       a.w += x.w;
     }
-    float4* ap = reinterpret_cast<float4*>(j.acc + (int64_t)row * j.lda + col);
-    if (j.acc_in) {
-      const float4 x = *ap;
-      a.x += x.x;
-      a.y += x.y;
-      a.z += x.z;
-      a.w += x.w;
-    }
-    if (!j.out) *ap = a;
   }
-  if (!j.out) return;
   float f[4] = {a.x * j.scale, a.y * j.scale, a.z * j.scale, a.w * j.scale};
   int orow = row, ocol = col, oN = j.Nn;
   if (j.t_out) {
@@ -905,20 +898,21 @@ int tiles_of(int64_t x) { return (int)((x + kLcTile - 1) / kLcTile); }
 
 // Pairs that share a product's tiles block by block: where whole tiles would
 // leave part of the grid idle (fewer than two per pair), as long as every pair
-// gets eight blocks. A function of the sizes alone, so the order of the sums
+// gets eight blocks and the longest pair saves more blocks (a third of a
+// microsecond each) than the join's launch costs. A function of the sizes alone, so the order of the sums
 // does not depend on the device.
 int split_of(int tiles, int nkb) {
   if (tiles >= 2 * kLcPairs) return 0;
   const int64_t most = (int64_t)tiles * nkb / 8;
   const int s = (int)(most < kLcPairs ? most : kLcPairs);
-  return s > tiles ? s : 0;
+  return s > tiles && nkb - (int)(((int64_t)tiles * nkb + s - 1) / s) > 12 ? s : 0;
 }
 
 // The gradient's pieces of the vocabulary and its scratch.
 struct LcPlan {
   int piece, pieces;
   int64_t ldg;
-  int dx_split, dw_split;
+  int dx_split, dw_split, dx_nkb;
   int64_t dx_lda;
   bool swap;    // the operand whose contraction index is its row goes to A (see make_plan)
   int64_t ldt;  // of X's transpose
@@ -926,7 +920,10 @@ struct LcPlan {
   size_t G[2], dx_acc, dx_slots, dw_slots, XT, bwd_total;  // gradient
 };
 
-constexpr int64_t kLcPieceBytes = 256ll << 20;
+// G's piece: small enough to stay in L2 where the products are short (K below
+// 1024: its 6 bytes of traffic a value take as long as 6 K operations at K = 265),
+// else few launches
+constexpr int64_t kLcPieceBytes = 256ll << 20, kLcPieceBytesL2 = 64ll << 20;
 
 LcPlan make_plan(const dspark_lce_dims& d) {
   LcPlan p;
@@ -941,7 +938,7 @@ LcPlan make_plan(const dspark_lce_dims& d) {
   p.part = carve(8 * N * 2 * tiles_of(V));
   p.zt = carve(4 * N);
   p.fwd_total = off;
-  int64_t most = kLcPieceBytes / (2 * (N > 0 ? N : 1)) / kLcTile * kLcTile;
+  int64_t most = (K < 1024 ? kLcPieceBytesL2 : kLcPieceBytes) / (2 * (N > 0 ? N : 1)) / kLcTile * kLcTile;
   most = most < 2048 ? 2048 : most;
   p.pieces = (int)((V + most - 1) / most);
   p.piece = (int)up((V + p.pieces - 1) / p.pieces, kLcTile);
@@ -949,6 +946,7 @@ LcPlan make_plan(const dspark_lce_dims& d) {
   const int64_t widest = p.piece < V ? p.piece : V;
   p.ldg = up(widest, 64);
   const int64_t nkb_v = (widest + kLcKb - 1) / kLcKb, nkb_n = (N + kLcKb - 1) / kLcKb;
+  p.dx_nkb = (int)nkb_v;
   p.dx_split = split_of(tiles_of(N) * tiles_of(K), (int)nkb_v);
   p.dw_split = split_of(tiles_of(widest) * tiles_of(K), (int)nkb_n);
   // An MN-major B (its contraction index is its row) costs the tensor cores
@@ -1061,10 +1059,7 @@ bool out_job(LcJob& j, LcJoin& q, float* slots, float* acc, int64_t lda, bool ac
   q.mt = tiles_of(j.M);
   q.nt = tiles_of(j.Nn);
   q.split = j.split;
-  q.acc = acc;
-  q.lda = lda;
-  q.acc_in = acc_in;
-  q.out = to_out ? out : nullptr;
+  q.out = out;
   q.ldo = ldo;
   q.t_out = t_out;
   q.scale = scale;
@@ -1165,8 +1160,8 @@ extern "C" dspark_status dspark_linear_ce_grad(const dspark_lce_dims* d, const v
         const bool t = p.swap && vk;  // dX^T = W^T G^T
         x.M = t ? d->K : d->N;
         x.Nn = t ? d->N : d->K;
-        x.nkb = (cols + kLcKb - 1) / kLcKb;
-        x.split = p.dx_split ? split_of(tiles_of(x.M) * tiles_of(x.Nn), x.nkb) : 0;
+        x.nkb = p.dx_nkb;  // every piece's (a narrower last piece reads zeros), so that slots keep their tiles
+        x.split = p.dx_split;
         if (!out_job(x, joins.j[njoin], reinterpret_cast<float*>(base + p.dx_slots),
                      reinterpret_cast<float*>(base + p.dx_acc), p.dx_lda, i > 1, i == p.pieces,
                      static_cast<__nv_bfloat16*>(dX), d->lddx, t, scale))
@@ -1183,7 +1178,7 @@ extern "C" dspark_status dspark_linear_ce_grad(const dspark_lce_dims* d, const v
                (vk ? encode(&x.tb, W, d->K, d->V, d->ldw, kLcKb) : encode(&x.tb, W, d->V, d->K, d->ldw, kLcHalf));
         }
         if (!ok) return DSPARK_EINVAL;
-        if (x.split) {
+        if (x.split && i == p.pieces) {
           ++njoin;
           join_tiles = tiles_of(x.M) * tiles_of(x.Nn);
         }

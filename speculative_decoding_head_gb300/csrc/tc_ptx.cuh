@@ -192,6 +192,13 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* m, int c0, int c
                "r"(c0), "r"(c1), "r"(src)
                : "memory");
 }
+// The same with fp32 values added to what is there.
+__device__ __forceinline__ void tma_add_2d(const CUtensorMap* m, int c0, int c1, uint32_t src) {
+  asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                   reinterpret_cast<uint64_t>(m)),
+               "r"(c0), "r"(c1), "r"(src)
+               : "memory");
+}
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 // All of this thread's committed bulk stores have read their shared memory / are complete.
 __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
