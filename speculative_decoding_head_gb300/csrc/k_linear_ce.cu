@@ -57,20 +57,19 @@ constexpr int kLcWarpCols = 128;
 constexpr int kLcPart = 32;
 constexpr int kLcThreads = 32 * (2 + kLcEpiWarps);
 constexpr int kLcTmemCols = 512;                  // two accumulators of 256 columns
-// Shared memory: the operand ring and, from its end, 32 x 32 boxes of the
-// epilogue warps. Statistics: six stages, or three and two boxes of U a warp.
-// Gradient: five stages and an output box a warp, or three, a box of U and an
-// output box a warp.
+// Shared memory: the operand ring and, from its end, boxes of the epilogue
+// warps: 32 rows of 32 fp32 columns of U (4 KB) with U, 32 rows of 64 bytes of
+// output (2 KB) in the gradient.
 constexpr int kLcMaxStages = 6;
-constexpr int kLcBoxBytes = 32 * kLcPart * 4;     // 4 KB (fp32)
-constexpr int kLcBoxesU = 2;                      // boxes of U a warp of the statistics has
+constexpr int kLcUBox = 32 * kLcPart * 4;
+constexpr int kLcOBox = 32 * 64;
 constexpr int kLcRing = 224 * 1024;
-__host__ __device__ constexpr int lc_stages(bool grad, bool u) { return u ? 3 : grad ? 5 : 6; }
-static_assert(lc_stages(true, false) * kLcStageBytes + kLcEpiWarps * kLcBoxBytes <= kLcRing, "gradient");
-static_assert(lc_stages(true, true) * kLcStageBytes + 2 * kLcEpiWarps * kLcBoxBytes <= kLcRing, "gradient with U");
-static_assert(lc_stages(false, true) * kLcStageBytes + kLcBoxesU * kLcEpiWarps * kLcBoxBytes <= kLcRing, "U");
+__host__ __device__ constexpr int lc_stages(bool grad, bool u) { return !u ? 6 : grad ? 4 : 5; }
+static_assert(lc_stages(true, false) * kLcStageBytes + kLcEpiWarps * kLcOBox <= kLcRing, "gradient");
+static_assert(lc_stages(true, true) * kLcStageBytes + kLcEpiWarps * (kLcOBox + kLcUBox) <= kLcRing, "gradient, U");
+static_assert(lc_stages(false, true) * kLcStageBytes + kLcEpiWarps * kLcUBox <= kLcRing, "U");
 constexpr int kLcAhead = 16;                      // tiles announced: the producer is at most 6 + 2 + 2 ahead
-constexpr int kLcBars = 2 * kLcMaxStages + 5 + 2 * kLcEpiWarps + kLcAhead + 1;
+constexpr int kLcBars = 2 * kLcMaxStages + 5 + kLcEpiWarps + kLcAhead + 1;
 constexpr int kLcBarBytes = 16 * kLcAhead + 8 * kLcBars + 16;
 static_assert(kLcBars % 2 == 0, "16-byte ring entries");
 constexpr size_t kLcSmem = (size_t)kLcRing + 1024 + kLcBarBytes;
@@ -222,8 +221,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
   auto tfull = [&](int b) { return bars + 8u * (2 * kLcMaxStages + b); };
   auto tempty = [&](int b) { return bars + 8u * (2 * kLcMaxStages + 2 + b); };
   const uint32_t drain = bars + 8u * (2 * kLcMaxStages + 4);
-  auto ufull = [&](int w, int b) { return bars + 8u * (2 * kLcMaxStages + 5 + 2 * w + b); };
-  auto told = [&](int i) { return bars + 8u * (2 * kLcMaxStages + 5 + 2 * kLcEpiWarps + (i & (kLcAhead - 1))); };
+  auto ufull = [&](int w) { return bars + 8u * (2 * kLcMaxStages + 5 + w); };
+  auto told = [&](int i) { return bars + 8u * (2 * kLcMaxStages + 5 + kLcEpiWarps + (i & (kLcAhead - 1))); };
   int4* tile_ring = reinterpret_cast<int4*>(smem + kLcRing + 8 * kLcBars);
   unsigned char* tail = reinterpret_cast<unsigned char*>(tile_ring + kLcAhead);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(tail);
@@ -243,7 +242,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
       tc::mbar_init(tempty(b), 2 * kLcGroupWarps);  // both CTAs' warps of a group, on the even CTA
     }
     tc::mbar_init(drain, 1);
-    for (int w = 0; w < 2 * kLcEpiWarps; ++w) tc::mbar_init(ufull(w >> 1, w & 1), 1);
+    for (int w = 0; w < kLcEpiWarps; ++w) tc::mbar_init(ufull(w), 1);
     for (int i = 0; i < kLcAhead; ++i) tc::mbar_init(told(i), 1);
     *abort = 0;
     tc::fence_barrier_init();
@@ -376,12 +375,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
     // 128 columns (half hf) of the accumulator in parts of 32, the next part on
     // its way while one is worked on
     const int e = warp - 2, grp = e >> 3, q = warp & 3, hf = (e >> 2) & 1, c0 = hf * kLcWarpCols;
-    // this warp's boxes: GRAD one for stores (the last 64 KB) and one of U before
-    // it, else kLcBoxesU of U
-    constexpr int kUb = GRAD ? 1 : kLcBoxesU;
-    const uint32_t box0 = kLcRing - (GRAD ? 1 : kUb) * kLcEpiWarps * kLcBoxBytes;
-    const uint32_t ooff = kLcRing - (kLcEpiWarps - e) * kLcBoxBytes;
-    const uint32_t uoff = GRAD ? ooff - kLcEpiWarps * kLcBoxBytes : box0 + e * kUb * kLcBoxBytes;
+    // this warp's boxes, from the end of the ring: output (gradient), U before them
+    const uint32_t ooff = kLcRing - (kLcEpiWarps - e) * kLcOBox;
+    const uint32_t uoff = kLcRing - (GRAD ? kLcEpiWarps * kLcOBox : 0) - (kLcEpiWarps - e) * kLcUBox;
     const uint32_t ta = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(grp * kLcTile + c0);
     const uint32_t released = tc::map_rank(tempty(grp), 0);
     const LcJob& z = p.job[GRAD ? kLcMakeG : 0];  // the job that makes logits
@@ -406,6 +402,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
           wt = z.wt ? z.wt[r] : 1.f;
         }
       }
+      if (has_u && (!GRAD || x.job == kLcMakeG) && lane == 0 && r < z.M) {
+        // its boxes of U on their way to L2
+        const int n = min(kLcWarpCols, lc_cols(z.Nn, x.n) - c0);
+        for (int c = 0; c < n; c += kLcPart) tc::tma_prefetch_2d(&z.tu, z.b_n0 + x.n * kLcTile + c0 + c, r);
+      }
     };
     auto announced = [&](int i) LC_INLINE {
       if (!asked) {
@@ -426,17 +427,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
       parts = row - lane < M ? max(0, min(kLcWarpCols, lc_cols(Nn, w.n) - c0)) / kLcPart : 0;
       return true;
     };
-    // box number b of U of the tile's parts, into the warp's slot for it
+    // the tile's box number b of U into the warp's box
     auto load_u = [&](int b) LC_INLINE {
       if (has_u && is_z && b < parts && lane == 0) {
-        const int s = (ubox + b) % kUb;
-        tc::mbar_arrive_expect_tx(ufull(e, s), kLcBoxBytes);
-        tc::tma_load_2d(sbase + uoff + s * kLcBoxBytes, &z.tu, z.b_n0 + w.n * kLcTile + c0 + b * kLcPart, row - lane, ufull(e, s),
+        tc::mbar_arrive_expect_tx(ufull(e), kLcUBox);
+        tc::tma_load_2d(sbase + uoff, &z.tu, z.b_n0 + w.n * kLcTile + c0 + b * kLcPart, row - lane, ufull(e),
                         tc::policy_evict_first());
       }
     };
     for (int tj = grp; announced(tj); tj += 2) {
-      for (int b = 0; b < kUb; ++b) load_u(b);
+      load_u(0);
       if (is_z && (tgt < -1 || tgt >= z.V)) {
         if (w.n == 0 && hf == 0) raise_status(p.status, DSPARK_ERANGE);
         tgt = -1;
@@ -487,9 +487,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
       };
       // U's columns of part h onto its logits
       auto add_u = [&](int h) LC_INLINE {
-        const int s = (ubox + h) % kUb;
-        ok = ok && tc::mbar_wait(ufull(e, s), ((ubox + h) / kUb) & 1, abort);
-        const unsigned char* box = smem + uoff + s * kLcBoxBytes + lane * 128;
+        ok = ok && tc::mbar_wait(ufull(e), (ubox + h) & 1, abort);
+        const unsigned char* box = smem + uoff + lane * 128;
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
           const float4 x = *reinterpret_cast<const float4*>(box + ((c ^ (lane & 7)) << 4));
@@ -499,13 +498,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
           v[4 * c + 3] += x.w;
         }
         __syncwarp();  // every lane has read the box before the next one lands on it
-        load_u(h + kUb);
+        load_u(h + 1);
       };
-      // Stores (gradient): through the warp's box in the layout of the store's
-      // swizzle (conflict-free both ways) and on by the copy engine, which leaves
-      // out what lies past the result's extents. bf16 results go 64 columns (two
-      // parts) at a time, fp32 parts and sums 32.
-      unsigned char* const obox = smem + ooff + lane * 128;
+      // Stores (gradient): 32 rows of 64 bytes through the warp's box in the layout
+      // of the store's swizzle (conflict-free both ways) and on by the copy engine,
+      // which leaves out what lies past the result's extents
+      unsigned char* const obox = smem + ooff + lane * 64;
+      const uint32_t osw = (lane >> 1) & 3;
       auto box_free = [&]() LC_INLINE {  // the store before has read the box
         if (lane == 0) tc::bulk_wait_read();
         __syncwarp();
@@ -522,22 +521,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
         }
       };
       auto put16 = [&](const uint32_t* r, int h, const CUtensorMap* tm, int Nn, __nv_bfloat16* out, int64_t ldo) LC_INLINE {
-        if ((h & 1) == 0) box_free();
+        box_free();
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          *reinterpret_cast<uint4*>(obox + (((k + 4 * (h & 1)) ^ (lane & 7)) << 4)) =
-              make_uint4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
-        if ((h & 1) != 0 || h + 1 == parts) {
-          const int cc = col + kLcPart * (h & ~1);
-          if ((Nn & 7) != 0 && cc + 64 > Nn) {
-            // the copy engine writes whole 16-byte pieces: each lane takes a ragged row's end value by value
-            if (has)
-              for (int i = 0; i < Nn - cc; ++i)
-                out[row * ldo + cc + i] =
-                    *reinterpret_cast<const __nv_bfloat16*>(obox + (((i >> 3) ^ (lane & 7)) << 4) + 2 * (i & 7));
-          } else {
-            put(tm, cc, row - lane);
-          }
+          *reinterpret_cast<uint4*>(obox + ((k ^ osw) << 4)) = make_uint4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
+        const int oc = col + kLcPart * h;
+        if ((Nn & 7) != 0 && oc + kLcPart > Nn) {
+          // the copy engine writes whole 16-byte pieces: each lane takes a ragged row's end value by value
+          if (has)
+            for (int i = 0; i < Nn - oc; ++i)
+              out[row * ldo + oc + i] =
+                  *reinterpret_cast<const __nv_bfloat16*>(obox + (((i >> 3) ^ osw) << 4) + 2 * (i & 7));
+        } else {
+          put(tm, oc, row - lane);
         }
       };
 
@@ -661,12 +657,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
           const int sc = whole ? col : c0, sr = whole ? row - lane : w.slot * kLcTile + row0;
           const bool add = dx ? jx.acc_in : jw.acc_in;  // onto the sums of the pieces before
           each_part([&](int h) LC_INLINE {
-            box_free();
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              *reinterpret_cast<float4*>(obox + ((k ^ (lane & 7)) << 4)) =
-                  make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-          }, [&](int h) LC_INLINE { put(tm, sc + kLcPart * h, sr, add); });
+            for (int g = 0; g < 2; ++g) {  // 16 columns at a time
+              box_free();
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                *reinterpret_cast<float4*>(obox + ((k ^ osw) << 4)) = make_float4(
+                    v[16 * g + 4 * k], v[16 * g + 4 * k + 1], v[16 * g + 4 * k + 2], v[16 * g + 4 * k + 3]);
+              put(tm, sc + kLcPart * h + 16 * g, sr, add);
+            }
+          }, [](int) {});
         }
       }
       if (has_u && is_z) ubox += parts;
@@ -679,7 +679,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
       // boxes of U still in flight land before the CTA can exit
       volatile int never = 0;
       for (int b = ubox; b < ubox + kLcWarpCols / kLcPart; ++b)
-        tc::mbar_wait(ufull(e, b % kUb), (b / kUb) & 1, &never);
+        tc::mbar_wait(ufull(e), b & 1, &never);
     }
     if (GRAD && lane == 0) tc::bulk_wait_all();
   }
@@ -881,16 +881,22 @@ bool encode(CUtensorMap* tm, const void* p, int64_t cols, int64_t rows, int64_t 
                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-// The epilogue's boxes of 32 rows of 128 bytes: fp32 (U, sums, parts) or bf16 (results).
-// Transposed results: bf16, 32 rows of 32 columns, as they lie.
-bool encode_box(CUtensorMap* tm, const void* p, bool bf16, int64_t cols, int64_t rows, int64_t ld, bool t = false) {
+// The epilogue's boxes of 32 rows: U (128 bytes of fp32, to shared memory), and
+// stores of 64 bytes: bf16 results, fp32 sums and parts, or bf16 results turned
+// (32 columns as they lie).
+enum { kBoxU, kBox16, kBox32, kBoxTurned };
+bool encode_box(CUtensorMap* tm, const void* p, int kind, int64_t cols, int64_t rows, int64_t ld) {
+  const bool bf16 = kind == kBox16 || kind == kBoxTurned;
   const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
   const cuuint64_t strides[1] = {(cuuint64_t)ld * (bf16 ? 2 : 4)};
-  const cuuint32_t box[2] = {bf16 && !t ? 64u : 32u, 32};
+  const cuuint32_t box[2] = {kind == kBox32 ? 16u : 32u, 32};
   const cuuint32_t es[2] = {1, 1};
   return encode_fn()(tm, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2,
                      const_cast<void*>(p), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                     t ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+                     kind == kBoxU        ? CU_TENSOR_MAP_SWIZZLE_128B
+                     : kind == kBoxTurned ? CU_TENSOR_MAP_SWIZZLE_NONE
+                                          : CU_TENSOR_MAP_SWIZZLE_64B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 int64_t up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
@@ -1034,7 +1040,7 @@ bool z_job(LcJob& j, const dspark_lce_dims* d, const void* X, const void* W, con
   j.has_u = U != nullptr;
   j.target = target;
   j.V = d->V;
-  if (U && !encode_box(&j.tu, U, false, d->V, d->N, d->ldu)) return false;
+  if (U && !encode_box(&j.tu, U, kBoxU, d->V, d->N, d->ldu)) return false;
   if (!encode(&j.ta, X, d->K, d->N, d->ldx, kLcHalf)) return false;
   return d->layout == DSPARK_W_VK ? encode(&j.tb, W, d->K, d->V, d->ldw, kLcHalf)
                                   : encode(&j.tb, W, d->V, d->K, d->ldw, kLcKb);
@@ -1063,9 +1069,9 @@ bool out_job(LcJob& j, LcJoin& q, float* slots, float* acc, int64_t lda, bool ac
   q.ldo = ldo;
   q.t_out = t_out;
   q.scale = scale;
-  if (j.split && !encode_box(&j.tslots, slots, false, kLcTile, 2ll * j.split * kLcTile, kLcTile)) return false;
-  if (!to_out) return encode_box(&j.tacc, acc, false, lda, j.M, lda);
-  return t_out ? encode_box(&j.to, out, true, j.M, j.Nn, ldo, true) : encode_box(&j.to, out, true, j.Nn, j.M, ldo);
+  if (j.split && !encode_box(&j.tslots, slots, kBox32, kLcTile, 2ll * j.split * kLcTile, kLcTile)) return false;
+  if (!to_out) return encode_box(&j.tacc, acc, kBox32, lda, j.M, lda);
+  return t_out ? encode_box(&j.to, out, kBoxTurned, j.M, j.Nn, ldo) : encode_box(&j.to, out, kBox16, j.Nn, j.M, ldo);
 }
 
 dspark_status lce_fail(cudaError_t e) {
@@ -1216,7 +1222,7 @@ extern "C" dspark_status dspark_linear_ce_grad(const dspark_lce_dims* d, const v
       if (!z_job(g, d, X, W, U, target, v0, cols)) return DSPARK_EINVAL;
       g.lse = lse;
       g.wt = wt;
-      if (!encode_box(&g.to, base + p.G[i & 1], true, cols, d->N, p.ldg)) return DSPARK_EINVAL;
+      if (!encode_box(&g.to, base + p.G[i & 1], kBox16, cols, d->N, p.ldg)) return DSPARK_EINVAL;
     }
     e = l.run(st);
     if (njoin > 0 && e == cudaSuccess)
