@@ -3,7 +3,7 @@
 //   norm = sqrt(sum over tensors and values of x^2),
 //   out  = x * min(1, max_norm / (norm + 1e-6)).
 //
-// Two launches over the same list of pieces (32768 values of one tensor each):
+// Two launches over the same list of pieces (16384 values of one tensor each):
 // the first leaves a partial sum of squares per CTA, the second adds those in
 // order (every CTA the same way) and scales, going through the pieces in
 // reverse so that what the first read last is still in L2. The list of tensors
@@ -24,8 +24,8 @@ namespace dspark {
 namespace {
 
 constexpr int kClThreads = 256;
-constexpr int kClPiece = 32768;    // values of a piece
-constexpr int kClCtas = 152 * 4;   // CTAs of a full grid; partial sums of a launch
+constexpr int kClPiece = 16384;    // values of a piece
+constexpr int kClCtas = 152 * 8;   // CTAs of a full grid; partial sums of a launch
 constexpr int kClLaunch = 512;     // tensors of one launch
 
 struct ClTensor {
@@ -73,10 +73,24 @@ __device__ __forceinline__ double cl_squares(const float* x) {
   return d;
 }
 
+// the CTA's sum of x, in every thread: lanes, then warps, in a fixed order
+__device__ __forceinline__ double cl_block_sum(double x) {
+  __shared__ double red[kClThreads / 32];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
+  __syncthreads();
+  x = 0.0;
+#pragma unroll
+  for (int w = 0; w < kClThreads / 32; ++w) x += red[w];
+  return x;
+}
+
 template <int MAXT>
 __global__ void __launch_bounds__(kClThreads)
     k_clip_norm(const __grid_constant__ ClList<MAXT> l, double* __restrict__ part) {
   double acc = 0.0;
+  pdl_wait();
   for (int i = blockIdx.x; i < l.pieces; i += gridDim.x) {
     const ClTensor& t = l.t[cl_find(l, i)];
     const long long off = (long long)(i - t.first) * kClPiece;
@@ -135,30 +149,20 @@ __global__ void __launch_bounds__(kClThreads)
       }
     }
   }
-  __shared__ double red[kClThreads];
-  red[threadIdx.x] = acc;
-  __syncthreads();
-  for (int o = kClThreads / 2; o > 0; o >>= 1) {
-    if ((int)threadIdx.x < o) red[threadIdx.x] += red[threadIdx.x + o];
-    __syncthreads();
-  }
-  if (threadIdx.x == 0) part[blockIdx.x] = red[0];
+
+  acc = cl_block_sum(acc);
+  if (threadIdx.x == 0) part[blockIdx.x] = acc;
 }
 
 template <int MAXT>
 __global__ void __launch_bounds__(kClThreads)
     k_clip_scale(const __grid_constant__ ClList<MAXT> l, const double* __restrict__ part, int parts, float max_norm,
                  int write_norm, float* __restrict__ norm_out, int* status) {
-  __shared__ double red[kClThreads];
+  pdl_wait();
   double s = 0.0;
   for (int i = threadIdx.x; i < parts; i += kClThreads) s += part[i];
-  red[threadIdx.x] = s;
-  __syncthreads();
-  for (int o = kClThreads / 2; o > 0; o >>= 1) {
-    if ((int)threadIdx.x < o) red[threadIdx.x] += red[threadIdx.x + o];
-    __syncthreads();
-  }
-  const double norm = sqrt(red[0]);
+  s = cl_block_sum(s);
+  const double norm = sqrt(s);
   const float nf = (float)norm;
   // a norm that is not finite scales nothing: the caller sees it and skips the step
   const bool finite = isfinite(nf);
@@ -251,12 +255,10 @@ bool cl_list(ClList<MAXT>& l, const void* const* in, void* const* out, const int
 template <int MAXT>
 cudaError_t cl_run(bool scale, const ClList<MAXT>& l, double* part, int parts, float max_norm, bool last, float* norm,
                    int* status, cudaStream_t st) {
-  const int grid = l.pieces < 1 ? 1 : l.pieces < kClCtas ? l.pieces : kClCtas;
-  if (scale)
-    k_clip_scale<MAXT><<<grid, kClThreads, 0, st>>>(l, part, parts, max_norm, last ? 1 : 0, norm, status);
-  else
-    k_clip_norm<MAXT><<<grid, kClThreads, 0, st>>>(l, part);
-  return cudaGetLastError();
+  const dim3 grid(l.pieces < 1 ? 1 : l.pieces < kClCtas ? l.pieces : kClCtas), block(kClThreads);
+  return scale ? launch_ex(k_clip_scale<MAXT>, grid, block, 0, st, true, l, part, parts, max_norm, last ? 1 : 0, norm,
+                           status)
+               : launch_ex(k_clip_norm<MAXT>, grid, block, 0, st, true, l, part);
 }
 
 int cl_grid(int64_t pieces) { return pieces < 1 ? 1 : pieces < kClCtas ? (int)pieces : kClCtas; }
