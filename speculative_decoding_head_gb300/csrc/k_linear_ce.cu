@@ -258,13 +258,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
   }
   tc::tc_fence_before();
   __syncthreads();
-  tc::cluster_sync();
+  tc::cluster_meet();
   tc::tc_fence_after();
   const uint32_t tmem = *tmem_holder;
-  pdl_wait();  // everything below reads or writes what earlier kernels of the stream write or read
   // a small grid leaves SMs on which the next kernel can set up meanwhile
+  // (which waits in turn: it reads and writes nothing before this grid has ended)
   const bool early = gridDim.x <= kLcPairs;
-  if (early) pdl_trigger();
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -279,7 +278,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
         tc::mbar_arrive(told(tj));
         ++tj;
       };
-      for (LcIter it(pair); ok && it.next(p, pair, npairs, w);) {
+      LcIter it(pair);
+      bool more = it.next(p, pair, npairs, w);
+      pdl_wait();  // the operands are what earlier kernels of the stream wrote
+      if (early) pdl_trigger();
+      for (; ok && more; more = it.next(p, pair, npairs, w)) {
         tell(LcTile::pack(w));
         const LcJob& j = p.job[w.job];
         const int half = lc_cols(j.Nn, w.n) >> 1;  // columns of B in each CTA
@@ -331,7 +334,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
     if (lane == 0 && rank == 0) {
       bool ok = true;
       LcRing r{0, 0};
-      for (int tj = 0;; ++tj) {
+      int tj = 0;
+      for (;; ++tj) {
         ok = tc::mbar_wait(told(tj), (tj / kLcAhead) & 1, abort);
         if (!ok) break;
         const int4 x = tile_ring[tj & (kLcAhead - 1)];
@@ -361,6 +365,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
         if (!ok) break;
         tc::mma_commit_pair(tfull(ab));
       }
+      // both CTAs' epilogues have released the last tiles: their arrivals have landed before this CTA exits
+      for (int t = max(0, tj - 2); t < tj && ok; ++t) ok = tc::mbar_wait(tempty(t & 1), (t >> 1) & 1, abort);
       if (!ok) {
         if (!*abort) raise_status(p.status, DSPARK_ETIMEOUT);
         *abort = 1;
@@ -385,6 +391,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
     const int row0 = (int)rank * kLcHalf + q * 32;  // the warp's first row in a tile
     bool ok = true;
     int ubox = 0;  // boxes of U taken so far
+    pdl_wait();    // rows' data, U and the outputs are other kernels' until they end
 
     // the tile announced as number i; a logit tile's target, lse and weight of this
     // lane's row, asked for a tile early where the tile is announced by then
@@ -687,7 +694,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
   __syncwarp();
   tc::tc_fence_before();
   __syncthreads();
-  tc::cluster_sync();  // the peer's MMAs have read this CTA's operands; remote arrivals have landed
+  tc::cluster_meet();  // the peer's MMAs have read this CTA's operands
   if (warp == 1) {
     tc::tc_fence_after();
     tc::tmem_dealloc_pair(tmem, kLcTmemCols);

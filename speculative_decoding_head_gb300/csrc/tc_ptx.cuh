@@ -334,8 +334,11 @@ __device__ __forceinline__ uint32_t cluster_ctarank() {
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
+// Both CTAs' threads meet. No memory is ordered by it (a release would wait for
+// every global store of the CTA): for barriers set up under fence_barrier_init,
+// and for an exit after which neither CTA is written to.
+__device__ __forceinline__ void cluster_meet() {
+  asm volatile("barrier.cluster.arrive.relaxed;\n barrier.cluster.wait;" ::: "memory");
 }
 // The shared::cluster address of CTA `rank`'s variable at this CTA's shared address `addr`.
 __device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
