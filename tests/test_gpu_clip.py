@@ -78,6 +78,16 @@ def test_large_list():
     _check(_make([30_000_001, 20_000_000, 5], [F32, BF16]), 1.0)
 
 
+def test_a_tensor_past_32_bits():
+    n = 2 ** 31 + 11
+    x = torch.zeros(n, dtype=BF16, device="cuda")
+    x[0], x[2 ** 31 - 1], x[n - 1] = 3.0, 4.0, 12.0
+    op = GradClip([x])
+    assert abs(float(op.clip(6.5)) - 13.0) <= 13.0 * NORM_TOL and op.device_status() == 0
+    assert float(x[0]) == 1.5 and float(x[2 ** 31 - 1]) == 2.0 and float(x[n - 1]) == 6.0
+    assert int(torch.count_nonzero(x[:2 ** 30])) == 1
+
+
 def test_within_the_norm_nothing_changes():
     ts = _make([1000, 333], [BF16, F32])
     keep = [t.clone() for t in ts]

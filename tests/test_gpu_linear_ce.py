@@ -350,6 +350,48 @@ def test_gradient_against_differences():
         assert abs(diff - along) <= third + loss_tol + along_tol, (which, diff, along, third, loss_tol, along_tol)
 
 
+def test_offsets_past_32_bits():
+    """W and dW of 2.2e9 values, U rows 2^31 values apart from end to end; the reference in pieces of the vocabulary."""
+    N, K, V = 2000, 8, 1_100_003
+    g = torch.Generator(device="cuda").manual_seed(9)
+    U = torch.randn(N, -(-V // 4) * 4, generator=g, device="cuda")[:, :V]
+    X = torch.randn(N, K, generator=g, device="cuda").bfloat16()
+    W = torch.randn(V, K, generator=g, device="cuda").bfloat16()
+    t = torch.randint(0, V, (N,), generator=g, device="cuda", dtype=torch.int32)
+    t[N - 1] = V - 1
+    rows = [0, 7, N - 2, N - 1]
+    op = LinearCE(N, K, V)
+    out = op.forward(X, W, t, U=U, out=op.new_outputs(dw=False))
+    op.grad(X, W, t, out["lse"], scale=1.0, U=U, out=out)
+    assert op.device_status() == 0
+    ref, tol = _reference(X[rows], W, U[rows], t[rows], None, 1.0, "vk")
+    for k in out:
+        _close(out[k][rows], ref[k], tol[k], k)
+    del U, out, op
+    N, K, V = 24, 2048, 1_100_003
+    X = torch.randn(N, K, generator=g, device="cuda").bfloat16()
+    W = torch.empty(V, K, dtype=BF16, device="cuda").normal_(0.0, 0.03, generator=g)
+    t = torch.randint(V - 200, V, (N,), generator=g, device="cuda", dtype=torch.int32)
+    op = LinearCE(N, K, V)
+    out = op.forward(X, W, t, out=op.new_outputs(dx=False))
+    op.grad(X, W, t, out["lse"], scale=1.0, out=out)
+    assert op.device_status() == 0
+    z = torch.cat([X.double() @ W[a:a + 100_000].double().t() for a in range(0, V, 100_000)], 1)
+    lse = torch.logsumexp(z, 1)
+    zmax = 2.0 * float(z.abs().max()) + 0.03 * K        # the partial sums' magnitude: sum |x w| <= 0.03 K on average
+    ez = 2.0 ** -23 * zmax * (K / 16 + 8)
+    el = ez + 2.0 ** -20 + 2.0 ** -22 * lse.abs()
+    _close(out["lse"], lse, el, "lse")
+    a = V - 300                                          # the last rows of dW, the targets among them
+    p = torch.exp(z[:, a:] - lse[:, None])
+    hot = torch.zeros_like(p)
+    hot[torch.arange(N, device="cuda"), t.long() - a] = 1.0
+    ref = (p - hot).t() @ X.double()
+    mag = (p + hot).t() @ X.double().abs()
+    tol = 2.0 ** -8 * 1.01 * ref.abs() + (2.0 ** -8 * 1.01 + float(ez + el.max()) + 2.0 ** -20 + 2.0 ** -23 * 66) * mag
+    _close(out["dW"][a:], ref, tol + 1e-30, "dW")
+
+
 def test_refusals():
     X, W, U, t, wt = _inputs(20, 64, 300, "vk", True)
     op = LinearCE(20, 64, 300)
