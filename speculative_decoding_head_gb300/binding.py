@@ -187,9 +187,14 @@ def _vec(t: Optional[torch.Tensor], n: int, dtype, name: str):
     return t.data_ptr()
 
 
+# torch's own short way to a device's current stream, where it has one
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
 def _raw_stream(stream, device: int) -> int:
     """Address of the stream (the current one of the device if None)."""
-    return torch.cuda.current_stream(device).cuda_stream if stream is None else stream.cuda_stream
+    return _current_stream(device) if stream is None else stream.cuda_stream
 
 
 def _stream(stream) -> C.c_void_p:

@@ -910,15 +910,18 @@ int64_t up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 int tiles_of(int64_t x) { return (int)((x + kLcTile - 1) / kLcTile); }
 
 // Pairs that share a product's tiles block by block: where whole tiles would
-// leave part of the grid idle (fewer than two per pair), as long as every pair
-// gets eight blocks and the longest pair saves more blocks (a third of a
-// microsecond each) than the join's launch costs. A function of the sizes alone, so the order of the sums
-// does not depend on the device.
+// leave more than a quarter of the grid idle in at most two waves, every pair
+// gets eight blocks, and the longest pair saves more blocks (a third of a
+// microsecond each) than the join's launch costs. Whole tiles run side by side on
+// the same stretch of the contraction and share its operands in L2, shares do
+// not (1001 x 4100 x 50257, dX of 68 tiles of 786 blocks: the gradient took 813 us
+// with shares and 535 with whole tiles). A function of the sizes alone, so the order of the sums does not depend on the device.
 int split_of(int tiles, int nkb) {
-  if (tiles >= 2 * kLcPairs) return 0;
+  const int waves = (tiles + kLcPairs - 1) / kLcPairs;
+  if (waves > 2 || 4 * tiles >= 3 * waves * kLcPairs) return 0;
   const int64_t most = (int64_t)tiles * nkb / 8;
   const int s = (int)(most < kLcPairs ? most : kLcPairs);
-  return s > tiles && nkb - (int)(((int64_t)tiles * nkb + s - 1) / s) > 12 ? s : 0;
+  return s > tiles && waves * nkb - (int)(((int64_t)tiles * nkb + s - 1) / s) > 12 ? s : 0;
 }
 
 // The gradient's pieces of the vocabulary and its scratch.
