@@ -365,15 +365,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
         if (!ok) break;
         tc::mma_commit_pair(tfull(ab));
       }
-      // both CTAs' epilogues have released the last tiles: their arrivals have landed before this CTA exits
+      // both CTAs' epilogues have released the last tiles: every MMA is complete, and
+      // their arrivals have landed before this CTA exits
       for (int t = max(0, tj - 2); t < tj && ok; ++t) ok = tc::mbar_wait(tempty(t & 1), (t >> 1) & 1, abort);
       if (!ok) {
         if (!*abort) raise_status(p.status, DSPARK_ETIMEOUT);
         *abort = 1;
+        tc::mma_commit_pair_own(drain);  // every MMA issued completes before TMEM and the peer's operands go
+        volatile int never = 0;
+        tc::mbar_wait(drain, 0, &never);
       }
-      tc::mma_commit_pair_own(drain);  // every MMA issued completes before TMEM and the peer's operands go
-      volatile int never = 0;
-      tc::mbar_wait(drain, 0, &never);
     }
   } else {
     // ------------------------------------------------------------ epilogue
