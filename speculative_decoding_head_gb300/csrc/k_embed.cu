@@ -2,18 +2,25 @@
 //
 //   out[n] = s E[idx_n],   dE[v] = base[v] + s sum_{n: idx_n = v} dout[n]
 //
-// The lookup moves each row once: a warp takes 4 rows x 64 pieces of 16 bytes
-// at a time, its loads in flight together.
+// The lookup moves each row once: a warp takes 4 rows and one or two spans of 256
+// columns at a time, its loads in flight together. 16384 rows of 5120 bf16: 43 us,
+// 81% of the measured copy rate (one span a warp: 59 us); small calls are one
+// launch's latency (4.2 us on the device).
 //
 // The gradient sorts the rows by token (a stable radix sort of (token, row)
 // pairs, digits of at most 10 bits: two passes up to V = 2^20) and then sums
 // the sorted rows, so that dout is read once, no atomics touch dE, and the
 // order of every sum is that of the rows: the same result each time. A CTA
-// takes 256 consecutive sorted rows whatever tokens they hold (frequent tokens
-// own long runs, rare ones short runs, most of a large vocabulary none), so the
-// work is even: runs inside the CTA are written at once, a run that crosses CTAs
-// leaves fp32 partial sums that the last kernel adds in order. That kernel also
-// writes the rows of the tokens that do not occur.
+// takes up to 256 consecutive sorted rows whatever tokens they hold (frequent
+// tokens own long runs, rare ones short runs, most of a large vocabulary none),
+// so the work is even: runs inside the CTA are written at once, a run that
+// crosses CTAs leaves fp32 partial sums that the last kernel adds in order. That
+// kernel also writes the rows of the tokens that do not occur.
+//
+// 262144 rows of 256 bf16 into V = 129280: 68 us, 2.45 times the floor of its
+// bytes: 24 us of sort (four launches, each a chain of latencies: load, count,
+// add up, place), 32 us of sums (512-byte rows in random order, 4.7 TB/s) and
+// 12 us of joins and absent rows.
 #include <math.h>
 #include <stdio.h>
 

@@ -187,6 +187,7 @@ def test_masks():
     U[7, :999] = torch.finfo(F32).min
     U[8] = -1e30                    # a mask's value throughout: nothing left
     U[9, 256:512] = -math.inf
+    U[10, int(t[10])] = torch.finfo(F32).min    # a target masked by the lowest value: loss +inf
     op = LinearCE(40, 64, 1000)
     out = op.forward(X, W, t, U=U, out=op.new_outputs())
     op.grad(X, W, t, out["lse"], wt=wt, scale=1.0, U=U, out=out)
@@ -198,7 +199,7 @@ def test_masks():
     for dead in (5, 8):
         assert out["lse"][dead] == -math.inf and out["loss"][dead] == math.inf and (out["dX"][dead] == 0).all()
     assert out["lse"][6] == -math.inf and out["loss"][6] == 0 and (out["dX"][6] == 0).all()
-    assert out["loss"][3] == math.inf
+    assert out["loss"][3] == math.inf and out["loss"][10] == math.inf
 
 
 def test_nan_and_infinity_stay_in_their_row():
