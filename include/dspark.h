@@ -410,9 +410,10 @@ dspark_status dspark_pctree_verify(dspark_ws* ws, const float* P, const int32_t*
  * target is masked has loss +inf. A row with every token masked has lse -inf,
  * loss +inf (0 if left out) and no part in the gradients. NaN and z above 1e38
  * make their row's results NaN. N = 0 is allowed (dW is then 0). 0 <= N <= 2^20,
- * K <= 65536, V <= 2^24, else DSPARK_EINVAL. The products' fp32 accumulation in
- * the tensor cores leaves lse a relative error of about 3e-10 K (1.3e-6 at K =
- * 4100). Asynchronous on `stream`; each result is the same from call to call.
+ * K <= 65536, V <= 2^24, else DSPARK_EINVAL. The tensor cores cut their fp32
+ * accumulator once per 16 terms; with the mean of that made up for, lse is off by
+ * about 1.3e-10 K of itself on random rows (5e-7 at K = 4096). Asynchronous on
+ * `stream`; each result is the same from call to call.
  */
 typedef enum { DSPARK_W_VK = 0, DSPARK_W_KV = 1 } dspark_w_layout;
 

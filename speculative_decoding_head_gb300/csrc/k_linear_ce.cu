@@ -102,6 +102,7 @@ struct LcJob {
   // logits (statistics, G)
   int has_u;
   int V;                // vocabulary
+  float gain;           // makes up for the accumulator's truncation (see logit_gain)
   const int32_t* target;
   const float* lse;
   const float* wt;
@@ -400,6 +401,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
     const uint32_t released = tc::map_rank(tempty(grp), 0);
     const LcJob& z = p.job[GRAD ? kLcMakeG : 0];  // the job that makes logits
     const bool has_u = z.has_u != 0;
+    // the gain goes to the logits when U is added, else into what they are multiplied by
+    const float gain = z.gain, zgain = has_u ? 1.f : gain, l2 = tc::kLog2e * zgain;
     const int row0 = (int)rank * kLcHalf + q * 32;  // the warp's first row in a tile
     bool ok = true;
     int ubox = 0;  // boxes of U taken so far
@@ -486,7 +489,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
         if (!GRAD && has) z.part[(int64_t)row * (2 * z.nt) + 2 * w.n + hf] = make_float2(kLcRefMin, 0.f);
         continue;
       }
-      const unsigned long long l2e = tc::f2pack(tc::kLog2e, tc::kLog2e);
+      const unsigned long long l2e = tc::f2pack(l2, l2);
 
       // the warp's parts in order: `use` takes a part's values from v, the next
       // part is asked for and `send` does what is left of this one meanwhile;
@@ -511,10 +514,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
           const float4 x = *reinterpret_cast<const float4*>(box + ((c ^ (lane & 7)) << 4));
-          v[4 * c] += x.x;
-          v[4 * c + 1] += x.y;
-          v[4 * c + 2] += x.z;
-          v[4 * c + 3] += x.w;
+          v[4 * c] = fmaf(v[4 * c], gain, x.x);
+          v[4 * c + 1] = fmaf(v[4 * c + 1], gain, x.y);
+          v[4 * c + 2] = fmaf(v[4 * c + 2], gain, x.z);
+          v[4 * c + 3] = fmaf(v[4 * c + 3], gain, x.w);
         }
         __syncwarp();  // every lane has read the box before the next one lands on it
         load_u(h + 1);
@@ -570,7 +573,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
             float x = 0.f;
 #pragma unroll
             for (int i = 0; i < kLcPart; ++i) x = i == t ? v[i] : x;
-            if (has) z.zt[row] = x;
+            if (has) z.zt[row] = x * zgain;
           }
           float mx[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
@@ -583,7 +586,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
           // so that one fused step gives each exponent with one rounding; what
           // lies below its least value (-inf, the type's lowest value as a
           // mask) adds nothing to the sum
-          const float nr = fmaxf(ref, ceilf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * tc::kLog2e));
+          const float nr = fmaxf(ref, ceilf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * l2));
           sum *= tc::ex2_ftz(ref - nr);
           ref = nr;
           const unsigned long long nref = tc::f2pack(-ref, -ref);
@@ -1052,6 +1055,14 @@ struct LcLaunch {
   }
 };
 
+// The tensor cores' fp32 accumulator is cut, not rounded, once per 16 terms: on
+// average by half a unit, 0.36 * 2^-23 of the partial sum (half the mean of 1/m
+// over significands m in [1, 2), 1 / (4 log 2)). The partial sums of a logit that
+// matters grow evenly towards it, so over n steps it loses 0.36 * 2^-23
+// (n + 1) / 2 of itself; the gain puts that back. A logit whose terms all come last
+// is then off by as much the other way.
+float logit_gain(int K) { return (float)(1.0 + 0.36 * 0x1p-23 * (K / 16.0 + 1.0) / 2.0); }
+
 // z of the columns [v0, v0 + cols) of the vocabulary (statistics or G)
 bool z_job(LcJob& j, const dspark_lce_dims* d, const void* X, const void* W, const float* U, const int32_t* target,
            int v0, int cols) {
@@ -1063,6 +1074,7 @@ bool z_job(LcJob& j, const dspark_lce_dims* d, const void* X, const void* W, con
   j.has_u = U != nullptr;
   j.target = target;
   j.V = d->V;
+  j.gain = logit_gain(d->K);
   if (U && !encode_box(&j.tu, U, kBoxU, d->V, d->N, d->ldu)) return false;
   if (!encode(&j.ta, X, d->K, d->N, d->ldx, kLcHalf)) return false;
   return d->layout == DSPARK_W_VK ? encode(&j.tb, W, d->K, d->V, d->ldw, kLcHalf)
