@@ -346,6 +346,16 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
 }
+// CTA `rank`'s variable at this CTA's shared address `addr`.
+__device__ __forceinline__ int ld_rank(uint32_t addr, uint32_t rank) {
+  int x;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(x) : "r"(map_rank(addr, rank)) : "memory");
+  return x;
+}
+// All threads of the cluster meet; what they wrote before is seen after.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
+}
 // Arrival without release: for tensor-memory reads that a tcgen05.wait has
 // completed (a release would also wait for this thread's global stores).
 __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_bar) {

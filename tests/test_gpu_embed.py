@@ -140,6 +140,14 @@ def test_large_vocabulary_and_three_digits():
     _check_grad(500, 129280, 16, BF16, BF16, _idx(500, 129280, "uniform"))
 
 
+@pytest.mark.parametrize("N", [4096, 4097, 16385, 32768, 32769, 70000])
+@pytest.mark.parametrize("V", [2, 1025, (1 << 20) + 1])
+def test_lengths_about_the_sorts_bounds(N, V):
+    """Sizes on both sides of where the sort's form changes, of one to three digits."""
+    for kind in ("uniform", "zipf"):
+        _check_grad(N, V, 3, F32, F32, _idx(N, V, kind))
+
+
 def test_offsets_past_32_bits():
     """A table whose rows lie more than 2^31 values apart from end to end."""
     V, D = 70001, 32768
