@@ -126,6 +126,7 @@ enum : int { kLcDx = 0, kLcDw = 1, kLcMakeG = 2, kLcJobs = 3 };
 struct LcParams {
   LcJob job[kLcJobs];
   int tiles[kLcJobs];   // whole tiles of jobs 0 .. i (running totals; split jobs add none)
+  int sharing, rounds;  // the first `sharing` pairs take whole tiles from round `rounds` on
   int stages;
   int* status;
 };
@@ -141,15 +142,16 @@ __host__ __device__ __forceinline__ int lc_share(int units, int split, int p) {
 }
 
 // What a pair works on next: its share of the split jobs, then whole tiles of
-// the others, one in npairs. The producer goes through it and announces each
+// the others, one a round (the first rounds without pairs busy with shares). The producer goes through it and announces each
 // tile to its CTA's other warps.
 struct LcWork {
   int job, m, n, kb0, kb1;
   int slot;  // part of a shared tile: its slot; -1: a whole tile
 };
 struct LcIter {
-  int j, u, uend, t;
-  __device__ __forceinline__ LcIter(int pair) : j(-1), u(0), uend(0), t(pair) {}
+  int j, u, uend, r;
+  __device__ __forceinline__ LcIter(const LcParams& p, int pair)
+      : j(-1), u(0), uend(0), r(pair < p.sharing ? p.rounds : 0) {}
   __device__ __forceinline__ bool next(const LcParams& p, int pair, int npairs, LcWork& w) {
     while (u >= uend && j + 1 < kLcJobs) {
       ++j;
@@ -170,6 +172,9 @@ struct LcIter {
       u += w.kb1 - w.kb0;
       w.slot = w.kb0 == 0 && w.kb1 == q.nkb ? -1 : 2 * pair + (w.kb0 == 0 ? 1 : 0);
     } else {
+      const int others = npairs - p.sharing;
+      const int t = r < p.rounds ? r * others + pair - p.sharing : p.rounds * others + (r - p.rounds) * npairs + pair;
+      ++r;
       if (t >= p.tiles[kLcJobs - 1]) return false;
       int k = 0, before = 0;
       while (t >= p.tiles[k]) before = p.tiles[k++];
@@ -178,7 +183,6 @@ struct LcIter {
       w.kb1 = p.job[k].nkb;
       w.slot = -1;
       tile = t - before;
-      t += npairs;
     }
     // column tiles outermost, up to 16 row tiles innermost, so that the tiles
     // in flight share their columns' operand in L2
@@ -290,7 +294,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
         tc::mbar_arrive(told(tj));
         ++tj;
       };
-      LcIter it(pair);
+      LcIter it(p, pair);
       bool more = it.next(p, pair, npairs, w);
       pdl_wait();  // the operands are what earlier kernels of the stream wrote
       if (early) pdl_trigger();
@@ -940,11 +944,15 @@ int split_of(int tiles, int nkb) {
   return s > tiles && waves * nkb - (int)(((int64_t)tiles * nkb + s - 1) / s) > 12 ? s : 0;
 }
 
+// A whole tile's time in blocks: an MN-major B (see make_plan), its start and end.
+double tile_cost(int nkb, bool b_mn) { return nkb * (b_mn ? 1.38 : 1.0) + 2.0; }
+
 // The gradient's pieces of the vocabulary and its scratch.
 struct LcPlan {
   int piece, pieces;
   int64_t ldg;
   int dx_split, dw_split, dx_nkb;
+  int dx_split_dw;  // dX's beside dW
   int64_t dx_lda;
   bool swap;    // the operand whose contraction index is its row goes to A (see make_plan)
   int64_t ldt;  // of X's transpose
@@ -981,6 +989,18 @@ LcPlan make_plan(const dspark_lce_dims& d) {
   p.dx_nkb = (int)nkb_v;
   p.dx_split = split_of(tiles_of(N) * tiles_of(K), (int)nkb_v);
   p.dw_split = split_of(tiles_of(widest) * tiles_of(K), (int)nkb_n);
+  // Beside whole tiles of dW, dX goes to as many pairs as its part of the work
+  // (those take whole tiles later): each pair more writes another 256 KB of sums
+  // a piece. 640 x 256 x 129280 without U: all 76 pairs 167 us, 38 pairs 156;
+  // 640 x 256 x 43093 with U 100 and 88, 100 x 512 x 129280 133 and 114. (64 x 4096 x
+  // 129280, bound by W's way from HBM, loses 3%.)
+  p.dx_split_dw = p.dx_split;
+  if (p.dx_split > 0 && p.dw_split == 0) {
+    const int tiles = tiles_of(N) * tiles_of(K);
+    const double x = (double)tiles * nkb_v, w = (double)tiles_of(widest) * tiles_of(K) * tile_cost((int)nkb_n, false);
+    const int s = (int)(kLcPairs * x / (x + w) + 0.5);
+    p.dx_split_dw = s <= tiles ? tiles + 1 : s < p.dx_split ? s : p.dx_split;
+  }
   // An MN-major B (its contraction index is its row) costs the tensor cores
   // 1.38x the time of a K-major one, an MN-major A nothing (256 x 256 tiles,
   // contraction 5376: 885 against 640 cycles a block). So where the products are
@@ -1050,6 +1070,19 @@ struct LcLaunch {
     }
     pairs = pairs > tiles ? pairs : tiles;
     pairs = pairs < kLcPairs ? pairs : kLcPairs;
+    // rounds of whole tiles that the other pairs do during one of dX's shares
+    const LcJob& x = p.job[kLcDx];
+    if (x.split > 0 && x.split < pairs && p.job[kLcDw].split == 0) {
+      const int others = pairs - x.split;
+      double left = (double)x.mt * x.nt * x.nkb / x.split;
+      p.sharing = x.split;
+      for (int t = 0; t < tiles; t += others, ++p.rounds) {
+        const LcJob& j = p.job[t < p.tiles[kLcDw] ? kLcDw : kLcMakeG];
+        const double cost = tile_cost(j.nkb, j.b_mn);
+        if (left < 0.5 * cost) break;
+        left -= cost;
+      }
+    }
     e = launch_ex(grad ? k_lce<true> : k_lce<false>, dim3(2 * pairs), dim3(kLcThreads), kLcSmem, st, true, p);
     return e != cudaSuccess ? e : cudaGetLastError();
   }
@@ -1202,7 +1235,7 @@ extern "C" dspark_status dspark_linear_ce_grad(const dspark_lce_dims* d, const v
         x.M = t ? d->K : d->N;
         x.Nn = t ? d->N : d->K;
         x.nkb = p.dx_nkb;  // every piece's (a narrower last piece reads zeros), so that slots keep their tiles
-        x.split = p.dx_split;
+        x.split = dW ? p.dx_split_dw : p.dx_split;
         if (!out_job(x, joins.j[njoin], reinterpret_cast<float*>(base + p.dx_slots),
                      reinterpret_cast<float*>(base + p.dx_acc), p.dx_lda, i > 1, i == p.pieces,
                      static_cast<__nv_bfloat16*>(dX), d->lddx, t, scale))
