@@ -94,7 +94,8 @@ struct LcJob {
   CUtensorMap to, tacc, tslots;  // stores: result (bf16; G's piece), fp32 sums, parts
   int M, Nn;            // rows and columns of the result
   int nkb;              // contraction blocks
-  int mt, nt;           // tiles of 256 rows, of 256 columns
+  int mt, nt;           // tiles of 256 rows, of tn columns
+  int tn;               // 256, or 128 or 64 where logits have few tiles (see z_cols)
   int split;            // pairs that share the tiles' blocks evenly (0: whole tiles)
   int a_mn, b_mn;       // operand's contraction index is its row (MN-major)
   int b_k0;             // contraction offset in B's map
@@ -211,7 +212,7 @@ struct LcTile {
 };
 
 // columns of B the MMA takes for a tile of a result of Nn columns: a multiple of 32
-__device__ __forceinline__ int lc_cols(int Nn, int n) { return min(kLcTile, (Nn - n * kLcTile + 31) & ~31); }
+__device__ __forceinline__ int lc_cols(int Nn, int n, int tn) { return min(tn, (Nn - n * tn + 31) & ~31); }
 
 // ring position and the parity of its pass
 struct LcRing {
@@ -301,10 +302,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
       for (; ok && more; more = it.next(p, pair, npairs, w)) {
         tell(LcTile::pack(w));
         const LcJob& j = p.job[w.job];
-        const int half = lc_cols(j.Nn, w.n) >> 1;  // columns of B in each CTA
-        const int am = w.m * kLcTile + (int)rank * kLcHalf, bn = j.b_n0 + w.n * kLcTile + (int)rank * half;
+        const int half = lc_cols(j.Nn, w.n, j.tn) >> 1;  // columns of B in each CTA
+        const int am = w.m * kLcTile + (int)rank * kLcHalf, bn = j.b_n0 + w.n * j.tn + (int)rank * half;
         const int bboxes = (half + 63) >> 6;  // boxes of an MN-major B
-        const uint32_t bytes = (uint32_t)(kLcOpBytes + (j.b_mn ? bboxes * kLcBox : kLcOpBytes));
+        const uint32_t bytes = (uint32_t)(kLcOpBytes + (j.b_mn ? bboxes * kLcBox : j.tn * kLcKb));
         const bool a_mn = j.a_mn, b_mn = j.b_mn;
         const int b_k0 = j.b_k0;
         for (int kb = w.kb0; kb < w.kb1; ++kb) {
@@ -358,7 +359,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
         if (x.x < 0) break;
         const LcTile w(x);
         const LcJob& j = p.job[w.job];
-        const uint32_t idesc = tc::idesc_bf16_f32(kLcTile, lc_cols(j.Nn, w.n), j.b_mn) | (j.a_mn ? 1u << 15 : 0u);
+        const uint32_t idesc = tc::idesc_bf16_f32(kLcTile, lc_cols(j.Nn, w.n, j.tn), j.b_mn) | (j.a_mn ? 1u << 15 : 0u);
         const int ab = tj & 1;
         ok = tc::mbar_wait(tempty(ab), ((tj >> 1) & 1) ^ 1, abort);
         if (!ok) break;
@@ -397,14 +398,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
     // group grp takes tiles grp, grp + 2, ..; its warp reads lane quarter q and
     // 128 columns (half hf) of the accumulator in parts of 32, the next part on
     // its way while one is worked on
-    const int e = warp - 2, grp = e >> 3, q = warp & 3, hf = (e >> 2) & 1, c0 = hf * kLcWarpCols;
+    const int e = warp - 2, grp = e >> 3, q = warp & 3, hf = (e >> 2) & 1;
     // this warp's boxes, from the end of the ring: output (gradient), U before them
     const uint32_t ooff = kLcRing - (kLcEpiWarps - e) * kLcOBox;
     const uint32_t uoff = kLcRing - (GRAD ? kLcEpiWarps * kLcOBox : 0) - (kLcEpiWarps - e) * kLcUBox;
-    const uint32_t ta = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(grp * kLcTile + c0);
+    const uint32_t ta = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(grp * kLcTile);
     const uint32_t released = tc::map_rank(tempty(grp), 0);
     const LcJob& z = p.job[GRAD ? kLcMakeG : 0];  // the job that makes logits
     const bool has_u = z.has_u != 0;
+    const int zn = z.tn;  // columns of a tile of logits
     // the gain goes to the logits when U is added, else into what they are multiplied by
     const float gain = z.gain, zgain = has_u ? 1.f : gain, l2 = tc::kLog2e * zgain;
     const int row0 = (int)rank * kLcHalf + q * 32;  // the warp's first row in a tile
@@ -415,7 +417,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
     // the tile announced as number i; a logit tile's target, lse and weight of this
     // lane's row, asked for a tile early where the tile is announced by then
     LcTile w;
-    int tgt = -1, row = 0, parts = 0;
+    int tgt = -1, row = 0, parts = 0, col = 0, half = 0;  // col, half: the warp's first column in the result; its columns
     float lse = 0.f, wt = 1.f;
     bool is_z = false, has = false, asked = false;
     auto ask = [&](const LcTile& x) LC_INLINE {
@@ -430,8 +432,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
       }
       if (has_u && (!GRAD || x.job == kLcMakeG) && lane == 0 && r < z.M) {
         // its boxes of U on their way to L2
-        const int n = min(kLcWarpCols, lc_cols(z.Nn, x.n) - c0);
-        for (int c = 0; c < n; c += kLcPart) tc::tma_prefetch_2d(&z.tu, z.b_n0 + x.n * kLcTile + c0 + c, r);
+        const int c0 = hf * (zn >> 1), n = min(zn >> 1, lc_cols(z.Nn, x.n, zn) - c0);
+        for (int c = 0; c < n; c += kLcPart) tc::tma_prefetch_2d(&z.tu, z.b_n0 + x.n * zn + c0 + c, r);
       }
     };
     auto announced = [&](int i) LC_INLINE {
@@ -450,14 +452,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
       row = w.m * kLcTile + row0 + lane;
       has = row < M;
       // parts of 32 columns this warp has (0: none, or no rows; the same for its lanes)
-      parts = row - lane < M ? max(0, min(kLcWarpCols, lc_cols(Nn, w.n) - c0)) / kLcPart : 0;
+      const int tn = is_z ? zn : kLcTile;
+      half = tn >> 1;
+      col = w.n * tn + hf * half;
+      parts = row - lane < M ? max(0, min(half, lc_cols(Nn, w.n, tn) - hf * half)) / kLcPart : 0;
       return true;
     };
     // the tile's box number b of U into the warp's box
     auto load_u = [&](int b) LC_INLINE {
       if (has_u && is_z && b < parts && lane == 0) {
         tc::mbar_arrive_expect_tx(ufull(e), kLcUBox);
-        tc::tma_load_2d(sbase + uoff, &z.tu, z.b_n0 + w.n * kLcTile + c0 + b * kLcPart, row - lane, ufull(e),
+        tc::tma_load_2d(sbase + uoff, &z.tu, z.b_n0 + col + b * kLcPart, row - lane, ufull(e),
                         tc::policy_evict_first());
       }
     };
@@ -468,7 +473,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
         tgt = -1;
       }
       // the target's place in the half, the exponent's offset: with the weight in it for G
-      const int te = tgt - (z.b_n0 + w.n * kLcTile + c0);
+      const int te = tgt - (z.b_n0 + col);
       const bool live = !is_z || (tgt >= 0 && lse != -INFINITY);  // else the row has no G
       const float wr = is_z ? wt : 1.f;
       const float off = GRAD ? fmaf(-lse, tc::kLog2e, log2f(fabsf(wr))) : 0.f;
@@ -487,7 +492,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
         __syncwarp();
         if (lane == 0) tc::mbar_arrive_cluster_relaxed(released);
       };
-      const int col = w.n * kLcTile + c0;  // the half's first column in the result
       if (parts == 0) {
         release();
         if (!GRAD && has) z.part[(int64_t)row * (2 * z.nt) + 2 * w.n + hf] = make_float2(kLcRefMin, 0.f);
@@ -500,14 +504,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
       // the accumulator is released with the last part's arrival
       float v[kLcPart];
       auto each_part = [&](auto&& use, auto&& send) LC_INLINE {
-        tc::tmem_ld32(ta, v);
+        const uint32_t t0 = ta + (uint32_t)(hf * half);
+        tc::tmem_ld32(t0, v);
 #pragma unroll 1
         for (int h = 0; h < parts; ++h) {
           tc::tmem_wait_ld();
           tc::tmem_tie32(v);
           if (h + 1 == parts) release();
           use(h);
-          if (h + 1 < parts) tc::tmem_ld32(ta + (h + 1) * kLcPart, v);
+          if (h + 1 < parts) tc::tmem_ld32(t0 + (h + 1) * kLcPart, v);
           send(h);
         }
       };
@@ -680,7 +685,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
           }
         } else {
           const CUtensorMap* tm = whole ? (dx ? &jx.tacc : &jw.tacc) : (dx ? &jx.tslots : &jw.tslots);
-          const int sc = whole ? col : c0, sr = whole ? row - lane : w.slot * kLcTile + row0;
+          const int sc = whole ? col : hf * half, sr = whole ? row - lane : w.slot * kLcTile + row0;
           const bool add = dx ? jx.acc_in : jw.acc_in;  // onto the sums of the pieces before
           each_part([&](int h) LC_INLINE {
 #pragma unroll
@@ -944,6 +949,16 @@ int split_of(int tiles, int nkb) {
   return s > tiles && waves * nkb - (int)(((int64_t)tiles * nkb + s - 1) / s) > 12 ? s : 0;
 }
 
+// Columns of a tile of logits: narrower where whole tiles would occupy half of
+// the pairs or fewer, as most of such a call is the epilogue's latency (6 x 80 x
+// 1024 22.1 -> 20.1 us, 2582 x 998 x 306 52 -> 49). Longer contractions are bound by
+// the ring's latency, a stage each, whatever its width (1 x 3246 x 6451: the
+// forward 20 us with 26 tiles, 26 with 51).
+int z_cols(int64_t N, int64_t cols, int64_t K) {
+  const int t = tiles_of(N) * tiles_of(cols);
+  return K > 1024 || 2 * t > kLcPairs ? kLcTile : 4 * t > kLcPairs ? kLcTile / 2 : kLcTile / 4;
+}
+
 // A whole tile's time in blocks: an MN-major B (see make_plan), its start and end.
 double tile_cost(int nkb, bool b_mn) { return nkb * (b_mn ? 1.38 : 1.0) + 2.0; }
 
@@ -965,6 +980,11 @@ struct LcPlan {
 // else few launches
 constexpr int64_t kLcPieceBytes = 256ll << 20, kLcPieceBytesL2 = 64ll << 20;
 
+int z_tiles(const dspark_lce_dims& d) {
+  const int n = z_cols(d.N, d.V, d.K);
+  return (d.V + n - 1) / n;
+}
+
 LcPlan make_plan(const dspark_lce_dims& d) {
   LcPlan p;
   memset(&p, 0, sizeof(p));
@@ -975,7 +995,7 @@ LcPlan make_plan(const dspark_lce_dims& d) {
     off += (size_t)up(bytes > 0 ? bytes : 1, 256);
     return o;
   };
-  p.part = carve(8 * N * 2 * tiles_of(V));
+  p.part = carve(8 * N * 2 * z_tiles(d));
   p.zt = carve(4 * N);
   p.fwd_total = off;
   int64_t most = (K < 1024 ? kLcPieceBytesL2 : kLcPieceBytes) / (2 * (N > 0 ? N : 1)) / kLcTile * kLcTile;
@@ -1062,7 +1082,8 @@ struct LcLaunch {
     for (int k = 0; k < kLcJobs; ++k) {
       LcJob& j = p.job[k];
       j.mt = tiles_of(j.M);
-      j.nt = tiles_of(j.Nn);
+      if (j.tn == 0) j.tn = kLcTile;
+      j.nt = (j.Nn + j.tn - 1) / j.tn;
       if (j.split == 0) tiles += j.mt * j.nt;
       p.tiles[k] = tiles;
       pairs = pairs > j.split ? pairs : j.split;
@@ -1108,9 +1129,10 @@ bool z_job(LcJob& j, const dspark_lce_dims* d, const void* X, const void* W, con
   j.target = target;
   j.V = d->V;
   j.gain = logit_gain(d->K);
+  j.tn = z_cols(d->N, cols, d->K);
   if (U && !encode_box(&j.tu, U, kBoxU, d->V, d->N, d->ldu)) return false;
   if (!encode(&j.ta, X, d->K, d->N, d->ldx, kLcHalf)) return false;
-  return d->layout == DSPARK_W_VK ? encode(&j.tb, W, d->K, d->V, d->ldw, kLcHalf)
+  return d->layout == DSPARK_W_VK ? encode(&j.tb, W, d->K, d->V, d->ldw, j.tn / 2)
                                   : encode(&j.tb, W, d->V, d->K, d->ldw, kLcKb);
 }
 
@@ -1191,7 +1213,7 @@ extern "C" dspark_status dspark_linear_ce(const dspark_lce_dims* d, const void* 
   cudaError_t e = l.run(st);
   if (e == cudaSuccess)
     e = launch_ex(k_lce_rows, dim3((d->N + kLcRowsCta - 1) / kLcRowsCta), dim3(32 * kLcRowsCta), 0, st,
-                  true, part, zt, target, d->N, 2 * tiles_of(d->V),
+                  true, part, zt, target, d->N, 2 * z_tiles(*d),
                   d->V, loss, lse);
   return lce_fail(e);
 }

@@ -156,6 +156,19 @@ def test_long_products(N, K, V, U, pad, ignored, layout):
     _check(X, W, Um, t, wt, 0.25, layout)
 
 
+@pytest.mark.parametrize("layout", ["vk", "kv"])
+@pytest.mark.parametrize("N,K,V,U", [
+    (9, 200, 4800, True),                       # logits in tiles of 64 columns,
+    (300, 130, 2561, True), (20, 72, 9473, False),   # of 128,
+    (300, 130, 5121, True), (20, 72, 9729, False),   # of 256
+    (33, 1025, 1100, True),                     # few tiles of a longer contraction
+    (130, 260, 40001, False),                   # dX on some of the pairs, dW on the others
+])
+def test_widths_of_tiles(N, K, V, U, layout):
+    X, W, Um, t, wt = _inputs(N, K, V, layout, U, 0, 0.1)
+    _check(X, W, Um, t, wt, 1.0, layout)
+
+
 @pytest.mark.parametrize("dx,dw", [(True, False), (False, True)])
 @pytest.mark.parametrize("layout", ["vk", "kv"])
 def test_one_gradient_alone(dx, dw, layout):
