@@ -977,8 +977,11 @@ struct LcPlan {
 
 // G's piece: small enough to stay in L2 where the products are short (K below
 // 1024: its 6 bytes of traffic a value take as long as 6 K operations at K = 265),
-// else few launches
-constexpr int64_t kLcPieceBytes = 256ll << 20, kLcPieceBytesL2 = 64ll << 20;
+// else few launches. At least 64 tiles wide where a GiB allows: narrower pieces
+// have too few tiles of dW (K = 256, V = 129280: N = 4096 976 us in pieces of 32
+// tiles, 736 of 64; N = 16384 3.94 ms of 8, 2.84 of 64, 2.71 of 128).
+constexpr int64_t kLcPieceBytes = 256ll << 20, kLcPieceBytesL2 = 64ll << 20, kLcPieceMost = 1ll << 30;
+constexpr int64_t kLcPieceCols = 64 * kLcTile;
 
 int z_tiles(const dspark_lce_dims& d) {
   const int n = z_cols(d.N, d.V, d.K);
@@ -998,7 +1001,9 @@ LcPlan make_plan(const dspark_lce_dims& d) {
   p.part = carve(8 * N * 2 * z_tiles(d));
   p.zt = carve(4 * N);
   p.fwd_total = off;
-  int64_t most = (K < 1024 ? kLcPieceBytesL2 : kLcPieceBytes) / (2 * (N > 0 ? N : 1)) / kLcTile * kLcTile;
+  const int64_t row = 2 * (N > 0 ? N : 1), wide = kLcPieceMost / row < kLcPieceCols ? kLcPieceMost / row : kLcPieceCols;
+  int64_t most = (K < 1024 ? kLcPieceBytesL2 : kLcPieceBytes) / row;
+  most = (most < wide ? wide : most) / kLcTile * kLcTile;
   most = most < 2048 ? 2048 : most;
   p.pieces = (int)((V + most - 1) / most);
   p.piece = (int)up((V + p.pieces - 1) / p.pieces, kLcTile);

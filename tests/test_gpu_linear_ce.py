@@ -145,6 +145,13 @@ def test_vocabulary_in_pieces():
 
 
 @pytest.mark.parametrize("layout", ["vk", "kv"])
+def test_whole_tiles_summed_over_pieces(layout):
+    """dX has tiles for most of the grid, so that each is summed in place from piece to piece."""
+    X, W, U, t, wt = _inputs(4100, 1000, 40003, layout, False, 0, 0.1)
+    _check(X, W, U, t, wt, 1.0, layout)
+
+
+@pytest.mark.parametrize("layout", ["vk", "kv"])
 @pytest.mark.parametrize("N,K,V,U,pad,ignored", [
     (1500, 1001, 7003, False, 0, 0.1),     # ragged in every size, parts of tiles shared by pairs of CTAs
     (1030, 1300, 9000, True, 8, 0.0),
