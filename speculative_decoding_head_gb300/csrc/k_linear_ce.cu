@@ -16,7 +16,7 @@
 // All four products run in one kernel: 256 x 256 tiles on CTA pairs (tcgen05
 // cta_group::2; each CTA holds 128 of the tile's rows and loads 128 of its
 // columns, 32 KB per 64-deep stage instead of the 48 KB of a 128 x 256 tile
-// per CTA), TMA into a six-stage ring, two accumulators so that the epilogue
+// per CTA), TMA into a ring of four to ten stages, two accumulators so that the epilogue
 // of a tile runs under the next tile's products. An operand whose contraction
 // index is its row (W in dX, G in dW) is read in place as an MN-major operand;
 // only X is transposed in memory, once, for a long dW (the reason is at
@@ -57,7 +57,7 @@ constexpr int kLcTile = 256;     // rows and columns of a pair's tile
 constexpr int kLcHalf = 128;     // rows (A) and columns (B) one CTA loads
 constexpr int kLcKb = 64;        // contraction depth of a stage (one 128-byte swizzled row)
 constexpr int kLcOpBytes = kLcHalf * kLcKb * 2;   // 16 KB: one operand's half of a stage
-constexpr int kLcStageBytes = 2 * kLcOpBytes;
+constexpr int kLcStageBytes = 2 * kLcOpBytes;  // less with narrow tiles of logits
 constexpr int kLcBox = 64 * kLcKb * 2;            // 8 KB: a 64 x 64 box of an MN-major operand
 // Epilogue warps: two groups that take tiles in turn (one accumulator each), so
 // that one's latencies lie under the other's arithmetic; in a group two warps
@@ -71,15 +71,17 @@ constexpr int kLcTmemCols = 512;                  // two accumulators of 256 col
 // Shared memory: the operand ring and, from its end, boxes of the epilogue
 // warps: 32 rows of 32 fp32 columns of U (4 KB) with U, 32 rows of 64 bytes of
 // output (2 KB) in the gradient.
-constexpr int kLcMaxStages = 6;
+constexpr int kLcMaxStages = 10;
 constexpr int kLcUBox = 32 * kLcPart * 4;
 constexpr int kLcOBox = 32 * 64;
 constexpr int kLcRing = 224 * 1024;
-__host__ __device__ constexpr int lc_stages(bool grad, bool u) { return !u ? 6 : grad ? 4 : 5; }
-static_assert(lc_stages(true, false) * kLcStageBytes + kLcEpiWarps * kLcOBox <= kLcRing, "gradient");
-static_assert(lc_stages(true, true) * kLcStageBytes + kLcEpiWarps * (kLcOBox + kLcUBox) <= kLcRing, "gradient, U");
-static_assert(lc_stages(false, true) * kLcStageBytes + kLcEpiWarps * kLcUBox <= kLcRing, "U");
-constexpr int kLcAhead = 16;                      // tiles announced: the producer is at most 6 + 2 + 2 ahead
+__host__ __device__ constexpr int lc_stages(bool grad, bool u, int stage_bytes) {
+  const int n = (kLcRing - (grad ? kLcEpiWarps * kLcOBox : 0) - (u ? kLcEpiWarps * kLcUBox : 0)) / stage_bytes;
+  const int most = stage_bytes < kLcStageBytes ? kLcMaxStages : 6;  // seven whole ones: 160 x 1024 x 32000 18.8 -> 19.2 us
+  return n < most ? n : most;
+}
+static_assert(lc_stages(true, true, kLcStageBytes) >= 4, "a ring of four stages at least");
+constexpr int kLcAhead = 16;                      // tiles announced: the producer is at most 10 + 2 + 2 ahead
 constexpr int kLcBars = 2 * kLcMaxStages + 5 + kLcEpiWarps + kLcAhead + 1;
 constexpr int kLcBarBytes = 16 * kLcAhead + 8 * kLcBars + 16;
 static_assert(kLcBars % 2 == 0, "16-byte ring entries");
@@ -128,7 +130,7 @@ struct LcParams {
   LcJob job[kLcJobs];
   int tiles[kLcJobs];   // whole tiles of jobs 0 .. i (running totals; split jobs add none)
   int sharing, rounds;  // the first `sharing` pairs take whole tiles from round `rounds` on
-  int stages;
+  int stages, stage_bytes;
   int* status;
 };
 
@@ -217,9 +219,12 @@ __device__ __forceinline__ int lc_cols(int Nn, int n, int tn) { return min(tn, (
 // ring position and the parity of its pass
 struct LcRing {
   int s, ph;
-  __device__ __forceinline__ void step(int stages) {
+  uint32_t at;  // the stage's address
+  __device__ __forceinline__ void step(int stages, int bytes, uint32_t base) {
+    at += bytes;
     if (++s == stages) {
       s = 0;
+      at = base;
       ph ^= 1;
     }
   }
@@ -249,20 +254,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
   const uint32_t rank = tc::cluster_ctarank();
   const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
 
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < kLcMaxStages; ++s) {
-      tc::mbar_init(full(s), 1);
-      tc::mbar_init(empty(s), 1);
-    }
-    for (int b = 0; b < 2; ++b) {
-      tc::mbar_init(tfull(b), 1);
-      tc::mbar_init(tempty(b), 2 * kLcGroupWarps);  // both CTAs' warps of a group, on the even CTA
-    }
-    tc::mbar_init(drain, 1);
-    for (int w = 0; w < kLcEpiWarps; ++w) tc::mbar_init(ufull(w), 1);
-    for (int i = 0; i < kLcAhead; ++i) tc::mbar_init(told(i), 1);
-    *abort = 0;
+  if (warp == 0) {
+    // one arrival each; the even CTA's tempty: both CTAs' warps of a group
+    for (int i = lane; i < kLcBars; i += 32)
+      tc::mbar_init(bars + 8u * i, (i >> 1) == kLcMaxStages + 1 ? 2 * kLcGroupWarps : 1);
     tc::fence_barrier_init();
+  }
+  if (threadIdx.x == 0) {
+    *abort = 0;
     for (int k = 0; k < kLcJobs; ++k) {
       if (p.job[k].mt == 0) continue;
       tc::prefetch_tmap(&p.job[k].ta);
@@ -285,7 +284,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
-      LcRing r{0, 0};
+      LcRing r{0, 0, sbase};
       int iss = 0;
       bool ok = true;
       LcWork w;
@@ -313,7 +312,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
           if (!ok) break;
           const uint32_t bar = tc::map_rank(full(r.s), 0);
           if (rank == 0) tc::mbar_arrive_expect_tx(full(r.s), 2 * bytes);  // both CTAs' copies
-          const uint32_t da = sbase + r.s * kLcStageBytes, db = da + kLcOpBytes;
+          const uint32_t da = r.at, db = da + kLcOpBytes;
           const int ka = kb * kLcKb, kbn = b_k0 + kb * kLcKb;
           if (a_mn) {
             tc::tma_load_2d_pair(da, &j.ta, am, ka, bar);
@@ -326,7 +325,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
           } else {
             tc::tma_load_2d_pair(db, &j.tb, kbn, bn, bar);
           }
-          r.step(p.stages);
+          r.step(p.stages, p.stage_bytes, sbase);
           ++iss;
         }
       }
@@ -350,7 +349,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0 && rank == 0) {
       bool ok = true;
-      LcRing r{0, 0};
+      LcRing r{0, 0, sbase};
       int tj = 0;
       for (;; ++tj) {
         ok = tc::mbar_wait(told(tj), (tj / kLcAhead) & 1, abort);
@@ -371,13 +370,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
           ok = tc::mbar_wait(full(r.s), r.ph, abort);
           if (!ok) break;
           tc::tc_fence_after();
-          const uint32_t da = sbase + r.s * kLcStageBytes, db = da + kLcOpBytes;
+          const uint32_t da = r.at, db = da + kLcOpBytes;
 #pragma unroll
           for (int kk = 0; kk < kLcKb / 16; ++kk)
             tc::mma_bf16_pair(d, tc::smem_desc(da + kk * a_step, a_lbo, 1024),
                               tc::smem_desc(db + kk * b_step, b_lbo, 1024), idesc, (kb > 0 || kk > 0) ? 1u : 0u);
           tc::mma_commit_pair(empty(r.s));
-          r.step(p.stages);
+          r.step(p.stages, p.stage_bytes, sbase);
         }
         if (!ok) break;
         tc::mma_commit_pair(tfull(ab));
@@ -950,13 +949,14 @@ int split_of(int tiles, int nkb) {
 }
 
 // Columns of a tile of logits: narrower where whole tiles would occupy half of
-// the pairs or fewer, as most of such a call is the epilogue's latency (6 x 80 x
-// 1024 22.1 -> 20.1 us, 2582 x 998 x 306 52 -> 49). Longer contractions are bound by
-// the ring's latency, a stage each, whatever its width (1 x 3246 x 6451: the
-// forward 20 us with 26 tiles, 26 with 51).
-int z_cols(int64_t N, int64_t cols, int64_t K) {
+// the pairs or fewer. A short contraction's time is mostly the epilogue's latency
+// (6 x 80 x 1024: step 22.1 -> 20.1 us), a long one's the operands', of which the
+// ring then holds more stages (234 x 5036 x 846 with U, 4 tiles: gradient of X 58 ->
+// 48 us; 64 x 4096 x 8000, 32 tiles: forward 33.4 -> 31.4, both with 12 us around
+// them; 1 x 3246 x 6451, 26 tiles, loses 3).
+int z_cols(int64_t N, int64_t cols) {
   const int t = tiles_of(N) * tiles_of(cols);
-  return K > 1024 || 2 * t > kLcPairs ? kLcTile : 4 * t > kLcPairs ? kLcTile / 2 : kLcTile / 4;
+  return 2 * t > kLcPairs ? kLcTile : 4 * t > kLcPairs ? kLcTile / 2 : kLcTile / 4;
 }
 
 // A whole tile's time in blocks: an MN-major B (see make_plan), its start and end.
@@ -984,7 +984,7 @@ constexpr int64_t kLcPieceBytes = 256ll << 20, kLcPieceBytesL2 = 64ll << 20, kLc
 constexpr int64_t kLcPieceCols = 64 * kLcTile;
 
 int z_tiles(const dspark_lce_dims& d) {
-  const int n = z_cols(d.N, d.V, d.K);
+  const int n = z_cols(d.N, d.V);
   return (d.V + n - 1) / n;
 }
 
@@ -1073,7 +1073,6 @@ struct LcLaunch {
   LcLaunch(bool grad, int* status) : grad(grad), any(false) {
     memset(&p, 0, sizeof(p));
     p.status = status;
-    p.stages = lc_stages(grad, false);
   }
   LcJob& add(int place) {
     any = true;
@@ -1084,6 +1083,7 @@ struct LcLaunch {
     cudaError_t e = lce_configure();
     if (e != cudaSuccess) return e;
     int pairs = 0, tiles = 0;
+    bool u = false;
     for (int k = 0; k < kLcJobs; ++k) {
       LcJob& j = p.job[k];
       j.mt = tiles_of(j.M);
@@ -1092,8 +1092,11 @@ struct LcLaunch {
       if (j.split == 0) tiles += j.mt * j.nt;
       p.tiles[k] = tiles;
       pairs = pairs > j.split ? pairs : j.split;
-      if (j.has_u) p.stages = lc_stages(grad, true);
+      const int b_bytes = j.b_mn ? (j.tn / 2 + 63) / 64 * kLcBox : j.tn * kLcKb;
+      if (j.mt > 0 && p.stage_bytes < kLcOpBytes + b_bytes) p.stage_bytes = kLcOpBytes + b_bytes;
+      u = u || j.has_u;
     }
+    p.stages = lc_stages(grad, u, p.stage_bytes);
     pairs = pairs > tiles ? pairs : tiles;
     pairs = pairs < kLcPairs ? pairs : kLcPairs;
     // rounds of whole tiles that the other pairs do during one of dX's shares
@@ -1134,7 +1137,7 @@ bool z_job(LcJob& j, const dspark_lce_dims* d, const void* X, const void* W, con
   j.target = target;
   j.V = d->V;
   j.gain = logit_gain(d->K);
-  j.tn = z_cols(d->N, cols, d->K);
+  j.tn = z_cols(d->N, cols);
   if (U && !encode_box(&j.tu, U, kBoxU, d->V, d->N, d->ldu)) return false;
   if (!encode(&j.ta, X, d->K, d->N, d->ldx, kLcHalf)) return false;
   return d->layout == DSPARK_W_VK ? encode(&j.tb, W, d->K, d->V, d->ldw, j.tn / 2)
