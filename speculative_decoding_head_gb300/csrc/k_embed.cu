@@ -3,7 +3,7 @@
 //   out[n] = s E[idx_n],   dE[v] = base[v] + s sum_{n: idx_n = v} dout[n]
 //
 // The lookup moves each row once: a warp takes 4 rows and one or two spans of 256
-// columns at a time, its loads in flight together. 16384 rows of 5120 bf16: 43 us,
+// columns at a time (more rows where they are short), its loads in flight together. 16384 rows of 5120 bf16: 43 us,
 // 81% of the measured copy rate (one span a warp: 59 us); small calls are one
 // launch's latency (4.2 us on the device).
 //
@@ -46,12 +46,13 @@ struct Num<__nv_bfloat16> {
 };
 
 // Eight values of a row per lane. Rows on 16 bytes: columns c .. c + 7 with
-// c = 8 lane, whole 16-byte pieces; others: columns lane + 32 i, one by one.
-template <typename T, bool VEC>
+// c = 8 lane, whole 16-byte pieces; others: columns lane + LANES i, one by one
+// (LANES lanes to a row).
+template <typename T, bool VEC, int LANES = 32>
 __device__ __forceinline__ int col_of(int lane, int i) {
-  return VEC ? lane * 8 + i : lane + 32 * i;
+  return VEC ? lane * 8 + i : lane + LANES * i;
 }
-template <typename T, bool VEC>
+template <typename T, bool VEC, int LANES = 32>
 __device__ __forceinline__ void load8(const T* row, int lane, int left, T* v) {
   if (VEC && lane * 8 + 8 <= left) {
     const uint4* p = reinterpret_cast<const uint4*>(row + lane * 8);
@@ -61,12 +62,12 @@ __device__ __forceinline__ void load8(const T* row, int lane, int left, T* v) {
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int c = col_of<T, VEC>(lane, i);
+      const int c = col_of<T, VEC, LANES>(lane, i);
       v[i] = c < left ? row[c] : Num<T>::down(0.f);
     }
   }
 }
-template <typename T, bool VEC>
+template <typename T, bool VEC, int LANES = 32>
 __device__ __forceinline__ void store8(T* row, int lane, int left, const T* v) {
   if (VEC && lane * 8 + 8 <= left) {
     uint4* p = reinterpret_cast<uint4*>(row + lane * 8);
@@ -76,33 +77,39 @@ __device__ __forceinline__ void store8(T* row, int lane, int left, const T* v) {
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int c = col_of<T, VEC>(lane, i);
+      const int c = col_of<T, VEC, LANES>(lane, i);
       if (c < left) row[c] = v[i];
     }
   }
 }
 
 constexpr int kEmSpan = 256;     // columns a warp covers at a time
-constexpr int kEmRows = 4;       // rows a warp of the lookup has in flight
+constexpr int kEmRows = 4;       // rows a lane of the lookup has in flight
 
 // ---------------------------------------------------------------- lookup
-// CH spans of 256 columns of four rows per warp, all loads in flight together.
-template <typename T, bool VEC, int CH>
+// LANES lanes to a row: CH spans of 8 LANES columns of four rows each, all loads
+// in flight together. Fewer than 32 lanes where rows are short and many (192139
+// rows, 32 lanes and as chosen: 9 bf16 27.1 and 5.9 us, 64 bf16 31.7 and 6.8, 128
+// bf16 31.7 and 11.7; 4000 rows of 16 fp32: 2.2 with 32 lanes, 3.1 with two).
+constexpr int kEmMany = 8192;
+template <typename T, bool VEC, int CH, int LANES>
 __global__ void __launch_bounds__(256)
     k_embed(const T* __restrict__ E, int64_t lde, int V, int D, const int32_t* __restrict__ idx, int N, float scale,
             T* __restrict__ out, int64_t ldo, int* status) {
-  constexpr int kCols = CH * kEmSpan;
-  const int lane = threadIdx.x & 31;
+  constexpr int kSpan = 8 * LANES, kCols = CH * kSpan;
+  const int lane = threadIdx.x & (LANES - 1);
   const int spans = (D + kCols - 1) / kCols, groups = (N + kEmRows - 1) / kEmRows;
-  const int64_t t = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int64_t t = (int64_t)blockIdx.x * (256 / LANES) + threadIdx.x / LANES;
   pdl_wait();
   if (t >= (int64_t)spans * groups) return;
+  // a group's rows lie `stride` apart, so that the groups of a warp read and write rows side by side
   const int g = (int)(t / spans), c0 = (int)(t - (int64_t)g * spans) * kCols, left = D - c0;
+  const int stride = LANES < 32 ? groups : 1, n0 = LANES < 32 ? g : g * kEmRows;
   __align__(16) T v[kEmRows][CH][8];
   int id[kEmRows];
 #pragma unroll
   for (int r = 0; r < kEmRows; ++r) {
-    const int n = g * kEmRows + r;
+    const int n = n0 + r * stride;
     id[r] = n < N ? idx[n] : -1;
     if (id[r] < -1 || id[r] >= V) {
       if (lane == 0) raise_status(status, DSPARK_ERANGE);
@@ -114,7 +121,7 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
     for (int h = 0; h < CH; ++h) {
       if (id[r] >= 0) {
-        load8<T, VEC>(E + id[r] * lde + c0 + h * kEmSpan, lane, left - h * kEmSpan, v[r][h]);
+        load8<T, VEC, LANES>(E + id[r] * lde + c0 + h * kSpan, lane, left - h * kSpan, v[r][h]);
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[r][h][i] = Num<T>::down(0.f);
@@ -122,27 +129,38 @@ __global__ void __launch_bounds__(256)
     }
 #pragma unroll
   for (int r = 0; r < kEmRows; ++r) {
-    const int n = g * kEmRows + r;
+    const int n = n0 + r * stride;
     if (n >= N) break;
 #pragma unroll
     for (int h = 0; h < CH; ++h) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[r][h][i] = Num<T>::down(id[r] >= 0 ? scale * Num<T>::up(v[r][h][i]) : 0.f);
-      store8<T, VEC>(out + n * ldo + c0 + h * kEmSpan, lane, left - h * kEmSpan, v[r][h]);
+      store8<T, VEC, LANES>(out + n * ldo + c0 + h * kSpan, lane, left - h * kSpan, v[r][h]);
     }
   }
 }
 
+template <typename T, bool VEC, int CH, int LANES>
+cudaError_t em_lookup_as(const void* E, int64_t lde, int V, int D, const int32_t* idx, int N, float scale, void* out,
+                         int64_t ldo, int* status, cudaStream_t st) {
+  const int64_t groups = (int64_t)((N + kEmRows - 1) / kEmRows) * ((D + 8 * LANES * CH - 1) / (8 * LANES * CH));
+  return launch_ex(k_embed<T, VEC, CH, LANES>, dim3((unsigned)((groups * LANES + 255) / 256)), dim3(256), 0, st, true,
+                   static_cast<const T*>(E), lde, V, D, idx, N, scale, static_cast<T*>(out), ldo, status);
+}
+template <typename T, bool VEC>
+cudaError_t em_lookup_v(const void* E, int64_t lde, int V, int D, const int32_t* idx, int N, float scale, void* out,
+                        int64_t ldo, int* status, cudaStream_t st) {
+  const auto f = D > kEmSpan && sizeof(T) == 2 ? em_lookup_as<T, VEC, 2, 32>
+                 : D > 128 || N < kEmMany      ? em_lookup_as<T, VEC, 1, 32>
+                 : D > 64                      ? em_lookup_as<T, VEC, 1, 16>
+                 : D > 16                      ? em_lookup_as<T, VEC, 1, 4>
+                                               : em_lookup_as<T, VEC, 1, 2>;
+  return f(E, lde, V, D, idx, N, scale, out, ldo, status, st);
+}
 template <typename T>
 cudaError_t em_lookup(bool vec, const void* E, int64_t lde, int V, int D, const int32_t* idx, int N, float scale,
                       void* out, int64_t ldo, int* status, cudaStream_t st) {
-  const bool wide = D > kEmSpan && sizeof(T) == 2;
-  const int cols = wide ? 2 * kEmSpan : kEmSpan;
-  const int64_t warps = (int64_t)((N + kEmRows - 1) / kEmRows) * ((D + cols - 1) / cols);
-  void (*k)(const T*, int64_t, int, int, const int32_t*, int, float, T*, int64_t, int*) =
-      wide ? (vec ? k_embed<T, true, 2> : k_embed<T, false, 2>) : (vec ? k_embed<T, true, 1> : k_embed<T, false, 1>);
-  return launch_ex(k, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, st, true, static_cast<const T*>(E), lde, V, D,
-                   idx, N, scale, static_cast<T*>(out), ldo, status);
+  return (vec ? em_lookup_v<T, true> : em_lookup_v<T, false>)(E, lde, V, D, idx, N, scale, out, ldo, status, st);
 }
 
 // ---------------------------------------------------------------- sort

@@ -57,6 +57,23 @@ def test_lookup(dtype, N, V, D, lde, ldo, shift):
     assert (full[:shift] == 5.0).all() and (full[shift:].view(N, ldo)[:, D:] == 5.0).all()
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("N", [8191, 8193, 20002])
+@pytest.mark.parametrize("D,ld,shift", [(1, 1, 0), (9, 11, 1), (16, 16, 0), (17, 24, 8), (64, 64, 0), (65, 65, 0),
+                                        (128, 128, 0), (129, 136, 0)])
+def test_lookup_of_many_short_rows(dtype, N, D, ld, shift):
+    g = _gen(N + D)
+    E = _mat(700, D, ld, dtype, g, shift)
+    idx = torch.randint(-1, 700, (N,), generator=g, device="cuda", dtype=torch.int32)
+    full = torch.full((N * ld + shift,), 5.0, dtype=dtype, device="cuda")
+    op = Embedding(N, 700, D)
+    got = op.lookup(E, idx, scale=0.5, out=full[shift:].view(N, ld)[:, :D])
+    assert op.device_status() == 0
+    # a product with 0.5 is exact
+    assert torch.equal(got, torch.where((idx >= 0)[:, None], E[idx.clamp(min=0).long()] * 0.5, 0.0))
+    assert (full[:shift] == 5.0).all() and (full[shift:].view(N, ld)[:, D:] == 5.0).all()
+
+
 def _grad_ref(dout, idx, V, scale, base):
     D = dout.shape[1]
     ref = torch.zeros(V, D, dtype=F64, device="cuda")
