@@ -1097,11 +1097,15 @@ struct LcLaunch {
       u = u || j.has_u;
     }
     p.stages = lc_stages(grad, u, p.stage_bytes);
+    // dX's shares and the others' whole tiles on pairs of their own (gradient of 706 x
+    // 1038 x 1415: 38.5 -> 32.4 us; of 100 x 1024 x 3000 30.3 -> 32.4)
+    const LcJob& x = p.job[kLcDx];
+    const bool apart = x.split > 0 && p.job[kLcDw].split == 0;
     pairs = pairs > tiles ? pairs : tiles;
+    if (apart && pairs < x.split + tiles) pairs = x.split + tiles;
     pairs = pairs < kLcPairs ? pairs : kLcPairs;
     // rounds of whole tiles that the other pairs do during one of dX's shares
-    const LcJob& x = p.job[kLcDx];
-    if (x.split > 0 && x.split < pairs && p.job[kLcDw].split == 0) {
+    if (apart && x.split < pairs) {
       const int others = pairs - x.split;
       double left = (double)x.mt * x.nt * x.nkb / x.split;
       p.sharing = x.split;
