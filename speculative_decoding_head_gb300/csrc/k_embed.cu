@@ -171,6 +171,7 @@ constexpr int kSoBins = 1 << kSoBits;
 constexpr int kSoKeys = 4;                              // pairs a thread holds
 constexpr int kSoTile = kSoThreads * kSoKeys;           // 4096 pairs a CTA holds at a time
 constexpr int kSoCtas = 128;
+constexpr int kSoAhead = 32;                            // counts of other CTAs a thread has on their way
 constexpr size_t kSoSmem = sizeof(int) * (size_t)kSoWarps * kSoBins;
 
 // One pass's input: the tokens themselves (rows without one are left out) or
@@ -332,31 +333,41 @@ __global__ void __launch_bounds__(kSoThreads) k_sort_place(SoPass q) {
   pdl_wait();
   const int n = so_n(q), a = min(n, (int)blockIdx.x * q.per), b = min(n, a + q.per);
   SoKeys<kSoKeys> k;
-  so_load(q, a, b, k);  // on their way while the counts are added up
-  // a digit's counts of all CTAs: kSoThreads / bins threads share them
+  so_load(q, a, b, k);
+  // a digit's counts of all CTAs: kSoThreads / bins threads share them; the first
+  // ones are on their way while the first tile is counted
+  const int digit = threadIdx.x & (q.bins - 1), share = kSoThreads / q.bins;
+  const int span = ((int)gridDim.x + share - 1) / share, i0 = threadIdx.x / q.bins * span;
+  const int i1 = min((int)gridDim.x, i0 + span);
+  const int* c = q.cta + digit;
+  int x[kSoAhead];
+#pragma unroll
+  for (int i = 0; i < kSoAhead; ++i) x[i] = i0 + i < i1 ? c[(i0 + i) * q.bins] : 0;
   for (int d = threadIdx.x; d < q.bins; d += kSoThreads) tot[d] = mine[d] = 0;
-  __syncthreads();
-  {
-    const int d = threadIdx.x & (q.bins - 1), share = kSoThreads / q.bins, g = threadIdx.x / q.bins;
-    const int per = ((int)gridDim.x + share - 1) / share, i0 = g * per, i1 = min((int)gridDim.x, i0 + per);
-    int s = 0, before = 0;
-    const int* c = q.cta + d;
-#pragma unroll 16
-    for (int i = i0; i < i1; ++i) {
-      const int x = c[i * q.bins];
-      before += i < (int)blockIdx.x ? x : 0;
-      s += x;
-    }
-    atomicAdd(&tot[d], s);
-    atomicAdd(&mine[d], before);
+  so_count(k, so_hist, q.bins);
+  int s = 0, before = 0;
+#pragma unroll
+  for (int i = 0; i < kSoAhead; ++i) {
+    before += i0 + i < (int)blockIdx.x ? x[i] : 0;
+    s += x[i];
   }
+#pragma unroll 16
+  for (int i = i0 + kSoAhead; i < i1; ++i) {
+    const int y = c[i * q.bins];
+    before += i < (int)blockIdx.x ? y : 0;
+    s += y;
+  }
+  atomicAdd(&tot[digit], s);
+  atomicAdd(&mine[digit], before);
   __syncthreads();
   const int all = so_scan(tot, q.bins, wsum);
   for (int d = threadIdx.x; d < q.bins; d += kSoThreads) mine[d] += tot[d];
   if (q.idx && blockIdx.x == 0 && threadIdx.x == 0) *q.total = all;
   for (int t = a; t < b; t += kSoTile) {
-    if (t > a) so_load(q, t, b, k);
-    so_count(k, so_hist, q.bins);
+    if (t > a) {
+      so_load(q, t, b, k);
+      so_count(k, so_hist, q.bins);
+    }
     so_offsets(so_hist, q.bins, mine);
     so_place(q, k, so_hist);
     __syncthreads();
