@@ -17,8 +17,8 @@
 // crosses CTAs leaves fp32 partial sums that the last kernel adds in order. That
 // kernel also writes the rows of the tokens that do not occur.
 //
-// 262144 rows of 256 bf16 into V = 129280: 68 us, 2.45 times the floor of its
-// bytes: 24 us of sort (four launches, each a chain of latencies: load, count,
+// 262144 rows of 256 bf16 into V = 129280: 66.5 us, 2.4 times the floor of its
+// bytes: 22 us of sort (four launches, each a chain of latencies: load, count,
 // add up, place), 32 us of sums (512-byte rows in random order, 4.7 TB/s) and
 // 12 us of joins and absent rows.
 #include <math.h>
@@ -168,8 +168,6 @@ constexpr int kSoThreads = 1024;
 constexpr int kSoWarps = kSoThreads / 32;
 constexpr int kSoBits = 10;
 constexpr int kSoBins = 1 << kSoBits;
-constexpr int kSoKeys = 4;                              // pairs a thread holds
-constexpr int kSoTile = kSoThreads * kSoKeys;           // 4096 pairs a CTA holds at a time
 constexpr int kSoCtas = 128;
 constexpr int kSoAhead = 32;                            // counts of other CTAs a thread has on their way
 constexpr size_t kSoSmem = sizeof(int) * (size_t)kSoWarps * kSoBins;
@@ -181,7 +179,7 @@ struct SoPass {
   const int2* pairs;    // (token, row)
   int N, V;
   int shift, bins;
-  int per;              // pairs of a CTA (a multiple of kSoTile)
+  int per;              // pairs of a CTA (whole tiles of kSoThreads * KEYS)
   int* cta;             // [CTAs][bins] counts
   int2* out;            // pairs, or null in the last pass:
   int32_t* rows;        // [N] sorted rows
@@ -306,6 +304,7 @@ __device__ __forceinline__ void so_offsets(int* hist, int bins, int* base) {
 
 __device__ __forceinline__ int so_n(const SoPass& q) { return q.idx ? q.N : *q.total; }
 
+template <int KEYS>
 __global__ void __launch_bounds__(kSoThreads) k_sort_count(SoPass q) {
   extern __shared__ int so_hist[];
   pdl_wait();
@@ -315,11 +314,11 @@ __global__ void __launch_bounds__(kSoThreads) k_sort_count(SoPass q) {
   const int n = so_n(q), a = min(n, (int)blockIdx.x * q.per), b = min(n, a + q.per);
   for (int i = threadIdx.x; i < q.bins; i += kSoThreads) so_hist[i] = 0;
   __syncthreads();
-  for (int t = a; t < b; t += kSoTile) {
-    SoKeys<kSoKeys> k;
+  for (int t = a; t < b; t += kSoThreads * KEYS) {
+    SoKeys<KEYS> k;
     so_load(q, t, b, k);
 #pragma unroll
-    for (int i = 0; i < kSoKeys; ++i)
+    for (int i = 0; i < KEYS; ++i)
       if (k.d[i] >= 0) atomicAdd(so_hist + k.d[i], 1);
     if (q.idx) so_check(q, k);
   }
@@ -327,12 +326,13 @@ __global__ void __launch_bounds__(kSoThreads) k_sort_count(SoPass q) {
   for (int d = threadIdx.x; d < q.bins; d += kSoThreads) q.cta[blockIdx.x * q.bins + d] = so_hist[d];
 }
 
+template <int KEYS>
 __global__ void __launch_bounds__(kSoThreads) k_sort_place(SoPass q) {
   extern __shared__ int so_hist[];
   __shared__ int tot[kSoBins], mine[kSoBins], wsum[kSoWarps];
   pdl_wait();
   const int n = so_n(q), a = min(n, (int)blockIdx.x * q.per), b = min(n, a + q.per);
-  SoKeys<kSoKeys> k;
+  SoKeys<KEYS> k;
   so_load(q, a, b, k);
   // a digit's counts of all CTAs: kSoThreads / bins threads share them; the first
   // ones are on their way while the first tile is counted
@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(kSoThreads) k_sort_place(SoPass q) {
   const int all = so_scan(tot, q.bins, wsum);
   for (int d = threadIdx.x; d < q.bins; d += kSoThreads) mine[d] += tot[d];
   if (q.idx && blockIdx.x == 0 && threadIdx.x == 0) *q.total = all;
-  for (int t = a; t < b; t += kSoTile) {
+  for (int t = a; t < b; t += kSoThreads * KEYS) {
     if (t > a) {
       so_load(q, t, b, k);
       so_count(k, so_hist, q.bins);
@@ -832,13 +832,13 @@ dspark_status em_fail(cudaError_t e) {
 cudaError_t em_sort(const int32_t* idx, int N, int V, char* base, const EmScratch& s, int* status, cudaStream_t st) {
   static bool configured = false;
   if (!configured) {
-    cudaError_t e = cudaFuncSetAttribute(k_sort_count, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSoSmem);
+    cudaError_t e = cudaFuncSetAttribute(k_sort_place<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSoSmem);
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(k_sort_place, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSoSmem);
+      e = cudaFuncSetAttribute(k_sort_place<4>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSoSmem);
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(k_sort_cluster<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSoSmem);
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(k_sort_cluster<kSoKeys>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSoSmem);
+      e = cudaFuncSetAttribute(k_sort_cluster<4>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSoSmem);
     if (e != cudaSuccess) return e;
     configured = true;
   }
@@ -846,7 +846,7 @@ cudaError_t em_sort(const int32_t* idx, int N, int V, char* base, const EmScratc
   while (width < 24 && (1 << width) < V) ++width;
   const int passes = (width + kSoBits - 1) / kSoBits, bits = (width + passes - 1) / passes;
   int2* buf[2] = {reinterpret_cast<int2*>(base + s.bufa), reinterpret_cast<int2*>(base + s.bufb)};
-  SoPass q;
+  SoPass q = {};
   q.idx = idx;
   q.pairs = nullptr;
   q.N = N;
@@ -860,24 +860,26 @@ cudaError_t em_sort(const int32_t* idx, int N, int V, char* base, const EmScratc
   q.seen = reinterpret_cast<unsigned char*>(base + s.seen);
   q.status = status;
   q.out = nullptr;
-  q.per = kSoTile;
   const size_t smem = sizeof(int) * (size_t)kSoWarps * q.bins;
-  if (N <= kScCtas * kSoTile) {
+  if (N <= kScCtas * 4 * kSoThreads) {
     const ScArgs a{q, passes, bits, {buf[0], buf[1]}};
-    return launch_ex(N <= kScCtas * kSoThreads ? k_sort_cluster<1> : k_sort_cluster<kSoKeys>, dim3(kScCtas),
+    return launch_ex(N <= kScCtas * kSoThreads ? k_sort_cluster<1> : k_sort_cluster<4>, dim3(kScCtas),
                      dim3(kSoThreads), smem, st, true, a);
   }
-  int ctas = (N + kSoTile - 1) / kSoTile;
-  if (ctas > kSoCtas) {
-    q.per = (((N + kSoCtas - 1) / kSoCtas) + kSoTile - 1) / kSoTile * kSoTile;
-    ctas = (N + q.per - 1) / q.per;
-  }
+  // two pairs a thread while 128 CTAs hold them all at once, else four (99306 rows of
+  // 19 fp32 into 63744: 60 us with four, 55 with two; 2 M rows of 16 bf16 360 and 372)
+  const bool few = N <= kSoCtas * 2 * kSoThreads;
+  const int tile = few ? 2 * kSoThreads : 4 * kSoThreads;
+  q.per = ((N + kSoCtas - 1) / kSoCtas + tile - 1) / tile * tile;
+  const int ctas = (N + q.per - 1) / q.per;
   cudaError_t e = cudaSuccess;
   for (int k = 0; k < passes && e == cudaSuccess; ++k) {
     q.shift = k * bits;
     q.out = k + 1 < passes ? buf[k & 1] : nullptr;
-    e = launch_ex(k_sort_count, dim3(ctas), dim3(kSoThreads), sizeof(int) * (size_t)q.bins, st, true, q);
-    if (e == cudaSuccess) e = launch_ex(k_sort_place, dim3(ctas), dim3(kSoThreads), smem, st, true, q);
+    e = launch_ex(few ? k_sort_count<2> : k_sort_count<4>, dim3(ctas), dim3(kSoThreads),
+                  sizeof(int) * (size_t)q.bins, st, true, q);
+    if (e == cudaSuccess)
+      e = launch_ex(few ? k_sort_place<2> : k_sort_place<4>, dim3(ctas), dim3(kSoThreads), smem, st, true, q);
     q.idx = nullptr;
     q.pairs = q.out;
   }

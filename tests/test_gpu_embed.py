@@ -157,7 +157,7 @@ def test_large_vocabulary_and_three_digits():
     _check_grad(500, 129280, 16, BF16, BF16, _idx(500, 129280, "uniform"))
 
 
-@pytest.mark.parametrize("N", [4096, 4097, 16385, 32768, 32769, 70000])
+@pytest.mark.parametrize("N", [4096, 4097, 16385, 32768, 32769, 70000, 262144, 262145, 530000])
 @pytest.mark.parametrize("V", [2, 1025, (1 << 20) + 1])
 def test_lengths_about_the_sorts_bounds(N, V):
     """Sizes on both sides of where the sort's form changes, of one to three digits."""
