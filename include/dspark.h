@@ -413,7 +413,8 @@ dspark_status dspark_pctree_verify(dspark_ws* ws, const float* P, const int32_t*
  * K <= 65536, V <= 2^24, else DSPARK_EINVAL. The tensor cores cut their fp32
  * accumulator once per 16 terms; with the mean of that made up for, lse is off by
  * about 1.3e-10 K of itself on random rows (5e-7 at K = 4096). Asynchronous on
- * `stream`; each result is the same from call to call.
+ * `stream`; each result is the same from call to call (dX's grouping of sums may
+ * differ between calls with and without dW).
  */
 typedef enum { DSPARK_W_VK = 0, DSPARK_W_KV = 1 } dspark_w_layout;
 
