@@ -88,6 +88,7 @@ static_assert(kLcBars % 2 == 0, "16-byte ring entries");
 constexpr size_t kLcSmem = (size_t)kLcRing + 1024 + kLcBarBytes;
 static_assert(kLcSmem <= 232448, "one CTA's shared memory");
 constexpr int kLcPairs = 76;                      // CTA pairs of a full grid (152 SMs)
+constexpr int kLcTurnedParts = 16;                // sums per row that a pair leaves of turned logits: one a warp
 constexpr float kLcRefMin = -1e29f;               // least log2 reference: what lies below it counts as masked
 
 // One product C[M][Nn] = A B^T over a contraction of nkb blocks of 64.
@@ -100,10 +101,14 @@ struct LcJob {
   int tn;               // 256, or 128 or 64 where logits have few tiles (see z_cols)
   int split;            // pairs that share the tiles' blocks evenly (0: whole tiles)
   int a_mn, b_mn;       // operand's contraction index is its row (MN-major)
+  int a_m0;             // row offset in A's map (turned logits: the piece's first token)
   int b_k0;             // contraction offset in B's map
   int b_n0;             // column offset in B's map (and in U's)
   // logits (statistics, G)
   int has_u;
+  int turned;           // the result's rows are tokens (see z_turned)
+  const float* u;       // U and its leading dimension, for turned logits
+  int64_t ldu;
   int V;                // vocabulary
   float gain;           // makes up for the accumulator's truncation (see logit_gain)
   const int32_t* target;
@@ -230,7 +235,7 @@ struct LcRing {
   }
 };
 
-template <bool GRAD>
+template <bool GRAD, bool TURNED>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
     k_lce(const __grid_constant__ LcParams p) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -302,7 +307,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
         tell(LcTile::pack(w));
         const LcJob& j = p.job[w.job];
         const int half = lc_cols(j.Nn, w.n, j.tn) >> 1;  // columns of B in each CTA
-        const int am = w.m * kLcTile + (int)rank * kLcHalf, bn = j.b_n0 + w.n * j.tn + (int)rank * half;
+        const int am = j.a_m0 + w.m * kLcTile + (int)rank * kLcHalf, bn = j.b_n0 + w.n * j.tn + (int)rank * half;
         const int bboxes = (half + 63) >> 6;  // boxes of an MN-major B
         const uint32_t bytes = (uint32_t)(kLcOpBytes + (j.b_mn ? bboxes * kLcBox : j.tn * kLcKb));
         const bool a_mn = j.a_mn, b_mn = j.b_mn;
@@ -406,6 +411,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
     const LcJob& z = p.job[GRAD ? kLcMakeG : 0];  // the job that makes logits
     const bool has_u = z.has_u != 0;
     const int zn = z.tn;  // columns of a tile of logits
+    const int v_off = TURNED ? z.a_m0 : z.b_n0;  // the piece's first token
+    // turned: the running sums of row hf 32 + lane over the warp's tokens
+    float tref = kLcRefMin, tsum = 0.f;
     // the gain goes to the logits when U is added, else into what they are multiplied by
     const float gain = z.gain, zgain = has_u ? 1.f : gain, l2 = tc::kLog2e * zgain;
     const int row0 = (int)rank * kLcHalf + q * 32;  // the warp's first row in a tile
@@ -420,17 +428,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
     float lse = 0.f, wt = 1.f;
     bool is_z = false, has = false, asked = false;
     auto ask = [&](const LcTile& x) LC_INLINE {
-      const int r = x.m * kLcTile + row0 + lane;
+      const int r = TURNED ? hf * 32 + lane : x.m * kLcTile + row0 + lane, rows = TURNED ? z.Nn : z.M;
       tgt = -1;
-      if ((!GRAD || x.job == kLcMakeG) && r < z.M) {
+      if ((!GRAD || x.job == kLcMakeG) && r < rows) {
         tgt = z.target[r];
         if (GRAD) {
           lse = z.lse[r];
           wt = z.wt ? z.wt[r] : 1.f;
         }
       }
-      if (has_u && (!GRAD || x.job == kLcMakeG) && lane == 0 && r < z.M) {
+      if (has_u && (!GRAD || x.job == kLcMakeG) && lane == 0 && r < rows) {
         // its boxes of U on their way to L2
+        if (TURNED) {
+          const int v = v_off + x.m * kLcTile + row0;
+          if (v < z.V) tc::tma_prefetch_2d(&z.tu, v, r);
+          return;
+        }
         const int c0 = hf * (zn >> 1), n = min(zn >> 1, lc_cols(z.Nn, x.n, zn) - c0);
         for (int c = 0; c < n; c += kLcPart) tc::tma_prefetch_2d(&z.tu, z.b_n0 + x.n * zn + c0 + c, r);
       }
@@ -455,24 +468,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
       half = tn >> 1;
       col = w.n * tn + hf * half;
       parts = row - lane < M ? max(0, min(half, lc_cols(Nn, w.n, tn) - hf * half)) / kLcPart : 0;
+      if (TURNED && is_z) {  // 32 tokens by 32 rows, the tokens' lanes turned into the rows'
+        col = w.m * kLcTile + row0;
+        row = hf * 32 + lane;
+        has = row < Nn;
+        parts = col < M && hf * 32 < Nn ? 1 : 0;
+      }
       return true;
     };
     // the tile's box number b of U into the warp's box
     auto load_u = [&](int b) LC_INLINE {
-      if (has_u && is_z && b < parts && lane == 0) {
+      if (!TURNED && has_u && is_z && b < parts && lane == 0) {
         tc::mbar_arrive_expect_tx(ufull(e), kLcUBox);
-        tc::tma_load_2d(sbase + uoff, &z.tu, z.b_n0 + col + b * kLcPart, row - lane, ufull(e),
+        tc::tma_load_2d(sbase + uoff, &z.tu, v_off + col + b * kLcPart, row - lane, ufull(e),
                         tc::policy_evict_first());
       }
     };
     for (int tj = grp; announced(tj); tj += 2) {
       load_u(0);
       if (is_z && (tgt < -1 || tgt >= z.V)) {
-        if (w.n == 0 && hf == 0) raise_status(p.status, DSPARK_ERANGE);
+        if (TURNED ? w.m == 0 && row0 == 0 : w.n == 0 && hf == 0) raise_status(p.status, DSPARK_ERANGE);
         tgt = -1;
       }
       // the target's place in the half, the exponent's offset: with the weight in it for G
-      const int te = tgt - (z.b_n0 + col);
+      const int te = tgt - (v_off + col);
       const bool live = !is_z || (tgt >= 0 && lse != -INFINITY);  // else the row has no G
       const float wr = is_z ? wt : 1.f;
       const float off = GRAD ? fmaf(-lse, tc::kLog2e, log2f(fabsf(wr))) : 0.f;
@@ -493,7 +512,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
       };
       if (parts == 0) {
         release();
-        if (!GRAD && has) z.part[(int64_t)row * (2 * z.nt) + 2 * w.n + hf] = make_float2(kLcRefMin, 0.f);
+        if (!GRAD && !TURNED && has) z.part[(int64_t)row * (2 * z.nt) + 2 * w.n + hf] = make_float2(kLcRefMin, 0.f);
         continue;
       }
       const unsigned long long l2e = tc::f2pack(l2, l2);
@@ -514,6 +533,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
           if (h + 1 < parts) tc::tmem_ld32(t0 + (h + 1) * kLcPart, v);
           send(h);
         }
+      };
+      // turned: a lane's token by 32 rows to its row by 32 tokens, through the warp's
+      // box (no bank is met twice); U is read on the way, lanes side by side
+      auto turn = [&]() LC_INLINE {
+        if (has_u) {
+          const int tok = v_off + col + lane;
+          const float* up = z.u + (int64_t)(hf * 32) * z.ldu + tok;
+#pragma unroll
+          for (int i = 0; i < kLcPart; ++i)
+            v[i] = fmaf(v[i], gain, tok < z.V && hf * 32 + i < z.Nn ? up[i * z.ldu] : 0.f);
+        }
+        float* box = reinterpret_cast<float*>(smem + uoff);
+#pragma unroll
+        for (int i = 0; i < kLcPart; ++i) box[i * 32 + (lane ^ i)] = v[i];
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < kLcPart; ++i) v[i] = box[lane * 32 + (i ^ lane)];
+        __syncwarp();
       };
       // U's columns of part h onto its logits
       auto add_u = [&](int h) LC_INLINE {
@@ -568,9 +605,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
       };
 
       if constexpr (!GRAD) {
-        float ref = kLcRefMin, sum = 0.f;
+        float ref = TURNED ? tref : kLcRefMin, sum = TURNED ? tsum : 0.f;
         each_part([&](int h) LC_INLINE {
-          if (has_u) add_u(h);
+          if (TURNED)
+            turn();
+          else if (has_u)
+            add_u(h);
           const int t = te - kLcPart * h, left = z.V - col - kLcPart * h;  // columns past the vocabulary are out
           if (left < kLcPart) {
 #pragma unroll
@@ -609,12 +649,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
           tc::f2unpack(tc::add2(tc::add2(s2[0], s2[1]), tc::add2(s2[2], s2[3])), a, b);
           sum += a + b;
         }, [](int) {});
-        if (has) z.part[(int64_t)row * (2 * z.nt) + 2 * w.n + hf] = make_float2(ref, sum);
+        if (TURNED) {
+          tref = ref;
+          tsum = sum;
+        } else if (has) {
+          z.part[(int64_t)row * (2 * z.nt) + 2 * w.n + hf] = make_float2(ref, sum);
+        }
       } else if (is_z) {
         const unsigned long long off2 = tc::f2pack(off, off);
         uint32_t r[kLcPart / 2];
         each_part([&](int h) LC_INLINE {
-          if (has_u) add_u(h);
+          if (TURNED)
+            turn();
+          else if (has_u)
+            add_u(h);
           const int t = te - kLcPart * h;
 #pragma unroll
           for (int i = 0; i < kLcPart; i += 2) {
@@ -699,16 +747,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
           }, [](int) {});
         }
       }
-      if (has_u && is_z) ubox += parts;
+      if (!TURNED && has_u && is_z) ubox += parts;
       ok = __all_sync(0xFFFFFFFFu, ok);
       if (!ok) break;
     }
+    if (!GRAD && TURNED && hf * 32 + lane < z.Nn)
+      z.part[(int64_t)(hf * 32 + lane) * (kLcTurnedParts * npairs) + kLcTurnedParts * pair + grp * 8 + (int)rank * 4 + q] =
+          make_float2(tref, tsum);
     if (!ok && lane == 0) {
       if (!*abort) raise_status(p.status, DSPARK_ETIMEOUT);
       *abort = 1;
       // boxes of U still in flight land before the CTA can exit
       volatile int never = 0;
-      for (int b = ubox; b < ubox + kLcWarpCols / kLcPart; ++b)
+      for (int b = ubox; !TURNED && b < ubox + kLcWarpCols / kLcPart; ++b)
         tc::mbar_wait(ufull(e), b & 1, &never);
     }
     if (GRAD && lane == 0) tc::bulk_wait_all();
@@ -983,9 +1034,21 @@ struct LcPlan {
 constexpr int64_t kLcPieceBytes = 256ll << 20, kLcPieceBytesL2 = 64ll << 20, kLcPieceMost = 1ll << 30;
 constexpr int64_t kLcPieceCols = 64 * kLcTile;
 
-int z_tiles(const dspark_lce_dims& d) {
+// Up to 64 rows of X, the logits' product is made with W's tokens as its 256 rows
+// and X's rows as at most 64 columns: rows of X would fill a quarter of the product
+// at most, and be what bounds it (6 x 2321 x 141668 with U: forward 193 -> 134 us,
+// gradient 534 -> 446; 1 x 256 x 129280 with U and W [K][V] 37.5 -> 29.3 and 69 -> 61,
+// all with 12 us around them). The epilogue turns 32 x 32 logits in shared memory and
+// goes on as with rows; each warp keeps its running sums to the end. Few tokens
+// (7 x 210 x 2676) are 2 us slower that way.
+bool z_turned(const dspark_lce_dims& d) { return d.N <= 64 && tiles_of(d.V) >= 16; }
+
+// Sums a row that the statistics leave.
+int z_parts(const dspark_lce_dims& d) {
+  const int tiles = tiles_of(d.V);
+  if (z_turned(d)) return kLcTurnedParts * (tiles < kLcPairs ? tiles : kLcPairs);
   const int n = z_cols(d.N, d.V);
-  return (d.V + n - 1) / n;
+  return 2 * ((d.V + n - 1) / n);
 }
 
 LcPlan make_plan(const dspark_lce_dims& d) {
@@ -998,7 +1061,7 @@ LcPlan make_plan(const dspark_lce_dims& d) {
     off += (size_t)up(bytes > 0 ? bytes : 1, 256);
     return o;
   };
-  p.part = carve(8 * N * 2 * z_tiles(d));
+  p.part = carve(8 * N * z_parts(d));
   p.zt = carve(4 * N);
   p.fwd_total = off;
   const int64_t row = 2 * (N > 0 ? N : 1), wide = kLcPieceMost / row < kLcPieceCols ? kLcPieceMost / row : kLcPieceCols;
@@ -1058,9 +1121,9 @@ bool ld_ok(int64_t ld, int64_t cols, int mult) { return ld >= cols && ld % mult 
 cudaError_t lce_configure() {
   static bool configured = false;
   if (configured) return cudaSuccess;
-  cudaError_t e = cudaFuncSetAttribute(k_lce<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kLcSmem);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(k_lce<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kLcSmem);
+  cudaError_t e = cudaSuccess;
+  for (const auto k : {k_lce<false, false>, k_lce<false, true>, k_lce<true, false>, k_lce<true, true>})
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kLcSmem);
   if (e == cudaSuccess) configured = true;
   return e;
 }
@@ -1083,7 +1146,7 @@ struct LcLaunch {
     cudaError_t e = lce_configure();
     if (e != cudaSuccess) return e;
     int pairs = 0, tiles = 0;
-    bool u = false;
+    bool u = false, turned = false;
     for (int k = 0; k < kLcJobs; ++k) {
       LcJob& j = p.job[k];
       j.mt = tiles_of(j.M);
@@ -1094,7 +1157,8 @@ struct LcLaunch {
       pairs = pairs > j.split ? pairs : j.split;
       const int b_bytes = j.b_mn ? (j.tn / 2 + 63) / 64 * kLcBox : j.tn * kLcKb;
       if (j.mt > 0 && p.stage_bytes < kLcOpBytes + b_bytes) p.stage_bytes = kLcOpBytes + b_bytes;
-      u = u || j.has_u;
+      turned = turned || j.turned;
+      u = u || j.has_u || j.turned;  // boxes
     }
     p.stages = lc_stages(grad, u, p.stage_bytes);
     // dX's shares and the others' whole tiles on pairs of their own (gradient of 706 x
@@ -1116,7 +1180,8 @@ struct LcLaunch {
         left -= cost;
       }
     }
-    e = launch_ex(grad ? k_lce<true> : k_lce<false>, dim3(2 * pairs), dim3(kLcThreads), kLcSmem, st, true, p);
+    e = launch_ex(grad ? (turned ? k_lce<true, true> : k_lce<true, false>)
+                       : (turned ? k_lce<false, true> : k_lce<false, false>), dim3(2 * pairs), dim3(kLcThreads), kLcSmem, st, true, p);
     return e != cudaSuccess ? e : cudaGetLastError();
   }
 };
@@ -1132,20 +1197,24 @@ float logit_gain(int K) { return (float)(1.0 + 0.36 * 0x1p-23 * (K / 16.0 + 1.0)
 // z of the columns [v0, v0 + cols) of the vocabulary (statistics or G)
 bool z_job(LcJob& j, const dspark_lce_dims* d, const void* X, const void* W, const float* U, const int32_t* target,
            int v0, int cols) {
-  j.M = d->N;
-  j.Nn = cols;
+  j.turned = z_turned(*d);
+  j.M = j.turned ? cols : d->N;
+  j.Nn = j.turned ? d->N : cols;
   j.nkb = (d->K + kLcKb - 1) / kLcKb;
-  j.b_mn = d->layout == DSPARK_W_KV;
-  j.b_n0 = v0;
+  (j.turned ? j.a_mn : j.b_mn) = d->layout == DSPARK_W_KV;
+  (j.turned ? j.a_m0 : j.b_n0) = v0;
+  j.u = U;
+  j.ldu = d->ldu;
   j.has_u = U != nullptr;
   j.target = target;
   j.V = d->V;
   j.gain = logit_gain(d->K);
-  j.tn = z_cols(d->N, cols);
+  j.tn = j.turned ? kLcTile / 4 : z_cols(d->N, cols);
   if (U && !encode_box(&j.tu, U, kBoxU, d->V, d->N, d->ldu)) return false;
-  if (!encode(&j.ta, X, d->K, d->N, d->ldx, kLcHalf)) return false;
-  return d->layout == DSPARK_W_VK ? encode(&j.tb, W, d->K, d->V, d->ldw, j.tn / 2)
-                                  : encode(&j.tb, W, d->V, d->K, d->ldw, kLcKb);
+  const int w_rows = j.turned ? kLcHalf : j.tn / 2;  // of a box of W [V][K]
+  return encode(j.turned ? &j.tb : &j.ta, X, d->K, d->N, d->ldx, j.turned ? j.tn / 2 : kLcHalf) &&
+         (d->layout == DSPARK_W_VK ? encode(j.turned ? &j.ta : &j.tb, W, d->K, d->V, d->ldw, w_rows)
+                                   : encode(j.turned ? &j.ta : &j.tb, W, d->V, d->K, d->ldw, kLcKb));
 }
 
 // Where a gradient's product goes: parts of shared tiles to slots, whole tiles
@@ -1225,7 +1294,7 @@ extern "C" dspark_status dspark_linear_ce(const dspark_lce_dims* d, const void* 
   cudaError_t e = l.run(st);
   if (e == cudaSuccess)
     e = launch_ex(k_lce_rows, dim3((d->N + kLcRowsCta - 1) / kLcRowsCta), dim3(32 * kLcRowsCta), 0, st,
-                  true, part, zt, target, d->N, 2 * z_tiles(*d),
+                  true, part, zt, target, d->N, z_parts(*d),
                   d->V, loss, lse);
   return lce_fail(e);
 }

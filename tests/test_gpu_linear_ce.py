@@ -145,6 +145,55 @@ def test_vocabulary_in_pieces():
 
 
 @pytest.mark.parametrize("layout", ["vk", "kv"])
+@pytest.mark.parametrize("N,K,V,U,pad,ignored", [
+    (1, 16, 4097, True, 0, 0.0), (1, 700, 40000, False, 0, 0.0), (31, 264, 4100, True, 8, 0.1), (32, 65, 5000, False, 0, 0.3),
+    (33, 1030, 4353, True, 0, 0.0), (63, 128, 24001, True, 8, 0.1), (64, 80, 33000, False, 0, 0.1), (65, 80, 33000, True, 0, 0.0),
+    (7, 72, 3840, True, 0, 0.0), (7, 72, 3841, True, 0, 0.0),
+])
+def test_few_rows(N, K, V, U, pad, ignored, layout):
+    """Up to 64 rows: the logits' product has tokens as its rows."""
+    X, W, Um, t, wt = _inputs(N, K, V, layout, U, pad, ignored)
+    _check(X, W, Um, t, wt, 0.5, layout)
+
+
+@pytest.mark.parametrize("layout", ["vk", "kv"])
+def test_masks_with_few_rows(layout):
+    V = 60000                       # several tiles to a warp
+    X, W, U, t, wt = _inputs(40, 64, V, layout, True)
+    U, t = U.clone(), t.clone()
+    t[0], t[1], t[2], t[3], t[4], t[5], t[6] = 1, 30000, 59999, 500, 7, -1, 100
+    U[0, ::2] = -math.inf
+    U[1, :30000] = -math.inf        # whole tiles at the start
+    U[2, :59999] = -math.inf        # the last token alone
+    U[3, 500] = -math.inf           # the target
+    U[4] = -math.inf                # nothing left
+    U[5] = -math.inf
+    U[6, 256:] = torch.finfo(F32).min
+    U[7] = -1e30
+    op = LinearCE(40, 64, V, layout)
+    out = op.forward(X, W, t, U=U, out=op.new_outputs())
+    op.grad(X, W, t, out["lse"], wt=wt, scale=1.0, U=U, out=out)
+    assert op.device_status() == 0
+    masked = torch.where(U <= -1e30, torch.full_like(U, -math.inf), U)
+    ref, tol = _reference(X, W, masked, t, wt, 1.0, layout)
+    for k in out:
+        _close(out[k], ref[k], tol[k], k)
+    for dead in (4, 7):
+        assert out["lse"][dead] == -math.inf and out["loss"][dead] == math.inf and (out["dX"][dead] == 0).all()
+    assert out["lse"][5] == -math.inf and out["loss"][5] == 0 and (out["dX"][5] == 0).all()
+    assert out["loss"][3] == math.inf
+    for bad in (V, -2):             # a target out of range: reported, the row left out
+        t[9] = bad
+        got = op.forward(X, W, t, U=U, out=op.new_outputs())
+        assert op.device_status() == 6
+        op.reset()
+        op.grad(X, W, t, got["lse"], wt=wt, U=U, out=got)
+        assert op.device_status() == 6
+        op.reset()
+        assert got["loss"][9] == 0 and (got["dX"][9] == 0).all()
+
+
+@pytest.mark.parametrize("layout", ["vk", "kv"])
 def test_whole_tiles_summed_over_pieces(layout):
     """dX has tiles for most of the grid, so that each is summed in place from piece to piece."""
     X, W, U, t, wt = _inputs(4100, 1000, 40003, layout, False, 0, 0.1)
@@ -168,6 +217,7 @@ def test_long_products(N, K, V, U, pad, ignored, layout):
     (9, 200, 4800, True),                       # logits in tiles of 64 columns,
     (300, 130, 2561, True), (20, 72, 9473, False),   # of 128,
     (300, 130, 5121, True), (20, 72, 9729, False),   # of 256
+    (70, 200, 4800, True), (65, 72, 9473, False), (129, 72, 9729, True),
     (33, 1025, 1100, True),                     # few tiles of a longer contraction
     (130, 260, 40001, False),                   # dX on some of the pairs, dW on the others
 ])
