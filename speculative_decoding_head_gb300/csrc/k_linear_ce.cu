@@ -356,6 +356,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
       bool ok = true;
       LcRing r{0, 0, sbase};
       int tj = 0;
+      // its own waits are for this grid's work alone: their limit does not run while an
+      // earlier kernel, which may have let this one start, is still at work
+      pdl_wait();
       for (;; ++tj) {
         ok = tc::mbar_wait(told(tj), (tj / kLcAhead) & 1, abort);
         if (!ok) break;

@@ -1,0 +1,77 @@
+"""The linear cross entropy where it can go wrong: rows left out, batches without rows, early starts, pieces, long sums.
+
+Tolerances are those of test_gpu_linear_ce.py where nothing else is said.
+"""
+
+import ctypes as C
+import subprocess
+
+import pytest
+import torch
+
+from speculative_decoding_head_gb300 import build
+from speculative_decoding_head_gb300.binding import LinearCE
+
+from test_gpu_linear_ce import _check, _inputs
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    build.build()
+
+
+LATE = r"""
+#include <cuda_runtime.h>
+#include <stdint.h>
+// Lets the kernel that follows start at once, then takes ms milliseconds and copies n pieces.
+__global__ void late(const uint4* src, uint4* dst, int n, unsigned long long ms) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  unsigned long long t0, t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
+  for (int i = 0; i < 1000000; ++i) {
+    __nanosleep(1000);
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    if (t - t0 > ms * 1000000ull) break;
+  }
+  for (int i = threadIdx.x; i < n; i += blockDim.x) dst[i] = src[i];
+}
+extern "C" int run_late(const void* src, void* dst, int n, int ms, void* stream) {
+  late<<<1, 256, 0, static_cast<cudaStream_t>(stream)>>>(static_cast<const uint4*>(src), static_cast<uint4*>(dst), n,
+                                                         ms);
+  return cudaGetLastError();
+}
+"""
+
+
+@pytest.mark.parametrize("N,K,V,layout", [(6, 80, 1024, "vk"), (6, 80, 5000, "vk"), (300, 64, 2000, "kv"),
+                                          (1500, 1000, 7000, "vk")])
+def test_behind_a_long_kernel_that_lets_it_start(N, K, V, layout, tmp_path_factory):
+    """A kernel that lets its dependents start early and then runs 0.6 s, longer
+    than any wait of the operator's own may last, delays a call and no more."""
+    at = tmp_path_factory.getbasetemp() / "late.so"
+    if not at.exists():
+        src = at.with_suffix(".cu")
+        src.write_text(LATE)
+        subprocess.run([build.nvcc(), *build.ARCH, "-shared", "-Xcompiler", "-fPIC", "-o", str(at), str(src)], check=True)
+    late = C.CDLL(str(at)).run_late
+    late.argtypes = [C.c_void_p, C.c_void_p, C.c_int, C.c_int, C.c_void_p]
+    X, W, _, t, wt = _inputs(N, K, V, layout)
+    op, first = _check(X, W, None, t, wt, 1.0, layout)
+    keep = X.contiguous().clone()
+    X2 = torch.zeros_like(keep)                  # K is a multiple of 8: rows on 16 bytes without padding
+    out = op.new_outputs()
+    stream = torch.cuda.current_stream().cuda_stream
+
+    def delay():
+        X2.zero_()
+        assert late(keep.data_ptr(), X2.data_ptr(), keep.numel() // 8, 600, stream) == 0
+
+    delay()
+    op.forward(X2, W, t, out=out)
+    delay()
+    op.grad(X2, W, t, out["lse"], wt=wt, scale=1.0, out=out)
+    assert op.device_status() == 0
+    for k in first:
+        assert torch.equal(out[k], first[k]), k
