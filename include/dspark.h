@@ -408,13 +408,14 @@ dspark_status dspark_pctree_verify(dspark_ws* ws, const float* P, const int32_t*
  * caller clears it. U may hold -inf, or the type's lowest value, where a token
  * is masked (z <= -1e29 counts as -inf): its probability is 0, and a row whose
  * target is masked has loss +inf. A row with every token masked has lse -inf,
- * loss +inf (0 if left out) and no part in the gradients. NaN and z above 1e38
- * make their row's results NaN. N = 0 is allowed (dW is then 0). 0 <= N <= 2^20,
- * K <= 65536, V <= 2^24, else DSPARK_EINVAL. The tensor cores cut their fp32
- * accumulator once per 16 terms; with the mean of that made up for, lse is off by
- * about 1.3e-10 K of itself on random rows (5e-7 at K = 4096). Asynchronous on
- * `stream`; each result is the same from call to call (dX's grouping of sums may
- * differ between calls with and without dW).
+ * loss +inf (0 if left out) and no part in the gradients. Whatever X and U hold
+ * in a row that is left out reaches no gradient. In the other rows NaN and z above
+ * 1e38 make the row's results NaN, and with them dW. N = 0 is allowed (dW is then
+ * 0). 0 <= N <= 2^20, K <= 65536, V <= 2^24, else DSPARK_EINVAL. The tensor cores
+ * cut their fp32 accumulator once per 16 terms; with the mean of that made up for,
+ * lse is off by about 1.3e-10 K of itself on random rows (5e-7 at K = 4096).
+ * Asynchronous on `stream`; each result is the same from call to call (dX's
+ * grouping of sums may differ between calls with and without dW).
  */
 typedef enum { DSPARK_W_VK = 0, DSPARK_W_KV = 1 } dspark_w_layout;
 

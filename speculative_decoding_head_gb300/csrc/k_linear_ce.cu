@@ -20,7 +20,7 @@
 // of a tile runs under the next tile's products. An operand whose contraction
 // index is its row (W in dX, G in dW) is read in place as an MN-major operand;
 // only X is transposed in memory, once, for a long dW (the reason is at
-// make_plan).
+// make_plan), and copied for a short one: dW sees zeros in rows that are left out.
 //
 //   warp 0      TMA producer (both CTAs; bytes counted on the even CTA)
 //   warp 1      allocates TMEM; in the even CTA issues the MMAs of the pair
@@ -137,6 +137,11 @@ struct LcParams {
   int sharing, rounds;  // the first `sharing` pairs take whole tiles from round `rounds` on
   int stages, stage_bytes;
   int* status;
+  // beside the first piece's G, where xc is given: X [N][K] to xc, rows `ldc` apart (see lc_live_rows)
+  const __nv_bfloat16* x;
+  __nv_bfloat16* xc;
+  int64_t ldx, ldc;
+  int N, K;
 };
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -147,6 +152,51 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // first block of pair p's share of `units` blocks split over `split` pairs
 __host__ __device__ __forceinline__ int lc_share(int units, int split, int p) {
   return (int)((long long)units * p / split);
+}
+
+// whether row n has a part in the gradients: a target, and a token that is not masked
+__device__ __forceinline__ bool lc_live(const int32_t* target, const float* lse, int V, int n) {
+  const int t = target[n];
+  return t >= 0 && t < V && lse[n] != -INFINITY;
+}
+
+// X's rows for dW's product, the ones that are left out as zeros: their rows of G are
+// zero, but zero times a NaN or an infinity would reach the feature's gradient of every
+// token. All epilogue warps of the launch that makes G share it, a lane four pieces
+// of 16 bytes at a time, under the first tile's products: dX and dW of 6 x 80 x 1024
+// 13.6 us with and without it, of 706 x 1038 x 1415 26.9 and 26.8; the most where rows
+// are many and all else is little, 131072 x 64 x 512: 119 and 104.
+__device__ __forceinline__ void lc_live_rows(const LcParams& p, const LcJob& z) {
+  const unsigned per = (unsigned)(p.K + 7) / 8, total = (unsigned)p.N * per;
+  const unsigned lanes = kLcEpiWarps * 32, first = blockIdx.x * lanes + threadIdx.x - 64, step = gridDim.x * lanes;
+#pragma unroll 1
+  for (unsigned i = first; i < total; i += 4 * step) {
+    uint4 x[4];
+#pragma unroll
+    for (int f = 0; f < 4; ++f) {
+      const unsigned j = i + f * step;
+      if (j >= total) break;
+      const unsigned n = j / per;
+      const int k = (int)(j - n * per) * 8;
+      const __nv_bfloat16* from = p.x + (int64_t)n * p.ldx + k;
+      if (k + 8 <= p.K) {
+        x[f] = *reinterpret_cast<const uint4*>(from);
+      } else {
+        unsigned short v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = k + e < p.K ? __bfloat16_as_ushort(from[e]) : 0;
+        x[f] = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+      }
+      if (!lc_live(z.target, z.lse, z.V, (int)n)) x[f] = make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int f = 0; f < 4; ++f) {
+      const unsigned j = i + f * step;
+      if (j >= total) break;
+      const unsigned n = j / per;
+      *reinterpret_cast<uint4*>(p.xc + (int64_t)n * p.ldc + (j - n * per) * 8) = x[f];
+    }
+  }
 }
 
 // What a pair works on next: its share of the split jobs, then whole tiles of
@@ -423,6 +473,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLcThreads, 1)
     bool ok = true;
     int ubox = 0;  // boxes of U taken so far
     pdl_wait();    // rows' data, U and the outputs are other kernels' until they end
+    if (GRAD && p.xc != nullptr) lc_live_rows(p, z);
 
     // the tile announced as number i; a logit tile's target, lse and weight of this
     // lane's row, asked for a tile early where the tile is announced by then
@@ -911,11 +962,12 @@ __global__ void __launch_bounds__(256) k_lce_join(const __grid_constant__ LcJoin
   }
 }
 
-// XT[k][n] = X[n][k], rows of XT padded to a multiple of 8 (with zeros): 64 x 64
-// through shared memory, 16-byte pieces on both sides.
+// XT[k][n] = X[n][k] for dW's product, zero for the rows that are left out (see
+// lc_live_rows), rows of XT padded to a multiple of 8 (with zeros): 64 x 64 through
+// shared memory, 16-byte pieces on both sides.
 __global__ void __launch_bounds__(256)
     k_lce_transpose(const __nv_bfloat16* __restrict__ X, int64_t ldx, int N, int K, __nv_bfloat16* __restrict__ XT,
-                    int64_t ldt) {
+                    int64_t ldt, const int32_t* __restrict__ target, const float* __restrict__ lse, int V) {
   __shared__ __nv_bfloat16 sh[64][66];
   pdl_wait();
   pdl_trigger();
@@ -929,8 +981,9 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[e] = n < N && k + e < K ? X[n * ldx + k + e] : __float2bfloat16_rn(0.f);
     }
+    const bool live = n < N && lc_live(target, lse, V, n);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sh[r][c + e] = x[e];
+    for (int e = 0; e < 8; ++e) sh[r][c + e] = live ? x[e] : __float2bfloat16_rn(0.f);
   }
   __syncthreads();
   for (int i = threadIdx.x; i < 512; i += 256) {
@@ -1024,7 +1077,7 @@ struct LcPlan {
   int dx_split_dw;  // dX's beside dW
   int64_t dx_lda;
   bool swap;    // the operand whose contraction index is its row goes to A (see make_plan)
-  int64_t ldt;  // of X's transpose
+  int64_t ldt;  // of X's transpose, or of its copy
   size_t part, zt, fwd_total;                              // forward
   size_t G[2], dx_acc, dx_slots, dw_slots, XT, bwd_total;  // gradient
 };
@@ -1097,15 +1150,16 @@ LcPlan make_plan(const dspark_lce_dims& d) {
   // contraction 5376: 885 against 640 cycles a block). So where the products are
   // long, dX with W [V][K] is made transposed (A = W, B = G) and turned in its
   // epilogue, and dW takes X's transpose, made once, as B. Where they are short
-  // the extra launch costs more than it saves (N K V = 2e10: 10 us saved, 3 spent).
+  // the extra launch costs more than it saves (N K V = 2e10: 10 us saved, 3 spent): dW
+  // takes a copy of X that the first launch makes.
   p.swap = (double)N * K * V >= 1e10;
-  p.ldt = up(N, 8);
+  p.ldt = up(p.swap ? N : K, 8);
   p.dx_lda = p.swap && d.layout == DSPARK_W_VK ? up(N, 32) : up(K, 32);
   off = 0;
   p.G[0] = carve(2 * N * p.ldg);
   p.G[1] = p.pieces > 1 ? carve(2 * N * p.ldg) : p.G[0];
   p.dx_acc = carve(p.pieces > 1 ? 4 * p.dx_lda * (p.swap && d.layout == DSPARK_W_VK ? K : N) : 0);
-  p.XT = carve(p.swap ? 2 * K * p.ldt : 0);
+  p.XT = carve(2 * (p.swap ? K : N) * p.ldt);
   p.dx_slots = carve(4ll * 2 * p.dx_split * kLcTile * kLcTile);
   p.dw_slots = carve(4ll * 2 * p.dw_split * kLcTile * kLcTile);
   p.bwd_total = off;
@@ -1169,6 +1223,10 @@ struct LcLaunch {
     const LcJob& x = p.job[kLcDx];
     const bool apart = x.split > 0 && p.job[kLcDw].split == 0;
     pairs = pairs > tiles ? pairs : tiles;
+    if (p.xc) {  // X's copy: up to four pieces a lane, on pairs without tiles too
+      const int64_t lanes = 2 * kLcEpiWarps * 32, need = ((int64_t)p.N * (p.ldc / 8) + 4 * lanes - 1) / (4 * lanes);
+      pairs = pairs > need ? pairs : (int)(need < kLcPairs ? need : kLcPairs);
+    }
     if (apart && pairs < x.split + tiles) pairs = x.split + tiles;
     pairs = pairs < kLcPairs ? pairs : kLcPairs;
     // rounds of whole tiles that the other pairs do during one of dX's shares
@@ -1326,7 +1384,7 @@ extern "C" dspark_status dspark_linear_ce_grad(const dspark_lce_dims* d, const v
   if (dW && p.swap)
     e = launch_ex(k_lce_transpose, dim3((d->K + 63) / 64, (d->N + 63) / 64), dim3(256), 0, st, true,
                   static_cast<const __nv_bfloat16*>(X), d->ldx, d->N, d->K, reinterpret_cast<__nv_bfloat16*>(base + p.XT),
-                  p.ldt);
+                  p.ldt, target, lse, d->V);
   // launch i makes G of piece i beside the gradients' products of piece i - 1
   for (int i = 0; i <= p.pieces && e == cudaSuccess; ++i) {
     LcLaunch l(true, device_status);
@@ -1381,7 +1439,7 @@ extern "C" dspark_status dspark_linear_ce_grad(const dspark_lce_dims* d, const v
         CUtensorMap* tx = rows_v ? &w.tb : &w.ta;
         if (!encode(tg, G, cols, d->N, p.ldg, kLcKb) ||
             !(p.swap ? encode(tx, base + p.XT, d->N, d->K, p.ldt, kLcHalf)
-                     : encode(tx, X, d->K, d->N, d->ldx, kLcKb)))
+                     : encode(tx, base + p.XT, d->K, d->N, p.ldt, kLcKb)))
           return DSPARK_EINVAL;
         if (w.split) {
           ++njoin;
@@ -1397,6 +1455,14 @@ extern "C" dspark_status dspark_linear_ce_grad(const dspark_lce_dims* d, const v
       g.lse = lse;
       g.wt = wt;
       if (!encode_box(&g.to, base + p.G[i & 1], kBox16, cols, d->N, p.ldg)) return DSPARK_EINVAL;
+      if (i == 0 && dW && !p.swap) {
+        l.p.x = static_cast<const __nv_bfloat16*>(X);
+        l.p.xc = reinterpret_cast<__nv_bfloat16*>(base + p.XT);
+        l.p.ldx = d->ldx;
+        l.p.ldc = p.ldt;
+        l.p.N = d->N;
+        l.p.K = d->K;
+      }
     }
     e = l.run(st);
     if (njoin > 0 && e == cudaSuccess)

@@ -4,6 +4,7 @@ Tolerances are those of test_gpu_linear_ce.py where nothing else is said.
 """
 
 import ctypes as C
+import math
 import subprocess
 
 import pytest
@@ -12,7 +13,7 @@ import torch
 from speculative_decoding_head_gb300 import build
 from speculative_decoding_head_gb300.binding import LinearCE
 
-from test_gpu_linear_ce import _check, _inputs
+from test_gpu_linear_ce import _check, _close, _inputs, _reference
 
 pytestmark = pytest.mark.gpu
 
@@ -20,6 +21,36 @@ pytestmark = pytest.mark.gpu
 @pytest.fixture(scope="module", autouse=True)
 def _built():
     build.build()
+
+
+@pytest.mark.parametrize("layout", ["vk", "kv"])
+@pytest.mark.parametrize("N,K,V", [(40, 70, 1000), (40, 64, 5000), (300, 136, 3000), (1500, 1001, 7003), (4100, 72, 50001)])
+def test_rows_left_out_hold_anything(N, K, V, layout):
+    """NaN and infinities in rows of X and U that are left out (no target, or
+    one out of range) reach no entry of dW; nor does a row with every token masked."""
+    X, W, U, t, wt = _inputs(N, K, V, layout, True, 8, 0.1)
+    t[0] = t[N - 1] = -1
+    t[1], t[2] = V, 3
+    U[2] = -math.inf
+    dead = torch.nonzero((t < 0) | (t >= V))[:, 0]
+    clean = X.clone()
+    clean[dead] = 0.0
+    for i, bad in enumerate((math.nan, math.inf, -math.inf)):
+        X[dead[i::3], i::2] = bad
+    U[dead[::2], ::3] = math.nan
+    op = LinearCE(N, K, V, layout)
+    out = op.forward(X, W, t, U=U, out=op.new_outputs())
+    op.grad(X, W, t, out["lse"], wt=wt, scale=0.5, U=U, out=out)
+    assert op.device_status() == 6              # the target out of range
+    t[1] = -1
+    U[dead] = 0.0
+    ref, tol = _reference(clean, W, U, t, wt, 0.5, layout)
+    assert (out["loss"][dead] == 0).all() and (out["dX"][dead] == 0).all()
+    for k in ("dX", "dW"):
+        _close(out[k], ref[k], tol[k], k)
+    alone = op.new_outputs(dx=False)
+    op.grad(X, W, t, out["lse"], wt=wt, scale=0.5, U=U, out=alone)
+    assert torch.equal(alone["dW"], out["dW"])
 
 
 LATE = r"""
