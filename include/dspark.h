@@ -400,7 +400,7 @@ dspark_status dspark_pctree_verify(dspark_ws* ws, const float* P, const int32_t*
  * values past a row's last are neither read nor written, and every base
  * pointer is 16-byte aligned (scratch: 256). Sums, statistics and the products'
  * accumulators are fp32; G enters the gradients' products as bf16. dX or dW
- * may be NULL (not both): a frozen X or W.
+ * may be NULL (not both, unless N = 0): a frozen X or W.
  *
  * target[n] = -1 leaves row n out: loss 0 and no part in either gradient; any
  * other value outside [0, V) does the same and sets DSPARK_ERANGE in

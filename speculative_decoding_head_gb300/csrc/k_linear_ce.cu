@@ -1368,7 +1368,7 @@ extern "C" dspark_status dspark_linear_ce_grad(const dspark_lce_dims* d, const v
   if (bad != DSPARK_OK) return bad;
   const bool vk = d->layout == DSPARK_W_VK;
   if (d->N > 0 && (!aligned16(lse) || (wt && !aligned16(wt)))) return DSPARK_EINVAL;
-  if (!dX && !dW) return DSPARK_EINVAL;
+  if (!dX && !dW && d->N > 0) return DSPARK_EINVAL;  // without rows dX is empty, and may have no address
   if (dX && (!aligned16(dX) || !ld_ok(d->lddx, d->K, 8))) return DSPARK_EINVAL;
   if (dW && (!aligned16(dW) || !ld_ok(d->lddw, vk ? d->K : d->V, 8))) return DSPARK_EINVAL;
   if (!encode_fn()) return DSPARK_ECUDA;

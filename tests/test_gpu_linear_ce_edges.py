@@ -13,7 +13,7 @@ import torch
 from speculative_decoding_head_gb300 import build
 from speculative_decoding_head_gb300.binding import LinearCE
 
-from test_gpu_linear_ce import _check, _close, _inputs, _reference
+from test_gpu_linear_ce import BF16, _check, _close, _inputs, _reference
 
 pytestmark = pytest.mark.gpu
 
@@ -51,6 +51,23 @@ def test_rows_left_out_hold_anything(N, K, V, layout):
     alone = op.new_outputs(dx=False)
     op.grad(X, W, t, out["lse"], wt=wt, scale=0.5, U=U, out=alone)
     assert torch.equal(alone["dW"], out["dW"])
+
+
+@pytest.mark.parametrize("layout", ["vk", "kv"])
+@pytest.mark.parametrize("dx,dw", [(True, False), (False, True)])
+def test_no_rows_and_one_gradient(dx, dw, layout):
+    """A batch without rows is allowed whichever gradient is asked for (an empty dX has no address)."""
+    op = LinearCE(0, 16, 50, layout)
+    out = op.new_outputs(dx, dw)
+    if dw:
+        out["dW"].fill_(7.0)
+    X, t = torch.empty(0, 16, dtype=BF16, device="cuda"), torch.empty(0, dtype=torch.int32, device="cuda")
+    W = torch.randn(*op.w_shape, device="cuda").bfloat16() if layout == "vk" else (
+        torch.randn(16, 56, device="cuda").bfloat16()[:, :50])
+    op.grad(X, W, t, out["lse"], out=out)
+    assert op.device_status() == 0
+    if dw:
+        assert (out["dW"] == 0).all()
 
 
 LATE = r"""
