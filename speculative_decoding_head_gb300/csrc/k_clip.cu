@@ -285,7 +285,8 @@ extern "C" dspark_status dspark_clip_grads(int count, const void* const* in, voi
   if (!(max_norm >= 0.f)) return DSPARK_EINVAL;
   for (int i = 0; i < count; ++i) {
     if (types[i] != DSPARK_F32 && types[i] != DSPARK_BF16) return DSPARK_EINVAL;
-    if (numel[i] < 0 || (numel[i] > 0 && (!in[i] || !out[i]))) return DSPARK_EINVAL;
+    if (numel[i] == 0) continue;
+    if (numel[i] < 0 || !in[i] || !out[i]) return DSPARK_EINVAL;
     const uintptr_t mask = types[i] == DSPARK_BF16 ? 1u : 3u;
     if (((reinterpret_cast<uintptr_t>(in[i]) | reinterpret_cast<uintptr_t>(out[i])) & mask) != 0) return DSPARK_EINVAL;
     if (numel[i] > ((int64_t)1 << 44)) return DSPARK_EINVAL;
