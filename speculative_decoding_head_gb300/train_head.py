@@ -44,7 +44,8 @@ class HeadTrainer:
     def step(self, U: torch.Tensor, anchor: torch.Tensor, xstar: torch.Tensor):
         """One step on U [B, gamma, V] fp32, anchor [B] and xstar [B, gamma]
         int32 (-1: no token there, and none drafted from). Returns the batch
-        loss before the step and the gradients' norm, on the device."""
+        loss before the step and the gradients' norm, on the device. A norm that
+        is not finite leaves the weights as they are (and sets the status)."""
         prev = torch.cat([anchor[:, None], xstar[:, :-1]], 1).reshape(-1)
         # a position whose previous token is missing has no row of W1: it is left out
         target = torch.where(prev >= 0, xstar.reshape(-1), torch.full_like(prev, -1))
@@ -54,8 +55,9 @@ class HeadTrainer:
         self.ce.grad(X, self.W2, target, self.out["lse"], wt=self.weight, scale=1.0 / self.B, U=U, out=self.out)
         self.emb.grad(self.out["dX"], prev, out=self.dW1)
         norm = self.clip.clip(self.max_norm).clone()
+        skip = ~torch.isfinite(norm)  # the clip has left such gradients as they are
         for m, w, d in zip(self.master, (self.W1, self.W2), (self.dW1, self.out["dW"])):
-            m.add_(d, alpha=-self.lr)
+            m.add_(d.masked_fill_(skip, 0.0), alpha=-self.lr)
             w.copy_(m)
         return (self.out["loss"] * self.weight).sum() / self.B, norm
 
