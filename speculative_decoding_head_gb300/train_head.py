@@ -19,21 +19,23 @@ import argparse
 
 import torch
 
-from .binding import Embedding, GradClip, LinearCE
+from .binding import DsparkError, Embedding, GradClip, LinearCE
 
 
 class HeadTrainer:
-    """W1 [V, r] and W2 [r, V] in training; ``W1`` and ``W2`` are the bf16 weights."""
+    """W1 [V, r] and W2 [r, V] in training, V a multiple of 8; ``W1`` and ``W2`` are the bf16 weights."""
 
     def __init__(self, B: int, gamma: int, V: int, r: int, lr: float = 1.0, tau: float = 4.0, max_norm: float = 1.0,
                  w_std: float = 0.02, seed: int = 0, device="cuda"):
+        if V % 8:
+            raise DsparkError(f"V must be a multiple of 8, as for a draft with bf16 weights, got {V}")
         g = torch.Generator(device=device).manual_seed(seed)
         self.B, self.gamma, self.lr, self.max_norm = B, gamma, lr, max_norm
         n, bf16 = B * gamma, torch.bfloat16
         self.master = [torch.empty(V, r, device=device).normal_(0.0, w_std, generator=g),
                        torch.empty(r, V, device=device).normal_(0.0, w_std, generator=g)]
         self.W1, self.W2 = (m.to(bf16) for m in self.master)
-        self.rows = torch.empty(n, r, dtype=bf16, device=device)
+        self.rows = torch.empty(n, -(-r // 8) * 8, dtype=bf16, device=device)[:, :r]  # LinearCE wants rows on 16 bytes
         self.dW1 = torch.empty(V, r, dtype=bf16, device=device)
         self.ce = LinearCE(n, r, V, layout="kv", device=device)
         self.out = self.ce.new_outputs()
