@@ -470,7 +470,37 @@ class Workspace:
         return out
 
 
-class LinearCE:
+class _TrainOp:
+    """What the training operators' objects share. Memory that a call makes
+    belongs to the stream it runs on; the object's own buffers (``_buffers``) are
+    noted with every stream that a call uses, so that their memory is not given
+    away while that stream's work on them goes on."""
+
+    def __init__(self):
+        self._streams = set()
+
+    def _buffers(self):
+        return (self.scratch, self.status)
+
+    def _on(self, stream) -> int:
+        """Address of the stream that a call runs on (the current one if None)."""
+        raw = _raw_stream(stream, self.status.device.index)
+        if raw not in self._streams:
+            self._streams.add(raw)
+            stream = torch.cuda.current_stream(self.status.device) if stream is None else stream
+            for t in self._buffers():
+                t.record_stream(stream)
+        return raw
+
+    def device_status(self) -> int:
+        """The first device error since the last reset (synchronises)."""
+        return int(self.status.item())
+
+    def reset(self) -> None:
+        self.status.zero_()
+
+
+class LinearCE(_TrainOp):
     """Softmax cross entropy of z = X W (+ U) over the vocabulary, with its
     gradients and without keeping z (``dspark_linear_ce``,
     ``dspark_linear_ce_grad``), for N rows of K features and V tokens. Holds
@@ -482,6 +512,7 @@ class LinearCE:
     a multiple of 4) or None; target [N] int32, -1 for a row left out."""
 
     def __init__(self, N: int, K: int, V: int, layout: str = "vk", device="cuda"):
+        super().__init__()
         self.lib = load()
         if layout not in LAYOUTS:
             raise DsparkError(f"layout must be one of {sorted(LAYOUTS)}, got {layout!r}")
@@ -496,13 +527,6 @@ class LinearCE:
     @property
     def w_shape(self):
         return (self.V, self.K) if self.layout == "vk" else (self.K, self.V)
-
-    def device_status(self) -> int:
-        """The first device error since the last reset (synchronises)."""
-        return int(self.status.item())
-
-    def reset(self) -> None:
-        self.status.zero_()
 
     def new_outputs(self, dx: bool = True, dw: bool = True) -> Dict[str, torch.Tensor]:
         """loss and lse [N] fp32; dX [N, K] and dW (W's shape) bf16 where wanted,
@@ -532,20 +556,24 @@ class LinearCE:
 
     def forward(self, X, W, target, U=None, out=None, stream=None):
         """loss and lse of every row."""
-        out = self.new_outputs(False, False) if out is None else out
+        if out is None:
+            with torch.cuda.stream(stream):
+                out = self.new_outputs(False, False)
         d = self._dims()
         ins = self._inputs(d, X, W, target, U)
         f32 = torch.float32
         code = self.lib.dspark_linear_ce(C.byref(d), *ins, _vec(out["loss"], self.N, f32, "loss"),
                                          _vec(out["lse"], self.N, f32, "lse"), self.scratch.data_ptr(),
-                                         self.status.data_ptr(), _raw_stream(stream, X.device.index))
+                                         self.status.data_ptr(), self._on(stream))
         _check(code, "dspark_linear_ce")
         return out
 
     def grad(self, X, W, target, lse, wt=None, scale: float = 1.0, U=None, out=None, stream=None):
         """Gradients of scale * sum_n wt[n] loss[n] with lse from ``forward``,
         into out["dX"] and out["dW"] (the ones that ``out`` has)."""
-        out = self.new_outputs() if out is None else out
+        if out is None:
+            with torch.cuda.stream(stream):
+                out = self.new_outputs()
         d = self._dims()
         ins = self._inputs(d, X, W, target, U)
         f32, bf16 = torch.float32, torch.bfloat16
@@ -556,12 +584,12 @@ class LinearCE:
             pw, d.lddw = _rows(out["dW"], *self.w_shape, bf16, "dW")
         code = self.lib.dspark_linear_ce_grad(C.byref(d), *ins, _vec(lse, self.N, f32, "lse"),
                                               _vec(wt, self.N, f32, "wt"), scale, px, pw, self.scratch.data_ptr(),
-                                              self.status.data_ptr(), _raw_stream(stream, X.device.index))
+                                              self.status.data_ptr(), self._on(stream))
         _check(code, "dspark_linear_ce_grad")
         return out
 
 
-class Embedding:
+class Embedding(_TrainOp):
     """Rows of a table [V, D] looked up for N tokens and scaled
     (``dspark_embed``), and the table's gradient (``dspark_embed_grad``).
     Holds the gradient's scratch (made at its first call) and a status word; calls that share one
@@ -569,6 +597,7 @@ class Embedding:
     rows; idx [N] int32, -1 for a row without a token."""
 
     def __init__(self, N: int, V: int, D: int, device="cuda"):
+        super().__init__()
         self.lib = load()
         self.N, self.V, self.D = int(N), int(V), int(D)
         self._bytes = int(self.lib.dspark_embed_grad_scratch_bytes(self.N, self.V, self.D))
@@ -577,12 +606,8 @@ class Embedding:
         self.scratch: Optional[torch.Tensor] = None
         self.status = torch.zeros(1, dtype=torch.int32, device=device)
 
-    def device_status(self) -> int:
-        """The first device error since the last reset (synchronises)."""
-        return int(self.status.item())
-
-    def reset(self) -> None:
-        self.status.zero_()
+    def _buffers(self):
+        return (self.status,) if self.scratch is None else (self.scratch, self.status)
 
     def _mat(self, t, rows, dtype, name):
         return _rows(t, rows, self.D, dtype, name)
@@ -591,11 +616,12 @@ class Embedding:
         """scale * E[idx] as [N, D] in E's type (into ``out`` if given)."""
         code = _dtype_code(E, "E")
         if out is None:
-            out = torch.empty(self.N, self.D, dtype=E.dtype, device=E.device)
+            with torch.cuda.stream(stream):
+                out = torch.empty(self.N, self.D, dtype=E.dtype, device=E.device)
         pe, lde = self._mat(E, self.V, E.dtype, "E")
         po, ldo = self._mat(out, self.N, E.dtype, "out")
         r = self.lib.dspark_embed(pe, code, lde, self.V, self.D, _vec(idx, self.N, torch.int32, "idx"), self.N,
-                                  scale, po, ldo, self.status.data_ptr(), _raw_stream(stream, E.device.index))
+                                  scale, po, ldo, self.status.data_ptr(), self._on(stream))
         _check(r, "dspark_embed")
         return out
 
@@ -605,26 +631,30 @@ class Embedding:
         it may be ``out`` itself."""
         code = _dtype_code(dout, "dout")
         if out is None:
-            out = torch.empty(self.V, self.D, dtype=dout.dtype if base is None else base.dtype, device=dout.device)
+            with torch.cuda.stream(stream):
+                out = torch.empty(self.V, self.D, dtype=dout.dtype if base is None else base.dtype, device=dout.device)
         if self.scratch is None:
-            self.scratch = torch.empty(self._bytes, dtype=torch.uint8, device=self.status.device)
+            with torch.cuda.stream(stream):
+                self.scratch = torch.empty(self._bytes, dtype=torch.uint8, device=self.status.device)
+            self._streams.clear()
         pd, ldd = self._mat(dout, self.N, dout.dtype, "dout")
         po, ldo = self._mat(out, self.V, out.dtype, "out")
         pb, ldb = (None, self.D) if base is None else self._mat(base, self.V, out.dtype, "base")
         r = self.lib.dspark_embed_grad(pd, code, ldd, _vec(idx, self.N, torch.int32, "idx"), self.N, self.V, self.D,
                                        scale, pb, ldb, po, _dtype_code(out, "out"), ldo, self.scratch.data_ptr(),
-                                       self.status.data_ptr(), _raw_stream(stream, dout.device.index))
+                                       self.status.data_ptr(), self._on(stream))
         _check(r, "dspark_embed_grad")
         return out
 
 
-class GradClip:
+class GradClip(_TrainOp):
     """The 2-norm over a list of gradient tensors and their scaling to a largest
     norm (``dspark_clip_grads``), in place or into ``outs``. The object keeps
     the list (and the scratch and status word): make it for the gradient buffers
     that a training loop reuses. Tensors are contiguous, bf16 or fp32."""
 
     def __init__(self, grads: Sequence[torch.Tensor], outs: Optional[Sequence[torch.Tensor]] = None):
+        super().__init__()
         self.lib = load()
         self.grads = list(grads)
         self.outs = self.grads if outs is None else list(outs)
@@ -645,17 +675,13 @@ class GradClip:
         self.norm = torch.zeros((), dtype=torch.float32, device=device)
         self.status = torch.zeros(1, dtype=torch.int32, device=device)
 
-    def device_status(self) -> int:
-        """The first device error since the last reset (synchronises)."""
-        return int(self.status.item())
-
-    def reset(self) -> None:
-        self.status.zero_()
+    def _buffers(self):
+        return (self.scratch, self.norm, self.status)
 
     def clip(self, max_norm: float, stream=None) -> torch.Tensor:
         """Scale the gradients; returns their norm before that (a device fp32 scalar)."""
         code = self.lib.dspark_clip_grads(self.count, self._in, self._out, self._numel, self._types, max_norm,
                                           self.norm.data_ptr(), self.scratch.data_ptr(), self.status.data_ptr(),
-                                          _raw_stream(stream, self.norm.device.index))
+                                          self._on(stream))
         _check(code, "dspark_clip_grads")
         return self.norm
