@@ -164,10 +164,11 @@ def _dtype_code(t: torch.Tensor, name: str) -> int:
     raise DsparkError(f"{name} must be bf16 or fp32, got {t.dtype}")
 
 
-def _rows(t: torch.Tensor, rows: int, cols: int, dtype, name: str):
-    """Address and leading dimension of a matrix whose rows are contiguous."""
-    if t.dtype != dtype or not t.is_cuda or t.dim() != 2:
-        raise DsparkError(f"{name} must be a CUDA matrix of {dtype}, got {list(t.shape)} {t.dtype} on {t.device}")
+def _rows(t: torch.Tensor, rows: int, cols: int, dtype, name: str, device: int):
+    """Address and leading dimension of a matrix on CUDA device ``device`` whose rows are contiguous."""
+    if t.dtype != dtype or t.get_device() != device or t.dim() != 2:
+        raise DsparkError(f"{name} must be a matrix of {dtype} on cuda:{device}, got {list(t.shape)} {t.dtype} on "
+                          f"{t.device}")
     r, c = t.shape
     if r != rows or c != cols:
         raise DsparkError(f"{name} must be [{rows}, {cols}], got {list(t.shape)}")
@@ -177,24 +178,20 @@ def _rows(t: torch.Tensor, rows: int, cols: int, dtype, name: str):
     return t.data_ptr(), (ld if r > 1 else -(-c // 8) * 8)
 
 
-def _vec(t: Optional[torch.Tensor], n: int, dtype, name: str):
-    """Address of a contiguous vector of n values (None: no vector)."""
+def _vec(t: Optional[torch.Tensor], n: int, dtype, name: str, device: int):
+    """Address of a contiguous vector of n values on CUDA device ``device`` (None: no vector)."""
     if t is None:
         return None
-    if t.dtype != dtype or not t.is_cuda or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
-        raise DsparkError(f"{name} must be a contiguous CUDA vector [{n}] of {dtype}, got {list(t.shape)} {t.dtype} "
-                          f"on {t.device}")
+    if t.dtype != dtype or t.get_device() != device or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        raise DsparkError(f"{name} must be a contiguous vector [{n}] of {dtype} on cuda:{device}, got {list(t.shape)} "
+                          f"{t.dtype} on {t.device}")
     return t.data_ptr()
 
 
-# torch's own short way to a device's current stream, where it has one
+# torch's own short ways to the current device and a device's current stream, where it has them
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda device: torch.cuda.current_stream(device).cuda_stream)
-
-
-def _raw_stream(stream, device: int) -> int:
-    """Address of the stream (the current one of the device if None)."""
-    return _current_stream(device) if stream is None else stream.cuda_stream
 
 
 def _stream(stream) -> C.c_void_p:
@@ -471,23 +468,34 @@ class Workspace:
 
 
 class _TrainOp:
-    """What the training operators' objects share. Memory that a call makes
+    """What the training operators' objects share. A call takes tensors of the
+    object's device and runs there, whichever device is current. Memory that it makes
     belongs to the stream it runs on; the object's own buffers (``_buffers``) are
     noted with every stream that a call uses, so that their memory is not given
     away while that stream's work on them goes on."""
 
-    def __init__(self):
+    def __init__(self, device):
+        self.status = torch.zeros(1, dtype=torch.int32, device=device)
+        self._index = self.status.get_device()
         self._streams = set()
 
     def _buffers(self):
         return (self.scratch, self.status)
 
+    def _call(self, f, *args) -> int:
+        if _current_device() == self._index:
+            return f(*args)
+        with torch.cuda.device(self._index):
+            return f(*args)
+
     def _on(self, stream) -> int:
         """Address of the stream that a call runs on (the current one if None)."""
-        raw = _raw_stream(stream, self.status.device.index)
+        raw = _current_stream(self._index) if stream is None else stream.cuda_stream
         if raw not in self._streams:
-            self._streams.add(raw)
             stream = torch.cuda.current_stream(self.status.device) if stream is None else stream
+            if stream.device != self.status.device:
+                raise DsparkError(f"the stream belongs to {stream.device}, the object to {self.status.device}")
+            self._streams.add(raw)
             for t in self._buffers():
                 t.record_stream(stream)
         return raw
@@ -512,7 +520,6 @@ class LinearCE(_TrainOp):
     a multiple of 4) or None; target [N] int32, -1 for a row left out."""
 
     def __init__(self, N: int, K: int, V: int, layout: str = "vk", device="cuda"):
-        super().__init__()
         self.lib = load()
         if layout not in LAYOUTS:
             raise DsparkError(f"layout must be one of {sorted(LAYOUTS)}, got {layout!r}")
@@ -522,7 +529,7 @@ class LinearCE(_TrainOp):
         if nbytes == 0:
             raise DsparkError(f"dspark_linear_ce: unsupported N={N}, K={K}, V={V}")
         self.scratch = torch.empty(nbytes, dtype=torch.uint8, device=device)
-        self.status = torch.zeros(1, dtype=torch.int32, device=device)
+        super().__init__(device)
 
     @property
     def w_shape(self):
@@ -544,12 +551,13 @@ class LinearCE(_TrainOp):
         return out
 
     def _inputs(self, d, X, W, target, U):
-        px, d.ldx = _rows(X, self.N, self.K, torch.bfloat16, "X")
-        pw, d.ldw = _rows(W, *self.w_shape, torch.bfloat16, "W")
+        dev = self._index
+        px, d.ldx = _rows(X, self.N, self.K, torch.bfloat16, "X", dev)
+        pw, d.ldw = _rows(W, *self.w_shape, torch.bfloat16, "W", dev)
         pu = None
         if U is not None:
-            pu, d.ldu = _rows(U, self.N, self.V, torch.float32, "U")
-        return px, pw, pu, _vec(target, self.N, torch.int32, "target")
+            pu, d.ldu = _rows(U, self.N, self.V, torch.float32, "U", dev)
+        return px, pw, pu, _vec(target, self.N, torch.int32, "target", dev)
 
     def _dims(self):
         return LceDims(self.N, self.K, self.V, LAYOUTS[self.layout], 0, 0, 0, 0, 0)
@@ -561,10 +569,10 @@ class LinearCE(_TrainOp):
                 out = self.new_outputs(False, False)
         d = self._dims()
         ins = self._inputs(d, X, W, target, U)
-        f32 = torch.float32
-        code = self.lib.dspark_linear_ce(C.byref(d), *ins, _vec(out["loss"], self.N, f32, "loss"),
-                                         _vec(out["lse"], self.N, f32, "lse"), self.scratch.data_ptr(),
-                                         self.status.data_ptr(), self._on(stream))
+        f32, dev = torch.float32, self._index
+        pl, ps = _vec(out["loss"], self.N, f32, "loss", dev), _vec(out["lse"], self.N, f32, "lse", dev)
+        code = self._call(self.lib.dspark_linear_ce, C.byref(d), *ins, pl, ps, self.scratch.data_ptr(),
+                          self.status.data_ptr(), self._on(stream))
         _check(code, "dspark_linear_ce")
         return out
 
@@ -576,15 +584,15 @@ class LinearCE(_TrainOp):
                 out = self.new_outputs()
         d = self._dims()
         ins = self._inputs(d, X, W, target, U)
-        f32, bf16 = torch.float32, torch.bfloat16
+        f32, bf16, dev = torch.float32, torch.bfloat16, self._index
         px = pw = None
         if out.get("dX") is not None:
-            px, d.lddx = _rows(out["dX"], self.N, self.K, bf16, "dX")
+            px, d.lddx = _rows(out["dX"], self.N, self.K, bf16, "dX", dev)
         if out.get("dW") is not None:
-            pw, d.lddw = _rows(out["dW"], *self.w_shape, bf16, "dW")
-        code = self.lib.dspark_linear_ce_grad(C.byref(d), *ins, _vec(lse, self.N, f32, "lse"),
-                                              _vec(wt, self.N, f32, "wt"), scale, px, pw, self.scratch.data_ptr(),
-                                              self.status.data_ptr(), self._on(stream))
+            pw, d.lddw = _rows(out["dW"], *self.w_shape, bf16, "dW", dev)
+        ps, pt = _vec(lse, self.N, f32, "lse", dev), _vec(wt, self.N, f32, "wt", dev)
+        code = self._call(self.lib.dspark_linear_ce_grad, C.byref(d), *ins, ps, pt, scale, px, pw,
+                          self.scratch.data_ptr(), self.status.data_ptr(), self._on(stream))
         _check(code, "dspark_linear_ce_grad")
         return out
 
@@ -597,20 +605,19 @@ class Embedding(_TrainOp):
     rows; idx [N] int32, -1 for a row without a token."""
 
     def __init__(self, N: int, V: int, D: int, device="cuda"):
-        super().__init__()
         self.lib = load()
         self.N, self.V, self.D = int(N), int(V), int(D)
         self._bytes = int(self.lib.dspark_embed_grad_scratch_bytes(self.N, self.V, self.D))
         if self._bytes == 0:
             raise DsparkError(f"dspark_embed: unsupported N={N}, V={V}, D={D}")
         self.scratch: Optional[torch.Tensor] = None
-        self.status = torch.zeros(1, dtype=torch.int32, device=device)
+        super().__init__(device)
 
     def _buffers(self):
         return (self.status,) if self.scratch is None else (self.scratch, self.status)
 
     def _mat(self, t, rows, dtype, name):
-        return _rows(t, rows, self.D, dtype, name)
+        return _rows(t, rows, self.D, dtype, name, self._index)
 
     def lookup(self, E, idx, scale: float = 1.0, out=None, stream=None):
         """scale * E[idx] as [N, D] in E's type (into ``out`` if given)."""
@@ -620,8 +627,9 @@ class Embedding(_TrainOp):
                 out = torch.empty(self.N, self.D, dtype=E.dtype, device=E.device)
         pe, lde = self._mat(E, self.V, E.dtype, "E")
         po, ldo = self._mat(out, self.N, E.dtype, "out")
-        r = self.lib.dspark_embed(pe, code, lde, self.V, self.D, _vec(idx, self.N, torch.int32, "idx"), self.N,
-                                  scale, po, ldo, self.status.data_ptr(), self._on(stream))
+        pi = _vec(idx, self.N, torch.int32, "idx", self._index)
+        r = self._call(self.lib.dspark_embed, pe, code, lde, self.V, self.D, pi, self.N, scale, po, ldo,
+                       self.status.data_ptr(), self._on(stream))
         _check(r, "dspark_embed")
         return out
 
@@ -640,9 +648,9 @@ class Embedding(_TrainOp):
         pd, ldd = self._mat(dout, self.N, dout.dtype, "dout")
         po, ldo = self._mat(out, self.V, out.dtype, "out")
         pb, ldb = (None, self.D) if base is None else self._mat(base, self.V, out.dtype, "base")
-        r = self.lib.dspark_embed_grad(pd, code, ldd, _vec(idx, self.N, torch.int32, "idx"), self.N, self.V, self.D,
-                                       scale, pb, ldb, po, _dtype_code(out, "out"), ldo, self.scratch.data_ptr(),
-                                       self.status.data_ptr(), self._on(stream))
+        pi = _vec(idx, self.N, torch.int32, "idx", self._index)
+        r = self._call(self.lib.dspark_embed_grad, pd, code, ldd, pi, self.N, self.V, self.D, scale, pb, ldb, po,
+                       _dtype_code(out, "out"), ldo, self.scratch.data_ptr(), self.status.data_ptr(), self._on(stream))
         _check(r, "dspark_embed_grad")
         return out
 
@@ -654,7 +662,6 @@ class GradClip(_TrainOp):
     that a training loop reuses. Tensors are contiguous, bf16 or fp32."""
 
     def __init__(self, grads: Sequence[torch.Tensor], outs: Optional[Sequence[torch.Tensor]] = None):
-        super().__init__()
         self.lib = load()
         self.grads = list(grads)
         self.outs = self.grads if outs is None else list(outs)
@@ -663,6 +670,8 @@ class GradClip(_TrainOp):
         for i, (g, o) in enumerate(zip(self.grads, self.outs)):
             _ptr(g, None, f"grads[{i}]")
             _ptr(o, g.dtype, f"outs[{i}]")
+            if g.device != self.grads[0].device or o.device != g.device:
+                raise DsparkError(f"grads[{i}] on {g.device}, outs[{i}] on {o.device}: all must be on one device")
             if o.shape != g.shape:
                 raise DsparkError(f"outs[{i}] must be {list(g.shape)}, got {list(o.shape)}")
         n = self.count = len(self.grads)
@@ -673,15 +682,15 @@ class GradClip(_TrainOp):
         device = self.grads[0].device if n else "cuda"
         self.scratch = torch.empty(int(self.lib.dspark_clip_grads_scratch_bytes(n)), dtype=torch.uint8, device=device)
         self.norm = torch.zeros((), dtype=torch.float32, device=device)
-        self.status = torch.zeros(1, dtype=torch.int32, device=device)
+        super().__init__(device)
 
     def _buffers(self):
         return (self.scratch, self.norm, self.status)
 
     def clip(self, max_norm: float, stream=None) -> torch.Tensor:
         """Scale the gradients; returns their norm before that (a device fp32 scalar)."""
-        code = self.lib.dspark_clip_grads(self.count, self._in, self._out, self._numel, self._types, max_norm,
-                                          self.norm.data_ptr(), self.scratch.data_ptr(), self.status.data_ptr(),
-                                          self._on(stream))
+        code = self._call(self.lib.dspark_clip_grads, self.count, self._in, self._out, self._numel, self._types,
+                          max_norm, self.norm.data_ptr(), self.scratch.data_ptr(), self.status.data_ptr(),
+                          self._on(stream))
         _check(code, "dspark_clip_grads")
         return self.norm

@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "dspark.h"
 
 namespace dspark {
@@ -146,6 +148,20 @@ cudaError_t launch_ex(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t sm
   cfg.attrs = at;
   cfg.numAttrs = pdl ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+}
+
+// Runs `configure` (kernel attributes, which belong to the current device) on the
+// first call on each device; `done` holds a bit per device.
+template <typename F>
+cudaError_t once_per_device(std::atomic<uint64_t>& done, F&& configure) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev >= 0 && dev < 64 ? (uint64_t)1 << dev : 0;  // devices past 64: every time
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = configure();
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
 }
 
 // Launchers: return cudaGetLastError() of their launches; add their launch

@@ -830,18 +830,16 @@ dspark_status em_fail(cudaError_t e) {
 }
 
 cudaError_t em_sort(const int32_t* idx, int N, int V, char* base, const EmScratch& s, int* status, cudaStream_t st) {
-  static bool configured = false;
-  if (!configured) {
-    cudaError_t e = cudaFuncSetAttribute(k_sort_place<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSoSmem);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(k_sort_place<4>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSoSmem);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(k_sort_cluster<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSoSmem);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(k_sort_cluster<4>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSoSmem);
-    if (e != cudaSuccess) return e;
-    configured = true;
-  }
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t c = once_per_device(done, [] {
+    const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
+    cudaError_t e = cudaFuncSetAttribute(k_sort_place<2>, attr, (int)kSoSmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(k_sort_place<4>, attr, (int)kSoSmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(k_sort_cluster<1>, attr, (int)kSoSmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(k_sort_cluster<4>, attr, (int)kSoSmem);
+    return e;
+  });
+  if (c != cudaSuccess) return c;
   int width = 1;
   while (width < 24 && (1 << width) < V) ++width;
   const int passes = (width + kSoBits - 1) / kSoBits, bits = (width + passes - 1) / passes;
@@ -893,13 +891,12 @@ cudaError_t em_sum(const SuArgs& a, const void* dout, const int32_t* idx, int N,
     return launch_ex(k_embed_few<TI, TO, VEC>, dim3((a.V + kDiVocab - 1) / kDiVocab, (a.D + kEmSpan - 1) / kEmSpan),
                      dim3(256), 0, st, true, a, static_cast<const TI*>(dout), idx, N, static_cast<const TO*>(base),
                      static_cast<TO*>(dE), base == dE ? 1 : 0, status);
-  static bool configured = false;
-  if (!configured) {
-    const cudaError_t c = cudaFuncSetAttribute(k_embed_sum<TI, TO, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)su_smem<TI>());
-    if (c != cudaSuccess) return c;
-    configured = true;
-  }
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t c = once_per_device(done, [] {
+    return cudaFuncSetAttribute(k_embed_sum<TI, TO, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)su_smem<TI>());
+  });
+  if (c != cudaSuccess) return c;
   const int spans = (a.D + kEmSpan - 1) / kEmSpan;
   const TO* b = static_cast<const TO*>(base);
   TO* o = static_cast<TO*>(dE);

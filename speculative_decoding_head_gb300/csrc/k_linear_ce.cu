@@ -1176,13 +1176,13 @@ bool dims_ok(const dspark_lce_dims* d) {
 bool ld_ok(int64_t ld, int64_t cols, int mult) { return ld >= cols && ld % mult == 0 && ld < ((int64_t)1 << 32); }
 
 cudaError_t lce_configure() {
-  static bool configured = false;
-  if (configured) return cudaSuccess;
-  cudaError_t e = cudaSuccess;
-  for (const auto k : {k_lce<false, false>, k_lce<false, true>, k_lce<true, false>, k_lce<true, true>})
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kLcSmem);
-  if (e == cudaSuccess) configured = true;
-  return e;
+  static std::atomic<uint64_t> done{0};
+  return once_per_device(done, [] {
+    cudaError_t e = cudaSuccess;
+    for (const auto k : {k_lce<false, false>, k_lce<false, true>, k_lce<true, false>, k_lce<true, true>})
+      if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kLcSmem);
+    return e;
+  });
 }
 
 // One launch: the statistics, or up to three of the gradient's products (the
