@@ -483,6 +483,14 @@ size_t dspark_embed_grad_scratch_bytes(int N, int V, int D);
 dspark_status dspark_clip_grads(int count, const void* const* in, void* const* out, const int64_t* numel,
                                 const int32_t* types, float max_norm, float* norm, void* scratch,
                                 int32_t* device_status, dspark_stream_t stream);
+/* The same over matrices of rows[i] x cols[i] values, rows ldi[i] (in) and ldo[i]
+ * (out) values apart: gradients with padded rows, such as dspark_linear_ce_grad's.
+ * What lies between the rows is neither read nor written. Leading dimensions are at
+ * least cols[i] (not looked at for one row); in place they are equal. */
+dspark_status dspark_clip_grads_rows(int count, const void* const* in, void* const* out, const int64_t* rows,
+                                     const int64_t* cols, const int64_t* ldi, const int64_t* ldo, const int32_t* types,
+                                     float max_norm, float* norm, void* scratch, int32_t* device_status,
+                                     dspark_stream_t stream);
 size_t dspark_clip_grads_scratch_bytes(int count);
 
 #ifdef __cplusplus

@@ -30,7 +30,7 @@ SYMBOLS = [
     "dspark_ws_set_shard", "dspark_plan_shard",
     "dspark_linear_ce", "dspark_linear_ce_grad", "dspark_linear_ce_scratch_bytes",
     "dspark_embed", "dspark_embed_grad", "dspark_embed_grad_scratch_bytes",
-    "dspark_clip_grads", "dspark_clip_grads_scratch_bytes",
+    "dspark_clip_grads", "dspark_clip_grads_rows", "dspark_clip_grads_scratch_bytes",
 ]
 
 
@@ -129,6 +129,8 @@ def load() -> C.CDLL:
         lib.dspark_embed_grad_scratch_bytes.restype = C.c_size_t
         lib.dspark_clip_grads.argtypes = [i32, P, P, P, P, f, P, P, P, P]
         lib.dspark_clip_grads.restype = i32
+        lib.dspark_clip_grads_rows.argtypes = [i32] + [P] * 7 + [f] + [P] * 4
+        lib.dspark_clip_grads_rows.restype = i32
         lib.dspark_clip_grads_scratch_bytes.argtypes = [i32]
         lib.dspark_clip_grads_scratch_bytes.restype = C.c_size_t
         _lib = lib
@@ -659,7 +661,8 @@ class GradClip(_TrainOp):
     """The 2-norm over a list of gradient tensors and their scaling to a largest
     norm (``dspark_clip_grads``), in place or into ``outs``. The object keeps
     the list (and the scratch and status word): make it for the gradient buffers
-    that a training loop reuses. Tensors are contiguous, bf16 or fp32."""
+    that a training loop reuses. Tensors are bf16 or fp32 and contiguous, or
+    matrices with contiguous rows (``dspark_clip_grads_rows``)."""
 
     def __init__(self, grads: Sequence[torch.Tensor], outs: Optional[Sequence[torch.Tensor]] = None):
         self.lib = load()
@@ -668,8 +671,8 @@ class GradClip(_TrainOp):
         if len(self.outs) != len(self.grads):
             raise DsparkError(f"{len(self.grads)} gradients, {len(self.outs)} outputs")
         for i, (g, o) in enumerate(zip(self.grads, self.outs)):
-            _ptr(g, None, f"grads[{i}]")
-            _ptr(o, g.dtype, f"outs[{i}]")
+            self._layout(g, None, f"grads[{i}]")
+            self._layout(o, g.dtype, f"outs[{i}]")
             if g.device != self.grads[0].device or o.device != g.device:
                 raise DsparkError(f"grads[{i}] on {g.device}, outs[{i}] on {o.device}: all must be on one device")
             if o.shape != g.shape:
@@ -677,20 +680,38 @@ class GradClip(_TrainOp):
         n = self.count = len(self.grads)
         self._in = (C.c_void_p * max(n, 1))(*[g.data_ptr() for g in self.grads])
         self._out = (C.c_void_p * max(n, 1))(*[o.data_ptr() for o in self.outs])
-        self._numel = (C.c_int64 * max(n, 1))(*[g.numel() for g in self.grads])
+        i64 = C.c_int64 * max(n, 1)
+        if all(t.is_contiguous() for t in (*self.grads, *self.outs)):
+            self._f, self._shape = self.lib.dspark_clip_grads, (i64(*[g.numel() for g in self.grads]),)
+        else:
+            lay = [(self._layout(g, None, ""), self._layout(o, None, "")) for g, o in zip(self.grads, self.outs)]
+            # a matrix's rows, unless both of a pair are contiguous: those are one row
+            flat = [a is None and b is None for a, b in lay]
+            shape = [(1, g.numel()) if f else tuple(g.shape) for f, g in zip(flat, self.grads)]
+            ld = [[c if x is None else x for x, (_, c) in zip(side, shape)] for side in zip(*lay)]
+            self._f = self.lib.dspark_clip_grads_rows
+            self._shape = (i64(*[r for r, _ in shape]), i64(*[c for _, c in shape]), i64(*ld[0]), i64(*ld[1]))
         self._types = (C.c_int32 * max(n, 1))(*[_dtype_code(g, f"grads[{i}]") for i, g in enumerate(self.grads)])
         device = self.grads[0].device if n else "cuda"
         self.scratch = torch.empty(int(self.lib.dspark_clip_grads_scratch_bytes(n)), dtype=torch.uint8, device=device)
         self.norm = torch.zeros((), dtype=torch.float32, device=device)
         super().__init__(device)
 
+    @staticmethod
+    def _layout(t: torch.Tensor, dtype, name: str) -> Optional[int]:
+        """None for a contiguous tensor, the leading dimension of a matrix with contiguous rows; others are refused."""
+        if t.is_contiguous() or t.dim() != 2 or t.stride(0) < t.shape[1] or (t.stride(1) != 1 and t.shape[1] > 1):
+            _ptr(t, dtype, name)
+            return None
+        _ptr(t[0], dtype, name)
+        return t.stride(0)
+
     def _buffers(self):
         return (self.scratch, self.norm, self.status)
 
     def clip(self, max_norm: float, stream=None) -> torch.Tensor:
         """Scale the gradients; returns their norm before that (a device fp32 scalar)."""
-        code = self._call(self.lib.dspark_clip_grads, self.count, self._in, self._out, self._numel, self._types,
-                          max_norm, self.norm.data_ptr(), self.scratch.data_ptr(), self.status.data_ptr(),
-                          self._on(stream))
+        code = self._call(self._f, self.count, self._in, self._out, *self._shape, self._types, max_norm,
+                          self.norm.data_ptr(), self.scratch.data_ptr(), self.status.data_ptr(), self._on(stream))
         _check(code, "dspark_clip_grads")
         return self.norm

@@ -3,10 +3,12 @@
 Runs without a GPU: nothing is launched.
 """
 
+import ctypes as C
+
 import pytest
 import torch
 
-from speculative_decoding_head_gb300 import binding
+from speculative_decoding_head_gb300 import binding, build
 from speculative_decoding_head_gb300.binding import DsparkError
 
 ZERO, ONE = torch.device("cuda", 0), torch.device("cuda", 1)
@@ -111,8 +113,9 @@ def test_calls_run_on_the_objects_device(devices):
     E, idx, rows = (Stand((32, 16), torch.float32, ONE), Stand((8,), torch.int32, ONE), Stand((8, 16), torch.float32, ONE))
     emb.lookup(E, idx, out=rows)
     emb.grad(rows, idx, out=E)
-    clip = _object(binding.GradClip, devices, ONE, count=0, _in=None, _out=None, _numel=None, _types=None,
+    clip = _object(binding.GradClip, devices, ONE, count=0, _in=None, _out=None, _shape=(None,), _types=None,
                    norm=Stand((), torch.float32, ONE))
+    clip._f = clip.lib.dspark_clip_grads
     clip.clip(1.0)
     calls = ce.lib.calls + emb.lib.calls + clip.lib.calls
     assert len(calls) == 5
@@ -171,3 +174,42 @@ def test_streams_of_another_device_are_refused(devices):
     assert not ce.lib.calls
     ce.forward(t["X"], t["W"], t["target"], out=t["out"], stream=FakeStream(ONE, 77))
     assert ce.lib.calls[0][1:] == (1, 77) and len(ce.scratch.streams) == len(ce.status.streams) == 1
+
+
+def test_clip_rows_arguments():
+    build.build()
+    lib, ok = binding.load(), C.c_void_p(256)     # never dereferenced: the checks come first
+
+    def clip(n=1, ptr=256, out=256, rows=3, cols=10, ldi=16, ldo=16, type=0, max_norm=1.0, **kw):
+        a = {**dict(norm=ok, scratch=ok, st=ok), **kw}
+        arr = lambda t, v: (t * 1)(v)  # noqa: E731
+        return lib.dspark_clip_grads_rows(n, arr(C.c_void_p, ptr), arr(C.c_void_p, out), arr(C.c_int64, rows),
+                                          arr(C.c_int64, cols), arr(C.c_int64, ldi), arr(C.c_int64, ldo),
+                                          arr(C.c_int32, type), max_norm, a["norm"], a["scratch"], a["st"], None)
+
+    for kw in (dict(n=-1), dict(ptr=None), dict(out=None), dict(ptr=258), dict(ptr=257, type=1), dict(rows=-1),
+               dict(cols=-1), dict(ldi=9), dict(ldo=9), dict(ldi=-16), dict(ldi=24), dict(out=512, ldo=(1 << 44) + 1),
+               dict(rows=1 << 40, cols=32, ldi=32, ldo=32), dict(rows=(1 << 44) + 1, cols=0), dict(type=2),
+               dict(max_norm=-1.0), dict(max_norm=float("nan")), dict(norm=None), dict(scratch=None), dict(st=None),
+               dict(scratch=C.c_void_p(260))):
+        assert clip(**kw) == 1, kw
+    assert lib.dspark_clip_grads_rows(1, *([None] * 7), 1.0, ok, ok, ok, None) == 1
+
+
+def test_what_clip_takes_for_a_matrix():
+    """Contiguous tensors of any shape, and matrices whose rows are contiguous."""
+    lay = lambda t: binding.GradClip._layout(t, None, "t")  # noqa: E731
+
+    class Cuda(torch.Tensor):       # a CPU tensor that answers as a CUDA one
+        is_cuda = True
+
+    def of(*shape):
+        return torch.zeros(*shape).as_subclass(Cuda)
+
+    assert lay(of(3, 4, 5)) is None and lay(of(7)) is None and lay(of(0, 5)) is None and lay(of(6, 8)[:1, :3]) is None
+    assert lay(of(6, 8)[:, :5]) == 8 and lay(of(6, 8)[:, 7:]) == 8 and lay(of(6, 8)[::2]) == 16
+    for bad in (of(9)[::2], of(3, 4).t(), of(3, 4, 5)[:, :, :2], of(1, 5).expand(4, 5), of(4, 6)[:, ::2]):
+        with pytest.raises(DsparkError):
+            lay(bad)
+    with pytest.raises(DsparkError):
+        lay(torch.zeros(6, 8)[:, :5])
