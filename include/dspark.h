@@ -389,10 +389,12 @@ dspark_status dspark_pctree_verify(dspark_ws* ws, const float* P, const int32_t*
  * DSPARK_W_KV), U = U_k; a head that trains with its hidden state has
  * X = [h, W1[x_prev]] and W the output matrix beside W2's transpose. The
  * logits are not kept: the gradient call makes them again from lse, a piece
- * of the vocabulary at a time. Scratch holds two pieces of G (each at most 256
- * MiB, or 2048 columns), 16 bytes per row and 256 tokens for the forward, and
- * fp32 sums of shared tiles: dspark_linear_ce_scratch_bytes(dims) bytes, for
- * either call.
+ * of the vocabulary at a time. Scratch, dspark_linear_ce_scratch_bytes(dims) bytes
+ * for either call, is the larger of what the two need. The forward: at most 16 bytes
+ * per row and 256 tokens, or 9728 per row where that is more. The gradient: G of two
+ * pieces (each at most 1 GiB, or 2048 columns where those are more; one where it is the
+ * whole vocabulary), X once more, for several pieces 4 N K bytes of sums, and up to 80 MB
+ * of shared tiles' parts.
  *
  * X [N][ldx], W [V][ldw] (DSPARK_W_VK) or [K][ldw] (DSPARK_W_KV), dX [N][lddx]
  * and dW (W's layout, lddw) are bf16; U [N][ldu] (or NULL), loss, lse and wt

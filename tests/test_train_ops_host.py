@@ -213,3 +213,18 @@ def test_what_clip_takes_for_a_matrix():
             lay(bad)
     with pytest.raises(DsparkError):
         lay(torch.zeros(6, 8)[:, :5])
+
+
+@pytest.mark.parametrize("layout", [0, 1])
+@pytest.mark.parametrize("N,K,V", [(1, 1, 1), (6, 80, 1024), (64, 256, 151936), (65, 64, 4000), (640, 256, 129280), (1001, 4100, 50257),
+                                   (4096, 5376, 129280), (16384, 256, 129280), (32768, 256, 129280), (1 << 20, 64, 50257),
+                                   (64, 16, 600003), (300000, 8, 300), (5, 65536, 2000)])
+def test_scratch_is_what_the_header_says(N, K, V, layout):
+    """The sizes that include/dspark.h gives, and no more than their roundings beside them."""
+    build.build()
+    got = binding.load().dspark_linear_ce_scratch_bytes(C.byref(binding.LceDims(N, K, V, layout, 0, 0, 0, 0, 0)))
+    up = lambda x, m: -(-x // m) * m  # noqa: E731
+    forward = N * max(16 * -(-V // 256), 9728) + 4 * N
+    piece = min(2 * N * up(V, 64), max(1 << 30, 2 * N * 2048))
+    gradient = 2 * piece + 2 * max(N * up(K, 8), K * up(N, 8)) + 4 * max(up(N, 32) * K, up(K, 32) * N) + 80_000_000
+    assert 0 < got <= max(forward, gradient) + 8 * 256, (got, forward, gradient)
