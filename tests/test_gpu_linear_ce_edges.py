@@ -123,3 +123,43 @@ def test_behind_a_long_kernel_that_lets_it_start(N, K, V, layout, tmp_path_facto
     assert op.device_status() == 0
     for k in first:
         assert torch.equal(out[k], first[k]), k
+
+
+def _launches(op, *a, **kw):
+    """Kernels of one gradient call (the nodes of a graph that records it)."""
+    g = torch.cuda.CUDAGraph(keep_graph=True)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        op.grad(*a, **kw)
+    n = C.c_size_t(0)
+    assert C.CDLL("libcudart.so.13").cudaGraphGetNodes(C.c_void_p(g.raw_cuda_graph()), None, C.byref(n)) == 0
+    return n.value
+
+
+@pytest.mark.parametrize("layout", ["vk", "kv"])
+@pytest.mark.parametrize("N,K,V,U", [(64, 16, 600003, True), (33, 24, 1100003, False)])
+def test_few_rows_and_pieces(N, K, V, U, layout):
+    """Tokens as rows of the logits' product, the vocabulary in two pieces:
+    targets at both sides of where the second begins, and at the ends."""
+    X, W, Um, t, wt = _inputs(N, K, V, layout, U, 0, 0.1)
+    half = -(-(-(-V // 2)) // 256) * 256
+    t[:8] = torch.tensor([half - 1, half, half + 1, half - 257, half + 255, 0, V - 1, -1], dtype=torch.int32)
+    op, out = _check(X, W, Um, t, wt, 1.0, layout)
+    # a launch that makes G alone, one a piece, and at most the transpose and a join
+    assert 3 <= _launches(op, X, W, t, out["lse"], wt=wt, U=Um, out=out) <= 5
+    one = LinearCE(N, K, 10000, layout)
+    w = W[:10000] if layout == "vk" else W[:, :10000]
+    u = Um[:, :10000] if U else None
+    assert _launches(one, X, w, t % 10000, out["lse"], wt=wt, U=u, out=one.new_outputs()) < _launches(
+        op, X, W, t, out["lse"], wt=wt, U=Um, out=out)
+
+
+@pytest.mark.parametrize("layout", ["vk", "kv"])
+def test_long_contraction_and_pieces(layout):
+    """K of 1024 and more and several pieces, the last one narrower, with targets about their edge."""
+    N, K, V = 4100, 1030, 40003
+    X, W, _, t, wt = _inputs(N, K, V, layout, False, 0, 0.1)
+    half = -(-(-(-V // 2)) // 256) * 256
+    t[:4] = torch.tensor([half - 1, half, 0, V - 1], dtype=torch.int32)
+    op, out = _check(X, W, None, t, wt, 1.0, layout)
+    assert _launches(op, X, W, t, out["lse"], wt=wt, out=out) >= 4     # the transpose, G alone, a launch a piece
