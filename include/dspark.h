@@ -415,7 +415,9 @@ dspark_status dspark_pctree_verify(dspark_ws* ws, const float* P, const int32_t*
  * 1e38 make the row's results NaN, and with them dW. N = 0 is allowed (dW is then
  * 0). 0 <= N <= 2^20, K <= 65536, V <= 2^24, else DSPARK_EINVAL. The tensor cores
  * cut their fp32 accumulator once per 16 terms; with the mean of that made up for,
- * lse is off by about 1.3e-10 K of itself on random rows (5e-7 at K = 4096).
+ * lse is off by about 1.3e-10 K of itself on random rows (5e-7 at K = 4096, 2e-6 at
+ * 16384). A logit whose terms all come last, or whose products are mostly zero, is off
+ * by 1.3e-9 K of itself; one that grows to A on its way, by up to 7.5e-9 K A.
  * Asynchronous on `stream`; each result is the same from call to call (dX's
  * grouping of sums may differ between calls with and without dW).
  */

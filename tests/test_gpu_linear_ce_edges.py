@@ -13,7 +13,7 @@ import torch
 from speculative_decoding_head_gb300 import build
 from speculative_decoding_head_gb300.binding import LinearCE
 
-from test_gpu_linear_ce import BF16, _check, _close, _inputs, _reference
+from test_gpu_linear_ce import BF16, F64, _check, _close, _inputs, _reference
 
 pytestmark = pytest.mark.gpu
 
@@ -163,3 +163,52 @@ def test_long_contraction_and_pieces(layout):
     t[:4] = torch.tensor([half - 1, half, 0, V - 1], dtype=torch.int32)
     op, out = _check(X, W, None, t, wt, 1.0, layout)
     assert _launches(op, X, W, t, out["lse"], wt=wt, out=out) >= 4     # the transpose, G alone, a launch a piece
+
+
+@pytest.mark.parametrize("layout,U", [("vk", False), ("vk", True), ("kv", False)])
+@pytest.mark.parametrize("N,K", [(192, 4096), (128, 16384), (48, 4096)])
+def test_what_the_accumulator_cuts_off_is_made_up_for(N, K, layout, U):
+    """The mean over rows of lse's signed error. Cut once per 16 terms, a sum of n
+    steps that grows evenly loses 0.36 2^-23 (n + 1) / 2 of itself, so that
+    uncorrected lse is off by that times E_p[x w] (the logit's product part). At
+    least half of it has to be made up for: a factor left out, twice as large,
+    applied to U too or of the wrong sign is off by all of it or more. Beside it
+    there is lse's own rounding, of mean zero over the rows: 2^-24 |lse|."""
+    V = 8192
+    X, W, Um, t, _ = _inputs(N, K, V, layout, U)
+    lse = LinearCE(N, K, V, layout).forward(X, W, t, U=Um)["lse"].double()
+    dot = X.double() @ (W.double().t() if layout == "vk" else W.double())
+    z = dot + Um.double() if U else dot
+    ref = torch.logsumexp(z, 1)
+    shift = 0.36 * 2.0 ** -23 * (K / 16 + 1) / 2 * float((torch.softmax(z, 1) * dot).sum(1).mean())
+    mean = float((lse - ref).mean())
+    print(f"shift {shift:.3e}, mean error {mean:.3e}")
+    assert abs(mean) <= 0.5 * shift + 2.0 ** -24 * float(ref.abs().mean()), (mean, shift)
+
+
+@pytest.mark.parametrize("K", [4096, 65536])
+def test_logits_that_do_not_grow_evenly(K):
+    """The correction at its worst. Row 0's terms all come last (its sums are
+    cut once or twice): off by the whole factor. Row 1 grows to +-A and comes back to a
+    small rest: off by what is cut on the way, one unit of A per 16 terms at most."""
+    V = 1024
+    g = torch.Generator(device="cuda").manual_seed(11)
+    X = torch.zeros(2, K, dtype=BF16, device="cuda")
+    X[0, K - 16:] = torch.randn(16, generator=g, device="cuda").bfloat16()
+    X[1] = 1.0
+    X[1, K // 2:] = -1.0
+    W = torch.empty(V, K, dtype=BF16, device="cuda")
+    W[:, :K // 2] = (torch.rand(V, K // 2, generator=g, device="cuda") * 0.25).bfloat16()
+    W[:, K // 2:] = W[:, :K // 2]
+    W[:, K - 16:] += torch.randn(V, 16, generator=g, device="cuda").bfloat16()
+    t = torch.zeros(2, dtype=torch.int32, device="cuda")
+    out = LinearCE(2, K, V).forward(X, W, t)
+    z = X.double() @ W.double().t()
+    lse = torch.logsumexp(z, 1)
+    peak = float((X.double()[1, :K // 2] @ W.double()[:, :K // 2].t()).max())
+    step = 2.0 ** -23
+    bound = torch.tensor([0.36 * step * (K / 16 + 1) / 2 * float(z[0].abs().max()) + 4 * step * float(z[0].abs().max()),
+                          step * peak * (K / 16 + 8)], device="cuda", dtype=F64)
+    err = (out["lse"].double() - lse).abs()
+    print(f"K {K}: lse error {err.tolist()}, bound {bound.tolist()}")
+    assert (err <= bound + 2.0 ** -20 + 2.0 ** -22 * lse.abs()).all(), (err, bound)
