@@ -526,8 +526,9 @@ class LinearCE(_TrainOp):
         if layout not in LAYOUTS:
             raise DsparkError(f"layout must be one of {sorted(LAYOUTS)}, got {layout!r}")
         self.N, self.K, self.V, self.layout = int(N), int(K), int(V), layout
-        d = LceDims(self.N, self.K, self.V, LAYOUTS[layout], 0, 0, 0, 0, 0)
-        nbytes = int(self.lib.dspark_linear_ce_scratch_bytes(C.byref(d)))
+        self._dims = LceDims(self.N, self.K, self.V, LAYOUTS[layout], 0, 0, 0, 0, 0)
+        self._pdims = C.byref(self._dims)
+        nbytes = int(self.lib.dspark_linear_ce_scratch_bytes(self._pdims))
         if nbytes == 0:
             raise DsparkError(f"dspark_linear_ce: unsupported N={N}, K={K}, V={V}")
         self.scratch = torch.empty(nbytes, dtype=torch.uint8, device=device)
@@ -552,8 +553,8 @@ class LinearCE(_TrainOp):
             out["dW"] = mat(*self.w_shape)
         return out
 
-    def _inputs(self, d, X, W, target, U):
-        dev = self._index
+    def _inputs(self, X, W, target, U):
+        dev, d = self._index, self._dims
         px, d.ldx = _rows(X, self.N, self.K, torch.bfloat16, "X", dev)
         pw, d.ldw = _rows(W, *self.w_shape, torch.bfloat16, "W", dev)
         pu = None
@@ -561,19 +562,15 @@ class LinearCE(_TrainOp):
             pu, d.ldu = _rows(U, self.N, self.V, torch.float32, "U", dev)
         return px, pw, pu, _vec(target, self.N, torch.int32, "target", dev)
 
-    def _dims(self):
-        return LceDims(self.N, self.K, self.V, LAYOUTS[self.layout], 0, 0, 0, 0, 0)
-
     def forward(self, X, W, target, U=None, out=None, stream=None):
         """loss and lse of every row."""
         if out is None:
             with torch.cuda.stream(stream):
                 out = self.new_outputs(False, False)
-        d = self._dims()
-        ins = self._inputs(d, X, W, target, U)
+        ins = self._inputs(X, W, target, U)
         f32, dev = torch.float32, self._index
         pl, ps = _vec(out["loss"], self.N, f32, "loss", dev), _vec(out["lse"], self.N, f32, "lse", dev)
-        code = self._call(self.lib.dspark_linear_ce, C.byref(d), *ins, pl, ps, self.scratch.data_ptr(),
+        code = self._call(self.lib.dspark_linear_ce, self._pdims, *ins, pl, ps, self.scratch.data_ptr(),
                           self.status.data_ptr(), self._on(stream))
         _check(code, "dspark_linear_ce")
         return out
@@ -584,16 +581,15 @@ class LinearCE(_TrainOp):
         if out is None:
             with torch.cuda.stream(stream):
                 out = self.new_outputs()
-        d = self._dims()
-        ins = self._inputs(d, X, W, target, U)
+        ins = self._inputs(X, W, target, U)
         f32, bf16, dev = torch.float32, torch.bfloat16, self._index
         px = pw = None
         if out.get("dX") is not None:
-            px, d.lddx = _rows(out["dX"], self.N, self.K, bf16, "dX", dev)
+            px, self._dims.lddx = _rows(out["dX"], self.N, self.K, bf16, "dX", dev)
         if out.get("dW") is not None:
-            pw, d.lddw = _rows(out["dW"], *self.w_shape, bf16, "dW", dev)
+            pw, self._dims.lddw = _rows(out["dW"], *self.w_shape, bf16, "dW", dev)
         ps, pt = _vec(lse, self.N, f32, "lse", dev), _vec(wt, self.N, f32, "wt", dev)
-        code = self._call(self.lib.dspark_linear_ce_grad, C.byref(d), *ins, ps, pt, scale, px, pw,
+        code = self._call(self.lib.dspark_linear_ce_grad, self._pdims, *ins, ps, pt, scale, px, pw,
                           self.scratch.data_ptr(), self.status.data_ptr(), self._on(stream))
         _check(code, "dspark_linear_ce_grad")
         return out

@@ -94,7 +94,8 @@ def _object(cls, current, device, **fields):
 
 
 def _lce(current, device):
-    return _object(binding.LinearCE, current, device, N=8, K=16, V=32, layout="vk")
+    dims = binding.LceDims(8, 16, 32, 0)
+    return _object(binding.LinearCE, current, device, N=8, K=16, V=32, layout="vk", _dims=dims, _pdims=C.byref(dims))
 
 
 def _lce_tensors(device):
