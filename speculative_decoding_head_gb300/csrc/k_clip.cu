@@ -7,8 +7,8 @@
 // the first leaves a partial sum of squares per CTA, the second adds those in
 // order (every CTA the same way) and scales. The list of tensors travels in the
 // kernel's parameters, so a call keeps nothing on the device. Bound by memory,
-// read twice and written once: 400 M values in 301 tensors 497 us, 95% of the
-// measured copy rate; the head's 141 MB 76 us (82%: the two kernels' start and end
+// read twice and written once: 400 M values in 301 tensors 494 us, 95% of the
+// measured copy rate; the head's 141 MB 77 us (81%: the two kernels' start and end
 // are 6 us of it; L2 keeps nothing from the first pass to the second, in any
 // order of the pieces).
 //

@@ -1059,8 +1059,7 @@ int split_of(int tiles, int nkb) {
 // the pairs or fewer. A short contraction's time is mostly the epilogue's latency
 // (6 x 80 x 1024: step 22.1 -> 20.1 us), a long one's the operands', of which the
 // ring then holds more stages (234 x 5036 x 846 with U, 4 tiles: gradient of X 58 ->
-// 48 us; 64 x 4096 x 8000, 32 tiles: forward 33.4 -> 31.4, both with 12 us around
-// them; 1 x 3246 x 6451, 26 tiles, loses 3).
+// 48 us, with 12 us around it).
 int z_cols(int64_t N, int64_t cols) {
   const int t = tiles_of(N) * tiles_of(cols);
   return 2 * t > kLcPairs ? kLcTile : 4 * t > kLcPairs ? kLcTile / 2 : kLcTile / 4;
@@ -1082,9 +1081,10 @@ struct LcPlan {
   size_t G[2], dx_acc, dx_slots, dw_slots, XT, bwd_total;  // gradient
 };
 
-// G's piece: small enough to stay in L2 where the products are short (K below
+// G's piece: 64 MiB, which stay in L2, where the products are short (K below
 // 1024: its 6 bytes of traffic a value take as long as 6 K operations at K = 265),
-// else few launches. At least 64 tiles wide where a GiB allows: narrower pieces
+// else few launches. At least 64 tiles wide where a GiB allows, for long batches at the
+// price of L2: narrower pieces
 // have too few tiles of dW (K = 256, V = 129280: N = 4096 976 us in pieces of 32
 // tiles, 736 of 64; N = 16384 3.94 ms of 8, 2.84 of 64, 2.71 of 128).
 constexpr int64_t kLcPieceBytes = 256ll << 20, kLcPieceBytesL2 = 64ll << 20, kLcPieceMost = 1ll << 30;

@@ -1,8 +1,11 @@
 """Training the Markov head's W1 and W2 on the cross entropy of eq. (9).
 
+This is one term of the objective: ``Workspace.train_loss`` reports all three,
+weighted, and the other two have no gradients here.
+
 One step over a teacher-forced batch (B blocks of gamma positions): the rows
 W1[x_prev] (``Embedding.lookup``), the loss of z = U + W1[x_prev] W2 against
-the reference tokens (``LinearCE.forward``), the gradients of the batch loss
+the reference tokens (``LinearCE.forward``), the gradients of
 (1/B) sum exp(-k / tau) ce, eq. (12)'s weights (``LinearCE.grad``), the
 gradient of W1 by token (``Embedding.grad``), both gradients clipped together
 (``GradClip``), and a step of plain gradient descent on fp32 copies. The logits
@@ -45,7 +48,7 @@ class HeadTrainer:
 
     def step(self, U: torch.Tensor, anchor: torch.Tensor, xstar: torch.Tensor):
         """One step on U [B, gamma, V] fp32, anchor [B] and xstar [B, gamma]
-        int32 (-1: no token there, and none drafted from). Returns the batch
+        int32 (-1: no token there, and none drafted from). Returns that
         loss before the step and the gradients' norm, on the device. A norm that
         is not finite leaves the weights as they are (and sets the status)."""
         prev = torch.cat([anchor[:, None], xstar[:, :-1]], 1).reshape(-1)
