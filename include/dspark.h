@@ -497,6 +497,132 @@ dspark_status dspark_clip_grads_rows(int count, const void* const* in, void* con
                                      dspark_stream_t stream);
 size_t dspark_clip_grads_scratch_bytes(int count);
 
+/*
+ * An output layer held in 4 bits: matrices of microscaled floating point. Each
+ * value is an e2m1 number (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives), and
+ * each block of consecutive values of a row has a scale:
+ *   DSPARK_MXFP4  blocks of 32, scale s = 2^(floor(log2 amax) - 2) as e8m0
+ *                 (the OCP microscaling formats' rule), factor f = 1;
+ *   DSPARK_NVFP4  blocks of 16, scale s = amax / (6 f) as e4m3 (nearest, ties to
+ *                 even), where the row's factor f is the least power of two with
+ *                 row amax <= 2688 f (2688 = 6 * 448; f >= 2^-100, 1 for a row of zeros).
+ * amax is the largest magnitude of the block. A value x is held as the e2m1
+ * number nearest to x / (s f), ties to even, at most 6 in magnitude, and stands
+ * for that number times s f. All of it is exact: one result for every input. A block that
+ * holds a NaN or an infinity stands for NaN throughout (its scale is the
+ * format's NaN), has no part in its row's amax, and sets DSPARK_ENUMERIC.
+ *
+ * A matrix of `rows` rows of K values is three device buffers of the caller:
+ *   codes   dspark_fp4_code_bytes(dims), 16-byte aligned: rows of
+ *           ceil(K / 32) * 16 bytes, two values a byte, the even column low;
+ *           values past K are 0;
+ *   scales  dspark_fp4_scale_bytes(dims), 16-byte aligned, in the tensor cores' order:
+ *           tiles of 128 rows by 4 blocks, 512 bytes each, row i's block j at byte
+ *           16 (i mod 32) + 4 (i div 32) + j; the tiles of 256 columns follow one
+ *           another along the row, then the next 128 rows;
+ *   rowf    f of each row, fp32, ceil(rows / 128) * 128 of them, 16-byte aligned
+ *           (DSPARK_MXFP4: not looked at, may be NULL).
+ *
+ *   dspark_fp4_quant   X [rows][ldx], bf16 or fp32, into the three buffers;
+ *   dspark_fp4_rows    out[n] = the values of row idx[n], n < N (idx NULL: row n, N <= rows).
+ *       idx[n] = -1 gives a row of zeros; any other value outside [0, rows) does the
+ *       same and sets DSPARK_ERANGE. bf16 and fp32 hold the values exactly (but for
+ *       subnormals, and values past 3.4e38, which become infinite);
+ *   dspark_fp4_linear  Y[n][v] = sum_k x[n][k] w[v][k] (+ U[n][v]) over the values
+ *       that x (N rows) and w (V rows) stand for: of one format, with the same K.
+ *       The products are exact and summed in fp32 by the tensor cores; Y [N][ldy]
+ *       is fp32 or bf16 (rounded once), U [N][ldu] fp32 or NULL. U may be Y itself where
+ *       Y is fp32 and ldu == ldy.
+ *
+ * Any leading dimension of at least the row's length and any base address on
+ * the type's own size will do for X, out, U and Y; rows on 16 bytes run faster.
+ * rows, N and V <= 2^24, K <= 65536 and none of them negative (K, V and the table's rows at least 1), else
+ * DSPARK_EINVAL. N = 0 is allowed. *device_status is the caller's int32 and keeps
+ * its first error until the caller clears it. Asynchronous on `stream`, one launch
+ * each; results are the same from call to call.
+ */
+typedef enum { DSPARK_NVFP4 = 0, DSPARK_MXFP4 = 1 } dspark_fp4_format;
+
+typedef struct {
+    int rows;
+    int K;
+    int format;   /* dspark_fp4_format */
+} dspark_fp4_dims;
+
+typedef struct {
+    void* codes;
+    void* scales;
+    float* rowf;
+} dspark_fp4_data;
+
+size_t dspark_fp4_code_bytes(const dspark_fp4_dims* dims);
+size_t dspark_fp4_scale_bytes(const dspark_fp4_dims* dims);
+dspark_status dspark_fp4_quant(const dspark_fp4_dims* dims, const void* X, dspark_wdtype type, int64_t ldx,
+                               const dspark_fp4_data* out, int32_t* device_status, dspark_stream_t stream);
+dspark_status dspark_fp4_rows(const dspark_fp4_dims* dims, const dspark_fp4_data* m, const int32_t* idx, int N, void* out,
+                              dspark_wdtype type, int64_t ldo, int32_t* device_status, dspark_stream_t stream);
+dspark_status dspark_fp4_linear(const dspark_fp4_dims* xdims, const dspark_fp4_data* x, const dspark_fp4_dims* wdims,
+                                const dspark_fp4_data* w, const float* U, int64_t ldu, void* Y, dspark_wdtype type,
+                                int64_t ldy, int32_t* device_status, dspark_stream_t stream);
+
+/*
+ * Drawing from logits with the settings that users give, and the distribution
+ * that they make of a row. The round's own draws have temperature 1 and no
+ * truncation; a verify is lossless against any target, so with the target's rows
+ * through dspark_sample_logprobs first, a round emits what dspark_sample would.
+ *
+ * For each of N rows of V logits z (fp32 or bf16, rows ldz apart), with
+ * x_v = (z_v - max z) / T:
+ *   top-k   keeps the k tokens of largest z (k <= 0 or >= V: all);
+ *   top-p   of those, by falling z, keeps each whose predecessors' mass
+ *           sum e^x is less than p of the mass of all of them (p >= 1: all), and the
+ *           first in any case;
+ *   min-p   of those, keeps z_v >= max z + T log(min_p) (min_p = 0: all);
+ * equal z go by the lower token first. T = 0 is greedy: the lowest token of
+ * largest z alone. The settings are device arrays, temperature, top_p and min_p
+ * fp32 and top_k int32 (each may be NULL: 1, 1, 0 and 0), with an entry
+ * for each row, or, with row_off [requests + 1] (as dspark_plan writes it), for
+ * each request b, whose rows are row_off[b] .. row_off[b + 1] - 1; rows
+ * outside row_off[0] .. row_off[requests] - 1 are then neither read nor
+ * written. row_off must not fall.
+ *   dspark_sample           token[n]: the lowest kept v such that the kept tokens up to
+ *       v hold more than u[n] of the kept mass, u in [0, 1); logp[n] (may be NULL) its log-probability;
+ *   dspark_sample_logprobs  out[n][v] (fp32, rows ldo apart): the log-probability
+ *       x_v - log(kept mass), or `fill` where v is left out (-infinity, or a low finite
+ *       value, for a reader that wants one).
+ *
+ * z = -inf, or at most -1e29 (the type's lowest value among them), is a masked
+ * token, never kept. A row with every token masked has token -1, logp -inf and
+ * `fill` throughout. A row with a NaN or +inf, or a setting out of range
+ * (T not finite or negative, p or min_p not in [0, 1] or NaN, min_p above 1, u not in
+ * [0, 1)), has token -1, logp NaN and `fill` throughout, and sets DSPARK_ENUMERIC in
+ * *device_status (the caller's int32; the first error is kept until the caller clears it).
+ *
+ * Masses are whole numbers: e^x with a relative error of about 2^-31, rounded to a multiple
+ * of 2^-Q, Q = min(46, 62 - ceil(log2 V)). Their sums are exact, whatever the order, so a row's
+ * result depends on its logits and settings alone. 0 <= N <= 2^24, V <= 2^24, else
+ * DSPARK_EINVAL; any leading dimension of at least V and any base address on the type's own
+ * size will do; rows on 16 bytes run faster. Outputs must not overlap inputs. One launch,
+ * asynchronous on `stream`, no scratch.
+ */
+typedef struct {
+    int N;
+    int V;
+    int requests;              /* entries of the settings with row_off; not looked at without */
+    dspark_wdtype type;        /* of z */
+    int64_t ldz;
+    const int32_t* row_off;    /* or NULL */
+    const float* temperature;
+    const int32_t* top_k;
+    const float* top_p;
+    const float* min_p;
+} dspark_sample_args;
+
+dspark_status dspark_sample(const dspark_sample_args* args, const void* Z, const float* u, int32_t* token, float* logp,
+                            int32_t* device_status, dspark_stream_t stream);
+dspark_status dspark_sample_logprobs(const dspark_sample_args* args, const void* Z, float fill, float* out, int64_t ldo,
+                                     int32_t* device_status, dspark_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

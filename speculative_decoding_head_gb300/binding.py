@@ -19,6 +19,7 @@ from .build import LIB_PATH
 MODES = {"static": 0, "compact": 1, "lagged": 2}
 WDTYPES = {"f32": 0, "bf16": 1}
 LAYOUTS = {"vk": 0, "kv": 1}
+FP4_FORMATS = {"nvfp4": 0, "mxfp4": 1}
 
 SYMBOLS = [
     "dspark_ws_create", "dspark_ws_destroy", "dspark_ws_reset", "dspark_last_error",
@@ -31,6 +32,8 @@ SYMBOLS = [
     "dspark_linear_ce", "dspark_linear_ce_grad", "dspark_linear_ce_scratch_bytes",
     "dspark_embed", "dspark_embed_grad", "dspark_embed_grad_scratch_bytes",
     "dspark_clip_grads", "dspark_clip_grads_rows", "dspark_clip_grads_scratch_bytes",
+    "dspark_fp4_code_bytes", "dspark_fp4_scale_bytes", "dspark_fp4_quant", "dspark_fp4_rows", "dspark_fp4_linear",
+    "dspark_sample", "dspark_sample_logprobs",
 ]
 
 
@@ -46,6 +49,20 @@ class Dims(C.Structure):
 class LceDims(C.Structure):
     _fields_ = [("N", C.c_int), ("K", C.c_int), ("V", C.c_int), ("layout", C.c_int), ("ldx", C.c_int64),
                 ("ldw", C.c_int64), ("ldu", C.c_int64), ("lddx", C.c_int64), ("lddw", C.c_int64)]
+
+
+class Fp4Dims(C.Structure):
+    _fields_ = [("rows", C.c_int), ("K", C.c_int), ("format", C.c_int)]
+
+
+class Fp4Data(C.Structure):
+    _fields_ = [("codes", C.c_void_p), ("scales", C.c_void_p), ("rowf", C.c_void_p)]
+
+
+class SampleArgs(C.Structure):
+    _fields_ = [("N", C.c_int), ("V", C.c_int), ("requests", C.c_int), ("type", C.c_int), ("ldz", C.c_int64),
+                ("row_off", C.c_void_p), ("temperature", C.c_void_p), ("top_k", C.c_void_p), ("top_p", C.c_void_p),
+                ("min_p", C.c_void_p)]
 
 
 _lock = threading.Lock()
@@ -133,6 +150,20 @@ def load() -> C.CDLL:
         lib.dspark_clip_grads_rows.restype = i32
         lib.dspark_clip_grads_scratch_bytes.argtypes = [i32]
         lib.dspark_clip_grads_scratch_bytes.restype = C.c_size_t
+        D4, M4 = C.POINTER(Fp4Dims), C.POINTER(Fp4Data)
+        for name in ("dspark_fp4_code_bytes", "dspark_fp4_scale_bytes"):
+            getattr(lib, name).argtypes = [D4]
+            getattr(lib, name).restype = C.c_size_t
+        lib.dspark_fp4_quant.argtypes = [D4, P, i32, i64, M4, P, P]
+        lib.dspark_fp4_quant.restype = i32
+        lib.dspark_fp4_rows.argtypes = [D4, M4, P, i32, P, i32, i64, P, P]
+        lib.dspark_fp4_rows.restype = i32
+        lib.dspark_fp4_linear.argtypes = [D4, M4, D4, M4, P, i64, P, i32, i64, P, P]
+        lib.dspark_fp4_linear.restype = i32
+        lib.dspark_sample.argtypes = [C.POINTER(SampleArgs), P, P, P, P, P, P]
+        lib.dspark_sample.restype = i32
+        lib.dspark_sample_logprobs.argtypes = [C.POINTER(SampleArgs), P, f, P, i64, P, P]
+        lib.dspark_sample_logprobs.restype = i32
         _lib = lib
         return lib
 
@@ -470,7 +501,8 @@ class Workspace:
 
 
 class _TrainOp:
-    """What the training operators' objects share. A call takes tensors of the
+    """What the objects of the operators without a workspace share (training the
+    head, matrices in 4 bits, sampling). A call takes tensors of the
     object's device and runs there, whichever device is current. Memory that it makes
     belongs to the stream it runs on; the object's own buffers (``_buffers``) are
     noted with every stream that a call uses, so that their memory is not given
@@ -711,3 +743,133 @@ class GradClip(_TrainOp):
                           self.norm.data_ptr(), self.scratch.data_ptr(), self.status.data_ptr(), self._on(stream))
         _check(code, "dspark_clip_grads")
         return self.norm
+
+
+class Fp4Matrix(_TrainOp):
+    """A matrix of ``rows`` rows of K values held in microscaled 4-bit floating
+    point, "nvfp4" (blocks of 16, e4m3 scales, a power of two per row) or "mxfp4"
+    (blocks of 32, power-of-two scales): an output layer [V, K], a table W1 [V, r], or the rows
+    that go through a layer. Holds the codes, their scales, the rows' factors and a
+    status word; calls that share one object must be ordered on one stream."""
+
+    def __init__(self, rows: int, K: int, fmt: str = "nvfp4", device="cuda"):
+        self.lib = load()
+        if fmt not in FP4_FORMATS:
+            raise DsparkError(f"fmt must be one of {sorted(FP4_FORMATS)}, got {fmt!r}")
+        self.rows, self.K, self.fmt = int(rows), int(K), fmt
+        self._dims = Fp4Dims(self.rows, self.K, FP4_FORMATS[fmt])
+        self._pdims = C.byref(self._dims)
+        codes, scales = (int(f(self._pdims)) for f in (self.lib.dspark_fp4_code_bytes, self.lib.dspark_fp4_scale_bytes))
+        if codes == 0 or scales == 0:
+            raise DsparkError(f"dspark_fp4: unsupported rows={rows}, K={K}")
+        self.codes = torch.empty(codes, dtype=torch.uint8, device=device)
+        self.scales = torch.empty(scales, dtype=torch.uint8, device=device)
+        self.rowf = torch.empty(max(1, -(-self.rows // 128)) * 128, dtype=torch.float32, device=device)
+        self._data = Fp4Data(self.codes.data_ptr(), self.scales.data_ptr(), self.rowf.data_ptr())
+        self._pdata = C.byref(self._data)
+        super().__init__(device)
+
+    def _buffers(self):
+        return (self.codes, self.scales, self.rowf, self.status)
+
+    def quantise(self, X: torch.Tensor, stream=None) -> "Fp4Matrix":
+        """Takes X [rows, K] (bf16 or fp32, contiguous rows) into the matrix (``dspark_fp4_quant``); returns it."""
+        code = _dtype_code(X, "X")
+        px, ldx = _rows(X, self.rows, self.K, X.dtype, "X", self._index)
+        r = self._call(self.lib.dspark_fp4_quant, self._pdims, px, code, max(ldx, self.K), self._pdata,
+                       self.status.data_ptr(), self._on(stream))
+        _check(r, "dspark_fp4_quant")
+        return self
+
+    def lookup(self, idx: Optional[torch.Tensor] = None, dtype=torch.bfloat16, out=None, stream=None):
+        """The values of rows idx [N] int32 (-1: zeros), or of all rows, as
+        [N, K] bf16 or fp32 (``dspark_fp4_rows``)."""
+        n = self.rows if idx is None else idx.shape[0]
+        if out is None:
+            with torch.cuda.stream(stream):
+                out = torch.empty(n, self.K, dtype=dtype, device=self.status.device)
+        code = _dtype_code(out, "out")
+        po, ldo = _rows(out, n, self.K, out.dtype, "out", self._index)
+        pi = _vec(idx, n, torch.int32, "idx", self._index)
+        r = self._call(self.lib.dspark_fp4_rows, self._pdims, self._pdata, pi, n, po, code, max(ldo, self.K),
+                       self.status.data_ptr(), self._on(stream))
+        _check(r, "dspark_fp4_rows")
+        return out
+
+    def linear(self, X: "Fp4Matrix", U: Optional[torch.Tensor] = None, dtype=torch.float32, out=None, stream=None):
+        """X W^T (+ U) as [N, rows] for this matrix W and X of the same format
+        and K (``dspark_fp4_linear``): fp32 or bf16, U [N, rows] fp32 (it may be ``out``)."""
+        if X._index != self._index:
+            raise DsparkError(f"X on {X.status.device}, the matrix on {self.status.device}")
+        if X.fmt != self.fmt or X.K != self.K:
+            raise DsparkError(f"X holds {X.fmt} rows of {X.K}, the matrix {self.fmt} rows of {self.K}")
+        if out is None:
+            with torch.cuda.stream(stream):
+                out = torch.empty(X.rows, self.rows, dtype=dtype, device=self.status.device)
+        code = _dtype_code(out, "out")
+        po, ldo = _rows(out, X.rows, self.rows, out.dtype, "out", self._index)
+        pu, ldu = (None, 0) if U is None else _rows(U, X.rows, self.rows, torch.float32, "U", self._index)
+        X._on(stream)
+        r = self._call(self.lib.dspark_fp4_linear, X._pdims, X._pdata, self._pdims, self._pdata, pu, max(ldu, self.rows),
+                       po, code, max(ldo, self.rows), self.status.data_ptr(), self._on(stream))
+        _check(r, "dspark_fp4_linear")
+        return out
+
+
+class Sampler(_TrainOp):
+    """Draws from up to N rows of V logits with temperature, top-k, top-p and min-p
+    (``dspark_sample``), and the distribution that they make of the rows
+    (``dspark_sample_logprobs``). The settings are device vectors (temperature, top_p and
+    min_p fp32, top_k int32; None: off), an entry per row, or per request where
+    ``row_off`` [requests + 1] int32 says which rows belong to whom. Holds a status
+    word; calls that share one object must be ordered on one stream."""
+
+    def __init__(self, N: int, V: int, requests: Optional[int] = None, device="cuda"):
+        self.lib = load()
+        self.N, self.V, self.requests = int(N), int(V), None if requests is None else int(requests)
+        if not (0 <= self.N <= 1 << 24 and 1 <= self.V <= 1 << 24 and (requests is None or self.requests >= 1)):
+            raise DsparkError(f"dspark_sample: unsupported N={N}, V={V}, requests={requests}")
+        super().__init__(device)
+
+    def _buffers(self):
+        return (self.status,)
+
+    def _args(self, Z, row_off, temperature, top_k, top_p, min_p):
+        dev, f32, i32 = self._index, torch.float32, torch.int32
+        code = _dtype_code(Z, "Z")
+        pz, ldz = _rows(Z, self.N, self.V, Z.dtype, "Z", dev)
+        if row_off is not None and self.requests is None:
+            raise DsparkError("row_off needs a Sampler made with requests")
+        n = self.N if row_off is None else self.requests
+        return pz, SampleArgs(self.N, self.V, self.requests or 0, code, max(ldz, self.V),
+                              None if row_off is None else _vec(row_off, n + 1, i32, "row_off", dev),
+                              _vec(temperature, n, f32, "temperature", dev), _vec(top_k, n, i32, "top_k", dev),
+                              _vec(top_p, n, f32, "top_p", dev), _vec(min_p, n, f32, "min_p", dev))
+
+    def sample(self, Z, u, temperature=None, top_k=None, top_p=None, min_p=None, row_off=None, out=None, stream=None):
+        """token [N] int32 and logp [N] fp32 drawn with u [N] fp32 in [0, 1);
+        rows that ``row_off`` gives to no request are left as they are."""
+        if out is None:
+            with torch.cuda.stream(stream):
+                out = {"token": torch.empty(self.N, dtype=torch.int32, device=self.status.device),
+                       "logp": torch.empty(self.N, dtype=torch.float32, device=self.status.device)}
+        dev, f32 = self._index, torch.float32
+        pz, args = self._args(Z, row_off, temperature, top_k, top_p, min_p)
+        pu = _vec(u, self.N, f32, "u", dev)
+        pt, pl = _vec(out["token"], self.N, torch.int32, "token", dev), _vec(out.get("logp"), self.N, f32, "logp", dev)
+        r = self._call(self.lib.dspark_sample, C.byref(args), pz, pu, pt, pl, self.status.data_ptr(), self._on(stream))
+        _check(r, "dspark_sample")
+        return out
+
+    def logprobs(self, Z, temperature=None, top_k=None, top_p=None, min_p=None, row_off=None,
+                 fill: float = float("-inf"), out=None, stream=None):
+        """[N, V] fp32: the log-probabilities that ``sample`` draws with, ``fill`` where a token is left out."""
+        if out is None:
+            with torch.cuda.stream(stream):
+                out = torch.empty(self.N, self.V, dtype=torch.float32, device=self.status.device)
+        pz, args = self._args(Z, row_off, temperature, top_k, top_p, min_p)
+        po, ldo = _rows(out, self.N, self.V, torch.float32, "out", self._index)
+        r = self._call(self.lib.dspark_sample_logprobs, C.byref(args), pz, fill, po, max(ldo, self.V),
+                       self.status.data_ptr(), self._on(stream))
+        _check(r, "dspark_sample_logprobs")
+        return out

@@ -1,0 +1,395 @@
+// k_fp4_linear.cu -- the product of two matrices held in microscaled 4-bit
+// floating point, Y[n][v] = sum_k x[n][k] w[v][k] (+ U[n][v]).
+//
+// The vocabulary is the MMA's M: a tile is 128 rows of w by up to 256 rows of
+// x, so that a few tokens make narrow tiles and w streams by once, and a warp
+// of the epilogue holds 32 neighbouring v of one token: its stores are whole
+// sectors of Y without a turn through shared memory. Persistent CTAs; a
+// producer thread loads 256 columns of both operands a stage (128-byte
+// swizzled boxes) with their scales (contiguous, as dspark_fp4_quant lays them
+// out); the MMA thread copies the scales to TMEM and issues four block-scaled
+// MMAs of 64 columns; eight warps store.
+//
+// TMEM: two accumulators, and 48 columns of scales. Accumulators of more than
+// 224 columns overlap in the middle: the epilogue empties the shared columns
+// first, and the next tile's MMAs wait for those alone.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <stdio.h>
+
+#include "dspark_common.cuh"
+#include "dspark_internal.h"
+#include "fp4.cuh"
+#include "tc_ptx.cuh"
+
+namespace dspark {
+
+namespace {
+
+using namespace fp4;
+
+constexpr int kFlTileV = 128;
+constexpr int kFlMaxN = 256;          // tokens of a tile
+constexpr int kFlThreads = 384;       // producer, MMA, TMEM and a spare warp, eight epilogue warps
+constexpr int kFlSfCol = 464;         // TMEM columns of the scales, after the accumulators
+constexpr int kFlMaxStages = 12;
+constexpr int kFlBoxBytes = 128;      // kChunk values
+constexpr int kFlABytes = kFlTileV * kFlBoxBytes;
+
+struct FlArgs {
+  const uint8_t* wsc;
+  const uint8_t* xsc;
+  const float* wf;
+  const float* xf;
+  const float* U;
+  void* Y;
+  int64_t ldu, ldy;
+  int N, K, V;
+  int tn;        // tokens of a tile, a multiple of 16
+  int vt, nt;    // tiles
+  int stages, stage_bytes;
+  int acc1, overlap;  // the second accumulator's first column; columns it shares with the first
+  int* status;
+};
+
+struct FlBars {
+  uint64_t full[kFlMaxStages], empty[kFlMaxStages], tfull[2], tempty[2], over, drain;
+  uint32_t tmem;
+  int abort;
+};
+
+__device__ __forceinline__ void put(float* p, float y) { __stcs(p, y); }
+
+// 16 columns (tokens n0 .. n0 + 15) of 32 lanes (v), scaled and stored.
+template <typename T, bool HASF, bool HASU>
+__device__ __forceinline__ void fl_store16(const FlArgs& a, float* z, int n0, int nn, int v, float wf) {
+  float u[16];
+  if (HASU) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) u[i] = i < nn && v < a.V ? __ldcs(a.U + (int64_t)(n0 + i) * a.ldu + v) : 0.f;
+  }
+  if (HASF) {
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      const float4 f = __ldg(reinterpret_cast<const float4*>(a.xf + n0 + i));
+      z[i] = z[i] * wf * f.x;
+      z[i + 1] = z[i + 1] * wf * f.y;
+      z[i + 2] = z[i + 2] * wf * f.z;
+      z[i + 3] = z[i + 3] * wf * f.w;
+    }
+  }
+  if (HASU) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) z[i] += u[i];
+  }
+  if (sizeof(T) == 4) {
+    float* y = static_cast<float*>(a.Y) + (int64_t)n0 * a.ldy + v;
+    if (v < a.V) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (i < nn) put(y + i * a.ldy, z[i]);
+    }
+  } else {
+    __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.Y) + (int64_t)n0 * a.ldy;
+    const int lane = threadIdx.x & 31, odd = lane & 1;
+    const bool pairs = (a.ldy & 1) == 0 && (reinterpret_cast<uintptr_t>(a.Y) & 3u) == 0;
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) {
+      // neighbouring lanes trade: the even one stores both v of token i, the odd one of token i + 1
+      const float other = __shfl_xor_sync(0xFFFFFFFFu, odd ? z[i] : z[i + 1], 1);
+      const float lo = odd ? other : z[i], hi = odd ? z[i + 1] : other;
+      const int n = i + odd, ve = v - odd;
+      __nv_bfloat16* p = y + n * a.ldy + ve;
+      const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+      if (n < nn && ve < a.V) {
+        if (pairs && ve + 1 < a.V) {
+          *reinterpret_cast<__nv_bfloat162*>(p) = h;
+        } else {
+          p[0] = h.x;
+          if (ve + 1 < a.V) p[1] = h.y;
+        }
+      }
+    }
+  }
+}
+
+template <int FMT, typename T, bool HASU>
+__global__ void __launch_bounds__(kFlThreads, 1)
+    k_fp4_linear(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUtensorMap tx, FlArgs a) {
+  constexpr int kSf = chunk_bytes(FMT);         // bytes of a 128-row group's scales of a stage
+  constexpr int kQ = kSf / 512;                 // tiles of four blocks in them
+  extern __shared__ uint8_t raw[];
+  __shared__ FlBars bars;
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+  const uint32_t sbase = tc::smem_u32(base);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tiles = a.vt * a.nt, chunks = chunks_of(a.K);
+  volatile int* abort = &bars.abort;
+  auto bar = [&](uint64_t* b) { return tc::smem_u32(b); };
+
+  if (tid == 0) {
+    for (int s = 0; s < a.stages; ++s) {
+      tc::mbar_init(bar(&bars.full[s]), 1);
+      tc::mbar_init(bar(&bars.empty[s]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(bar(&bars.tfull[i]), 1);
+      tc::mbar_init(bar(&bars.tempty[i]), 8);
+    }
+    tc::mbar_init(bar(&bars.over), 8);
+    tc::mbar_init(bar(&bars.drain), 1);
+    bars.abort = 0;
+    tc::fence_barrier_init();
+    tc::prefetch_tmap(&tw);
+    tc::prefetch_tmap(&tx);
+  }
+  if (warp == 2) tc::tmem_alloc(tc::smem_u32(&bars.tmem), 512);
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = bars.tmem;
+  pdl_wait();
+  pdl_trigger();
+
+  const int b_off = kFlABytes, sa_off = b_off + a.tn * kFlBoxBytes, sb_off = sa_off + kSf;
+  bool ok = true;
+  if (warp == 0) {
+    if (lane == 0) {
+      const uint64_t keep = tc::policy_evict_last();   // x is read for every tile of w
+      const uint64_t first = tc::policy_evict_first(); // w once by neighbouring tiles
+      int k = 0;
+      for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+        const int v0 = t / a.nt * kFlTileV, n0 = t % a.nt * a.tn;
+        const int nsb = (min(a.tn, a.N - n0) + kRows - 1) / kRows;
+        for (int c = 0; c < chunks && ok; ++c, ++k) {
+          const int s = k % a.stages;
+          ok = tc::mbar_wait(bar(&bars.empty[s]), (k / a.stages & 1) ^ 1, abort);
+          if (!ok) break;
+          const uint32_t st = sbase + s * a.stage_bytes, f = bar(&bars.full[s]);
+          tc::mbar_arrive_expect_tx(f, kFlABytes + a.tn * kFlBoxBytes + (1 + nsb) * kSf);
+          tc::tma_load_2d(st, &tw, c * kFlBoxBytes, v0, f, a.nt > 1 ? keep : first);
+          tc::tma_load_2d(st + b_off, &tx, c * kFlBoxBytes, n0, f, keep);
+          tc::bulk_load(st + sa_off, a.wsc + ((int64_t)(v0 / kRows) * chunks + c) * kSf, kSf, f);
+          for (int i = 0; i < nsb; ++i)
+            tc::bulk_load(st + sb_off + i * kSf, a.xsc + ((int64_t)(n0 / kRows + i) * chunks + c) * kSf, kSf, f);
+        }
+      }
+      if (!ok) {
+        *abort = 1;
+        raise_status(a.status, DSPARK_ETIMEOUT);
+        int never = 0;  // copies in flight land before the CTA ends
+        for (int j = max(0, k - a.stages); j < k; ++j)
+          tc::mbar_wait(bar(&bars.full[j % a.stages]), j / a.stages & 1, &never);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      int k = 0, i = 0;
+      for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++i) {
+        const int n0 = t % a.nt * a.tn, nn = min(a.tn, a.N - n0), nm = (nn + 15) / 16 * 16;
+        const int nsb = (nn + kRows - 1) / kRows, buf = i & 1;
+        const uint32_t d = tmem + (buf ? a.acc1 : 0), sfa = tmem + kFlSfCol, sfb = sfa + 4 * kQ;
+        ok = tc::mbar_wait(bar(&bars.tempty[buf]), (i >> 1 & 1) ^ 1, abort);
+        if (ok && a.overlap && i > 0) ok = tc::mbar_wait(bar(&bars.over), (i - 1) & 1, abort);
+        tc::tc_fence_after();
+        for (int c = 0; c < chunks && ok; ++c, ++k) {
+          const int s = k % a.stages;
+          ok = tc::mbar_wait(bar(&bars.full[s]), k / a.stages & 1, abort);
+          if (!ok) break;
+          tc::tc_fence_after();
+          const uint32_t st = sbase + s * a.stage_bytes;
+          const int steps = min(4, (a.K - c * kChunk + 63) / 64);
+#pragma unroll
+          for (int q = 0; q < kQ; ++q) {
+            tc::cp_scales(sfa + 4 * q, tc::scales_desc(st + sa_off + q * 512));
+            for (int j = 0; j < nsb; ++j)
+              tc::cp_scales(sfb + 4 * (nsb * q + j), tc::scales_desc(st + sb_off + j * kSf + q * 512));
+          }
+          const uint64_t ad = tc::smem_desc(st, 16, 1024), bd = tc::smem_desc(st + b_off, 16, 1024);
+          for (int kk = 0; kk < steps; ++kk) {
+            const uint32_t acc = (c | kk) != 0;
+            if (FMT == DSPARK_NVFP4) {
+              tc::mma_nvfp4(d, ad + 2 * kk, bd + 2 * kk, tc::idesc_fp4(kFlTileV, nm, false, 0), sfa + 4 * kk,
+                            sfb + 4 * nsb * kk, acc);
+            } else {
+              const int q = kk >> 1;
+              tc::mma_mxfp4(d, ad + 2 * kk, bd + 2 * kk, tc::idesc_fp4(kFlTileV, nm, true, (kk & 1) * 2), sfa + 4 * q,
+                            sfb + 4 * nsb * q, acc);
+            }
+          }
+          tc::mma_commit(bar(&bars.empty[s]));
+        }
+        if (ok) tc::mma_commit(bar(&bars.tfull[buf]));
+      }
+      if (!ok) {
+        *abort = 1;
+        raise_status(a.status, DSPARK_ETIMEOUT);
+        int never = 0;
+        tc::mma_commit(bar(&bars.drain));
+        tc::mbar_wait(bar(&bars.drain), 0, &never);
+      }
+    }
+  } else if (warp >= 4) {
+    const int q = warp & 3, h = (warp - 4) >> 2;
+    const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
+    const int units = a.tn / 16, nov = a.overlap / 16;
+    int i = 0;
+    for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++i) {
+      const int v0 = t / a.nt * kFlTileV, n0 = t % a.nt * a.tn, nn = min(a.tn, a.N - n0), buf = i & 1;
+      const int v = v0 + q * 32 + lane;
+      float wf = 1.f;
+      if (FMT == DSPARK_NVFP4) wf = __ldg(a.wf + v);  // padded to whole 128-row groups
+      ok = tc::mbar_wait(bar(&bars.tfull[buf]), i >> 1 & 1, abort);
+      if (!ok) break;
+      tc::tc_fence_after();
+      const uint32_t d = lanes + (buf ? a.acc1 : 0);
+      // the shared columns are the first accumulator's last and the second's first
+      auto unit = [&](int j) { return buf ? j : units - 1 - j; };
+      int j = h;
+      if (nov) {
+        float o[2][16];
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (h + 2 * e < nov) tc::tmem_ld16(d + 16 * unit(h + 2 * e), o[e]);
+        tc::tmem_wait_ld();
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(bar(&bars.over));
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int c = 16 * unit(h + 2 * e);
+          if (h + 2 * e < nov) {
+            if (c < nn) fl_store16<T, FMT == DSPARK_NVFP4, HASU>(a, o[e], n0 + c, nn - c, v, wf);
+            j = h + 2 * e + 2;
+          }
+        }
+      }
+      for (; j < units; j += 2) {
+        const int c = 16 * unit(j);
+        if (c >= nn) continue;
+        float z[16];
+        tc::tmem_ld16(d + c, z);
+        tc::tmem_wait_ld();
+        fl_store16<T, FMT == DSPARK_NVFP4, HASU>(a, z, n0 + c, nn - c, v, wf);
+      }
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(bar(&bars.tempty[buf]));
+    }
+    if (!ok) {
+      *abort = 1;
+      raise_status(a.status, DSPARK_ETIMEOUT);
+    }
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  if (warp == 2) {
+    tc::tmem_relinquish();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  }();
+  return fn;
+}
+
+// The codes of `rows` rows; boxes of 256 values (128 bytes) by box_rows.
+bool encode(CUtensorMap* tm, const void* codes, int K, int rows, int box_rows) {
+  const cuuint64_t dims[2] = {(cuuint64_t)row_bytes(K), (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)row_bytes(K)};
+  const cuuint32_t box[2] = {kFlBoxBytes, (cuuint32_t)box_rows};
+  const cuuint32_t es[2] = {1, 1};
+  return encode_fn()(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(codes), dims, strides, box, es,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int FMT, typename T, bool HASU>
+cudaError_t launch(const CUtensorMap& tw, const CUtensorMap& tx, const FlArgs& a, int grid, cudaStream_t st) {
+  static std::atomic<uint64_t> done{0};
+  constexpr int kMax = 227 * 1024 - 1024;  // the barriers are static
+  const cudaError_t c = once_per_device(done, [] {
+    return cudaFuncSetAttribute(k_fp4_linear<FMT, T, HASU>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMax);
+  });
+  if (c != cudaSuccess) return c;
+  return launch_ex(k_fp4_linear<FMT, T, HASU>, dim3(grid), dim3(kFlThreads), (size_t)a.stages * a.stage_bytes + 1024, st,
+                   true, tw, tx, a);
+}
+template <int FMT>
+cudaError_t launch_t(bool bf16, const CUtensorMap& tw, const CUtensorMap& tx, const FlArgs& a, int grid,
+                     cudaStream_t st) {
+  if (bf16)
+    return a.U ? launch<FMT, __nv_bfloat16, true>(tw, tx, a, grid, st)
+               : launch<FMT, __nv_bfloat16, false>(tw, tx, a, grid, st);
+  return a.U ? launch<FMT, float, true>(tw, tx, a, grid, st) : launch<FMT, float, false>(tw, tx, a, grid, st);
+}
+
+bool on_type(const void* p, int size) { return p && (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(size - 1)) == 0; }
+
+}  // namespace
+
+}  // namespace dspark
+
+using namespace dspark;
+
+extern "C" dspark_status dspark_fp4_linear(const dspark_fp4_dims* xd, const dspark_fp4_data* x,
+                                           const dspark_fp4_dims* wd, const dspark_fp4_data* w, const float* U,
+                                           int64_t ldu, void* Y, dspark_wdtype type, int64_t ldy,
+                                           int32_t* device_status, dspark_stream_t stream) {
+  if (!fp4::dims_ok(xd) || !fp4::dims_ok(wd) || wd->rows < 1 || xd->K != wd->K || xd->format != wd->format)
+    return DSPARK_EINVAL;
+  if ((type != DSPARK_F32 && type != DSPARK_BF16) || !device_status || ldy < wd->rows) return DSPARK_EINVAL;
+  if (U && (!on_type(U, 4) || ldu < wd->rows)) return DSPARK_EINVAL;
+  if (xd->rows == 0) return DSPARK_OK;
+  if (!fp4::data_ok(xd, x) || !fp4::data_ok(wd, w) || !on_type(Y, type == DSPARK_BF16 ? 2 : 4)) return DSPARK_EINVAL;
+  if (U == Y && (type != DSPARK_F32 || ldu != ldy)) return DSPARK_EINVAL;
+  if (!encode_fn()) return DSPARK_ECUDA;
+  FlArgs a = {};
+  a.wsc = static_cast<const uint8_t*>(w->scales);
+  a.xsc = static_cast<const uint8_t*>(x->scales);
+  a.wf = w->rowf;
+  a.xf = x->rowf;
+  a.U = U;
+  a.Y = Y;
+  a.ldu = ldu;
+  a.ldy = ldy;
+  a.N = xd->rows;
+  a.K = xd->K;
+  a.V = wd->rows;
+  a.status = device_status;
+  // one tile of tokens for up to 256 of them; more in tiles of 256 (scales come in groups of 128 rows)
+  a.tn = a.N >= kFlMaxN ? kFlMaxN : (a.N + 15) / 16 * 16;
+  a.vt = (a.V + kFlTileV - 1) / kFlTileV;
+  a.nt = (a.N + a.tn - 1) / a.tn;
+  const int acc = kFlSfCol / 2 / 16 * 16;  // 224 columns each without overlap
+  a.overlap = a.tn > acc ? 2 * a.tn - kFlSfCol : 0;
+  a.acc1 = a.tn - a.overlap;
+  const int sf = fp4::chunk_bytes(wd->format);
+  const int bytes = kFlABytes + a.tn * kFlBoxBytes + sf * (1 + (a.tn + fp4::kRows - 1) / fp4::kRows);
+  a.stage_bytes = (bytes + 1023) / 1024 * 1024;
+  a.stages = (227 * 1024 - 2048) / a.stage_bytes;
+  if (a.stages > kFlMaxStages) a.stages = kFlMaxStages;
+  CUtensorMap tw, tx;
+  if (!encode(&tw, w->codes, a.K, a.V, kFlTileV) || !encode(&tx, x->codes, a.K, a.N, a.tn)) return DSPARK_ECUDA;
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const int64_t tiles = (int64_t)a.vt * a.nt;
+  if (tiles > (1ll << 30)) return DSPARK_EUNSUPPORTED;
+  const int grid = (int)(tiles < sms ? tiles : sms);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (e == cudaSuccess)
+    e = wd->format == DSPARK_NVFP4 ? launch_t<DSPARK_NVFP4>(type == DSPARK_BF16, tw, tx, a, grid, st)
+                                   : launch_t<DSPARK_MXFP4>(type == DSPARK_BF16, tw, tx, a, grid, st);
+  if (e != cudaSuccess) fprintf(stderr, "dspark: CUDA error %s\n", cudaGetErrorString(e));
+  return e == cudaSuccess ? DSPARK_OK : DSPARK_ECUDA;
+}
