@@ -3,20 +3,23 @@
 //
 // A cluster of CTAs takes a row: each holds its part in shared memory, so that
 // the logits are read from memory once and every later pass runs on chip
-// (vocabularies that sixteen CTAs cannot hold are read again each pass). With
-// m the row's maximum, a token's mass is the whole number
-//   W = round(2^Q 2^((z - m) log2(e) / T)),   Q = min(46, 62 - ceil(log2 V)),
-// taken to a relative 2^-31 (see weight()), so that masses are added in any order
-// with one result, and a border of the top-p set or of the draw is missed by 1e-10
-// of the mass at the most: next to nothing against one token's share.
+// (vocabularies that sixteen CTAs cannot hold are read again each pass).
 //
-// top-k and top-p are one search, for the last token of a prefix of the row sorted by
-// falling z (then by index): the first whose running sum, of ones or of masses,
-// reaches a target. A histogram of 2048 bins of m - z gives the bin that holds
-// it; the bin's tokens (some hundreds of a flat row of 129280) are brought to one CTA, sorted and
-// added up. A bin of more than 2048 tokens (many equal logits) is instead narrowed by three
-// histograms of the bits of z, down to one value, whose tokens are counted by index.
-// What is kept is z > cut, or z == cut and index <= last: the stricter of the three settings' pairs.
+// A token's mass, with m the row's maximum, is 2^y, y = (z - m) log2(e) / T, as a
+// whole number `mant` of 31 bits times 2^(-e-30), to a relative 2^-30 at the worst and
+// without a bias (see Mass). Masses are added as whole numbers, so in any order with one
+// result, and a border of the top-p set or of the draw is missed by 1e-10 of the
+// mass at the most: next to nothing against one token's share.
+//
+// top-k and top-p are one search, for the first token of the row sorted by
+// falling z (then by index) at which the running sum, of ones or of masses,
+// reaches a target. A histogram of 1536 bins of z (for masses 1/32 of an octave each, so that
+// a bin's tokens share e and their mants are added as they are) gives the bin; its tokens
+// (some hundreds of a flat row of 129280) are brought to one CTA, which splits them
+// into 512 narrower bins and looks at the few tokens of one of those. A bin of more than 1536 tokens (many
+// equal logits) is instead narrowed by three histograms of the bits of z, down to one value,
+// whose tokens are counted by index. What is kept is z >= cut; tokens that equal the cut
+// but come after its last index are masked in shared memory.
 #include <math.h>
 #include <stdio.h>
 
@@ -31,13 +34,17 @@ namespace {
 typedef unsigned long long u64;
 
 constexpr int kSpThreads = 512, kSpWarps = kSpThreads / 32;
-constexpr int kSpMaxC = 16;     // CTAs of a cluster
-constexpr int kSpBins = 2048;
-constexpr int kSpList = 2048;   // tokens of a bin that are sorted
-constexpr int kSpChunk = 512;   // tokens that a warp takes at a time
+constexpr int kSpMaxC = 16;       // CTAs of a cluster
+constexpr int kSpBins = 1536;     // 48 octaves of 32 bins
+constexpr int kSpLast = 1504;     // bins from here on (masses below 2^-47) count as nothing
+constexpr int kSpList = kSpBins;  // tokens of a bin that are brought together
+constexpr int kSpChunk = 512;     // tokens that a warp takes at a time
 constexpr int kSpMaxChunks = 2048;
 constexpr float kSpMasked = -1e29f;
-constexpr int kSpHist = kSpBins * 8;  // bytes: the histogram, the list or the chunks' sums
+constexpr float kSpLowest = -3.402823466e38f;
+constexpr int kSpHist = kSpMaxChunks * 8;  // bytes: the histogram, the list or the chunks' sums
+constexpr float kSpMagic = 12582912.f;     // 1.5 * 2^23: sums with it round to whole numbers
+constexpr uint32_t kSpMagicBits = 0x4B400000u;
 
 struct SpArgs {
   const void* Z;
@@ -55,16 +62,14 @@ struct SpArgs {
   int64_t ldo;
   float fill;
   int part;      // tokens of a CTA, a multiple of kSpChunk
-  int q;         // Q
+  int q;         // sums of masses are multiples of 2^-q
   int vec, vec_out;
   int* status;
 };
 
-// Of the row, in every CTA of its cluster.
-struct SpRow {
-  float m, c_hi, c_lo;  // maximum; log2(e) / T as a sum of two
-  float inv_t;
-  int q;
+// A rounding of z to bins: the whole number nearest to (z - sub) hi + mb - kSpMagic, at most 0 for the maximum.
+struct SpScale {
+  float sub, hi, mb;
 };
 
 struct SpCut {
@@ -73,58 +78,91 @@ struct SpCut {
 };
 
 struct SpShared {
-  uint2 exp2[64];              // 2^(i/64): times 2^31 as a whole number and as fp32
+  uint2 exp2[16];              // kSpExp2 as a whole number and as fp32
   u64 slot[2][kSpMaxC][2];     // what each CTA tells the others
   u64 res[2];                  // a search's answer: bin and sum before it, or a cut
   u64 warp[kSpWarps], warp2[kSpWarps];
   u64 bcast[2];
-  float c_hi, c_lo, inv_t, min_z, p, u;
-  int k, n, bad;
+  u64 few[32];
+  float c_hi, c_lo, inv_t, p, u;
+  int k, n, m, bad;
 };
 
-// round(2^31 2^(i/64))
-__constant__ uint32_t kSpExp2[64] = {
-    2147483648u, 2170868212u, 2194507417u, 2218404036u, 2242560872u, 2266980759u, 2291666561u, 2316621173u,
-    2341847524u, 2367348571u, 2393127307u, 2419186755u, 2445529972u, 2472160047u, 2499080105u, 2526293303u,
-    2553802834u, 2581611923u, 2609723834u, 2638141863u, 2666869345u, 2695909648u, 2725266179u, 2754942382u,
-    2784941738u, 2815267765u, 2845924021u, 2876914102u, 2908241642u, 2939910317u, 2971923842u, 3004285971u,
-    3037000500u, 3070071267u, 3103502151u, 3137297074u, 3171459999u, 3205994934u, 3240905930u, 3276197082u,
-    3311872529u, 3347936457u, 3384393094u, 3421246719u, 3458501653u, 3496162267u, 3534232978u, 3572718252u,
-    3611622603u, 3650950594u, 3690706840u, 3730896002u, 3771522796u, 3812591987u, 3854108391u, 3896076880u,
-    3938502376u, 3981389855u, 4024744348u, 4068570940u, 4112874773u, 4157661043u, 4202935003u, 4248701965u};
+// round(2^30 2^((2 i + 1/2) / 32))
+__constant__ uint32_t kSpExp2[16] = {
+    1085434106u, 1133490379u, 1183674286u, 1236080024u, 1290805962u, 1347954824u, 1407633882u, 1469955159u,
+    1535035634u, 1602997467u, 1673968228u, 1748081133u, 1825475297u, 1906295993u, 1990694927u, 2078830522u};
 
 __device__ __forceinline__ uint32_t ordered(float z) {
-  const uint32_t b = __float_as_uint(z);
+  const uint32_t b = __float_as_uint(z + 0.f);  // -0 is 0
   return b ^ ((int32_t)b < 0 ? 0xFFFFFFFFu : 0x80000000u);
 }
 __device__ __forceinline__ float unordered(uint32_t o) {
   return __uint_as_float(o ^ ((int32_t)o < 0 ? 0x80000000u : 0xFFFFFFFFu));
 }
 
-// The mass of a token. The exponent y = (z - m) log2(e) / T is carried as a sum
-// of two fp32 (z - m with its rounding error, by Knuth's two-sum; the product with its error by
-// an fma), split into n + i/64 + r, |r| <= 1/128, and
-//   2^y = 2^n 2^(i/64) (1 + r l + (r l)^2 / 2 + (r l)^3 / 6),  l = ln 2,
-// Taylor's next term being 2^-35 of it. The bracket less one is fp32, at most
-// 2^-7.5, so its rounding is 2^-31 of the mass; 2^(i/64) is held in 32 bits.
-__device__ __forceinline__ u64 weight(float z, const SpRow& r, const uint2* tab) {
-  const float s = z - r.m;
-  const float y = s * r.c_hi;
-  if (!(y > -(float)(r.q + 1))) return 0;
-  const float a = s + r.m, b = s - a;
-  const float e = (z - a) + (-r.m - b);
-  const float lo = fmaf(s, r.c_hi, -y) + fmaf(s, r.c_lo, e * r.c_hi);
-  const float magic = 196608.f;  // 1.5 * 2^17: a step of 1/64
-  const float t = y + magic;
-  const int yi = __float_as_int(t) - __float_as_int(magic);
-  const float f = (y - (t - magic)) + lo;
-  const uint2 w = tab[yi & 63];
-  const float p = f * fmaf(f, fmaf(f, 0.05550411f, 0.24022651f), 0.69314718f);
-  const uint32_t mant = w.x + (uint32_t)__float2int_rn(__uint_as_float(w.y) * p);
-  const int sh = -(yi >> 6) - (r.q - 31);  // mant 2^31 stands for 1
-  if (sh <= 0) return (u64)mant << -sh;
-  if (sh > 32) return 0;
-  return ((u64)mant + (1ull << (sh - 1))) >> sh;
+// The mass of tokens, of two at a time where it matters. In units of 1/32 octave y is
+//   x = (z - sub) (hi + lo) - B,   hi + lo = 32 log2(e) / T,   B = mb's whole number,
+// J = round(x) <= 0 names the token's bin, q = J rounded down to an even number its
+// table entry and octave (e = -floor(q / 32)), and with r = x - q - 1/2, |r| <= 1,
+//   2^(x/32) = 2^-e T[q mod 32 / 2] (1 + w + w^2/2 + w^3/6 + w^4/24),  w = r ln(2) / 32,
+// Taylor's next term being 2^-34. x is never rounded: the fma of z hi with -(q + B) is
+// exact up to its own rounding of r, 2^-25 of 1/32 octave, and the bracket less one is at
+// most 2^-5.5 in fp32. sub is 0; where the maximum is so many octaves from 0 that B would not fit (2^16)
+// it is the maximum, and z - m is exact for every z whose mass counts (it is within 1/300 of m).
+// The table's sixteen entries of 8 bytes take a bank each: reads of it never conflict.
+struct Mass {
+  SpScale s;
+  float lo;
+  __device__ __forceinline__ void poly(float r, float tf, uint32_t ti, uint32_t& mant) const {
+    const float p = r * fmaf(r, fmaf(r, fmaf(r, 9.1725627e-09f, 1.69385097e-06f), 0.000234596198f), 0.0216608494f);
+    mant = ti + (uint32_t)__float2int_rn(tf * p);
+  }
+  __device__ __forceinline__ uint32_t one(float z, const uint2* tab, int& J) const {
+    const float x = z - s.sub;
+    const uint32_t t = __float_as_uint(fmaf(x, s.hi, s.mb));
+    const uint32_t tq = t & ~1u;
+    float r = fmaf(x, s.hi, fmaf(__uint_as_float(tq), -1.f, s.mb) + -0.5f);
+    r = fmaf(x, lo, r);
+    const uint2 w = tab[(tq >> 1) & 15u];
+    uint32_t mant;
+    poly(r, __uint_as_float(w.y), w.x, mant);
+    J = (int)(t - kSpMagicBits);
+    return mant;
+  }
+  // the same of two tokens; t: the bits of kSpMagic + J
+  __device__ __forceinline__ void two(float z0, float z1, const uint2* tab, uint32_t* t, uint32_t* mant) const {
+    const u64 x = tc::add2(tc::f2pack(z0, z1), tc::f2pack(-s.sub, -s.sub));
+    const u64 hi = tc::f2pack(s.hi, s.hi), mb = tc::f2pack(s.mb, s.mb);
+    float a, b;
+    tc::f2unpack(tc::fma2(x, hi, mb), a, b);
+    t[0] = __float_as_uint(a);
+    t[1] = __float_as_uint(b);
+    const uint32_t q0 = t[0] & ~1u, q1 = t[1] & ~1u;
+    u64 r = tc::fma2(tc::f2pack(__uint_as_float(q0), __uint_as_float(q1)), tc::f2pack(-1.f, -1.f), mb);
+    r = tc::add2(r, tc::f2pack(-0.5f, -0.5f));
+    r = tc::fma2(x, hi, r);
+    r = tc::fma2(x, tc::f2pack(lo, lo), r);
+    u64 p = tc::fma2(r, tc::f2pack(9.1725627e-09f, 9.1725627e-09f), tc::f2pack(1.69385097e-06f, 1.69385097e-06f));
+    p = tc::fma2(r, p, tc::f2pack(0.000234596198f, 0.000234596198f));
+    p = tc::fma2(r, p, tc::f2pack(0.0216608494f, 0.0216608494f));
+    p = tc::mul2(r, p);
+    tc::f2unpack(p, a, b);
+    const uint2 w0 = tab[(q0 >> 1) & 15u], w1 = tab[(q1 >> 1) & 15u];
+    mant[0] = w0.x + (uint32_t)__float2int_rn(__uint_as_float(w0.y) * a);
+    mant[1] = w1.x + (uint32_t)__float2int_rn(__uint_as_float(w1.y) * b);
+  }
+};
+// bin -J: the octave of its masses
+__device__ __forceinline__ int octave(int bin) { return (((bin + 1) & ~1) + 31) >> 5; }
+// raw mants of octave e as a multiple of 2^-q, rounded; and the least raw sum that reaches `need`
+__device__ __forceinline__ u64 scaled(u64 raw, int e, int q) {
+  const int sh = e - (q - 30);
+  return sh <= 0 ? raw << -sh : (raw + (1ull << (sh - 1))) >> sh;
+}
+__device__ __forceinline__ u64 unscaled(u64 need, int e, int q) {
+  const int sh = e - (q - 30);
+  return sh <= 0 ? (need + (1ull << -sh) - 1) >> -sh : (need << sh) - (1ull << (sh - 1));
 }
 
 __device__ __forceinline__ void st_rank(void* p, uint32_t rank, u64 x) {
@@ -153,6 +191,11 @@ __device__ __forceinline__ u64 warp_scan64(u64 x) {  // inclusive
   }
   return x;
 }
+__device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
 // floor(x a) and ceil(x a) for 0 <= a < 1
 __device__ __forceinline__ u64 mul_floor(u64 x, float a, bool ceil) {
   const uint32_t b = __float_as_uint(a), e = b >> 23;
@@ -174,13 +217,14 @@ template <>
 __device__ __forceinline__ float up<__nv_bfloat16>(__nv_bfloat16 x) {
   return __bfloat162float(x);
 }
-// masked tokens are -inf, -0 is 0
-__device__ __forceinline__ float clean(float z) { return z <= kSpMasked ? -INFINITY : z + 0.f; }
+// masked tokens are -inf
+__device__ __forceinline__ float clean(float z) { return z <= kSpMasked ? -INFINITY : z; }
 
 // One row's work in one CTA. RES: its part lies in shared memory.
 template <typename T, bool RES>
 struct Row {
   static constexpr int kPer = 16 / (int)sizeof(T);  // values of 16 bytes
+  static constexpr int kStep = 8;                   // tokens of a lane that are looked at together
   const SpArgs& a;
   SpShared& sh;
   uint8_t* buf;        // kSpHist bytes
@@ -190,25 +234,27 @@ struct Row {
   uint32_t rank, C;
   int start, count, chunks;  // the part's first token, its tokens, its chunks
   int par = 0;
-  SpRow r;
-  SpCut cut{-INFINITY, -1};
+  float m;                   // the row's maximum
+  Mass mass;
+  u64 held = 0;              // the mass up to the cut of a search for masses
+  SpCut cut{kSpLowest, 0x7FFFFFFF};
 
   __device__ Row(const SpArgs& a_, SpShared& s_) : a(a_), sh(s_) {}
 
-  // place of value i of a lane in a chunk
-  __device__ __forceinline__ int at(int ch, int i) const {
-    return ch * kSpChunk + i / kPer * (32 * kPer) + lane * kPer + i % kPer;
+  // place of value i (< 8) of a lane in step h (0, 1) of a chunk
+  __device__ __forceinline__ int at(int ch, int h, int i) const {
+    return ch * kSpChunk + h * (32 * kStep) + i / kPer * (32 * kPer) + lane * kPer + i % kPer;
   }
   __device__ __forceinline__ void unpack(const uint4& q, float* v) const {
     const T* t = reinterpret_cast<const T*>(&q);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) v[i] = up<T>(t[i]);
   }
-  // 16 / kPer * kPer = 16 tokens of a lane, from global memory; past the end -inf
-  __device__ __forceinline__ void fetch(int ch, float* v) const {
+  // 8 tokens of a lane, from global memory; past the end -inf
+  __device__ __forceinline__ void fetch(int ch, int h, float* v) const {
 #pragma unroll
-    for (int g = 0; g < 16 / kPer; ++g) {
-      const int l = at(ch, g * kPer);
+    for (int g = 0; g < kStep / kPer; ++g) {
+      const int l = at(ch, h, g * kPer);
       if (a.vec && l + kPer <= count) {
         unpack(__ldg(reinterpret_cast<const uint4*>(row + start + l)), v + g * kPer);
       } else {
@@ -217,14 +263,15 @@ struct Row {
       }
     }
   }
-  __device__ __forceinline__ void values(int ch, float* v) const {
+  __device__ __forceinline__ void values(int ch, int h, float* v) const {
     if (RES) {
 #pragma unroll
-      for (int g = 0; g < 16 / kPer; ++g) unpack(*reinterpret_cast<const uint4*>(part + at(ch, g * kPer)), v + g * kPer);
+      for (int g = 0; g < kStep / kPer; ++g)
+        unpack(*reinterpret_cast<const uint4*>(part + at(ch, h, g * kPer)), v + g * kPer);
     } else {
-      fetch(ch, v);
+      fetch(ch, h, v);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = clean(v[i]);
+      for (int i = 0; i < kStep; ++i) v[i] = clean(v[i]);
     }
   }
   __device__ __forceinline__ float value(int l) const {
@@ -232,15 +279,18 @@ struct Row {
     return l < count ? clean(up<T>(row[start + l])) : -INFINITY;
   }
   __device__ __forceinline__ bool kept(float z, int l) const {
-    return z > cut.z || (z == cut.z && start + l <= cut.last);
+    return RES ? z >= cut.z : z > cut.z || (z == cut.z && start + l <= cut.last);
   }
+  // f(the eight values of a step, chunk, step)
   template <typename F>
   __device__ __forceinline__ void each(F f) const {
     for (int ch = warp; ch < chunks; ch += kSpWarps) {
-      float v[16];
-      values(ch, v);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) f(v[i], at(ch, i));
+#pragma unroll 1
+      for (int h = 0; h < kSpChunk / (32 * kStep); ++h) {
+        float v[kStep];
+        values(ch, h, v);
+        f(v, ch, h);
+      }
     }
   }
   // Every CTA's thread 0 tells x, y to all; all see them in slot[][].
@@ -259,80 +309,82 @@ struct Row {
     par ^= 1;
     return s;
   }
-  __device__ __forceinline__ u64 block_sum(u64 x) {  // in every thread
-    x = warp_sum64(x);
-    __syncthreads();
-    if (lane == 0) sh.warp[warp] = x;
-    __syncthreads();
-    u64 t = 0;
-#pragma unroll
-    for (int i = 0; i < kSpWarps; ++i) t += sh.warp[i];
-    return t;
-  }
-  // sum of the threads before this one; every thread takes part
-  __device__ __forceinline__ u64 block_before(u64 x) {
+  // the sum over the CTA's threads, and over those before this one
+  __device__ __forceinline__ u64 block_scan(u64 x, u64& before) {
     const u64 inc = warp_scan64(x);
     __syncthreads();
-    if (lane == 31) sh.warp2[warp] = inc;
+    if (lane == 31) sh.warp[warp] = inc;
     __syncthreads();
-    u64 t = inc - x;
-    for (int i = 0; i < warp; ++i) t += sh.warp2[i];
+    u64 t = 0, b = 0;
+#pragma unroll
+    for (int i = 0; i < kSpWarps; ++i) {
+      if (i == warp) b = t;
+      t += sh.warp[i];
+    }
+    before = b + inc - x;
     return t;
   }
 
   __device__ __forceinline__ uint32_t* lo() const { return reinterpret_cast<uint32_t*>(buf); }
   __device__ __forceinline__ uint32_t* hi() const { return reinterpret_cast<uint32_t*>(buf) + kSpBins; }
-  __device__ __forceinline__ void clear() {
-    for (int i = tid; i < kSpBins * 2; i += kSpThreads) lo()[i] = 0;
+  __device__ __forceinline__ void clear(int n) {
+    for (int i = tid; i < n; i += kSpThreads) {
+      lo()[i] = 0;
+      hi()[i] = 0;
+    }
     __syncthreads();
   }
+  // 64-bit sums as two words: a carry goes to the upper one
   template <bool MASS>
-  __device__ __forceinline__ void add(int bin, float z) {
+  __device__ __forceinline__ void add(int bin, uint32_t x) {
     if (!MASS) {
       atomicAdd(lo() + bin, 1u);
     } else {
-      const u64 w = weight(z, r, sh.exp2);
-      const uint32_t l = (uint32_t)w, old = atomicAdd(lo() + bin, l);
-      const uint32_t h = (uint32_t)(w >> 32) + (old + l < old ? 1u : 0u);
-      if (h) atomicAdd(hi() + bin, h);
+      const uint32_t old = atomicAdd(lo() + bin, x);
+      if (old + x < old) atomicAdd(hi() + bin, 1u);
     }
   }
-  // With every CTA's histogram filled: the first bin at which before + the sum up to it reaches the
-  // target, and the sum before it. target 0: ceil(p of all of it), at least 1.
-  __device__ __forceinline__ void find(u64& target, u64& before, int& bin) {
+  // With every CTA's histogram filled: the first bin at which the sum up to it reaches the target, and
+  // the sum before it. OCT: the bins hold raw mants of their octaves. target 0: ceil(p of all of it), at
+  // least 1. Returns whether the sum reaches the target at all.
+  template <bool OCT>
+  __device__ __forceinline__ bool find(u64& target, u64& before, int& bin) {
     tc::cluster_sync();
-    const int seg = kSpBins / (int)C, per = (seg + kSpThreads - 1) / kSpThreads;
-    u64 v[4], sum = 0;
+    const int seg = kSpBins / (int)C;
+    u64 v[3], sum = 0;  // 1536 bins of one CTA alone: three a thread
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 3; ++i) {
       v[i] = 0;
-      const int b = tid * per + i;
-      if (i < per && b < seg) {
+      const int b = tid * (C == 1 ? 3 : C == 2 ? 2 : 1) + i;
+      if ((C == 1 || (C == 2 && i < 2) || i < 1) && b < seg) {
         const int g = (int)rank * seg + b;
         for (uint32_t c = 0; c < C; ++c)
           v[i] += (u64)(uint32_t)tc::ld_rank(tc::smem_u32(lo() + g), c) +
                   ((u64)(uint32_t)tc::ld_rank(tc::smem_u32(hi() + g), c) << 32);
+        if (OCT) v[i] = g < kSpLast && octave(g) <= a.q + 1 ? scaled(v[i], octave(g), a.q) : 0;
       }
       sum += v[i];
     }
-    const u64 mine = block_before(sum);
-    const u64 all = block_sum(sum);
+    u64 mine;
+    const u64 all = block_scan(sum, mine);
     const u64(*s)[2] = tell(all, 0);
-    u64 total = 0, pre = before;
+    u64 total = 0, pre = 0;
     for (uint32_t c = 0; c < C; ++c) {
-      if (c == rank) pre += total;
+      if (c == rank) pre = total;
       total += s[c][0];
     }
     if (target == 0) {
       target = mul_floor(total, sh.p, true);
       if (target == 0) target = 1;
     }
+    if (target > total) return false;
     u64 t = pre + mine;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 3; ++i) {
       if (t < target && t + v[i] >= target) {
+        const int g = (int)rank * seg + tid * (C == 1 ? 3 : C == 2 ? 2 : 1) + i;
         for (uint32_t c = 0; c < C; ++c) {
-          st_rank(&sh.res[0], c, (u64)(rank * seg + tid * per + i));
+          st_rank(&sh.res[0], c, (u64)g);
           st_rank(&sh.res[1], c, t);
         }
       }
@@ -341,47 +393,177 @@ struct Row {
     tc::cluster_sync();
     bin = (int)sh.res[0];
     before = sh.res[1];
+    return true;
   }
 
-  // Tightens the cut to the first of the kept tokens, in order, whose running
+  // Tightens the cut to the first of the kept tokens, in order, at which the running
   // count (MASS: mass) reaches the target.
   template <bool MASS>
-  __device__ void select(u64 target, float beta) {
-    auto bin_of = [&](float z) { return min(kSpBins - 1, (int)((r.m - z) * beta)); };
-    clear();
+  __device__ void select(u64 target, const SpScale& b) {
+    constexpr uint32_t kLow = kSpMagicBits - (MASS ? kSpLast - 1 : kSpBins - 1);
+    auto bits_of = [&](float z) { return __float_as_uint(fmaf(z - b.sub, b.hi, b.mb)); };
+    clear(kSpBins);
     if (tid == 0) sh.n = 0;
-    each([&](float z, int l) {
-      if (kept(z, l)) add<MASS>(bin_of(z), z);
+    each([&](const float* v, int ch, int h) {
+#pragma unroll
+      for (int i = 0; i < kStep; i += 2) {
+        uint32_t t[2], mant[2] = {1, 1};
+        if (MASS) {
+          mass.two(v[i], v[i + 1], sh.exp2, t, mant);
+        } else {
+          t[0] = max((int)bits_of(v[i]), (int)kLow);  // -inf and below the bins: the last one
+          t[1] = max((int)bits_of(v[i + 1]), (int)kLow);
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          if (kept(v[i + k], at(ch, h, i + k)) && (int)t[k] >= (int)kLow) add<MASS>((int)(kSpMagicBits - t[k]), mant[k]);
+      }
     });
     u64 before = 0;
     int bin;
-    find(target, before, bin);
-    // the bin's tokens to CTA 0, sorted by falling z, then by index
+    if (!find<MASS>(target, before, bin)) return;
+    const int e = octave(bin);
+    const u64 goal = MASS ? unscaled(target - before, e, a.q) : target - before;  // of the bin's raw sum
+    const bool low = !MASS && bin == kSpBins - 1;  // and everything below it
+    const uint32_t bits = kSpMagicBits - bin;
+    auto inside = [&](float z) { return low ? (int)bits_of(z) <= (int)bits : bits_of(z) == bits; };
+    // the bin's tokens to CTA 0
     u64* list = reinterpret_cast<u64*>(buf);
-    each([&](float z, int l) {
-      if (kept(z, l) && bin_of(z) == bin) {
-        const int n = add_rank(&sh.n, 0, 1);
-        if (n < kSpList) st_rank(list + n, 0, (u64)~ordered(z) << 32 | (uint32_t)(start + l));
+    each([&](const float* v, int ch, int h) {
+#pragma unroll
+      for (int i = 0; i < kStep; ++i) {
+        if (inside(v[i]) && kept(v[i], at(ch, h, i))) {
+          const int n = add_rank(&sh.n, 0, 1);
+          if (n < kSpList) st_rank(list + n, 0, (u64)~ordered(v[i]) << 32 | (uint32_t)(start + at(ch, h, i)));
+        }
       }
     });
     tc::cluster_sync();
     const int n = tc::ld_rank(tc::smem_u32(&sh.n), 0);
     if (n <= kSpList) {
-      if (rank == 0) cut_of_list<MASS>(n, target, before);
+      if (rank == 0) cut_of_list<MASS>(n, goal);
     } else {
-      narrow<MASS>(bin_of, bin, target, before);
+      narrow<MASS>(inside, goal);
     }
     tc::cluster_sync();
     cut.z = unordered((uint32_t)(sh.res[0] >> 32));
     cut.last = (int)(uint32_t)sh.res[0];
+    if (MASS) held = before + scaled(sh.res[1], e, a.q);
+    if (RES && n > kSpList) {  // cut_of_list has masked the others
+      each([&](const float* v, int ch, int h) {
+#pragma unroll
+        for (int i = 0; i < kStep; ++i)
+          if (v[i] == cut.z && start + at(ch, h, i) > cut.last) part[at(ch, h, i)] = T(-INFINITY);
+      });
+      __syncthreads();
+    }
   }
 
   template <bool MASS>
-  __device__ void cut_of_list(int n, u64 target, u64 before) {
+  __device__ __forceinline__ uint32_t raw(u64 key) const {
+    int J;
+    return MASS ? mass.one(unordered(~(uint32_t)(key >> 32)), sh.exp2, J) : 1;
+  }
+  // The cut (ordered z, index) and the raw sum up to it, to every CTA.
+  __device__ __forceinline__ void answer(u64 key, u64 sum) {
+    for (uint32_t c = 0; c < C; ++c) {
+      st_rank(&sh.res[0], c, (u64)~(uint32_t)(key >> 32) << 32 | (uint32_t)key);
+      st_rank(&sh.res[1], c, sum);
+    }
+  }
+
+  // In CTA 0: keys (falling z, index) in any order.
+  template <bool MASS>
+  __device__ void cut_of_list(int n, u64 goal) {
+    u64* list = reinterpret_cast<u64*>(buf);
+    constexpr int kOf = (kSpList + kSpThreads - 1) / kSpThreads;
+    u64 key[kOf];
+    uint32_t least = ~0u, most = 0;
+#pragma unroll
+    for (int i = 0; i < kOf; ++i) {
+      const int e = tid + i * kSpThreads;
+      key[i] = e < n ? list[e] : ~0ull;
+      if (e < n) {
+        least = min(least, (uint32_t)(key[i] >> 32));
+        most = max(most, (uint32_t)(key[i] >> 32));
+      }
+    }
+    least = __reduce_min_sync(0xFFFFFFFFu, least);
+    most = __reduce_max_sync(0xFFFFFFFFu, most);
+    if (lane == 0) sh.warp2[warp] = (u64)least << 32 | most;
+    if (tid == 0) sh.m = 0;
+    __syncthreads();  // the list is in registers, its memory free
+#pragma unroll
+    for (int i = 0; i < kSpWarps; ++i) {
+      least = min(least, (uint32_t)(sh.warp2[i] >> 32));
+      most = max(most, (uint32_t)sh.warp2[i]);
+    }
+    const int shift = max(0, 32 - __clz(most - least) - 9);  // 512 narrower bins
+    clear(kSpThreads);
+#pragma unroll
+    for (int i = 0; i < kOf; ++i)
+      if (tid + i * kSpThreads < n) add<MASS>((int)(((uint32_t)(key[i] >> 32) - least) >> shift), raw<MASS>(key[i]));
+    __syncthreads();
+    const u64 here = (u64)lo()[tid] | (u64)hi()[tid] << 32;
+    u64 before;
+    block_scan(here, before);
+    if (before < goal && before + here >= goal) {
+      sh.bcast[0] = (u64)tid;
+      sh.bcast[1] = before;
+    }
+    __syncthreads();
+    const int bin = (int)sh.bcast[0];
+    const u64 base = sh.bcast[1];
+#pragma unroll
+    for (int i = 0; i < kOf; ++i)
+      if (tid + i * kSpThreads < n && (int)(((uint32_t)(key[i] >> 32) - least) >> shift) == bin) {
+        const int at = atomicAdd(&sh.m, 1);
+        if (at < 32) sh.few[at] = key[i];
+      }
+    __syncthreads();
+    if (sh.m <= 32) {
+      if (warp == 0) {
+        const u64 mine = lane < sh.m ? sh.few[lane] : ~0ull;
+        const u64 w = lane < sh.m ? raw<MASS>(mine) : 0;
+        u64 sum = base;
+        for (int i = 0; i < sh.m; ++i) {
+          const u64 other = __shfl_sync(0xFFFFFFFFu, mine, i), ow = __shfl_sync(0xFFFFFFFFu, w, i);
+          if (other < mine) sum += ow;
+        }
+        if (lane < sh.m && sum < goal && sum + w >= goal) {
+          answer(mine, sum + w);
+          sh.bcast[0] = mine;
+        }
+      }
+    } else {
+      sorted<MASS>(key, n, goal);
+    }
+    __syncthreads();
+    if (RES) {  // equals of the cut that come after it
+      const u64 end = sh.bcast[0];
+#pragma unroll
+      for (int i = 0; i < kOf; ++i)
+        if (tid + i * kSpThreads < n && key[i] > end && key[i] >> 32 == end >> 32) {
+          const int idx = (int)(uint32_t)key[i];
+          const uint32_t owner = idx / a.part;
+          const uint32_t p = tc::map_rank(tc::smem_u32(part + (idx - (int)owner * a.part)), owner);
+          if (sizeof(T) == 4)
+            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(p), "r"(0xFF800000u) : "memory");
+          else
+            asm volatile("st.shared::cluster.u16 [%0], %1;" ::"r"(p), "h"((unsigned short)0xFF80u) : "memory");
+        }
+    }
+  }
+  // The same by sorting the whole list, where a narrower bin holds more than 32 tokens.
+  template <bool MASS, int KOF>
+  __device__ void sorted(const u64 (&key)[KOF], int n, u64 goal) {
     u64* list = reinterpret_cast<u64*>(buf);
     int size = 32;
     while (size < n) size *= 2;
-    for (int i = n + tid; i < size; i += kSpThreads) list[i] = ~0ull;
+#pragma unroll
+    for (int i = 0; i < KOF; ++i)
+      if (tid + i * kSpThreads < size) list[tid + i * kSpThreads] = key[i];
+    for (int i = tid + KOF * kSpThreads; i < size; i += kSpThreads) list[i] = ~0ull;
     __syncthreads();
     for (int k = 2; k <= size; k *= 2) {
       for (int j = k / 2; j > 0; j /= 2) {
@@ -396,59 +578,74 @@ struct Row {
         __syncthreads();
       }
     }
-    u64 w[4], sum = 0;
+    u64 w[KOF], sum = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int e = tid * 4 + i;
-      w[i] = e >= n ? 0 : !MASS ? 1 : weight(unordered(~(uint32_t)(list[e] >> 32)), r, sh.exp2);
+    for (int i = 0; i < KOF; ++i) {
+      w[i] = tid * KOF + i < n ? raw<MASS>(list[tid * KOF + i]) : 0;
       sum += w[i];
     }
-    u64 t = before + block_before(sum);
+    u64 t;
+    block_scan(sum, t);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (t < target && t + w[i] >= target) {
-        const u64 e = list[tid * 4 + i];
-        for (uint32_t c = 0; c < C; ++c) st_rank(&sh.res[0], c, (u64)~(uint32_t)(e >> 32) << 32 | (uint32_t)e);
+    for (int i = 0; i < KOF; ++i) {
+      if (t < goal && t + w[i] >= goal) {
+        answer(list[tid * KOF + i], t + w[i]);
+        sh.bcast[0] = list[tid * KOF + i];
       }
       t += w[i];
     }
   }
 
-  // The same by the bits of z: 11, 11 and 10 of them, then by index among equals.
+  // The same of a bin with many tokens, by the bits of z: 11 at a time, then by index among equals.
   template <bool MASS, typename B>
-  __device__ void narrow(B bin_of, int bin, u64 target, u64 before) {
+  __device__ void narrow(B inside, u64 goal) {
     uint32_t prefix = 0;
-    for (int level = 0; level < 3; ++level) {
-      const int shift = level == 0 ? 21 : level == 1 ? 10 : 0, bits = level == 2 ? 10 : 11;
+    u64 before = 0;
+    for (int level = 0; level < 4; ++level) {
+      const int shift = 24 - 8 * level;
       tc::cluster_sync();
-      clear();
-      each([&](float z, int l) {
-        if (!kept(z, l) || bin_of(z) != bin) return;
-        const uint32_t key = ~ordered(z);
-        if (level > 0 && (key >> (shift + bits)) != prefix) return;
-        add<MASS>((int)(key >> shift) & ((1 << bits) - 1), z);
+      clear(kSpBins);
+      each([&](const float* v, int ch, int h) {
+#pragma unroll
+        for (int i = 0; i < kStep; ++i) {
+          if (!inside(v[i]) || !kept(v[i], at(ch, h, i))) continue;
+          const uint32_t key = ~ordered(v[i]);
+          if (level > 0 && key >> (shift + 8) != prefix) continue;
+          int J;
+          add<MASS>((int)(key >> shift & 255u), MASS ? mass.one(v[i], sh.exp2, J) : 1);
+        }
       });
       int digit;
-      find(target, before, digit);
-      prefix = prefix << bits | (uint32_t)digit;
+      u64 here;
+      find<false>(goal, here, digit);
+      goal -= here;
+      before += here;
+      prefix = prefix << 8 | (uint32_t)digit;
     }
+    const u64 end = (u64)prefix << 32;
     const float zc = unordered(~prefix);
-    const u64 w = MASS ? weight(zc, r, sh.exp2) : 1;
-    u64 keep = (target - before + w - 1) / w;  // the sum reached the target here, so w > 0
+    const u64 w = raw<MASS>(end);
+    u64 keep = (goal + w - 1) / w;
+    before += keep * w;
     // how many equals each CTA's chunks hold
     u64* cnt = reinterpret_cast<u64*>(buf);
     u64 mine = 0;
     for (int ch = warp; ch < chunks; ch += kSpWarps) {
-      float v[16];
-      values(ch, v);
-      u64 c = 0;
+      int c = 0;
+      for (int h = 0; h < kSpChunk / (32 * kStep); ++h) {
+        float v[kStep];
+        values(ch, h, v);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) c += v[i] == zc && kept(v[i], at(ch, i)) ? 1 : 0;
-      c = warp_sum64(c);
-      if (lane == 0) cnt[ch] = c;
-      mine += c;
+        for (int i = 0; i < kStep; ++i) c += v[i] == zc && kept(v[i], at(ch, h, i)) ? 1 : 0;
+      }
+      c = __reduce_add_sync(0xFFFFFFFFu, c);
+      if (lane == 0) {
+        cnt[ch] = (u64)c;
+        mine += (u64)c;
+      }
     }
-    mine = block_sum(lane == 0 ? mine : 0);
+    u64 ignored;
+    mine = block_scan(mine, ignored);
     const u64(*s)[2] = tell(mine, 0);
     u64 pre = 0;
     for (uint32_t c = 0; c < rank; ++c) pre += s[c][0];
@@ -463,13 +660,40 @@ struct Row {
         const uint32_t hit = __ballot_sync(0xFFFFFFFFu, z == zc && kept(z, l));
         const int here = __popc(hit);
         if (keep <= (u64)here) {
-          const int last = start + ch * kSpChunk + g * 32 + (int)__fns(hit, 0, (int)keep);
-          if (lane < (int)C) st_rank(&sh.res[0], lane, (u64)ordered(zc) << 32 | (uint32_t)last);
+          if (lane == 0) answer(end | (uint32_t)(start + ch * kSpChunk + g * 32 + (int)__fns(hit, 0, (int)keep)), before);
           break;
         }
         keep -= here;
       }
     }
+  }
+
+  // Masses are relative to the bins' zero: the logarithm of what that is off the maximum.
+  __device__ __forceinline__ float offset() const {
+    const float b = kSpMagic - mass.s.mb, x = m - mass.s.sub;
+    return -(fmaf(x, mass.s.hi, -b) + x * mass.lo) * 0.0216608494f;  // ln(2) / 32
+  }
+  // The kept mass of a step, a multiple of 2^-q.
+  __device__ __forceinline__ u64 sum_of(const float* v, int ch, int h) const {
+    u64 sum = 0;
+#pragma unroll
+    for (int i = 0; i < kStep; i += 2) {
+      uint32_t t[2], mant[2];
+      mass.two(v[i], v[i + 1], sh.exp2, t, mant);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const u64 w = weigh(mant[k], (int)t[k]);
+        if (kept(v[i + k], at(ch, h, i + k))) sum += w;
+      }
+    }
+    return sum;
+  }
+  // t: the bits of kSpMagic + J
+  __device__ __forceinline__ u64 weigh(uint32_t mant, int t) const {
+    const int e = (int)((kSpMagicBits >> 5) - ((uint32_t)(t & ~1) >> 5));
+    const int s = e + 62 - a.q;
+    const u64 w = (((u64)mant << 32) + (1ull << (s - 1 & 63))) >> (s & 63);
+    return t > (int)(kSpMagicBits - kSpLast) && s < 64 ? w : 0;
   }
 };
 
@@ -478,7 +702,8 @@ template <typename T, bool RES, bool DIST>
 __global__ void __launch_bounds__(kSpThreads, 2) k_sample(SpArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ SpShared sh;
-  Row<T, RES> w(a, sh);
+  typedef Row<T, RES> R;
+  R w(a, sh);
   w.tid = threadIdx.x;
   w.warp = w.tid >> 5;
   w.lane = w.tid & 31;
@@ -492,8 +717,7 @@ __global__ void __launch_bounds__(kSpThreads, 2) k_sample(SpArgs a) {
   w.start = (int)min((int64_t)w.rank * a.part, (int64_t)a.V);
   w.count = min(a.part, a.V - w.start);
   w.chunks = (w.count + kSpChunk - 1) / kSpChunk;
-  w.r.q = a.q;
-  if (tid < 64) sh.exp2[tid] = make_uint2(kSpExp2[tid], __float_as_uint((float)kSpExp2[tid]));
+  if (tid < 16) sh.exp2[tid] = make_uint2(kSpExp2[tid], __float_as_uint((float)kSpExp2[tid]));
   pdl_wait();
   pdl_trigger();
 
@@ -519,8 +743,8 @@ __global__ void __launch_bounds__(kSpThreads, 2) k_sample(SpArgs a) {
       k = 1;
     }
     t = fmaxf(t, 1e-30f);
-    // log2(e) / T, its rounding error with it
-    const float l_hi = 1.44269502f, l_lo = 1.92596303e-08f;
+    // 32 log2(e) / T, its rounding error with it
+    const float l_hi = 46.1662407f, l_lo = 6.16308171e-07f;
     sh.c_hi = l_hi / t;
     sh.c_lo = (fmaf(-sh.c_hi, t, l_hi) + l_lo) / t;
     sh.inv_t = 1.f / t;
@@ -530,71 +754,64 @@ __global__ void __launch_bounds__(kSpThreads, 2) k_sample(SpArgs a) {
     sh.k = k;
   }
 
-  // the row's part: to shared memory, its maximum and the sum of its logits on the way
-  float top = -INFINITY, sum = 0.f;
-  u64 seen = 0;  // tokens not masked; above them, whether there is a NaN or +inf
+  // the row's part: to shared memory, its maximum on the way, and a sample of its logits
+  float top = -INFINITY, sum = 0.f, seen = 0.f;
   for (int ch = w.warp; ch < w.chunks; ch += kSpWarps) {
-    float v[16];
-    w.fetch(ch, v);
+    float v[2][R::kStep];
+    w.fetch(ch, 0, v[0]);
+    w.fetch(ch, 1, v[1]);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      if (!(v[i] < INFINITY)) seen |= 1ull << 40;
-      v[i] = clean(v[i]);
-      top = fmaxf(top, v[i]);
-      if (v[i] > -INFINITY) {
-        sum += fmaxf(v[i], -1e4f);
-        ++seen;
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int i = 0; i < R::kStep; ++i) {
+        v[h][i] = clean(v[h][i]);
+        top = max_nan(top, v[h][i]);
+      }
+      if (RES) {
+#pragma unroll
+        for (int g = 0; g < R::kStep / R::kPer; ++g) {
+          T t[R::kPer];
+#pragma unroll
+          for (int i = 0; i < R::kPer; ++i) t[i] = T(v[h][g * R::kPer + i]);
+          *reinterpret_cast<uint4*>(w.part + w.at(ch, h, g * R::kPer)) = *reinterpret_cast<const uint4*>(t);
+        }
       }
     }
-    if (RES) {
-#pragma unroll
-      for (int g = 0; g < 16 / Row<T, RES>::kPer; ++g) {
-        T t[Row<T, RES>::kPer];
-#pragma unroll
-        for (int i = 0; i < Row<T, RES>::kPer; ++i) t[i] = T(v[g * Row<T, RES>::kPer + i]);
-        *reinterpret_cast<uint4*>(w.part + w.at(ch, g * Row<T, RES>::kPer)) = *reinterpret_cast<const uint4*>(t);
-      }
+    if (v[0][0] > -INFINITY) {
+      sum += fmaxf(v[0][0], -1e4f);
+      seen += 1.f;
     }
   }
-  top = warp_max(top);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
   sum = warp_sum(sum);
-  const u64 bad_here = (u64)__any_sync(0xFFFFFFFFu, seen >> 40 != 0) << 40;
-  seen = (warp_sum64(seen & 0xFFFFFFFFFFull) & 0xFFFFFFFFFFull) | bad_here;
+  seen = warp_sum(seen);
   if (w.lane == 0) {
-    sh.warp[w.warp] = (u64)ordered(top) << 32 | __float_as_uint(sum);
-    sh.warp2[w.warp] = seen;
+    sh.warp[w.warp] = __float_as_uint(top);
+    sh.warp2[w.warp] = (u64)__float_as_uint(sum) << 32 | __float_as_uint(seen);
   }
   __syncthreads();
   const double t_log = __longlong_as_double((long long)sh.bcast[0]);
-  if (tid == 0) {
-    uint32_t o = 0;
-    u64 c = 0;
-    float s = 0.f;
-    for (int i = 0; i < kSpWarps; ++i) {
-      o = max(o, (uint32_t)(sh.warp[i] >> 32));
-      s += __uint_as_float((uint32_t)sh.warp[i]);
-      c = ((c | sh.warp2[i]) & (1ull << 40)) | ((c & 0xFFFFFFFFFFull) + (sh.warp2[i] & 0xFFFFFFFFFFull));
-    }
-    sh.warp[0] = (u64)o << 32 | __float_as_uint(s);
-    sh.warp2[0] = c;
+  bool bad = sh.bad;
+  sum = seen = 0.f;
+  for (int i = 0; i < kSpWarps; ++i) {
+    top = max_nan(top, __uint_as_float((uint32_t)sh.warp[i]));
+    sum += __uint_as_float((uint32_t)(sh.warp2[i] >> 32));
+    seen += __uint_as_float((uint32_t)sh.warp2[i]);
   }
   __syncthreads();
-  uint32_t o = 0;
-  u64 live = 0;
-  float all = 0.f;
-  bool bad = sh.bad;
   asm volatile("barrier.cluster.wait;" ::: "memory");
   {
-    const u64(*s)[2] = w.tell(sh.warp[0], sh.warp2[0]);
+    const u64(*s)[2] = w.tell(__float_as_uint(top), (u64)__float_as_uint(sum) << 32 | __float_as_uint(seen));
+    sum = seen = 0.f;
     for (uint32_t c = 0; c < w.C; ++c) {
-      o = max(o, (uint32_t)(s[c][0] >> 32));
-      all += __uint_as_float((uint32_t)s[c][0]);
-      live += s[c][1] & 0xFFFFFFFFFFull;
-      bad |= s[c][1] >> 40 != 0;
+      top = max_nan(top, __uint_as_float((uint32_t)s[c][0]));
+      sum += __uint_as_float((uint32_t)(s[c][1] >> 32));
+      seen += __uint_as_float((uint32_t)s[c][1]);
     }
   }
-  const bool none = bad || live == 0;
-  if (none) {
+  bad |= !(top < INFINITY);
+  if (bad || top == -INFINITY) {
     if (bad && w.rank == 0 && tid == 0) raise_status(a.status, DSPARK_ENUMERIC);
     if (DIST) {
       float* out = a.out + (int64_t)n * a.ldo + w.start;
@@ -606,72 +823,84 @@ __global__ void __launch_bounds__(kSpThreads, 2) k_sample(SpArgs a) {
     tc::cluster_sync();  // no CTA ends while another may still write to it
     return;
   }
-  w.r.m = unordered(o);
-  w.r.c_hi = sh.c_hi;
-  w.r.c_lo = sh.c_lo;
-  w.r.inv_t = sh.inv_t;
-
-  // top-k: bins up to four times the mean distance from the maximum (half of the tokens lie within two)
-  if (sh.k > 0 && (u64)sh.k < live) {
-    const float mean = w.r.m - all / (float)live;
-    w.template select<false>((u64)sh.k, mean > 0.f ? kSpBins / (4.f * mean) : 0.f);
+  w.m = top;
+  {
+    // the bins' zero: a whole number next to the maximum, one above it, so that its product's rounding error
+    // (2^-3 of a bin) leaves J <= 0
+    const float at = top * sh.c_hi;
+    const bool far = !(fabsf(at) < 2097152.f);
+    w.mass.s.sub = far ? top : 0.f;
+    w.mass.s.hi = sh.c_hi;
+    w.mass.s.mb = kSpMagic - 1.f - (far ? 0.f : rintf(at));
+    w.mass.lo = sh.c_lo;
   }
-  // top-p: bins of 1/64 bit of mass
-  if (sh.p < 1.f) w.template select<true>(0, kSpBins / 32 * w.r.c_hi);
+
+  if (sh.k > 0 && sh.k < a.V) {
+    // bins up to four times the mean distance from the maximum: half of the tokens lie within two
+    const float mean = top - sum / fmaxf(seen, 1.f);
+    const float beta = mean > 0.f ? fminf(kSpBins / (4.f * mean), 1e30f) : 0.f;
+    w.template select<false>((u64)sh.k, SpScale{top, beta, kSpMagic});
+  }
+  if (sh.p < 1.f) w.template select<true>(0, w.mass.s);
+  bool exact = sh.p < 1.f;  // held is the kept mass
   if (t_log > -INFINITY) {
-    const double t = (double)w.r.m + t_log;
-    float z = __double2float_ru(t);
-    if (z > w.cut.z) w.cut = SpCut{z, a.V};
+    const float z = __double2float_ru((double)top + t_log);
+    if (z > w.cut.z) {
+      w.cut = SpCut{z, 0x7FFFFFFF};
+      exact = false;
+    }
   }
 
-  // the kept mass
-  u64 S = 0, before = 0;
   if (DIST) {
-    u64 t = 0;
-    w.each([&](float z, int l) {
-      if (w.kept(z, l)) t += weight(z, w.r, sh.exp2);
-    });
-    const u64 mine = w.block_sum(t);
-    const u64(*s)[2] = w.tell(mine, 0);
-    for (uint32_t c = 0; c < w.C; ++c) S += s[c][0];
-    const float ls = logf((float)S * exp2f(-(float)a.q));
+    u64 S = w.held;
+    if (!exact) {
+      u64 t = 0, ignored;
+      w.each([&](const float* v, int ch, int h) { t += w.sum_of(v, ch, h); });
+      const u64 mine = w.block_scan(t, ignored);
+      const u64(*s)[2] = w.tell(mine, 0);
+      S = 0;
+      for (uint32_t c = 0; c < w.C; ++c) S += s[c][0];
+    }
+    const float ls = logf((float)S * exp2f(-(float)a.q)) + w.offset();
     float* out = a.out + (int64_t)n * a.ldo + w.start;
-    for (int ch = w.warp; ch < w.chunks; ch += kSpWarps) {
-      float v[16];
-      w.values(ch, v);
+    w.each([&](const float* v, int ch, int h) {
+      float y[R::kStep];
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        v[i] = w.kept(v[i], w.at(ch, i)) ? fmaf(v[i] - w.r.m, w.r.inv_t, -ls) : a.fill;
+      for (int i = 0; i < R::kStep; ++i)
+        y[i] = w.kept(v[i], w.at(ch, h, i)) ? fmaf(v[i] - top, sh.inv_t, -ls) : a.fill;
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int l = w.at(ch, g * 4);
+      for (int g = 0; g < R::kStep / 4; ++g) {
+        const int l = w.at(ch, h, g * 4);
         if (a.vec_out && l + 4 <= w.count) {
-          __stcs(reinterpret_cast<float4*>(out + l), make_float4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]));
+          __stcs(reinterpret_cast<float4*>(out + l), make_float4(y[4 * g], y[4 * g + 1], y[4 * g + 2], y[4 * g + 3]));
         } else {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (l + i < w.count) out[l + i] = v[4 * g + i];
+            if (l + i < w.count) out[l + i] = y[4 * g + i];
         }
       }
-    }
+    });
   } else {
     u64* chunk = reinterpret_cast<u64*>(w.buf);
     for (int ch = w.warp; ch < w.chunks; ch += kSpWarps) {
-      float v[16];
-      w.values(ch, v);
       u64 t = 0;
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {
+        float v[R::kStep];
+        w.values(ch, h, v);
+        bool some = false;  // of most rows few tokens are kept
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (w.kept(v[i], w.at(ch, i))) t += weight(v[i], w.r, sh.exp2);
+        for (int i = 0; i < R::kStep; ++i) some |= v[i] >= w.cut.z;
+        if (__any_sync(0xFFFFFFFFu, some)) t += w.sum_of(v, ch, h);
+      }
       t = warp_sum64(t);
       if (w.lane == 0) chunk[ch] = t;
     }
     __syncthreads();
     constexpr int kEach = kSpMaxChunks / kSpThreads;
-    u64 t = 0;
+    u64 t = 0, S = 0, before = 0, mine_before;
     for (int i = 0; i < kEach; ++i) t += tid * kEach + i < w.chunks ? chunk[tid * kEach + i] : 0;
-    const u64 mine_before = w.block_before(t);
-    const u64 mine = w.block_sum(t);
+    const u64 mine = w.block_scan(t, mine_before);
     const u64(*s)[2] = w.tell(mine, 0);
     for (uint32_t c = 0; c < w.C; ++c) {
       if (c == w.rank) before = S;
@@ -695,17 +924,14 @@ __global__ void __launch_bounds__(kSpThreads, 2) k_sample(SpArgs a) {
       // 32 tokens of the chunk a warp
       const int l = ch * kSpChunk + w.warp * 32 + w.lane;
       const float z = w.value(l);
-      const u64 own = w.kept(z, l) ? weight(z, w.r, sh.exp2) : 0;
-      const u64 inc = warp_scan64(own);
-      __syncthreads();
-      if (w.lane == 31) sh.warp[w.warp] = inc;
-      __syncthreads();
-      u64 y = inc - own;
-      for (int i = 0; i < w.warp; ++i) y += sh.warp[i];
+      int J;
+      const uint32_t mant = w.mass.one(z, sh.exp2, J);
+      const u64 own = w.kept(z, l) ? w.weigh(mant, J + (int)kSpMagicBits) : 0;
+      u64 y;
+      w.block_scan(own, y);
       if (rest >= y && rest < y + own) {
         a.token[n] = w.start + l;
-        if (a.logp)
-          a.logp[n] = (float)((double)(z - w.r.m) * (double)w.r.inv_t - (double)logf((float)S * exp2f(-(float)a.q)));
+        if (a.logp) a.logp[n] = (z - top) * sh.inv_t - (logf((float)S * exp2f(-(float)a.q)) + w.offset());
       }
     }
   }
