@@ -13,13 +13,16 @@
 //
 // top-k and top-p are one search, for the first token of the row sorted by
 // falling z (then by index) at which the running sum, of ones or of masses,
-// reaches a target. A histogram of 1536 bins of z (for masses 1/32 of an octave each, so that
+// reaches a target. A histogram of 1216 bins of z (for masses 1/32 of an octave each, so that
 // a bin's tokens share e and their mants are added as they are) gives the bin; its tokens
 // (some hundreds of a flat row of 129280) are brought to one CTA, which splits them
-// into 512 narrower bins and looks at the few tokens of one of those. A bin of more than 1536 tokens (many
-// equal logits) is instead narrowed by three histograms of the bits of z, down to one value,
+// into 256 narrower bins, again and again until few are left. A bin of more than 1216 tokens (many
+// equal logits) is instead narrowed by four histograms of the bits of z, down to one value,
 // whose tokens are counted by index. What is kept is z >= cut; tokens that equal the cut
 // but come after its last index are masked in shared memory.
+//
+// Three CTAs share an SM, so that a row's barriers and loads pass under the others' arithmetic: 64 KB of a
+// row each, 256 threads.
 #include <math.h>
 #include <stdio.h>
 
@@ -33,16 +36,15 @@ namespace {
 
 typedef unsigned long long u64;
 
-constexpr int kSpThreads = 512, kSpWarps = kSpThreads / 32;
+constexpr int kSpThreads = 256, kSpWarps = kSpThreads / 32;
 constexpr int kSpMaxC = 16;       // CTAs of a cluster
-constexpr int kSpBins = 1536;     // 48 octaves of 32 bins
-constexpr int kSpLast = 1504;     // bins from here on (masses below 2^-47) count as nothing
+constexpr int kSpBins = 1216;     // 38 octaves of 32 bins, the last one for what lies below
+constexpr int kSpNone = 1504;     // from here on (2^-47) a mass is nothing
 constexpr int kSpList = kSpBins;  // tokens of a bin that are brought together
 constexpr int kSpChunk = 512;     // tokens that a warp takes at a time
-constexpr int kSpMaxChunks = 2048;
 constexpr float kSpMasked = -1e29f;
 constexpr float kSpLowest = -3.402823466e38f;
-constexpr int kSpHist = kSpMaxChunks * 8;  // bytes: the histogram, the list or the chunks' sums
+constexpr int kSpHist = kSpBins * 8;  // bytes: the histogram, the list or the chunks' sums
 constexpr float kSpMagic = 12582912.f;     // 1.5 * 2^23: sums with it round to whole numbers
 constexpr uint32_t kSpMagicBits = 0x4B400000u;
 
@@ -101,6 +103,31 @@ __device__ __forceinline__ float unordered(uint32_t o) {
   return __uint_as_float(o ^ ((int32_t)o < 0 ? 0x80000000u : 0xFFFFFFFFu));
 }
 
+// Shared memory by 32-bit addresses, the histogram's updates under a predicate in place of a branch.
+__device__ __forceinline__ uint4 lds128(uint32_t p) {
+  uint4 q;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w) : "r"(p) : "memory");
+  return q;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t p) {  // of what no one changes
+  uint2 q;
+  asm("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(q.x), "=r"(q.y) : "r"(p));
+  return q;
+}
+__device__ __forceinline__ void count_if(uint32_t p, bool on) {
+  asm volatile("{\n .reg .pred p;\n setp.ne.s32 p, %1, 0;\n @p red.shared.add.u32 [%0], 1;\n}" ::"r"(p), "r"((int)on)
+               : "memory");
+}
+// a 64-bit sum as two words kSpBins apart: a carry goes to the upper one
+__device__ __forceinline__ void add_if(uint32_t p, uint32_t x, bool on) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n .reg .u32 o, s;\n setp.ne.s32 p, %2, 0;\n mov.u32 o, 0;\n"
+      " @p atom.shared.add.u32 o, [%0], %1;\n add.u32 s, o, %1;\n setp.lt.and.u32 q, s, o, p;\n"
+      " @q red.shared.add.u32 [%0 + %3], 1;\n}" ::"r"(p),
+      "r"(x), "r"((int)on), "n"(kSpBins * 4)
+      : "memory");
+}
+
 // The mass of tokens, of two at a time where it matters. In units of 1/32 octave y is
 //   x = (z - sub) (hi + lo) - B,   hi + lo = 32 log2(e) / T,   B = mb's whole number,
 // J = round(x) <= 0 names the token's bin, q = J rounded down to an even number its
@@ -118,20 +145,20 @@ struct Mass {
     const float p = r * fmaf(r, fmaf(r, fmaf(r, 9.1725627e-09f, 1.69385097e-06f), 0.000234596198f), 0.0216608494f);
     mant = ti + (uint32_t)__float2int_rn(tf * p);
   }
-  __device__ __forceinline__ uint32_t one(float z, const uint2* tab, int& J) const {
+  __device__ __forceinline__ uint32_t one(float z, uint32_t tab, int& J) const {
     const float x = z - s.sub;
     const uint32_t t = __float_as_uint(fmaf(x, s.hi, s.mb));
     const uint32_t tq = t & ~1u;
     float r = fmaf(x, s.hi, fmaf(__uint_as_float(tq), -1.f, s.mb) + -0.5f);
     r = fmaf(x, lo, r);
-    const uint2 w = tab[(tq >> 1) & 15u];
+    const uint2 w = lds64(tab + (tq << 2 & 0x78u));
     uint32_t mant;
     poly(r, __uint_as_float(w.y), w.x, mant);
     J = (int)(t - kSpMagicBits);
     return mant;
   }
   // the same of two tokens; t: the bits of kSpMagic + J
-  __device__ __forceinline__ void two(float z0, float z1, const uint2* tab, uint32_t* t, uint32_t* mant) const {
+  __device__ __forceinline__ void two(float z0, float z1, uint32_t tab, uint32_t* t, uint32_t* mant) const {
     const u64 x = tc::add2(tc::f2pack(z0, z1), tc::f2pack(-s.sub, -s.sub));
     const u64 hi = tc::f2pack(s.hi, s.hi), mb = tc::f2pack(s.mb, s.mb);
     float a, b;
@@ -148,7 +175,7 @@ struct Mass {
     p = tc::fma2(r, p, tc::f2pack(0.0216608494f, 0.0216608494f));
     p = tc::mul2(r, p);
     tc::f2unpack(p, a, b);
-    const uint2 w0 = tab[(q0 >> 1) & 15u], w1 = tab[(q1 >> 1) & 15u];
+    const uint2 w0 = lds64(tab + (q0 << 2 & 0x78u)), w1 = lds64(tab + (q1 << 2 & 0x78u));
     mant[0] = w0.x + (uint32_t)__float2int_rn(__uint_as_float(w0.y) * a);
     mant[1] = w1.x + (uint32_t)__float2int_rn(__uint_as_float(w1.y) * b);
   }
@@ -229,6 +256,7 @@ struct Row {
   SpShared& sh;
   uint8_t* buf;        // kSpHist bytes
   T* part;             // RES: the row's part
+  uint32_t tab, hist, data;  // shared addresses of sh.exp2, buf and part
   const T* row;        // the whole row, in global memory
   int tid, warp, lane;
   uint32_t rank, C;
@@ -237,6 +265,7 @@ struct Row {
   float m;                   // the row's maximum
   Mass mass;
   u64 held = 0;              // the mass up to the cut of a search for masses
+  bool low_mass = false;     // the search is in the last bin
   SpCut cut{kSpLowest, 0x7FFFFFFF};
 
   __device__ Row(const SpArgs& a_, SpShared& s_) : a(a_), sh(s_) {}
@@ -267,7 +296,7 @@ struct Row {
     if (RES) {
 #pragma unroll
       for (int g = 0; g < kStep / kPer; ++g)
-        unpack(*reinterpret_cast<const uint4*>(part + at(ch, h, g * kPer)), v + g * kPer);
+        unpack(lds128(data + (uint32_t)(at(ch, h, g * kPer) * (int)sizeof(T))), v + g * kPer);
     } else {
       fetch(ch, h, v);
 #pragma unroll
@@ -334,37 +363,28 @@ struct Row {
     }
     __syncthreads();
   }
-  // 64-bit sums as two words: a carry goes to the upper one
   template <bool MASS>
-  __device__ __forceinline__ void add(int bin, uint32_t x) {
-    if (!MASS) {
-      atomicAdd(lo() + bin, 1u);
-    } else {
-      const uint32_t old = atomicAdd(lo() + bin, x);
-      if (old + x < old) atomicAdd(hi() + bin, 1u);
-    }
+  __device__ __forceinline__ void add(int bin, uint32_t x, bool on) {
+    if (MASS) add_if(hist + 4u * (uint32_t)bin, x, on);
+    else count_if(hist + 4u * (uint32_t)bin, on);
+  }
+  // Bin g of all CTAs' histograms. OCT: raw mants of its octave, brought to multiples of 2^-q.
+  template <bool OCT>
+  __device__ __forceinline__ u64 bin_sum(int g) const {
+    u64 v = 0;
+    for (uint32_t c = 0; c < C; ++c)
+      v += (u64)(uint32_t)tc::ld_rank(hist + 4 * g, c) + ((u64)(uint32_t)tc::ld_rank(hist + 4 * (g + kSpBins), c) << 32);
+    return OCT && g < kSpBins - 1 ? scaled(v, octave(g), a.q) : v;
   }
   // With every CTA's histogram filled: the first bin at which the sum up to it reaches the target, and
-  // the sum before it. OCT: the bins hold raw mants of their octaves. target 0: ceil(p of all of it), at
-  // least 1. Returns whether the sum reaches the target at all.
+  // the sum before it. target 0: ceil(p of all of it), at least 1. Returns whether the sum reaches the target at all.
   template <bool OCT>
   __device__ __forceinline__ bool find(u64& target, u64& before, int& bin) {
     tc::cluster_sync();
-    const int seg = kSpBins / (int)C;
-    u64 v[3], sum = 0;  // 1536 bins of one CTA alone: three a thread
-#pragma unroll
-    for (int i = 0; i < 3; ++i) {
-      v[i] = 0;
-      const int b = tid * (C == 1 ? 3 : C == 2 ? 2 : 1) + i;
-      if ((C == 1 || (C == 2 && i < 2) || i < 1) && b < seg) {
-        const int g = (int)rank * seg + b;
-        for (uint32_t c = 0; c < C; ++c)
-          v[i] += (u64)(uint32_t)tc::ld_rank(tc::smem_u32(lo() + g), c) +
-                  ((u64)(uint32_t)tc::ld_rank(tc::smem_u32(hi() + g), c) << 32);
-        if (OCT) v[i] = g < kSpLast && octave(g) <= a.q + 1 ? scaled(v[i], octave(g), a.q) : 0;
-      }
-      sum += v[i];
-    }
+    const int seg = kSpBins / (int)C, per = (seg + kSpThreads - 1) / kSpThreads;
+    const int b0 = min(tid * per, seg), b1 = min(b0 + per, seg);
+    u64 sum = 0;
+    for (int b = b0; b < b1; ++b) sum += bin_sum<OCT>((int)rank * seg + b);
     u64 mine;
     const u64 all = block_scan(sum, mine);
     const u64(*s)[2] = tell(all, 0);
@@ -379,16 +399,19 @@ struct Row {
     }
     if (target > total) return false;
     u64 t = pre + mine;
-#pragma unroll
-    for (int i = 0; i < 3; ++i) {
-      if (t < target && t + v[i] >= target) {
-        const int g = (int)rank * seg + tid * (C == 1 ? 3 : C == 2 ? 2 : 1) + i;
-        for (uint32_t c = 0; c < C; ++c) {
-          st_rank(&sh.res[0], c, (u64)g);
-          st_rank(&sh.res[1], c, t);
+    if (t < target && t + sum >= target) {
+      int b = b0;
+      if (per > 1) {
+        for (;; ++b) {
+          const u64 v = bin_sum<OCT>((int)rank * seg + b);
+          if (t + v >= target) break;
+          t += v;
         }
       }
-      t += v[i];
+      for (uint32_t c = 0; c < C; ++c) {
+        st_rank(&sh.res[0], c, (u64)((int)rank * seg + b));
+        st_rank(&sh.res[1], c, t);
+      }
     }
     tc::cluster_sync();
     bin = (int)sh.res[0];
@@ -397,39 +420,57 @@ struct Row {
   }
 
   // Tightens the cut to the first of the kept tokens, in order, at which the running
-  // count (MASS: mass) reaches the target.
+  // count (MASS: mass) reaches the target. The last bin takes in what lies below the others (its masses
+  // are added as multiples of 2^-q).
   template <bool MASS>
   __device__ void select(u64 target, const SpScale& b) {
-    constexpr uint32_t kLow = kSpMagicBits - (MASS ? kSpLast - 1 : kSpBins - 1);
-    auto bits_of = [&](float z) { return __float_as_uint(fmaf(z - b.sub, b.hi, b.mb)); };
+    constexpr int kLow = (int)kSpMagicBits - (kSpBins - 1);
+    auto bits_of = [&](float z) { return __float_as_int(fmaf(z - b.sub, b.hi, b.mb)); };
     clear(kSpBins);
     if (tid == 0) sh.n = 0;
+    u64 light = 0;
     each([&](const float* v, int ch, int h) {
 #pragma unroll
       for (int i = 0; i < kStep; i += 2) {
         uint32_t t[2], mant[2] = {1, 1};
         if (MASS) {
-          mass.two(v[i], v[i + 1], sh.exp2, t, mant);
+          mass.two(v[i], v[i + 1], tab, t, mant);
         } else {
-          t[0] = max((int)bits_of(v[i]), (int)kLow);  // -inf and below the bins: the last one
-          t[1] = max((int)bits_of(v[i + 1]), (int)kLow);
+          t[0] = (uint32_t)max(bits_of(v[i]), kLow);
+          t[1] = (uint32_t)max(bits_of(v[i + 1]), kLow);
         }
+        bool on[2];
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
-          if (kept(v[i + k], at(ch, h, i + k)) && (int)t[k] >= (int)kLow) add<MASS>((int)(kSpMagicBits - t[k]), mant[k]);
+        for (int k = 0; k < 2; ++k) {
+          on[k] = kept(v[i + k], at(ch, h, i + k));
+          if (MASS && on[k] && (int)t[k] <= kLow) light += weigh(mant[k], (int)t[k]);
+          add<MASS>((int)(kSpMagicBits - t[k]), mant[k], on[k] && (!MASS || (int)t[k] > kLow));
+        }
       }
     });
+    if (MASS) {
+      light = warp_sum64(light);
+      if (lane == 0 && light) {  // at most 2^17 tokens of 2^-36
+        add_if(hist + 4 * (kSpBins - 1), (uint32_t)light, true);
+        if (light >> 32) atomicAdd(hi() + kSpBins - 1, (uint32_t)(light >> 32));
+      }
+    }
     u64 before = 0;
     int bin;
     if (!find<MASS>(target, before, bin)) return;
+    const bool low = bin == kSpBins - 1;
+    low_mass = MASS && low;
     const int e = octave(bin);
-    const u64 goal = MASS ? unscaled(target - before, e, a.q) : target - before;  // of the bin's raw sum
-    const bool low = !MASS && bin == kSpBins - 1;  // and everything below it
-    const uint32_t bits = kSpMagicBits - bin;
-    auto inside = [&](float z) { return low ? (int)bits_of(z) <= (int)bits : bits_of(z) == bits; };
+    const u64 goal = MASS && !low ? unscaled(target - before, e, a.q) : target - before;  // of the bin's raw sum
+    const int bits = (int)kSpMagicBits - bin;
+    auto inside = [&](float z) { return low ? bits_of(z) <= bits : bits_of(z) == bits; };
     // the bin's tokens to CTA 0
     u64* list = reinterpret_cast<u64*>(buf);
     each([&](const float* v, int ch, int h) {
+      bool some = false;
+#pragma unroll
+      for (int i = 0; i < kStep; ++i) some |= inside(v[i]);
+      if (!some) return;
 #pragma unroll
       for (int i = 0; i < kStep; ++i) {
         if (inside(v[i]) && kept(v[i], at(ch, h, i))) {
@@ -448,7 +489,7 @@ struct Row {
     tc::cluster_sync();
     cut.z = unordered((uint32_t)(sh.res[0] >> 32));
     cut.last = (int)(uint32_t)sh.res[0];
-    if (MASS) held = before + scaled(sh.res[1], e, a.q);
+    if (MASS) held = before + (low ? sh.res[1] : scaled(sh.res[1], e, a.q));
     if (RES && n > kSpList) {  // cut_of_list has masked the others
       each([&](const float* v, int ch, int h) {
 #pragma unroll
@@ -461,8 +502,12 @@ struct Row {
 
   template <bool MASS>
   __device__ __forceinline__ uint32_t raw(u64 key) const {
+    return MASS ? raw_of(unordered(~(uint32_t)(key >> 32))) : 1;
+  }
+  __device__ __forceinline__ uint32_t raw_of(float z) const {
     int J;
-    return MASS ? mass.one(unordered(~(uint32_t)(key >> 32)), sh.exp2, J) : 1;
+    const uint32_t mant = mass.one(z, tab, J);
+    return low_mass ? (uint32_t)weigh(mant, J + (int)kSpMagicBits) : mant;
   }
   // The cut (ordered z, index) and the raw sum up to it, to every CTA.
   __device__ __forceinline__ void answer(u64 key, u64 sum) {
@@ -475,68 +520,81 @@ struct Row {
   // In CTA 0: keys (falling z, index) in any order.
   template <bool MASS>
   __device__ void cut_of_list(int n, u64 goal) {
-    u64* list = reinterpret_cast<u64*>(buf);
     constexpr int kOf = (kSpList + kSpThreads - 1) / kSpThreads;
     u64 key[kOf];
-    uint32_t least = ~0u, most = 0;
+    uint32_t live = 0;
 #pragma unroll
     for (int i = 0; i < kOf; ++i) {
       const int e = tid + i * kSpThreads;
-      key[i] = e < n ? list[e] : ~0ull;
-      if (e < n) {
-        least = min(least, (uint32_t)(key[i] >> 32));
-        most = max(most, (uint32_t)(key[i] >> 32));
-      }
+      key[i] = e < n ? reinterpret_cast<const u64*>(buf)[e] : ~0ull;
+      if (e < n) live |= 1u << i;
     }
-    least = __reduce_min_sync(0xFFFFFFFFu, least);
-    most = __reduce_max_sync(0xFFFFFFFFu, most);
-    if (lane == 0) sh.warp2[warp] = (u64)least << 32 | most;
-    if (tid == 0) sh.m = 0;
-    __syncthreads();  // the list is in registers, its memory free
+    u64 base = 0;
+    for (;;) {
+      u64 least = ~0ull, most = 0;
 #pragma unroll
-    for (int i = 0; i < kSpWarps; ++i) {
-      least = min(least, (uint32_t)(sh.warp2[i] >> 32));
-      most = max(most, (uint32_t)sh.warp2[i]);
-    }
-    const int shift = max(0, 32 - __clz(most - least) - 9);  // 512 narrower bins
-    clear(kSpThreads);
-#pragma unroll
-    for (int i = 0; i < kOf; ++i)
-      if (tid + i * kSpThreads < n) add<MASS>((int)(((uint32_t)(key[i] >> 32) - least) >> shift), raw<MASS>(key[i]));
-    __syncthreads();
-    const u64 here = (u64)lo()[tid] | (u64)hi()[tid] << 32;
-    u64 before;
-    block_scan(here, before);
-    if (before < goal && before + here >= goal) {
-      sh.bcast[0] = (u64)tid;
-      sh.bcast[1] = before;
-    }
-    __syncthreads();
-    const int bin = (int)sh.bcast[0];
-    const u64 base = sh.bcast[1];
-#pragma unroll
-    for (int i = 0; i < kOf; ++i)
-      if (tid + i * kSpThreads < n && (int)(((uint32_t)(key[i] >> 32) - least) >> shift) == bin) {
-        const int at = atomicAdd(&sh.m, 1);
-        if (at < 32) sh.few[at] = key[i];
-      }
-    __syncthreads();
-    if (sh.m <= 32) {
-      if (warp == 0) {
-        const u64 mine = lane < sh.m ? sh.few[lane] : ~0ull;
-        const u64 w = lane < sh.m ? raw<MASS>(mine) : 0;
-        u64 sum = base;
-        for (int i = 0; i < sh.m; ++i) {
-          const u64 other = __shfl_sync(0xFFFFFFFFu, mine, i), ow = __shfl_sync(0xFFFFFFFFu, w, i);
-          if (other < mine) sum += ow;
+      for (int i = 0; i < kOf; ++i)
+        if (live >> i & 1) {
+          least = min(least, key[i]);
+          most = max(most, key[i]);
         }
-        if (lane < sh.m && sum < goal && sum + w >= goal) {
-          answer(mine, sum + w);
-          sh.bcast[0] = mine;
-        }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        least = min(least, __shfl_xor_sync(0xFFFFFFFFu, least, o));
+        most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
       }
-    } else {
-      sorted<MASS>(key, n, goal);
+      __syncthreads();  // the list is in registers, and the last turn's words have been read
+      if (lane == 0) {
+        sh.warp[warp] = least;
+        sh.warp2[warp] = most;
+      }
+      if (tid == 0) sh.m = 0;
+      clear(kSpThreads);
+#pragma unroll
+      for (int i = 0; i < kSpWarps; ++i) {
+        least = min(least, sh.warp[i]);
+        most = max(most, sh.warp2[i]);
+      }
+      const int shift = max(0, 64 - __clzll(most - least) - 8);  // 256 bins
+#pragma unroll
+      for (int i = 0; i < kOf; ++i)
+        if (live >> i & 1) add<MASS>((int)((key[i] - least) >> shift), raw<MASS>(key[i]), true);
+      __syncthreads();
+      const u64 here = (u64)lo()[tid] | (u64)hi()[tid] << 32;
+      u64 before;
+      block_scan(here, before);
+      before += base;
+      if (before < goal && before + here >= goal) {
+        sh.bcast[0] = (u64)tid;
+        sh.bcast[1] = before;
+      }
+      __syncthreads();
+      base = sh.bcast[1];
+#pragma unroll
+      for (int i = 0; i < kOf; ++i)
+        if (live >> i & 1) {
+          if ((key[i] - least) >> shift == sh.bcast[0]) {
+            const int at = atomicAdd(&sh.m, 1);
+            if (at < 32) sh.few[at] = key[i];
+          } else {
+            live &= ~(1u << i);
+          }
+        }
+      __syncthreads();
+      if (sh.m <= 32) break;
+    }
+    if (warp == 0) {
+      const u64 mine = lane < sh.m ? sh.few[lane] : ~0ull;
+      const u64 w = lane < sh.m ? raw<MASS>(mine) : 0;
+      u64 sum = base;
+      for (int i = 0; i < sh.m; ++i) {
+        const u64 other = __shfl_sync(0xFFFFFFFFu, mine, i), ow = __shfl_sync(0xFFFFFFFFu, w, i);
+        if (other < mine) sum += ow;
+      }
+      if (lane < sh.m && sum < goal && sum + w >= goal) {
+        answer(mine, sum + w);
+        sh.bcast[0] = mine;
+      }
     }
     __syncthreads();
     if (RES) {  // equals of the cut that come after it
@@ -546,7 +604,7 @@ struct Row {
         if (tid + i * kSpThreads < n && key[i] > end && key[i] >> 32 == end >> 32) {
           const int idx = (int)(uint32_t)key[i];
           const uint32_t owner = idx / a.part;
-          const uint32_t p = tc::map_rank(tc::smem_u32(part + (idx - (int)owner * a.part)), owner);
+          const uint32_t p = tc::map_rank(data + (uint32_t)((idx - (int)owner * a.part) * (int)sizeof(T)), owner);
           if (sizeof(T) == 4)
             asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(p), "r"(0xFF800000u) : "memory");
           else
@@ -554,49 +612,8 @@ struct Row {
         }
     }
   }
-  // The same by sorting the whole list, where a narrower bin holds more than 32 tokens.
-  template <bool MASS, int KOF>
-  __device__ void sorted(const u64 (&key)[KOF], int n, u64 goal) {
-    u64* list = reinterpret_cast<u64*>(buf);
-    int size = 32;
-    while (size < n) size *= 2;
-#pragma unroll
-    for (int i = 0; i < KOF; ++i)
-      if (tid + i * kSpThreads < size) list[tid + i * kSpThreads] = key[i];
-    for (int i = tid + KOF * kSpThreads; i < size; i += kSpThreads) list[i] = ~0ull;
-    __syncthreads();
-    for (int k = 2; k <= size; k *= 2) {
-      for (int j = k / 2; j > 0; j /= 2) {
-        for (int i = tid; i < size / 2; i += kSpThreads) {
-          const int x = 2 * i - (i & (j - 1)), y = x + j;
-          const u64 p = list[x], q = list[y];
-          if ((p > q) == ((x & k) == 0)) {
-            list[x] = q;
-            list[y] = p;
-          }
-        }
-        __syncthreads();
-      }
-    }
-    u64 w[KOF], sum = 0;
-#pragma unroll
-    for (int i = 0; i < KOF; ++i) {
-      w[i] = tid * KOF + i < n ? raw<MASS>(list[tid * KOF + i]) : 0;
-      sum += w[i];
-    }
-    u64 t;
-    block_scan(sum, t);
-#pragma unroll
-    for (int i = 0; i < KOF; ++i) {
-      if (t < goal && t + w[i] >= goal) {
-        answer(list[tid * KOF + i], t + w[i]);
-        sh.bcast[0] = list[tid * KOF + i];
-      }
-      t += w[i];
-    }
-  }
 
-  // The same of a bin with many tokens, by the bits of z: 11 at a time, then by index among equals.
+  // The same of a bin with many tokens, by the bits of z, eight at a time, then by index among equals.
   template <bool MASS, typename B>
   __device__ void narrow(B inside, u64 goal) {
     uint32_t prefix = 0;
@@ -611,8 +628,7 @@ struct Row {
           if (!inside(v[i]) || !kept(v[i], at(ch, h, i))) continue;
           const uint32_t key = ~ordered(v[i]);
           if (level > 0 && key >> (shift + 8) != prefix) continue;
-          int J;
-          add<MASS>((int)(key >> shift & 255u), MASS ? mass.one(v[i], sh.exp2, J) : 1);
+          add<MASS>((int)(key >> shift & 255u), MASS ? raw_of(v[i]) : 1, true);
         }
       });
       int digit;
@@ -679,7 +695,7 @@ struct Row {
 #pragma unroll
     for (int i = 0; i < kStep; i += 2) {
       uint32_t t[2], mant[2];
-      mass.two(v[i], v[i + 1], sh.exp2, t, mant);
+      mass.two(v[i], v[i + 1], tab, t, mant);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const u64 w = weigh(mant[k], (int)t[k]);
@@ -693,13 +709,13 @@ struct Row {
     const int e = (int)((kSpMagicBits >> 5) - ((uint32_t)(t & ~1) >> 5));
     const int s = e + 62 - a.q;
     const u64 w = (((u64)mant << 32) + (1ull << (s - 1 & 63))) >> (s & 63);
-    return t > (int)(kSpMagicBits - kSpLast) && s < 64 ? w : 0;
+    return t > (int)(kSpMagicBits - kSpNone) && s < 64 ? w : 0;
   }
 };
 
 // DIST: the whole distribution is written; otherwise a token is drawn.
 template <typename T, bool RES, bool DIST>
-__global__ void __launch_bounds__(kSpThreads, 2) k_sample(SpArgs a) {
+__global__ void __launch_bounds__(kSpThreads, 3) k_sample(SpArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ SpShared sh;
   typedef Row<T, RES> R;
@@ -713,6 +729,9 @@ __global__ void __launch_bounds__(kSpThreads, 2) k_sample(SpArgs a) {
   const int n = (int)(blockIdx.x / w.C);
   w.buf = smem;
   w.part = reinterpret_cast<T*>(smem + kSpHist);
+  w.tab = tc::smem_u32(sh.exp2);
+  w.hist = tc::smem_u32(smem);
+  w.data = w.hist + kSpHist;
   w.row = static_cast<const T*>(a.Z) + (int64_t)n * a.ldz;
   w.start = (int)min((int64_t)w.rank * a.part, (int64_t)a.V);
   w.count = min(a.part, a.V - w.start);
@@ -820,8 +839,7 @@ __global__ void __launch_bounds__(kSpThreads, 2) k_sample(SpArgs a) {
       a.token[n] = -1;
       if (a.logp) a.logp[n] = bad ? NAN : -INFINITY;
     }
-    tc::cluster_sync();  // no CTA ends while another may still write to it
-    return;
+    return;  // nothing is written to another CTA after tell()
   }
   w.m = top;
   {
@@ -897,7 +915,7 @@ __global__ void __launch_bounds__(kSpThreads, 2) k_sample(SpArgs a) {
       if (w.lane == 0) chunk[ch] = t;
     }
     __syncthreads();
-    constexpr int kEach = kSpMaxChunks / kSpThreads;
+    const int kEach = (w.chunks + kSpThreads - 1) / kSpThreads;
     u64 t = 0, S = 0, before = 0, mine_before;
     for (int i = 0; i < kEach; ++i) t += tid * kEach + i < w.chunks ? chunk[tid * kEach + i] : 0;
     const u64 mine = w.block_scan(t, mine_before);
@@ -921,21 +939,29 @@ __global__ void __launch_bounds__(kSpThreads, 2) k_sample(SpArgs a) {
       __syncthreads();
       const int ch = (int)sh.bcast[0];
       const u64 rest = sh.bcast[1];
-      // 32 tokens of the chunk a warp
-      const int l = ch * kSpChunk + w.warp * 32 + w.lane;
-      const float z = w.value(l);
-      int J;
-      const uint32_t mant = w.mass.one(z, sh.exp2, J);
-      const u64 own = w.kept(z, l) ? w.weigh(mant, J + (int)kSpMagicBits) : 0;
-      u64 y;
-      w.block_scan(own, y);
-      if (rest >= y && rest < y + own) {
-        a.token[n] = w.start + l;
-        if (a.logp) a.logp[n] = (z - top) * sh.inv_t - (logf((float)S * exp2f(-(float)a.q)) + w.offset());
+      constexpr int kOwn = kSpChunk / kSpThreads;
+      u64 own[kOwn], sum = 0, y;
+#pragma unroll
+      for (int i = 0; i < kOwn; ++i) {
+        const int l = ch * kSpChunk + tid * kOwn + i;
+        const float z = w.value(l);
+        int J;
+        const uint32_t mant = w.mass.one(z, w.tab, J);
+        own[i] = w.kept(z, l) ? w.weigh(mant, J + (int)kSpMagicBits) : 0;
+        sum += own[i];
+      }
+      w.block_scan(sum, y);
+#pragma unroll
+      for (int i = 0; i < kOwn; ++i) {
+        if (rest >= y && rest < y + own[i]) {
+          const int l = ch * kSpChunk + tid * kOwn + i;
+          a.token[n] = w.start + l;
+          if (a.logp) a.logp[n] = (w.value(l) - top) * sh.inv_t - (logf((float)S * exp2f(-(float)a.q)) + w.offset());
+        }
+        y += own[i];
       }
     }
   }
-  tc::cluster_sync();  // no CTA ends while another may still write to it
 }
 
 bool type_ok(int t) { return t == DSPARK_F32 || t == DSPARK_BF16; }
@@ -996,15 +1022,16 @@ dspark_status sample(const dspark_sample_args* s, const void* Z, SpArgs a, int32
   int bits = 0;
   while ((1 << bits) < a.V) ++bits;
   a.q = 62 - bits < 46 ? 62 - bits : 46;
-  // The smallest cluster whose parts leave room for two CTAs on an SM, and more CTAs where the rows do
+  // The smallest cluster whose parts leave room for three CTAs on an SM, and more CTAs where the rows do
   // not fill the SMs, down to 2048 tokens a CTA.
   auto part = [&](int C) { return ((a.V + C - 1) / C + kSpChunk - 1) / kSpChunk * kSpChunk; };
   int C = 1;
-  while (C < kSpMaxC && (size_t)part(C) * size > 92 * 1024) C *= 2;
+  while (C < kSpMaxC && (size_t)part(C) * size > 64 * 1024) C *= 2;
   while (C < kSpMaxC && (int64_t)a.N * C < 152 && part(C) > 2048) C *= 2;
   a.part = part(C);
   const bool res = (size_t)a.part * size <= 180 * 1024;
-  const size_t smem = kSpHist + (res ? (size_t)a.part * size : 0);
+  const size_t sums = (size_t)a.part / kSpChunk * 8;
+  const size_t smem = res ? kSpHist + (size_t)a.part * size : sums > kSpHist ? sums : kSpHist;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   typedef __nv_bfloat16 bf;
   cudaError_t e;
