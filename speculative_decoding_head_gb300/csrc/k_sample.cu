@@ -90,10 +90,10 @@ struct SpShared {
   int k, n, m, bad;
 };
 
-// round(2^30 2^((2 i + 1/2) / 32))
+// round(2^30 2^(i / 16))
 __constant__ uint32_t kSpExp2[16] = {
-    1085434106u, 1133490379u, 1183674286u, 1236080024u, 1290805962u, 1347954824u, 1407633882u, 1469955159u,
-    1535035634u, 1602997467u, 1673968228u, 1748081133u, 1825475297u, 1906295993u, 1990694927u, 2078830522u};
+    1073741824u, 1121280436u, 1170923762u, 1222764986u, 1276901417u, 1333434672u, 1392470869u, 1454120821u,
+    1518500250u, 1585730000u, 1655936265u, 1729250827u, 1805811301u, 1885761398u, 1969251188u, 2056437387u};
 
 __device__ __forceinline__ uint32_t ordered(float z) {
   const uint32_t b = __float_as_uint(z + 0.f);  // -0 is 0
@@ -118,24 +118,31 @@ __device__ __forceinline__ void count_if(uint32_t p, bool on) {
   asm volatile("{\n .reg .pred p;\n setp.ne.s32 p, %1, 0;\n @p red.shared.add.u32 [%0], 1;\n}" ::"r"(p), "r"((int)on)
                : "memory");
 }
-// a 64-bit sum as two words kSpBins apart: a carry goes to the upper one
-__device__ __forceinline__ void add_if(uint32_t p, uint32_t x, bool on) {
+// A sum of numbers of 31 bits as two words kSpBins apart, of their lower 16 bits and of the rest: neither
+// overflows with up to 65536 numbers. Where v >= cut and t > low.
+__device__ __forceinline__ void add_if(uint32_t p, uint32_t x, float v, float cut, int t, int low) {
   asm volatile(
-      "{\n .reg .pred p, q;\n .reg .u32 o, s;\n setp.ne.s32 p, %2, 0;\n mov.u32 o, 0;\n"
-      " @p atom.shared.add.u32 o, [%0], %1;\n add.u32 s, o, %1;\n setp.lt.and.u32 q, s, o, p;\n"
-      " @q red.shared.add.u32 [%0 + %3], 1;\n}" ::"r"(p),
-      "r"(x), "r"((int)on), "n"(kSpBins * 4)
+      "{\n .reg .pred p;\n .reg .u32 l, h;\n setp.ge.f32 p, %2, %3;\n setp.gt.and.s32 p, %4, %5, p;\n"
+      " and.b32 l, %1, 65535;\n shr.u32 h, %1, 16;\n @p red.shared.add.u32 [%0], l;\n"
+      " @p red.shared.add.u32 [%0 + %6], h;\n}" ::"r"(p),
+      "r"(x), "f"(v), "f"(cut), "r"(t), "r"(low), "n"(kSpBins * 4)
       : "memory");
+}
+// The same of any many numbers, 32 bits in the lower word: a carry goes to the upper one.
+__device__ __forceinline__ void add_carry(uint32_t p, uint32_t x) {
+  uint32_t old;
+  asm volatile("atom.shared.add.u32 %0, [%1], %2;" : "=r"(old) : "r"(p), "r"(x) : "memory");
+  if (old + x < old) asm volatile("red.shared.add.u32 [%0 + %1], 1;" ::"r"(p), "n"(kSpBins * 4) : "memory");
 }
 
 // The mass of tokens, of two at a time where it matters. In units of 1/32 octave y is
 //   x = (z - sub) (hi + lo) - B,   hi + lo = 32 log2(e) / T,   B = mb's whole number,
 // J = round(x) <= 0 names the token's bin, q = J rounded down to an even number its
-// table entry and octave (e = -floor(q / 32)), and with r = x - q - 1/2, |r| <= 1,
+// table entry and octave (e = -floor(q / 32)), and with r = x - q in [-1/2, 3/2],
 //   2^(x/32) = 2^-e T[q mod 32 / 2] (1 + w + w^2/2 + w^3/6 + w^4/24),  w = r ln(2) / 32,
-// Taylor's next term being 2^-34. x is never rounded: the fma of z hi with -(q + B) is
-// exact up to its own rounding of r, 2^-25 of 1/32 octave, and the bracket less one is at
-// most 2^-5.5 in fp32. sub is 0; where the maximum is so many octaves from 0 that B would not fit (2^16)
+// Taylor's next term being 2^-31.5 at the most. x is never rounded: the fma of z hi with -(q + B) is
+// exact up to its own rounding of r, 2^-24 of 1/32 octave, and the bracket less one is at
+// most 2^-4.9 in fp32. sub is 0; where the maximum is so many octaves from 0 that B would not fit (2^16)
 // it is the maximum, and z - m is exact for every z whose mass counts (it is within 1/300 of m).
 // The table's sixteen entries of 8 bytes take a bank each: reads of it never conflict.
 struct Mass {
@@ -149,7 +156,7 @@ struct Mass {
     const float x = z - s.sub;
     const uint32_t t = __float_as_uint(fmaf(x, s.hi, s.mb));
     const uint32_t tq = t & ~1u;
-    float r = fmaf(x, s.hi, fmaf(__uint_as_float(tq), -1.f, s.mb) + -0.5f);
+    float r = fmaf(x, s.hi, fmaf(__uint_as_float(tq), -1.f, s.mb));
     r = fmaf(x, lo, r);
     const uint2 w = lds64(tab + (tq << 2 & 0x78u));
     uint32_t mant;
@@ -167,7 +174,6 @@ struct Mass {
     t[1] = __float_as_uint(b);
     const uint32_t q0 = t[0] & ~1u, q1 = t[1] & ~1u;
     u64 r = tc::fma2(tc::f2pack(__uint_as_float(q0), __uint_as_float(q1)), tc::f2pack(-1.f, -1.f), mb);
-    r = tc::add2(r, tc::f2pack(-0.5f, -0.5f));
     r = tc::fma2(x, hi, r);
     r = tc::fma2(x, tc::f2pack(lo, lo), r);
     u64 p = tc::fma2(r, tc::f2pack(9.1725627e-09f, 9.1725627e-09f), tc::f2pack(1.69385097e-06f, 1.69385097e-06f));
@@ -363,17 +369,20 @@ struct Row {
     }
     __syncthreads();
   }
+  static constexpr int kUp = RES ? 16 : 32;  // what a bin's upper word counts is 2^kUp
   template <bool MASS>
-  __device__ __forceinline__ void add(int bin, uint32_t x, bool on) {
-    if (MASS) add_if(hist + 4u * (uint32_t)bin, x, on);
-    else count_if(hist + 4u * (uint32_t)bin, on);
+  __device__ __forceinline__ void add(int bin, uint32_t x) {
+    const uint32_t p = hist + 4u * (uint32_t)bin;
+    if (!MASS) count_if(p, true);
+    else if (RES) add_if(p, x, 0.f, 0.f, 1, 0);
+    else add_carry(p, x);
   }
   // Bin g of all CTAs' histograms. OCT: raw mants of its octave, brought to multiples of 2^-q.
   template <bool OCT>
   __device__ __forceinline__ u64 bin_sum(int g) const {
     u64 v = 0;
     for (uint32_t c = 0; c < C; ++c)
-      v += (u64)(uint32_t)tc::ld_rank(hist + 4 * g, c) + ((u64)(uint32_t)tc::ld_rank(hist + 4 * (g + kSpBins), c) << 32);
+      v += (u64)(uint32_t)tc::ld_rank(hist + 4 * g, c) + ((u64)(uint32_t)tc::ld_rank(hist + 4 * (g + kSpBins), c) << kUp);
     return OCT && g < kSpBins - 1 ? scaled(v, octave(g), a.q) : v;
   }
   // With every CTA's histogram filled: the first bin at which the sum up to it reaches the target, and
@@ -430,29 +439,39 @@ struct Row {
     if (tid == 0) sh.n = 0;
     u64 light = 0;
     each([&](const float* v, int ch, int h) {
+      uint32_t t[kStep], mant[kStep];
+      if (MASS) {
+        // what lies between kLow and nothing, as one comparison of unsigned numbers
+        constexpr uint32_t kNone = kSpMagicBits - kSpNone;
+        uint32_t least = ~0u;
 #pragma unroll
-      for (int i = 0; i < kStep; i += 2) {
-        uint32_t t[2], mant[2] = {1, 1};
-        if (MASS) {
-          mass.two(v[i], v[i + 1], tab, t, mant);
-        } else {
-          t[0] = (uint32_t)max(bits_of(v[i]), kLow);
-          t[1] = (uint32_t)max(bits_of(v[i + 1]), kLow);
+        for (int i = 0; i < kStep; i += 2) {
+          mass.two(v[i], v[i + 1], tab, t + i, mant + i);
+          least = min(least, min(t[i] - kNone, t[i + 1] - kNone));
         }
-        bool on[2];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          on[k] = kept(v[i + k], at(ch, h, i + k));
-          if (MASS && on[k] && (int)t[k] <= kLow) light += weigh(mant[k], (int)t[k]);
-          add<MASS>((int)(kSpMagicBits - t[k]), mant[k], on[k] && (!MASS || (int)t[k] > kLow));
+        for (int i = 0; i < kStep; ++i) {
+          const uint32_t p = hist + 4u * kSpMagicBits - 4u * t[i];
+          if (RES) add_if(p, mant[i], v[i], cut.z, (int)t[i], kLow);
+          else if ((int)t[i] > kLow && kept(v[i], at(ch, h, i))) add_carry(p, mant[i]);
         }
+        if (least <= (uint32_t)kLow - kNone) {
+#pragma unroll
+          for (int i = 0; i < kStep; ++i)
+            if ((int)t[i] <= kLow && kept(v[i], at(ch, h, i))) light += weigh(mant[i], (int)t[i]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kStep; ++i)
+          count_if(hist + 4u * kSpMagicBits - 4u * (uint32_t)max(bits_of(v[i]), kLow), kept(v[i], at(ch, h, i)));
       }
     });
     if (MASS) {
       light = warp_sum64(light);
-      if (lane == 0 && light) {  // at most 2^17 tokens of 2^-36
-        add_if(hist + 4 * (kSpBins - 1), (uint32_t)light, true);
-        if (light >> 32) atomicAdd(hi() + kSpBins - 1, (uint32_t)(light >> 32));
+      if (lane == 0 && light) {
+        constexpr u64 kMask = (1ull << kUp) - 1;
+        const uint32_t l = (uint32_t)(light & kMask), old = atomicAdd(lo() + kSpBins - 1, l);
+        atomicAdd(hi() + kSpBins - 1, (uint32_t)(light >> kUp) + (old + l < old ? 1u : 0u));
       }
     }
     u64 before = 0;
@@ -466,11 +485,7 @@ struct Row {
     auto inside = [&](float z) { return low ? bits_of(z) <= bits : bits_of(z) == bits; };
     // the bin's tokens to CTA 0
     u64* list = reinterpret_cast<u64*>(buf);
-    each([&](const float* v, int ch, int h) {
-      bool some = false;
-#pragma unroll
-      for (int i = 0; i < kStep; ++i) some |= inside(v[i]);
-      if (!some) return;
+    auto gather = [&](const float* v, int ch, int h) {
 #pragma unroll
       for (int i = 0; i < kStep; ++i) {
         if (inside(v[i]) && kept(v[i], at(ch, h, i))) {
@@ -478,7 +493,22 @@ struct Row {
           if (n < kSpList) st_rank(list + n, 0, (u64)~ordered(v[i]) << 32 | (uint32_t)(start + at(ch, h, i)));
         }
       }
-    });
+    };
+    if (low) {
+      each(gather);
+    } else {
+      const u64 sub = tc::f2pack(-b.sub, -b.sub), up = tc::f2pack(b.hi, b.hi), mb = tc::f2pack(b.mb, b.mb);
+      each([&](const float* v, int ch, int h) {
+        bool some = false;
+#pragma unroll
+        for (int i = 0; i < kStep; i += 2) {
+          float x, y;
+          tc::f2unpack(tc::fma2(tc::add2(tc::f2pack(v[i], v[i + 1]), sub), up, mb), x, y);
+          some |= __float_as_int(x) == bits || __float_as_int(y) == bits;
+        }
+        if (some) gather(v, ch, h);
+      });
+    }
     tc::cluster_sync();
     const int n = tc::ld_rank(tc::smem_u32(&sh.n), 0);
     if (n <= kSpList) {
@@ -558,9 +588,9 @@ struct Row {
       const int shift = max(0, 64 - __clzll(most - least) - 8);  // 256 bins
 #pragma unroll
       for (int i = 0; i < kOf; ++i)
-        if (live >> i & 1) add<MASS>((int)((key[i] - least) >> shift), raw<MASS>(key[i]), true);
+        if (live >> i & 1) add<MASS>((int)((key[i] - least) >> shift), raw<MASS>(key[i]));
       __syncthreads();
-      const u64 here = (u64)lo()[tid] | (u64)hi()[tid] << 32;
+      const u64 here = (u64)lo()[tid] + ((u64)hi()[tid] << kUp);
       u64 before;
       block_scan(here, before);
       before += base;
@@ -628,7 +658,7 @@ struct Row {
           if (!inside(v[i]) || !kept(v[i], at(ch, h, i))) continue;
           const uint32_t key = ~ordered(v[i]);
           if (level > 0 && key >> (shift + 8) != prefix) continue;
-          add<MASS>((int)(key >> shift & 255u), MASS ? raw_of(v[i]) : 1, true);
+          add<MASS>((int)(key >> shift & 255u), MASS ? raw_of(v[i]) : 1);
         }
       });
       int digit;
@@ -704,12 +734,13 @@ struct Row {
     }
     return sum;
   }
-  // t: the bits of kSpMagic + J
+  // The same of one token: mant 2^(q-30-e), rounded. t: the bits of kSpMagic + J. One product serves both
+  // ways: by 2^(q-30-e) where that is whole, else by 2^32 times it, whose upper word is the result.
   __device__ __forceinline__ u64 weigh(uint32_t mant, int t) const {
-    const int e = (int)((kSpMagicBits >> 5) - ((uint32_t)(t & ~1) >> 5));
-    const int s = e + 62 - a.q;
-    const u64 w = (((u64)mant << 32) + (1ull << (s - 1 & 63))) >> (s & 63);
-    return t > (int)(kSpMagicBits - kSpNone) && s < 64 ? w : 0;
+    const int n = (t >> 5) - (int)(kSpMagicBits >> 5) + a.q - 30;  // q - 30 - e
+    const u64 p = (u64)mant * (1u << (n & 31));
+    const u64 w = n >= 0 ? p : (p + 0x80000000ull) >> 32;
+    return n >= -32 && t > (int)(kSpMagicBits - kSpNone) ? w : 0;
   }
 };
 
@@ -1029,7 +1060,7 @@ dspark_status sample(const dspark_sample_args* s, const void* Z, SpArgs a, int32
   while (C < kSpMaxC && (size_t)part(C) * size > 64 * 1024) C *= 2;
   while (C < kSpMaxC && (int64_t)a.N * C < 152 && part(C) > 2048) C *= 2;
   a.part = part(C);
-  const bool res = (size_t)a.part * size <= 180 * 1024;
+  const bool res = (size_t)a.part * size <= 180 * 1024 && a.part <= 65536;  // see add_if
   const size_t sums = (size_t)a.part / kSpChunk * 8;
   const size_t smem = res ? kSpHist + (size_t)a.part * size : sums > kSpHist ? sums : kSpHist;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
