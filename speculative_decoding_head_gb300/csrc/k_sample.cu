@@ -13,10 +13,10 @@
 //
 // top-k and top-p are one search, for the first token of the row sorted by
 // falling z (then by index) at which the running sum, of ones or of masses,
-// reaches a target. A histogram of 1216 bins of z (for masses 1/32 of an octave each, so that
+// reaches a target. A histogram of 1088 bins of z (for masses 1/32 of an octave each, so that
 // a bin's tokens share e and their mants are added as they are) gives the bin; its tokens
 // (some hundreds of a flat row of 129280) are brought to one CTA, which splits them
-// into 256 narrower bins, again and again until few are left. A bin of more than 1216 tokens (many
+// into 256 narrower bins, again and again until few are left. A bin of more than 1088 tokens (many
 // equal logits) is instead narrowed by four histograms of the bits of z, down to one value,
 // whose tokens are counted by index. What is kept is z >= cut; tokens that equal the cut
 // but come after its last index are masked in shared memory.
@@ -38,7 +38,7 @@ typedef unsigned long long u64;
 
 constexpr int kSpThreads = 256, kSpWarps = kSpThreads / 32;
 constexpr int kSpMaxC = 16;       // CTAs of a cluster
-constexpr int kSpBins = 1216;     // 38 octaves of 32 bins, the last one for what lies below
+constexpr int kSpBins = 1088;     // 34 octaves of 32 bins, the last one for what lies below
 constexpr int kSpNone = 1504;     // from here on (2^-47) a mass is nothing
 constexpr int kSpList = kSpBins;  // tokens of a bin that are brought together
 constexpr int kSpChunk = 512;     // tokens that a warp takes at a time
@@ -82,7 +82,8 @@ struct SpCut {
 struct SpShared {
   uint2 exp2[16];              // kSpExp2 as a whole number and as fp32
   u64 slot[2][kSpMaxC][2];     // what each CTA tells the others
-  u64 res[2];                  // a search's answer: bin and sum before it, or a cut
+  u64 res[3];                  // a search's answer: bin, sum before it and what is missing in it; or a cut and its sum
+  u64 segs[kSpMaxC][8];        // each CTA's sums of its histogram's eighths
   u64 warp[kSpWarps], warp2[kSpWarps];
   u64 bcast[2];
   u64 few[32];
@@ -201,6 +202,12 @@ __device__ __forceinline__ u64 unscaled(u64 need, int e, int q) {
 __device__ __forceinline__ void st_rank(void* p, uint32_t rank, u64 x) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(tc::map_rank(tc::smem_u32(p), rank)), "l"(x) : "memory");
 }
+// not ordered with anything but barriers, so that several are in flight
+__device__ __forceinline__ uint32_t ld_rank(uint32_t addr, uint32_t rank) {
+  uint32_t x;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(tc::map_rank(addr, rank)));
+  return x;
+}
 __device__ __forceinline__ int add_rank(int* p, uint32_t rank, int x) {
   int old;
   asm volatile("atom.shared::cluster.add.s32 %0, [%1], %2;"
@@ -286,6 +293,11 @@ struct Row {
     for (int i = 0; i < kPer; ++i) v[i] = up<T>(t[i]);
   }
   // 8 tokens of a lane, from global memory; past the end -inf
+  __device__ __forceinline__ void fetch_full(int ch, int h, float* v) const {
+#pragma unroll
+    for (int g = 0; g < kStep / kPer; ++g)
+      unpack(__ldg(reinterpret_cast<const uint4*>(row + start + at(ch, h, g * kPer))), v + g * kPer);
+  }
   __device__ __forceinline__ void fetch(int ch, int h, float* v) const {
 #pragma unroll
     for (int g = 0; g < kStep / kPer; ++g) {
@@ -377,54 +389,84 @@ struct Row {
     else if (RES) add_if(p, x, 0.f, 0.f, 1, 0);
     else add_carry(p, x);
   }
-  // Bin g of all CTAs' histograms. OCT: raw mants of its octave, brought to multiples of 2^-q.
+  // With every CTA's histogram filled: the first bin at which the sum up to it reaches the target, the sum before
+  // it, and how much of the bin's raw sum is missing there. OCT: the bins, but for the last, hold raw mants of their octaves, and
+  // count as multiples of 2^-q, each CTA's rounded. target 0: ceil(p of all of it), at least 1. Returns whether the
+  // sum reaches the target at all.
+  // Every CTA tells the others its sums of eight segments, so that all know the segment; one CTA looks at its bins.
   template <bool OCT>
-  __device__ __forceinline__ u64 bin_sum(int g) const {
-    u64 v = 0;
-    for (uint32_t c = 0; c < C; ++c)
-      v += (u64)(uint32_t)tc::ld_rank(hist + 4 * g, c) + ((u64)(uint32_t)tc::ld_rank(hist + 4 * (g + kSpBins), c) << kUp);
-    return OCT && g < kSpBins - 1 ? scaled(v, octave(g), a.q) : v;
-  }
-  // With every CTA's histogram filled: the first bin at which the sum up to it reaches the target, and
-  // the sum before it. target 0: ceil(p of all of it), at least 1. Returns whether the sum reaches the target at all.
-  template <bool OCT>
-  __device__ __forceinline__ bool find(u64& target, u64& before, int& bin) {
-    tc::cluster_sync();
-    const int seg = kSpBins / (int)C, per = (seg + kSpThreads - 1) / kSpThreads;
-    const int b0 = min(tid * per, seg), b1 = min(b0 + per, seg);
-    u64 sum = 0;
-    for (int b = b0; b < b1; ++b) sum += bin_sum<OCT>((int)rank * seg + b);
-    u64 mine;
-    const u64 all = block_scan(sum, mine);
-    const u64(*s)[2] = tell(all, 0);
-    u64 total = 0, pre = 0;
-    for (uint32_t c = 0; c < C; ++c) {
-      if (c == rank) pre = total;
-      total += s[c][0];
+  __device__ __forceinline__ bool find(u64& target, u64& goal, u64& before, int& bin) {
+    constexpr int kSeg = kSpBins / 8, kEach = (kSeg + 31) / 32;
+    auto value = [&](uint32_t l, uint32_t h, int g) {
+      const u64 v = (u64)l + ((u64)h << kUp);
+      return OCT && g < kSpBins - 1 ? scaled(v, octave(g), a.q) : v;
+    };
+    __syncthreads();
+    {
+      u64 sum = 0;
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        const int b = lane * kEach + i, g = warp * kSeg + b;
+        if (b < kSeg) sum += value(lo()[g], hi()[g], g);
+      }
+      sum = warp_sum64(sum);
+      if (lane < (int)C) st_rank(&sh.segs[rank][warp], lane, sum);
     }
+    tc::cluster_sync();
+    u64 v = 0;
+    for (uint32_t c = lane >> 3; c < C; c += 4) v += sh.segs[c][lane & 7];
+    v += __shfl_xor_sync(0xFFFFFFFFu, v, 8);
+    v += __shfl_xor_sync(0xFFFFFFFFu, v, 16);
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) {
+      const u64 y = __shfl_up_sync(0xFFFFFFFFu, v, o);
+      if ((lane & 7) >= o) v += y;
+    }
+    const u64 total = __shfl_sync(0xFFFFFFFFu, v, 7);
     if (target == 0) {
       target = mul_floor(total, sh.p, true);
       if (target == 0) target = 1;
     }
     if (target > total) return false;
-    u64 t = pre + mine;
-    if (t < target && t + sum >= target) {
-      int b = b0;
-      if (per > 1) {
-        for (;; ++b) {
-          const u64 v = bin_sum<OCT>((int)rank * seg + b);
-          if (t + v >= target) break;
-          t += v;
+    const int seg = __ffs((int)__ballot_sync(0xFFFFFFFFu, v >= target)) - 1;
+    u64 t = __shfl_sync(0xFFFFFFFFu, v, max(seg, 1) - 1);
+    if (seg == 0) t = 0;
+    if (rank == (uint32_t)seg % C) {
+      const int g = seg * kSeg + tid;
+      u64 x = 0, raw = 0, mine;
+      if (tid < kSeg) {
+#pragma unroll
+        for (uint32_t c0 = 0; c0 < kSpMaxC; c0 += 4) {
+          uint32_t l[4] = {}, h[4] = {};
+#pragma unroll
+          for (uint32_t c = 0; c < 4; ++c)
+            if (c0 + c < C) {
+              l[c] = ld_rank(hist + 4 * g, c0 + c);
+              h[c] = ld_rank(hist + 4 * (g + kSpBins), c0 + c);
+            }
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            raw += (u64)l[c] + ((u64)h[c] << kUp);
+            x += value(l[c], h[c], g);
+          }
         }
       }
-      for (uint32_t c = 0; c < C; ++c) {
-        st_rank(&sh.res[0], c, (u64)((int)rank * seg + b));
-        st_rank(&sh.res[1], c, t);
+      block_scan(x, mine);
+      t += mine;
+      if (t < target && t + x >= target) {
+        const u64 need = target - t;
+        const u64 miss = OCT && g < kSpBins - 1 ? min(unscaled(need, octave(g), a.q), raw) : need;
+        for (uint32_t c = 0; c < C; ++c) {
+          st_rank(&sh.res[0], c, (u64)g);
+          st_rank(&sh.res[1], c, t);
+          st_rank(&sh.res[2], c, miss);
+        }
       }
     }
     tc::cluster_sync();
     bin = (int)sh.res[0];
     before = sh.res[1];
+    goal = sh.res[2];
     return true;
   }
 
@@ -474,13 +516,12 @@ struct Row {
         atomicAdd(hi() + kSpBins - 1, (uint32_t)(light >> kUp) + (old + l < old ? 1u : 0u));
       }
     }
-    u64 before = 0;
+    u64 before, goal;
     int bin;
-    if (!find<MASS>(target, before, bin)) return;
+    if (!find<MASS>(target, goal, before, bin)) return;
     const bool low = bin == kSpBins - 1;
     low_mass = MASS && low;
     const int e = octave(bin);
-    const u64 goal = MASS && !low ? unscaled(target - before, e, a.q) : target - before;  // of the bin's raw sum
     const int bits = (int)kSpMagicBits - bin;
     auto inside = [&](float z) { return low ? bits_of(z) <= bits : bits_of(z) == bits; };
     // the bin's tokens to CTA 0
@@ -662,9 +703,9 @@ struct Row {
         }
       });
       int digit;
-      u64 here;
-      find<false>(goal, here, digit);
-      goal -= here;
+      u64 here, rest;
+      find<false>(goal, rest, here, digit);
+      goal = rest;
       before += here;
       prefix = prefix << 8 | (uint32_t)digit;
     }
@@ -808,8 +849,13 @@ __global__ void __launch_bounds__(kSpThreads, 3) k_sample(SpArgs a) {
   float top = -INFINITY, sum = 0.f, seen = 0.f;
   for (int ch = w.warp; ch < w.chunks; ch += kSpWarps) {
     float v[2][R::kStep];
-    w.fetch(ch, 0, v[0]);
-    w.fetch(ch, 1, v[1]);
+    if (a.vec && (ch + 1) * kSpChunk <= w.count) {
+      w.fetch_full(ch, 0, v[0]);
+      w.fetch_full(ch, 1, v[1]);
+    } else {
+      w.fetch(ch, 0, v[0]);
+      w.fetch(ch, 1, v[1]);
+    }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
 #pragma unroll
