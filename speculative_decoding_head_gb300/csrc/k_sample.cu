@@ -40,7 +40,9 @@ constexpr int kSpThreads = 256, kSpWarps = kSpThreads / 32;
 constexpr int kSpMaxC = 16;       // CTAs of a cluster
 constexpr int kSpBins = 1088;     // 34 octaves of 32 bins, the last one for what lies below
 constexpr int kSpNone = 1504;     // from here on (2^-47) a mass is nothing
-constexpr int kSpList = kSpBins;  // tokens of a bin that are brought together
+constexpr int kSpSeg = kSpBins / 8;
+constexpr int kSpList = kSpBins;      // tokens of a bin that are brought together,
+constexpr int kSpOwn = kSpSeg * 4 / 2; // and of one CTA: half of the histogram's lower words
 constexpr int kSpChunk = 512;     // tokens that a warp takes at a time
 constexpr float kSpMasked = -1e29f;
 constexpr float kSpLowest = -3.402823466e38f;
@@ -82,13 +84,15 @@ struct SpCut {
 struct SpShared {
   uint2 exp2[16];              // kSpExp2 as a whole number and as fp32
   u64 slot[2][kSpMaxC][2];     // what each CTA tells the others
-  u64 res[3];                  // a search's answer: bin, sum before it and what is missing in it; or a cut and its sum
+  u64 res[2];                  // a cut and the raw sum of its bin up to it
+  u64 found[3];                // a search's bin, the sum before it and what is missing in it
   u64 segs[kSpMaxC][8];        // each CTA's sums of its histogram's eighths
   u64 warp[kSpWarps], warp2[kSpWarps];
   u64 bcast[2];
   u64 few[32];
   float c_hi, c_lo, inv_t, p, u;
   int k, n, m, bad;
+  int counts[kSpMaxC];         // tokens of the bin in each CTA
 };
 
 // round(2^30 2^(i / 16))
@@ -189,17 +193,21 @@ struct Mass {
 };
 // bin -J: the octave of its masses
 __device__ __forceinline__ int octave(int bin) { return (((bin + 1) & ~1) + 31) >> 5; }
-// raw mants of octave e as a multiple of 2^-q, rounded; and the least raw sum that reaches `need`
+// Raw mants of octave e as a multiple of 2^-q, cut off, so that a sum's is at least its parts' together (and with
+// some hundred bins and CTAs 2^-34 less at the most); and the least raw sum that reaches `need`.
 __device__ __forceinline__ u64 scaled(u64 raw, int e, int q) {
   const int sh = e - (q - 30);
-  return sh <= 0 ? raw << -sh : (raw + (1ull << (sh - 1))) >> sh;
+  return sh <= 0 ? raw << -sh : raw >> sh;
 }
 __device__ __forceinline__ u64 unscaled(u64 need, int e, int q) {
   const int sh = e - (q - 30);
-  return sh <= 0 ? (need + (1ull << -sh) - 1) >> -sh : (need << sh) - (1ull << (sh - 1));
+  return sh <= 0 ? (need + (1ull << -sh) - 1) >> -sh : need << sh;
 }
 
-__device__ __forceinline__ void st_rank(void* p, uint32_t rank, u64 x) {
+__device__ __forceinline__ void st_rank(int* p, uint32_t rank, int x) {
+  asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(tc::map_rank(tc::smem_u32(p), rank)), "r"(x) : "memory");
+}
+__device__ __forceinline__ void st_rank(u64* p, uint32_t rank, u64 x) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(tc::map_rank(tc::smem_u32(p), rank)), "l"(x) : "memory");
 }
 // not ordered with anything but barriers, so that several are in flight
@@ -208,13 +216,10 @@ __device__ __forceinline__ uint32_t ld_rank(uint32_t addr, uint32_t rank) {
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(tc::map_rank(addr, rank)));
   return x;
 }
-__device__ __forceinline__ int add_rank(int* p, uint32_t rank, int x) {
-  int old;
-  asm volatile("atom.shared::cluster.add.s32 %0, [%1], %2;"
-               : "=r"(old)
-               : "r"(tc::map_rank(tc::smem_u32(p), rank)), "r"(x)
-               : "memory");
-  return old;
+__device__ __forceinline__ u64 ld_rank64(uint32_t addr, uint32_t rank) {
+  u64 x;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(x) : "r"(tc::map_rank(addr, rank)));
+  return x;
 }
 
 __device__ __forceinline__ u64 warp_sum64(u64 x) {
@@ -391,23 +396,20 @@ struct Row {
   }
   // With every CTA's histogram filled: the first bin at which the sum up to it reaches the target, the sum before
   // it, and how much of the bin's raw sum is missing there. OCT: the bins, but for the last, hold raw mants of their octaves, and
-  // count as multiples of 2^-q, each CTA's rounded. target 0: ceil(p of all of it), at least 1. Returns whether the
-  // sum reaches the target at all.
-  // Every CTA tells the others its sums of eight segments, so that all know the segment; one CTA looks at its bins.
+  // count as multiples of 2^-q. target 0: ceil(p of all of it), at least 1. Returns whether the sum reaches the target at all.
+  // Every CTA tells the others its sums of eight segments, so that all know the segment, and all look at its bins:
+  // they are not to change before the cluster's next barrier.
   template <bool OCT>
   __device__ __forceinline__ bool find(u64& target, u64& goal, u64& before, int& bin) {
-    constexpr int kSeg = kSpBins / 8, kEach = (kSeg + 31) / 32;
-    auto value = [&](uint32_t l, uint32_t h, int g) {
-      const u64 v = (u64)l + ((u64)h << kUp);
-      return OCT && g < kSpBins - 1 ? scaled(v, octave(g), a.q) : v;
-    };
+    constexpr int kEach = (kSpSeg + 31) / 32;
+    auto value = [&](u64 v, int g) { return OCT && g < kSpBins - 1 ? scaled(v, octave(g), a.q) : v; };
     __syncthreads();
     {
       u64 sum = 0;
 #pragma unroll
       for (int i = 0; i < kEach; ++i) {
-        const int b = lane * kEach + i, g = warp * kSeg + b;
-        if (b < kSeg) sum += value(lo()[g], hi()[g], g);
+        const int b = lane * kEach + i, g = warp * kSpSeg + b;
+        if (b < kSpSeg) sum += value((u64)lo()[g] + ((u64)hi()[g] << kUp), g);
       }
       sum = warp_sum64(sum);
       if (lane < (int)C) st_rank(&sh.segs[rank][warp], lane, sum);
@@ -427,46 +429,42 @@ struct Row {
       target = mul_floor(total, sh.p, true);
       if (target == 0) target = 1;
     }
-    if (target > total) return false;
+    if (target > total) {
+      tc::cluster_sync();  // the sums have been read
+      return false;
+    }
     const int seg = __ffs((int)__ballot_sync(0xFFFFFFFFu, v >= target)) - 1;
     u64 t = __shfl_sync(0xFFFFFFFFu, v, max(seg, 1) - 1);
     if (seg == 0) t = 0;
-    if (rank == (uint32_t)seg % C) {
-      const int g = seg * kSeg + tid;
-      u64 x = 0, raw = 0, mine;
-      if (tid < kSeg) {
+    const int g = seg * kSpSeg + tid;
+    u64 raw = 0, mine;
+    if (tid < kSpSeg) {
 #pragma unroll
-        for (uint32_t c0 = 0; c0 < kSpMaxC; c0 += 4) {
-          uint32_t l[4] = {}, h[4] = {};
+      for (uint32_t c0 = 0; c0 < kSpMaxC; c0 += 4) {
+        uint32_t l[4] = {}, h[4] = {};
 #pragma unroll
-          for (uint32_t c = 0; c < 4; ++c)
-            if (c0 + c < C) {
-              l[c] = ld_rank(hist + 4 * g, c0 + c);
-              h[c] = ld_rank(hist + 4 * (g + kSpBins), c0 + c);
-            }
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            raw += (u64)l[c] + ((u64)h[c] << kUp);
-            x += value(l[c], h[c], g);
+        for (uint32_t c = 0; c < 4; ++c)
+          if (c0 + c < C) {
+            l[c] = ld_rank(hist + 4 * g, c0 + c);
+            h[c] = ld_rank(hist + 4 * (g + kSpBins), c0 + c);
           }
-        }
-      }
-      block_scan(x, mine);
-      t += mine;
-      if (t < target && t + x >= target) {
-        const u64 need = target - t;
-        const u64 miss = OCT && g < kSpBins - 1 ? min(unscaled(need, octave(g), a.q), raw) : need;
-        for (uint32_t c = 0; c < C; ++c) {
-          st_rank(&sh.res[0], c, (u64)g);
-          st_rank(&sh.res[1], c, t);
-          st_rank(&sh.res[2], c, miss);
-        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) raw += (u64)l[c] + ((u64)h[c] << kUp);
       }
     }
-    tc::cluster_sync();
-    bin = (int)sh.res[0];
-    before = sh.res[1];
-    goal = sh.res[2];
+    const u64 x = value(raw, g);
+    block_scan(x, mine);
+    t += mine;
+    if (t < target && t + x >= target) {
+      const u64 need = target - t;
+      sh.found[0] = (u64)g;
+      sh.found[1] = t;
+      sh.found[2] = OCT && g < kSpBins - 1 ? min(unscaled(need, octave(g), a.q), raw) : need;
+    }
+    __syncthreads();
+    bin = (int)sh.found[0];
+    before = sh.found[1];
+    goal = sh.found[2];
     return true;
   }
 
@@ -524,14 +522,15 @@ struct Row {
     const int e = octave(bin);
     const int bits = (int)kSpMagicBits - bin;
     auto inside = [&](float z) { return low ? bits_of(z) <= bits : bits_of(z) == bits; };
-    // the bin's tokens to CTA 0
-    u64* list = reinterpret_cast<u64*>(buf);
+    // the CTA's tokens of the bin, into the half of the histogram's lower words that find() leaves alone
+    const int at0 = bin < kSpBins / 2 ? kSpBins / 2 * 4 : 0;
+    u64* list = reinterpret_cast<u64*>(buf + at0);
     auto gather = [&](const float* v, int ch, int h) {
 #pragma unroll
       for (int i = 0; i < kStep; ++i) {
         if (inside(v[i]) && kept(v[i], at(ch, h, i))) {
-          const int n = add_rank(&sh.n, 0, 1);
-          if (n < kSpList) st_rank(list + n, 0, (u64)~ordered(v[i]) << 32 | (uint32_t)(start + at(ch, h, i)));
+          const int n = atomicAdd(&sh.n, 1);
+          if (n < kSpOwn) list[n] = (u64)~ordered(v[i]) << 32 | (uint32_t)(start + at(ch, h, i));
         }
       }
     };
@@ -550,10 +549,18 @@ struct Row {
         if (some) gather(v, ch, h);
       });
     }
+    __syncthreads();
+    if (tid < (int)C) st_rank(&sh.counts[rank], tid, sh.n);
     tc::cluster_sync();
-    const int n = tc::ld_rank(tc::smem_u32(&sh.n), 0);
-    if (n <= kSpList) {
-      if (rank == 0) cut_of_list<MASS>(n, goal);
+    int n = 0;
+    bool few = true;
+    for (uint32_t c = 0; c < C; ++c) {
+      n += sh.counts[c];
+      few &= sh.counts[c] <= kSpOwn;
+    }
+    few &= n <= kSpList;
+    if (few) {
+      if (rank == 0) cut_of_list<MASS>(n, goal, hist + at0);
     } else {
       narrow<MASS>(inside, goal);
     }
@@ -561,7 +568,7 @@ struct Row {
     cut.z = unordered((uint32_t)(sh.res[0] >> 32));
     cut.last = (int)(uint32_t)sh.res[0];
     if (MASS) held = before + (low ? sh.res[1] : scaled(sh.res[1], e, a.q));
-    if (RES && n > kSpList) {  // cut_of_list has masked the others
+    if (RES && !few) {  // cut_of_list has masked the others
       each([&](const float* v, int ch, int h) {
 #pragma unroll
         for (int i = 0; i < kStep; ++i)
@@ -588,17 +595,22 @@ struct Row {
     }
   }
 
-  // In CTA 0: keys (falling z, index) in any order.
+  // In CTA 0: keys (falling z, index) in any order, each CTA's at its shared address `at`.
   template <bool MASS>
-  __device__ void cut_of_list(int n, u64 goal) {
+  __device__ void cut_of_list(int n, u64 goal, uint32_t at) {
     constexpr int kOf = (kSpList + kSpThreads - 1) / kSpThreads;
     u64 key[kOf];
     uint32_t live = 0;
 #pragma unroll
     for (int i = 0; i < kOf; ++i) {
-      const int e = tid + i * kSpThreads;
-      key[i] = e < n ? reinterpret_cast<const u64*>(buf)[e] : ~0ull;
-      if (e < n) live |= 1u << i;
+      int e = tid + i * kSpThreads;
+      key[i] = ~0ull;
+      if (e < n) {
+        uint32_t c = 0;
+        while (e >= sh.counts[c]) e -= sh.counts[c++];
+        key[i] = ld_rank64(at + 8u * (uint32_t)e, c);
+        live |= 1u << i;
+      }
     }
     u64 base = 0;
     for (;;) {
@@ -709,6 +721,7 @@ struct Row {
       before += here;
       prefix = prefix << 8 | (uint32_t)digit;
     }
+    tc::cluster_sync();
     const u64 end = (u64)prefix << 32;
     const float zc = unordered(~prefix);
     const u64 w = raw<MASS>(end);
@@ -774,6 +787,13 @@ struct Row {
       }
     }
     return sum;
+  }
+  // Of most rows few tokens are kept: steps without any are passed over.
+  __device__ __forceinline__ u64 sum_kept(const float* v, int ch, int h) const {
+    float top = v[0];
+#pragma unroll
+    for (int i = 1; i < kStep; ++i) top = fmaxf(top, v[i]);
+    return __any_sync(0xFFFFFFFFu, top >= cut.z) ? sum_of(v, ch, h) : 0;
   }
   // The same of one token: mant 2^(q-30-e), rounded. t: the bits of kSpMagic + J. One product serves both
   // ways: by 2^(q-30-e) where that is whole, else by 2^32 times it, whose upper word is the result.
@@ -950,7 +970,7 @@ __global__ void __launch_bounds__(kSpThreads, 3) k_sample(SpArgs a) {
     u64 S = w.held;
     if (!exact) {
       u64 t = 0, ignored;
-      w.each([&](const float* v, int ch, int h) { t += w.sum_of(v, ch, h); });
+      w.each([&](const float* v, int ch, int h) { t += w.sum_kept(v, ch, h); });
       const u64 mine = w.block_scan(t, ignored);
       const u64(*s)[2] = w.tell(mine, 0);
       S = 0;
@@ -983,10 +1003,7 @@ __global__ void __launch_bounds__(kSpThreads, 3) k_sample(SpArgs a) {
       for (int h = 0; h < 2; ++h) {
         float v[R::kStep];
         w.values(ch, h, v);
-        bool some = false;  // of most rows few tokens are kept
-#pragma unroll
-        for (int i = 0; i < R::kStep; ++i) some |= v[i] >= w.cut.z;
-        if (__any_sync(0xFFFFFFFFu, some)) t += w.sum_of(v, ch, h);
+        t += w.sum_kept(v, ch, h);
       }
       t = warp_sum64(t);
       if (w.lane == 0) chunk[ch] = t;
