@@ -153,81 +153,107 @@ __global__ void __launch_bounds__(kFlThreads, 1)
 
   const int b_off = kFlABytes, sa_off = b_off + a.tn * kFlBoxBytes, sb_off = sa_off + kSf;
   bool ok = true;
+  // The producer and the MMA warp run their loops whole; one lane issues (see elect_one).
   if (warp == 0) {
-    if (lane == 0) {
-      const uint64_t keep = tc::policy_evict_last();   // x is read for every tile of w
-      const uint64_t first = tc::policy_evict_first(); // w once by neighbouring tiles
-      int k = 0;
-      for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-        const int v0 = t / a.nt * kFlTileV, n0 = t % a.nt * a.tn;
-        const int nsb = (min(a.tn, a.N - n0) + kRows - 1) / kRows;
-        for (int c = 0; c < chunks && ok; ++c, ++k) {
-          const int s = k % a.stages;
-          ok = tc::mbar_wait(bar(&bars.empty[s]), (k / a.stages & 1) ^ 1, abort);
-          if (!ok) break;
+    const uint64_t keep = tc::policy_evict_last();   // x is read for every tile of w
+    const uint64_t first = tc::policy_evict_first(); // w once by neighbouring tiles
+    int k = 0, s = 0, ph = 1;
+    for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+      const int v0 = t / a.nt * kFlTileV, n0 = t % a.nt * a.tn;
+      const int nsb = (min(a.tn, a.N - n0) + kRows - 1) / kRows;
+      const uint32_t bytes = kFlABytes + a.tn * kFlBoxBytes + (1 + nsb) * kSf;
+      const uint8_t* wsc = a.wsc + (int64_t)(v0 / kRows) * chunks * kSf;
+      const uint8_t* xsc = a.xsc + (int64_t)(n0 / kRows) * chunks * kSf;
+      for (int c = 0; c < chunks; ++c, ++k) {
+        ok = tc::mbar_wait(bar(&bars.empty[s]), ph, abort);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
+        if (tc::elect_one()) {
           const uint32_t st = sbase + s * a.stage_bytes, f = bar(&bars.full[s]);
-          tc::mbar_arrive_expect_tx(f, kFlABytes + a.tn * kFlBoxBytes + (1 + nsb) * kSf);
+          tc::mbar_arrive_expect_tx(f, bytes);
           tc::tma_load_2d(st, &tw, c * kFlBoxBytes, v0, f, a.nt > 1 ? keep : first);
           tc::tma_load_2d(st + b_off, &tx, c * kFlBoxBytes, n0, f, keep);
-          tc::bulk_load(st + sa_off, a.wsc + ((int64_t)(v0 / kRows) * chunks + c) * kSf, kSf, f);
-          for (int i = 0; i < nsb; ++i)
-            tc::bulk_load(st + sb_off + i * kSf, a.xsc + ((int64_t)(n0 / kRows + i) * chunks + c) * kSf, kSf, f);
+          tc::bulk_load(st + sa_off, wsc + (int64_t)c * kSf, kSf, f);
+          tc::bulk_load(st + sb_off, xsc + (int64_t)c * kSf, kSf, f);
+          if (nsb > 1) tc::bulk_load(st + sb_off + kSf, xsc + (int64_t)(chunks + c) * kSf, kSf, f);
+        }
+        if (++s == a.stages) {
+          s = 0;
+          ph ^= 1;
         }
       }
-      if (!ok) {
-        *abort = 1;
-        raise_status(a.status, DSPARK_ETIMEOUT);
-        int never = 0;  // copies in flight land before the CTA ends
-        for (int j = max(0, k - a.stages); j < k; ++j)
-          tc::mbar_wait(bar(&bars.full[j % a.stages]), j / a.stages & 1, &never);
-      }
+    }
+    if (!ok && lane == 0) {
+      *abort = 1;
+      raise_status(a.status, DSPARK_ETIMEOUT);
+      int never = 0;  // copies in flight land before the CTA ends
+      for (int j = max(0, k - a.stages); j < k; ++j)
+        tc::mbar_wait(bar(&bars.full[j % a.stages]), j / a.stages & 1, &never);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      int k = 0, i = 0;
-      for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++i) {
-        const int n0 = t % a.nt * a.tn, nn = min(a.tn, a.N - n0), nm = (nn + 15) / 16 * 16;
-        const int nsb = (nn + kRows - 1) / kRows, buf = i & 1;
-        const uint32_t d = tmem + (buf ? a.acc1 : 0), sfa = tmem + kFlSfCol, sfb = sfa + 4 * kQ;
-        ok = tc::mbar_wait(bar(&bars.tempty[buf]), (i >> 1 & 1) ^ 1, abort);
-        if (ok && a.overlap && i > 0) ok = tc::mbar_wait(bar(&bars.over), (i - 1) & 1, abort);
+    const uint32_t sfa = tmem + kFlSfCol, sfb = sfa + 4 * kQ;
+    const uint64_t ad0 = tc::smem_desc(sbase, 16, 1024), sd0 = tc::scales_desc(sbase);
+    int i = 0, s = 0, ph = 0;
+    for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++i) {
+      const int n0 = t % a.nt * a.tn, nn = min(a.tn, a.N - n0), nm = (nn + 15) / 16 * 16;
+      const int nsb = (nn + kRows - 1) / kRows, buf = i & 1;
+      const uint32_t d = tmem + (buf ? a.acc1 : 0);
+      const uint32_t id = tc::idesc_fp4(kFlTileV, nm, FMT == DSPARK_MXFP4, 0);
+      ok = tc::mbar_wait(bar(&bars.tempty[buf]), (i >> 1 & 1) ^ 1, abort);
+      if (ok && a.overlap && i > 0) ok = tc::mbar_wait(bar(&bars.over), (i - 1) & 1, abort);
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      tc::tc_fence_after();
+      for (int c = 0; c < chunks && ok; ++c) {
+        ok = tc::mbar_wait(bar(&bars.full[s]), ph, abort);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
         tc::tc_fence_after();
-        for (int c = 0; c < chunks && ok; ++c, ++k) {
-          const int s = k % a.stages;
-          ok = tc::mbar_wait(bar(&bars.full[s]), k / a.stages & 1, abort);
-          if (!ok) break;
-          tc::tc_fence_after();
-          const uint32_t st = sbase + s * a.stage_bytes;
+        if (tc::elect_one()) {
+          const uint32_t off = (uint32_t)(s * a.stage_bytes) >> 4;
+          const uint64_t ad = ad0 + off, bd = ad + (b_off >> 4);
+          const uint64_t sa = sd0 + off + (sa_off >> 4), sb = sd0 + off + (sb_off >> 4);
+#pragma unroll
+          for (int q = 0; q < kQ; ++q) tc::cp_scales(sfa + 4 * q, sa + 32 * q);
+          if (nsb == 1) {
+#pragma unroll
+            for (int q = 0; q < kQ; ++q) tc::cp_scales(sfb + 4 * q, sb + 32 * q);
+          } else {
+#pragma unroll
+            for (int q = 0; q < kQ; ++q) {
+              tc::cp_scales(sfb + 8 * q, sb + 32 * q);
+              tc::cp_scales(sfb + 8 * q + 4, sb + (kSf >> 4) + 32 * q);
+            }
+          }
           const int steps = min(4, (a.K - c * kChunk + 63) / 64);
 #pragma unroll
-          for (int q = 0; q < kQ; ++q) {
-            tc::cp_scales(sfa + 4 * q, tc::scales_desc(st + sa_off + q * 512));
-            for (int j = 0; j < nsb; ++j)
-              tc::cp_scales(sfb + 4 * (nsb * q + j), tc::scales_desc(st + sb_off + j * kSf + q * 512));
-          }
-          const uint64_t ad = tc::smem_desc(st, 16, 1024), bd = tc::smem_desc(st + b_off, 16, 1024);
-          for (int kk = 0; kk < steps; ++kk) {
-            const uint32_t acc = (c | kk) != 0;
-            if (FMT == DSPARK_NVFP4) {
-              tc::mma_nvfp4(d, ad + 2 * kk, bd + 2 * kk, tc::idesc_fp4(kFlTileV, nm, false, 0), sfa + 4 * kk,
-                            sfb + 4 * nsb * kk, acc);
-            } else {
-              const int q = kk >> 1;
-              tc::mma_mxfp4(d, ad + 2 * kk, bd + 2 * kk, tc::idesc_fp4(kFlTileV, nm, true, (kk & 1) * 2), sfa + 4 * q,
-                            sfb + 4 * nsb * q, acc);
+          for (int kk = 0; kk < 4; ++kk) {
+            if (kk < steps) {
+              // an nvfp4 step has its own word of scales; two mxfp4 steps share one, by halves
+              const int q = FMT == DSPARK_NVFP4 ? kk : kk >> 1;
+              const uint32_t half = FMT == DSPARK_NVFP4 ? 0 : (kk & 1) * 2;
+              const uint32_t idk = id | half << 4 | half << 29;
+              if (FMT == DSPARK_NVFP4)
+                tc::mma_nvfp4(d, ad + 2 * kk, bd + 2 * kk, idk, sfa + 4 * q, sfb + 4 * nsb * q, (c | kk) != 0);
+              else
+                tc::mma_mxfp4(d, ad + 2 * kk, bd + 2 * kk, idk, sfa + 4 * q, sfb + 4 * nsb * q, (c | kk) != 0);
             }
           }
           tc::mma_commit(bar(&bars.empty[s]));
+          if (c == chunks - 1) tc::mma_commit(bar(&bars.tfull[buf]));
         }
-        if (ok) tc::mma_commit(bar(&bars.tfull[buf]));
+        __syncwarp();
+        if (++s == a.stages) {
+          s = 0;
+          ph ^= 1;
+        }
       }
-      if (!ok) {
-        *abort = 1;
-        raise_status(a.status, DSPARK_ETIMEOUT);
-        int never = 0;
-        tc::mma_commit(bar(&bars.drain));
-        tc::mbar_wait(bar(&bars.drain), 0, &never);
-      }
+    }
+    if (!ok && lane == 0) {
+      *abort = 1;
+      raise_status(a.status, DSPARK_ETIMEOUT);
+      int never = 0;
+      tc::mma_commit(bar(&bars.drain));
+      tc::mbar_wait(bar(&bars.drain), 0, &never);
     }
   } else if (warp >= 4) {
     const int q = warp & 3, h = (warp - 4) >> 2;

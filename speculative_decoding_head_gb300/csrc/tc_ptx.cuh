@@ -366,6 +366,14 @@ __device__ __forceinline__ void tmem_tie32(float* v) {
 }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
+// One lane of a converged warp. Instructions whose operands are in uniform registers (tcgen05, TMA) issue
+// several times as fast under it, in a loop that the whole warp runs, as in a branch of one lane's own.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
+}
+
 // ---------------------------------------------------------------- CTA pairs (cta_group::2)
 // A cluster of two CTAs computes one tile: each holds half of A's rows and
 // half of B's columns in its own shared memory, the even CTA issues the MMAs
