@@ -1,13 +1,13 @@
 // k_fp4_linear.cu -- the product of two matrices held in microscaled 4-bit
 // floating point, Y[n][v] = sum_k x[n][k] w[v][k] (+ U[n][v]).
 //
-// The vocabulary is the MMA's M: a tile is 128 rows of w by up to 256 rows of
+// The vocabulary is the MMA's M: a tile is 256 rows of w by up to 256 rows of
 // x, so that a few tokens make narrow tiles and w streams by once, and a warp
 // of the epilogue holds 32 neighbouring v of one token: its stores are whole
-// sectors of Y without a turn through shared memory. Persistent CTAs; a
-// producer thread loads 256 columns of both operands a stage (128-byte
+// sectors of Y without a turn through shared memory. Persistent CTA pairs: each CTA holds half of a
+// tile's w and half of its x. A producer warp loads 256 columns of both operands a stage (128-byte
 // swizzled boxes) with their scales (contiguous, as dspark_fp4_quant lays them
-// out); the MMA thread copies the scales to TMEM and issues four block-scaled
+// out); the MMA warp copies the scales to TMEM and issues four block-scaled
 // MMAs of 64 columns; eight warps store.
 //
 // TMEM: two accumulators, and 48 columns of scales. Accumulators of more than
@@ -28,28 +28,31 @@ namespace {
 
 using namespace fp4;
 
-constexpr int kFlTileV = 128;
+constexpr int kFlTileV = 256;         // of a pair
+constexpr int kFlHalfV = 128;
 constexpr int kFlMaxN = 256;          // tokens of a tile
 constexpr int kFlThreads = 384;       // producer, MMA, TMEM and a spare warp, eight epilogue warps
 constexpr int kFlSfCol = 464;         // TMEM columns of the scales, after the accumulators
 constexpr int kFlMaxStages = 12;
 constexpr int kFlBoxBytes = 128;      // kChunk values
-constexpr int kFlABytes = kFlTileV * kFlBoxBytes;
+constexpr int kFlABytes = kFlHalfV * kFlBoxBytes;
 
 struct FlArgs {
-  const uint8_t* wsc;
-  const uint8_t* xsc;
   const float* wf;
   const float* xf;
   const float* U;
   void* Y;
   int64_t ldu, ldy;
   int N, K, V;
-  int tn;        // tokens of a tile, a multiple of 16
+  int tn;        // tokens of a tile, a multiple of 32
   int vt, nt;    // tiles
   int stages, stage_bytes;
   int acc1, overlap;  // the second accumulator's first column; columns it shares with the first
   int* status;
+};
+
+struct FlMaps {
+  CUtensorMap w, x, ws, xs;  // codes and scales
 };
 
 struct FlBars {
@@ -114,8 +117,8 @@ __device__ __forceinline__ void fl_store16(const FlArgs& a, float* z, int n0, in
 }
 
 template <int FMT, typename T, bool HASU>
-__global__ void __launch_bounds__(kFlThreads, 1)
-    k_fp4_linear(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUtensorMap tx, FlArgs a) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFlThreads, 1)
+    k_fp4_linear(const __grid_constant__ FlMaps maps, FlArgs a) {
   constexpr int kSf = chunk_bytes(FMT);         // bytes of a 128-row group's scales of a stage
   constexpr int kQ = kSf / 512;                 // tiles of four blocks in them
   extern __shared__ uint8_t raw[];
@@ -124,6 +127,8 @@ __global__ void __launch_bounds__(kFlThreads, 1)
   const uint32_t sbase = tc::smem_u32(base);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int tiles = a.vt * a.nt, chunks = chunks_of(a.K);
+  const uint32_t rank = tc::cluster_ctarank();
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   volatile int* abort = &bars.abort;
   auto bar = [&](uint64_t* b) { return tc::smem_u32(b); };
 
@@ -134,112 +139,53 @@ __global__ void __launch_bounds__(kFlThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(bar(&bars.tfull[i]), 1);
-      tc::mbar_init(bar(&bars.tempty[i]), 8);
+      tc::mbar_init(bar(&bars.tempty[i]), 16);  // the even CTA's: both CTAs' epilogue warps
     }
-    tc::mbar_init(bar(&bars.over), 8);
+    tc::mbar_init(bar(&bars.over), 16);
     tc::mbar_init(bar(&bars.drain), 1);
     bars.abort = 0;
     tc::fence_barrier_init();
-    tc::prefetch_tmap(&tw);
-    tc::prefetch_tmap(&tx);
+    tc::prefetch_tmap(&maps.w);
+    tc::prefetch_tmap(&maps.x);
+    tc::prefetch_tmap(&maps.ws);
+    tc::prefetch_tmap(&maps.xs);
   }
-  if (warp == 2) tc::tmem_alloc(tc::smem_u32(&bars.tmem), 512);
+  if (warp == 2) {
+    tc::tmem_alloc_pair(tc::smem_u32(&bars.tmem), 512);
+    tc::tmem_relinquish_pair();
+  }
   tc::tc_fence_before();
   __syncthreads();
+  tc::cluster_meet();
   tc::tc_fence_after();
   const uint32_t tmem = bars.tmem;
   pdl_wait();
   pdl_trigger();
 
-  const int b_off = kFlABytes, sa_off = b_off + a.tn * kFlBoxBytes, sb_off = sa_off + kSf;
+  const int half = a.tn / 2;  // rows of x that a stage has room for in each CTA
+  const int b_off = kFlABytes, sa_off = b_off + half * kFlBoxBytes, sb_off = sa_off + kSf;
   bool ok = true;
   // The producer and the MMA warp run their loops whole; one lane issues (see elect_one).
   if (warp == 0) {
-    const uint64_t keep = tc::policy_evict_last();   // x is read for every tile of w
-    const uint64_t first = tc::policy_evict_first(); // w once by neighbouring tiles
     int k = 0, s = 0, ph = 1;
-    for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-      const int v0 = t / a.nt * kFlTileV, n0 = t % a.nt * a.tn;
-      const int nsb = (min(a.tn, a.N - n0) + kRows - 1) / kRows;
-      const uint32_t bytes = kFlABytes + a.tn * kFlBoxBytes + (1 + nsb) * kSf;
-      const uint8_t* wsc = a.wsc + (int64_t)(v0 / kRows) * chunks * kSf;
-      const uint8_t* xsc = a.xsc + (int64_t)(n0 / kRows) * chunks * kSf;
+    for (int t = pair; t < tiles && ok; t += pairs) {
+      const int v0 = t / a.nt * kFlTileV + (int)rank * kFlHalfV, n0 = t % a.nt * a.tn;
+      const int nn = min(a.tn, a.N - n0), nsb = (nn + kRows - 1) / kRows;
+      const int nb = n0 + (int)rank * ((nn + 31) / 32 * 16);  // this CTA's first column of B
+      const uint32_t bytes = kFlABytes + half * kFlBoxBytes + (1 + nsb) * kSf;
+      const int wrow = v0 / kRows * chunks * kQ, xrow = n0 / kRows * chunks * kQ;  // rows of 512 bytes
       for (int c = 0; c < chunks; ++c, ++k) {
         ok = tc::mbar_wait(bar(&bars.empty[s]), ph, abort);
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) break;
         if (tc::elect_one()) {
-          const uint32_t st = sbase + s * a.stage_bytes, f = bar(&bars.full[s]);
-          tc::mbar_arrive_expect_tx(f, bytes);
-          tc::tma_load_2d(st, &tw, c * kFlBoxBytes, v0, f, a.nt > 1 ? keep : first);
-          tc::tma_load_2d(st + b_off, &tx, c * kFlBoxBytes, n0, f, keep);
-          tc::bulk_load(st + sa_off, wsc + (int64_t)c * kSf, kSf, f);
-          tc::bulk_load(st + sb_off, xsc + (int64_t)c * kSf, kSf, f);
-          if (nsb > 1) tc::bulk_load(st + sb_off + kSf, xsc + (int64_t)(chunks + c) * kSf, kSf, f);
-        }
-        if (++s == a.stages) {
-          s = 0;
-          ph ^= 1;
-        }
-      }
-    }
-    if (!ok && lane == 0) {
-      *abort = 1;
-      raise_status(a.status, DSPARK_ETIMEOUT);
-      int never = 0;  // copies in flight land before the CTA ends
-      for (int j = max(0, k - a.stages); j < k; ++j)
-        tc::mbar_wait(bar(&bars.full[j % a.stages]), j / a.stages & 1, &never);
-    }
-  } else if (warp == 1) {
-    const uint32_t sfa = tmem + kFlSfCol, sfb = sfa + 4 * kQ;
-    const uint64_t ad0 = tc::smem_desc(sbase, 16, 1024), sd0 = tc::scales_desc(sbase);
-    int i = 0, s = 0, ph = 0;
-    for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++i) {
-      const int n0 = t % a.nt * a.tn, nn = min(a.tn, a.N - n0), nm = (nn + 15) / 16 * 16;
-      const int nsb = (nn + kRows - 1) / kRows, buf = i & 1;
-      const uint32_t d = tmem + (buf ? a.acc1 : 0);
-      const uint32_t id = tc::idesc_fp4(kFlTileV, nm, FMT == DSPARK_MXFP4, 0);
-      ok = tc::mbar_wait(bar(&bars.tempty[buf]), (i >> 1 & 1) ^ 1, abort);
-      if (ok && a.overlap && i > 0) ok = tc::mbar_wait(bar(&bars.over), (i - 1) & 1, abort);
-      ok = __all_sync(0xFFFFFFFFu, ok);
-      tc::tc_fence_after();
-      for (int c = 0; c < chunks && ok; ++c) {
-        ok = tc::mbar_wait(bar(&bars.full[s]), ph, abort);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok) break;
-        tc::tc_fence_after();
-        if (tc::elect_one()) {
-          const uint32_t off = (uint32_t)(s * a.stage_bytes) >> 4;
-          const uint64_t ad = ad0 + off, bd = ad + (b_off >> 4);
-          const uint64_t sa = sd0 + off + (sa_off >> 4), sb = sd0 + off + (sb_off >> 4);
-#pragma unroll
-          for (int q = 0; q < kQ; ++q) tc::cp_scales(sfa + 4 * q, sa + 32 * q);
-          if (nsb == 1) {
-#pragma unroll
-            for (int q = 0; q < kQ; ++q) tc::cp_scales(sfb + 4 * q, sb + 32 * q);
-          } else {
-#pragma unroll
-            for (int q = 0; q < kQ; ++q) {
-              tc::cp_scales(sfb + 8 * q, sb + 32 * q);
-              tc::cp_scales(sfb + 8 * q + 4, sb + (kSf >> 4) + 32 * q);
-            }
-          }
-          const int steps = min(4, (a.K - c * kChunk + 63) / 64);
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            if (kk < steps) {
-              // an nvfp4 step has its own word of scales; two mxfp4 steps share one, by halves
-              const int q = FMT == DSPARK_NVFP4 ? kk : kk >> 1;
-              const uint32_t half = FMT == DSPARK_NVFP4 ? 0 : (kk & 1) * 2;
-              const uint32_t idk = id | half << 4 | half << 29;
-              if (FMT == DSPARK_NVFP4)
-                tc::mma_nvfp4(d, ad + 2 * kk, bd + 2 * kk, idk, sfa + 4 * q, sfb + 4 * nsb * q, (c | kk) != 0);
-              else
-                tc::mma_mxfp4(d, ad + 2 * kk, bd + 2 * kk, idk, sfa + 4 * q, sfb + 4 * nsb * q, (c | kk) != 0);
-            }
-          }
-          tc::mma_commit(bar(&bars.empty[s]));
-          if (c == chunks - 1) tc::mma_commit(bar(&bars.tfull[buf]));
+          const uint32_t st = sbase + s * a.stage_bytes, f = tc::map_rank(bar(&bars.full[s]), 0);
+          if (rank == 0) tc::mbar_arrive_expect_tx(bar(&bars.full[s]), 2 * bytes);  // both CTAs' copies
+          tc::tma_load_2d_pair(st, &maps.w, c * kFlBoxBytes, v0, f);
+          tc::tma_load_2d_pair(st + b_off, &maps.x, c * kFlBoxBytes, nb, f);
+          tc::tma_load_2d_pair(st + sa_off, &maps.ws, 0, wrow + c * kQ, f);
+          tc::tma_load_2d_pair(st + sb_off, &maps.xs, 0, xrow + c * kQ, f);
+          if (nsb > 1) tc::tma_load_2d_pair(st + sb_off + kSf, &maps.xs, 0, xrow + (chunks + c) * kQ, f);
         }
         __syncwarp();
         if (++s == a.stages) {
@@ -248,23 +194,100 @@ __global__ void __launch_bounds__(kFlThreads, 1)
         }
       }
     }
+    // the last stages' releases, which the even CTA's MMAs send to both CTAs, have arrived before either exits
+    for (int j = max(0, k - a.stages); j < k && ok; ++j)
+      ok = tc::mbar_wait(bar(&bars.empty[j % a.stages]), j / a.stages & 1, abort);
     if (!ok && lane == 0) {
       *abort = 1;
       raise_status(a.status, DSPARK_ETIMEOUT);
-      int never = 0;
-      tc::mma_commit(bar(&bars.drain));
-      tc::mbar_wait(bar(&bars.drain), 0, &never);
+      int never = 0;  // copies in flight (they complete on the even CTA's barriers) land before the pair ends
+      if (rank == 0)
+        for (int j = max(0, k - a.stages); j < k; ++j)
+          tc::mbar_wait(bar(&bars.full[j % a.stages]), j / a.stages & 1, &never);
+    }
+  } else if (warp == 1) {
+    if (rank == 0) {
+      const uint32_t sfa = tmem + kFlSfCol, sfb = sfa + 4 * kQ;
+      const uint64_t ad0 = tc::smem_desc(sbase, 16, 1024), sd0 = tc::scales_desc(sbase);
+      int i = 0, s = 0, ph = 0;
+      for (int t = pair; t < tiles && ok; t += pairs, ++i) {
+        const int n0 = t % a.nt * a.tn, nn = min(a.tn, a.N - n0), nm = (nn + 31) / 32 * 32;
+        const int nsb = (nn + kRows - 1) / kRows, buf = i & 1;
+        const uint32_t d = tmem + (buf ? a.acc1 : 0);
+        const uint32_t id = tc::idesc_fp4(kFlTileV, nm, FMT == DSPARK_MXFP4, 0);
+        ok = tc::mbar_wait(bar(&bars.tempty[buf]), (i >> 1 & 1) ^ 1, abort);
+        if (ok && a.overlap && i > 0) ok = tc::mbar_wait(bar(&bars.over), (i - 1) & 1, abort);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        tc::tc_fence_after();
+        for (int c = 0; c < chunks && ok; ++c) {
+          ok = tc::mbar_wait(bar(&bars.full[s]), ph, abort);
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          if (!ok) break;
+          tc::tc_fence_after();
+          if (tc::elect_one()) {
+            const uint32_t off = (uint32_t)(s * a.stage_bytes) >> 4;
+            const uint64_t ad = ad0 + off, bd = ad + (b_off >> 4);
+            const uint64_t sa = sd0 + off + (sa_off >> 4), sb = sd0 + off + (sb_off >> 4);
+#pragma unroll
+            for (int q = 0; q < kQ; ++q) tc::cp_scales_pair(sfa + 4 * q, sa + 32 * q);
+            if (nsb == 1) {
+#pragma unroll
+              for (int q = 0; q < kQ; ++q) tc::cp_scales_pair(sfb + 4 * q, sb + 32 * q);
+            } else {
+#pragma unroll
+              for (int q = 0; q < kQ; ++q) {
+                tc::cp_scales_pair(sfb + 8 * q, sb + 32 * q);
+                tc::cp_scales_pair(sfb + 8 * q + 4, sb + (kSf >> 4) + 32 * q);
+              }
+            }
+            const int steps = min(4, (a.K - c * kChunk + 63) / 64);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+              if (kk < steps) {
+                // an nvfp4 step has its own word of scales; two mxfp4 steps share one, by halves
+                const int q = FMT == DSPARK_NVFP4 ? kk : kk >> 1;
+                const uint32_t part = FMT == DSPARK_NVFP4 ? 0 : (kk & 1) * 2;
+                const uint32_t idk = id | part << 4 | part << 29;
+                if (FMT == DSPARK_NVFP4)
+                  tc::mma_nvfp4_pair(d, ad + 2 * kk, bd + 2 * kk, idk, sfa + 4 * q, sfb + 4 * nsb * q, (c | kk) != 0);
+                else
+                  tc::mma_mxfp4_pair(d, ad + 2 * kk, bd + 2 * kk, idk, sfa + 4 * q, sfb + 4 * nsb * q, (c | kk) != 0);
+              }
+            }
+            tc::mma_commit_pair(bar(&bars.empty[s]));
+            if (c == chunks - 1) tc::mma_commit_pair(bar(&bars.tfull[buf]));
+          }
+          __syncwarp();
+          if (++s == a.stages) {
+            s = 0;
+            ph ^= 1;
+          }
+        }
+      }
+      // both CTAs' epilogues have released the last tiles: every MMA is complete, and their arrivals have landed
+      // before this CTA exits
+      for (int j = max(0, i - 2); j < i && ok; ++j) ok = tc::mbar_wait(bar(&bars.tempty[j & 1]), j >> 1 & 1, abort);
+      if (ok && a.overlap && i > 0) ok = tc::mbar_wait(bar(&bars.over), (i - 1) & 1, abort);
+      if (!ok && lane == 0) {
+        *abort = 1;
+        raise_status(a.status, DSPARK_ETIMEOUT);
+        int never = 0;
+        tc::mma_commit_pair_own(bar(&bars.drain));  // every MMA issued completes before TMEM and operands go
+        tc::mbar_wait(bar(&bars.drain), 0, &never);
+      }
     }
   } else if (warp >= 4) {
     const int q = warp & 3, h = (warp - 4) >> 2;
     const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
+    const uint32_t over = tc::map_rank(bar(&bars.over), 0);
     const int units = a.tn / 16, nov = a.overlap / 16;
     int i = 0;
-    for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++i) {
+    for (int t = pair; t < tiles; t += pairs, ++i) {
       const int v0 = t / a.nt * kFlTileV, n0 = t % a.nt * a.tn, nn = min(a.tn, a.N - n0), buf = i & 1;
-      const int v = v0 + q * 32 + lane;
+      const int v = v0 + (int)rank * kFlHalfV + q * 32 + lane;
       float wf = 1.f;
-      if (FMT == DSPARK_NVFP4) wf = __ldg(a.wf + v);  // padded to whole 128-row groups
+      // rows' factors are padded to whole 128-row groups
+      if (FMT == DSPARK_NVFP4 && v < (a.V + kRows - 1) / kRows * kRows) wf = __ldg(a.wf + v);
       ok = tc::mbar_wait(bar(&bars.tfull[buf]), i >> 1 & 1, abort);
       if (!ok) break;
       tc::tc_fence_after();
@@ -280,7 +303,7 @@ __global__ void __launch_bounds__(kFlThreads, 1)
         tc::tmem_wait_ld();
         tc::tc_fence_before();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(bar(&bars.over));
+        if (lane == 0) tc::mbar_arrive_cluster_relaxed(over);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int c = 16 * unit(h + 2 * e);
@@ -300,7 +323,7 @@ __global__ void __launch_bounds__(kFlThreads, 1)
       }
       tc::tc_fence_before();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(bar(&bars.tempty[buf]));
+      if (lane == 0) tc::mbar_arrive_cluster_relaxed(tc::map_rank(bar(&bars.tempty[buf]), 0));
     }
     if (!ok) {
       *abort = 1;
@@ -309,11 +332,9 @@ __global__ void __launch_bounds__(kFlThreads, 1)
   }
   tc::tc_fence_before();
   __syncthreads();
+  tc::cluster_meet();
   tc::tc_fence_after();
-  if (warp == 2) {
-    tc::tmem_relinquish();
-    tc::tmem_dealloc(tmem, 512);
-  }
+  if (warp == 2) tc::tmem_dealloc_pair(tmem, 512);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
@@ -339,8 +360,21 @@ bool encode(CUtensorMap* tm, const void* codes, int K, int rows, int box_rows) {
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Scales as rows of 512 bytes; boxes of one 128-row group's of 256 columns.
+bool encode_scales(CUtensorMap* tm, const void* scales, int K, int rows, int format) {
+  const cuuint64_t groups = ((cuuint64_t)rows + kRows - 1) / kRows;
+  const int per = chunk_bytes(format) / 512;
+  const cuuint64_t dims[2] = {128, groups * chunks_of(K) * per};
+  const cuuint64_t strides[1] = {512};
+  const cuuint32_t box[2] = {128, (cuuint32_t)per};
+  const cuuint32_t es[2] = {1, 1};
+  return encode_fn()(tm, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(scales), dims, strides, box, es,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int FMT, typename T, bool HASU>
-cudaError_t launch(const CUtensorMap& tw, const CUtensorMap& tx, const FlArgs& a, int grid, cudaStream_t st) {
+cudaError_t launch(const FlMaps& maps, const FlArgs& a, int grid, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
   constexpr int kMax = 227 * 1024 - 1024;  // the barriers are static
   const cudaError_t c = once_per_device(done, [] {
@@ -348,15 +382,13 @@ cudaError_t launch(const CUtensorMap& tw, const CUtensorMap& tx, const FlArgs& a
   });
   if (c != cudaSuccess) return c;
   return launch_ex(k_fp4_linear<FMT, T, HASU>, dim3(grid), dim3(kFlThreads), (size_t)a.stages * a.stage_bytes + 1024, st,
-                   true, tw, tx, a);
+                   true, maps, a);
 }
 template <int FMT>
-cudaError_t launch_t(bool bf16, const CUtensorMap& tw, const CUtensorMap& tx, const FlArgs& a, int grid,
-                     cudaStream_t st) {
+cudaError_t launch_t(bool bf16, const FlMaps& maps, const FlArgs& a, int grid, cudaStream_t st) {
   if (bf16)
-    return a.U ? launch<FMT, __nv_bfloat16, true>(tw, tx, a, grid, st)
-               : launch<FMT, __nv_bfloat16, false>(tw, tx, a, grid, st);
-  return a.U ? launch<FMT, float, true>(tw, tx, a, grid, st) : launch<FMT, float, false>(tw, tx, a, grid, st);
+    return a.U ? launch<FMT, __nv_bfloat16, true>(maps, a, grid, st) : launch<FMT, __nv_bfloat16, false>(maps, a, grid, st);
+  return a.U ? launch<FMT, float, true>(maps, a, grid, st) : launch<FMT, float, false>(maps, a, grid, st);
 }
 
 bool on_type(const void* p, int size) { return p && (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(size - 1)) == 0; }
@@ -380,8 +412,6 @@ extern "C" dspark_status dspark_fp4_linear(const dspark_fp4_dims* xd, const dspa
   if (U == Y && (type != DSPARK_F32 || ldu != ldy)) return DSPARK_EINVAL;
   if (!encode_fn()) return DSPARK_ECUDA;
   FlArgs a = {};
-  a.wsc = static_cast<const uint8_t*>(w->scales);
-  a.xsc = static_cast<const uint8_t*>(x->scales);
   a.wf = w->rowf;
   a.xf = x->rowf;
   a.U = U;
@@ -393,29 +423,32 @@ extern "C" dspark_status dspark_fp4_linear(const dspark_fp4_dims* xd, const dspa
   a.V = wd->rows;
   a.status = device_status;
   // one tile of tokens for up to 256 of them; more in tiles of 256 (scales come in groups of 128 rows)
-  a.tn = a.N >= kFlMaxN ? kFlMaxN : (a.N + 15) / 16 * 16;
+  a.tn = a.N >= kFlMaxN ? kFlMaxN : (a.N + 31) / 32 * 32;
   a.vt = (a.V + kFlTileV - 1) / kFlTileV;
   a.nt = (a.N + a.tn - 1) / a.tn;
   const int acc = kFlSfCol / 2 / 16 * 16;  // 224 columns each without overlap
   a.overlap = a.tn > acc ? 2 * a.tn - kFlSfCol : 0;
   a.acc1 = a.tn - a.overlap;
   const int sf = fp4::chunk_bytes(wd->format);
-  const int bytes = kFlABytes + a.tn * kFlBoxBytes + sf * (1 + (a.tn + fp4::kRows - 1) / fp4::kRows);
+  const int bytes = kFlABytes + a.tn / 2 * kFlBoxBytes + sf * (1 + (a.tn + fp4::kRows - 1) / fp4::kRows);
   a.stage_bytes = (bytes + 1023) / 1024 * 1024;
   a.stages = (227 * 1024 - 2048) / a.stage_bytes;
   if (a.stages > kFlMaxStages) a.stages = kFlMaxStages;
-  CUtensorMap tw, tx;
-  if (!encode(&tw, w->codes, a.K, a.V, kFlTileV) || !encode(&tx, x->codes, a.K, a.N, a.tn)) return DSPARK_ECUDA;
+  FlMaps maps;
+  if (!encode(&maps.w, w->codes, a.K, a.V, kFlHalfV) || !encode(&maps.x, x->codes, a.K, a.N, a.tn / 2) ||
+      !encode_scales(&maps.ws, w->scales, a.K, a.V, wd->format) ||
+      !encode_scales(&maps.xs, x->scales, a.K, a.N, wd->format))
+    return DSPARK_ECUDA;
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   const int64_t tiles = (int64_t)a.vt * a.nt;
   if (tiles > (1ll << 30)) return DSPARK_EUNSUPPORTED;
-  const int grid = (int)(tiles < sms ? tiles : sms);
+  const int grid = 2 * (int)(tiles < sms / 2 ? tiles : sms / 2);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (e == cudaSuccess)
-    e = wd->format == DSPARK_NVFP4 ? launch_t<DSPARK_NVFP4>(type == DSPARK_BF16, tw, tx, a, grid, st)
-                                   : launch_t<DSPARK_MXFP4>(type == DSPARK_BF16, tw, tx, a, grid, st);
+    e = wd->format == DSPARK_NVFP4 ? launch_t<DSPARK_NVFP4>(type == DSPARK_BF16, maps, a, grid, st)
+                                   : launch_t<DSPARK_MXFP4>(type == DSPARK_BF16, maps, a, grid, st);
   if (e != cudaSuccess) fprintf(stderr, "dspark: CUDA error %s\n", cudaGetErrorString(e));
   return e == cudaSuccess ? DSPARK_OK : DSPARK_ECUDA;
 }
