@@ -8,7 +8,8 @@
 // tile's w and half of its x. A producer warp loads 256 columns of both operands a stage (128-byte
 // swizzled boxes) with their scales (contiguous, as dspark_fp4_quant lays them
 // out); the MMA warp copies the scales to TMEM and issues four block-scaled
-// MMAs of 64 columns; eight warps store.
+// MMAs of 64 columns; eight warps work off accumulators, 16 tokens by 32 v a box of shared memory: U comes in by the
+// copy engine some boxes ahead, the result goes out from the same box (unaligned rows go by plain loads and stores).
 //
 // TMEM: two accumulators, and 48 columns of scales. Accumulators of more than
 // 224 columns overlap in the middle: the epilogue empties the shared columns
@@ -48,14 +49,21 @@ struct FlArgs {
   int vt, nt;    // tiles
   int stages, stage_bytes;
   int acc1, overlap;  // the second accumulator's first column; columns it shares with the first
+  int boxes;     // U and Y go by boxes
   int* status;
 };
 
 struct FlMaps {
   CUtensorMap w, x, ws, xs;  // codes and scales
+  CUtensorMap u, y;          // with boxes
 };
 
+// Boxes of 16 tokens by 32 v of each epilogue warp: with U four, three of them on their way, else two.
+__host__ __device__ constexpr int fl_slots(bool has_u) { return has_u ? 4 : 2; }
+__host__ __device__ constexpr int fl_slot_bytes(bool has_u, int size) { return has_u || size == 4 ? 2048 : 1024; }
+
 struct FlBars {
+  uint64_t ufull[8][4];
   uint64_t full[kFlMaxStages], empty[kFlMaxStages], tfull[2], tempty[2], over, drain;
   uint32_t tmem;
   int abort;
@@ -116,6 +124,21 @@ __device__ __forceinline__ void fl_store16(const FlArgs& a, float* z, int n0, in
   }
 }
 
+__device__ __forceinline__ void fl_scale16(const FlArgs& a, float* z, int n0, float wf) {
+  const unsigned long long w2 = tc::f2pack(wf, wf);
+#pragma unroll
+  for (int i = 0; i < 16; i += 4) {
+    const float4 f = __ldg(reinterpret_cast<const float4*>(a.xf + n0 + i));
+    tc::f2unpack(tc::mul2(tc::mul2(tc::f2pack(z[i], z[i + 1]), w2), tc::f2pack(f.x, f.y)), z[i], z[i + 1]);
+    tc::f2unpack(tc::mul2(tc::mul2(tc::f2pack(z[i + 2], z[i + 3]), w2), tc::f2pack(f.z, f.w)), z[i + 2], z[i + 3]);
+  }
+}
+
+// The boxes of one epilogue warp, in the order that it takes them.
+struct FlUnits {
+  int t, i, j;  // tile, its number among the pair's, place in its order
+};
+
 template <int FMT, typename T, bool HASU>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFlThreads, 1)
     k_fp4_linear(const __grid_constant__ FlMaps maps, FlArgs a) {
@@ -142,6 +165,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFlThreads, 1)
       tc::mbar_init(bar(&bars.tempty[i]), 16);  // the even CTA's: both CTAs' epilogue warps
     }
     tc::mbar_init(bar(&bars.over), 16);
+    for (int i = 0; i < 32; ++i) tc::mbar_init(bar(&bars.ufull[i >> 2][i & 3]), 1);
     tc::mbar_init(bar(&bars.drain), 1);
     bars.abort = 0;
     tc::fence_barrier_init();
@@ -277,54 +301,122 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFlThreads, 1)
       }
     }
   } else if (warp >= 4) {
-    const int q = warp & 3, h = (warp - 4) >> 2;
+    constexpr int kSlots = fl_slots(HASU), kSlot = fl_slot_bytes(HASU, sizeof(T));
+    const int e = warp - 4, q = e & 3, h = e >> 2;
     const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
     const uint32_t over = tc::map_rank(bar(&bars.over), 0);
     const int units = a.tn / 16, nov = a.overlap / 16;
+    const int vq = (int)rank * kFlHalfV + q * 32;  // the warp's first row in a tile
+    const uint32_t slots = sbase + a.stages * a.stage_bytes + e * (kSlots * kSlot);
+    // the first accumulator's last columns and the second's first are the shared ones: they come first
+    auto col = [&](int i, int j) { return 16 * (i & 1 ? j : units - 1 - j); };
+    // the next unit of 16 tokens that there are any of, from unit u on
+    auto live = [&](FlUnits u) {
+      for (; u.t < tiles; u.t += pairs, ++u.i, u.j = h) {
+        const int nn = min(a.tn, a.N - u.t % a.nt * a.tn);
+        for (; u.j < units; u.j += 2)
+          if (col(u.i, u.j) < nn) return u;
+      }
+      return u;
+    };
+    int g = 0;  // boxes taken
+    FlUnits ahead{pair, 0, h};
+    int asked = 0;
+    auto ask = [&]() {  // U's next box
+      ahead = live(ahead);
+      if (ahead.t >= tiles) return;
+      if (lane == 0) {
+        const uint32_t b = bar(&bars.ufull[e][asked % kSlots]);
+        tc::mbar_arrive_expect_tx(b, 2048);
+        tc::tma_load_2d(slots + asked % kSlots * kSlot, &maps.u, ahead.t / a.nt * kFlTileV + vq,
+                        ahead.t % a.nt * a.tn + col(ahead.i, ahead.j), b, tc::policy_evict_first());
+      }
+      ++asked;
+      ahead.j += 2;
+    };
+    if (HASU && a.boxes)
+      for (int i = 0; i < kSlots - 1; ++i) ask();
+    // 16 columns: scaled, U added, to their box and out
+    auto put = [&](float* z, int c, int v0, int n0, int nn, float wf) {
+      if (!a.boxes) {
+        fl_store16<T, FMT == DSPARK_NVFP4, HASU>(a, z, n0 + c, nn - c, v0 + vq + lane, wf);
+        return;
+      }
+      if (FMT == DSPARK_NVFP4) fl_scale16(a, z, n0 + c, wf);
+      const uint32_t box = slots + g % kSlots * kSlot;
+      if (HASU) {
+        ok = ok && tc::mbar_wait(bar(&bars.ufull[e][g % kSlots]), g / kSlots & 1, abort);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          float u;
+          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(u) : "r"(box + i * 128 + lane * 4));
+          z[i] += u;
+        }
+        if (sizeof(T) == 2) __syncwarp();  // the box is written with other rows
+      } else {
+        // the store before the last has read this box
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+        __syncwarp();
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        if (sizeof(T) == 4)
+          asm volatile("st.shared.f32 [%0], %1;" ::"r"(box + i * 128 + lane * 4), "f"(z[i]) : "memory");
+        else
+          asm volatile("st.shared.b16 [%0], %1;" ::"r"(box + i * 64 + lane * 2),
+                       "h"(__bfloat16_as_ushort(__float2bfloat16_rn(z[i])))
+                       : "memory");
+      }
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        tc::tma_store_2d(&maps.y, v0 + vq, n0 + c, box);
+        tc::bulk_commit();
+        // U's next box goes where the store before this one came from
+        if (HASU) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+      }
+      if (HASU) {
+        __syncwarp();
+        ask();
+      }
+      ++g;
+    };
     int i = 0;
     for (int t = pair; t < tiles; t += pairs, ++i) {
       const int v0 = t / a.nt * kFlTileV, n0 = t % a.nt * a.tn, nn = min(a.tn, a.N - n0), buf = i & 1;
-      const int v = v0 + (int)rank * kFlHalfV + q * 32 + lane;
+      const int v = v0 + vq + lane;
       float wf = 1.f;
       // rows' factors are padded to whole 128-row groups
       if (FMT == DSPARK_NVFP4 && v < (a.V + kRows - 1) / kRows * kRows) wf = __ldg(a.wf + v);
-      ok = tc::mbar_wait(bar(&bars.tfull[buf]), i >> 1 & 1, abort);
+      ok = ok && tc::mbar_wait(bar(&bars.tfull[buf]), i >> 1 & 1, abort);
       if (!ok) break;
       tc::tc_fence_after();
       const uint32_t d = lanes + (buf ? a.acc1 : 0);
-      // the shared columns are the first accumulator's last and the second's first
-      auto unit = [&](int j) { return buf ? j : units - 1 - j; };
-      int j = h;
-      if (nov) {
-        float o[2][16];
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          if (h + 2 * e < nov) tc::tmem_ld16(d + 16 * unit(h + 2 * e), o[e]);
+      // two units at a time; their columns are free once they are in registers
+      for (int j = h; j < units; j += 4) {
+        float z[2][16];
+        const int c0 = col(i, j), c1 = j + 2 < units ? col(i, j + 2) : kFlMaxN;
+        tc::tmem_ld16(d + c0, z[0]);
+        if (j + 2 < units) tc::tmem_ld16(d + c1, z[1]);
         tc::tmem_wait_ld();
         tc::tc_fence_before();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive_cluster_relaxed(over);
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int c = 16 * unit(h + 2 * e);
-          if (h + 2 * e < nov) {
-            if (c < nn) fl_store16<T, FMT == DSPARK_NVFP4, HASU>(a, o[e], n0 + c, nn - c, v, wf);
-            j = h + 2 * e + 2;
-          }
+        if (lane == 0) {
+          if (nov && j == h) tc::mbar_arrive_cluster_relaxed(over);  // nov <= 4: they are all in registers
+          if (j + 4 >= units) tc::mbar_arrive_cluster_relaxed(tc::map_rank(bar(&bars.tempty[buf]), 0));
         }
+        if (c0 < nn) put(z[0], c0, v0, n0, nn, wf);
+        if (c1 < nn) put(z[1], c1, v0, n0, nn, wf);
       }
-      for (; j < units; j += 2) {
-        const int c = 16 * unit(j);
-        if (c >= nn) continue;
-        float z[16];
-        tc::tmem_ld16(d + c, z);
-        tc::tmem_wait_ld();
-        fl_store16<T, FMT == DSPARK_NVFP4, HASU>(a, z, n0 + c, nn - c, v, wf);
-      }
-      tc::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive_cluster_relaxed(tc::map_rank(bar(&bars.tempty[buf]), 0));
     }
+    // stores are complete, and U's boxes that no one took have come
+    if (a.boxes && lane == 0) {
+      asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+      int never = 0;
+      if (HASU && !ok)
+        for (int x = g; x < asked; ++x) tc::mbar_wait(bar(&bars.ufull[e][x % kSlots]), x / kSlots & 1, &never);
+    }
+    __syncwarp();
     if (!ok) {
       *abort = 1;
       raise_status(a.status, DSPARK_ETIMEOUT);
@@ -373,6 +465,18 @@ bool encode_scales(CUtensorMap* tm, const void* scales, int K, int rows, int for
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// U or Y by boxes of 16 rows and 32 columns.
+bool encode_boxes(CUtensorMap* tm, const void* p, bool bf16, int V, int N, int64_t ld) {
+  const cuuint64_t dims[2] = {(cuuint64_t)V, (cuuint64_t)N};
+  const cuuint64_t strides[1] = {(cuuint64_t)ld * (bf16 ? 2 : 4)};
+  const cuuint32_t box[2] = {32, 16};
+  const cuuint32_t es[2] = {1, 1};
+  return encode_fn()(tm, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2,
+                     const_cast<void*>(p), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int FMT, typename T, bool HASU>
 cudaError_t launch(const FlMaps& maps, const FlArgs& a, int grid, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
@@ -381,7 +485,7 @@ cudaError_t launch(const FlMaps& maps, const FlArgs& a, int grid, cudaStream_t s
     return cudaFuncSetAttribute(k_fp4_linear<FMT, T, HASU>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMax);
   });
   if (c != cudaSuccess) return c;
-  return launch_ex(k_fp4_linear<FMT, T, HASU>, dim3(grid), dim3(kFlThreads), (size_t)a.stages * a.stage_bytes + 1024, st,
+  return launch_ex(k_fp4_linear<FMT, T, HASU>, dim3(grid), dim3(kFlThreads), (size_t)a.stages * a.stage_bytes + 8 * fl_slots(HASU) * fl_slot_bytes(HASU, sizeof(T)) + 1024, st,
                    true, maps, a);
 }
 template <int FMT>
@@ -432,12 +536,18 @@ extern "C" dspark_status dspark_fp4_linear(const dspark_fp4_dims* xd, const dspa
   const int sf = fp4::chunk_bytes(wd->format);
   const int bytes = kFlABytes + a.tn / 2 * kFlBoxBytes + sf * (1 + (a.tn + fp4::kRows - 1) / fp4::kRows);
   a.stage_bytes = (bytes + 1023) / 1024 * 1024;
-  a.stages = (227 * 1024 - 2048) / a.stage_bytes;
+  const int slots = 8 * fl_slots(U != nullptr) * fl_slot_bytes(U != nullptr, type == DSPARK_BF16 ? 2 : 4);
+  a.stages = (227 * 1024 - 2048 - slots) / a.stage_bytes;
   if (a.stages > kFlMaxStages) a.stages = kFlMaxStages;
-  FlMaps maps;
+  FlMaps maps = {};
   if (!encode(&maps.w, w->codes, a.K, a.V, kFlHalfV) || !encode(&maps.x, x->codes, a.K, a.N, a.tn / 2) ||
       !encode_scales(&maps.ws, w->scales, a.K, a.V, wd->format) ||
       !encode_scales(&maps.xs, x->scales, a.K, a.N, wd->format))
+    return DSPARK_ECUDA;
+  const int size = type == DSPARK_BF16 ? 2 : 4;
+  a.boxes = (reinterpret_cast<uintptr_t>(Y) & 15u) == 0 && ldy * size % 16 == 0 &&
+            (!U || ((reinterpret_cast<uintptr_t>(U) & 15u) == 0 && ldu % 4 == 0));
+  if (a.boxes && (!encode_boxes(&maps.y, Y, size == 2, a.V, a.N, ldy) || (U && !encode_boxes(&maps.u, U, false, a.V, a.N, ldu))))
     return DSPARK_ECUDA;
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
