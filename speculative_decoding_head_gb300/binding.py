@@ -215,7 +215,7 @@ def _vec(t: Optional[torch.Tensor], n: int, dtype, name: str, device: int):
     """Address of a contiguous vector of n values on CUDA device ``device`` (None: no vector)."""
     if t is None:
         return None
-    if t.dtype != dtype or t.get_device() != device or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+    if t.dtype != dtype or t.get_device() != device or t.shape != (n,) or not t.is_contiguous():
         raise DsparkError(f"{name} must be a contiguous vector [{n}] of {dtype} on cuda:{device}, got {list(t.shape)} "
                           f"{t.dtype} on {t.device}")
     return t.data_ptr()
@@ -534,6 +534,13 @@ class _TrainOp:
                 t.record_stream(stream)
         return raw
 
+    def _new(self, shape, dtype, stream):
+        """A new tensor on the object's device, of the stream that a call runs on."""
+        if stream is None:
+            return self.status.new_empty(shape, dtype=dtype)
+        with torch.cuda.stream(stream):
+            return self.status.new_empty(shape, dtype=dtype)
+
     def device_status(self) -> int:
         """The first device error since the last reset (synchronises)."""
         return int(self.status.item())
@@ -786,8 +793,7 @@ class Fp4Matrix(_TrainOp):
         [N, K] bf16 or fp32 (``dspark_fp4_rows``)."""
         n = self.rows if idx is None else idx.shape[0]
         if out is None:
-            with torch.cuda.stream(stream):
-                out = torch.empty(n, self.K, dtype=dtype, device=self.status.device)
+            out = self._new((n, self.K), dtype, stream)
         code = _dtype_code(out, "out")
         po, ldo = _rows(out, n, self.K, out.dtype, "out", self._index)
         pi = _vec(idx, n, torch.int32, "idx", self._index)
@@ -804,8 +810,7 @@ class Fp4Matrix(_TrainOp):
         if X.fmt != self.fmt or X.K != self.K:
             raise DsparkError(f"X holds {X.fmt} rows of {X.K}, the matrix {self.fmt} rows of {self.K}")
         if out is None:
-            with torch.cuda.stream(stream):
-                out = torch.empty(X.rows, self.rows, dtype=dtype, device=self.status.device)
+            out = self._new((X.rows, self.rows), dtype, stream)
         code = _dtype_code(out, "out")
         po, ldo = _rows(out, X.rows, self.rows, out.dtype, "out", self._index)
         pu, ldu = (None, 0) if U is None else _rows(U, X.rows, self.rows, torch.float32, "U", self._index)
@@ -829,35 +834,43 @@ class Sampler(_TrainOp):
         self.N, self.V, self.requests = int(N), int(V), None if requests is None else int(requests)
         if not (0 <= self.N <= 1 << 24 and 1 <= self.V <= 1 << 24 and (requests is None or self.requests >= 1)):
             raise DsparkError(f"dspark_sample: unsupported N={N}, V={V}, requests={requests}")
+        self._args = SampleArgs(self.N, self.V, self.requests or 0)
+        self._pargs = C.byref(self._args)
         super().__init__(device)
 
     def _buffers(self):
         return (self.status,)
 
-    def _args(self, Z, row_off, temperature, top_k, top_p, min_p):
-        dev, f32, i32 = self._index, torch.float32, torch.int32
-        code = _dtype_code(Z, "Z")
+    def _set(self, Z, row_off, temperature, top_k, top_p, min_p) -> int:
+        """Takes a call's inputs into the argument block; returns the address of the logits."""
+        dev, f32, i32, a = self._index, torch.float32, torch.int32, self._args
+        a.type = _dtype_code(Z, "Z")
         pz, ldz = _rows(Z, self.N, self.V, Z.dtype, "Z", dev)
-        if row_off is not None and self.requests is None:
+        a.ldz = max(ldz, self.V)
+        n = self.N
+        if row_off is None:
+            a.row_off = None
+        elif self.requests is None:
             raise DsparkError("row_off needs a Sampler made with requests")
-        n = self.N if row_off is None else self.requests
-        return pz, SampleArgs(self.N, self.V, self.requests or 0, code, max(ldz, self.V),
-                              None if row_off is None else _vec(row_off, n + 1, i32, "row_off", dev),
-                              _vec(temperature, n, f32, "temperature", dev), _vec(top_k, n, i32, "top_k", dev),
-                              _vec(top_p, n, f32, "top_p", dev), _vec(min_p, n, f32, "min_p", dev))
+        else:
+            n = self.requests
+            a.row_off = _vec(row_off, n + 1, i32, "row_off", dev)
+        a.temperature = _vec(temperature, n, f32, "temperature", dev)
+        a.top_k = _vec(top_k, n, i32, "top_k", dev)
+        a.top_p = _vec(top_p, n, f32, "top_p", dev)
+        a.min_p = _vec(min_p, n, f32, "min_p", dev)
+        return pz
 
     def sample(self, Z, u, temperature=None, top_k=None, top_p=None, min_p=None, row_off=None, out=None, stream=None):
         """token [N] int32 and logp [N] fp32 drawn with u [N] fp32 in [0, 1);
         rows that ``row_off`` gives to no request are left as they are."""
         if out is None:
-            with torch.cuda.stream(stream):
-                out = {"token": torch.empty(self.N, dtype=torch.int32, device=self.status.device),
-                       "logp": torch.empty(self.N, dtype=torch.float32, device=self.status.device)}
+            out = {"token": self._new((self.N,), torch.int32, stream), "logp": self._new((self.N,), torch.float32, stream)}
         dev, f32 = self._index, torch.float32
-        pz, args = self._args(Z, row_off, temperature, top_k, top_p, min_p)
+        pz = self._set(Z, row_off, temperature, top_k, top_p, min_p)
         pu = _vec(u, self.N, f32, "u", dev)
         pt, pl = _vec(out["token"], self.N, torch.int32, "token", dev), _vec(out.get("logp"), self.N, f32, "logp", dev)
-        r = self._call(self.lib.dspark_sample, C.byref(args), pz, pu, pt, pl, self.status.data_ptr(), self._on(stream))
+        r = self._call(self.lib.dspark_sample, self._pargs, pz, pu, pt, pl, self.status.data_ptr(), self._on(stream))
         _check(r, "dspark_sample")
         return out
 
@@ -865,11 +878,10 @@ class Sampler(_TrainOp):
                  fill: float = float("-inf"), out=None, stream=None):
         """[N, V] fp32: the log-probabilities that ``sample`` draws with, ``fill`` where a token is left out."""
         if out is None:
-            with torch.cuda.stream(stream):
-                out = torch.empty(self.N, self.V, dtype=torch.float32, device=self.status.device)
-        pz, args = self._args(Z, row_off, temperature, top_k, top_p, min_p)
+            out = self._new((self.N, self.V), torch.float32, stream)
+        pz = self._set(Z, row_off, temperature, top_k, top_p, min_p)
         po, ldo = _rows(out, self.N, self.V, torch.float32, "out", self._index)
-        r = self._call(self.lib.dspark_sample_logprobs, C.byref(args), pz, fill, po, max(ldo, self.V),
+        r = self._call(self.lib.dspark_sample_logprobs, self._pargs, pz, fill, po, max(ldo, self.V),
                        self.status.data_ptr(), self._on(stream))
         _check(r, "dspark_sample_logprobs")
         return out
