@@ -510,7 +510,7 @@ class _TrainOp:
 
     def __init__(self, device):
         self.status = torch.zeros(1, dtype=torch.int32, device=device)
-        self._index = self.status.get_device()
+        self._index, self._device = self.status.get_device(), self.status.device
         self._streams = set()
 
     def _buffers(self):
@@ -537,9 +537,9 @@ class _TrainOp:
     def _new(self, shape, dtype, stream):
         """A new tensor on the object's device, of the stream that a call runs on."""
         if stream is None:
-            return self.status.new_empty(shape, dtype=dtype)
+            return torch.empty(shape, dtype=dtype, device=self._device)
         with torch.cuda.stream(stream):
-            return self.status.new_empty(shape, dtype=dtype)
+            return torch.empty(shape, dtype=dtype, device=self._device)
 
     def device_status(self) -> int:
         """The first device error since the last reset (synchronises)."""
