@@ -2,17 +2,21 @@
 // rows, and rows looked up as values.
 //
 // A block's scale s comes from its largest magnitude, its values are
-// RNE_e2m1(x / (s f)). Both roundings are those of the exact quotients: the
-// quotient is brought to its nearest fp32 number, and where that sits on a
-// border of the coarse format although the remainder is not zero, it moves a
-// step to the remainder's side (fp32 inputs; a bf16 quotient cannot round onto a border
-// that it is not on: 8 bits against a scale of 4 leave 2^-11 of room).
+// RNE_e2m1(x / (s f)). Both roundings are those of the exact quotients. A bf16 x that is not on a border of
+// two e2m1 numbers is 2^-8 of itself off it (8 bits against a border of 7 in the scale's units), so its product with
+// the scale's rounded reciprocal only has to be brought back to borders that it is on: rounded to multiples of
+// 2^-10, by the addition of 1.5 2^13. An fp32 product within two units of a border (five in a million)
+// is decided by the remainder instead.
+//
+// Both kernels move each byte once; quantisation has 3 to 6 instructions a value, most of them its largest
+// magnitude's and the products', on two values at a time.
 #include <math.h>
 #include <stdio.h>
 
 #include "dspark_common.cuh"
 #include "dspark_internal.h"
 #include "fp4.cuh"
+#include "tc_ptx.cuh"
 
 namespace dspark {
 
@@ -93,13 +97,13 @@ __global__ void __launch_bounds__(FMT == DSPARK_NVFP4 ? 512 : 1024) k_fp4_quant(
 #pragma unroll
   for (int j = 0; j < BPL; ++j) {
     uint32_t m = 0;
+    if (sizeof(T) == 4) {
 #pragma unroll
-    for (int i = 0; i < W; ++i) {
-      if (sizeof(T) == 4) {
-        m = max(m, w[j][i] & 0x7FFFFFFFu);
-      } else {
-        m = max(m, max(w[j][i] & 0x7FFF0000u, (w[j][i] << 16) & 0x7FFF0000u));
-      }
+      for (int i = 0; i < W; ++i) m = max(m, w[j][i] & 0x7FFFFFFFu);
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; ++i) m = __vmaxu2(m, w[j][i] & 0x7FFF7FFFu);
+      m = max(m & 0xFFFF0000u, m << 16);
     }
     top[j] = m;
     if (m < 0x7F800000u) rtop = max(rtop, m);
@@ -127,15 +131,16 @@ __global__ void __launch_bounds__(FMT == DSPARK_NVFP4 ? 512 : 1024) k_fp4_quant(
   for (int j = 0; j < BPL; ++j) {
     const int b = lane + j * a.lanes;
     if (top[j] >= 0x7F800000u) bad = true;
-    uint32_t code;       // the scale's
-    float s, inv;        // the scale (without f), and what x is multiplied by
+    uint32_t code;  // the scale's
+    float s, inv;   // the scale, with f, and what x is multiplied by
     if (FMT == DSPARK_NVFP4) {
       const float t = __uint_as_float(top[j]) * inv_f;  // exact: f is a power of two
       float q = __fdiv_rn(t, 6.f);
       q = off_border(q, fmaf(-q, 6.f, t), 0x7FFFFu);
       code = top[j] >= 0x7F800000u ? 0x7Fu : to_e4m3(q);
       s = from_e4m3(code);
-      inv = s == 0.f ? 0.f : __frcp_rn(s);
+      inv = s == 0.f ? 0.f : __frcp_rn(s) * inv_f;
+      s *= f;
     } else {
       const int e = top[j] >= 0x00800000u ? (int)(top[j] >> 23) - 127 : top[j] ? 31 - __clz(top[j]) - 149 : -149;
       const int es = max(e - 2, -127);
@@ -146,26 +151,42 @@ __global__ void __launch_bounds__(FMT == DSPARK_NVFP4 ? 512 : 1024) k_fp4_quant(
     const int c = b * B;
     if (row && c < (int)(2 * ldc)) {
       uint32_t o[B / 8];
+      const unsigned long long inv2 = tc::f2pack(inv, inv);
+      uint32_t near = ~0u;
 #pragma unroll
       for (int g = 0; g < B / 8; ++g) {
         float v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 8; i += 2) {
           const int k = 8 * g + i;
-          const float xv = sizeof(T) == 4 ? __uint_as_float(w[j][k])
-                                          : __uint_as_float((k & 1) ? w[j][k / 2] & 0xFFFF0000u : w[j][k / 2] << 16);
-          if (FMT == DSPARK_NVFP4) {
-            const float xs = xv * inv_f;
-            float q = xs * inv;
-            float rem = fmaf(-q, s, xs);
-            q = fmaf(rem, inv, q);  // the nearest to xs / s
-            if (sizeof(T) == 4) q = off_border(q, fmaf(-q, s, xs), 0xFFFFFu);
-            v[i] = q;
+          const float x0 = sizeof(T) == 4 ? __uint_as_float(w[j][k]) : __uint_as_float(w[j][k / 2] << 16);
+          const float x1 = sizeof(T) == 4 ? __uint_as_float(w[j][k + 1]) : __uint_as_float(w[j][k / 2] & 0xFFFF0000u);
+          unsigned long long q;
+          if (FMT == DSPARK_NVFP4 && sizeof(T) == 2) {
+            const float m = 12288.f;
+            q = tc::add2(tc::fma2(tc::f2pack(x0, x1), inv2, tc::f2pack(m, m)), tc::f2pack(-m, -m));
           } else {
-            v[i] = xv * inv;
+            q = tc::mul2(tc::f2pack(x0, x1), inv2);  // mxfp4: exact
           }
+          tc::f2unpack(q, v[i], v[i + 1]);
+          if (FMT == DSPARK_NVFP4 && sizeof(T) == 4)
+            near = min(near, min((__float_as_uint(v[i]) + 2u) & 0xFFFFFu, (__float_as_uint(v[i + 1]) + 2u) & 0xFFFFFu));
         }
         o[g] = to_e2m1x8(v);
+      }
+      if (FMT == DSPARK_NVFP4 && sizeof(T) == 4 && near <= 4u && s != 0.f) {
+#pragma unroll
+        for (int g = 0; g < B / 8; ++g) {
+          float v[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float x = __uint_as_float(w[j][8 * g + i]);
+            float q = x * inv;
+            q = fmaf(fmaf(-q, s, x), inv, q);  // the nearest to x / s
+            v[i] = off_border(q, fmaf(-q, s, x), 0xFFFFFu);
+          }
+          o[g] = to_e2m1x8(v);
+        }
       }
       uint8_t* p = a.codes + r * ldc + c / 2;
       if (B == 16) {
@@ -193,7 +214,7 @@ struct RoArgs {
   int N;
   void* out;
   int64_t ldo;
-  int vec;
+  int vec, shift;
   int* status;
 };
 
@@ -224,30 +245,53 @@ __device__ __forceinline__ void put8<__nv_bfloat16>(__nv_bfloat16* p, const floa
   }
 }
 
-// A thread takes eight values of a row: 4 bytes of codes, a scale, 16 or 32 bytes out.
-template <typename T, int FMT>
+// A thread takes eight values of a row at a time, 4 bytes of codes and a scale in, 16 or 32 bytes out, and four of
+// these together, whose loads are in flight at once: of four rows, or of one where a row is wider than 256 threads
+// (WIDE). 2^shift threads a row.
+constexpr int kRoEach = 4;
+template <typename T, int FMT, bool WIDE>
 __global__ void __launch_bounds__(256) k_fp4_rows(RoArgs a) {
   pdl_wait();
   pdl_trigger();
-  const int groups = (a.K + 7) / 8;
-  const int64_t all = (int64_t)a.N * groups;
-  for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < all; t += (int64_t)gridDim.x * 256) {
-    const int n = (int)(t / groups), g = (int)(t - (int64_t)n * groups);
-    const int r = a.idx ? __ldg(a.idx + n) : n;
-    float v[8];
-    if (r < 0 || r >= a.rows) {
-      if (g == 0 && r != -1) raise_status(a.status, DSPARK_ERANGE);
+  constexpr int kNb = kChunk / block_of(FMT);
+  const int groups = (a.K + 7) / 8, per = 256 >> a.shift;
+  const int n0 = blockIdx.x * (WIDE ? 1 : per * kRoEach) + (int)(threadIdx.x >> a.shift);
+  const int g0 = threadIdx.x & ((1 << a.shift) - 1);
+  for (int gg = g0; gg < groups; gg += WIDE ? 256 * kRoEach : groups) {
+    uint32_t c[kRoEach], sb[kRoEach];
+    float f[kRoEach];
+    int r[kRoEach];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = 0.f;
-    } else {
-      const uint32_t c = __ldg(reinterpret_cast<const uint32_t*>(a.codes + r * row_bytes(a.K)) + g);
-      const uint32_t sb = __ldg(a.scales + scale_at(FMT, a.K, r, 8 * g / block_of(FMT)));
-      const float s = FMT == DSPARK_NVFP4 ? from_e4m3(sb) * __ldg(a.rowf + r) : from_e8m0(sb);
-      from_e2m1x8(c, v);
+    for (int u = 0; u < kRoEach; ++u) {
+      const int n = WIDE ? n0 : n0 + u * per;
+      r[u] = n >= a.N ? -1 : a.idx ? __ldg(a.idx + n) : n;
+    }
+#pragma unroll
+    for (int u = 0; u < kRoEach; ++u) {
+      const int g = WIDE ? gg + u * 256 : gg;
+      c[u] = sb[u] = 0;
+      f[u] = 0.f;
+      if (r[u] >= 0 && r[u] < a.rows && (!WIDE || g < groups)) {
+        const int b = 8 * g / block_of(FMT);
+        c[u] = __ldg(reinterpret_cast<const uint32_t*>(a.codes + r[u] * row_bytes(a.K)) + g);
+        sb[u] = __ldg(a.scales + scale_at(FMT, a.K, r[u], 0) + b / kNb * chunk_bytes(FMT) + b % kNb / 4 * 512 + b % 4);
+        f[u] = FMT == DSPARK_NVFP4 ? __ldg(a.rowf + r[u]) : 1.f;
+      } else if (r[u] != -1 && g == 0 && !(r[u] >= 0 && r[u] < a.rows)) {
+        raise_status(a.status, DSPARK_ERANGE);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kRoEach; ++u) {
+      const int n = WIDE ? n0 : n0 + u * per, g = WIDE ? gg + u * 256 : gg;
+      if (n >= a.N || (WIDE && g >= groups)) continue;
+      // a row without a token: codes and scale 0
+      const float s = FMT == DSPARK_NVFP4 ? from_e4m3(sb[u]) * f[u] : f[u] == 0.f ? 0.f : from_e8m0(sb[u]);
+      float v[8];
+      from_e2m1x8(c[u], v);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] *= s;
+      put8<T>(static_cast<T*>(a.out) + n * a.ldo + 8 * g, v, a.vec, a.K - 8 * g);
     }
-    put8<T>(static_cast<T*>(a.out) + n * a.ldo + 8 * g, v, a.vec, a.K - 8 * g);
   }
 }
 
@@ -347,15 +391,20 @@ extern "C" dspark_status dspark_fp4_rows(const dspark_fp4_dims* d, const dspark_
   a.vec = on_16(out, ldo, type);
   a.status = device_status;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const int64_t ctas = ((int64_t)N * ((d->K + 7) / 8) + 255) / 256;
-  const dim3 grid((unsigned)(ctas < 152 * 64 ? ctas : 152 * 64)), block(256);
+  while (a.shift < 8 && (8 << a.shift) < d->K) ++a.shift;
+  const bool wide = d->K > 8 * 256;
+  const int per = wide ? 1 : (256 >> a.shift) * kRoEach;
+  const dim3 grid((unsigned)((N + per - 1) / per)), block(256);
   typedef __nv_bfloat16 bf;
+  auto go = [&](auto narrow_kernel, auto wide_kernel) {
+    return launch_ex(wide ? wide_kernel : narrow_kernel, grid, block, 0, st, true, a);
+  };
   cudaError_t e;
   if (d->format == DSPARK_NVFP4)
-    e = type == DSPARK_BF16 ? launch_ex(k_fp4_rows<bf, DSPARK_NVFP4>, grid, block, 0, st, true, a)
-                            : launch_ex(k_fp4_rows<float, DSPARK_NVFP4>, grid, block, 0, st, true, a);
+    e = type == DSPARK_BF16 ? go(k_fp4_rows<bf, DSPARK_NVFP4, false>, k_fp4_rows<bf, DSPARK_NVFP4, true>)
+                            : go(k_fp4_rows<float, DSPARK_NVFP4, false>, k_fp4_rows<float, DSPARK_NVFP4, true>);
   else
-    e = type == DSPARK_BF16 ? launch_ex(k_fp4_rows<bf, DSPARK_MXFP4>, grid, block, 0, st, true, a)
-                            : launch_ex(k_fp4_rows<float, DSPARK_MXFP4>, grid, block, 0, st, true, a);
+    e = type == DSPARK_BF16 ? go(k_fp4_rows<bf, DSPARK_MXFP4, false>, k_fp4_rows<bf, DSPARK_MXFP4, true>)
+                            : go(k_fp4_rows<float, DSPARK_MXFP4, false>, k_fp4_rows<float, DSPARK_MXFP4, true>);
   return fp4_fail(e);
 }
