@@ -218,34 +218,28 @@ struct RoArgs {
   int* status;
 };
 
+// 16 bytes of a row: eight bf16 or four fp32.
 template <typename T>
-__device__ __forceinline__ void put8(T* p, const float* v, bool vec, int left);
-template <>
-__device__ __forceinline__ void put8<float>(float* p, const float* v, bool vec, int left) {
-  if (vec && left >= 8) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+__device__ __forceinline__ void put16(T* p, const float* v, bool vec, int left) {
+  constexpr int kVals = 16 / (int)sizeof(T);
+  uint4 q;
+  if (sizeof(T) == 4) {
+    q = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
   } else {
+    __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&q);
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < left) p[i] = v[i];
+    for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
   }
-}
-template <>
-__device__ __forceinline__ void put8<__nv_bfloat16>(__nv_bfloat16* p, const float* v, bool vec, int left) {
-  __nv_bfloat162 h[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-  if (vec && left >= 8) {
-    *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(h);
+  if (vec && left >= kVals) {
+    *reinterpret_cast<uint4*>(p) = q;
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < left) p[i] = reinterpret_cast<const __nv_bfloat16*>(h)[i];
+    for (int i = 0; i < kVals; ++i)
+      if (i < left) p[i] = reinterpret_cast<const T*>(&q)[i];
   }
 }
 
-// A thread takes eight values of a row at a time, 4 bytes of codes and a scale in, 16 or 32 bytes out, and four of
+// A thread takes 16 bytes of the output at a time, 4 or 2 bytes of codes and a scale in, and four of
 // these together, whose loads are in flight at once: of four rows, or of one where a row is wider than 256 threads
 // (WIDE). 2^shift threads a row.
 constexpr int kRoEach = 4;
@@ -253,8 +247,8 @@ template <typename T, int FMT, bool WIDE>
 __global__ void __launch_bounds__(256) k_fp4_rows(RoArgs a) {
   pdl_wait();
   pdl_trigger();
-  constexpr int kNb = kChunk / block_of(FMT);
-  const int groups = (a.K + 7) / 8, per = 256 >> a.shift;
+  constexpr int kNb = kChunk / block_of(FMT), kVals = 16 / (int)sizeof(T);
+  const int groups = (a.K + kVals - 1) / kVals, per = 256 >> a.shift;
   const int n0 = blockIdx.x * (WIDE ? 1 : per * kRoEach) + (int)(threadIdx.x >> a.shift);
   const int g0 = threadIdx.x & ((1 << a.shift) - 1);
   for (int gg = g0; gg < groups; gg += WIDE ? 256 * kRoEach : groups) {
@@ -272,8 +266,10 @@ __global__ void __launch_bounds__(256) k_fp4_rows(RoArgs a) {
       c[u] = sb[u] = 0;
       f[u] = 0.f;
       if (r[u] >= 0 && r[u] < a.rows && (!WIDE || g < groups)) {
-        const int b = 8 * g / block_of(FMT);
-        c[u] = __ldg(reinterpret_cast<const uint32_t*>(a.codes + r[u] * row_bytes(a.K)) + g);
+        const int b = kVals * g / block_of(FMT);
+        const uint8_t* row = a.codes + r[u] * row_bytes(a.K);
+        c[u] = kVals == 8 ? __ldg(reinterpret_cast<const uint32_t*>(row) + g)
+                          : __ldg(reinterpret_cast<const unsigned short*>(row) + g);
         sb[u] = __ldg(a.scales + scale_at(FMT, a.K, r[u], 0) + b / kNb * chunk_bytes(FMT) + b % kNb / 4 * 512 + b % 4);
         f[u] = FMT == DSPARK_NVFP4 ? __ldg(a.rowf + r[u]) : 1.f;
       } else if (r[u] != -1 && g == 0 && !(r[u] >= 0 && r[u] < a.rows)) {
@@ -289,8 +285,8 @@ __global__ void __launch_bounds__(256) k_fp4_rows(RoArgs a) {
       float v[8];
       from_e2m1x8(c[u], v);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] *= s;
-      put8<T>(static_cast<T*>(a.out) + n * a.ldo + 8 * g, v, a.vec, a.K - 8 * g);
+      for (int i = 0; i < kVals; ++i) v[i] *= s;
+      put16<T>(static_cast<T*>(a.out) + n * a.ldo + kVals * g, v, a.vec, a.K - kVals * g);
     }
   }
 }
@@ -312,9 +308,12 @@ template <typename T, int FMT>
 cudaError_t quant(QuArgs a, cudaStream_t st) {
   // blocks with those that only fill up the last tile of scales
   const int nb = chunks_of(a.K) * (kChunk / block_of(FMT));
-  // An nvfp4 row belongs to one CTA (its largest value goes into every scale): a block a thread for up to four warps,
-  // then four, whose loads are in flight together, then eight in 512 threads. mxfp4's blocks have twice the values.
-  const int bpl = FMT == DSPARK_NVFP4 ? (nb <= 128 ? 1 : nb <= 2048 ? 4 : 8) : (nb <= 1024 ? 1 : 2);
+  // An nvfp4 row belongs to one CTA (its largest value goes into every scale): four blocks a thread, whose loads are
+  // in flight together (129280 rows of 256: 20.6 us with one, 15.6 with four), one where that leaves SMs without work,
+  // five where those fit the row (320 blocks: 346 us with four, of which one in six is idle, 300 with five), eight past 2048 blocks. mxfp4's
+  // blocks have twice the values.
+  const bool few = (int64_t)a.rows * nb < 152 * 2048;
+  const int bpl = FMT == DSPARK_NVFP4 ? (nb <= 512 && few ? 1 : nb > 2048 ? 8 : nb % 160 == 0 ? 5 : 4) : (nb <= 1024 ? 1 : 2);
   int lanes = 4;
   if (nb > 32 * bpl) {
     lanes = (nb + 32 * bpl - 1) / (32 * bpl) * 32;
@@ -326,8 +325,10 @@ cudaError_t quant(QuArgs a, cudaStream_t st) {
   const int64_t rows_up = ((int64_t)a.rows + kRows - 1) / kRows * kRows;
   const dim3 grid((unsigned)((rows_up + a.per_cta - 1) / a.per_cta)), block(lanes * a.per_cta);
   constexpr int kMore = FMT == DSPARK_NVFP4 ? 4 : 2, kMost = FMT == DSPARK_NVFP4 ? 8 : 2;
+  constexpr int kFive = FMT == DSPARK_NVFP4 ? 5 : 2;
   return launch_ex(bpl == 1       ? k_fp4_quant<T, FMT, 1>
                    : bpl == kMore ? k_fp4_quant<T, FMT, kMore>
+                   : bpl == kFive ? k_fp4_quant<T, FMT, kFive>
                                   : k_fp4_quant<T, FMT, kMost>,
                    grid, block, 0, st, true, a);
 }
@@ -391,8 +392,9 @@ extern "C" dspark_status dspark_fp4_rows(const dspark_fp4_dims* d, const dspark_
   a.vec = on_16(out, ldo, type);
   a.status = device_status;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  while (a.shift < 8 && (8 << a.shift) < d->K) ++a.shift;
-  const bool wide = d->K > 8 * 256;
+  const int vals = type == DSPARK_BF16 ? 8 : 4;
+  while (a.shift < 8 && (vals << a.shift) < d->K) ++a.shift;
+  const bool wide = d->K > vals * 256;
   const int per = wide ? 1 : (256 >> a.shift) * kRoEach;
   const dim3 grid((unsigned)((N + per - 1) / per)), block(256);
   typedef __nv_bfloat16 bf;
