@@ -81,8 +81,8 @@ struct SpCut {
   int last;  // of the tokens with this z, those up to this index are kept
 };
 
-struct SpShared {
-  uint2 exp2[16];              // kSpExp2 as a whole number and as fp32
+struct alignas(128) SpShared {
+  uint2 exp2[16];              // kSpExp2 as a whole number and as fp32 (its address has no bits below 128)
   u64 slot[2][kSpMaxC][2];     // what each CTA tells the others
   u64 res[2];                  // a cut and the raw sum of its bin up to it
   u64 found[3];                // a search's bin, the sum before it and what is missing in it
@@ -133,6 +133,15 @@ __device__ __forceinline__ void add_if(uint32_t p, uint32_t x, float v, float cu
       "r"(x), "f"(v), "f"(cut), "r"(t), "r"(low), "n"(kSpBins * 4)
       : "memory");
 }
+// The same where t > low alone.
+__device__ __forceinline__ void add_over(uint32_t p, uint32_t x, int t, int low) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .u32 l, h;\n setp.gt.s32 p, %2, %3;\n"
+      " and.b32 l, %1, 65535;\n shr.u32 h, %1, 16;\n @p red.shared.add.u32 [%0], l;\n"
+      " @p red.shared.add.u32 [%0 + %4], h;\n}" ::"r"(p),
+      "r"(x), "r"(t), "r"(low), "n"(kSpBins * 4)
+      : "memory");
+}
 // The same of any many numbers, 32 bits in the lower word: a carry goes to the upper one.
 __device__ __forceinline__ void add_carry(uint32_t p, uint32_t x) {
   uint32_t old;
@@ -163,15 +172,16 @@ struct Mass {
     const uint32_t tq = t & ~1u;
     float r = fmaf(x, s.hi, fmaf(__uint_as_float(tq), -1.f, s.mb));
     r = fmaf(x, lo, r);
-    const uint2 w = lds64(tab + (tq << 2 & 0x78u));
+    const uint2 w = lds64(tab | (tq << 2 & 0x78u));
     uint32_t mant;
     poly(r, __uint_as_float(w.y), w.x, mant);
     J = (int)(t - kSpMagicBits);
     return mant;
   }
   // the same of two tokens; t: the bits of kSpMagic + J
+  template <bool FAR>
   __device__ __forceinline__ void two(float z0, float z1, uint32_t tab, uint32_t* t, uint32_t* mant) const {
-    const u64 x = tc::add2(tc::f2pack(z0, z1), tc::f2pack(-s.sub, -s.sub));
+    const u64 x = FAR ? tc::add2(tc::f2pack(z0, z1), tc::f2pack(-s.sub, -s.sub)) : tc::f2pack(z0, z1);
     const u64 hi = tc::f2pack(s.hi, s.hi), mb = tc::f2pack(s.mb, s.mb);
     float a, b;
     tc::f2unpack(tc::fma2(x, hi, mb), a, b);
@@ -186,7 +196,7 @@ struct Mass {
     p = tc::fma2(r, p, tc::f2pack(0.0216608494f, 0.0216608494f));
     p = tc::mul2(r, p);
     tc::f2unpack(p, a, b);
-    const uint2 w0 = lds64(tab + (q0 << 2 & 0x78u)), w1 = lds64(tab + (q1 << 2 & 0x78u));
+    const uint2 w0 = lds64(tab | (q0 << 2 & 0x78u)), w1 = lds64(tab | (q1 << 2 & 0x78u));
     mant[0] = w0.x + (uint32_t)__float2int_rn(__uint_as_float(w0.y) * a);
     mant[1] = w1.x + (uint32_t)__float2int_rn(__uint_as_float(w1.y) * b);
   }
@@ -468,6 +478,47 @@ struct Row {
     return true;
   }
 
+  // Lists a token of the part.
+  __device__ __forceinline__ void note(u64* list, int room, float z, int l) {
+    const int n = atomicAdd(&sh.n, 1);
+    if (n < room) list[n] = (u64)~ordered(z) << 32 | (uint32_t)(start + l);
+  }
+
+  // Greedy: the cut is the lowest token of the row's maximum.
+  __device__ void first_max() {
+    if (tid == 0) {
+      sh.n = 0x7FFFFFFF;
+      sh.m = 0;
+    }
+    __syncthreads();
+    each([&](const float* v, int ch, int h) {
+      uint32_t hits = 0;
+#pragma unroll
+      for (int i = 0; i < kStep; ++i)
+        if (v[i] == m) hits |= 1u << i;
+      for (; hits; hits &= hits - 1) {
+        atomicMin(&sh.n, start + at(ch, h, __ffs((int)hits) - 1));
+        atomicAdd(&sh.m, 1);
+      }
+    });
+    __syncthreads();
+    const u64(*s)[2] = tell((u64)(uint32_t)sh.n, (u64)(uint32_t)sh.m);
+    u64 first = ~0ull, equals = 0;
+    for (uint32_t c = 0; c < C; ++c) {
+      first = min(first, s[c][0]);
+      equals += s[c][1];
+    }
+    cut = SpCut{m, (int)first};
+    if (RES && equals > 1) {
+      each([&](const float* v, int ch, int h) {
+#pragma unroll
+        for (int i = 0; i < kStep; ++i)
+          if (v[i] == m && start + at(ch, h, i) > cut.last) part[at(ch, h, i)] = T(-INFINITY);
+      });
+      __syncthreads();
+    }
+  }
+
   // Tightens the cut to the first of the kept tokens, in order, at which the running
   // count (MASS: mass) reaches the target. The last bin takes in what lies below the others (its masses
   // are added as multiples of 2^-q).
@@ -478,34 +529,47 @@ struct Row {
     clear(kSpBins);
     if (tid == 0) sh.n = 0;
     u64 light = 0;
-    each([&](const float* v, int ch, int h) {
-      uint32_t t[kStep], mant[kStep];
-      if (MASS) {
-        // what lies between kLow and nothing, as one comparison of unsigned numbers
-        constexpr uint32_t kNone = kSpMagicBits - kSpNone;
-        uint32_t least = ~0u;
+    // what lies between kLow and nothing is one comparison of unsigned numbers
+    constexpr uint32_t kNone = kSpMagicBits - kSpNone;
+    auto lightest = [&](const float* v, const uint32_t* t, const uint32_t* mant, int ch, int h) {
+      uint32_t least = ~0u;
 #pragma unroll
-        for (int i = 0; i < kStep; i += 2) {
-          mass.two(v[i], v[i + 1], tab, t + i, mant + i);
-          least = min(least, min(t[i] - kNone, t[i + 1] - kNone));
-        }
+      for (int i = 0; i < kStep; i += 2) least = min(least, min(t[i] - kNone, t[i + 1] - kNone));
+      if (least <= (uint32_t)kLow - kNone) {
+#pragma unroll
+        for (int i = 0; i < kStep; ++i)
+          if ((int)t[i] <= kLow && kept(v[i], at(ch, h, i))) light += weigh(mant[i], (int)t[i]);
+      }
+    };
+    if (!MASS) {
+      each([&](const float* v, int ch, int h) {
+#pragma unroll
+        for (int i = 0; i < kStep; ++i)
+          count_if(hist + 4u * kSpMagicBits - 4u * (uint32_t)max(bits_of(v[i]), kLow), kept(v[i], at(ch, h, i)));
+      });
+    } else if (RES && b.sub == 0.f && cut.z == kSpLowest) {  // masked tokens lie below the bins
+      each([&](const float* v, int ch, int h) {
+        uint32_t t[kStep], mant[kStep];
+#pragma unroll
+        for (int i = 0; i < kStep; i += 2) mass.template two<false>(v[i], v[i + 1], tab, t + i, mant + i);
+#pragma unroll
+        for (int i = 0; i < kStep; ++i) add_over(hist + 4u * kSpMagicBits - 4u * t[i], mant[i], (int)t[i], kLow);
+        lightest(v, t, mant, ch, h);
+      });
+    } else {
+      each([&](const float* v, int ch, int h) {
+        uint32_t t[kStep], mant[kStep];
+#pragma unroll
+        for (int i = 0; i < kStep; i += 2) mass.template two<true>(v[i], v[i + 1], tab, t + i, mant + i);
 #pragma unroll
         for (int i = 0; i < kStep; ++i) {
           const uint32_t p = hist + 4u * kSpMagicBits - 4u * t[i];
           if (RES) add_if(p, mant[i], v[i], cut.z, (int)t[i], kLow);
           else if ((int)t[i] > kLow && kept(v[i], at(ch, h, i))) add_carry(p, mant[i]);
         }
-        if (least <= (uint32_t)kLow - kNone) {
-#pragma unroll
-          for (int i = 0; i < kStep; ++i)
-            if ((int)t[i] <= kLow && kept(v[i], at(ch, h, i))) light += weigh(mant[i], (int)t[i]);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < kStep; ++i)
-          count_if(hist + 4u * kSpMagicBits - 4u * (uint32_t)max(bits_of(v[i]), kLow), kept(v[i], at(ch, h, i)));
-      }
-    });
+        lightest(v, t, mant, ch, h);
+      });
+    }
     if (MASS) {
       light = warp_sum64(light);
       if (lane == 0 && light) {
@@ -525,28 +589,28 @@ struct Row {
     // the CTA's tokens of the bin, into the half of the histogram's lower words that find() leaves alone
     const int at0 = bin < kSpBins / 2 ? kSpBins / 2 * 4 : 0;
     u64* list = reinterpret_cast<u64*>(buf + at0);
-    auto gather = [&](const float* v, int ch, int h) {
-#pragma unroll
-      for (int i = 0; i < kStep; ++i) {
-        if (inside(v[i]) && kept(v[i], at(ch, h, i))) {
-          const int n = atomicAdd(&sh.n, 1);
-          if (n < kSpOwn) list[n] = (u64)~ordered(v[i]) << 32 | (uint32_t)(start + at(ch, h, i));
-        }
-      }
-    };
     if (low) {
-      each(gather);
+      each([&](const float* v, int ch, int h) {
+#pragma unroll
+        for (int i = 0; i < kStep; ++i)
+          if (inside(v[i]) && kept(v[i], at(ch, h, i))) note(list, kSpOwn, v[i], at(ch, h, i));
+      });
     } else {
       const u64 sub = tc::f2pack(-b.sub, -b.sub), up = tc::f2pack(b.hi, b.hi), mb = tc::f2pack(b.mb, b.mb);
       each([&](const float* v, int ch, int h) {
-        bool some = false;
+        uint32_t hits = 0;
 #pragma unroll
         for (int i = 0; i < kStep; i += 2) {
           float x, y;
           tc::f2unpack(tc::fma2(tc::add2(tc::f2pack(v[i], v[i + 1]), sub), up, mb), x, y);
-          some |= __float_as_int(x) == bits || __float_as_int(y) == bits;
+          if (__float_as_int(x) == bits) hits |= 1u << i;
+          if (__float_as_int(y) == bits) hits |= 2u << i;
         }
-        if (some) gather(v, ch, h);
+        for (; hits; hits &= hits - 1) {
+          const int l = at(ch, h, __ffs((int)hits) - 1);
+          const float z = value(l);
+          if (kept(z, l)) note(list, kSpOwn, z, l);
+        }
       });
     }
     __syncthreads();
@@ -779,7 +843,7 @@ struct Row {
 #pragma unroll
     for (int i = 0; i < kStep; i += 2) {
       uint32_t t[2], mant[2];
-      mass.two(v[i], v[i + 1], tab, t, mant);
+      mass.two<true>(v[i], v[i + 1], tab, t, mant);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const u64 w = weigh(mant[k], (int)t[k]);
@@ -950,15 +1014,18 @@ __global__ void __launch_bounds__(kSpThreads, 3) k_sample(SpArgs a) {
     w.mass.lo = sh.c_lo;
   }
 
-  if (sh.k > 0 && sh.k < a.V) {
+  const bool greedy = sh.k == 1;
+  if (greedy) {
+    w.first_max();
+  } else if (sh.k > 0 && sh.k < a.V) {
     // bins up to four times the mean distance from the maximum: half of the tokens lie within two
     const float mean = top - sum / fmaxf(seen, 1.f);
     const float beta = mean > 0.f ? fminf(kSpBins / (4.f * mean), 1e30f) : 0.f;
     w.template select<false>((u64)sh.k, SpScale{top, beta, kSpMagic});
   }
-  if (sh.p < 1.f) w.template select<true>(0, w.mass.s);
-  bool exact = sh.p < 1.f;  // held is the kept mass
-  if (t_log > -INFINITY) {
+  bool exact = !greedy && sh.p < 1.f;  // held is the kept mass
+  if (exact) w.template select<true>(0, w.mass.s);
+  if (!greedy && t_log > -INFINITY) {
     const float z = __double2float_ru((double)top + t_log);
     if (z > w.cut.z) {
       w.cut = SpCut{z, 0x7FFFFFFF};
