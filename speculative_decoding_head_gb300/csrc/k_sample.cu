@@ -613,17 +613,9 @@ struct Row {
         }
       });
     }
-    __syncthreads();
-    if (tid < (int)C) st_rank(&sh.counts[rank], tid, sh.n);
-    tc::cluster_sync();
-    int n = 0;
-    bool few = true;
-    for (uint32_t c = 0; c < C; ++c) {
-      n += sh.counts[c];
-      few &= sh.counts[c] <= kSpOwn;
-    }
-    few &= n <= kSpList;
-    if (few) {
+    int n;
+    const bool fit = lists_fit(kSpOwn, n);
+    if (fit) {
       if (rank == 0) cut_of_list<MASS>(n, goal, hist + at0);
     } else {
       narrow<MASS>(inside, goal);
@@ -632,7 +624,7 @@ struct Row {
     cut.z = unordered((uint32_t)(sh.res[0] >> 32));
     cut.last = (int)(uint32_t)sh.res[0];
     if (MASS) held = before + (low ? sh.res[1] : scaled(sh.res[1], e, a.q));
-    if (RES && !few) {  // cut_of_list has masked the others
+    if (RES && !fit) {  // settle() has masked the others
       each([&](const float* v, int ch, int h) {
 #pragma unroll
         for (int i = 0; i < kStep; ++i)
@@ -659,11 +651,9 @@ struct Row {
     }
   }
 
-  // In CTA 0: keys (falling z, index) in any order, each CTA's at its shared address `at`.
-  template <bool MASS>
-  __device__ void cut_of_list(int n, u64 goal, uint32_t at) {
-    constexpr int kOf = (kSpList + kSpThreads - 1) / kSpThreads;
-    u64 key[kOf];
+  static constexpr int kOf = (kSpList + kSpThreads - 1) / kSpThreads;  // listed tokens of a thread of CTA 0
+  // In CTA 0: the keys (falling z, index) that the CTAs have listed, in any order, each at its shared address `at`.
+  __device__ __forceinline__ uint32_t take_list(u64 (&key)[kOf], int n, uint32_t at) {
     uint32_t live = 0;
 #pragma unroll
     for (int i = 0; i < kOf; ++i) {
@@ -676,6 +666,13 @@ struct Row {
         live |= 1u << i;
       }
     }
+    return live;
+  }
+  // The first of the live keys, in order, at which the running sum of weight(key) reaches the goal, in bcast[0] and
+  // returned, and the sum there: 256 bins of the keys' range, again and again until 32 are left.
+  template <typename W>
+  __device__ u64 reach(const u64 (&key)[kOf], uint32_t live, W weight, u64 goal, u64& sum) {
+    u64* bins = reinterpret_cast<u64*>(buf);
     u64 base = 0;
     for (;;) {
       u64 least = ~0ull, most = 0;
@@ -696,18 +693,19 @@ struct Row {
         sh.warp2[warp] = most;
       }
       if (tid == 0) sh.m = 0;
-      clear(kSpThreads);
+      bins[tid] = 0;
+      __syncthreads();
 #pragma unroll
       for (int i = 0; i < kSpWarps; ++i) {
         least = min(least, sh.warp[i]);
         most = max(most, sh.warp2[i]);
       }
-      const int shift = max(0, 64 - __clzll(most - least) - 8);  // 256 bins
+      const int shift = max(0, 64 - __clzll(most - least) - 8);
 #pragma unroll
       for (int i = 0; i < kOf; ++i)
-        if (live >> i & 1) add<MASS>((int)((key[i] - least) >> shift), raw<MASS>(key[i]));
+        if (live >> i & 1) atomicAdd(bins + (int)((key[i] - least) >> shift), weight(key[i]));
       __syncthreads();
-      const u64 here = (u64)lo()[tid] + ((u64)hi()[tid] << kUp);
+      const u64 here = bins[tid];
       u64 before;
       block_scan(here, before);
       before += base;
@@ -732,20 +730,25 @@ struct Row {
     }
     if (warp == 0) {
       const u64 mine = lane < sh.m ? sh.few[lane] : ~0ull;
-      const u64 w = lane < sh.m ? raw<MASS>(mine) : 0;
-      u64 sum = base;
+      const u64 w = lane < sh.m ? weight(mine) : 0;
+      u64 t = base;
       for (int i = 0; i < sh.m; ++i) {
         const u64 other = __shfl_sync(0xFFFFFFFFu, mine, i), ow = __shfl_sync(0xFFFFFFFFu, w, i);
-        if (other < mine) sum += ow;
+        if (other < mine) t += ow;
       }
-      if (lane < sh.m && sum < goal && sum + w >= goal) {
-        answer(mine, sum + w);
+      if (lane < sh.m && t < goal && t + w >= goal) {
         sh.bcast[0] = mine;
+        sh.bcast[1] = t + w;
       }
     }
     __syncthreads();
-    if (RES) {  // equals of the cut that come after it
-      const u64 end = sh.bcast[0];
+    sum = sh.bcast[1];
+    return sh.bcast[0];
+  }
+  // CTA 0's answer to all: the cut, and the sum up to it. Listed equals of the cut that come after it are masked.
+  __device__ __forceinline__ void settle(const u64 (&key)[kOf], int n, u64 end, u64 sum) {
+    if (tid == 0) answer(end, sum);
+    if (RES) {
 #pragma unroll
       for (int i = 0; i < kOf; ++i)
         if (tid + i * kSpThreads < n && key[i] > end && key[i] >> 32 == end >> 32) {
@@ -758,6 +761,95 @@ struct Row {
             asm volatile("st.shared::cluster.u16 [%0], %1;" ::"r"(p), "h"((unsigned short)0xFF80u) : "memory");
         }
     }
+  }
+  // Every CTA's list is complete: their lengths to all. Returns whether they fit, and how many there are.
+  __device__ __forceinline__ bool lists_fit(int room, int& n) {
+    __syncthreads();
+    if (tid < (int)C) st_rank(&sh.counts[rank], tid, sh.n);
+    tc::cluster_sync();
+    n = 0;
+    bool few = true;
+    for (uint32_t c = 0; c < C; ++c) {
+      n += sh.counts[c];
+      few &= sh.counts[c] <= room;
+    }
+    return few && n <= kSpList;
+  }
+  template <bool MASS>
+  __device__ void cut_of_list(int n, u64 goal, uint32_t at) {
+    u64 key[kOf], sum;
+    const uint32_t live = take_list(key, n, at);
+    const u64 end = reach(key, live, [&](u64 k) { return (u64)raw<MASS>(k); }, goal, sum);
+    settle(key, n, end, sum);
+  }
+
+  // top-k and top-p of rows of which few tokens are kept, without looking at all of them twice: the k-th largest of
+  // the threads' maxima (`mine`) is at most the k-th largest token, so what is not below its bin holds all that is kept; on
+  // flat rows a tenth more than k tokens. Those are listed, and one CTA finds both cuts. Returns false, with nothing
+  // changed, where they do not fit a list.
+  __device__ bool few(int k, const SpScale& b, float mine) {
+    auto bits_of = [&](float z) { return __float_as_int(fmaf(z - b.sub, b.hi, b.mb)); };
+    clear(kSpBins);
+    if (tid == 0) sh.n = 0;
+    const int t = max(bits_of(mine), (int)kSpMagicBits - (kSpBins - 1));
+    if (mine > -INFINITY) add<false>((int)kSpMagicBits - t, 1);
+    u64 target = (u64)k, goal, before;
+    int bin;
+    if (!find<false>(target, goal, before, bin)) return false;
+    if (bin == kSpBins - 1) {
+      tc::cluster_sync();  // the histogram has been read
+      return false;
+    }
+    const int bits = (int)kSpMagicBits - bin;
+    const int at0 = bin < kSpBins / 2 ? kSpBins / 2 * 4 : 0;  // away from what find() reads
+    u64* list = reinterpret_cast<u64*>(buf + at0);
+    const u64 sub = tc::f2pack(-b.sub, -b.sub), up = tc::f2pack(b.hi, b.hi), mb = tc::f2pack(b.mb, b.mb);
+    each([&](const float* v, int ch, int h) {
+      uint32_t hits = 0;
+#pragma unroll
+      for (int i = 0; i < kStep; i += 2) {
+        float x, y;
+        tc::f2unpack(tc::fma2(tc::add2(tc::f2pack(v[i], v[i + 1]), sub), up, mb), x, y);
+        if (__float_as_int(x) >= bits) hits |= 1u << i;
+        if (__float_as_int(y) >= bits) hits |= 2u << i;
+      }
+      for (; hits; hits &= hits - 1) {
+        const int l = at(ch, h, __ffs((int)hits) - 1);
+        note(list, kSpOwn, value(l), l);
+      }
+    });
+    int n;
+    if (!lists_fit(kSpOwn, n)) {
+      tc::cluster_sync();  // the lengths have been read
+      return false;
+    }
+    if (rank == 0) {
+      u64 key[kOf], sum;
+      uint32_t live = take_list(key, n, hist + at0);
+      u64 end = reach(key, live, [](u64) { return 1ull; }, (u64)k, sum);
+      auto mass_of = [&](u64 x) {
+        int J;
+        const uint32_t mant = mass.one(unordered(~(uint32_t)(x >> 32)), tab, J);
+        return weigh(mant, J + (int)kSpMagicBits);
+      };
+      u64 all = 0, ignored;
+#pragma unroll
+      for (int i = 0; i < kOf; ++i) {
+        if (key[i] > end) live &= ~(1u << i);
+        if (live >> i & 1) all += mass_of(key[i]);
+      }
+      sum = block_scan(all, ignored);
+      if (sh.p < 1.f) {
+        const u64 goal2 = max(mul_floor(sum, sh.p, true), 1ull);
+        end = reach(key, live, mass_of, goal2, sum);
+      }
+      settle(key, n, end, sum);
+    }
+    tc::cluster_sync();
+    cut.z = unordered((uint32_t)(sh.res[0] >> 32));
+    cut.last = (int)(uint32_t)sh.res[0];
+    held = sh.res[1];
+    return true;
   }
 
   // The same of a bin with many tokens, by the bits of z, eight at a time, then by index among equals.
@@ -962,6 +1054,7 @@ __global__ void __launch_bounds__(kSpThreads, 3) k_sample(SpArgs a) {
       seen += 1.f;
     }
   }
+  const float mine = top;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
   sum = warp_sum(sum);
@@ -1014,17 +1107,30 @@ __global__ void __launch_bounds__(kSpThreads, 3) k_sample(SpArgs a) {
     w.mass.lo = sh.c_lo;
   }
 
+  bool exact = false;  // held is the kept mass
   const bool greedy = sh.k == 1;
   if (greedy) {
     w.first_max();
-  } else if (sh.k > 0 && sh.k < a.V) {
-    // bins up to four times the mean distance from the maximum: half of the tokens lie within two
-    const float mean = top - sum / fmaxf(seen, 1.f);
-    const float beta = mean > 0.f ? fminf(kSpBins / (4.f * mean), 1e30f) : 0.f;
-    w.template select<false>((u64)sh.k, SpScale{top, beta, kSpMagic});
+  } else {
+    bool cut_p = sh.p < 1.f;
+    if (sh.k > 0 && sh.k < a.V) {
+      // bins up to four times the mean distance from the maximum: half of the tokens lie within two
+      const float mean = top - sum / fmaxf(seen, 1.f);
+      const float beta = mean > 0.f ? fminf(kSpBins / (4.f * mean), 1e30f) : 0.f;
+      const SpScale b{top, beta, kSpMagic};
+      // a quarter as many tokens as threads: 1.15 listed for each
+      if (sh.k <= (int)w.C * kSpThreads / 4 && w.few(sh.k, b, mine)) {
+        exact = true;
+        cut_p = false;
+      } else {
+        w.template select<false>((u64)sh.k, b);
+      }
+    }
+    if (cut_p) {
+      w.template select<true>(0, w.mass.s);
+      exact = true;
+    }
   }
-  bool exact = !greedy && sh.p < 1.f;  // held is the kept mass
-  if (exact) w.template select<true>(0, w.mass.s);
   if (!greedy && t_log > -INFINITY) {
     const float z = __double2float_ru((double)top + t_log);
     if (z > w.cut.z) {
