@@ -929,27 +929,39 @@ struct Row {
     const float b = kSpMagic - mass.s.mb, x = m - mass.s.sub;
     return -(fmaf(x, mass.s.hi, -b) + x * mass.lo) * 0.0216608494f;  // ln(2) / 32
   }
-  // The kept mass of a step, a multiple of 2^-q.
-  __device__ __forceinline__ u64 sum_of(const float* v, int ch, int h) const {
-    u64 sum = 0;
+  // The kept mass of a lane's tokens of a step: mants times 2^(q-30-e), added up in two words, of those where that is
+  // whole and of the others, times 2^29 (which leaves out what is below 2^-(q-2)). lane_sum() rounds a
+  // chunk's together.
+  __device__ __forceinline__ void sum_of(const float* v, int ch, int h, u64& heavy, u64& light) const {
 #pragma unroll
     for (int i = 0; i < kStep; i += 2) {
       uint32_t t[2], mant[2];
-      mass.two<true>(v[i], v[i + 1], tab, t, mant);
+      mass.template two<true>(v[i], v[i + 1], tab, t, mant);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const u64 w = weigh(mant[k], (int)t[k]);
-        if (kept(v[i + k], at(ch, h, i + k))) sum += w;
+        const int n = ((int)t[k] >> 5) - (int)(kSpMagicBits >> 5) + a.q - 30;
+        uint32_t mult;  // 0 for masked tokens and for those that are nothing
+        asm("shl.b32 %0, 1, %1;" : "=r"(mult) : "r"(n >= 0 ? n : n + 29));
+        if (!kept(v[i + k], at(ch, h, i + k))) mult = 0;
+        if (n >= 0) heavy += (u64)mant[k] * mult;
+        else light += (u64)mant[k] * mult;
       }
     }
-    return sum;
   }
+  __device__ __forceinline__ u64 lane_sum(u64 heavy, u64 light) const { return heavy + ((light + (1ull << 28)) >> 29); }
   // Of most rows few tokens are kept: steps without any are passed over.
-  __device__ __forceinline__ u64 sum_kept(const float* v, int ch, int h) const {
-    float top = v[0];
+  __device__ __forceinline__ u64 sum_kept(int ch) const {
+    u64 heavy = 0, light = 0;
+#pragma unroll 1
+    for (int h = 0; h < kSpChunk / (32 * kStep); ++h) {
+      float v[kStep];
+      values(ch, h, v);
+      float top = v[0];
 #pragma unroll
-    for (int i = 1; i < kStep; ++i) top = fmaxf(top, v[i]);
-    return __any_sync(0xFFFFFFFFu, top >= cut.z) ? sum_of(v, ch, h) : 0;
+      for (int i = 1; i < kStep; ++i) top = fmaxf(top, v[i]);
+      if (__any_sync(0xFFFFFFFFu, top >= cut.z)) sum_of(v, ch, h, heavy, light);
+    }
+    return lane_sum(heavy, light);
   }
   // The same of one token: mant 2^(q-30-e), rounded. t: the bits of kSpMagic + J. One product serves both
   // ways: by 2^(q-30-e) where that is whole, else by 2^32 times it, whose upper word is the result.
@@ -1143,7 +1155,7 @@ __global__ void __launch_bounds__(kSpThreads, 3) k_sample(SpArgs a) {
     u64 S = w.held;
     if (!exact) {
       u64 t = 0, ignored;
-      w.each([&](const float* v, int ch, int h) { t += w.sum_kept(v, ch, h); });
+      for (int ch = w.warp; ch < w.chunks; ch += kSpWarps) t += w.sum_kept(ch);
       const u64 mine = w.block_scan(t, ignored);
       const u64(*s)[2] = w.tell(mine, 0);
       S = 0;
@@ -1171,13 +1183,7 @@ __global__ void __launch_bounds__(kSpThreads, 3) k_sample(SpArgs a) {
   } else {
     u64* chunk = reinterpret_cast<u64*>(w.buf);
     for (int ch = w.warp; ch < w.chunks; ch += kSpWarps) {
-      u64 t = 0;
-#pragma unroll 1
-      for (int h = 0; h < 2; ++h) {
-        float v[R::kStep];
-        w.values(ch, h, v);
-        t += w.sum_kept(v, ch, h);
-      }
+      u64 t = w.sum_kept(ch);
       t = warp_sum64(t);
       if (w.lane == 0) chunk[ch] = t;
     }
@@ -1217,10 +1223,11 @@ __global__ void __launch_bounds__(kSpThreads, 3) k_sample(SpArgs a) {
         own[i] = w.kept(z, l) ? w.weigh(mant, J + (int)kSpMagicBits) : 0;
         sum += own[i];
       }
-      w.block_scan(sum, y);
+      // the chunk's sum may be a few units more than its tokens', each rounded by itself
+      const u64 rest2 = min(rest, w.block_scan(sum, y) - 1);
 #pragma unroll
       for (int i = 0; i < kOwn; ++i) {
-        if (rest >= y && rest < y + own[i]) {
+        if (rest2 >= y && rest2 < y + own[i]) {
           const int l = ch * kSpChunk + tid * kOwn + i;
           a.token[n] = w.start + l;
           if (a.logp) a.logp[n] = (w.value(l) - top) * sh.inv_t - (logf((float)S * exp2f(-(float)a.q)) + w.offset());
