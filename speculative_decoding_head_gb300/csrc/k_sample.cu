@@ -44,8 +44,8 @@ constexpr int kSpSeg = kSpBins / 8;
 constexpr int kSpList = kSpBins;      // tokens of a bin that are brought together,
 constexpr int kSpOwn = kSpSeg * 4 / 2; // and of one CTA: half of the histogram's lower words
 constexpr int kSpChunk = 512;     // tokens that a warp takes at a time
-constexpr float kSpMasked = -1e29f;
-constexpr float kSpLowest = -3.402823466e38f;
+constexpr float kSpMasked = -1e29f;      // masked tokens are at most this,
+constexpr float kSpLeast = -9.9999994e28f;  // the others at least this
 constexpr int kSpHist = kSpBins * 8;  // bytes: the histogram, the list or the chunks' sums
 constexpr float kSpMagic = 12582912.f;     // 1.5 * 2^23: sums with it round to whole numbers
 constexpr uint32_t kSpMagicBits = 0x4B400000u;
@@ -246,9 +246,20 @@ __device__ __forceinline__ u64 warp_scan64(u64 x) {  // inclusive
   }
   return x;
 }
-__device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
+// maxima that are NaN if one of their inputs is
+__device__ __forceinline__ float max_nan(float a, float b) {
   float d;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ uint32_t max_nan2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
 // floor(x a) and ceil(x a) for 0 <= a < 1
@@ -272,9 +283,6 @@ template <>
 __device__ __forceinline__ float up<__nv_bfloat16>(__nv_bfloat16 x) {
   return __bfloat162float(x);
 }
-// masked tokens are -inf
-__device__ __forceinline__ float clean(float z) { return z <= kSpMasked ? -INFINITY : z; }
-
 // One row's work in one CTA. RES: its part lies in shared memory.
 template <typename T, bool RES>
 struct Row {
@@ -294,7 +302,7 @@ struct Row {
   Mass mass;
   u64 held = 0;              // the mass up to the cut of a search for masses
   bool low_mass = false;     // the search is in the last bin
-  SpCut cut{kSpLowest, 0x7FFFFFFF};
+  SpCut cut{kSpLeast, 0x7FFFFFFF};
 
   __device__ Row(const SpArgs& a_, SpShared& s_) : a(a_), sh(s_) {}
 
@@ -307,38 +315,38 @@ struct Row {
 #pragma unroll
     for (int i = 0; i < kPer; ++i) v[i] = up<T>(t[i]);
   }
-  // 8 tokens of a lane, from global memory; past the end -inf
-  __device__ __forceinline__ void fetch_full(int ch, int h, float* v) const {
+  // A lane's tokens of a chunk, from global memory; past the end -inf.
+  template <int WORDS>
+  __device__ __forceinline__ void fetch(int ch, uint4 (&q)[WORDS], int h = 0) const {
+    if (a.vec && (ch + 1) * kSpChunk <= count) {
 #pragma unroll
-    for (int g = 0; g < kStep / kPer; ++g)
-      unpack(__ldg(reinterpret_cast<const uint4*>(row + start + at(ch, h, g * kPer))), v + g * kPer);
-  }
-  __device__ __forceinline__ void fetch(int ch, int h, float* v) const {
+      for (int g = 0; g < WORDS; ++g)
+        q[g] = __ldg(reinterpret_cast<const uint4*>(row + start + at(ch, h, 0) + g * (32 * kPer)));
+    } else {
 #pragma unroll
-    for (int g = 0; g < kStep / kPer; ++g) {
-      const int l = at(ch, h, g * kPer);
-      if (a.vec && l + kPer <= count) {
-        unpack(__ldg(reinterpret_cast<const uint4*>(row + start + l)), v + g * kPer);
-      } else {
+      for (int g = 0; g < WORDS; ++g) {
+        T t[kPer];
+        const int l = at(ch, h, 0) + g * (32 * kPer);
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) v[g * kPer + i] = l + i < count ? up<T>(row[start + l + i]) : -INFINITY;
+        for (int i = 0; i < kPer; ++i) t[i] = l + i < count ? row[start + l + i] : T(-INFINITY);
+        q[g] = *reinterpret_cast<const uint4*>(t);
       }
     }
   }
   __device__ __forceinline__ void values(int ch, int h, float* v) const {
+    uint4 q[kStep / kPer];
     if (RES) {
 #pragma unroll
-      for (int g = 0; g < kStep / kPer; ++g)
-        unpack(lds128(data + (uint32_t)(at(ch, h, g * kPer) * (int)sizeof(T))), v + g * kPer);
+      for (int g = 0; g < kStep / kPer; ++g) q[g] = lds128(data + (uint32_t)(at(ch, h, g * kPer) * (int)sizeof(T)));
     } else {
-      fetch(ch, h, v);
-#pragma unroll
-      for (int i = 0; i < kStep; ++i) v[i] = clean(v[i]);
+      fetch(ch, q, h);
     }
+#pragma unroll
+    for (int g = 0; g < kStep / kPer; ++g) unpack(q[g], v + g * kPer);
   }
   __device__ __forceinline__ float value(int l) const {
     if (RES) return up<T>(part[l]);
-    return l < count ? clean(up<T>(row[start + l])) : -INFINITY;
+    return l < count ? up<T>(row[start + l]) : -INFINITY;
   }
   __device__ __forceinline__ bool kept(float z, int l) const {
     return RES ? z >= cut.z : z > cut.z || (z == cut.z && start + l <= cut.last);
@@ -547,7 +555,7 @@ struct Row {
         for (int i = 0; i < kStep; ++i)
           count_if(hist + 4u * kSpMagicBits - 4u * (uint32_t)max(bits_of(v[i]), kLow), kept(v[i], at(ch, h, i)));
       });
-    } else if (RES && b.sub == 0.f && cut.z == kSpLowest) {  // masked tokens lie below the bins
+    } else if (RES && b.sub == 0.f && cut.z == kSpLeast && b.hi > 1e-24f) {  // masked tokens lie below the bins
       each([&](const float* v, int ch, int h) {
         uint32_t t[kStep], mant[kStep];
 #pragma unroll
@@ -792,7 +800,7 @@ struct Row {
     clear(kSpBins);
     if (tid == 0) sh.n = 0;
     const int t = max(bits_of(mine), (int)kSpMagicBits - (kSpBins - 1));
-    if (mine > -INFINITY) add<false>((int)kSpMagicBits - t, 1);
+    if (mine > kSpMasked) add<false>((int)kSpMagicBits - t, 1);
     u64 target = (u64)k, goal, before;
     int bin;
     if (!find<false>(target, goal, before, bin)) return false;
@@ -1033,38 +1041,39 @@ __global__ void __launch_bounds__(kSpThreads, 3) k_sample(SpArgs a) {
     sh.k = k;
   }
 
-  // the row's part: to shared memory, its maximum on the way, and a sample of its logits
+  // the row's part: to shared memory, its maximum on the way, and a sample of its logits; eight loads of a lane in flight
   float top = -INFINITY, sum = 0.f, seen = 0.f;
-  for (int ch = w.warp; ch < w.chunks; ch += kSpWarps) {
-    float v[2][R::kStep];
-    if (a.vec && (ch + 1) * kSpChunk <= w.count) {
-      w.fetch_full(ch, 0, v[0]);
-      w.fetch_full(ch, 1, v[1]);
-    } else {
-      w.fetch(ch, 0, v[0]);
-      w.fetch(ch, 1, v[1]);
-    }
+  {
+    constexpr int kWords = kSpChunk / (32 * R::kPer), kBatch = 8 / kWords;
+    uint32_t pairs = 0xFF80FF80u;  // of bf16: the maximum of the even and of the odd places
+    for (int c0 = w.warp; c0 < w.chunks; c0 += kSpWarps * kBatch) {
+      uint4 q[kBatch][kWords];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+      for (int b = 0; b < kBatch; ++b)
+        if (c0 + b * kSpWarps < w.chunks) w.fetch(c0 + b * kSpWarps, q[b]);
 #pragma unroll
-      for (int i = 0; i < R::kStep; ++i) {
-        v[h][i] = clean(v[h][i]);
-        top = max_nan(top, v[h][i]);
-      }
-      if (RES) {
+      for (int b = 0; b < kBatch; ++b) {
+        const int ch = c0 + b * kSpWarps;
+        if (ch >= w.chunks) break;
 #pragma unroll
-        for (int g = 0; g < R::kStep / R::kPer; ++g) {
-          T t[R::kPer];
-#pragma unroll
-          for (int i = 0; i < R::kPer; ++i) t[i] = T(v[h][g * R::kPer + i]);
-          *reinterpret_cast<uint4*>(w.part + w.at(ch, h, g * R::kPer)) = *reinterpret_cast<const uint4*>(t);
+        for (int g = 0; g < kWords; ++g) {
+          const uint4 x = q[b][g];
+          if (sizeof(T) == 4) {
+            top = max_nan(top, __uint_as_float(x.x), __uint_as_float(x.y));
+            top = max_nan(top, __uint_as_float(x.z), __uint_as_float(x.w));
+          } else {
+            pairs = max_nan2(max_nan2(pairs, max_nan2(x.x, x.y)), max_nan2(x.z, x.w));
+          }
+          if (RES) *reinterpret_cast<uint4*>(w.part + w.at(ch, 0, 0) + g * (32 * R::kPer)) = x;
+        }
+        const float z = sizeof(T) == 4 ? __uint_as_float(q[b][0].x) : __uint_as_float(q[b][0].x << 16);
+        if (z > kSpMasked) {
+          sum += fmaxf(z, -1e4f);
+          seen += 1.f;
         }
       }
     }
-    if (v[0][0] > -INFINITY) {
-      sum += fmaxf(v[0][0], -1e4f);
-      seen += 1.f;
-    }
+    if (sizeof(T) == 2) top = max_nan(__uint_as_float(pairs << 16), __uint_as_float(pairs & 0xFFFF0000u));
   }
   const float mine = top;
 #pragma unroll
@@ -1096,7 +1105,7 @@ __global__ void __launch_bounds__(kSpThreads, 3) k_sample(SpArgs a) {
     }
   }
   bad |= !(top < INFINITY);
-  if (bad || top == -INFINITY) {
+  if (bad || top <= kSpMasked) {
     if (bad && w.rank == 0 && tid == 0) raise_status(a.status, DSPARK_ENUMERIC);
     if (DIST) {
       float* out = a.out + (int64_t)n * a.ldo + w.start;
