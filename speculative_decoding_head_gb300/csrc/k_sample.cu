@@ -417,7 +417,8 @@ struct Row {
   // count as multiples of 2^-q. target 0: ceil(p of all of it), at least 1. Returns whether the sum reaches the target at all.
   // Every CTA tells the others its sums of eight segments, so that all know the segment, and all look at its bins:
   // they are not to change before the cluster's next barrier.
-  template <bool OCT>
+  // HIGH: the bins have upper words.
+  template <bool OCT, bool HIGH>
   __device__ __forceinline__ bool find(u64& target, u64& goal, u64& before, int& bin) {
     constexpr int kEach = (kSpSeg + 31) / 32;
     auto value = [&](u64 v, int g) { return OCT && g < kSpBins - 1 ? scaled(v, octave(g), a.q) : v; };
@@ -427,7 +428,7 @@ struct Row {
 #pragma unroll
       for (int i = 0; i < kEach; ++i) {
         const int b = lane * kEach + i, g = warp * kSpSeg + b;
-        if (b < kSpSeg) sum += value((u64)lo()[g] + ((u64)hi()[g] << kUp), g);
+        if (b < kSpSeg) sum += value((u64)lo()[g] + (HIGH ? (u64)hi()[g] << kUp : 0), g);
       }
       sum = warp_sum64(sum);
       if (lane < (int)C) st_rank(&sh.segs[rank][warp], lane, sum);
@@ -458,16 +459,17 @@ struct Row {
     u64 raw = 0, mine;
     if (tid < kSpSeg) {
 #pragma unroll
-      for (uint32_t c0 = 0; c0 < kSpMaxC; c0 += 4) {
-        uint32_t l[4] = {}, h[4] = {};
+      for (uint32_t c0 = 0; c0 < kSpMaxC; c0 += 8) {
+        if (c0 >= C) break;
+        uint32_t l[8] = {}, h[8] = {};
 #pragma unroll
-        for (uint32_t c = 0; c < 4; ++c)
+        for (uint32_t c = 0; c < 8; ++c)
           if (c0 + c < C) {
             l[c] = ld_rank(hist + 4 * g, c0 + c);
-            h[c] = ld_rank(hist + 4 * (g + kSpBins), c0 + c);
+            if (HIGH) h[c] = ld_rank(hist + 4 * (g + kSpBins), c0 + c);
           }
 #pragma unroll
-        for (int c = 0; c < 4; ++c) raw += (u64)l[c] + ((u64)h[c] << kUp);
+        for (int c = 0; c < 8; ++c) raw += (u64)l[c] + ((u64)h[c] << kUp);
       }
     }
     const u64 x = value(raw, g);
@@ -588,7 +590,7 @@ struct Row {
     }
     u64 before, goal;
     int bin;
-    if (!find<MASS>(target, goal, before, bin)) return;
+    if (!find<MASS, MASS>(target, goal, before, bin)) return;
     const bool low = bin == kSpBins - 1;
     low_mass = MASS && low;
     const int e = octave(bin);
@@ -682,36 +684,36 @@ struct Row {
   __device__ u64 reach(const u64 (&key)[kOf], uint32_t live, W weight, u64 goal, u64& sum) {
     u64* bins = reinterpret_cast<u64*>(buf);
     u64 base = 0;
+    int up = 32;  // keys are told apart by their upper words, falling z, and those of one z by index
     for (;;) {
-      u64 least = ~0ull, most = 0;
+      uint32_t least = ~0u, most = 0;
 #pragma unroll
       for (int i = 0; i < kOf; ++i)
         if (live >> i & 1) {
-          least = min(least, key[i]);
-          most = max(most, key[i]);
+          least = min(least, (uint32_t)(key[i] >> up));
+          most = max(most, (uint32_t)(key[i] >> up));
         }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        least = min(least, __shfl_xor_sync(0xFFFFFFFFu, least, o));
-        most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
-      }
+      least = __reduce_min_sync(0xFFFFFFFFu, least);
+      most = __reduce_max_sync(0xFFFFFFFFu, most);
       __syncthreads();  // the list is in registers, and the last turn's words have been read
-      if (lane == 0) {
-        sh.warp[warp] = least;
-        sh.warp2[warp] = most;
-      }
+      if (lane == 0) sh.warp2[warp] = (u64)least << 32 | most;
       if (tid == 0) sh.m = 0;
       bins[tid] = 0;
       __syncthreads();
 #pragma unroll
       for (int i = 0; i < kSpWarps; ++i) {
-        least = min(least, sh.warp[i]);
-        most = max(most, sh.warp2[i]);
+        least = min(least, (uint32_t)(sh.warp2[i] >> 32));
+        most = max(most, (uint32_t)sh.warp2[i]);
       }
-      const int shift = max(0, 64 - __clzll(most - least) - 8);
+      if (up == 32 && most == least) {
+        up = 0;
+        continue;
+      }
+      const int shift = max(0, 32 - __clz(most - least) - 8);
+      auto bin_of = [&](u64 k) { return (int)(((uint32_t)(k >> up) - least) >> shift); };
 #pragma unroll
       for (int i = 0; i < kOf; ++i)
-        if (live >> i & 1) atomicAdd(bins + (int)((key[i] - least) >> shift), weight(key[i]));
+        if (live >> i & 1) atomicAdd(bins + bin_of(key[i]), weight(key[i]));
       __syncthreads();
       const u64 here = bins[tid];
       u64 before;
@@ -726,7 +728,7 @@ struct Row {
 #pragma unroll
       for (int i = 0; i < kOf; ++i)
         if (live >> i & 1) {
-          if ((key[i] - least) >> shift == sh.bcast[0]) {
+          if (bin_of(key[i]) == (int)sh.bcast[0]) {
             const int at = atomicAdd(&sh.m, 1);
             if (at < 32) sh.few[at] = key[i];
           } else {
@@ -803,7 +805,7 @@ struct Row {
     if (mine > kSpMasked) add<false>((int)kSpMagicBits - t, 1);
     u64 target = (u64)k, goal, before;
     int bin;
-    if (!find<false>(target, goal, before, bin)) return false;
+    if (!find<false, false>(target, goal, before, bin)) return false;
     if (bin == kSpBins - 1) {
       tc::cluster_sync();  // the histogram has been read
       return false;
@@ -880,7 +882,7 @@ struct Row {
       });
       int digit;
       u64 here, rest;
-      find<false>(goal, rest, here, digit);
+      find<false, MASS>(goal, rest, here, digit);
       goal = rest;
       before += here;
       prefix = prefix << 8 | (uint32_t)digit;
