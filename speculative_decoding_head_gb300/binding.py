@@ -794,8 +794,10 @@ class Fp4Matrix(_TrainOp):
         n = self.rows if idx is None else idx.shape[0]
         if out is None:
             out = self._new((n, self.K), dtype, stream)
+            po, ldo = out.data_ptr(), self.K
+        else:
+            po, ldo = _rows(out, n, self.K, out.dtype, "out", self._index)
         code = _dtype_code(out, "out")
-        po, ldo = _rows(out, n, self.K, out.dtype, "out", self._index)
         pi = _vec(idx, n, torch.int32, "idx", self._index)
         r = self._call(self.lib.dspark_fp4_rows, self._pdims, self._pdata, pi, n, po, code, max(ldo, self.K),
                        self.status.data_ptr(), self._on(stream))
@@ -864,12 +866,16 @@ class Sampler(_TrainOp):
     def sample(self, Z, u, temperature=None, top_k=None, top_p=None, min_p=None, row_off=None, out=None, stream=None):
         """token [N] int32 and logp [N] fp32 drawn with u [N] fp32 in [0, 1);
         rows that ``row_off`` gives to no request are left as they are."""
-        if out is None:
+        made = out is None
+        if made:
             out = {"token": self._new((self.N,), torch.int32, stream), "logp": self._new((self.N,), torch.float32, stream)}
         dev, f32 = self._index, torch.float32
         pz = self._set(Z, row_off, temperature, top_k, top_p, min_p)
         pu = _vec(u, self.N, f32, "u", dev)
-        pt, pl = _vec(out["token"], self.N, torch.int32, "token", dev), _vec(out.get("logp"), self.N, f32, "logp", dev)
+        if made:
+            pt, pl = out["token"].data_ptr(), out["logp"].data_ptr()
+        else:
+            pt, pl = _vec(out["token"], self.N, torch.int32, "token", dev), _vec(out.get("logp"), self.N, f32, "logp", dev)
         r = self._call(self.lib.dspark_sample, self._pargs, pz, pu, pt, pl, self.status.data_ptr(), self._on(stream))
         _check(r, "dspark_sample")
         return out
