@@ -532,7 +532,7 @@ size_t dspark_clip_grads_scratch_bytes(int count);
  *       that x (N rows) and w (V rows) stand for: of one format, with the same K.
  *       The products are exact and summed in fp32 by the tensor cores; Y [N][ldy]
  *       is fp32 or bf16 (rounded once), U [N][ldu] fp32 or NULL. U may be Y itself where
- *       Y is fp32 and ldu == ldy.
+ *       Y is fp32 and ldu == ldy; outputs must not overlap inputs otherwise.
  *
  * Any leading dimension of at least the row's length and any base address on
  * the type's own size will do for X, out, U and Y; rows on 16 bytes run faster.
@@ -598,9 +598,10 @@ dspark_status dspark_fp4_linear(const dspark_fp4_dims* xdims, const dspark_fp4_d
  * [0, 1)), has token -1, logp NaN and `fill` throughout, and sets DSPARK_ENUMERIC in
  * *device_status (the caller's int32; the first error is kept until the caller clears it).
  *
- * Masses are whole numbers: e^x with a relative error of about 2^-31, rounded to a multiple
- * of 2^-Q, Q = min(46, 62 - ceil(log2 V)). Their sums are exact, whatever the order, so a row's
- * result depends on its logits and settings alone. 0 <= N <= 2^24, V <= 2^24, else
+ * Masses are whole numbers of 31 bits and an octave (a relative error of at most
+ * 2^-29, without a bias), added as they are: results are the same from call to call, and a
+ * border of the top-p set or of a draw is missed only where it lies within some 1e-10 of
+ * the mass. 0 <= N <= 2^24, V <= 2^24, else
  * DSPARK_EINVAL; any leading dimension of at least V and any base address on the type's own
  * size will do; rows on 16 bytes run faster. Outputs must not overlap inputs. One launch,
  * asynchronous on `stream`, no scratch.

@@ -783,7 +783,7 @@ class Fp4Matrix(_TrainOp):
         """Takes X [rows, K] (bf16 or fp32, contiguous rows) into the matrix (``dspark_fp4_quant``); returns it."""
         code = _dtype_code(X, "X")
         px, ldx = _rows(X, self.rows, self.K, X.dtype, "X", self._index)
-        r = self._call(self.lib.dspark_fp4_quant, self._pdims, px, code, max(ldx, self.K), self._pdata,
+        r = self._call(self.lib.dspark_fp4_quant, self._pdims, px, code, ldx, self._pdata,
                        self.status.data_ptr(), self._on(stream))
         _check(r, "dspark_fp4_quant")
         return self
@@ -791,7 +791,7 @@ class Fp4Matrix(_TrainOp):
     def lookup(self, idx: Optional[torch.Tensor] = None, dtype=torch.bfloat16, out=None, stream=None):
         """The values of rows idx [N] int32 (-1: zeros), or of all rows, as
         [N, K] bf16 or fp32 (``dspark_fp4_rows``)."""
-        n = self.rows if idx is None else idx.shape[0]
+        n = self.rows if idx is None else idx.numel()
         if out is None:
             out = self._new((n, self.K), dtype, stream)
             po, ldo = out.data_ptr(), self.K
@@ -799,7 +799,7 @@ class Fp4Matrix(_TrainOp):
             po, ldo = _rows(out, n, self.K, out.dtype, "out", self._index)
         code = _dtype_code(out, "out")
         pi = _vec(idx, n, torch.int32, "idx", self._index)
-        r = self._call(self.lib.dspark_fp4_rows, self._pdims, self._pdata, pi, n, po, code, max(ldo, self.K),
+        r = self._call(self.lib.dspark_fp4_rows, self._pdims, self._pdata, pi, n, po, code, ldo,
                        self.status.data_ptr(), self._on(stream))
         _check(r, "dspark_fp4_rows")
         return out
@@ -817,8 +817,8 @@ class Fp4Matrix(_TrainOp):
         po, ldo = _rows(out, X.rows, self.rows, out.dtype, "out", self._index)
         pu, ldu = (None, 0) if U is None else _rows(U, X.rows, self.rows, torch.float32, "U", self._index)
         X._on(stream)
-        r = self._call(self.lib.dspark_fp4_linear, X._pdims, X._pdata, self._pdims, self._pdata, pu, max(ldu, self.rows),
-                       po, code, max(ldo, self.rows), self.status.data_ptr(), self._on(stream))
+        r = self._call(self.lib.dspark_fp4_linear, X._pdims, X._pdata, self._pdims, self._pdata, pu, ldu,
+                       po, code, ldo, self.status.data_ptr(), self._on(stream))
         _check(r, "dspark_fp4_linear")
         return out
 
@@ -847,8 +847,7 @@ class Sampler(_TrainOp):
         """Takes a call's inputs into the argument block; returns the address of the logits."""
         dev, f32, i32, a = self._index, torch.float32, torch.int32, self._args
         a.type = _dtype_code(Z, "Z")
-        pz, ldz = _rows(Z, self.N, self.V, Z.dtype, "Z", dev)
-        a.ldz = max(ldz, self.V)
+        pz, a.ldz = _rows(Z, self.N, self.V, Z.dtype, "Z", dev)
         n = self.N
         if row_off is None:
             a.row_off = None
@@ -887,7 +886,7 @@ class Sampler(_TrainOp):
             out = self._new((self.N, self.V), torch.float32, stream)
         pz = self._set(Z, row_off, temperature, top_k, top_p, min_p)
         po, ldo = _rows(out, self.N, self.V, torch.float32, "out", self._index)
-        r = self._call(self.lib.dspark_sample_logprobs, self._pargs, pz, fill, po, max(ldo, self.V),
+        r = self._call(self.lib.dspark_sample_logprobs, self._pargs, pz, fill, po, ldo,
                        self.status.data_ptr(), self._on(stream))
         _check(r, "dspark_sample_logprobs")
         return out

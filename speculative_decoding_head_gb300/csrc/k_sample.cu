@@ -557,7 +557,8 @@ struct Row {
         for (int i = 0; i < kStep; ++i)
           count_if(hist + 4u * kSpMagicBits - 4u * (uint32_t)max(bits_of(v[i]), kLow), kept(v[i], at(ch, h, i)));
       });
-    } else if (RES && b.sub == 0.f && cut.z == kSpLeast && b.hi > 1e-24f) {  // masked tokens lie below the bins
+    } else if (RES && b.sub == 0.f && cut.z == kSpLeast && b.hi > 1e-24f && m > -1e28f) {
+      // masked tokens lie 9e28 and more below the maximum, below the bins
       each([&](const float* v, int ch, int h) {
         uint32_t t[kStep], mant[kStep];
 #pragma unroll
@@ -1288,7 +1289,7 @@ dspark_status sample(const dspark_sample_args* s, const void* Z, SpArgs a, int32
     return DSPARK_EINVAL;
   if (s->N == 0) return DSPARK_OK;
   const int size = s->type == DSPARK_BF16 ? 2 : 4;
-  if (!Z || !on(Z, size)) return DSPARK_EINVAL;
+  if (!Z || !on(Z, size) || Z == a.out) return DSPARK_EINVAL;
   if (DIST ? (!a.out || !on(a.out, 4) || a.ldo < s->V) : (!a.u || !a.token || !on(a.u, 4) || !on(a.token, 4) || !on(a.logp, 4)))
     return DSPARK_EINVAL;
   a.Z = Z;

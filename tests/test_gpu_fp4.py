@@ -272,5 +272,14 @@ def test_refusals():
         w.linear(a, U=torch.empty(4, 6, device="cuda", dtype=BF16))
     with pytest.raises(DsparkError):
         a.lookup(torch.zeros(2, dtype=torch.int64, device="cuda"))
+    flat = x[:1].expand(4, 64)  # rows that overlap
+    with pytest.raises(DsparkError):
+        a.quantise(flat)
+    with pytest.raises(DsparkError):
+        a.lookup(out=flat)
+    with pytest.raises(DsparkError):
+        w.linear(a, out=torch.empty(1, 6, device="cuda").expand(4, 6))
+    with pytest.raises(DsparkError):
+        w.linear(a, U=torch.empty(1, 6, device="cuda").expand(4, 6))
     assert Fp4Matrix(0, 64).quantise(torch.zeros(0, 64, device="cuda")).rows == 0
     assert w.linear(Fp4Matrix(0, 64)).shape == (0, 6)

@@ -91,6 +91,15 @@ def test_vocabularies(N, V, kind, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("kind", ("none", "k", "p", "all"))
+def test_large_parts_of_a_cluster(kind, dtype):
+    """Sixteen CTAs that hold some 40000 (fp32) or 62500 (bf16) tokens each."""
+    V = 600001 if dtype == F32 else 1000001
+    g = gen(V)
+    check(logits(2, V, dtype, seed=3), ref.settings(kind, 2, g), torch.rand(2, generator=g, device="cuda"))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 def test_vocabularies_past_shared_memory(dtype):
     V = (1 << 21) + 77
     g = gen(1)
@@ -155,6 +164,32 @@ def test_far_values():
     u = torch.rand(6, generator=g, device="cuda")
     for kind in KINDS:
         check(z, ref.settings(kind, 6, g), u)
+
+
+def test_masks_next_to_the_maximum():
+    """Temperatures so high that a masked token's finite logit would have a mass beside a maximum of -9e28."""
+    V = 600
+    z = torch.full((4, V), -1.00001e29, device="cuda")
+    z[:, ::3] = -9.99e28
+    z[:, 1::7] = -9.5e28
+    g = gen(4)
+    u = torch.rand(4, generator=g, device="cuda")
+    T = torch.tensor([1e24, 1e26, 5e27, 1e30], device="cuda")
+    check(z, (T, None, torch.full((4,), 0.7, device="cuda"), None), u)
+    check(z, (T, torch.full((4,), 150, device="cuda", dtype=torch.int32), None, torch.full((4,), 0.5, device="cuda")), u)
+    check(z, (T, None, None, None), u)
+
+
+def test_many_kept_tokens():
+    """top-k from the lists' limits on: as many tokens as threads, thousands, and nearly all."""
+    N, V = 6, 40000
+    z = logits(N, V, F32, seed=21)
+    g = gen(21)
+    u = torch.rand(N, generator=g, device="cuda")
+    for k in (127, 128, 129, 256, 512, 640, 641, 1024, 3000, 30000):
+        kk = torch.full((N,), k, device="cuda", dtype=torch.int32)
+        check(z, (None, kk, torch.full((N,), 0.95, device="cuda"), None), u)
+        check((z * 2).round() / 2, (None, kk, None, None), u)
 
 
 def test_rows_with_nothing_left():
@@ -313,6 +348,13 @@ def test_refusals():
             s.sample(z, u, **kw)
     with pytest.raises(DsparkError):
         s.sample(z, u[:2])
+    for rows in (z[:1].expand(4, 64), torch.zeros(300, device="cuda").as_strided((4, 64), (63, 1))):
+        with pytest.raises(DsparkError):  # rows that overlap
+            s.sample(rows, u)
+        with pytest.raises(DsparkError):
+            s.logprobs(z, out=rows)
+    with pytest.raises(DsparkError):
+        s.logprobs(z, out=z)
     with pytest.raises(DsparkError):
         s.logprobs(z, out=torch.zeros(4, 64, device="cuda", dtype=BF16))
     assert Sampler(0, 64).sample(z[:0], u[:0])["token"].shape == (0,)

@@ -120,7 +120,7 @@ def test_sample_arguments(lib):
         assert draw(**kw) == EINVAL and dist(**kw) == EINVAL, kw
     for kw in (dict(u=None), dict(u=258), dict(token=None), dict(token=257), dict(logp=258)):
         assert draw(**kw) == EINVAL, kw
-    for kw in (dict(out=None), dict(out=514), dict(ldo=63)):
+    for kw in (dict(out=None), dict(out=514), dict(ldo=63), dict(out=OK)):
         assert dist(**kw) == EINVAL, kw
     assert draw(_args(type=1), Z=257) == EINVAL
     assert lib.dspark_sample(None, OK, OK, OK, OK, OK, None) == EINVAL
