@@ -523,7 +523,8 @@ size_t dspark_clip_grads_scratch_bytes(int count);
  *   rowf    f of each row, fp32, ceil(rows / 128) * 128 of them, 16-byte aligned
  *           (DSPARK_MXFP4: not looked at, may be NULL).
  *
- *   dspark_fp4_quant   X [rows][ldx], bf16 or fp32, into the three buffers;
+ *   dspark_fp4_quant   X [rows][ldx], bf16 or fp32, into the three buffers. Rows from *count on
+ *       (a device int32, such as the end of a packed batch; NULL: none) are not read and stand for zeros;
  *   dspark_fp4_rows    out[n] = the values of row idx[n], n < N (idx NULL: row n, N <= rows).
  *       idx[n] = -1 gives a row of zeros; any other value outside [0, rows) does the
  *       same and sets DSPARK_ERANGE. bf16 and fp32 hold the values exactly (but for
@@ -558,7 +559,8 @@ typedef struct {
 size_t dspark_fp4_code_bytes(const dspark_fp4_dims* dims);
 size_t dspark_fp4_scale_bytes(const dspark_fp4_dims* dims);
 dspark_status dspark_fp4_quant(const dspark_fp4_dims* dims, const void* X, dspark_wdtype type, int64_t ldx,
-                               const dspark_fp4_data* out, int32_t* device_status, dspark_stream_t stream);
+                               const int32_t* count, const dspark_fp4_data* out, int32_t* device_status,
+                               dspark_stream_t stream);
 dspark_status dspark_fp4_rows(const dspark_fp4_dims* dims, const dspark_fp4_data* m, const int32_t* idx, int N, void* out,
                               dspark_wdtype type, int64_t ldo, int32_t* device_status, dspark_stream_t stream);
 dspark_status dspark_fp4_linear(const dspark_fp4_dims* xdims, const dspark_fp4_data* x, const dspark_fp4_dims* wdims,

@@ -154,7 +154,7 @@ def load() -> C.CDLL:
         for name in ("dspark_fp4_code_bytes", "dspark_fp4_scale_bytes"):
             getattr(lib, name).argtypes = [D4]
             getattr(lib, name).restype = C.c_size_t
-        lib.dspark_fp4_quant.argtypes = [D4, P, i32, i64, M4, P, P]
+        lib.dspark_fp4_quant.argtypes = [D4, P, i32, i64, P, M4, P, P]
         lib.dspark_fp4_quant.restype = i32
         lib.dspark_fp4_rows.argtypes = [D4, M4, P, i32, P, i32, i64, P, P]
         lib.dspark_fp4_rows.restype = i32
@@ -779,11 +779,13 @@ class Fp4Matrix(_TrainOp):
     def _buffers(self):
         return (self.codes, self.scales, self.rowf, self.status)
 
-    def quantise(self, X: torch.Tensor, stream=None) -> "Fp4Matrix":
-        """Takes X [rows, K] (bf16 or fp32, contiguous rows) into the matrix (``dspark_fp4_quant``); returns it."""
+    def quantise(self, X: torch.Tensor, count: Optional[torch.Tensor] = None, stream=None) -> "Fp4Matrix":
+        """Takes X [rows, K] (bf16 or fp32, contiguous rows) into the matrix (``dspark_fp4_quant``); returns it.
+        Rows from ``count`` [1] int32 on (a packed batch's end, on the device) are not read and become zeros."""
         code = _dtype_code(X, "X")
         px, ldx = _rows(X, self.rows, self.K, X.dtype, "X", self._index)
-        r = self._call(self.lib.dspark_fp4_quant, self._pdims, px, code, ldx, self._pdata,
+        pc = _vec(count, 1, torch.int32, "count", self._index)
+        r = self._call(self.lib.dspark_fp4_quant, self._pdims, px, code, ldx, pc, self._pdata,
                        self.status.data_ptr(), self._on(stream))
         _check(r, "dspark_fp4_quant")
         return self

@@ -49,6 +49,7 @@ __device__ __forceinline__ float off_border(float q, float rem, uint32_t low) {
 struct QuArgs {
   const void* X;
   int64_t ldx;
+  const int32_t* count;  // rows from here on are zeros
   uint8_t* codes;
   uint8_t* scales;
   float* rowf;
@@ -69,12 +70,13 @@ __global__ void __launch_bounds__(FMT == DSPARK_NVFP4 ? 512 : 1024) k_fp4_quant(
   const int tid = threadIdx.x, lane = tid % a.lanes;
   const int64_t r = (int64_t)blockIdx.x * a.per_cta + tid / a.lanes;
   const bool row = r < a.rows;
-  const T* x = static_cast<const T*>(a.X) + (row ? r : 0) * a.ldx;
+  const bool held = row && (!a.count || r < __ldg(a.count));
+  const T* x = static_cast<const T*>(a.X) + (held ? r : 0) * a.ldx;
   uint32_t w[BPL][W], top[BPL];
   uint32_t rtop = 0;
 #pragma unroll
   for (int j = 0; j < BPL; ++j) {
-    const int c = (lane + j * a.lanes) * B, left = row ? a.K - c : 0;
+    const int c = (lane + j * a.lanes) * B, left = held ? a.K - c : 0;
     if (a.vec && left >= B) {
       const uint4* p = reinterpret_cast<const uint4*>(x + c);
 #pragma unroll
@@ -351,13 +353,15 @@ extern "C" size_t dspark_fp4_scale_bytes(const dspark_fp4_dims* d) {
 }
 
 extern "C" dspark_status dspark_fp4_quant(const dspark_fp4_dims* d, const void* X, dspark_wdtype type, int64_t ldx,
-                                          const dspark_fp4_data* out, int32_t* device_status, dspark_stream_t stream) {
+                                          const int32_t* count, const dspark_fp4_data* out, int32_t* device_status,
+                                          dspark_stream_t stream) {
   if (!fp4::dims_ok(d) || !type_ok(type) || !device_status || ldx < d->K) return DSPARK_EINVAL;
   if (d->rows == 0) return DSPARK_OK;
-  if (!on_type(X, type) || !fp4::data_ok(d, out)) return DSPARK_EINVAL;
+  if (!on_type(X, type) || !fp4::data_ok(d, out) || (reinterpret_cast<uintptr_t>(count) & 3u) != 0) return DSPARK_EINVAL;
   QuArgs a = {};
   a.X = X;
   a.ldx = ldx;
+  a.count = count;
   a.codes = static_cast<uint8_t*>(out->codes);
   a.scales = static_cast<uint8_t*>(out->scales);
   a.rowf = out->rowf;

@@ -56,7 +56,7 @@ class HeadServer:
         """Verifies a draft against the target's hidden states ht [B (gamma + 1), H], packed by the plan's
         row_off (rows past its last are not looked at), under ``Sampler``'s settings, an entry per request:
         ``Workspace.verify``'s outputs."""
-        self.layer.linear(self.rows.quantise(ht), out=self.P)
+        self.layer.linear(self.rows.quantise(ht, count=d["row_off"][self.B :]), out=self.P)
         self.sampler.logprobs(self.P, row_off=d["row_off"], out=self.Q, **settings)
         return self.ws.verify(self.Q, d["row_off"], d["lengths"], anchor, d["tokens"], d["pd_tok"], d["lse"], self.U,
                               self.W1, self.W2, seed, rnd)

@@ -5,6 +5,8 @@ are exact and summed in fp32 by the tensor cores, which cut a running sum off to
 so; the tolerance counts one unit in the last place (2^-23 of the sum of magnitudes) for
 every 16 terms and 8 more for the joins, then the output's own rounding (half a step)."""
 
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -143,6 +145,28 @@ def test_strides_and_alignment():
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("K", [40, 256, 5376])  # several rows a CTA, one, and one of many threads
+@pytest.mark.parametrize("count", [-1, 0, 1, 129, 200, 1 << 30])
+def test_rows_behind_the_last_are_not_read(count, K, dtype, fmt):
+    R = 200
+    x = values((R, K), dtype, seed=count & 255)
+    n = min(max(count, 0), R)
+    x[n:] = math.nan
+    m = Fp4Matrix(R, K, fmt)
+    m.codes.fill_(255)
+    m.scales.fill_(255)
+    m.rowf.fill_(math.nan)
+    m.quantise(x, count=torch.tensor([count], dtype=torch.int32, device="cuda"))
+    full = Fp4Matrix(R, K, fmt).quantise(torch.where(torch.arange(R, device="cuda")[:, None] < n, x, 0).to(dtype))
+    assert m.device_status() == 0
+    assert torch.equal(m.codes, full.codes) and torch.equal(m.scales, full.scales)
+    assert torch.equal(m.lookup(), full.lookup()) and (m.lookup()[n:] == 0).all()
+    if fmt == "nvfp4":
+        assert torch.equal(m.rowf[:R], full.rowf[:R])
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("V,D,N", [(1, 16, 3), (300, 256, 1000), (1000, 100, 77), (129280, 33, 500)])
 def test_rows_by_token(V, D, N, fmt):
     x = values((V, D), BF16, seed=6, std=0.02)
@@ -272,6 +296,10 @@ def test_refusals():
         w.linear(a, U=torch.empty(4, 6, device="cuda", dtype=BF16))
     with pytest.raises(DsparkError):
         a.lookup(torch.zeros(2, dtype=torch.int64, device="cuda"))
+    for count in (torch.zeros(2, device="cuda", dtype=torch.int32), torch.zeros(1, device="cuda"),
+                  torch.zeros(1, dtype=torch.int32)):
+        with pytest.raises(DsparkError):
+            a.quantise(x, count=count)
     flat = x[:1].expand(4, 64)  # rows that overlap
     with pytest.raises(DsparkError):
         a.quantise(flat)

@@ -77,6 +77,21 @@ def test_without_settings_a_round_is_the_plain_one():
     assert (((v["n_acc"] == plain["n_acc"]) & (v["next_anchor"] == plain["next_anchor"])).cpu().numpy() | close).all()
 
 
+def test_hidden_states_behind_the_last_row_are_not_looked_at():
+    B, gamma, V = 24, 4, 8192
+    chain, s, sps, g = server(B, gamma, V, 256, 64, mode="compact")
+    sps = 400.0 / (1.0 + 0.2 * torch.arange(sps.numel(), dtype=torch.float64, device="cuda"))  # short lengths pay
+    anchor = torch.randint(0, V, (B,), generator=g, device="cuda", dtype=torch.int32)
+    d = s.draft(chain.draft_hidden(anchor, gamma, 0.5), anchor, sps, 1, 0)
+    ht, last = chain.target_hidden(anchor, d), int(d["row_off"][B])
+    assert last < B * (gamma + 1)
+    want = {k: t.clone() for k, t in s.verify(ht, anchor, d, 1, 0).items()}
+    ht[last:] = float("nan")
+    got = s.verify(ht, anchor, d, 1, 0)
+    assert s.device_status() == 0
+    assert all(torch.equal(got[k], want[k]) for k in want)
+
+
 def test_emitted_tokens_follow_the_settings():
     """The first token of a round has the processed distribution whatever the draft: chi-squared over the
     kept tokens of one row (at most 20, so 19 degrees of freedom; the value 80 has a probability below 1e-8)."""

@@ -48,17 +48,18 @@ def test_fp4_sizes(lib):
 
 def test_fp4_quant_arguments(lib):
     def f(d=None, m=None, **kw):
-        a = {**dict(X=OK, type=1, ldx=64, st=OK), **kw}
-        return lib.dspark_fp4_quant(d or _dims(), a["X"], a["type"], a["ldx"], m or _data(), a["st"], None)
+        a = {**dict(X=OK, type=1, ldx=64, count=None, st=OK), **kw}
+        return lib.dspark_fp4_quant(d or _dims(), a["X"], a["type"], a["ldx"], a["count"], m or _data(), a["st"], None)
 
     for kw in BAD_DIMS:
         assert f(d=_dims(**kw)) == EINVAL, kw
     for kw in BAD_DATA:
         assert f(m=_data(**kw)) == EINVAL, kw
-    for kw in (dict(X=None), dict(X=257), dict(X=258, type=0), dict(type=2), dict(ldx=63), dict(st=None)):
+    for kw in (dict(X=None), dict(X=257), dict(X=258, type=0), dict(type=2), dict(ldx=63), dict(st=None),
+               dict(count=258)):
         assert f(**kw) == EINVAL, kw
-    assert lib.dspark_fp4_quant(None, OK, 1, 64, _data(), OK, None) == EINVAL
-    assert lib.dspark_fp4_quant(_dims(), OK, 1, 64, None, OK, None) == EINVAL
+    assert lib.dspark_fp4_quant(None, OK, 1, 64, None, _data(), OK, None) == EINVAL
+    assert lib.dspark_fp4_quant(_dims(), OK, 1, 64, None, None, OK, None) == EINVAL
     assert f(d=_dims(rows=0), X=None) == 0
 
 
