@@ -363,16 +363,11 @@ struct Row {
       }
     }
   }
-  // Every CTA's thread 0 tells x, y to all; all see them in slot[][].
+  // Every CTA tells x, y, which all of its threads have, to all; all see them in slot[][].
   __device__ __forceinline__ const u64 (*tell(u64 x, u64 y))[2] {
-    if (tid == 0) {
-      sh.bcast[0] = x;
-      sh.bcast[1] = y;
-    }
-    __syncthreads();
     if (tid < (int)C) {
-      st_rank(&sh.slot[par][rank][0], tid, sh.bcast[0]);
-      st_rank(&sh.slot[par][rank][1], tid, sh.bcast[1]);
+      st_rank(&sh.slot[par][rank][0], tid, x);
+      st_rank(&sh.slot[par][rank][1], tid, y);
     }
     tc::cluster_sync();
     const u64(*s)[2] = sh.slot[par];
@@ -1096,7 +1091,6 @@ __global__ void __launch_bounds__(kSpThreads, 3) k_sample(SpArgs a) {
     sum += __uint_as_float((uint32_t)(sh.warp2[i] >> 32));
     seen += __uint_as_float((uint32_t)sh.warp2[i]);
   }
-  __syncthreads();
   asm volatile("barrier.cluster.wait;" ::: "memory");
   {
     const u64(*s)[2] = w.tell(__float_as_uint(top), (u64)__float_as_uint(sum) << 32 | __float_as_uint(seen));
