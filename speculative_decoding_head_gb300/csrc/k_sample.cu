@@ -6,23 +6,34 @@
 // (vocabularies that sixteen CTAs cannot hold are read again each pass).
 //
 // A token's mass, with m the row's maximum, is 2^y, y = (z - m) log2(e) / T, as a
-// whole number `mant` of 31 bits times 2^(-e-30), to a relative 2^-30 at the worst and
-// without a bias (see Mass). Masses are added as whole numbers, so in any order with one
-// result, and a border of the top-p set or of the draw is missed by 1e-10 of the
-// mass at the most: next to nothing against one token's share.
+// whole number `mant` of 31 bits times 2^(-e-30), to a relative 2^-30 at the worst
+// and without a bias (see Mass). Masses are added as whole numbers, so in any order
+// with one result, and a border of the top-p set or of the draw is missed by 1e-10
+// of the mass at the most: next to nothing against one token's share.
 //
 // top-k and top-p are one search, for the first token of the row sorted by
 // falling z (then by index) at which the running sum, of ones or of masses,
-// reaches a target. A histogram of 1088 bins of z (for masses 1/32 of an octave each, so that
-// a bin's tokens share e and their mants are added as they are) gives the bin; its tokens
-// (some hundreds of a flat row of 129280) are brought to one CTA, which splits them
-// into 256 narrower bins, again and again until few are left. A bin of more than 1088 tokens (many
-// equal logits) is instead narrowed by four histograms of the bits of z, down to one value,
-// whose tokens are counted by index. What is kept is z >= cut; tokens that equal the cut
-// but come after its last index are masked in shared memory.
+// reaches a target. A histogram of 1088 bins of z (for masses 1/32 of an octave
+// each, so that a bin's tokens share e and their mants are added as they are) gives
+// the bin; its tokens (some hundreds of a flat row of 129280) are brought to one
+// CTA, which splits them into 256 narrower bins, again and again until few are
+// left. A bin of more than 1088 tokens (many equal logits) is instead narrowed by
+// four histograms of the bits of z, down to one value, whose tokens are counted by
+// index. What is kept is z >= cut; tokens that equal the cut but come after its last
+// index are masked in shared memory.
 //
-// Three CTAs share an SM, so that a row's barriers and loads pass under the others' arithmetic: 64 KB of a
-// row each, 256 threads.
+// Three CTAs share an SM (64 KB of a row each, 256 threads), so that a row's
+// barriers and loads pass under the others' arithmetic. Two CTAs, 320 to 512
+// threads, and parts read again from L2 were slower or the same; clusters that take
+// row after row (one launch's worth of CTAs) spilled and took 20% more.
+//
+// 768 rows of 129280, fp32, as log-probabilities (794 MB): temperature alone 207 us
+// (3.8 TB/s), top-k 50 252, top-k and top-p 274, top-p 0.9 365 us (2.2 TB/s); bf16
+// (596 MB) 167, 188, 200 and 312. One row 8 to 20 us. With top-p a CTA spends 6 of its
+// 23 us on the histogram (two shared additions a token, 1.6 ns for 32 of them) and
+// 10 in five meetings of the cluster; schedulers issue in 48% of the cycles. 51
+// clusters of eight run at once (of 57 that SMs have room for), and a place stays
+// empty for 15% of the time between two of them.
 #include <math.h>
 #include <stdio.h>
 
