@@ -51,6 +51,7 @@ constexpr int kSpThreads = 256, kSpWarps = kSpThreads / 32;
 constexpr int kSpMaxC = 16;       // CTAs of a cluster
 constexpr int kSpBins = 1088;     // 34 octaves of 32 bins, the last one for what lies below
 constexpr int kSpNone = 1504;     // from here on (2^-47) a mass is nothing
+constexpr int kSpLowQ = 60;      // masses of the last bin are multiples of 2^-60
 constexpr int kSpSeg = kSpBins / 8;
 constexpr int kSpList = kSpBins;      // tokens of a bin that are brought together,
 constexpr int kSpOwn = kSpSeg * 4 / 2; // and of one CTA: half of the histogram's lower words
@@ -77,7 +78,7 @@ struct SpArgs {
   int64_t ldo;
   float fill;
   int part;      // tokens of a CTA, a multiple of kSpChunk
-  int q;         // sums of masses are multiples of 2^-q
+  int q, fine;   // sums of masses are multiples of 2^-q, of a lane or a chunk of 2^-fine
   int vec, vec_out;
   int* status;
 };
@@ -419,15 +420,17 @@ struct Row {
     else add_carry(p, x);
   }
   // With every CTA's histogram filled: the first bin at which the sum up to it reaches the target, the sum before
-  // it, and how much of the bin's raw sum is missing there. OCT: the bins, but for the last, hold raw mants of their octaves, and
-  // count as multiples of 2^-q. target 0: ceil(p of all of it), at least 1. Returns whether the sum reaches the target at all.
+  // it, and how much of the bin's raw sum is missing there. OCT: the bins hold raw mants of their octaves, the last one multiples of 2^-60, and
+  // all count as multiples of 2^-q. target 0: ceil(p of all of it), at least 1. Returns whether the sum reaches the target at all.
   // Every CTA tells the others its sums of eight segments, so that all know the segment, and all look at its bins:
   // they are not to change before the cluster's next barrier.
   // HIGH: the bins have upper words.
   template <bool OCT, bool HIGH>
   __device__ __forceinline__ bool find(u64& target, u64& goal, u64& before, int& bin) {
     constexpr int kEach = (kSpSeg + 31) / 32;
-    auto value = [&](u64 v, int g) { return OCT && g < kSpBins - 1 ? scaled(v, octave(g), a.q) : v; };
+    auto value = [&](u64 v, int g) {
+      return !OCT ? v : g < kSpBins - 1 ? scaled(v, octave(g), a.q) : v >> (kSpLowQ - a.q);
+    };
     __syncthreads();
     {
       u64 sum = 0;
@@ -485,7 +488,7 @@ struct Row {
       const u64 need = target - t;
       sh.found[0] = (u64)g;
       sh.found[1] = t;
-      sh.found[2] = OCT && g < kSpBins - 1 ? min(unscaled(need, octave(g), a.q), raw) : need;
+      sh.found[2] = !OCT ? need : min(g < kSpBins - 1 ? unscaled(need, octave(g), a.q) : need << (kSpLowQ - a.q), raw);
     }
     __syncthreads();
     bin = (int)sh.found[0];
@@ -537,7 +540,7 @@ struct Row {
 
   // Tightens the cut to the first of the kept tokens, in order, at which the running
   // count (MASS: mass) reaches the target. The last bin takes in what lies below the others (its masses
-  // are added as multiples of 2^-q).
+  // are added as multiples of 2^-60).
   template <bool MASS>
   __device__ void select(u64 target, const SpScale& b) {
     constexpr int kLow = (int)kSpMagicBits - (kSpBins - 1);
@@ -554,7 +557,7 @@ struct Row {
       if (least <= (uint32_t)kLow - kNone) {
 #pragma unroll
         for (int i = 0; i < kStep; ++i)
-          if ((int)t[i] <= kLow && kept(v[i], at(ch, h, i))) light += weigh(mant[i], (int)t[i]);
+          if ((int)t[i] <= kLow && kept(v[i], at(ch, h, i))) light += weigh(mant[i], (int)t[i], kSpLowQ);
       }
     };
     if (!MASS) {
@@ -640,7 +643,7 @@ struct Row {
     tc::cluster_sync();
     cut.z = unordered((uint32_t)(sh.res[0] >> 32));
     cut.last = (int)(uint32_t)sh.res[0];
-    if (MASS) held = before + (low ? sh.res[1] : scaled(sh.res[1], e, a.q));
+    if (MASS) held = before + (low ? sh.res[1] >> (kSpLowQ - a.q) : scaled(sh.res[1], e, a.q));
     if (RES && !fit) {  // settle() has masked the others
       each([&](const float* v, int ch, int h) {
 #pragma unroll
@@ -658,7 +661,7 @@ struct Row {
   __device__ __forceinline__ uint32_t raw_of(float z) const {
     int J;
     const uint32_t mant = mass.one(z, tab, J);
-    return low_mass ? (uint32_t)weigh(mant, J + (int)kSpMagicBits) : mant;
+    return low_mass ? (uint32_t)weigh(mant, J + (int)kSpMagicBits, kSpLowQ) : mant;
   }
   // The cut (ordered z, index) and the raw sum up to it, to every CTA.
   __device__ __forceinline__ void answer(u64 key, u64 sum) {
@@ -847,7 +850,7 @@ struct Row {
       auto mass_of = [&](u64 x) {
         int J;
         const uint32_t mant = mass.one(unordered(~(uint32_t)(x >> 32)), tab, J);
-        return weigh(mant, J + (int)kSpMagicBits);
+        return weigh(mant, J + (int)kSpMagicBits, a.q);
       };
       u64 all = 0, ignored;
 #pragma unroll
@@ -946,9 +949,8 @@ struct Row {
     const float b = kSpMagic - mass.s.mb, x = m - mass.s.sub;
     return -(fmaf(x, mass.s.hi, -b) + x * mass.lo) * 0.0216608494f;  // ln(2) / 32
   }
-  // The kept mass of a lane's tokens of a step: mants times 2^(q-30-e), added up in two words, of those where that is
-  // whole and of the others, times 2^29 (which leaves out what is below 2^-(q-2)). lane_sum() rounds a
-  // chunk's together.
+  // The kept mass of a lane's tokens of a step: mants times 2^(fine-30-e), added up in two words, of those where that
+  // is whole and of the others, times 2^29: all down to 2^-47.
   __device__ __forceinline__ void sum_of(const float* v, int ch, int h, u64& heavy, u64& light) const {
 #pragma unroll
     for (int i = 0; i < kStep; i += 2) {
@@ -956,7 +958,7 @@ struct Row {
       mass.template two<true>(v[i], v[i + 1], tab, t, mant);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const int n = ((int)t[k] >> 5) - (int)(kSpMagicBits >> 5) + a.q - 30;
+        const int n = ((int)t[k] >> 5) - (int)(kSpMagicBits >> 5) + a.fine - 30;
         uint32_t mult;  // 0 for masked tokens and for those that are nothing
         asm("shl.b32 %0, 1, %1;" : "=r"(mult) : "r"(n >= 0 ? n : n + 29));
         if (!kept(v[i + k], at(ch, h, i + k))) mult = 0;
@@ -965,8 +967,8 @@ struct Row {
       }
     }
   }
-  __device__ __forceinline__ u64 lane_sum(u64 heavy, u64 light) const { return heavy + ((light + (1ull << 28)) >> 29); }
-  // Of most rows few tokens are kept: steps without any are passed over.
+  // Of most rows few tokens are kept: steps without any are passed over. A lane's sum is a multiple of 2^-fine,
+  // so that light tokens are not lost one by one.
   __device__ __forceinline__ u64 sum_kept(int ch) const {
     u64 heavy = 0, light = 0;
 #pragma unroll 1
@@ -978,12 +980,15 @@ struct Row {
       for (int i = 1; i < kStep; ++i) top = fmaxf(top, v[i]);
       if (__any_sync(0xFFFFFFFFu, top >= cut.z)) sum_of(v, ch, h, heavy, light);
     }
-    return lane_sum(heavy, light);
+    return heavy + ((light + (1ull << 28)) >> 29);
+  }
+  __device__ __forceinline__ u64 rounded(u64 x) const {
+    return (x + (1ull << (a.fine - a.q - 1))) >> (a.fine - a.q);
   }
   // The same of one token: mant 2^(q-30-e), rounded. t: the bits of kSpMagic + J. One product serves both
   // ways: by 2^(q-30-e) where that is whole, else by 2^32 times it, whose upper word is the result.
-  __device__ __forceinline__ u64 weigh(uint32_t mant, int t) const {
-    const int n = (t >> 5) - (int)(kSpMagicBits >> 5) + a.q - 30;  // q - 30 - e
+  __device__ __forceinline__ u64 weigh(uint32_t mant, int t, int q) const {
+    const int n = (t >> 5) - (int)(kSpMagicBits >> 5) + q - 30;  // q - 30 - e
     const u64 p = (u64)mant * (1u << (n & 31));
     const u64 w = n >= 0 ? p : (p + 0x80000000ull) >> 32;
     return n >= -32 && t > (int)(kSpMagicBits - kSpNone) ? w : 0;
@@ -1173,7 +1178,7 @@ __global__ void __launch_bounds__(kSpThreads, 3) k_sample(SpArgs a) {
     if (!exact) {
       u64 t = 0, ignored;
       for (int ch = w.warp; ch < w.chunks; ch += kSpWarps) t += w.sum_kept(ch);
-      const u64 mine = w.block_scan(t, ignored);
+      const u64 mine = w.block_scan(w.rounded(t), ignored);
       const u64(*s)[2] = w.tell(mine, 0);
       S = 0;
       for (uint32_t c = 0; c < w.C; ++c) S += s[c][0];
@@ -1202,7 +1207,7 @@ __global__ void __launch_bounds__(kSpThreads, 3) k_sample(SpArgs a) {
     for (int ch = w.warp; ch < w.chunks; ch += kSpWarps) {
       u64 t = w.sum_kept(ch);
       t = warp_sum64(t);
-      if (w.lane == 0) chunk[ch] = t;
+      if (w.lane == 0) chunk[ch] = w.rounded(t);
     }
     __syncthreads();
     const int kEach = (w.chunks + kSpThreads - 1) / kSpThreads;
@@ -1237,11 +1242,22 @@ __global__ void __launch_bounds__(kSpThreads, 3) k_sample(SpArgs a) {
         const float z = w.value(l);
         int J;
         const uint32_t mant = w.mass.one(z, w.tab, J);
-        own[i] = w.kept(z, l) ? w.weigh(mant, J + (int)kSpMagicBits) : 0;
+        own[i] = w.kept(z, l) ? w.weigh(mant, J + (int)kSpMagicBits, a.q) : 0;
         sum += own[i];
       }
+      u64 total = w.block_scan(sum, y);
+      if (total == 0) {  // tokens so light that only their sum is a unit: the first of them
+        sum = 0;
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) {
+          const int l = ch * kSpChunk + tid * kOwn + i;
+          sum += own[i] = w.kept(w.value(l), l) ? 1 : 0;
+        }
+        w.block_scan(sum, y);
+        total = 1;
+      }
       // the chunk's sum may be a few units more than its tokens', each rounded by itself
-      const u64 rest2 = min(rest, w.block_scan(sum, y) - 1);
+      const u64 rest2 = min(rest, total - 1);
 #pragma unroll
       for (int i = 0; i < kOwn; ++i) {
         if (rest2 >= y && rest2 < y + own[i]) {
@@ -1313,6 +1329,7 @@ dspark_status sample(const dspark_sample_args* s, const void* Z, SpArgs a, int32
   int bits = 0;
   while ((1 << bits) < a.V) ++bits;
   a.q = 62 - bits < 46 ? 62 - bits : 46;
+  a.fine = bits <= 20 ? 52 : 49;  // a lane has at most 2^8 tokens, or 2^12, and a chunk 2^9
   // The smallest cluster whose parts leave room for three CTAs on an SM, and more CTAs where the rows do
   // not fill the SMs, down to 4096 tokens a CTA (16 rows of 32000 with top-p: 13.3 us with eight CTAs each, 16.3 with 16).
   auto part = [&](int C) { return ((a.V + C - 1) / C + kSpChunk - 1) / kSpChunk * kSpChunk; };

@@ -166,6 +166,60 @@ def test_far_values():
         check(z, ref.settings(kind, 6, g), u)
 
 
+@pytest.mark.parametrize("V", [129280, (1 << 21) + 77])
+def test_draws_among_the_lightest_tokens(V):
+    """u below what one of the light tokens holds, and some of theirs: 2^-46.5 of the maximum's mass each."""
+    light = -46.5 * math.log(2.0)
+    z = torch.full((4, V), light, device="cuda")
+    z[:, V - 1] = 0.0
+    z[1::2, :700] = -math.inf
+    u = torch.tensor([0.0, 0.0, 1e-12, 0.5], device="cuda")
+    out = {"token": torch.full((4,), -7, device="cuda", dtype=torch.int32), "logp": torch.full((4,), 9.0, device="cuda")}
+    Sampler(4, V).sample(z, u, out=out)
+    tok = out["token"].tolist()
+    # u S is less than one token's mass, and in the third row less than a hundred tokens'
+    assert tok[0] == 0 and tok[1] == 700 and 0 <= tok[2] <= 200 and tok[3] == V - 1
+    want = torch.tensor([light, light, light, 0.0], device="cuda") - math.log1p(V * 2.0 ** -46.5)
+    assert ((out["logp"] - want).abs() <= 2.0 ** -22 * (1 + want.abs())).all()
+
+
+@pytest.mark.parametrize("octaves", [20.5, 30.5, 36.5, 40.5, 44.5, 46.5])
+@pytest.mark.parametrize("V", [129280, (1 << 21) + 77, 1 << 24])
+def test_masses_of_many_light_tokens(V, octaves):
+    """One heavy token and V - 1 light ones, whose mass together is 1 / 2 of its own down to 1e-14: the
+    logarithm, and the top-p border in the middle of them, to 2e-10 of the mass."""
+    z = torch.full((1, V), -octaves * math.log(2.0), device="cuda")
+    z[0, V // 3] = 0.0
+    m = math.exp(float(z[0, 0]))
+    S = 1.0 + (V - 1) * m
+    s = Sampler(1, V)
+    lp = s.logprobs(z)
+    for at, x in ((V // 3, 0.0), (0, float(z[0, 0])), (V - 1, float(z[0, 0]))):
+        # half a step each of the mass in fp32, its logarithm and the result, and the light tokens' product
+        assert abs(float(lp[0, at]) - (x - math.log(S))) <= 2.0 ** -24 * (3 + 2 * abs(x)) + 2e-10
+    p = float(torch.tensor((1.0 + 0.5 * (V - 1) * m) / S, dtype=F32))
+    if p < 1.0:
+        kept = s.logprobs(z, top_p=torch.tensor([p], device="cuda")) > -math.inf
+        n = int(kept.sum())
+        want = 1 + max(0, math.ceil((p * S - 1.0) / m))
+        assert abs(n - want) <= 1 + 2e-10 * S / m
+        light = kept[0].clone()
+        assert bool(light[V // 3])
+        light[V // 3] = False
+        first = int(light.sum())
+        assert bool(light[:first + (first > V // 3)].sum() == first)  # the lowest of the light ones
+    # Draws on both sides of the heavy token. Sums of 512 tokens are multiples of 2^-q of the mass, off by half a unit
+    # each (equal sums all the same way), and in one of them so is each of 512 tokens.
+    q = min(46, 62 - (V - 1).bit_length())
+    off = 2e-10 + V * 2.0 ** -(q + 10) + 2.0 ** (8 - q)
+    u = torch.tensor([(V // 3) * m / S * f for f in (0.0, 0.5)] + [((V // 3) * m + 0.5) / S], device="cuda")
+    tok = Sampler(3, V).sample(z.expand(3, V).contiguous(), u)["token"].tolist()
+    for t, x in zip(tok, u.double().tolist()):
+        c = x * S
+        want = math.floor(c / m) if c < (V // 3) * m else V // 3
+        assert abs(t - want) <= 1 + off * S / m and (want == V // 3) == (t == V // 3)
+
+
 def test_masks_next_to_the_maximum():
     """Temperatures so high that a masked token's finite logit would have a mass beside a maximum of -9e28."""
     V = 600
