@@ -503,7 +503,8 @@ struct Row {
     if (n < room) list[n] = (u64)~ordered(z) << 32 | (uint32_t)(start + l);
   }
 
-  // Greedy: the cut is the lowest token of the row's maximum.
+  // Greedy: the cut is the lowest token of the row's maximum. MASK: the others are masked.
+  template <bool MASK>
   __device__ void first_max() {
     if (tid == 0) {
       sh.n = 0x7FFFFFFF;
@@ -528,7 +529,7 @@ struct Row {
       equals += s[c][1];
     }
     cut = SpCut{m, (int)first};
-    if (RES && equals > 1) {
+    if (MASK && RES && equals > 1) {
       each([&](const float* v, int ch, int h) {
 #pragma unroll
         for (int i = 0; i < kStep; ++i)
@@ -806,8 +807,10 @@ struct Row {
   // top-k and top-p of rows of which few tokens are kept, without looking at all of them twice: the k-th largest of
   // the threads' maxima (`mine`) is at most the k-th largest token, so what is not below its bin holds all that is kept; on
   // flat rows a tenth more than k tokens. Those are listed, and one CTA finds both cuts. Returns false, with nothing
-  // changed, where they do not fit a list.
-  __device__ bool few(int k, const SpScale& b, float mine) {
+  // changed, where they do not fit a list. DRAW: that CTA also leaves out what is below z_min, and draws row n's token
+  // from its list, while the others end.
+  template <bool DRAW>
+  __device__ bool few(int k, const SpScale& b, float mine, float z_min, int row_n) {
     auto bits_of = [&](float z) { return __float_as_int(fmaf(z - b.sub, b.hi, b.mb)); };
     clear(kSpBins);
     if (tid == 0) sh.n = 0;
@@ -843,9 +846,14 @@ struct Row {
       tc::cluster_sync();  // the lengths have been read
       return false;
     }
+    if (DRAW && rank != 0) {
+      tc::cluster_sync();
+      return true;
+    }
     if (rank == 0) {
       u64 key[kOf], sum;
       uint32_t live = take_list(key, n, hist + at0);
+      if (DRAW) tc::cluster_sync();  // the others' lists have been read
       u64 end = reach(key, live, [](u64) { return 1ull; }, (u64)k, sum);
       auto mass_of = [&](u64 x) {
         int J;
@@ -862,6 +870,20 @@ struct Row {
       if (sh.p < 1.f) {
         const u64 goal2 = max(mul_floor(sum, sh.p, true), 1ull);
         end = reach(key, live, mass_of, goal2, sum);
+      }
+      if (DRAW) {
+        all = 0;
+#pragma unroll
+        for (int i = 0; i < kOf; ++i) {
+          if (key[i] > end || unordered(~(uint32_t)(key[i] >> 32)) < z_min) live &= ~(1u << i);
+          if (live >> i & 1) all += mass_of(key[i]);
+          key[i] = key[i] << 32 | key[i] >> 32;  // by index
+        }
+        const u64 S = block_scan(all, ignored);
+        const u64 at = mul_floor(S, sh.u, false) + 1;
+        const u64 got = reach(key, live, [&](u64 x) { return mass_of(x << 32 | x >> 32); }, at, sum);
+        if (tid == 0) put(row_n, (int)(got >> 32), unordered(~(uint32_t)got), S);
+        return true;
       }
       settle(key, n, end, sum);
     }
@@ -944,6 +966,11 @@ struct Row {
     }
   }
 
+  // A row's answer: a token with its z, of kept mass S.
+  __device__ __forceinline__ void put(int n, int token, float z, u64 S) const {
+    a.token[n] = token;
+    if (a.logp) a.logp[n] = (z - m) * sh.inv_t - (logf((float)S * exp2f(-(float)a.q)) + offset());
+  }
   // Masses are relative to the bins' zero: the logarithm of what that is off the maximum.
   __device__ __forceinline__ float offset() const {
     const float b = kSpMagic - mass.s.mb, x = m - mass.s.sub;
@@ -1142,9 +1169,17 @@ __global__ void __launch_bounds__(kSpThreads, 3) k_sample(SpArgs a) {
   }
 
   bool exact = false;  // held is the kept mass
+  const float z_min = t_log > -INFINITY ? __double2float_ru((double)top + t_log) : kSpLeast;
   const bool greedy = sh.k == 1;
   if (greedy) {
-    w.first_max();
+    w.template first_max<DIST>();
+    if (!DIST) {  // its probability is 1
+      if (w.rank == 0 && tid == 0) {
+        a.token[n] = w.cut.last;
+        if (a.logp) a.logp[n] = 0.f;
+      }
+      return;
+    }
   } else {
     bool cut_p = sh.p < 1.f;
     if (sh.k > 0 && sh.k < a.V) {
@@ -1153,7 +1188,8 @@ __global__ void __launch_bounds__(kSpThreads, 3) k_sample(SpArgs a) {
       const float beta = mean > 0.f ? fminf(kSpBins / (4.f * mean), 1e30f) : 0.f;
       const SpScale b{top, beta, kSpMagic};
       // half as many tokens as threads: up to 1.4 listed for each; 640 of a list's 1088
-      if (sh.k <= min((int)w.C * kSpThreads / 2, 640) && w.few(sh.k, b, mine)) {
+      if (sh.k <= min((int)w.C * kSpThreads / 2, 640) && w.template few<!DIST>(sh.k, b, mine, z_min, n)) {
+        if (!DIST) return;
         exact = true;
         cut_p = false;
       } else {
@@ -1165,12 +1201,9 @@ __global__ void __launch_bounds__(kSpThreads, 3) k_sample(SpArgs a) {
       exact = true;
     }
   }
-  if (!greedy && t_log > -INFINITY) {
-    const float z = __double2float_ru((double)top + t_log);
-    if (z > w.cut.z) {
-      w.cut = SpCut{z, 0x7FFFFFFF};
-      exact = false;
-    }
+  if (!greedy && z_min > w.cut.z) {
+    w.cut = SpCut{z_min, 0x7FFFFFFF};
+    exact = false;
   }
 
   if (DIST) {
@@ -1262,8 +1295,7 @@ __global__ void __launch_bounds__(kSpThreads, 3) k_sample(SpArgs a) {
       for (int i = 0; i < kOwn; ++i) {
         if (rest2 >= y && rest2 < y + own[i]) {
           const int l = ch * kSpChunk + tid * kOwn + i;
-          a.token[n] = w.start + l;
-          if (a.logp) a.logp[n] = (w.value(l) - top) * sh.inv_t - (logf((float)S * exp2f(-(float)a.q)) + w.offset());
+          w.put(n, w.start + l, w.value(l), S);
         }
         y += own[i];
       }
