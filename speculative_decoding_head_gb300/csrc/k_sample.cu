@@ -313,6 +313,7 @@ struct Row {
   float m;                   // the row's maximum
   Mass mass;
   u64 held = 0;              // the mass up to the cut of a search for masses
+  u64 own = 0;               // and what of it lies in this CTA (a lane's share, until it is summed)
   bool low_mass = false;     // the search is in the last bin
   SpCut cut{kSpLeast, 0x7FFFFFFF};
 
@@ -541,9 +542,9 @@ struct Row {
 
   // Tightens the cut to the first of the kept tokens, in order, at which the running
   // count (MASS: mass) reaches the target. The last bin takes in what lies below the others (its masses
-  // are added as multiples of 2^-60).
-  template <bool MASS>
-  __device__ void select(u64 target, const SpScale& b) {
+  // are added as multiples of 2^-60). OWN: the CTA's kept mass is wanted too. Returns whether it is known.
+  template <bool MASS, bool OWN>
+  __device__ bool select(u64 target, const SpScale& b) {
     constexpr int kLow = (int)kSpMagicBits - (kSpBins - 1);
     auto bits_of = [&](float z) { return __float_as_int(fmaf(z - b.sub, b.hi, b.mb)); };
     clear(kSpBins);
@@ -601,12 +602,18 @@ struct Row {
     }
     u64 before, goal;
     int bin;
-    if (!find<MASS, MASS>(target, goal, before, bin)) return;
+    if (!find<MASS, MASS>(target, goal, before, bin)) return false;
     const bool low = bin == kSpBins - 1;
     low_mass = MASS && low;
     const int e = octave(bin);
     const int bits = (int)kSpMagicBits - bin;
     auto inside = [&](float z) { return low ? bits_of(z) <= bits : bits_of(z) == bits; };
+    auto units = [&](u64 sum) { return low ? sum >> (kSpLowQ - a.q) : scaled(sum, e, a.q); };
+    if (OWN) {
+      own = 0;
+      for (int g = tid; g < bin; g += kSpThreads) own += scaled((u64)lo()[g] + ((u64)hi()[g] << kUp), octave(g), a.q);
+      __syncthreads();  // the histogram has been read
+    }
     // the CTA's tokens of the bin, into the half of the histogram's lower words that find() leaves alone
     const int at0 = bin < kSpBins / 2 ? kSpBins / 2 * 4 : 0;
     u64* list = reinterpret_cast<u64*>(buf + at0);
@@ -637,14 +644,26 @@ struct Row {
     int n;
     const bool fit = lists_fit(kSpOwn, n);
     if (fit) {
-      if (rank == 0) cut_of_list<MASS>(n, goal, hist + at0);
+      if (rank == 0) {
+        const u64 mine = cut_of_list<MASS>(n, goal, hist + at0);
+        if (OWN) own += units(mine);
+      }
     } else {
       narrow<MASS>(inside, goal);
     }
     tc::cluster_sync();
     cut.z = unordered((uint32_t)(sh.res[0] >> 32));
     cut.last = (int)(uint32_t)sh.res[0];
-    if (MASS) held = before + (low ? sh.res[1] >> (kSpLowQ - a.q) : scaled(sh.res[1], e, a.q));
+    if (MASS) held = before + units(sh.res[1]);
+    if (OWN && fit) {
+      if (rank != 0) {
+        const u64 end = (u64)~(uint32_t)(sh.res[0] >> 32) << 32 | (uint32_t)sh.res[0];
+        for (int i = tid; i < sh.n; i += kSpThreads)
+          if (list[i] <= end) own += units(raw<MASS>(list[i]));
+      }
+      u64 ignored;
+      own = block_scan(own, ignored);
+    }
     if (RES && !fit) {  // settle() has masked the others
       each([&](const float* v, int ch, int h) {
 #pragma unroll
@@ -653,6 +672,7 @@ struct Row {
       });
       __syncthreads();
     }
+    return OWN && fit;
   }
 
   template <bool MASS>
@@ -796,12 +816,18 @@ struct Row {
     }
     return few && n <= kSpList;
   }
+  // Returns a lane's share of CTA 0's own raw sum up to the cut.
   template <bool MASS>
-  __device__ void cut_of_list(int n, u64 goal, uint32_t at) {
+  __device__ u64 cut_of_list(int n, u64 goal, uint32_t at) {
     u64 key[kOf], sum;
     const uint32_t live = take_list(key, n, at);
     const u64 end = reach(key, live, [&](u64 k) { return (u64)raw<MASS>(k); }, goal, sum);
     settle(key, n, end, sum);
+    u64 mine = 0;
+#pragma unroll
+    for (int i = 0; i < kOf; ++i)
+      if (key[i] <= end && (int)(uint32_t)key[i] < a.part) mine += raw<MASS>(key[i]);
+    return mine;
   }
 
   // top-k and top-p of rows of which few tokens are kept, without looking at all of them twice: the k-th largest of
@@ -1169,6 +1195,7 @@ __global__ void __launch_bounds__(kSpThreads, 3) k_sample(SpArgs a) {
   }
 
   bool exact = false;  // held is the kept mass
+  bool shared_out = false;  // and own the CTA's share of it
   const float z_min = t_log > -INFINITY ? __double2float_ru((double)top + t_log) : kSpLeast;
   const bool greedy = sh.k == 1;
   if (greedy) {
@@ -1193,17 +1220,17 @@ __global__ void __launch_bounds__(kSpThreads, 3) k_sample(SpArgs a) {
         exact = true;
         cut_p = false;
       } else {
-        w.template select<false>((u64)sh.k, b);
+        w.template select<false, false>((u64)sh.k, b);
       }
     }
     if (cut_p) {
-      w.template select<true>(0, w.mass.s);
+      shared_out = w.template select<true, !DIST>(0, w.mass.s);
       exact = true;
     }
   }
   if (!greedy && z_min > w.cut.z) {
     w.cut = SpCut{z_min, 0x7FFFFFFF};
-    exact = false;
+    exact = shared_out = false;
   }
 
   if (DIST) {
@@ -1237,23 +1264,31 @@ __global__ void __launch_bounds__(kSpThreads, 3) k_sample(SpArgs a) {
     });
   } else {
     u64* chunk = reinterpret_cast<u64*>(w.buf);
-    for (int ch = w.warp; ch < w.chunks; ch += kSpWarps) {
-      u64 t = w.sum_kept(ch);
-      t = warp_sum64(t);
-      if (w.lane == 0) chunk[ch] = w.rounded(t);
-    }
-    __syncthreads();
     const int kEach = (w.chunks + kSpThreads - 1) / kSpThreads;
-    u64 t = 0, S = 0, before = 0, mine_before;
-    for (int i = 0; i < kEach; ++i) t += tid * kEach + i < w.chunks ? chunk[tid * kEach + i] : 0;
-    const u64 mine = w.block_scan(t, mine_before);
+    u64 mine_before;
+    // the chunks' sums, at least 1 if there is anything; returns the CTA's
+    auto sums = [&] {
+      for (int ch = w.warp; ch < w.chunks; ch += kSpWarps) {
+        const u64 t = warp_sum64(w.sum_kept(ch));
+        if (w.lane == 0) chunk[ch] = t ? max(w.rounded(t), 1ull) : 0;
+      }
+      __syncthreads();
+      u64 t = 0;
+      for (int i = 0; i < kEach; ++i) t += tid * kEach + i < w.chunks ? chunk[tid * kEach + i] : 0;
+      return w.block_scan(t, mine_before);
+    };
+    u64 mine = shared_out ? w.own : sums(), S = 0, before = 0;
     const u64(*s)[2] = w.tell(mine, 0);
     for (uint32_t c = 0; c < w.C; ++c) {
       if (c == w.rank) before = S;
       S += s[c][0];
     }
-    const u64 target = mul_floor(S, sh.u, false);
+    u64 target = mul_floor(S, sh.u, false);
     if (target >= before && target < before + mine) {
+      if (shared_out) {  // only here are they looked at: the last bits may differ
+        mine = sums();
+        target = before + min(target - before, mine - 1);
+      }
       u64 x = before + mine_before;
       for (int i = 0; i < kEach; ++i) {
         const int ch = tid * kEach + i;
