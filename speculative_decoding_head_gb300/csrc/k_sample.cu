@@ -832,10 +832,10 @@ struct Row {
 
   // top-k and top-p of rows of which few tokens are kept, without looking at all of them twice: the k-th largest of
   // the threads' maxima (`mine`) is at most the k-th largest token, so what is not below its bin holds all that is kept; on
-  // flat rows a tenth more than k tokens. Those are listed, and one CTA finds both cuts. Returns false, with nothing
-  // changed, where they do not fit a list. DRAW: that CTA also leaves out what is below z_min, and draws row n's token
-  // from its list, while the others end.
-  template <bool DRAW>
+  // flat rows a tenth more than k tokens. Those are listed, and one CTA finds both cuts, leaves out
+  // what is below z_min, and draws row_n's token or writes its distribution's tokens (the others write `fill` meanwhile).
+  // Returns false, with nothing done, where they do not fit a list.
+  template <bool DIST>
   __device__ bool few(int k, const SpScale& b, float mine, float z_min, int row_n) {
     auto bits_of = [&](float z) { return __float_as_int(fmaf(z - b.sub, b.hi, b.mb)); };
     clear(kSpBins);
@@ -872,51 +872,57 @@ struct Row {
       tc::cluster_sync();  // the lengths have been read
       return false;
     }
-    if (DRAW && rank != 0) {
-      tc::cluster_sync();
+    u64 key[kOf], sum = 0, ignored;
+    uint32_t live = rank == 0 ? take_list(key, n, hist + at0) : 0;
+    if (DIST) {
+      float* out = a.out + (int64_t)row_n * a.ldo + start;
+      if (a.vec_out) {
+        for (int i = tid * 4; i + 4 <= count; i += kSpThreads * 4)
+          __stcs(reinterpret_cast<float4*>(out + i), make_float4(a.fill, a.fill, a.fill, a.fill));
+      }
+      for (int i = (a.vec_out ? max(count, 0) & ~3 : 0) + tid; i < count; i += kSpThreads) out[i] = a.fill;
+    }
+    tc::cluster_arrive();  // the lists have been read, and `fill` written
+    if (rank != 0) {
+      tc::cluster_wait();
       return true;
     }
-    if (rank == 0) {
-      u64 key[kOf], sum;
-      uint32_t live = take_list(key, n, hist + at0);
-      if (DRAW) tc::cluster_sync();  // the others' lists have been read
-      u64 end = reach(key, live, [](u64) { return 1ull; }, (u64)k, sum);
-      auto mass_of = [&](u64 x) {
-        int J;
-        const uint32_t mant = mass.one(unordered(~(uint32_t)(x >> 32)), tab, J);
-        return weigh(mant, J + (int)kSpMagicBits, a.q);
-      };
-      u64 all = 0, ignored;
+    u64 end = reach(key, live, [](u64) { return 1ull; }, (u64)k, sum);
+    auto mass_of = [&](u64 x) {
+      int J;
+      const uint32_t mant = mass.one(unordered(~(uint32_t)(x >> 32)), tab, J);
+      return weigh(mant, J + (int)kSpMagicBits, a.q);
+    };
+    auto mass_up_to = [&](u64 last, float least) {
+      u64 all = 0;
 #pragma unroll
       for (int i = 0; i < kOf; ++i) {
-        if (key[i] > end) live &= ~(1u << i);
+        if (key[i] > last || unordered(~(uint32_t)(key[i] >> 32)) < least) live &= ~(1u << i);
         if (live >> i & 1) all += mass_of(key[i]);
       }
-      sum = block_scan(all, ignored);
-      if (sh.p < 1.f) {
-        const u64 goal2 = max(mul_floor(sum, sh.p, true), 1ull);
-        end = reach(key, live, mass_of, goal2, sum);
-      }
-      if (DRAW) {
-        all = 0;
-#pragma unroll
-        for (int i = 0; i < kOf; ++i) {
-          if (key[i] > end || unordered(~(uint32_t)(key[i] >> 32)) < z_min) live &= ~(1u << i);
-          if (live >> i & 1) all += mass_of(key[i]);
-          key[i] = key[i] << 32 | key[i] >> 32;  // by index
-        }
-        const u64 S = block_scan(all, ignored);
-        const u64 at = mul_floor(S, sh.u, false) + 1;
-        const u64 got = reach(key, live, [&](u64 x) { return mass_of(x << 32 | x >> 32); }, at, sum);
-        if (tid == 0) put(row_n, (int)(got >> 32), unordered(~(uint32_t)got), S);
-        return true;
-      }
-      settle(key, n, end, sum);
+      return block_scan(all, ignored);
+    };
+    if (sh.p < 1.f) {
+      const u64 goal2 = max(mul_floor(mass_up_to(end, kSpLeast), sh.p, true), 1ull);
+      end = reach(key, live, mass_of, goal2, sum);
     }
-    tc::cluster_sync();
-    cut.z = unordered((uint32_t)(sh.res[0] >> 32));
-    cut.last = (int)(uint32_t)sh.res[0];
-    held = sh.res[1];
+    const u64 S = mass_up_to(end, z_min);
+    if (DIST) {
+      const float ls = log_of(S);
+      tc::cluster_wait();
+#pragma unroll
+      for (int i = 0; i < kOf; ++i)
+        if (live >> i & 1)
+          a.out[(int64_t)row_n * a.ldo + (uint32_t)key[i]] =
+              fmaf(unordered(~(uint32_t)(key[i] >> 32)) - m, sh.inv_t, -ls);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kOf; ++i) key[i] = key[i] << 32 | key[i] >> 32;  // by index
+      const u64 goal2 = mul_floor(S, sh.u, false) + 1;
+      const u64 got = reach(key, live, [&](u64 x) { return mass_of(x << 32 | x >> 32); }, goal2, sum);
+      if (tid == 0) put(row_n, (int)(got >> 32), unordered(~(uint32_t)got), S);
+      tc::cluster_wait();
+    }
     return true;
   }
 
@@ -992,10 +998,11 @@ struct Row {
     }
   }
 
+  __device__ __forceinline__ float log_of(u64 S) const { return logf((float)S * exp2f(-(float)a.q)) + offset(); }
   // A row's answer: a token with its z, of kept mass S.
   __device__ __forceinline__ void put(int n, int token, float z, u64 S) const {
     a.token[n] = token;
-    if (a.logp) a.logp[n] = (z - m) * sh.inv_t - (logf((float)S * exp2f(-(float)a.q)) + offset());
+    if (a.logp) a.logp[n] = (z - m) * sh.inv_t - log_of(S);
   }
   // Masses are relative to the bins' zero: the logarithm of what that is off the maximum.
   __device__ __forceinline__ float offset() const {
@@ -1208,22 +1215,16 @@ __global__ void __launch_bounds__(kSpThreads, 3) k_sample(SpArgs a) {
       return;
     }
   } else {
-    bool cut_p = sh.p < 1.f;
     if (sh.k > 0 && sh.k < a.V) {
       // bins up to four times the mean distance from the maximum: half of the tokens lie within two
       const float mean = top - sum / fmaxf(seen, 1.f);
       const float beta = mean > 0.f ? fminf(kSpBins / (4.f * mean), 1e30f) : 0.f;
       const SpScale b{top, beta, kSpMagic};
       // half as many tokens as threads: up to 1.4 listed for each; 640 of a list's 1088
-      if (sh.k <= min((int)w.C * kSpThreads / 2, 640) && w.template few<!DIST>(sh.k, b, mine, z_min, n)) {
-        if (!DIST) return;
-        exact = true;
-        cut_p = false;
-      } else {
-        w.template select<false, false>((u64)sh.k, b);
-      }
+      if (sh.k <= min((int)w.C * kSpThreads / 2, 640) && w.template few<DIST>(sh.k, b, mine, z_min, n)) return;
+      w.template select<false, false>((u64)sh.k, b);
     }
-    if (cut_p) {
+    if (sh.p < 1.f) {
       shared_out = w.template select<true, !DIST>(0, w.mass.s);
       exact = true;
     }
@@ -1243,7 +1244,7 @@ __global__ void __launch_bounds__(kSpThreads, 3) k_sample(SpArgs a) {
       S = 0;
       for (uint32_t c = 0; c < w.C; ++c) S += s[c][0];
     }
-    const float ls = logf((float)S * exp2f(-(float)a.q)) + w.offset();
+    const float ls = w.log_of(S);
     float* out = a.out + (int64_t)n * a.ldo + w.start;
     w.each([&](const float* v, int ch, int h) {
       float y[R::kStep];
