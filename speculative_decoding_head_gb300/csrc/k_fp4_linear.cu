@@ -37,6 +37,8 @@ namespace {
 
 using namespace fp4;
 
+// How U comes in: not at all, by the copy engine, or by copies of four bytes a lane where its rows are not on 16 bytes.
+enum FlU { kFlNoU, kFlBoxU, kFlLaneU };
 constexpr int kFlTileV = 256;         // of a pair
 constexpr int kFlHalfV = 128;
 constexpr int kFlMaxN = 256;          // tokens of a tile
@@ -57,7 +59,7 @@ struct FlArgs {
   int vt, nt;    // tiles
   int stages, stage_bytes;
   int acc1, overlap;  // the second accumulator's first column; columns it shares with the first
-  int boxes;     // U and Y go by boxes
+  int ybox;      // Y goes out by the copy engine
   int* status;
 };
 
@@ -79,28 +81,9 @@ struct FlBars {
 
 __device__ __forceinline__ void put(float* p, float y) { __stcs(p, y); }
 
-// 16 columns (tokens n0 .. n0 + 15) of 32 lanes (v), scaled and stored.
-template <typename T, bool HASF, bool HASU>
-__device__ __forceinline__ void fl_store16(const FlArgs& a, float* z, int n0, int nn, int v, float wf) {
-  float u[16];
-  if (HASU) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) u[i] = i < nn && v < a.V ? __ldcs(a.U + (int64_t)(n0 + i) * a.ldu + v) : 0.f;
-  }
-  if (HASF) {
-#pragma unroll
-    for (int i = 0; i < 16; i += 4) {
-      const float4 f = __ldg(reinterpret_cast<const float4*>(a.xf + n0 + i));
-      z[i] = z[i] * wf * f.x;
-      z[i + 1] = z[i + 1] * wf * f.y;
-      z[i + 2] = z[i + 2] * wf * f.z;
-      z[i + 3] = z[i + 3] * wf * f.w;
-    }
-  }
-  if (HASU) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) z[i] += u[i];
-  }
+// 16 columns (tokens n0 .. n0 + 15) of 32 lanes (v), stored.
+template <typename T>
+__device__ __forceinline__ void fl_store16(const FlArgs& a, float* z, int n0, int nn, int v) {
   if (sizeof(T) == 4) {
     float* y = static_cast<float*>(a.Y) + (int64_t)n0 * a.ldy + v;
     if (v < a.V) {
@@ -147,7 +130,7 @@ struct FlUnits {
   int t, i, j;  // tile, its number among the pair's, place in its order
 };
 
-template <int FMT, typename T, bool HASU>
+template <int FMT, typename T, int U>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFlThreads, 1)
     k_fp4_linear(const __grid_constant__ FlMaps maps, FlArgs a) {
   constexpr int kSf = chunk_bytes(FMT);         // bytes of a 128-row group's scales of a stage
@@ -309,7 +292,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFlThreads, 1)
       }
     }
   } else if (warp >= 4) {
-    constexpr int kSlots = fl_slots(HASU), kSlot = fl_slot_bytes(HASU, sizeof(T));
+    constexpr int kSlots = fl_slots(U != kFlNoU), kSlot = fl_slot_bytes(U != kFlNoU, sizeof(T));
     const int e = warp - 4, q = e & 3, h = e >> 2;
     const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
     const uint32_t over = tc::map_rank(bar(&bars.over), 0);
@@ -333,27 +316,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFlThreads, 1)
     auto ask = [&]() {  // U's next box
       ahead = live(ahead);
       if (ahead.t >= tiles) return;
-      if (lane == 0) {
+      const int v = ahead.t / a.nt * kFlTileV + vq, n = ahead.t % a.nt * a.tn + col(ahead.i, ahead.j);
+      const uint32_t to = slots + asked % kSlots * kSlot;
+      if (U == kFlLaneU) {  // four bytes a lane and token, which that lane reads
+        const float* u = a.U + (int64_t)n * a.ldu + v + lane;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const bool there = n + i < a.N && v + lane < a.V;
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to + i * 128 + lane * 4),
+                       "l"(there ? u + i * a.ldu : a.U), "r"(there ? 4 : 0)
+                       : "memory");
+        }
+      } else if (lane == 0) {
         const uint32_t b = bar(&bars.ufull[e][asked % kSlots]);
         tc::mbar_arrive_expect_tx(b, 2048);
-        tc::tma_load_2d(slots + asked % kSlots * kSlot, &maps.u, ahead.t / a.nt * kFlTileV + vq,
-                        ahead.t % a.nt * a.tn + col(ahead.i, ahead.j), b, tc::policy_evict_first());
+        tc::tma_load_2d(to, &maps.u, v, n, b, tc::policy_evict_first());
       }
       ++asked;
       ahead.j += 2;
     };
-    if (HASU && a.boxes)
-      for (int i = 0; i < kSlots - 1; ++i) ask();
+    auto ask_next = [&]() {
+      ask();
+      if (U == kFlLaneU) asm volatile("cp.async.commit_group;" ::: "memory");  // an empty one too: they are counted
+    };
+    if (U != kFlNoU)
+      for (int i = 0; i < kSlots - 1; ++i) ask_next();
     // 16 columns: scaled, U added, to their box and out
     auto put = [&](float* z, int c, int v0, int n0, int nn, float wf) {
-      if (!a.boxes) {
-        fl_store16<T, FMT == DSPARK_NVFP4, HASU>(a, z, n0 + c, nn - c, v0 + vq + lane, wf);
-        return;
-      }
       if (FMT == DSPARK_NVFP4) fl_scale16(a, z, n0 + c, wf);
       const uint32_t box = slots + g % kSlots * kSlot;
-      if (HASU) {
-        ok = ok && tc::mbar_wait(bar(&bars.ufull[e][g % kSlots]), g / kSlots & 1, abort);
+      if (U != kFlNoU) {
+        if (U == kFlBoxU)
+          ok = ok && tc::mbar_wait(bar(&bars.ufull[e][g % kSlots]), g / kSlots & 1, abort);
+        else
+          asm volatile("cp.async.wait_group %0;" ::"n"(kSlots - 2) : "memory");
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           float u;
@@ -361,31 +357,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFlThreads, 1)
           z[i] += u;
         }
         if (sizeof(T) == 2) __syncwarp();  // the box is written with other rows
-      } else {
+      } else if (a.ybox) {
         // the store before the last has read this box
         if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
         __syncwarp();
       }
+      if (a.ybox) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        if (sizeof(T) == 4)
-          asm volatile("st.shared.f32 [%0], %1;" ::"r"(box + i * 128 + lane * 4), "f"(z[i]) : "memory");
-        else
-          asm volatile("st.shared.b16 [%0], %1;" ::"r"(box + i * 64 + lane * 2),
-                       "h"(__bfloat16_as_ushort(__float2bfloat16_rn(z[i])))
-                       : "memory");
-      }
-      tc::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        tc::tma_store_2d(&maps.y, v0 + vq, n0 + c, box);
-        tc::bulk_commit();
-        // U's next box goes where the store before this one came from
-        if (HASU) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-      }
-      if (HASU) {
+        for (int i = 0; i < 16; ++i) {
+          if (sizeof(T) == 4)
+            asm volatile("st.shared.f32 [%0], %1;" ::"r"(box + i * 128 + lane * 4), "f"(z[i]) : "memory");
+          else
+            asm volatile("st.shared.b16 [%0], %1;" ::"r"(box + i * 64 + lane * 2),
+                         "h"(__bfloat16_as_ushort(__float2bfloat16_rn(z[i])))
+                         : "memory");
+        }
+        tc::fence_proxy_async_smem();
         __syncwarp();
-        ask();
+        if (lane == 0) {
+          tc::tma_store_2d(&maps.y, v0 + vq, n0 + c, box);
+          tc::bulk_commit();
+          // U's next box goes where the store before this one came from
+          if (U != kFlNoU) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+        }
+      } else {
+        fl_store16<T>(a, z, n0 + c, nn - c, v0 + vq + lane);
+      }
+      if (U != kFlNoU) {
+        __syncwarp();
+        ask_next();
       }
       ++g;
     };
@@ -418,10 +418,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFlThreads, 1)
       }
     }
     // stores are complete, and U's boxes that no one took have come
-    if (a.boxes && lane == 0) {
+    if (U == kFlLaneU) asm volatile("cp.async.wait_all;" ::: "memory");
+    if (lane == 0) {
       asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
       int never = 0;
-      if (HASU && !ok)
+      if (U == kFlBoxU && !ok)
         for (int x = g; x < asked; ++x) tc::mbar_wait(bar(&bars.ufull[e][x % kSlots]), x / kSlots & 1, &never);
     }
     __syncwarp();
@@ -485,22 +486,27 @@ bool encode_boxes(CUtensorMap* tm, const void* p, bool bf16, int V, int N, int64
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int FMT, typename T, bool HASU>
+template <int FMT, typename T, int U>
 cudaError_t launch(const FlMaps& maps, const FlArgs& a, int grid, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
   constexpr int kMax = 227 * 1024 - 1024;  // the barriers are static
   const cudaError_t c = once_per_device(done, [] {
-    return cudaFuncSetAttribute(k_fp4_linear<FMT, T, HASU>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMax);
+    return cudaFuncSetAttribute(k_fp4_linear<FMT, T, U>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMax);
   });
   if (c != cudaSuccess) return c;
-  return launch_ex(k_fp4_linear<FMT, T, HASU>, dim3(grid), dim3(kFlThreads), (size_t)a.stages * a.stage_bytes + 8 * fl_slots(HASU) * fl_slot_bytes(HASU, sizeof(T)) + 1024, st,
-                   true, maps, a);
+  const size_t slots = 8 * fl_slots(U != kFlNoU) * fl_slot_bytes(U != kFlNoU, sizeof(T));
+  return launch_ex(k_fp4_linear<FMT, T, U>, dim3(grid), dim3(kFlThreads), (size_t)a.stages * a.stage_bytes + slots + 1024,
+                   st, true, maps, a);
+}
+template <int FMT, typename T>
+cudaError_t launch_u(int u, const FlMaps& maps, const FlArgs& a, int grid, cudaStream_t st) {
+  return u == kFlNoU    ? launch<FMT, T, kFlNoU>(maps, a, grid, st)
+         : u == kFlBoxU ? launch<FMT, T, kFlBoxU>(maps, a, grid, st)
+                        : launch<FMT, T, kFlLaneU>(maps, a, grid, st);
 }
 template <int FMT>
-cudaError_t launch_t(bool bf16, const FlMaps& maps, const FlArgs& a, int grid, cudaStream_t st) {
-  if (bf16)
-    return a.U ? launch<FMT, __nv_bfloat16, true>(maps, a, grid, st) : launch<FMT, __nv_bfloat16, false>(maps, a, grid, st);
-  return a.U ? launch<FMT, float, true>(maps, a, grid, st) : launch<FMT, float, false>(maps, a, grid, st);
+cudaError_t launch_t(bool bf16, int u, const FlMaps& maps, const FlArgs& a, int grid, cudaStream_t st) {
+  return bf16 ? launch_u<FMT, __nv_bfloat16>(u, maps, a, grid, st) : launch_u<FMT, float>(u, maps, a, grid, st);
 }
 
 bool on_type(const void* p, int size) { return p && (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(size - 1)) == 0; }
@@ -553,9 +559,10 @@ extern "C" dspark_status dspark_fp4_linear(const dspark_fp4_dims* xd, const dspa
       !encode_scales(&maps.xs, x->scales, a.K, a.N, wd->format))
     return DSPARK_ECUDA;
   const int size = type == DSPARK_BF16 ? 2 : 4;
-  a.boxes = (reinterpret_cast<uintptr_t>(Y) & 15u) == 0 && ldy * size % 16 == 0 &&
-            (!U || ((reinterpret_cast<uintptr_t>(U) & 15u) == 0 && ldu % 4 == 0));
-  if (a.boxes && (!encode_boxes(&maps.y, Y, size == 2, a.V, a.N, ldy) || (U && !encode_boxes(&maps.u, U, false, a.V, a.N, ldu))))
+  a.ybox = (reinterpret_cast<uintptr_t>(Y) & 15u) == 0 && ldy * size % 16 == 0;
+  const int u = !U ? kFlNoU : (reinterpret_cast<uintptr_t>(U) & 15u) == 0 && ldu % 4 == 0 ? kFlBoxU : kFlLaneU;
+  if ((a.ybox && !encode_boxes(&maps.y, Y, size == 2, a.V, a.N, ldy)) ||
+      (u == kFlBoxU && !encode_boxes(&maps.u, U, false, a.V, a.N, ldu)))
     return DSPARK_ECUDA;
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -565,8 +572,8 @@ extern "C" dspark_status dspark_fp4_linear(const dspark_fp4_dims* xd, const dspa
   const int grid = 2 * (int)(tiles < sms / 2 ? tiles : sms / 2);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (e == cudaSuccess)
-    e = wd->format == DSPARK_NVFP4 ? launch_t<DSPARK_NVFP4>(type == DSPARK_BF16, maps, a, grid, st)
-                                   : launch_t<DSPARK_MXFP4>(type == DSPARK_BF16, maps, a, grid, st);
+    e = wd->format == DSPARK_NVFP4 ? launch_t<DSPARK_NVFP4>(type == DSPARK_BF16, u, maps, a, grid, st)
+                                   : launch_t<DSPARK_MXFP4>(type == DSPARK_BF16, u, maps, a, grid, st);
   if (e != cudaSuccess) fprintf(stderr, "dspark: CUDA error %s\n", cudaGetErrorString(e));
   return e == cudaSuccess ? DSPARK_OK : DSPARK_ECUDA;
 }
