@@ -59,7 +59,7 @@ struct FlArgs {
   int vt, nt;    // tiles
   int stages, stage_bytes;
   int acc1, overlap;  // the second accumulator's first column; columns it shares with the first
-  int ybox;      // Y goes out by the copy engine
+  int ybox;      // columns of Y that go out by the copy engine: its stores write 16 bytes, so up to a multiple of those
   int* status;
 };
 
@@ -380,6 +380,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFlThreads, 1)
           // U's next box goes where the store before this one came from
           if (U != kFlNoU) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
         }
+        const int v = v0 + vq + lane;
+        if (v >= a.ybox && v < a.V) {  // the last columns
+          T* y = static_cast<T*>(a.Y) + (int64_t)(n0 + c) * a.ldy + v;
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (c + i < nn) y[i * a.ldy] = T(z[i]);
+        }
       } else {
         fl_store16<T>(a, z, n0 + c, nn - c, v0 + vq + lane);
       }
@@ -559,9 +566,9 @@ extern "C" dspark_status dspark_fp4_linear(const dspark_fp4_dims* xd, const dspa
       !encode_scales(&maps.xs, x->scales, a.K, a.N, wd->format))
     return DSPARK_ECUDA;
   const int size = type == DSPARK_BF16 ? 2 : 4;
-  a.ybox = (reinterpret_cast<uintptr_t>(Y) & 15u) == 0 && ldy * size % 16 == 0;
+  a.ybox = (reinterpret_cast<uintptr_t>(Y) & 15u) == 0 && ldy * size % 16 == 0 ? a.V & ~(16 / size - 1) : 0;
   const int u = !U ? kFlNoU : (reinterpret_cast<uintptr_t>(U) & 15u) == 0 && ldu % 4 == 0 ? kFlBoxU : kFlLaneU;
-  if ((a.ybox && !encode_boxes(&maps.y, Y, size == 2, a.V, a.N, ldy)) ||
+  if ((a.ybox && !encode_boxes(&maps.y, Y, size == 2, a.ybox, a.N, ldy)) ||
       (u == kFlBoxU && !encode_boxes(&maps.u, U, false, a.V, a.N, ldu)))
     return DSPARK_ECUDA;
   int dev = 0, sms = 0;

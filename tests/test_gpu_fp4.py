@@ -243,6 +243,29 @@ def test_many_tiles_and_persistent_ctas():
             assert torch.equal(w4.linear(x4), y)
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("N,K,V", [(5, 100, 700), (601, 64, 20011)])  # of the second a pair has several tiles
+def test_logits_of_any_alignment_are_added(N, K, V, fmt):
+    """The sum is one rounding of the product's fp32 result, however U's and Y's rows lie."""
+    x4 = Fp4Matrix(N, K, fmt).quantise(values((N, K), F32, seed=1))
+    w4 = Fp4Matrix(V, K, fmt).quantise(values((V, K), F32, seed=2))
+    z = w4.linear(x4)
+    even = -(-V // 8) * 8
+    for ldu, offu in ((even, 0), (even, 1), (even + 1, 0), (even + 5, 3)):
+        U = torch.empty(N, ldu + 4, device="cuda").normal_(generator=gen(ldu + offu))[:, offu:offu + V]
+        U = U.as_strided((N, V), (ldu, 1), offu) if ldu >= V + offu else U
+        want = z + U
+        for ldy, offy in ((even, 0), (even + 8, 1), (even + 1, 0)):
+            for dtype in (F32, BF16):
+                big = torch.full((N, ldy + 8), 7.0, dtype=dtype, device="cuda")
+                y = big[:, offy:offy + V]
+                assert torch.equal(w4.linear(x4, U=U, out=y), want.to(dtype))
+                assert (big[:, :offy] == 7).all() and (big[:, offy + V:] == 7).all()
+        inplace = torch.empty(N, ldu + 4, device="cuda")[:, offu:offu + V]
+        inplace.copy_(U)
+        assert torch.equal(w4.linear(x4, U=inplace, out=inplace), want)
+
+
 def test_offsets_past_32_bits():
     N, K, V = 16700, 64, 129280
     x4 = Fp4Matrix(N, K).quantise(values((N, K), BF16, seed=1))
