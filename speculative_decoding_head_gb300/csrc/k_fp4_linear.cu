@@ -10,7 +10,8 @@
 // dspark_fp4_quant lays them out); the MMA warp copies the scales to TMEM and issues
 // four block-scaled MMAs of 64 columns; eight warps work off accumulators, 16 tokens
 // by 32 v a box of shared memory: U comes in by the copy engine some boxes ahead, the
-// result goes out from the same box (unaligned rows go by plain loads and stores).
+// result goes out from the same box. Where U's rows are not on 16 bytes its boxes come by
+// four-byte copies of the lanes, where Y's are not they leave by plain stores.
 //
 // TMEM: two accumulators, and 48 columns of scales. Accumulators of more than
 // 224 columns overlap in the middle: the epilogue empties the shared columns
@@ -20,7 +21,8 @@
 // bound by memory, as up to some 100 tokens); N = 640 163 us (5.2 PFLOP/s; its loads
 // alone take 100 us, from L2 at 21 TB/s, without the stores of 331 MB 130);
 // N = 4096, K = 5376 to bf16 800 us (7.1 PFLOP/s), 910 in a long run under the
-// power limit. mxfp4, K = 256, N = 640 with U 118 us (680 MB at 5.8 TB/s; without boxes 287).
+// power limit. mxfp4, K = 256, N = 640 with U 118 us (680 MB at 5.8 TB/s; with plain loads
+// and stores 287); V = 50257 53 us, with U's rows, Y's, or both off 16 bytes 72, 76 and 98.
 // More or fewer stages change nothing.
 #include <cuda.h>
 #include <cudaTypedefs.h>

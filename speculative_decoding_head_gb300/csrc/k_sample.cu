@@ -20,20 +20,22 @@
 // left. A bin of more than 1088 tokens (many equal logits) is instead narrowed by
 // four histograms of the bits of z, down to one value, whose tokens are counted by
 // index. What is kept is z >= cut; tokens that equal the cut but come after its last
-// index are masked in shared memory.
+// index are masked in shared memory. Few tokens of a top-k are listed at once, and one
+// CTA does all the rest with them. A draw takes the CTA, then 512 tokens, then the token
+// that the target mass falls in.
 //
 // Three CTAs share an SM (64 KB of a row each, 256 threads), so that a row's
 // barriers and loads pass under the others' arithmetic. Two CTAs, 320 to 512
 // threads, and parts read again from L2 were slower or the same; clusters that take
 // row after row (one launch's worth of CTAs) spilled and took 20% more.
 //
-// 768 rows of 129280, fp32, as log-probabilities (794 MB): temperature alone 207 us
-// (3.8 TB/s), top-k 50 252, top-k and top-p 274, top-p 0.9 365 us (2.2 TB/s); bf16
-// (596 MB) 167, 188, 200 and 312. One row 8 to 20 us. With top-p a CTA spends 6 of its
-// 23 us on the histogram (two shared additions a token, 1.6 ns for 32 of them) and
-// 10 in five meetings of the cluster; schedulers issue in 48% of the cycles. 51
-// clusters of eight run at once (of 57 that SMs have room for), and a place stays
-// empty for 15% of the time between two of them.
+// 768 rows of 129280, fp32, as log-probabilities (794 MB): temperature alone 210 us
+// (3.8 TB/s), top-k 50 229, top-k and top-p 235, top-p 0.9 365 us (2.2 TB/s); bf16
+// (596 MB) 172, 151, 158 and 313. Drawn: 193, 179, 190 and 368 us; bf16 144, 107, 117 and
+// 308. One row 8 to 20 us. With top-p a CTA spends 6 of its 23 us on the histogram (two
+// shared additions a token, 1.6 ns for 32 of them) and 10 in five meetings of the
+// cluster; schedulers issue in 46% of the cycles. 51 clusters of eight run at once (of 57
+// that SMs have room for), and a place stays empty for 15% of the time between two.
 #include <math.h>
 #include <stdio.h>
 
