@@ -317,10 +317,11 @@ cudaError_t quant(QuArgs a, cudaStream_t st) {
   const int nb = chunks_of(a.K) * (kChunk / block_of(FMT));
   // An nvfp4 row belongs to one CTA (its largest value goes into every scale): four blocks a thread, whose loads are
   // in flight together (129280 rows of 256: 20.6 us with one, 15.6 with four), one where that leaves SMs without work,
-  // five where those fit the row (320 blocks: 346 us with four, of which one in six is idle, 300 with five), eight past 2048 blocks. mxfp4's
-  // blocks have twice the values.
+  // five where those fit the row (320 blocks: 346 us with four, of which one in six is idle, 300 with five), eight
+  // past 2048 blocks. mxfp4's blocks have twice the values.
   const bool few = (int64_t)a.rows * nb < 152 * 2048;
-  const int bpl = FMT == DSPARK_NVFP4 ? (nb <= 512 && few ? 1 : nb > 2048 ? 8 : nb % 160 == 0 ? 5 : 4) : (nb <= 1024 ? 1 : 2);
+  const int bpl = FMT == DSPARK_NVFP4 ? (nb <= 512 && few ? 1 : nb > 2048 ? 8 : nb % 160 == 0 ? 5 : 4)
+                                      : (nb <= 1024 ? 1 : 2);
   int lanes = 4;
   if (nb > 32 * bpl) {
     lanes = (nb + 32 * bpl - 1) / (32 * bpl) * 32;

@@ -423,11 +423,11 @@ struct Row {
     else add_carry(p, x);
   }
   // With every CTA's histogram filled: the first bin at which the sum up to it reaches the target, the sum before
-  // it, and how much of the bin's raw sum is missing there. OCT: the bins hold raw mants of their octaves, the last one multiples of 2^-60, and
-  // all count as multiples of 2^-q. target 0: ceil(p of all of it), at least 1. Returns whether the sum reaches the target at all.
+  // it, and how much of the bin's raw sum is missing there. target 0: ceil(p of all of it), at least 1. Returns
+  // whether the sum reaches the target at all. OCT: the bins hold raw mants of their octaves, the last one multiples
+  // of 2^-60, and all count as multiples of 2^-q. HIGH: the bins have upper words.
   // Every CTA tells the others its sums of eight segments, so that all know the segment, and all look at its bins:
   // they are not to change before the cluster's next barrier.
-  // HIGH: the bins have upper words.
   template <bool OCT, bool HIGH>
   __device__ __forceinline__ bool find(u64& target, u64& goal, u64& before, int& bin) {
     constexpr int kEach = (kSpSeg + 31) / 32;
@@ -832,11 +832,11 @@ struct Row {
     return mine;
   }
 
-  // top-k and top-p of rows of which few tokens are kept, without looking at all of them twice: the k-th largest of
-  // the threads' maxima (`mine`) is at most the k-th largest token, so what is not below its bin holds all that is kept; on
-  // flat rows a tenth more than k tokens. Those are listed, and one CTA finds both cuts, leaves out
-  // what is below z_min, and draws row_n's token or writes its distribution's tokens (the others write `fill` meanwhile).
-  // Returns false, with nothing done, where they do not fit a list.
+  // A row of which top-k keeps few tokens, without looking at all of them twice: the k-th largest of the threads'
+  // maxima (`mine`) is at most the k-th largest token, so what is not below its bin holds all that is kept; on flat
+  // rows a tenth more than k tokens. Those are listed, and one CTA finds both cuts, leaves out what is below z_min,
+  // and draws row_n's token or writes the kept tokens (the others write `fill` meanwhile). Returns false, with
+  // nothing done, where they do not fit a list.
   template <bool DIST>
   __device__ bool few(int k, const SpScale& b, float mine, float z_min, int row_n) {
     auto bits_of = [&](float z) { return __float_as_int(fmaf(z - b.sub, b.hi, b.mb)); };
@@ -1000,16 +1000,17 @@ struct Row {
     }
   }
 
-  __device__ __forceinline__ float log_of(u64 S) const { return logf((float)S * exp2f(-(float)a.q)) + offset(); }
+  // The logarithm of a kept mass over the maximum's own: of what it has more, so that it is 0 if nothing else is kept.
+  __device__ __forceinline__ float log_of(u64 S) const {
+    int J;
+    const uint32_t mant = mass.one(m, tab, J);
+    const u64 w = weigh(mant, J + (int)kSpMagicBits, a.q);
+    return log1pf((float)(S > w ? S - w : 0) / (float)w);
+  }
   // A row's answer: a token with its z, of kept mass S.
   __device__ __forceinline__ void put(int n, int token, float z, u64 S) const {
     a.token[n] = token;
     if (a.logp) a.logp[n] = (z - m) * sh.inv_t - log_of(S);
-  }
-  // Masses are relative to the bins' zero: the logarithm of what that is off the maximum.
-  __device__ __forceinline__ float offset() const {
-    const float b = kSpMagic - mass.s.mb, x = m - mass.s.sub;
-    return -(fmaf(x, mass.s.hi, -b) + x * mass.lo) * 0.0216608494f;  // ln(2) / 32
   }
   // The kept mass of a lane's tokens of a step: mants times 2^(fine-30-e), added up in two words, of those where that
   // is whole and of the others, times 2^29: all down to 2^-47.
@@ -1117,7 +1118,7 @@ __global__ void __launch_bounds__(kSpThreads, 3) k_sample(SpArgs a) {
     sh.k = k;
   }
 
-  // the row's part: to shared memory, its maximum on the way, and a sample of its logits; eight loads of a lane in flight
+  // the row's part: to shared memory, its maximum on the way, and a sample of its logits; a lane has eight loads in flight
   float top = -INFINITY, sum = 0.f, seen = 0.f;
   {
     constexpr int kWords = kSpChunk / (32 * R::kPer), kBatch = 8 / kWords;
@@ -1381,7 +1382,8 @@ dspark_status sample(const dspark_sample_args* s, const void* Z, SpArgs a, int32
   if (s->N == 0) return DSPARK_OK;
   const int size = s->type == DSPARK_BF16 ? 2 : 4;
   if (!Z || !on(Z, size) || Z == a.out) return DSPARK_EINVAL;
-  if (DIST ? (!a.out || !on(a.out, 4) || a.ldo < s->V) : (!a.u || !a.token || !on(a.u, 4) || !on(a.token, 4) || !on(a.logp, 4)))
+  if (DIST ? (!a.out || !on(a.out, 4) || a.ldo < s->V)
+           : (!a.u || !a.token || !on(a.u, 4) || !on(a.token, 4) || !on(a.logp, 4)))
     return DSPARK_EINVAL;
   a.Z = Z;
   a.ldz = s->ldz;

@@ -234,6 +234,33 @@ def test_masks_next_to_the_maximum():
     check(z, (T, None, None, None), u)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("V", [3, 700, 40000])
+def test_the_logarithm_next_to_one_kept_token(V, dtype):
+    """A token that is kept alone has log-probability 0, one beside a light token that token's share to 2^-21 of it
+    (two roundings of the sums, a division, the logarithm and the light token's mass: 2^-24 each at the most), and to
+    2^-46: the sum and the token's own mass are multiples of 2^-46, half of that off each."""
+    z = torch.empty(8, V, device="cuda").normal_(0.0, 0.5, generator=gen(V))
+    z = (z - 60.0).to(dtype)
+    z[torch.arange(8), torch.arange(8) * 7 % V] = torch.linspace(-9.0, 30.0, 8, device="cuda").to(dtype)
+    u = torch.linspace(0.0, 0.99, 8, device="cuda")
+    s, at = Sampler(8, V), torch.arange(8, device="cuda") * 7 % V
+    full = lambda v, t=F32: torch.full((8,), v, device="cuda", dtype=t)  # noqa: E731
+    for T in (0.7, 1.0, 1.9):
+        for how in (dict(top_k=full(1, torch.int32)), dict(top_p=full(1e-3)), dict(min_p=full(0.5)),
+                    dict(top_k=full(2, torch.int32), top_p=full(0.5))):
+            got = s.sample(z, u, temperature=full(T), **how)
+            lp = s.logprobs(z, temperature=full(T), **how)
+            assert torch.equal(got["token"].long(), at) and (got["logp"] == 0).all()
+            assert (lp.gather(1, at[:, None]) == 0).all() and torch.isfinite(lp).sum() == 8
+    z = torch.full((1, V), -math.inf, device="cuda", dtype=dtype)
+    z[0, 1], z[0, 2] = 1.5, -10.0
+    for T in (0.5, 1.0, 2.0):
+        lp = Sampler(1, V).logprobs(z, temperature=torch.tensor([T], device="cuda"))
+        want = -math.log1p(math.exp(-11.5 / T))
+        assert abs(float(lp[0, 1]) - want) <= 2.0 ** -21 * abs(want) + 2.0 ** -46
+
+
 def test_many_kept_tokens():
     """top-k from the lists' limits on: as many tokens as threads, thousands, and nearly all."""
     N, V = 6, 40000
