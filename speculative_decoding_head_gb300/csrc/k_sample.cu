@@ -276,7 +276,7 @@ __device__ __forceinline__ uint32_t max_nan2(uint32_t a, uint32_t b) {
   asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
-// floor(x a) and ceil(x a) for 0 <= a < 1
+// floor(x a) and ceil(x a) for 0 <= a < 1, not -0
 __device__ __forceinline__ u64 mul_floor(u64 x, float a, bool ceil) {
   const uint32_t b = __float_as_uint(a), e = b >> 23;
   const uint32_t mant = e ? (b & 0x7FFFFFu) | 0x800000u : b;
@@ -1113,8 +1113,8 @@ __global__ void __launch_bounds__(kSpThreads, 3) k_sample(SpArgs a) {
     sh.c_lo = (fmaf(-sh.c_hi, t, l_hi) + l_lo) / t;
     sh.inv_t = 1.f / t;
     sh.bcast[0] = __double_as_longlong(mp > 0.f ? (double)t * log((double)mp) : -INFINITY);
-    sh.p = p;
-    sh.u = u;
+    sh.p = fabsf(p);  // -0 is 0: mul_floor takes its factor's bits
+    sh.u = fabsf(u);
     sh.k = k;
   }
 
