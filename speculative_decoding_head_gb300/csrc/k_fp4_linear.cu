@@ -192,8 +192,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFlThreads, 1)
       const uint32_t bytes = kFlABytes + half * kFlBoxBytes + (1 + nsb) * kSf;
       const int wrow = v0 / kRows * chunks * kQ, xrow = n0 / kRows * chunks * kQ;  // rows of 512 bytes
       for (int c = 0; c < chunks; ++c, ++k) {
-        ok = tc::mbar_wait(bar(&bars.empty[s]), ph, abort);
-        ok = __all_sync(0xFFFFFFFFu, ok);
+        ok = tc::mbar_wait_warp(bar(&bars.empty[s]), ph, abort);
         if (!ok) break;
         if (tc::elect_one()) {
           const uint32_t st = sbase + s * a.stage_bytes, f = tc::map_rank(bar(&bars.full[s]), 0);
@@ -213,7 +212,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFlThreads, 1)
     }
     // the last stages' releases, which the even CTA's MMAs send to both CTAs, have arrived before either exits
     for (int j = max(0, k - a.stages); j < k && ok; ++j)
-      ok = tc::mbar_wait(bar(&bars.empty[j % a.stages]), j / a.stages & 1, abort);
+      ok = tc::mbar_wait_warp(bar(&bars.empty[j % a.stages]), j / a.stages & 1, abort);
     if (!ok && lane == 0) {
       *abort = 1;
       raise_status(a.status, DSPARK_ETIMEOUT);
@@ -232,13 +231,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFlThreads, 1)
         const int nsb = (nn + kRows - 1) / kRows, buf = i & 1;
         const uint32_t d = tmem + (buf ? a.acc1 : 0);
         const uint32_t id = tc::idesc_fp4(kFlTileV, nm, FMT == DSPARK_MXFP4, 0);
-        ok = tc::mbar_wait(bar(&bars.tempty[buf]), (i >> 1 & 1) ^ 1, abort);
-        if (ok && a.overlap && i > 0) ok = tc::mbar_wait(bar(&bars.over), (i - 1) & 1, abort);
-        ok = __all_sync(0xFFFFFFFFu, ok);
+        ok = tc::mbar_wait_warp(bar(&bars.tempty[buf]), (i >> 1 & 1) ^ 1, abort);
+        if (ok && a.overlap && i > 0) ok = tc::mbar_wait_warp(bar(&bars.over), (i - 1) & 1, abort);
         tc::tc_fence_after();
         for (int c = 0; c < chunks && ok; ++c) {
-          ok = tc::mbar_wait(bar(&bars.full[s]), ph, abort);
-          ok = __all_sync(0xFFFFFFFFu, ok);
+          ok = tc::mbar_wait_warp(bar(&bars.full[s]), ph, abort);
           if (!ok) break;
           tc::tc_fence_after();
           if (tc::elect_one()) {
@@ -283,8 +280,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFlThreads, 1)
       }
       // both CTAs' epilogues have released the last tiles: every MMA is complete, and their arrivals have landed
       // before this CTA exits
-      for (int j = max(0, i - 2); j < i && ok; ++j) ok = tc::mbar_wait(bar(&bars.tempty[j & 1]), j >> 1 & 1, abort);
-      if (ok && a.overlap && i > 0) ok = tc::mbar_wait(bar(&bars.over), (i - 1) & 1, abort);
+      for (int j = max(0, i - 2); j < i && ok; ++j) ok = tc::mbar_wait_warp(bar(&bars.tempty[j & 1]), j >> 1 & 1, abort);
+      if (ok && a.overlap && i > 0) ok = tc::mbar_wait_warp(bar(&bars.over), (i - 1) & 1, abort);
       if (!ok && lane == 0) {
         *abort = 1;
         raise_status(a.status, DSPARK_ETIMEOUT);
@@ -348,10 +345,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFlThreads, 1)
       if (FMT == DSPARK_NVFP4) fl_scale16(a, z, n0 + c, wf);
       const uint32_t box = slots + g % kSlots * kSlot;
       if (U != kFlNoU) {
-        if (U == kFlBoxU)
-          ok = ok && tc::mbar_wait(bar(&bars.ufull[e][g % kSlots]), g / kSlots & 1, abort);
-        else
+        if (U == kFlBoxU) {
+          ok = ok && tc::mbar_wait_warp(bar(&bars.ufull[e][g % kSlots]), g / kSlots & 1, abort);
+          if (!ok) return;  // this box and those after it may still be on their way
+        } else {
           asm volatile("cp.async.wait_group %0;" ::"n"(kSlots - 2) : "memory");
+        }
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           float u;
@@ -405,7 +404,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFlThreads, 1)
       float wf = 1.f;
       // rows' factors are padded to whole 128-row groups
       if (FMT == DSPARK_NVFP4 && v < (a.V + kRows - 1) / kRows * kRows) wf = __ldg(a.wf + v);
-      ok = ok && tc::mbar_wait(bar(&bars.tfull[buf]), i >> 1 & 1, abort);
+      ok = ok && tc::mbar_wait_warp(bar(&bars.tfull[buf]), i >> 1 & 1, abort);
       if (!ok) break;
       tc::tc_fence_after();
       const uint32_t d = lanes + (buf ? a.acc1 : 0);

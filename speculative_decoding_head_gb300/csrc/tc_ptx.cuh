@@ -79,6 +79,11 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
     }
   }
 }
+// The same by a whole warp, which goes on or gives up as one: its lanes' limits run out each at its own time, and what
+// comes after a wait is mostly for whole warps alone (tcgen05.ld, barriers, votes).
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort) {
+  return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort));
+}
 
 // ---------------------------------------------------------------- fp32 arithmetic
 constexpr float kLog2e = 1.4426950408889634f;  // log2(e): e^x = 2^(x log2 e)
