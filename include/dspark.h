@@ -581,7 +581,7 @@ dspark_status dspark_fp4_linear(const dspark_fp4_dims* xdims, const dspark_fp4_d
  *           first in any case;
  *   min-p   of those, keeps z_v >= max z + T log(min_p) (min_p = 0: all);
  * equal z go by the lower token first. T = 0 is greedy: the lowest token of
- * largest z alone. The settings are device arrays, temperature, top_p and min_p
+ * largest z alone. T above 0 and below 1e-30 counts as 1e-30. The settings are device arrays, temperature, top_p and min_p
  * fp32 and top_k int32 (each may be NULL: 1, 1, 0 and 0), with an entry
  * for each row, or, with row_off [requests + 1] (as dspark_plan writes it), for
  * each request b, whose rows are row_off[b] .. row_off[b + 1] - 1; rows

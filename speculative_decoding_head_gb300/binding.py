@@ -828,7 +828,7 @@ class Fp4Matrix(_TrainOp):
 class Sampler(_TrainOp):
     """Draws from up to N rows of V logits with temperature, top-k, top-p and min-p
     (``dspark_sample``), and the distribution that they make of the rows
-    (``dspark_sample_logprobs``). The settings are device vectors (temperature, top_p and
+    (``dspark_sample_logprobs``). The settings are device vectors (temperature (0: greedy, below 1e-30: 1e-30), top_p and
     min_p fp32, top_k int32; None: off), an entry per row, or per request where
     ``row_off`` [requests + 1] int32 says which rows belong to whom. Holds a status
     word; calls that share one object must be ordered on one stream."""

@@ -1106,7 +1106,7 @@ __global__ void __launch_bounds__(kSpThreads, 3) k_sample(SpArgs a) {
       t = 1.f;
       k = 1;
     }
-    t = fmaxf(t, 1e-30f);
+    t = fmaxf(t, 1e-30f);  // 32 log2(e) / T and 1 / T stay in fp32's range
     // 32 log2(e) / T, its rounding error with it
     const float l_hi = 46.1662407f, l_lo = 6.16308171e-07f;
     sh.c_hi = l_hi / t;
