@@ -601,9 +601,10 @@ dspark_status dspark_fp4_linear(const dspark_fp4_dims* xdims, const dspark_fp4_d
  * *device_status (the caller's int32; the first error is kept until the caller clears it).
  *
  * Masses are whole numbers of 31 bits and an octave (a relative error of at most
- * 2^-29, without a bias; below 2^-47 of the maximum's they are nothing), added as they are:
+ * 2^-26.5, 2^-30 in the mean square; below 2^-47 of the maximum's they are nothing), added as they are:
  * results are the same from call to call, and a border of the top-p set or of a draw is
- * missed only where it lies within some 1e-10 of the mass (1e-7 for V near 2^24). 0 <= N <= 2^24, V <= 2^24, else
+ * missed only where it lies within 6e-9 of the mass, and within some 1e-10 where a hundred
+ * logits and more share the mass (1e-7 for V near 2^24). 0 <= N <= 2^24, V <= 2^24, else
  * DSPARK_EINVAL; any leading dimension of at least V and any base address on the type's own
  * size will do; rows on 16 bytes run faster. Outputs must not overlap inputs. One launch,
  * asynchronous on `stream`, no scratch.

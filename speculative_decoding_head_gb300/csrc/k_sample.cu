@@ -6,10 +6,11 @@
 // (vocabularies that sixteen CTAs cannot hold are read again each pass).
 //
 // A token's mass, with m the row's maximum, is 2^y, y = (z - m) log2(e) / T, as a
-// whole number `mant` of 31 bits times 2^(-e-30), to a relative 2^-30 at the worst
-// and without a bias (see Mass). Masses are added as whole numbers, so in any order
-// with one result, and a border of the top-p set or of the draw is missed by 1e-10
-// of the mass at the most: next to nothing against one token's share.
+// whole number `mant` of 31 bits times 2^(-e-30), to a relative 2^-26.5 at the worst
+// and 2^-30 in the mean square, with next to no bias (see Mass). Masses are added as whole
+// numbers, so in any order with one result. A border of the top-p set or of the draw is
+// missed by half of that, 6e-9 of the mass, between a few heavy tokens (less than
+// half a step of u or p), by some 1e-10 where a hundred logits and more share the mass.
 //
 // top-k and top-p are one search, for the first token of the row sorted by
 // falling z (then by index) at which the running sum, of ones or of masses,
@@ -170,7 +171,8 @@ __device__ __forceinline__ void add_carry(uint32_t p, uint32_t x) {
 //   2^(x/32) = 2^-e T[q mod 32 / 2] (1 + w + w^2/2 + w^3/6 + w^4/24),  w = r ln(2) / 32,
 // Taylor's next term being 2^-31.5 at the most. x is never rounded: the fma of z hi with -(q + B) is
 // exact up to its own rounding of r, 2^-24 of 1/32 octave, and the bracket less one is at
-// most 2^-4.9 in fp32. sub is 0; where the maximum is so many octaves from 0 that B would not fit (2^16)
+// most 2^-4.9 in fp32: its roundings and r's are 2^-29 each, 2^-26.9 together at the worst of 33 million
+// logits, 2^-29.9 in the mean square, -2^-36 in the mean. sub is 0; where the maximum is so many octaves from 0 that B would not fit (2^16)
 // it is the maximum, and z - m is exact for every z whose mass counts (it is within 1/300 of m).
 // The table's sixteen entries of 8 bytes take a bank each: reads of it never conflict.
 struct Mass {

@@ -66,3 +66,61 @@ def test_temperatures_that_count_as_the_least():
         greedy = s.sample(z, u, temperature=full(0.0), **kw)
         assert torch.equal(greedy["token"].long(), z.argmax(1)) and (greedy["logp"] == 0).all()
     assert s.device_status() == 0
+
+
+def beside(border, tol):
+    """The largest fp32 numbers at or below border - tol and the least ones at or above border + tol (float64 arrays)."""
+    lo, hi = (border - tol).astype(np.float32), (border + tol).astype(np.float32)
+    lo = np.where(lo > border - tol, np.nextafter(lo, np.float32(0)), lo)
+    hi = np.where(hi < border + tol, np.nextafter(hi, np.float32(1)), hi)
+    return lo, hi
+
+
+# A token's mass is off by 2^-26.5 of itself at the most: with w = r ln(2) / 32 < 2^-4.9 the two roundings of r
+# are off by 2^-29.5 each, the two last ones of the polynomial, of its product with the table's entry and of the entry by
+# 2^-28.9 each, the whole number by 2^-31. So a border at a share b of the mass, between tokens that are off to different
+# sides, is off by b (1 - b) 2^-25.5, and by some units of 2^-46 of the maximum's mass. (fp32 settings lie 2^-24 apart.)
+def tolerance(b):
+    return b * (1 - b) * 2.0 ** -25.5 + 2.0 ** -40
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("heavy,each", [(2, 1), (3, 1), (3, 300), (2, 5000)])  # some values, the tokens that have each
+def test_borders_of_heavy_tokens(heavy, each, dtype):
+    """u and top-p on both sides of a border of few heavy tokens, and of many that share few logits (and so their errors)."""
+    N = 4096 if each == 1 else 256
+    V, g = heavy * each, gen(heavy * each)
+    z = torch.empty(N, heavy, device="cuda").normal_(0.0, 1.5, generator=g).to(dtype)
+    T = torch.rand(N, generator=g, device="cuda") * 1.7 + 0.3
+    zz, t = z.double().cpu().numpy(), T.double().cpu().numpy()
+    w = np.exp((zz - zz.max(1, keepdims=True)) / t[:, None])
+    z = z.repeat_interleave(each, 1)  # the tokens of one value are neighbours
+    w = np.repeat(w, each, 1)
+    c = np.cumsum(w, 1)
+    S, rows = c[:, -1:], np.arange(N)
+    s = Sampler(N, V)
+    for at in (np.full(N, (V - 1) // 2), np.full(N, V - 2), np.random.default_rng(V).integers(0, V - 1, N)):
+        b = (c / S)[rows, at]
+        for u, side in zip(beside(b, tolerance(b)), (0, 1)):
+            # the token that 64 bits draw: far from a border of theirs but for this one's
+            x = u.astype(np.float64)
+            clear = np.abs(c / S - x[:, None]) >= (tolerance(c / S) * (np.arange(V) != at[:, None]))
+            fine = clear.all(1) & (x >= 0) & (x < 1)
+            want = (c <= x[:, None] * S).sum(1)
+            # u lies on the side that is meant, but where a token beside the border has less than u's own step
+            assert fine.sum() > N // 2 and (want[fine] == at[fine] + side).mean() > 0.9
+            got = s.sample(z, torch.from_numpy(np.where(fine, u, 0.5).astype(np.float32)).cuda(), temperature=T)["token"]
+            assert np.array_equal(got.cpu().numpy()[fine], want[fine])
+    # top-p: a token is kept while what comes before it is less than p of the mass
+    order = np.argsort(-w, 1, kind="stable")
+    ws = np.take_along_axis(w, order, 1)
+    c = np.cumsum(ws, 1)
+    for at in (np.zeros(N, int), np.full(N, (V - 1) // 2), np.full(N, V - 2)):
+        b = (c / S)[rows, at]
+        for p in beside(b, tolerance(b)):
+            x = p.astype(np.float64)
+            clear = np.abs(c / S - x[:, None]) >= (tolerance(c / S) * (np.arange(V) != at[:, None]))
+            fine = clear.all(1) & (x > 0) & (x < 1)
+            want = ((c - ws) < x[:, None] * S).sum(1)
+            got = s.logprobs(z, temperature=T, top_p=torch.from_numpy(np.where(fine, p, 0.5).astype(np.float32)).cuda())
+            assert np.array_equal(torch.isfinite(got).sum(1).cpu().numpy()[fine], want[fine])
