@@ -26,7 +26,8 @@ from .binding import DsparkError, Fp4Matrix, Sampler, Workspace
 class HeadServer:
     """Rounds of B requests and gamma positions over an output layer ``W_out``
     [V, H] (bf16 or fp32; kept in 4 bits, format ``fmt``), with the Markov head's W1 [V, r] and W2 [r, V] and the
-    confidence head's w [H + r] and T [gamma] (1 if None)."""
+    confidence head's w [H + r] and T [gamma] (1 if None). They are all on one CUDA device, where the rounds run on
+    its current stream, whichever device is current."""
 
     def __init__(self, B: int, gamma: int, W_out: torch.Tensor, W1: torch.Tensor, W2: torch.Tensor, w: torch.Tensor,
                  T: Optional[torch.Tensor] = None, mode: str = "static", fmt: str = "nvfp4"):
@@ -34,37 +35,53 @@ class HeadServer:
         if W1.shape[0] != V or W2.shape != (W1.shape[1], V) or w.shape != (H + W1.shape[1],):
             raise DsparkError(f"W1 {list(W1.shape)}, W2 {list(W2.shape)} and w {list(w.shape)} do not fit W_out {[V, H]}")
         dev, f32 = W_out.device, torch.float32
+        if dev.type != "cuda":
+            raise DsparkError(f"W_out must be on a CUDA device, got {dev}")
+        self.device = dev
+        self._here(W1=W1, W2=W2, w=w, **({} if T is None else {"T": T}))
         self.B, self.gamma, self.V, self.H = B, gamma, V, H
         self.W1, self.W2, self.w = W1, W2, w
         self.T = torch.ones(gamma, dtype=f32, device=dev) if T is None else T
-        self.ws = Workspace(B, gamma, V, W1.shape[1], H, "bf16" if W1.dtype == torch.bfloat16 else "f32", mode)
+        with torch.cuda.device(dev):  # a workspace belongs to the current device, and so do its calls
+            self.ws = Workspace(B, gamma, V, W1.shape[1], H, "bf16" if W1.dtype == torch.bfloat16 else "f32", mode)
         self.layer = Fp4Matrix(V, H, fmt, device=dev).quantise(W_out)
         self.hidden, self.rows = (Fp4Matrix(n, H, fmt, device=dev) for n in (B * gamma, B * (gamma + 1)))
         self.sampler = Sampler(B * (gamma + 1), V, requests=B, device=dev)
         self.U = torch.empty(B * gamma, V, dtype=f32, device=dev)
         self.P, self.Q = (torch.empty(B * (gamma + 1), V, dtype=f32, device=dev) for _ in range(2))
 
+    def _here(self, **tensors: torch.Tensor) -> None:
+        """Refuses tensors of another device: the workspace takes their addresses as they are."""
+        for name, t in tensors.items():
+            if t.device != self.device:
+                raise DsparkError(f"{name} on {t.device}, the server on {self.device}")
+
     def draft(self, h: torch.Tensor, anchor: torch.Tensor, sps: torch.Tensor, seed: int, rnd: int) -> Dict[str, torch.Tensor]:
         """Drafts and plans from the draft's hidden states h [B, gamma, H]:
         ``Workspace.draft``'s and ``Workspace.plan``'s outputs."""
-        self.layer.linear(self.hidden.quantise(h.view(-1, self.H)), out=self.U)
-        d = self.ws.draft(self.U, self.W1, self.W2, anchor, h.float().contiguous(), self.w, self.T, seed, rnd)
-        return {**d, **self.ws.plan(d["conf"], sps)}
+        self._here(h=h, anchor=anchor, sps=sps)
+        with torch.cuda.device(self.device):
+            self.layer.linear(self.hidden.quantise(h.view(-1, self.H)), out=self.U)
+            d = self.ws.draft(self.U, self.W1, self.W2, anchor, h.float().contiguous(), self.w, self.T, seed, rnd)
+            return {**d, **self.ws.plan(d["conf"], sps)}
 
     def verify(self, ht: torch.Tensor, anchor: torch.Tensor, d: Dict[str, torch.Tensor], seed: int, rnd: int,
                **settings) -> Dict[str, torch.Tensor]:
         """Verifies a draft against the target's hidden states ht [B (gamma + 1), H], packed by the plan's
         row_off (rows past its last are not looked at), under ``Sampler``'s settings, an entry per request:
         ``Workspace.verify``'s outputs."""
-        self.layer.linear(self.rows.quantise(ht, count=d["row_off"][self.B :]), out=self.P)
-        self.sampler.logprobs(self.P, row_off=d["row_off"], out=self.Q, **settings)
-        return self.ws.verify(self.Q, d["row_off"], d["lengths"], anchor, d["tokens"], d["pd_tok"], d["lse"], self.U,
-                              self.W1, self.W2, seed, rnd)
+        self._here(ht=ht, anchor=anchor, **{k: d[k] for k in ("row_off", "lengths", "tokens", "pd_tok", "lse")})
+        with torch.cuda.device(self.device):
+            self.layer.linear(self.rows.quantise(ht, count=d["row_off"][self.B :]), out=self.P)
+            self.sampler.logprobs(self.P, row_off=d["row_off"], out=self.Q, **settings)
+            return self.ws.verify(self.Q, d["row_off"], d["lengths"], anchor, d["tokens"], d["pd_tok"], d["lse"], self.U,
+                                  self.W1, self.W2, seed, rnd)
 
     def device_status(self) -> int:
         """The first device error of any of the rounds' calls (synchronises)."""
         parts = (self.layer, self.hidden, self.rows, self.sampler, self.ws)
-        return next((s for s in (o.device_status() for o in parts) if s), 0)
+        with torch.cuda.device(self.device):
+            return next((s for s in (o.device_status() for o in parts) if s), 0)
 
 
 class Chain:

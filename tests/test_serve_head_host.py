@@ -1,0 +1,137 @@
+"""What a head server does on the host with several devices, on stand-ins for tensors and for the operators.
+
+Runs without a GPU: nothing is launched."""
+
+import types
+
+import pytest
+import torch
+
+from speculative_decoding_head_gb300 import serve_head
+from speculative_decoding_head_gb300.binding import DsparkError
+
+ZERO, ONE = torch.device("cuda", 0), torch.device("cuda", 1)
+B, GAMMA, V, H, R = 4, 3, 64, 32, 16
+
+
+class Stand:
+    """What a server looks at of a tensor."""
+
+    def __init__(self, shape, dtype, device):
+        self.shape, self.dtype, self.device = torch.Size(shape), dtype, device
+
+    def view(self, *shape):
+        return self
+
+    def float(self):
+        return self
+
+    def contiguous(self):
+        return self
+
+    def __getitem__(self, _):
+        return self
+
+
+@pytest.fixture
+def devices(monkeypatch):
+    """Device 0 is current. Returns the current devices' stack and what was current at each call of an operator."""
+    current, calls = [0], []
+
+    class On:
+        def __init__(self, device):
+            self.index = torch.device(device).index
+
+        def __enter__(self):
+            current.append(self.index)
+
+        def __exit__(self, *_):
+            current.pop()
+
+    class Op:
+        """A workspace follows the current device; the other operators have a device of their own."""
+
+        def __init__(self, *args, device=None, **kw):
+            self.device = device
+            calls.append(("new", current[-1] if device is None else device.index))
+
+        def __getattr__(self, name):
+            def call(*args, **kw):
+                calls.append((name, current[-1] if self.device is None else self.device.index))
+                where = torch.device("cuda", calls[-1][1])
+                if name == "quantise":
+                    return self
+                if name == "device_status":
+                    return 0
+                return {k: Stand((B,), torch.int32, where) for k in
+                        ("tokens", "pd_tok", "lse", "conf", "lengths", "row_off", "n_acc", "next_anchor")}
+            return call
+
+    def make(*shape, dtype=None, device=None):
+        return Stand(shape, dtype, torch.device("cuda", current[-1]) if device is None else torch.device(device))
+
+    fake = types.SimpleNamespace(**{k: getattr(torch, k) for k in ("float32", "int32", "bfloat16", "device")})
+    fake.empty = fake.ones = fake.zeros = make
+    fake.full = lambda shape, _, dtype=None, device=None: make(*shape, dtype=dtype, device=device)
+    fake.cuda = types.SimpleNamespace(device=On)
+    monkeypatch.setattr(serve_head, "torch", fake)
+    for name in ("Workspace", "Fp4Matrix", "Sampler"):
+        monkeypatch.setattr(serve_head, name, Op)
+    return current, calls
+
+
+def tensors(device, **other):
+    f32, i32 = torch.float32, torch.int32
+    at = lambda name, shape, dtype: Stand(shape, dtype, other.get(name, device))  # noqa: E731
+    return dict(W_out=at("W_out", (V, H), f32), W1=at("W1", (V, R), f32), W2=at("W2", (R, V), f32),
+                w=at("w", (H + R,), f32), T=at("T", (GAMMA,), f32)), dict(
+        h=at("h", (B, GAMMA, H), f32), ht=at("ht", (B * (GAMMA + 1), H), f32), anchor=at("anchor", (B,), i32),
+        sps=at("sps", (1 + B * (GAMMA + 1),), torch.float64))
+
+
+@pytest.mark.parametrize("device", [ZERO, ONE])
+def test_a_server_runs_on_its_own_device(devices, device):
+    current, calls = devices
+    weights, ins = tensors(device)
+    s = serve_head.HeadServer(B, GAMMA, **weights)
+    d = s.draft(ins["h"], ins["anchor"], ins["sps"], 0, 0)
+    s.verify(ins["ht"], ins["anchor"], d, 0, 0)
+    s.device_status()
+    assert current == [0]
+    names = {name for name, _ in calls}
+    assert {"new", "draft", "plan", "verify", "linear", "logprobs", "device_status"} <= names
+    assert {where for _, where in calls} == {device.index}, calls
+
+
+@pytest.mark.parametrize("name", ["W1", "W2", "w", "T"])
+def test_weights_of_another_device_are_refused(devices, name):
+    weights, _ = tensors(ONE, **{name: ZERO})
+    with pytest.raises(DsparkError):
+        serve_head.HeadServer(B, GAMMA, **weights)
+    assert not devices[1]
+
+
+def test_a_server_off_the_gpu_is_refused(devices):
+    weights, _ = tensors(torch.device("cpu"))
+    with pytest.raises(DsparkError):
+        serve_head.HeadServer(B, GAMMA, **weights)
+    assert not devices[1]
+
+
+@pytest.mark.parametrize("name", ["h", "ht", "anchor", "sps", "tokens", "lengths", "row_off", "pd_tok", "lse"])
+def test_a_rounds_tensors_of_another_device_are_refused(devices, name):
+    calls = devices[1]
+    weights, ins = tensors(ONE)
+    s = serve_head.HeadServer(B, GAMMA, **weights)
+    d = s.draft(ins["h"], ins["anchor"], ins["sps"], 0, 0)
+    calls.clear()
+    _, bad = tensors(ONE, **{name: ZERO})
+    if name in d:
+        d[name] = Stand((B,), torch.int32, ZERO)
+    if name in ("h", "anchor", "sps"):
+        with pytest.raises(DsparkError):
+            s.draft(bad["h"], bad["anchor"], bad["sps"], 0, 1)
+    if name not in ("h", "sps"):
+        with pytest.raises(DsparkError):
+            s.verify(bad["ht"], bad["anchor"], d, 0, 1)
+    assert not calls
