@@ -511,6 +511,8 @@ class _TrainOp:
     def __init__(self, device):
         self.status = torch.zeros(1, dtype=torch.int32, device=device)
         self._index, self._device = self.status.get_device(), self.status.device
+        if self._index < 0:
+            raise DsparkError(f"the object must be on a CUDA device, got {self._device}")
         self._streams = set()
 
     def _buffers(self):
