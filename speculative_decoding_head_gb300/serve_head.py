@@ -38,8 +38,11 @@ class HeadServer:
         if dev.type != "cuda":
             raise DsparkError(f"W_out must be on a CUDA device, got {dev}")
         self.device = dev
-        self._here(W1=W1, W2=W2, w=w, **({} if T is None else {"T": T}))
-        self.B, self.gamma, self.V, self.H = B, gamma, V, H
+        self.B, self.gamma, self.V, self.H, self.mode = B, gamma, V, H, mode
+        self._here(W1=W1, W2=W2, w=w)
+        if T is not None:
+            self._here(T=T)
+            self._long("T", T, gamma)
         self.W1, self.W2, self.w = W1, W2, w
         self.T = torch.ones(gamma, dtype=f32, device=dev) if T is None else T
         with torch.cuda.device(dev):  # a workspace belongs to the current device, and so do its calls
@@ -56,10 +59,19 @@ class HeadServer:
             if t.device != self.device:
                 raise DsparkError(f"{name} on {t.device}, the server on {self.device}")
 
+    @staticmethod
+    def _long(name: str, t: torch.Tensor, n: int) -> None:
+        """Refuses a vector of another length: the workspace reads as many values as its shape says."""
+        if t.shape != (n,):
+            raise DsparkError(f"{name} must be [{n}], got {list(t.shape)}")
+
     def draft(self, h: torch.Tensor, anchor: torch.Tensor, sps: torch.Tensor, seed: int, rnd: int) -> Dict[str, torch.Tensor]:
         """Drafts and plans from the draft's hidden states h [B, gamma, H]:
         ``Workspace.draft``'s and ``Workspace.plan``'s outputs."""
         self._here(h=h, anchor=anchor, sps=sps)
+        self._long("anchor", anchor, self.B)
+        if self.mode != "static":  # a static plan does not look at it
+            self._long("sps", sps, 1 + self.B * (self.gamma + 1))
         with torch.cuda.device(self.device):
             self.layer.linear(self.hidden.quantise(h.view(-1, self.H)), out=self.U)
             d = self.ws.draft(self.U, self.W1, self.W2, anchor, h.float().contiguous(), self.w, self.T, seed, rnd)
@@ -71,6 +83,7 @@ class HeadServer:
         row_off (rows past its last are not looked at), under ``Sampler``'s settings, an entry per request:
         ``Workspace.verify``'s outputs."""
         self._here(ht=ht, anchor=anchor, **{k: d[k] for k in ("row_off", "lengths", "tokens", "pd_tok", "lse")})
+        self._long("anchor", anchor, self.B)
         with torch.cuda.device(self.device):
             self.layer.linear(self.rows.quantise(ht, count=d["row_off"][self.B :]), out=self.P)
             self.sampler.logprobs(self.P, row_off=d["row_off"], out=self.Q, **settings)

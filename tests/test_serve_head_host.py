@@ -135,3 +135,30 @@ def test_a_rounds_tensors_of_another_device_are_refused(devices, name):
         with pytest.raises(DsparkError):
             s.verify(bad["ht"], bad["anchor"], d, 0, 1)
     assert not calls
+
+
+@pytest.mark.parametrize("mode", ["static", "compact"])
+def test_vectors_of_another_length_are_refused(devices, mode):
+    """The workspace takes as many values from an address as its shape says."""
+    calls = devices[1]
+    weights, ins = tensors(ONE)
+    for n in (GAMMA - 1, GAMMA + 1):
+        with pytest.raises(DsparkError):
+            serve_head.HeadServer(B, GAMMA, **{**weights, "T": Stand((n,), torch.float32, ONE)}, mode=mode)
+    assert not calls
+    s = serve_head.HeadServer(B, GAMMA, **weights, mode=mode)
+    d = s.draft(ins["h"], ins["anchor"], ins["sps"], 0, 0)
+    calls.clear()
+    for n in (B - 1, B + 1):
+        short = Stand((n,), torch.int32, ONE)
+        with pytest.raises(DsparkError):
+            s.draft(ins["h"], short, ins["sps"], 0, 1)
+        with pytest.raises(DsparkError):
+            s.verify(ins["ht"], short, d, 0, 1)
+    sps = Stand((B * (GAMMA + 1),), torch.float64, ONE)
+    if mode == "compact":
+        with pytest.raises(DsparkError):
+            s.draft(ins["h"], ins["anchor"], sps, 0, 1)
+        assert not calls
+    else:  # not looked at
+        s.draft(ins["h"], ins["anchor"], sps, 0, 1)
