@@ -81,20 +81,31 @@ class HeadServer:
                **settings) -> Dict[str, torch.Tensor]:
         """Verifies a draft against the target's hidden states ht [B (gamma + 1), H], packed by the plan's
         row_off (rows past its last are not looked at), under ``Sampler``'s settings, an entry per request:
-        ``Workspace.verify``'s outputs."""
+        ``Workspace.verify``'s outputs. One request that cannot be verified (a setting out of range, hidden states that
+        are not finite) ends the round: ``device_status`` tells of it, and the outputs mean nothing until ``reset``, but
+        for that next_anchor holds no id outside of the vocabulary."""
         self._here(ht=ht, anchor=anchor, **{k: d[k] for k in ("row_off", "lengths", "tokens", "pd_tok", "lse")})
         self._long("anchor", anchor, self.B)
         with torch.cuda.device(self.device):
             self.layer.linear(self.rows.quantise(ht, count=d["row_off"][self.B :]), out=self.P)
             self.sampler.logprobs(self.P, row_off=d["row_off"], out=self.Q, **settings)
+            out = {"n_acc": torch.full((self.B,), -1, dtype=torch.int32, device=self.device), "next_anchor": anchor.clone()}
             return self.ws.verify(self.Q, d["row_off"], d["lengths"], anchor, d["tokens"], d["pd_tok"], d["lse"], self.U,
-                                  self.W1, self.W2, seed, rnd)
+                                  self.W1, self.W2, seed, rnd, out=out)
+
+    def _parts(self):
+        return (self.layer, self.hidden, self.rows, self.sampler, self.ws)
 
     def device_status(self) -> int:
         """The first device error of any of the rounds' calls (synchronises)."""
-        parts = (self.layer, self.hidden, self.rows, self.sampler, self.ws)
         with torch.cuda.device(self.device):
-            return next((s for s in (o.device_status() for o in parts) if s), 0)
+            return next((s for s in (o.device_status() for o in self._parts()) if s), 0)
+
+    def reset(self) -> None:
+        """Clears the device errors, so that rounds go on (and the lagged planner's history)."""
+        with torch.cuda.device(self.device):
+            for o in self._parts():
+                o.reset()
 
 
 class Chain:

@@ -29,6 +29,9 @@ class Stand:
     def contiguous(self):
         return self
 
+    def clone(self):
+        return self
+
     def __getitem__(self, _):
         return self
 
