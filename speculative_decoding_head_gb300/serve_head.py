@@ -16,6 +16,7 @@ chain of tokens and prints what the rounds emit.
 from __future__ import annotations
 
 import argparse
+import math
 from typing import Dict, Optional
 
 import torch
@@ -148,6 +149,10 @@ def main():
         ap.add_argument(f"--{name}", type=float, default=value)
     ap.add_argument("--format", choices=["nvfp4", "mxfp4"], default="nvfp4")
     a = ap.parse_args()
+    for name, low, high in (("batch", 1, 4096), ("gamma", 1, 32), ("vocab", 1, 1 << 24), ("hidden", 1, 65536), ("rank", 1, 1024),
+                            ("rounds", 1, math.inf), ("temperature", 0, 3e38), ("top-p", 0, 1), ("min-p", 0, 1), ("noise", 0, 3e38)):
+        if not low <= getattr(a, name.replace("-", "_")) <= high:
+            ap.error(f"--{name} must be {f'from {low} to {high:g}' if high < 3e38 else f'at least {low} and finite'}")
     g = torch.Generator(device="cuda").manual_seed(a.seed)
     chain = Chain(a.vocab, a.hidden, g)
     W1 = torch.empty(a.vocab, a.rank, device="cuda").normal_(0.0, 0.02, generator=g).to(torch.bfloat16)

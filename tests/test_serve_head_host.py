@@ -165,3 +165,14 @@ def test_vectors_of_another_length_are_refused(devices, mode):
         assert not calls
     else:  # not looked at
         s.draft(ins["h"], ins["anchor"], sps, 0, 1)
+
+
+@pytest.mark.parametrize("args", ["--temperature -1", "--temperature nan", "--temperature inf", "--top-p 1.5", "--top-p -0.1",
+                                  "--top-p nan", "--min-p 2", "--min-p -1", "--batch 0", "--gamma 0", "--rounds 0",
+                                  "--noise -1", "--hidden 0"])
+def test_the_command_refuses_settings_out_of_range(args, monkeypatch, capsys):
+    """Before anything runs: a round with such a setting has no next tokens to go on from."""
+    monkeypatch.setattr("sys.argv", ["serve_head", *args.split()])
+    with pytest.raises(SystemExit) as e:
+        serve_head.main()
+    assert e.value.code == 2 and args.split()[0] in capsys.readouterr().err
