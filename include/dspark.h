@@ -538,7 +538,8 @@ size_t dspark_clip_grads_scratch_bytes(int count);
  * Any leading dimension of at least the row's length and any base address on
  * the type's own size will do for X, out, U and Y; rows on 16 bytes run faster.
  * rows, N and V <= 2^24, K <= 65536 and none of them negative (K, V and the table's rows at least 1), else
- * DSPARK_EINVAL. N = 0 is allowed. *device_status is the caller's int32 and keeps
+ * DSPARK_EINVAL. A product of more than 2^30 tiles of 256 by 256 values is DSPARK_EUNSUPPORTED. N = 0 is
+ * allowed. *device_status is the caller's int32 and keeps
  * its first error until the caller clears it. Asynchronous on `stream`, one launch
  * each; results are the same from call to call.
  */

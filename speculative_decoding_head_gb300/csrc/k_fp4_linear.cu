@@ -558,7 +558,6 @@ extern "C" dspark_status dspark_fp4_linear(const dspark_fp4_dims* xd, const dspa
   if (xd->rows == 0) return DSPARK_OK;
   if (!fp4::data_ok(xd, x) || !fp4::data_ok(wd, w) || !on_type(Y, type == DSPARK_BF16 ? 2 : 4)) return DSPARK_EINVAL;
   if (U == Y && (type != DSPARK_F32 || ldu != ldy)) return DSPARK_EINVAL;
-  if (!encode_fn()) return DSPARK_ECUDA;
   FlArgs a = {};
   a.wf = w->rowf;
   a.xf = x->rowf;
@@ -574,6 +573,9 @@ extern "C" dspark_status dspark_fp4_linear(const dspark_fp4_dims* xd, const dspa
   a.tn = a.N >= kFlMaxN ? kFlMaxN : (a.N + 31) / 32 * 32;
   a.vt = (a.V + kFlTileV - 1) / kFlTileV;
   a.nt = (a.N + a.tn - 1) / a.tn;
+  const int64_t tiles = (int64_t)a.vt * a.nt;
+  if (tiles > (1ll << 30)) return DSPARK_EUNSUPPORTED;  // they are counted in 32 bits, steps of the grid beyond the last among them
+  if (!encode_fn()) return DSPARK_ECUDA;
   const int acc = kFlSfCol / 2 / 16 * 16;  // 224 columns each without overlap
   a.overlap = a.tn > acc ? 2 * a.tn - kFlSfCol : 0;
   a.acc1 = a.tn - a.overlap;
@@ -597,8 +599,6 @@ extern "C" dspark_status dspark_fp4_linear(const dspark_fp4_dims* xd, const dspa
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  const int64_t tiles = (int64_t)a.vt * a.nt;
-  if (tiles > (1ll << 30)) return DSPARK_EUNSUPPORTED;
   const int grid = 2 * (int)(tiles < sms / 2 ? tiles : sms / 2);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (e == cudaSuccess)
