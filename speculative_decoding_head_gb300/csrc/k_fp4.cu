@@ -318,7 +318,10 @@ cudaError_t quant(QuArgs a, cudaStream_t st) {
   // An nvfp4 row belongs to one CTA (its largest value goes into every scale): four blocks a thread, whose loads are
   // in flight together (129280 rows of 256: 20.6 us with one, 15.6 with four), one where that leaves SMs without work,
   // five where those fit the row (320 blocks: 346 us with four, of which one in six is idle, 300 with five), eight
-  // past 2048 blocks. mxfp4's blocks have twice the values.
+  // past 2048 blocks. Four elsewhere, where one in eight is idle too (65536 rows of 5376, bf16 and fp32: 186 and 333 us
+  // with four, 276 and 401 with one, 238 and 358 with five, 292 and 530 with eight; of 4096: 120 and 211, 181 and 242,
+  // 154 and 226, 142 and 313). mxfp4's blocks have twice the values. Eight of fp32 and two of mxfp4's (K above
+  // 32768) do not fit the registers of so many threads: 380 and 188 bytes a thread go to memory.
   const bool few = (int64_t)a.rows * nb < 152 * 2048;
   const int bpl = FMT == DSPARK_NVFP4 ? (nb <= 512 && few ? 1 : nb > 2048 ? 8 : nb % 160 == 0 ? 5 : 4)
                                       : (nb <= 1024 ? 1 : 2);

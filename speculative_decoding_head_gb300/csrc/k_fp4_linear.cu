@@ -21,8 +21,9 @@
 // bound by memory, as up to some 100 tokens); N = 640 163 us (5.2 PFLOP/s; its loads
 // alone take 100 us, from L2 at 21 TB/s, without the stores of 331 MB 130);
 // N = 4096, K = 5376 to bf16 800 us (7.1 PFLOP/s), 910 in a long run under the
-// power limit. mxfp4, K = 256, N = 640 with U 118 us (680 MB at 5.8 TB/s; with plain loads
-// and stores 287); V = 50257 53 us, with U's rows, Y's, or both off 16 bytes 72, 76 and 98.
+// power limit. mxfp4, K = 256, N = 640 with U 120 us (680 MB at 5.6 TB/s; with plain loads
+// and stores 287); V = 50257 53 us, with U's rows, Y's, or both off 16 bytes 74, 78 and 101. Without U 62 us, to
+// bf16 56 (nvfp4 64 and 66, with U 150 and 137): the epilogue's work a value, the same for half the bytes.
 // More or fewer stages change nothing.
 #include <cuda.h>
 #include <cudaTypedefs.h>

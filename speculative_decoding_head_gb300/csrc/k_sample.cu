@@ -30,10 +30,10 @@
 // threads, and parts read again from L2 were slower or the same; clusters that take
 // row after row (one launch's worth of CTAs) spilled and took 20% more.
 //
-// 768 rows of 129280, fp32, as log-probabilities (794 MB): temperature alone 210 us
-// (3.8 TB/s), top-k 50 229, top-k and top-p 235, top-p 0.9 370 us (2.1 TB/s); bf16
-// (596 MB) 172, 151, 158 and 313. Drawn: 193, 179, 190 and 371 us; bf16 144, 107, 117 and
-// 308. One row 8 to 20 us. With top-p a CTA spends 6 of its 23 us on the histogram (two
+// 768 rows of 129280, fp32, as log-probabilities (794 MB): temperature alone 215 us
+// (3.7 TB/s), top-k 229, top-k and top-p 236, top-p 372 us (2.1 TB/s); bf16
+// (596 MB) 172, 152, 159 and 315. Drawn: 195, 182, 198 and 372 us; bf16 141, 111, 121 and
+// 308 (settings of each row its own). One row 8 to 20 us. With top-p a CTA spends 6 of its 23 us on the histogram (two
 // shared additions a token, 1.6 ns for 32 of them) and 10 in five meetings of the
 // cluster; schedulers issue in 46% of the cycles. 51 clusters of eight run at once (of 57
 // that SMs have room for), and a place stays empty for 15% of the time between two.
