@@ -358,12 +358,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFlThreads, 1)
       if (FMT == DSPARK_NVFP4) fl_scale16<decltype(far)::value>(a, z, n0 + c, wf);
       const uint32_t box = slots + g % kSlots * kSlot;
       if (U != kFlNoU) {
-        if (U == kFlBoxU) {
-          ok = ok && tc::mbar_wait_warp(bar(&bars.ufull[e][g % kSlots]), g / kSlots & 1, abort);
-          if (!ok) return;  // this box and those after it may still be on their way
-        } else {
+        if (U == kFlBoxU)  // each lane for itself: no one goes by it before the next tile's vote
+          ok = ok && tc::mbar_wait(bar(&bars.ufull[e][g % kSlots]), g / kSlots & 1, abort);
+        else
           asm volatile("cp.async.wait_group %0;" ::"n"(kSlots - 2) : "memory");
-        }
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           float u;
@@ -421,7 +419,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFlThreads, 1)
       const int v0 = t / a.nt * kFlTileV, n0 = t % a.nt * a.tn, nn = min(a.tn, a.N - n0), buf = i & 1;
       const float wf = wf_next;
       wf_next = factor(t + pairs);
-      ok = ok && tc::mbar_wait_warp(bar(&bars.tfull[buf]), i >> 1 & 1, abort);
+      ok = __all_sync(0xFFFFFFFFu, ok && tc::mbar_wait(bar(&bars.tfull[buf]), i >> 1 & 1, abort));
       if (!ok) break;
       tc::tc_fence_after();
       const uint32_t d = lanes + (buf ? a.acc1 : 0);
@@ -454,7 +452,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFlThreads, 1)
       asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
       int never = 0;
       if (U == kFlBoxU && !ok)
-        for (int x = g; x < asked; ++x) tc::mbar_wait(bar(&bars.ufull[e][x % kSlots]), x / kSlots & 1, &never);
+        for (int x = max(0, asked - kSlots); x < asked; ++x)  // of each slot the last one, taken or not
+          tc::mbar_wait(bar(&bars.ufull[e][x % kSlots]), x / kSlots & 1, &never);
     }
     __syncwarp();
     if (!ok) {
