@@ -80,7 +80,7 @@ class HeadServer:
 
     def verify(self, ht: torch.Tensor, anchor: torch.Tensor, d: Dict[str, torch.Tensor], seed: int, rnd: int,
                **settings) -> Dict[str, torch.Tensor]:
-        """Verifies a draft against the target's hidden states ht [B (gamma + 1), H], packed by the plan's
+        """Verifies the last draft against the target's hidden states ht [B (gamma + 1), H], packed by the plan's
         row_off (rows past its last are not looked at), under ``Sampler``'s settings, an entry per request:
         ``Workspace.verify``'s outputs. One request that cannot be verified (a setting out of range, hidden states that
         are not finite) ends the round: ``device_status`` tells of it, and the outputs mean nothing until ``reset``, but
