@@ -75,7 +75,9 @@ class HeadServer:
             self._long("sps", sps, 1 + self.B * (self.gamma + 1))
         with torch.cuda.device(self.device):
             self.layer.linear(self.hidden.quantise(h.view(-1, self.H)), out=self.U)
-            d = self.ws.draft(self.U, self.W1, self.W2, anchor, h.float().contiguous(), self.w, self.T, seed, rnd)
+            out = self.ws.new_draft_outputs(self.device)
+            out["tokens"].zero_()  # ids of the vocabulary, whatever becomes of the draft
+            d = self.ws.draft(self.U, self.W1, self.W2, anchor, h.float().contiguous(), self.w, self.T, seed, rnd, out=out)
             return {**d, **self.ws.plan(d["conf"], sps)}
 
     def verify(self, ht: torch.Tensor, anchor: torch.Tensor, d: Dict[str, torch.Tensor], seed: int, rnd: int,

@@ -32,6 +32,10 @@ class Stand:
     def clone(self):
         return self
 
+    def zero_(self):
+        self.zeroed = True
+        return self
+
     def __getitem__(self, _):
         return self
 
@@ -66,6 +70,8 @@ def devices(monkeypatch):
                     return self
                 if name == "device_status":
                     return 0
+                if kw.get("out") is not None and name == "draft":
+                    return kw["out"]
                 return {k: Stand((B,), torch.int32, where) for k in
                         ("tokens", "pd_tok", "lse", "conf", "lengths", "row_off", "n_acc", "next_anchor")}
             return call
@@ -176,3 +182,11 @@ def test_the_command_refuses_settings_out_of_range(args, monkeypatch, capsys):
     with pytest.raises(SystemExit) as e:
         serve_head.main()
     assert e.value.code == 2 and args.split()[0] in capsys.readouterr().err
+
+
+def test_a_drafts_tokens_are_ids_before_it_writes_them(devices):
+    """A draft that ends with a device error leaves tokens as they were: what a caller looks up next, so not memory as
+    it was."""
+    weights, ins = tensors(ONE)
+    s = serve_head.HeadServer(B, GAMMA, **weights)
+    assert s.draft(ins["h"], ins["anchor"], ins["sps"], 0, 0)["tokens"].zeroed
