@@ -72,8 +72,8 @@ def devices(monkeypatch):
                     return 0
                 if kw.get("out") is not None and name == "draft":
                     return kw["out"]
-                return {k: Stand((B,), torch.int32, where) for k in
-                        ("tokens", "pd_tok", "lse", "conf", "lengths", "row_off", "n_acc", "next_anchor")}
+                keys = {"plan": ("lengths", "row_off"), "verify": ("n_acc", "next_anchor")}
+                return {k: Stand((B,), torch.int32, where) for k in keys.get(name, ("tokens", "pd_tok", "lse", "conf"))}
             return call
 
     def make(*shape, dtype=None, device=None):
